@@ -11,6 +11,7 @@ Layouts: q, o, dO, dq are [B, T, Hq, D]; k, v, dk, dv are [B, T, Hkv, D]; lse is
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -35,7 +36,23 @@ EXPORTS = (
     "ne_attn_decode_f32", "ne_noalloc_get_device_error", "ne_attn_fwd_varlen", "ne_attn_fwd_varlen_f32",
     "ne_attn_bwd_varlen", "ne_attn_bwd_varlen_f32", "ne_qkv_prologue", "ne_attn_fwd_train",
     "ne_attn_fwd_train_f32", "ne_attn_bwd_train", "ne_attn_bwd_train_f32", "ne_qkv_prologue_workspace_size",
+    "ne_rope_spec_init", "ne_paged_append", "ne_paged_append_f32", "ne_paged_attn_workspace_size", "ne_paged_attn",
+    "ne_paged_attn_f32", "ne_pages_workspace_size", "ne_pages_fork", "ne_pages_resize", "ne_pages_compact",
 )
+
+
+class PagedCache(ctypes.Structure):
+    """ne_paged_cache of include/neattn.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("elem_bytes", ctypes.c_int), ("layers", ctypes.c_int),
+                ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int),
+                ("layer_stride", ctypes.c_int64), ("page_stride", ctypes.c_int64), ("tok_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class RopeSpec(ctypes.Structure):
+    """ne_rope_spec of include/neattn.h (made by rope_spec)."""
+    _fields_ = [("D", ctypes.c_int), ("rot_dim", ctypes.c_int), ("layout", ctypes.c_int), ("mscale", ctypes.c_float),
+                ("turns", ctypes.c_uint64 * 64)]
 
 
 class NeError(RuntimeError):
@@ -93,11 +110,25 @@ def load(path: str | None = None):
         lib.ne_attn_decode_workspace_size.restype = sz
         lib.ne_attn_decode.argtypes = [vp] * 6 + [i] * 5 + [d, vp, sz, vp]
         lib.ne_attn_decode_f32.argtypes = lib.ne_attn_decode.argtypes
+        i64 = ctypes.c_int64
+        lib.ne_rope_spec_init.argtypes = [vp, i, i, i, d, i, d, i, d, d, d]
+        lib.ne_paged_append.argtypes = [vp] * 8 + [i, vp] + [i64] * 4 + [i] * 4 + [vp]
+        lib.ne_paged_append_f32.argtypes = lib.ne_paged_append.argtypes
+        lib.ne_paged_attn_workspace_size.argtypes = [i] * 5
+        lib.ne_paged_attn_workspace_size.restype = sz
+        lib.ne_paged_attn.argtypes = [vp] * 7 + [i64] + [i] * 5 + [vp, sz, vp]
+        lib.ne_paged_attn_f32.argtypes = lib.ne_paged_attn.argtypes
+        lib.ne_pages_workspace_size.argtypes = [i, i, i]
+        lib.ne_pages_workspace_size.restype = sz
+        lib.ne_pages_fork.argtypes = [vp] * 5 + [i] + [vp] * 4 + [i] * 3 + [vp, sz, vp]
+        lib.ne_pages_resize.argtypes = [vp] * 8 + [i] * 2 + [vp, sz, vp]
+        lib.ne_pages_compact.argtypes = [vp] * 7 + [i] * 2 + [vp, sz, vp]
         for f in ("ne_rope_table", "ne_attn_fwd", "ne_attn_fwd_f32", "ne_attn_bwd", "ne_attn_bwd_f32",
                   "ne_get_device_error", "ne_selftest_wait_timeout", "ne_attn_bwd_noalloc", "ne_attn_decode",
                   "ne_noalloc_get_device_error", "ne_attn_fwd_varlen", "ne_attn_fwd_varlen_f32",
                   "ne_attn_bwd_varlen", "ne_attn_bwd_varlen_f32", "ne_qkv_prologue",
-                  "ne_attn_decode_f32"):
+                  "ne_attn_decode_f32", "ne_rope_spec_init", "ne_paged_append", "ne_paged_append_f32", "ne_paged_attn",
+                  "ne_paged_attn_f32", "ne_pages_fork", "ne_pages_resize", "ne_pages_compact"):
             getattr(lib, f).restype = i
         _lib = lib
     return _lib
@@ -325,6 +356,241 @@ def attn_decode(q, k_cache, v_cache, seq_lens, theta: float = 10000.0, o=None, l
     _check(fn(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(seq_lens), _ptr(o), _ptr(lse), B, T_max, Hq, Hkv, D,
               float(theta), _ptr(workspace), ws_bytes, _stream(q)))
     return o, lse
+
+
+# ---------------------------------------------------------------- paged cache
+
+ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "parts": 3}
+
+
+def rope_spec(D: int, rot_dim: int | None = None, theta: float = 10000.0, layout: str = "interleaved",
+              scaling: str = "none", factor: float = 1.0, orig_len: int = 0, beta_fast: float = 32.0,
+              beta_slow: float = 1.0, mscale: float = 1.0) -> RopeSpec:
+    """Rotary positions for paged_append (see ne_rope_spec in include/neattn.h): `layout`
+    interleaved (pairs 2i, 2i+1) or half (pairs i, i + rot_dim/2), the first `rot_dim`
+    elements of a head, `scaling` none, linear, base or parts for contexts `factor` times
+    longer than trained.  A host value: make it once and keep it."""
+    if layout not in ROPE_LAYOUTS or scaling not in ROPE_SCALINGS:
+        raise ValueError(f"layout must be one of {tuple(ROPE_LAYOUTS)}, scaling one of {tuple(ROPE_SCALINGS)}")
+    out = RopeSpec()
+    _check(load().ne_rope_spec_init(ctypes.byref(out), D, D if rot_dim is None else rot_dim, ROPE_LAYOUTS[layout],
+                                    float(theta), ROPE_SCALINGS[scaling], float(factor), orig_len, float(beta_fast),
+                                    float(beta_slow), float(mscale)))
+    return out
+
+
+def _on(device):
+    """The device's context when it is not the current one (kernels launch on the current)."""
+    return torch.cuda.device(device) if torch.cuda.current_device() != device.index else contextlib.nullcontext()
+
+
+def _paged_cache(k_pages, v_pages, layers: bool) -> PagedCache:
+    """The pools [P, page_size, Hkv, D] ([L, P, page_size, Hkv, D] with `layers`) as the C
+    struct.  Any strides in multiples of 16 bytes with D dense (head-major pages are a
+    transposed view), the same for both."""
+    if layers and k_pages.dim() == 4:
+        k_pages, v_pages = k_pages.unsqueeze(0), v_pages.unsqueeze(0)
+    want = 5 if layers else 4
+    if k_pages.dim() != want or v_pages.shape != k_pages.shape:
+        raise ValueError(f"k_pages and v_pages must be [{'L, ' if layers else ''}P, page_size, Hkv, D]; got "
+                         f"{tuple(k_pages.shape)}, {tuple(v_pages.shape)}")
+    if not k_pages.is_cuda or v_pages.device != k_pages.device:
+        raise ValueError("k_pages and v_pages must be CUDA tensors on one device")
+    if k_pages.dtype not in (torch.bfloat16, torch.float32) or v_pages.dtype != k_pages.dtype:
+        raise ValueError("k_pages and v_pages must both be bfloat16 or float32")
+    st = k_pages.stride()
+    if v_pages.stride() != st or st[-1] != 1:
+        raise ValueError("k_pages and v_pages must have the same strides, D dense")
+    shape = k_pages.shape
+    L, ls = (shape[0], st[0]) if layers else (1, 0)
+    P, ps, H, D = shape[-4:]
+    return PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), k_pages.element_size(), L, P, ps, H, D, ls, st[-4], st[-3],
+                      st[-2])
+
+
+def _check_ints(device, **tensors):
+    for name, (t, shape) in tensors.items():
+        if t.dtype != torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 CUDA tensor {list(shape)} on the pages' device")
+
+
+def _check_paged_batch(page_table, seq_lens, cu_new, N, device):
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    B = page_table.shape[0]
+    ints = {"page_table": (page_table, page_table.shape), "seq_lens": (seq_lens, (B,))}
+    if cu_new is not None:
+        ints["cu_new"] = (cu_new, (B + 1,))
+    elif N != B:
+        raise ValueError(f"without cu_new every sequence has one row: {N} rows for {B} sequences")
+    _check_ints(device, **ints)
+    return B
+
+
+def _rows(t, name, heads, like):
+    """Row stride of a [N, heads, D] tensor whose rows are dense."""
+    D = like.shape[-1]
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D or t.dtype != like.dtype or t.device != like.device:
+        raise ValueError(f"{name} must be a [N, {heads}, {D}] {like.dtype} tensor on the pages' device; got "
+                         f"{tuple(t.shape)} {t.dtype}")
+    if (D > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}: the heads of a row must be dense")
+    return t.stride(0) if t.shape[0] > 1 else heads * D
+
+
+def paged_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_new=None, rope=None, pos_offset: int = 0, q=None,
+                 q_out=None):
+    """New tokens into the paged cache (ne_paged_append): k, v [N, Hkv, D] packed rows
+    cu_new[b] .. cu_new[b+1]-1 of sequence b (None: one row each) go to positions
+    seq_lens[b] - n_b .. seq_lens[b] - 1 of its pages, k rotated by `rope` (a rope_spec, None:
+    not).  With q [N, Hq, D] the query rows are rotated into q_out (which may be q), returned.
+    Row slices of one fused projection are taken as they are."""
+    lib = load()
+    c = _paged_cache(k_pages, v_pages, False)
+    N = k.shape[0]
+    B = _check_paged_batch(page_table, seq_lens, cu_new, N, k_pages.device)
+    k_ld, v_ld = _rows(k, "k", c.Hkv, k_pages), _rows(v, "v", c.Hkv, k_pages)
+    if v.shape[0] != N:
+        raise ValueError("k and v must have the same rows")
+    Hq, q_ld, qo_ld = 0, 0, 0
+    if q is not None:
+        Hq = q.shape[1]
+        q_ld = _rows(q, "q", Hq, k_pages)
+        if q_out is None:
+            q_out = torch.zeros((N, Hq, c.D), dtype=q.dtype, device=q.device)
+        qo_ld = _rows(q_out, "q_out", Hq, k_pages)
+        if q.shape[0] != N or q_out.shape[0] != N:
+            raise ValueError("q, q_out, k and v must have the same rows")
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    fn = lib.ne_paged_append if c.elem_bytes == 2 else lib.ne_paged_append_f32
+    with _on(k_pages.device):
+        _check(fn(_ptr(q), _ptr(k), _ptr(v), ctypes.byref(c), _ptr(page_table), _ptr(seq_lens), _ptr(cu_new),
+                  ctypes.byref(rope) if rope is not None else None, pos_offset, _ptr(q_out), q_ld, k_ld, v_ld, qo_ld, B, N,
+                  Hq, page_table.shape[1], _stream(k_pages)))
+    return q_out
+
+
+def paged_workspace_size(B, N, Hq, Hkv, D) -> int:
+    return int(load().ne_paged_attn_workspace_size(B, N, Hq, Hkv, D))
+
+
+def alloc_paged_workspace(B, N, Hq, Hkv, D, device="cuda"):
+    """Workspace of paged_attn calls of this shape that run one after another."""
+    return torch.empty(max(paged_workspace_size(B, N, Hq, Hkv, D), 256), dtype=torch.uint8, device=device)
+
+
+def paged_attn(q, k_pages, v_pages, page_table, seq_lens, cu_new=None, max_new: int | None = None, o=None, lse=None,
+               workspace=None):
+    """Attention of the new tokens over the paged cache (ne_paged_attn): q [N, Hq, D]
+    rotated rows, packed as in paged_append; row i of sequence b attends to its first
+    seq_lens[b] - n_b + i + 1 positions.  Returns (o [N, Hq, D], lse [N, Hq] fp32); rows
+    outside the sequences are not written (zeros in a fresh o and lse).  max_new: the most
+    new tokens of a sequence, if known (a choice of kernel, not of results)."""
+    lib = load()
+    c = _paged_cache(k_pages, v_pages, False)
+    N, Hq = q.shape[0], q.shape[1]
+    B = _check_paged_batch(page_table, seq_lens, cu_new, N, k_pages.device)
+    q_ld = _rows(q, "q", Hq, k_pages)
+    if o is None:
+        o = torch.zeros((N, Hq, c.D), dtype=q.dtype, device=q.device)
+    elif o.shape != q.shape or o.dtype != q.dtype or o.device != q.device or not o.is_contiguous():
+        raise ValueError("o must be contiguous and match q")
+    if lse is None:
+        lse = torch.zeros((N, Hq), dtype=torch.float32, device=q.device)
+    elif lse.shape != (N, Hq) or lse.dtype != torch.float32 or lse.device != q.device or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous fp32 [N, Hq]")
+    if workspace is None:
+        workspace = alloc_paged_workspace(B, N, Hq, c.Hkv, c.D, q.device)
+    fn = lib.ne_paged_attn if c.elem_bytes == 2 else lib.ne_paged_attn_f32
+    with _on(k_pages.device):
+        _check(fn(_ptr(q), ctypes.byref(c), _ptr(page_table), _ptr(seq_lens), _ptr(cu_new), _ptr(o), _ptr(lse), q_ld, B, N,
+                  Hq, page_table.shape[1], max(1, N if max_new is None else max_new), _ptr(workspace),
+                  workspace.numel() * workspace.element_size(), _stream(k_pages)))
+    return o, lse
+
+
+def alloc_pages_workspace(n_pages: int, n: int, max_pages: int, device="cuda"):
+    """Workspace of pages_* calls over a pool of n_pages and tables of n sequences (a fork: children)."""
+    return torch.empty(max(int(load().ne_pages_workspace_size(n_pages, n, max_pages)), 256), dtype=torch.uint8,
+                       device=device)
+
+
+def _pages_call(k_pages, v_pages, refcount, page_table, n, refcount_out, workspace):
+    c = _paged_cache(k_pages, v_pages, True)
+    dev = k_pages.device
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    if refcount_out is None:
+        refcount_out = torch.empty_like(refcount)
+    _check_ints(dev, refcount=(refcount, (c.n_pages,)), refcount_out=(refcount_out, (c.n_pages,)),
+                page_table=(page_table, page_table.shape))
+    if workspace is None:
+        workspace = alloc_pages_workspace(c.n_pages, n, page_table.shape[1], dev)
+    return c, dev, refcount_out, workspace, workspace.numel() * workspace.element_size()
+
+
+def pages_fork(refcount, page_table, seq_lens, parents, k_pages, v_pages, deep: bool = False, refcount_out=None,
+               child_table=None, child_lens=None, short=None, workspace=None):
+    """Children continue sequences parents[c] (int32 [C], -1: empty): whole pages shared and
+    the partly filled last one copied, or (deep) every page copied, over all layers of
+    k_pages, v_pages [L, P, page_size, Hkv, D].  Returns (refcount_out [P], child_table
+    [C, max_pages], child_lens [C], short [1]); short > 0: that many pages were missing and
+    nothing changed.  refcount_out may be refcount."""
+    lib = load()
+    C, W = parents.shape[0], page_table.shape[-1]
+    c, dev, refcount_out, workspace, nb = _pages_call(k_pages, v_pages, refcount, page_table, C, refcount_out, workspace)
+    new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=dev)  # noqa: E731
+    child_table = new(C, W) if child_table is None else child_table
+    child_lens = new(C) if child_lens is None else child_lens
+    short = new(1) if short is None else short
+    B = page_table.shape[0]
+    _check_ints(dev, seq_lens=(seq_lens, (B,)), parents=(parents, (C,)), child_table=(child_table, (C, W)),
+                child_lens=(child_lens, (C,)), short=(short, (1,)))
+    with _on(dev):
+        _check(lib.ne_pages_fork(ctypes.byref(c), _ptr(refcount), _ptr(page_table), _ptr(seq_lens), _ptr(parents),
+                                 1 if deep else 0, _ptr(refcount_out), _ptr(child_table), _ptr(child_lens), _ptr(short), B,
+                                 C, W, _ptr(workspace), nb, _stream(k_pages)))
+    return refcount_out, child_table, child_lens, short
+
+
+def pages_resize(refcount, page_table, seq_lens, new_lens, k_pages, v_pages, refcount_out=None, table_out=None, short=None,
+                 workspace=None):
+    """Sequences go from seq_lens to new_lens positions (0: freed): pages behind the new
+    lengths are given back, a shared page that would be written is copied, new pages are
+    taken, lowest free ids first.  Returns (refcount_out, table_out, short [1]); short > 0:
+    that many pages were missing and nothing changed.  Both outputs may be the inputs."""
+    lib = load()
+    B, W = page_table.shape
+    c, dev, refcount_out, workspace, nb = _pages_call(k_pages, v_pages, refcount, page_table, B, refcount_out, workspace)
+    table_out = torch.empty_like(page_table) if table_out is None else table_out
+    short = torch.empty(1, dtype=torch.int32, device=dev) if short is None else short
+    _check_ints(dev, seq_lens=(seq_lens, (B,)), new_lens=(new_lens, (B,)), table_out=(table_out, (B, W)), short=(short, (1,)))
+    with _on(dev):
+        _check(lib.ne_pages_resize(ctypes.byref(c), _ptr(refcount), _ptr(page_table), _ptr(seq_lens), _ptr(new_lens),
+                                   _ptr(refcount_out), _ptr(table_out), _ptr(short), B, W, _ptr(workspace), nb,
+                                   _stream(k_pages)))
+    return refcount_out, table_out, short
+
+
+def pages_compact(refcount, page_table, k_pages, v_pages, refcount_out=None, table_out=None, remap=None, n_live=None,
+                  workspace=None):
+    """Moves the live pages of the pool into 0 .. n_live - 1.  Returns (refcount_out,
+    table_out, remap [P]: new id of every live page, -1 for free ones, n_live [1]).  Both
+    outputs may be the inputs; further tables go through remap."""
+    lib = load()
+    c, dev, refcount_out, workspace, nb = _pages_call(k_pages, v_pages, refcount, page_table, page_table.shape[0],
+                                                      refcount_out, workspace)
+    B, W = page_table.shape
+    table_out = torch.empty_like(page_table) if table_out is None else table_out
+    remap = torch.empty_like(refcount) if remap is None else remap
+    n_live = torch.empty(1, dtype=torch.int32, device=dev) if n_live is None else n_live
+    _check_ints(dev, table_out=(table_out, (B, W)), remap=(remap, (c.n_pages,)), n_live=(n_live, (1,)))
+    with _on(dev):
+        _check(lib.ne_pages_compact(ctypes.byref(c), _ptr(refcount), _ptr(page_table), _ptr(refcount_out), _ptr(table_out),
+                                    _ptr(remap), _ptr(n_live), B, W, _ptr(workspace), nb, _stream(k_pages)))
+    return refcount_out, table_out, remap, n_live
 
 
 def get_device_error(device=None) -> int:

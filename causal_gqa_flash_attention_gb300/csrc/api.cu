@@ -14,10 +14,12 @@
 #include <utility>
 #include <vector>
 
+#include "api.h"
 #include "kernels.h"
 #include "neattn.h"
 
-namespace {
+namespace ne {
+namespace api {
 
 thread_local std::string g_last_error;
 
@@ -31,9 +33,18 @@ ne_status fail(ne_status s, const char* fmt, ...) {
     return s;
 }
 
+void clear_error() { g_last_error.clear(); }
+
 ne_status cuda_fail(cudaError_t e, const char* what) {
     return fail(NE_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
+
+}  // namespace api
+}  // namespace ne
+
+using namespace ne::api;
+
+namespace {
 
 // ------------------------------------------------------------------ per-device state
 struct DeviceState {
@@ -49,6 +60,11 @@ struct DeviceState {
 std::mutex g_mu;
 std::map<int, DeviceState> g_dev;
 uint32_t g_timeout_ms = 0;   // 0 = default
+
+}  // namespace
+
+namespace ne {
+namespace api {
 
 unsigned long long timeout_ns() {
     uint32_t ms = g_timeout_ms;
@@ -85,6 +101,43 @@ ne_status error_word(int dev, int** out) {
     *out = ds.err_word;
     return NE_OK;
 }
+
+bool have_error_word(int dev) {
+    std::lock_guard<std::mutex> lk(g_mu);
+    const auto it = g_dev.find(dev);
+    return it != g_dev.end() && it->second.err_word != nullptr;
+}
+
+ne_status encode_fn(EncodeTiledFn* out) {
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+    });
+    if (!fn) return fail(NE_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    *out = fn;
+    return NE_OK;
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+ne_status check_ptrs(std::initializer_list<const void*> ps) {
+    for (const void* p : ps) {
+        if (!p) return fail(NE_ERR_INVALID_ARG, "null tensor pointer");
+        if (!aligned16(p)) return fail(NE_ERR_INVALID_ARG, "tensor pointer %p is not 16-byte aligned", p);
+    }
+    return NE_OK;
+}
+
+}  // namespace api
+}  // namespace ne
+
+namespace {
 
 // Cached interleaved (cos, sin) table [T, ld] (ld >= D/2 pairs per row; pairs past D/2
 // hold angle 0) for the current device.  Built on `st` by the rope kernel the first
@@ -169,26 +222,6 @@ cudaError_t timed(int phase, cudaStream_t st, F&& launch) {
 }
 
 // ------------------------------------------------------------------ tensor maps
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-ne_status encode_fn(EncodeTiledFn* out) {
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
-    if (!fn) return fail(NE_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-    *out = fn;
-    return NE_OK;
-}
-
 // Tiled map over a [B, T, H, D] tensor: box = (128 bytes of D, 1 head, rows, 1 batch),
 // 128-byte swizzle, zero fill out of bounds (ragged T tails).
 ne_status map_bthd(CUtensorMap* m, const void* ptr, bool f32, int B, int T, int H, int D, int rows,
@@ -229,8 +262,6 @@ ne_status map_rows_bf16(CUtensorMap* m, const void* ptr, long long rows, int col
 }
 
 // ------------------------------------------------------------------ validation
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 ne_status check_shape(int B, int T, int Hq, int Hkv, int D, double theta, bool f32) {
     if (B < 0 || T < 0) return fail(NE_ERR_INVALID_ARG, "B and T must be >= 0 (B=%d T=%d)", B, T);
     if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0)
@@ -244,16 +275,6 @@ ne_status check_shape(int B, int T, int Hq, int Hkv, int D, double theta, bool f
     if (elems >= (1LL << 31)) return fail(NE_ERR_INVALID_ARG, "B*T*Hq*D must be < 2^31");
     return NE_OK;
 }
-
-ne_status check_ptrs(std::initializer_list<const void*> ps) {
-    for (const void* p : ps) {
-        if (!p) return fail(NE_ERR_INVALID_ARG, "null tensor pointer");
-        if (!aligned16(p)) return fail(NE_ERR_INVALID_ARG, "tensor pointer %p is not 16-byte aligned", p);
-    }
-    return NE_OK;
-}
-
-size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Backward workspace: Delta fp32 [B,Hq,T] | dQ accumulator fp32 [B,T,Hq,D] | rotated fp16
 // Q' [B,T,Hq,D] (written by the preprocess kernel for the bf16 head_dim-64 kernel).
@@ -510,6 +531,20 @@ ne_status read_and_clear(int* err) {
         return fail(NE_ERR_INVALID_ARG,
                     "a rotated q or k value or a dS value exceeded 65504, the fp16 range of an MMA operand of "
                     "the bf16 path; the outputs of that call are invalid");
+    if (h == ne::SITE_PAGED_CU)
+        return fail(NE_ERR_INVALID_ARG,
+                    "a paged call got a cu_new entry outside [0, N] or below the one before it; the rows of that "
+                    "sequence are invalid");
+    if (h == ne::SITE_PAGED_LEN)
+        return fail(NE_ERR_INVALID_ARG,
+                    "a paged call got a length outside [0, max_pages * page_size]; it was clamped and the outputs of "
+                    "that sequence are invalid");
+    if (h == ne::SITE_PAGED_PAGE)
+        return fail(NE_ERR_INVALID_ARG,
+                    "a paged call met a page id outside the pool; nothing was read from or written to it and the "
+                    "outputs of that sequence are invalid");
+    if (h == ne::SITE_PAGES_PARENT)
+        return fail(NE_ERR_INVALID_ARG, "a fork got a parent outside [-1, B); that child is empty");
     return fail(NE_ERR_DEVICE_TIMEOUT, "a bounded wait inside a kernel ran out (site 0x%x)", h);
 }
 

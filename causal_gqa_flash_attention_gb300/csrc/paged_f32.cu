@@ -1,0 +1,251 @@
+// paged_f32.cu -- attention over the paged cache for fp32 tensors, in fp32 throughout.
+//
+// The fp32 entry points of the training kernels use TF32 tensor cores; a cache that is
+// kept in fp32 is kept for its precision, so here products and sums are fp32 FMAs (packed,
+// two per instruction).  Few rows per kv head are bound by the read of the cache (8 D bytes
+// per key against 4 D FMAs per row: 8 rows use about a third of the FMA rate at the copy
+// bandwidth); many rows by the FMAs and the shared-memory reads that feed them.
+//
+// A warp holds RW query rows.  S: lane = key, the query rows broadcast from shared memory;
+// O: lane = two (or one) elements of D, the weights broadcast.  FEW: four warps take
+// interleaved 32-key steps of the same 8 rows, each with a private ring, and are joined at
+// the end of a unit.  MANY: eight warps take 8 of 64 rows each over one shared ring.
+#include "paged_load.cuh"
+#include "paged_sched.cuh"
+
+namespace ne {
+namespace {
+
+constexpr int kStages = 3;
+constexpr int RW = 8;                                      // query rows per warp
+
+template <int D, bool MANY>
+struct F32Cfg {
+    static constexpr int WK = MANY ? 1 : 4;                // warps along the keys
+    static constexpr int WR = MANY ? 8 : 1;                // warps along the rows
+    static constexpr int WARPS = WK * WR;
+    static constexpr int THREADS = WARPS * 32;
+    static constexpr int ROWS = WR * RW;
+    static constexpr int BN = 32 * WK;
+    static constexpr int U = D / 4;                        // 16-byte units per row
+    static constexpr int TILE = 32 * D * 4;                // one K or V step of 32 keys
+    static constexpr int RINGS = WK * kStages * 2 * TILE;
+    static constexpr int Q_BYTES = ROWS * D * 4;
+    static constexpr int P_BYTES = WARPS * 32 * RW * 4;
+    static constexpr int SMEM = RINGS + Q_BYTES + P_BYTES;
+    static constexpr int DL = D / 32;                      // output elements per lane
+    static_assert(WK * ROWS * D * 4 <= RINGS, "the join fits into the rings");
+};
+
+template <int D, bool MANY>
+__global__ void __launch_bounds__(F32Cfg<D, MANY>::THREADS) paged_f32_kernel(const PagedAttnArgs a) {
+    using C = F32Cfg<D, MANY>;
+    constexpr int U = C::U, DL = C::DL;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ PagedLocate loc;
+    __shared__ float s_m[C::WK][C::ROWS], s_l[C::WK][C::ROWS];
+    float* s_q = reinterpret_cast<float*>(smem + C::RINGS);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int wk = MANY ? 0 : warp, row0 = MANY ? warp * RW : 0;
+    float* s_p = reinterpret_cast<float*>(smem + C::RINGS + C::Q_BYTES) + warp * 32 * RW;   // [key][RW]
+
+    griddep_launch_dependents();
+    griddep_wait();
+    paged_locate<C::THREADS>(a, blockIdx.x, loc, blockIdx.x == 0);
+    if (tid < 2) a.part_info[blockIdx.x * 2 + tid] = make_int4(0, 0, 0, 0);
+
+    const int ngrp = (a.G + a.p.gs - 1) / a.p.gs;          // head groups of a kv head
+    const uint32_t ring0 = smem_u32(smem) + wk * kStages * 2 * C::TILE;
+    PagedWalk walk;
+    walk.init(a, loc.w0, loc.w1, loc.b, loc.start);
+    PagedSeg g;
+    while (walk.next(a, g)) {
+        const int hkv = g.hg / ngrp, hs = g.hg % ngrp;
+        const int h0 = hkv * a.G + hs * a.p.gs;
+        const int gs = min(a.p.gs, a.G - hs * a.p.gs);
+        const int live_rows = g.ntok * gs;
+        const int* trow = a.s.table + (size_t)g.b * a.s.W;
+        const char* kp = static_cast<const char*>(a.c.k) + (long long)hkv * a.c.head_stride * 4;
+        const char* vp = static_cast<const char*>(a.c.v) + (long long)hkv * a.c.head_stride * 4;
+
+        // Query rows, in log2 units of the scaled logit.
+        for (int i = tid; i < C::ROWS * U; i += C::THREADS) {
+            const int row = i / U, u = i % U;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (row < live_rows) {
+                const float* src = static_cast<const float*>(a.q) + (long long)(g.tok0 + g.tok + row / gs) * a.q_ld +
+                                   (long long)(h0 + row % gs) * D;
+                x = __ldg(reinterpret_cast<const float4*>(src) + u);
+            }
+            reinterpret_cast<float4*>(s_q)[i] = x;
+        }
+        int lim[RW];
+#pragma unroll
+        for (int r = 0; r < RW; ++r) lim[r] = row0 + r < live_rows ? g.base + g.tok + (row0 + r) / gs + 1 : 0;
+
+        float m[RW], l[RW], o[RW][DL];
+#pragma unroll
+        for (int r = 0; r < RW; ++r) {
+            m[r] = -INFINITY;
+            l[r] = 0.f;
+#pragma unroll
+            for (int e = 0; e < DL; ++e) o[r][e] = 0.f;
+        }
+
+        // Loading: a private 32-key step per warp (FEW), or four rows of the shared step (MANY).
+        constexpr int LROWS = MANY ? 4 : 32;
+        const int nsteps = g.t1 - g.t0;
+        const int first = g.t0 * C::BN + wk * 32;
+        const int lfirst = first + (MANY ? warp * LROWS : 0);
+        int pid = page_of(a.c, trow, lfirst + lane, g.kv, a.err);
+        auto issue = [&](int j) {
+            if (j < nsteps) {
+                const int at = lfirst + j * C::BN;
+                const int pnext = j + 1 < nsteps ? page_of(a.c, trow, at + C::BN + lane, g.kv, a.err) : -1;
+                const uint32_t st = ring0 + (j % kStages) * 2 * C::TILE;
+                load_rows<LROWS, U>(st, st + C::TILE, kp, vp, a.c, 4, MANY ? warp * LROWS : 0, at, g.kv, pid, lane);
+                pid = pnext;
+            }
+            cp_async_commit();
+        };
+#pragma unroll
+        for (int j = 0; j < kStages - 1; ++j) issue(j);
+        __syncthreads();                                   // the query rows are there
+        for (int j = 0; j < nsteps; ++j) {
+            cp_async_wait<kStages - 2>();
+            if (MANY) __syncthreads();
+            else __syncwarp();
+            issue(j + kStages - 1);
+            const float4* sk = reinterpret_cast<const float4*>(smem + wk * kStages * 2 * C::TILE + (j % kStages) * 2 * C::TILE);
+            const float* sv = reinterpret_cast<const float*>(sk) + C::TILE / 4;
+            const int key = first + j * C::BN + lane;
+
+            float2 acc[RW];
+#pragma unroll
+            for (int r = 0; r < RW; ++r) acc[r] = make_float2(0.f, 0.f);
+#pragma unroll 4
+            for (int u = 0; u < U; ++u) {
+                const float4 kf = sk[tile_unit<U>(lane, u)];
+#pragma unroll
+                for (int r = 0; r < RW; ++r) {
+                    const float4 qv = reinterpret_cast<const float4*>(s_q)[(row0 + r) * U + u];
+                    acc[r] = __ffma2_rn(make_float2(kf.x, kf.y), make_float2(qv.x, qv.y), acc[r]);
+                    acc[r] = __ffma2_rn(make_float2(kf.z, kf.w), make_float2(qv.z, qv.w), acc[r]);
+                }
+            }
+            float p[RW];
+#pragma unroll
+            for (int r = 0; r < RW; ++r) {
+                const float s = key < lim[r] ? (acc[r].x + acc[r].y) * a.scale_log2 : -INFINITY;
+                float x = s;
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
+                const float now = fmaxf(m[r], x);
+                const float ref = now == -INFINITY ? 0.f : now;
+                const float al = ex2(m[r] - ref);
+                p[r] = ex2(s - ref);
+                m[r] = now;
+                l[r] = l[r] * al + p[r];
+#pragma unroll
+                for (int e = 0; e < DL; ++e) o[r][e] *= al;
+            }
+            *reinterpret_cast<float4*>(s_p + lane * RW) = make_float4(p[0], p[1], p[2], p[3]);
+            *reinterpret_cast<float4*>(s_p + lane * RW + 4) = make_float4(p[4], p[5], p[6], p[7]);
+            __syncwarp();
+#pragma unroll 4
+            for (int k = 0; k < 32; ++k) {
+                const float4 pa = *reinterpret_cast<const float4*>(s_p + k * RW);
+                const float4 pb = *reinterpret_cast<const float4*>(s_p + k * RW + 4);
+                const float pr[RW] = {pa.x, pa.y, pa.z, pa.w, pb.x, pb.y, pb.z, pb.w};
+                if constexpr (DL == 2) {
+                    const float2 v = *reinterpret_cast<const float2*>(sv + tile_unit<U>(k, lane >> 1) * 4 + (lane & 1) * 2);
+#pragma unroll
+                    for (int r = 0; r < RW; ++r) {
+                        const float2 x = __ffma2_rn(make_float2(pr[r], pr[r]), v, make_float2(o[r][0], o[r][1]));
+                        o[r][0] = x.x;
+                        o[r][1] = x.y;
+                    }
+                } else {
+                    const float v = sv[tile_unit<U>(k, lane >> 2) * 4 + (lane & 3)];
+#pragma unroll
+                    for (int r = 0; r < RW; ++r) o[r][0] = fmaf(pr[r], v, o[r][0]);
+                }
+            }
+        }
+        cp_async_wait<0>();
+        __syncthreads();                                   // rings and query rows are idle
+#pragma unroll
+        for (int r = 0; r < RW; ++r) {
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], off);
+            if (lane == 0) {
+                s_m[wk][row0 + r] = m[r];
+                s_l[wk][row0 + r] = l[r];
+            }
+        }
+        float* s_o = reinterpret_cast<float*>(smem);       // [WK][ROWS][D]
+#pragma unroll
+        for (int r = 0; r < RW; ++r)
+#pragma unroll
+            for (int e = 0; e < DL; ++e) s_o[(size_t)(wk * C::ROWS + row0 + r) * D + lane * DL + e] = o[r][e];
+        __syncthreads();
+        const int pslot = blockIdx.x * 2 + g.slot();
+        for (int i = tid; i < live_rows * U; i += C::THREADS) {
+            const int row = i / U, e = (i % U) * 4;
+            float mm = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < C::WK; ++w) mm = fmaxf(mm, s_m[w][row]);
+            const float ref = mm == -INFINITY ? 0.f : mm;
+            float ll = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < C::WK; ++w) {
+                const float wt = ex2(s_m[w][row] - ref);
+                const float4 x = *reinterpret_cast<const float4*>(s_o + (size_t)(w * C::ROWS + row) * D + e);
+                ll += s_l[w][row] * wt;
+                acc.x += x.x * wt;
+                acc.y += x.y * wt;
+                acc.z += x.z * wt;
+                acc.w += x.w * wt;
+            }
+            if (g.whole()) {
+                const float inv = ll > 0.f ? 1.f / ll : 0.f;
+                const long long orow = (long long)(g.tok0 + g.tok + row / gs) * a.Hq + h0 + row % gs;
+                *reinterpret_cast<float4*>(static_cast<float*>(a.o) + orow * D + e) =
+                    make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+                if (e == 0) a.lse[orow] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+            } else {
+                const size_t prow = (size_t)pslot * a.p.rows + row;
+                *reinterpret_cast<float4*>(a.part_o + prow * D + e) = acc;
+                if (e == 0) a.part_ml[prow] = make_float2(mm, ll);
+            }
+        }
+        if (!g.whole() && tid == 0) a.part_info[pslot] = paged_record(g);
+        __syncthreads();
+    }
+}
+
+template <int D, bool MANY>
+cudaError_t launch_f32_t(const PagedAttnArgs& a, cudaStream_t st) {
+    using C = F32Cfg<D, MANY>;
+    auto kfn = paged_f32_kernel<D, MANY>;
+    static_assert(C::SMEM + 4096 <= 227 * 1024, "shared memory");
+    cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_k(kfn, dim3(a.p.C), dim3(C::THREADS), C::SMEM, st, a);
+}
+
+}  // namespace
+
+int paged_f32_bn(bool many) { return many ? F32Cfg<64, true>::BN : F32Cfg<64, false>::BN; }
+
+cudaError_t launch_paged_f32(PagedKind kind, int D, const PagedAttnArgs& a, cudaStream_t st) {
+    const bool many = kind == PAGED_F32_MANY;
+    switch (D) {
+        case 32: return many ? launch_f32_t<32, true>(a, st) : launch_f32_t<32, false>(a, st);
+        case 64: return many ? launch_f32_t<64, true>(a, st) : launch_f32_t<64, false>(a, st);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace ne

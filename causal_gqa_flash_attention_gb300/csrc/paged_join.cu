@@ -1,0 +1,185 @@
+// paged_join.cu -- the parts of cut units put together: for every query row the parts
+// (m_i, l_i, o_i) of its keys give o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i with m
+// the largest m_i, and LSE = m + log2 of that sum.  Reads 4 (D + 2) bytes per row and part,
+// writes a row: bound by the latency of a few dependent loads, a microsecond or two.
+// Parts are added in the order of the key axis, so the result has one value.
+#include <cuda_bf16.h>
+#include "paged_sched.cuh"
+
+namespace ne {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxParts = 1024;
+
+__device__ __forceinline__ void put(__nv_bfloat16* dst, const float4& x) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+__device__ __forceinline__ void put(float* dst, const float4& x) { *reinterpret_cast<float4*>(dst) = x; }
+
+// (m, l, o) += (m2, l2, o2), both unnormalised; m = -inf for no keys.
+__device__ __forceinline__ void add_part(float& m, float& l, float4& o, float m2, float l2, const float4& o2) {
+    const float mx = fmaxf(m, m2);
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    const float w1 = ex2(m - ref), w2 = ex2(m2 - ref);
+    l = l * w1 + l2 * w2;
+    o.x = o.x * w1 + o2.x * w2;
+    o.y = o.y * w1 + o2.y * w2;
+    o.z = o.z * w1 + o2.z * w2;
+    o.w = o.w * w1 + o2.w * w2;
+    m = mx;
+}
+
+// Block (j, y): the unit whose first part CTA j left in its slot 1; rows y, y + gridDim.y, ...
+// in turn (or that stride in groups of rows).
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedAttnArgs a) {
+    constexpr int LPR = D / 4;                             // lanes of a row, four elements each
+    constexpr int GR = kThreads / LPR;                     // lane groups
+    __shared__ int s_part[kMaxParts], s_n;
+    __shared__ float s_m[GR], s_l[GR];
+    __shared__ float4 s_o[kThreads];
+    const int tid = threadIdx.x, j = blockIdx.x;
+    griddep_launch_dependents();
+    griddep_wait();
+    const int4 rec = a.part_info[j * 2 + 1];
+    if (rec.x == 0) return;
+    if (tid < 32) {
+        // The parts in order: this slot, then the following CTAs' slots 0 up to the last.
+        int n = 1;
+        if (tid == 0) s_part[0] = j * 2 + 1;
+        for (int c0 = j + 1; c0 < a.p.C; c0 += 32) {
+            const int c = c0 + tid;
+            const int st = c < a.p.C ? a.part_info[c * 2].x : 0;
+            const unsigned ends = __ballot_sync(0xffffffffu, st == 2);
+            const unsigned upto = ends ? (ends & (0u - ends)) * 2u - 1u : 0xffffffffu;   // lanes up to the first end
+            const unsigned have = __ballot_sync(0xffffffffu, st != 0) & upto;
+            if ((have >> tid) & 1u) s_part[n + __popc(have & ((1u << tid) - 1u))] = c * 2;
+            n += __popc(have);
+            if (ends) break;
+        }
+        if (tid == 0) s_n = n;
+    }
+    __syncthreads();
+    const int np = s_n;
+    int bad = 0;
+    const PagedSeq q = paged_seq(a.s, rec.y, bad);
+    const int ngrp = (a.G + a.p.gs - 1) / a.p.gs;
+    const int hkv = rec.z / ngrp, hs = rec.z % ngrp;
+    const int gs = min(a.p.gs, a.G - hs * a.p.gs);
+    const int tok = rec.w * a.p.tpt;
+    const int live = min(a.p.tpt, q.n - tok) * gs;
+    const int grp = tid / LPR, e = (tid % LPR) * 4;
+    auto stored = [&](int i) { return a.p.sub == 0 || i < a.p.sub * gs ? i : i - a.p.sub * gs + 128; };
+    auto finish = [&](int i, float m, float l, const float4& o) {
+        const long long row = (long long)(q.tok0 + tok + i / gs) * a.Hq + hkv * a.G + hs * a.p.gs + i % gs;
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        put(static_cast<T*>(a.o) + row * D + e, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+        if (e == 0) a.lse[row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    };
+    if (np <= 12) {                                        // few parts: a row per lane group
+        for (int i = blockIdx.y * GR + grp; i < live; i += gridDim.y * GR) {
+            float m = -INFINITY, l = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = 0; k < np; ++k) {
+                const size_t at = (size_t)s_part[k] * a.p.rows + stored(i);
+                const float2 ml = a.part_ml[at];
+                add_part(m, l, o, ml.x, ml.y, *reinterpret_cast<const float4*>(a.part_o + at * D + e));
+            }
+            finish(i, m, l, o);
+        }
+        return;
+    }
+    for (int i = blockIdx.y; i < live; i += gridDim.y) {   // many parts: the groups share a row's
+        float m = -INFINITY, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int per = (np + GR - 1) / GR;
+        for (int k = grp * per; k < min(np, (grp + 1) * per); ++k) {
+            const size_t at = (size_t)s_part[k] * a.p.rows + stored(i);
+            const float2 ml = a.part_ml[at];
+            add_part(m, l, o, ml.x, ml.y, *reinterpret_cast<const float4*>(a.part_o + at * D + e));
+        }
+        s_o[tid] = o;
+        if (e == 0) {
+            s_m[grp] = m;
+            s_l[grp] = l;
+        }
+        __syncthreads();
+        if (grp == 0) {
+            for (int k = 1; k < GR; ++k) add_part(m, l, o, s_m[k], s_l[k], s_o[k * LPR + tid]);
+            finish(i, m, l, o);
+        }
+        __syncthreads();
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_paged_join(bool f32, int D, const PagedAttnArgs& a, cudaStream_t st) {
+    const dim3 grid(a.p.C, a.p.rows < 8 ? a.p.rows : 8), block(kThreads);
+    switch (D) {
+        case 32:
+            return f32 ? launch_k(paged_join_kernel<float, 32>, grid, block, 0, st, a)
+                       : launch_k(paged_join_kernel<__nv_bfloat16, 32>, grid, block, 0, st, a);
+        case 64:
+            return f32 ? launch_k(paged_join_kernel<float, 64>, grid, block, 0, st, a)
+                       : launch_k(paged_join_kernel<__nv_bfloat16, 64>, grid, block, 0, st, a);
+        case 128: return launch_k(paged_join_kernel<__nv_bfloat16, 128>, grid, block, 0, st, a);
+    }
+    return cudaErrorInvalidValue;
+}
+
+// ---------------------------------------------------------------- which kernel, which split
+int paged_short_bn(int D);
+int paged_f32_bn(bool many);
+
+constexpr int kSms = 152;
+static_assert(2 * kSms <= kMaxParts, "the part list holds every CTA");
+
+PagedKind paged_kind(bool f32, int D, int G, int max_new) {
+    const long long rows = (long long)G * max_new;
+    if (f32) return rows <= 8 ? PAGED_F32_FEW : PAGED_F32_MANY;
+    if (rows <= 16) return PAGED_SHORT16;
+    return PAGED_SHORT32;
+}
+
+PagedSplit paged_split(PagedKind kind, int D, int Hkv, int G) {
+    PagedSplit p = {};
+    auto rows = [&](int r) {
+        p.rows = r;
+        p.gs = G < r ? G : r;
+        p.tpt = r / p.gs;
+        p.hg = Hkv * ((G + p.gs - 1) / p.gs);
+    };
+    p.ovh = 128;
+    p.min_work = 512;
+    switch (kind) {
+        case PAGED_SHORT16:
+        case PAGED_SHORT32:
+            rows(kind == PAGED_SHORT16 ? 16 : 32);
+            p.bn = paged_short_bn(D);
+            p.C = 2 * kSms;
+            break;
+        case PAGED_F32_FEW:
+            rows(8);
+            p.bn = paged_f32_bn(false);
+            p.C = D == 32 ? 2 * kSms : kSms;
+            break;
+        case PAGED_F32_MANY:
+            rows(64);
+            p.bn = paged_f32_bn(true);
+            p.C = 2 * kSms;
+            break;
+        case PAGED_TILES: break;
+    }
+    return p;
+}
+
+size_t paged_part_bytes(const PagedSplit& p, int D) {
+    const size_t parts = 2 * (size_t)p.C;
+    return parts * p.rows * D * sizeof(float) + parts * p.rows * sizeof(float2) + parts * sizeof(int4);
+}
+
+}  // namespace ne

@@ -1,0 +1,230 @@
+// paged_sched.cuh -- how the attention over a paged cache is cut into equal shares.
+//
+// Work units: a sequence's new tokens are cut into tiles of `tpt` tokens, and each tile and
+// head group is one unit: up to `rows` query rows (token, head) that read the same keys,
+// kv(r) = base + min((r + 1) tpt, n) of them in tile r (base = len - n: positions before
+// the new tokens).  A unit costs ovh + kv(r) keys.  The units stand in one line, sequence
+// by sequence, head group by head group, tile by tile; CTA c of C takes the interval
+// [W c / C, W (c + 1) / C) of the total W and walks the units that it touches.  A unit that
+// an interval's end cuts is cut at the key tile nearest to it; both sides compute that tile
+// alike.  So every CTA has the same work whatever the lengths (one sequence of 100,000
+// positions beside fifty of ten, a prompt beside single tokens), no list is built, and the
+// split depends on the lengths alone, never on timing.
+//
+// Parts of cut units go to the workspace: a CTA has at most one part that begins inside a
+// unit (its first, slot 0) and one that begins a unit and leaves its end to others (its
+// last, slot 1).  The join kernel starts from the slot-1 records and walks the following
+// CTAs' slot-0 records to the one marked last.
+#pragma once
+#include "paged.h"
+#include "ptx.cuh"
+
+namespace ne {
+
+struct PagedSeq {
+    int tok0, n, len;
+};
+
+// Row range and length of sequence b, clamped to what the tensors hold; `bad` collects
+// which argument was out of range.
+__device__ __forceinline__ PagedSeq paged_seq(const PagedBatch& s, int b, int& bad) {
+    PagedSeq q;
+    if (s.cu) {
+        const int c0 = __ldg(s.cu + b), c1 = __ldg(s.cu + b + 1);
+        if (c0 < 0 || c1 > s.N || c1 < c0) bad = SITE_PAGED_CU;
+        q.tok0 = min(max(c0, 0), s.N);
+        q.n = min(max(c1, q.tok0), s.N) - q.tok0;
+    } else {
+        q.tok0 = b;
+        q.n = 1;
+    }
+    const int l = __ldg(s.lens + b);
+    if (l < 0 || l > s.cap) bad = SITE_PAGED_LEN;
+    q.len = min(max(l, 0), s.cap);
+    return q;
+}
+
+// Cost of tiles 0 .. r-1 of a sequence (r below its tile count): each ovh + max(0, base + (k+1) tpt).
+__device__ __forceinline__ long long paged_prefix(int r, int base, int tpt, int ovh) {
+    const int r0 = base < 0 ? min(r, -base / tpt) : 0;    // tiles without a key
+    const long long m = r - r0;
+    return (long long)r * ovh + m * base + (long long)tpt * (((long long)r * (r + 1) - (long long)r0 * (r0 + 1)) / 2);
+}
+
+// Cost of one head group of a sequence.
+__device__ __forceinline__ long long paged_group_cost(const PagedSeq& q, int tpt, int ovh) {
+    if (q.n == 0) return 0;
+    const int nt = (q.n + tpt - 1) / tpt;
+    return paged_prefix(nt - 1, q.len - q.n, tpt, ovh) + ovh + q.len;
+}
+
+// What a CTA does with one unit: key tiles [t0, t1) of nt_keys, for tokens tok .. tok+ntok-1
+// of the sequence.
+struct PagedSeg {
+    int b, hg, r;
+    int tok, ntok;      // first token of the unit within the sequence, and how many
+    int tok0, base;     // the sequence's first row; position of its token 0
+    int kv;             // keys the unit may see (0: rows with nothing to attend to)
+    int t0, t1, nt;     // key tiles of this part; key tiles of the unit
+    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == nt; }
+    __device__ __forceinline__ int slot() const { return t0 == 0 ? 1 : 0; }
+};
+
+struct PagedWalk {
+    long long w0, w1;   // the CTA's interval
+    long long cur;      // start of the current unit
+    PagedSeq q;
+    int b, hg, r, nt;
+
+    __device__ __forceinline__ void load(const PagedAttnArgs& a) {
+        int bad = 0;
+        q = paged_seq(a.s, b, bad);
+        nt = (q.n + a.p.tpt - 1) / a.p.tpt;
+    }
+    // From the sequence that holds w0 and where that sequence starts.
+    __device__ __forceinline__ void init(const PagedAttnArgs& a, long long w0_, long long w1_, int b_, long long start) {
+        w0 = w0_;
+        w1 = w1_;
+        b = b_;
+        cur = start;
+        if (w0 >= w1) {
+            cur = w1;
+            return;
+        }
+        load(a);
+        const long long S = paged_group_cost(q, a.p.tpt, a.p.ovh);
+        const long long off = w0 - start;
+        hg = (int)(off / S);
+        const long long x = off - (long long)hg * S;
+        int lo = 0, hi = nt - 1;                           // the last tile whose start is at or before x
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (paged_prefix(mid, q.len - q.n, a.p.tpt, a.p.ovh) <= x) lo = mid;
+            else hi = mid - 1;
+        }
+        r = lo;
+        cur = start + (long long)hg * S + paged_prefix(r, q.len - q.n, a.p.tpt, a.p.ovh);
+    }
+    // The next part of the interval, false at its end.
+    __device__ __forceinline__ bool next(const PagedAttnArgs& a, PagedSeg& g) {
+        while (cur < w1) {
+            const int base = q.len - q.n;
+            const int kv = r == nt - 1 ? q.len : max(0, base + (r + 1) * a.p.tpt);
+            const int cost = a.p.ovh + kv;
+            const int ntk = (kv + a.p.bn - 1) / a.p.bn;
+            g.t0 = w0 <= cur ? 0 : (int)(((w0 - cur) * ntk + cost / 2) / cost);
+            g.t1 = w1 >= cur + cost ? ntk : (int)(((w1 - cur) * ntk + cost / 2) / cost);
+            g.b = b;
+            g.hg = hg;
+            g.r = r;
+            g.tok = r * a.p.tpt;
+            g.ntok = min(a.p.tpt, q.n - g.tok);
+            g.tok0 = q.tok0;
+            g.base = base;
+            g.kv = kv;
+            g.nt = ntk;
+            const bool mine = g.t0 < g.t1 || (ntk == 0 && w0 <= cur);   // a unit without keys: its rows are still written
+            cur += cost;
+            if (++r == nt) {
+                r = 0;
+                if (++hg == a.p.hg) {
+                    hg = 0;
+                    do ++b;
+                    while (b < a.s.B && (load(a), q.n == 0));
+                    if (b >= a.s.B) cur = w1 > cur ? w1 : cur;         // (the line ends here)
+                }
+            }
+            if (mine) return true;
+        }
+        return false;
+    }
+};
+
+// Shared scratch of paged_locate.
+struct PagedLocate {
+    long long warp_sum[32];
+    long long w0, w1, start;
+    int b;
+};
+
+// All T threads of the CTA: the total work, this CTA's interval, and the sequence that its
+// start falls into.  Two passes over the lengths when they exceed T sequences (the first
+// sums, the second finds), one otherwise.
+template <int T>
+__device__ __forceinline__ void paged_locate(const PagedAttnArgs& a, int c, PagedLocate& sm, bool report) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int B = a.s.B;
+    int bad = 0;
+    auto work = [&](int b) -> long long {
+        if (b >= B) return 0;
+        const PagedSeq q = paged_seq(a.s, b, bad);
+        return paged_group_cost(q, a.p.tpt, a.p.ovh) * a.p.hg;
+    };
+    // Inclusive sums over the CTA; the total in sm.warp_sum[T / 32 - 1].
+    auto scan = [&](long long x) -> long long {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) sm.warp_sum[warp] = x;
+        __syncthreads();
+        if (warp == 0) {
+            long long y = lane < T / 32 ? sm.warp_sum[lane] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long z = __shfl_up_sync(0xffffffffu, y, o);
+                if (lane >= o) y += z;
+            }
+            sm.warp_sum[lane] = y;
+        }
+        __syncthreads();
+        return x + (warp ? sm.warp_sum[warp - 1] : 0);
+    };
+    auto interval = [&](long long total) {
+        const long long most = total / a.p.min_work;
+        const int C = most < 1 ? 1 : (most < a.p.C ? (int)most : a.p.C);
+        const long long each = total / C, rest = total % C;
+        const long long i = min(c, C), j = min(c + 1, C);
+        sm.w0 = each * i + min(i, rest);
+        sm.w1 = each * j + min(j, rest);
+        sm.start = 0;
+        sm.b = 0;
+    };
+    long long mine = work(tid), incl = scan(mine);
+    long long total = sm.warp_sum[T / 32 - 1];
+    for (int b0 = T; b0 < B; b0 += T) {
+        __syncthreads();
+        scan(work(b0 + tid));
+        total += sm.warp_sum[T / 32 - 1];
+    }
+    if (tid == 0) interval(total);
+    __syncthreads();
+    const long long w0 = sm.w0, w1 = sm.w1;
+    if (w0 < w1) {
+        long long before = 0;
+        for (int b0 = 0; b0 < B; b0 += T) {
+            if (B > T) {
+                mine = work(b0 + tid);
+                __syncthreads();
+                incl = scan(mine);
+            }
+            const long long end = before + incl;
+            if (mine > 0 && w0 >= end - mine && w0 < end) {   // exactly one thread of one pass
+                sm.b = b0 + tid;
+                sm.start = end - mine;
+            }
+            before += sm.warp_sum[T / 32 - 1];
+            if (w0 < before) break;                           // (uniform)
+        }
+    }
+    if (report && bad) report_error(a.err, bad);
+    __syncthreads();
+}
+
+// The records of both slots of CTA c are written by every call (state 0: no such part).
+__device__ __forceinline__ int4 paged_record(const PagedSeg& g) {
+    return make_int4(g.t1 == g.nt ? 2 : 1, g.b, g.hg, g.r);
+}
+
+}  // namespace ne

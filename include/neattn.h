@@ -266,6 +266,149 @@ ne_status ne_qkv_prologue(const void* x, const void* gamma, const void* w, void*
                           double rope_theta, int rotate, void* workspace, size_t workspace_bytes,
                           ne_stream_t stream);
 
+/* ------------------------------------------------------------------ paged cache
+ * A key/value cache in pages of `page_size` positions, for generation over many sequences
+ * of different and growing lengths (generation: "NanoEuler – 순수 C/CUDA로 처음부터 만든
+ * GPT-2 규모 언어 모델", Code Example; the pages describe no paged cache: its design is this
+ * library's).  Position p of sequence b lies in slot p % page_size of page
+ * page_table[b][p / page_size].  Keys are stored ROTATED (ne_paged_append rotates them
+ * once; the contiguous cache of ne_attn_decode holds them unrotated), so attention over
+ * pages rotates nothing and its queries come rotated from ne_paged_append too.
+ *
+ * One pool of keys and one of values, over `layers` layers that share the page tables:
+ * element d of head h in slot t of page p of layer l lies at
+ *   l * layer_stride + p * page_stride + t * tok_stride + h * head_stride + d   (elements).
+ * The strides cover [layers, pages, page_size, Hkv, D] as well as head-major pages and
+ * pools with keys and values side by side.  ne_paged_append and ne_paged_attn work on one
+ * layer (layers = 1, k and v pointing at it); the ne_pages_* calls move page contents of
+ * every layer at once.
+ * Supported: page_size a power of two from 8 to 256; D in {32, 64, 128} for bf16
+ * (elem_bytes 2) and {32, 64} for f32 (elem_bytes 4); k, v 16-byte aligned and strides
+ * multiples of 16 bytes, below 2^39 elements, the strides of an extent above 1 at least D; n_pages < 2^24. */
+typedef struct {
+    void* k;
+    void* v;
+    int elem_bytes;             /* 2 (bf16) or 4 (f32) */
+    int layers, n_pages, page_size, Hkv, D;
+    int64_t layer_stride, page_stride, tok_stride, head_stride;
+} ne_paged_cache;
+
+/* Rotary positions as a value (host struct; ne_rope_spec_init fills it, the caller keeps
+ * it).  Pair i < rot_dim / 2 of a row at position p is rotated by the angle p * f_i; the
+ * elements from rot_dim on pass through.  layout 0: pairs (2i, 2i+1), the attention calls'
+ * convention; layout 1: pairs (i, i + rot_dim/2).  f_i = theta^(-2i/rot_dim), changed by
+ *   NE_ROPE_NONE   nothing;
+ *   NE_ROPE_LINEAR f_i / factor (positions interpolated);
+ *   NE_ROPE_BASE   theta replaced by theta * factor^(rot_dim / (rot_dim - 2));
+ *   NE_ROPE_PARTS  f_i (g + (1 - g) / factor), g = clamp((n_i - beta_slow) / (beta_fast -
+ *                  beta_slow), 0, 1), n_i = orig_len * f_i / (2 pi) the turns of the pair over
+ *                  the trained context: fast pairs keep their angle, slow ones interpolate.
+ * cos and sin are multiplied by mscale.  The angle is kept as a 64-bit fraction of a turn
+ * (turns[i] = f_i / (2 pi) * 2^64), so p * turns[i] mod 2^64 is exact for every position:
+ * far positions lose nothing and no table is built. */
+enum { NE_ROPE_NONE = 0, NE_ROPE_LINEAR = 1, NE_ROPE_BASE = 2, NE_ROPE_PARTS = 3 };
+typedef struct {
+    int D, rot_dim, layout;
+    float mscale;
+    uint64_t turns[64];
+} ne_rope_spec;
+ne_status ne_rope_spec_init(ne_rope_spec* out, int D, int rot_dim, int layout, double theta, int scaling,
+                            double factor, int orig_len, double beta_fast, double beta_slow, double mscale);
+
+/* New tokens into the cache: the rows of sequence b are cu_new[b] .. cu_new[b+1]-1 of the
+ * packed inputs, n_b of them, and take positions seq_lens[b] - n_b .. seq_lens[b] - 1
+ * (seq_lens counts them already).  k rows are rotated (spec at position + pos_offset; a null spec stores
+ * them as they are) and stored, v rows are stored; with q, the query rows are rotated into
+ * q_out (which may be q itself, with the same row stride).
+ *   k, v  [N, Hkv, D] rows k_ld, v_ld elements apart;  q [N, Hq, D] rows q_ld apart
+ *   q_out [N, Hq, D] rows q_out_ld apart (both or neither of q, q_out; Hq ignored without)
+ *   page_table [B, max_pages] int32, seq_lens [B] int32, cu_new [B+1] int32 or NULL
+ *   (one row per sequence, N == B); device memory, 4-byte aligned.
+ *   pos_offset: added to every position for the rotation alone (a cache that dropped its
+ *   first pages); 0 <= pos_offset < 2^30.
+ * Rows outside [cu_new[0], cu_new[B]) are neither read nor written.  A row whose position
+ * is negative (n_b > seq_lens[b]) is not stored and gets q_out = 0.  Bad device-side
+ * arguments never reach memory: a cu_new entry outside [0, N] or decreasing, a length
+ * outside [0, max_pages * page_size], a page id outside [0, n_pages) are clamped or skipped
+ * and reported by ne_get_device_error() as NE_ERR_INVALID_ARG.  No two rows may name one
+ * slot (a page to be written belongs to one sequence; ne_pages_fork sees to it).
+ * Row strides are multiples of 16 bytes.  N * max(Hq, Hkv) * D < 2^31. */
+ne_status ne_paged_append(const void* q, const void* k, const void* v, const ne_paged_cache* cache,
+                          const int* page_table, const int* seq_lens, const int* cu_new,
+                          const ne_rope_spec* spec, int pos_offset, void* q_out, int64_t q_ld, int64_t k_ld, int64_t v_ld,
+                          int64_t q_out_ld, int B, int N, int Hq, int max_pages, ne_stream_t stream);
+ne_status ne_paged_append_f32(const float* q, const float* k, const float* v, const ne_paged_cache* cache,
+                              const int* page_table, const int* seq_lens, const int* cu_new,
+                              const ne_rope_spec* spec, int pos_offset, float* q_out, int64_t q_ld, int64_t k_ld, int64_t v_ld,
+                              int64_t q_out_ld, int B, int N, int Hq, int max_pages, ne_stream_t stream);
+
+/* Attention of the new tokens over the pages: row i of sequence b (packed as above), at
+ * position seq_lens[b] - n_b + i, attends to the cached positions up to its own.  n_b = 1 is
+ * a generation step, n_b = seq_lens[b] a whole prompt, anything between a chunk; one call
+ * mixes them.
+ *   q   [N, Hq, D] rotated, rows q_ld elements apart (in)
+ *   o   [N, Hq, D] dense (out)        lse [N, Hq] fp32, natural log (out)
+ * Rows outside [cu_new[0], cu_new[B]) stay as they were.  A row with nothing to attend to
+ * (a negative position) gets o = 0 and lse = -inf.  Slots at or behind a sequence's length
+ * may hold anything (NaN included); values in front of it must be finite.
+ * max_new: the largest n_b as far as the caller knows (N if not).  It chooses between
+ * kernels (a few rows per kv head stream the cache through registers; more use tcgen05
+ * tiles) and changes no result beyond rounding: any n_b is right with any max_new >= 1.
+ * bf16: tensor-core products of bf16 inputs with fp32 accumulation and fp32 softmax
+ * statistics; f32: fp32 throughout (no TF32).  Work is split over the key axis by counted
+ * work, so results depend on the shape, lengths and device but never on timing: the same
+ * call gives the same bits.  workspace: ne_paged_attn_workspace_size() bytes, 256-byte
+ * aligned, caller-owned, rewritten by every call (two calls that may overlap need two).
+ * Device-side arguments are checked as in ne_paged_append; a bad page id reads as zeros. */
+size_t ne_paged_attn_workspace_size(int B, int N, int Hq, int Hkv, int D);
+ne_status ne_paged_attn(const void* q, const ne_paged_cache* cache, const int* page_table, const int* seq_lens,
+                        const int* cu_new, void* o, float* lse, int64_t q_ld, int B, int N, int Hq,
+                        int max_pages, int max_new, void* workspace, size_t workspace_bytes, ne_stream_t stream);
+ne_status ne_paged_attn_f32(const float* q, const ne_paged_cache* cache, const int* page_table,
+                            const int* seq_lens, const int* cu_new, float* o, float* lse, int64_t q_ld, int B,
+                            int N, int Hq, int max_pages, int max_new, void* workspace, size_t workspace_bytes,
+                            ne_stream_t stream);
+
+/* Pages of sequences.  The pool's state is refcount [n_pages] int32 (device memory, owned
+ * by the caller, zero at first): a page is free when its count is 0.  New pages are always
+ * the lowest free ids, in the order of the sequences, so a call has one result.  Every
+ * call is all or nothing: when the pool has too few free pages, short_out[0] is how many
+ * are missing, the outputs equal the inputs (for a fork: every child empty) and no page is
+ * written; otherwise it is 0.  refcount_out (and, but for a fork, table_out) may be the
+ * input itself; partial overlaps are refused.  Nothing synchronises: a whole scheduling
+ * step can be captured.  page_table entries behind a sequence's pages are -1 on output.
+ * workspace: ne_pages_workspace_size(n_pages, n, max_pages) bytes, n the number of
+ * sequences (for a fork: of children), 256-byte aligned, caller-owned, rewritten by every call.  int arrays
+ * are 16-byte aligned.  Bad ids are skipped and reported by ne_get_device_error().
+ *
+ * ne_pages_fork: child c continues sequence parents[c] (-1: an empty child).  Shared
+ * (deep == 0): whole pages are shared (their counts rise), the partly filled last page is
+ * copied to a new page, so a page that is still written belongs to one sequence.  deep:
+ * every page is copied.  Only filled slots are copied.
+ *   child_table [C, max_pages] (out), child_lens [C] (out) */
+size_t ne_pages_workspace_size(int n_pages, int n, int max_pages);
+ne_status ne_pages_fork(const ne_paged_cache* cache, const int* refcount, const int* page_table,
+                        const int* seq_lens, const int* parents, int deep, int* refcount_out,
+                        int* child_table, int* child_lens, int* short_out, int B, int C, int max_pages,
+                        void* workspace, size_t workspace_bytes, ne_stream_t stream);
+/* ne_pages_resize: sequence b goes from seq_lens[b] to new_lens[b] positions (0 frees it).
+ * Pages behind the new length are given back first, then a partly filled last page (of
+ * min(old, new) positions) that other sequences still hold is copied to a page of its own,
+ * then new pages are taken; a page that only such copies leave behind is free for the
+ * next call.  seq_lens itself is left to the caller.  Lengths are clamped to
+ * [0, max_pages * page_size] and reported. */
+ne_status ne_pages_resize(const ne_paged_cache* cache, const int* refcount, const int* page_table,
+                          const int* seq_lens, const int* new_lens, int* refcount_out, int* table_out,
+                          int* short_out, int B, int max_pages, void* workspace, size_t workspace_bytes,
+                          ne_stream_t stream);
+/* ne_pages_compact: moves the live pages into 0 .. n_live - 1: the j-th live page at or
+ * behind n_live goes to the j-th free page in front of it, the others stay.
+ *   remap [n_pages] (out): a live page's new id, -1 for a free page;  n_live [1] (out)
+ * The one table given is rewritten; further tables go through remap.  Never short. */
+ne_status ne_pages_compact(const ne_paged_cache* cache, const int* refcount, const int* page_table,
+                           int* refcount_out, int* table_out, int* remap, int* n_live, int B, int max_pages,
+                           void* workspace, size_t workspace_bytes, ne_stream_t stream);
+
 /* Human-readable name of a status code (static string). */
 const char* ne_status_string(ne_status s);
 /* Detail of the last error on the calling thread ("" if none). */
