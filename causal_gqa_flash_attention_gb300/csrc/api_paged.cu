@@ -169,13 +169,37 @@ ne_status append_impl(int eb, const void* q, const void* k, const void* v, const
     return NE_OK;
 }
 
+// Tensor maps of the tile kernel: a query box is (64 columns, G heads, `sub` tokens), a
+// key or value box (64 columns, one head, the rows of a page that fall into one tile).
+ne_status tile_maps(CUtensorMap* tq, CUtensorMap* tk, CUtensorMap* tv, const ne_paged_cache* c, const ne::PagedAttnArgs& a) {
+    EncodeTiledFn enc;
+    ne_status s = encode_fn(&enc);
+    if (s != NE_OK) return s;
+    auto encode = [&](CUtensorMap* m, const void* p, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                      const cuuint32_t* box) -> ne_status {
+        const cuuint32_t one[4] = {1, 1, 1, 1};
+        CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(p), dims, strides, box, one,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        return r == CUDA_SUCCESS ? NE_OK : fail(NE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+    };
+    const cuuint64_t qd[3] = {(cuuint64_t)c->D, (cuuint64_t)a.Hq, (cuuint64_t)a.s.N};
+    const cuuint64_t qs[2] = {(cuuint64_t)c->D * 2, (cuuint64_t)a.q_ld * 2};
+    const cuuint32_t qb[3] = {64, (cuuint32_t)a.G, (cuuint32_t)a.p.sub};
+    if ((s = encode(tq, a.q, 3, qd, qs, qb)) != NE_OK) return s;
+    const cuuint64_t kd[4] = {(cuuint64_t)c->D, (cuuint64_t)c->Hkv, (cuuint64_t)c->page_size, (cuuint64_t)c->n_pages};
+    const cuuint64_t ks[3] = {(cuuint64_t)a.c.head_stride * 2, (cuuint64_t)a.c.tok_stride * 2, (cuuint64_t)a.c.page_stride * 2};
+    const cuuint32_t kb[4] = {64, 1, (cuuint32_t)std::min(c->page_size, 128), 1};
+    if ((s = encode(tk, a.c.k, 4, kd, ks, kb)) != NE_OK) return s;
+    return encode(tv, a.c.v, 4, kd, ks, kb);
+}
+
 size_t attn_ws_bytes(int D, int Hkv, int G) {
     size_t most = 0;
     for (int f32 = 0; f32 < 2; ++f32)
         for (int rows : {1, 8, 9, 16, 17, 32, 33, 1 << 20}) {
             if (f32 && D > 64) continue;
-            const ne::PagedKind kind = ne::paged_kind(f32 != 0, D, 1, rows);
-            if (kind == ne::PAGED_TILES && G > 128) continue;
+            const ne::PagedKind kind = ne::paged_kind(f32 != 0, D, G, rows);
             most = std::max(most, ne::paged_part_bytes(ne::paged_split(kind, D, Hkv, G), D));
         }
     return round_up(most, 256);
@@ -222,7 +246,11 @@ ne_status attn_impl(int eb, const void* q, const ne_paged_cache* c, const int* t
     a.timeout_ns = timeout_ns();
     cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e;
-    if (f32) e = ne::launch_paged_f32(kind, c->D, a, st);
+    if (kind == ne::PAGED_TILES) {
+        CUtensorMap tq, tk, tv;
+        if ((s = tile_maps(&tq, &tk, &tv, c, a)) != NE_OK) return s;
+        e = ne::launch_paged_tiles(c->D, tq, tk, tv, a, st);
+    } else if (f32) e = ne::launch_paged_f32(kind, c->D, a, st);
     else e = ne::launch_paged_short(kind, c->D, a, st);
     if (e != cudaSuccess) return cuda_fail(e, "paged_attn launch");
     e = ne::launch_paged_join(f32, c->D, a, st);

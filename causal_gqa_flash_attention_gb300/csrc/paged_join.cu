@@ -142,7 +142,7 @@ PagedKind paged_kind(bool f32, int D, int G, int max_new) {
     const long long rows = (long long)G * max_new;
     if (f32) return rows <= 8 ? PAGED_F32_FEW : PAGED_F32_MANY;
     if (rows <= 16) return PAGED_SHORT16;
-    return PAGED_SHORT32;
+    return rows <= 32 || D == 32 || G > 128 ? PAGED_SHORT32 : PAGED_TILES;
 }
 
 PagedSplit paged_split(PagedKind kind, int D, int Hkv, int G) {
@@ -172,7 +172,15 @@ PagedSplit paged_split(PagedKind kind, int D, int Hkv, int G) {
             p.bn = paged_f32_bn(true);
             p.C = 2 * kSms;
             break;
-        case PAGED_TILES: break;
+        case PAGED_TILES:                                  // G <= 128
+            p.rows = 256;
+            p.gs = G;
+            p.sub = 128 / G;
+            p.tpt = 2 * p.sub;
+            p.hg = Hkv;
+            p.bn = 128;
+            p.C = kSms;
+            break;
     }
     return p;
 }

@@ -64,6 +64,7 @@ struct PagedSeg {
     int b, hg, r;
     int tok, ntok;      // first token of the unit within the sequence, and how many
     int tok0, base;     // the sequence's first row; position of its token 0
+    int len;            // the sequence's length
     int kv;             // keys the unit may see (0: rows with nothing to attend to)
     int t0, t1, nt;     // key tiles of this part; key tiles of the unit
     __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == nt; }
@@ -121,6 +122,7 @@ struct PagedWalk {
             g.ntok = min(a.p.tpt, q.n - g.tok);
             g.tok0 = q.tok0;
             g.base = base;
+            g.len = q.len;
             g.kv = kv;
             g.nt = ntk;
             const bool mine = g.t0 < g.t1 || (ntk == 0 && w0 <= cur);   // a unit without keys: its rows are still written
