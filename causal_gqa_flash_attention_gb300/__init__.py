@@ -11,7 +11,6 @@ Layouts: q, o, dO, dq are [B, T, Hq, D]; k, v, dk, dv are [B, T, Hkv, D]; lse is
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import threading
@@ -380,63 +379,79 @@ def rope_spec(D: int, rot_dim: int | None = None, theta: float = 10000.0, layout
     return out
 
 
-def _on(device):
-    """The device's context when it is not the current one (kernels launch on the current)."""
-    return torch.cuda.device(device) if torch.cuda.current_device() != device.index else contextlib.nullcontext()
+# A generation step is a few small kernels, so these bindings keep the host's share low:
+# plain comparisons, addresses as integers, and no stream object (the current stream's
+# handle is all the C calls take).
+
+def _launch(fn, index, *args):
+    """Calls fn with the device's current stream as last argument, on that device."""
+    if torch.cuda.current_device() == index:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status != NE_OK:
+        _check(status)
 
 
 def _paged_cache(k_pages, v_pages, layers: bool) -> PagedCache:
     """The pools [P, page_size, Hkv, D] ([L, P, page_size, Hkv, D] with `layers`) as the C
     struct.  Any strides in multiples of 16 bytes with D dense (head-major pages are a
     transposed view), the same for both."""
-    if layers and k_pages.dim() == 4:
-        k_pages, v_pages = k_pages.unsqueeze(0), v_pages.unsqueeze(0)
-    want = 5 if layers else 4
-    if k_pages.dim() != want or v_pages.shape != k_pages.shape:
+    shape, st = k_pages.shape, k_pages.stride()
+    nd = len(shape)
+    if nd not in ((4, 5) if layers else (4,)) or v_pages.shape != shape:
         raise ValueError(f"k_pages and v_pages must be [{'L, ' if layers else ''}P, page_size, Hkv, D]; got "
-                         f"{tuple(k_pages.shape)}, {tuple(v_pages.shape)}")
+                         f"{tuple(shape)}, {tuple(v_pages.shape)}")
+    dt = k_pages.dtype
     if not k_pages.is_cuda or v_pages.device != k_pages.device:
         raise ValueError("k_pages and v_pages must be CUDA tensors on one device")
-    if k_pages.dtype not in (torch.bfloat16, torch.float32) or v_pages.dtype != k_pages.dtype:
+    if (dt is not torch.bfloat16 and dt is not torch.float32) or v_pages.dtype is not dt:
         raise ValueError("k_pages and v_pages must both be bfloat16 or float32")
-    st = k_pages.stride()
     if v_pages.stride() != st or st[-1] != 1:
         raise ValueError("k_pages and v_pages must have the same strides, D dense")
-    shape = k_pages.shape
-    L, ls = (shape[0], st[0]) if layers else (1, 0)
+    L, ls = (shape[0], st[0]) if nd == 5 else (1, 0)
     P, ps, H, D = shape[-4:]
-    return PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), k_pages.element_size(), L, P, ps, H, D, ls, st[-4], st[-3],
-                      st[-2])
+    return PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), 2 if dt is torch.bfloat16 else 4, L, P, ps, H, D, ls, st[-4],
+                      st[-3], st[-2])
 
 
-def _check_ints(device, **tensors):
-    for name, (t, shape) in tensors.items():
-        if t.dtype != torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous int32 CUDA tensor {list(shape)} on the pages' device")
+def _ws(t, device):
+    """Address and bytes of a workspace."""
+    if t.device != device or not t.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on the pages' device")
+    return t.data_ptr(), t.nbytes
 
 
-def _check_paged_batch(page_table, seq_lens, cu_new, N, device):
-    if page_table.dim() != 2:
+def _ints(t, shape, device, name):
+    """Address of an int32 tensor of that shape."""
+    if t.dtype is not torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor {list(shape)} on the pages' device")
+    return t.data_ptr()
+
+
+def _paged_batch(page_table, seq_lens, cu_new, N, device):
+    """B, max_pages and the addresses of page_table, seq_lens and cu_new (0: one row each)."""
+    shape = page_table.shape
+    if len(shape) != 2:
         raise ValueError("page_table must be [B, max_pages]")
-    B = page_table.shape[0]
-    ints = {"page_table": (page_table, page_table.shape), "seq_lens": (seq_lens, (B,))}
-    if cu_new is not None:
-        ints["cu_new"] = (cu_new, (B + 1,))
-    elif N != B:
+    B = shape[0]
+    if cu_new is None and N != B:
         raise ValueError(f"without cu_new every sequence has one row: {N} rows for {B} sequences")
-    _check_ints(device, **ints)
-    return B
+    return (B, shape[1], _ints(page_table, shape, device, "page_table"), _ints(seq_lens, (B,), device, "seq_lens"),
+            0 if cu_new is None else _ints(cu_new, (B + 1,), device, "cu_new"))
 
 
-def _rows(t, name, heads, like):
+def _rows(t, name, N, heads, c, like, device):
     """Row stride of a [N, heads, D] tensor whose rows are dense."""
-    D = like.shape[-1]
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D or t.dtype != like.dtype or t.device != like.device:
-        raise ValueError(f"{name} must be a [N, {heads}, {D}] {like.dtype} tensor on the pages' device; got "
+    D = c.D
+    if t.shape != (N, heads, D) or t.dtype is not like.dtype or t.device != device:
+        raise ValueError(f"{name} must be a {[N, heads, D]} {like.dtype} tensor on the pages' device; got "
                          f"{tuple(t.shape)} {t.dtype}")
-    if (D > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != D):
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (heads > 1 and s1 != D):
         raise ValueError(f"{name}: the heads of a row must be dense")
-    return t.stride(0) if t.shape[0] > 1 else heads * D
+    return s0 if N > 1 else heads * D
 
 
 def paged_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_new=None, rope=None, pos_offset: int = 0, q=None,
@@ -446,29 +461,25 @@ def paged_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_new=None, rope
     seq_lens[b] - n_b .. seq_lens[b] - 1 of its pages, k rotated by `rope` (a rope_spec, None:
     not).  With q [N, Hq, D] the query rows are rotated into q_out (which may be q), returned.
     Row slices of one fused projection are taken as they are."""
-    lib = load()
+    lib = _lib or load()
     c = _paged_cache(k_pages, v_pages, False)
+    dev = k_pages.device
     N = k.shape[0]
-    B = _check_paged_batch(page_table, seq_lens, cu_new, N, k_pages.device)
-    k_ld, v_ld = _rows(k, "k", c.Hkv, k_pages), _rows(v, "v", c.Hkv, k_pages)
-    if v.shape[0] != N:
-        raise ValueError("k and v must have the same rows")
-    Hq, q_ld, qo_ld = 0, 0, 0
+    B, W, pt, ln, cu = _paged_batch(page_table, seq_lens, cu_new, N, dev)
+    k_ld, v_ld = _rows(k, "k", N, c.Hkv, c, k_pages, dev), _rows(v, "v", N, c.Hkv, c, k_pages, dev)
+    Hq = q_ld = qo_ld = qp = qop = 0
     if q is not None:
         Hq = q.shape[1]
-        q_ld = _rows(q, "q", Hq, k_pages)
+        q_ld = _rows(q, "q", N, Hq, c, k_pages, dev)
         if q_out is None:
-            q_out = torch.zeros((N, Hq, c.D), dtype=q.dtype, device=q.device)
-        qo_ld = _rows(q_out, "q_out", Hq, k_pages)
-        if q.shape[0] != N or q_out.shape[0] != N:
-            raise ValueError("q, q_out, k and v must have the same rows")
+            q_out = torch.zeros((N, Hq, c.D), dtype=q.dtype, device=dev)
+        qo_ld = _rows(q_out, "q_out", N, Hq, c, k_pages, dev)
+        qp, qop = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out needs q")
-    fn = lib.ne_paged_append if c.elem_bytes == 2 else lib.ne_paged_append_f32
-    with _on(k_pages.device):
-        _check(fn(_ptr(q), _ptr(k), _ptr(v), ctypes.byref(c), _ptr(page_table), _ptr(seq_lens), _ptr(cu_new),
-                  ctypes.byref(rope) if rope is not None else None, pos_offset, _ptr(q_out), q_ld, k_ld, v_ld, qo_ld, B, N,
-                  Hq, page_table.shape[1], _stream(k_pages)))
+    _launch(lib.ne_paged_append if c.elem_bytes == 2 else lib.ne_paged_append_f32, dev.index, qp, k.data_ptr(), v.data_ptr(),
+            ctypes.byref(c), pt, ln, cu, ctypes.byref(rope) if rope is not None else None, pos_offset, qop, q_ld, k_ld, v_ld,
+            qo_ld, B, N, Hq, W)
     return q_out
 
 
@@ -488,26 +499,25 @@ def paged_attn(q, k_pages, v_pages, page_table, seq_lens, cu_new=None, max_new: 
     seq_lens[b] - n_b + i + 1 positions.  Returns (o [N, Hq, D], lse [N, Hq] fp32); rows
     outside the sequences are not written (zeros in a fresh o and lse).  max_new: the most
     new tokens of a sequence, if known (a choice of kernel, not of results)."""
-    lib = load()
+    lib = _lib or load()
     c = _paged_cache(k_pages, v_pages, False)
-    N, Hq = q.shape[0], q.shape[1]
-    B = _check_paged_batch(page_table, seq_lens, cu_new, N, k_pages.device)
-    q_ld = _rows(q, "q", Hq, k_pages)
+    dev = k_pages.device
+    N, Hq = q.shape[:2]
+    B, W, pt, ln, cu = _paged_batch(page_table, seq_lens, cu_new, N, dev)
+    q_ld = _rows(q, "q", N, Hq, c, k_pages, dev)
     if o is None:
-        o = torch.zeros((N, Hq, c.D), dtype=q.dtype, device=q.device)
-    elif o.shape != q.shape or o.dtype != q.dtype or o.device != q.device or not o.is_contiguous():
+        o = torch.zeros((N, Hq, c.D), dtype=q.dtype, device=dev)
+    elif o.shape != q.shape or o.dtype is not q.dtype or o.device != dev or not o.is_contiguous():
         raise ValueError("o must be contiguous and match q")
     if lse is None:
-        lse = torch.zeros((N, Hq), dtype=torch.float32, device=q.device)
-    elif lse.shape != (N, Hq) or lse.dtype != torch.float32 or lse.device != q.device or not lse.is_contiguous():
+        lse = torch.zeros((N, Hq), dtype=torch.float32, device=dev)
+    elif lse.shape != (N, Hq) or lse.dtype is not torch.float32 or lse.device != dev or not lse.is_contiguous():
         raise ValueError("lse must be contiguous fp32 [N, Hq]")
     if workspace is None:
-        workspace = alloc_paged_workspace(B, N, Hq, c.Hkv, c.D, q.device)
-    fn = lib.ne_paged_attn if c.elem_bytes == 2 else lib.ne_paged_attn_f32
-    with _on(k_pages.device):
-        _check(fn(_ptr(q), ctypes.byref(c), _ptr(page_table), _ptr(seq_lens), _ptr(cu_new), _ptr(o), _ptr(lse), q_ld, B, N,
-                  Hq, page_table.shape[1], max(1, N if max_new is None else max_new), _ptr(workspace),
-                  workspace.numel() * workspace.element_size(), _stream(k_pages)))
+        workspace = alloc_paged_workspace(B, N, Hq, c.Hkv, c.D, dev)
+    _launch(lib.ne_paged_attn if c.elem_bytes == 2 else lib.ne_paged_attn_f32, dev.index, q.data_ptr(), ctypes.byref(c), pt,
+            ln, cu, o.data_ptr(), lse.data_ptr(), q_ld, B, N, Hq, W, max(1, N) if max_new is None else max_new,
+            *_ws(workspace, dev))
     return o, lse
 
 
@@ -517,18 +527,8 @@ def alloc_pages_workspace(n_pages: int, n: int, max_pages: int, device="cuda"):
                        device=device)
 
 
-def _pages_call(k_pages, v_pages, refcount, page_table, n, refcount_out, workspace):
-    c = _paged_cache(k_pages, v_pages, True)
-    dev = k_pages.device
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be [B, max_pages]")
-    if refcount_out is None:
-        refcount_out = torch.empty_like(refcount)
-    _check_ints(dev, refcount=(refcount, (c.n_pages,)), refcount_out=(refcount_out, (c.n_pages,)),
-                page_table=(page_table, page_table.shape))
-    if workspace is None:
-        workspace = alloc_pages_workspace(c.n_pages, n, page_table.shape[1], dev)
-    return c, dev, refcount_out, workspace, workspace.numel() * workspace.element_size()
+def _new_ints(shape, device):
+    return torch.empty(shape, dtype=torch.int32, device=device)
 
 
 def pages_fork(refcount, page_table, seq_lens, parents, k_pages, v_pages, deep: bool = False, refcount_out=None,
@@ -538,20 +538,24 @@ def pages_fork(refcount, page_table, seq_lens, parents, k_pages, v_pages, deep: 
     k_pages, v_pages [L, P, page_size, Hkv, D].  Returns (refcount_out [P], child_table
     [C, max_pages], child_lens [C], short [1]); short > 0: that many pages were missing and
     nothing changed.  refcount_out may be refcount."""
-    lib = load()
-    C, W = parents.shape[0], page_table.shape[-1]
-    c, dev, refcount_out, workspace, nb = _pages_call(k_pages, v_pages, refcount, page_table, C, refcount_out, workspace)
-    new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=dev)  # noqa: E731
-    child_table = new(C, W) if child_table is None else child_table
-    child_lens = new(C) if child_lens is None else child_lens
-    short = new(1) if short is None else short
-    B = page_table.shape[0]
-    _check_ints(dev, seq_lens=(seq_lens, (B,)), parents=(parents, (C,)), child_table=(child_table, (C, W)),
-                child_lens=(child_lens, (C,)), short=(short, (1,)))
-    with _on(dev):
-        _check(lib.ne_pages_fork(ctypes.byref(c), _ptr(refcount), _ptr(page_table), _ptr(seq_lens), _ptr(parents),
-                                 1 if deep else 0, _ptr(refcount_out), _ptr(child_table), _ptr(child_lens), _ptr(short), B,
-                                 C, W, _ptr(workspace), nb, _stream(k_pages)))
+    lib = _lib or load()
+    c = _paged_cache(k_pages, v_pages, True)
+    dev = k_pages.device
+    P = (c.n_pages,)
+    if page_table.dim() != 2 or parents.dim() != 1:
+        raise ValueError("page_table must be [B, max_pages] and parents [C]")
+    B, W = page_table.shape
+    C = parents.shape[0]
+    refcount_out = _new_ints(P, dev) if refcount_out is None else refcount_out
+    child_table = _new_ints((C, W), dev) if child_table is None else child_table
+    child_lens = _new_ints((C,), dev) if child_lens is None else child_lens
+    short = _new_ints((1,), dev) if short is None else short
+    workspace = alloc_pages_workspace(c.n_pages, C, W, dev) if workspace is None else workspace
+    _launch(lib.ne_pages_fork, dev.index, ctypes.byref(c), _ints(refcount, P, dev, "refcount"),
+            _ints(page_table, (B, W), dev, "page_table"), _ints(seq_lens, (B,), dev, "seq_lens"),
+            _ints(parents, (C,), dev, "parents"), 1 if deep else 0, _ints(refcount_out, P, dev, "refcount_out"),
+            _ints(child_table, (C, W), dev, "child_table"), _ints(child_lens, (C,), dev, "child_lens"),
+            _ints(short, (1,), dev, "short"), B, C, W, *_ws(workspace, dev))
     return refcount_out, child_table, child_lens, short
 
 
@@ -561,16 +565,22 @@ def pages_resize(refcount, page_table, seq_lens, new_lens, k_pages, v_pages, ref
     lengths are given back, a shared page that would be written is copied, new pages are
     taken, lowest free ids first.  Returns (refcount_out, table_out, short [1]); short > 0:
     that many pages were missing and nothing changed.  Both outputs may be the inputs."""
-    lib = load()
-    B, W = page_table.shape
-    c, dev, refcount_out, workspace, nb = _pages_call(k_pages, v_pages, refcount, page_table, B, refcount_out, workspace)
-    table_out = torch.empty_like(page_table) if table_out is None else table_out
-    short = torch.empty(1, dtype=torch.int32, device=dev) if short is None else short
-    _check_ints(dev, seq_lens=(seq_lens, (B,)), new_lens=(new_lens, (B,)), table_out=(table_out, (B, W)), short=(short, (1,)))
-    with _on(dev):
-        _check(lib.ne_pages_resize(ctypes.byref(c), _ptr(refcount), _ptr(page_table), _ptr(seq_lens), _ptr(new_lens),
-                                   _ptr(refcount_out), _ptr(table_out), _ptr(short), B, W, _ptr(workspace), nb,
-                                   _stream(k_pages)))
+    lib = _lib or load()
+    c = _paged_cache(k_pages, v_pages, True)
+    dev = k_pages.device
+    P, T = (c.n_pages,), page_table.shape
+    if len(T) != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    B, W = T
+    refcount_out = _new_ints(P, dev) if refcount_out is None else refcount_out
+    table_out = _new_ints(T, dev) if table_out is None else table_out
+    short = _new_ints((1,), dev) if short is None else short
+    workspace = alloc_pages_workspace(c.n_pages, B, W, dev) if workspace is None else workspace
+    _launch(lib.ne_pages_resize, dev.index, ctypes.byref(c), _ints(refcount, P, dev, "refcount"),
+            _ints(page_table, T, dev, "page_table"), _ints(seq_lens, (B,), dev, "seq_lens"),
+            _ints(new_lens, (B,), dev, "new_lens"), _ints(refcount_out, P, dev, "refcount_out"),
+            _ints(table_out, T, dev, "table_out"), _ints(short, (1,), dev, "short"), B, W,
+            *_ws(workspace, dev))
     return refcount_out, table_out, short
 
 
@@ -579,17 +589,22 @@ def pages_compact(refcount, page_table, k_pages, v_pages, refcount_out=None, tab
     """Moves the live pages of the pool into 0 .. n_live - 1.  Returns (refcount_out,
     table_out, remap [P]: new id of every live page, -1 for free ones, n_live [1]).  Both
     outputs may be the inputs; further tables go through remap."""
-    lib = load()
-    c, dev, refcount_out, workspace, nb = _pages_call(k_pages, v_pages, refcount, page_table, page_table.shape[0],
-                                                      refcount_out, workspace)
-    B, W = page_table.shape
-    table_out = torch.empty_like(page_table) if table_out is None else table_out
-    remap = torch.empty_like(refcount) if remap is None else remap
-    n_live = torch.empty(1, dtype=torch.int32, device=dev) if n_live is None else n_live
-    _check_ints(dev, table_out=(table_out, (B, W)), remap=(remap, (c.n_pages,)), n_live=(n_live, (1,)))
-    with _on(dev):
-        _check(lib.ne_pages_compact(ctypes.byref(c), _ptr(refcount), _ptr(page_table), _ptr(refcount_out), _ptr(table_out),
-                                    _ptr(remap), _ptr(n_live), B, W, _ptr(workspace), nb, _stream(k_pages)))
+    lib = _lib or load()
+    c = _paged_cache(k_pages, v_pages, True)
+    dev = k_pages.device
+    P, T = (c.n_pages,), page_table.shape
+    if len(T) != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    B, W = T
+    refcount_out = _new_ints(P, dev) if refcount_out is None else refcount_out
+    table_out = _new_ints(T, dev) if table_out is None else table_out
+    remap = _new_ints(P, dev) if remap is None else remap
+    n_live = _new_ints((1,), dev) if n_live is None else n_live
+    workspace = alloc_pages_workspace(c.n_pages, B, W, dev) if workspace is None else workspace
+    _launch(lib.ne_pages_compact, dev.index, ctypes.byref(c), _ints(refcount, P, dev, "refcount"),
+            _ints(page_table, T, dev, "page_table"), _ints(refcount_out, P, dev, "refcount_out"),
+            _ints(table_out, T, dev, "table_out"), _ints(remap, P, dev, "remap"), _ints(n_live, (1,), dev, "n_live"), B, W,
+            *_ws(workspace, dev))
     return refcount_out, table_out, remap, n_live
 
 

@@ -31,9 +31,10 @@ ne_status check_cache(const ne_paged_cache* c, int want_bytes, bool attn) {
     if (want_bytes && c->elem_bytes != want_bytes)
         return fail(NE_ERR_INVALID_ARG, "the cache holds %d-byte elements, the call takes %d-byte ones", c->elem_bytes,
                     want_bytes);
-    if (c->layers < 1 || c->n_pages < 1 || c->n_pages >= (1 << 24) || c->Hkv < 1 || c->Hkv > 65536)
-        return fail(NE_ERR_INVALID_ARG, "need layers >= 1, 1 <= n_pages < 2^24, 1 <= Hkv <= 65536 (layers=%d n_pages=%d Hkv=%d)",
-                    c->layers, c->n_pages, c->Hkv);
+    if (c->layers < 1 || c->layers > 4096 || c->n_pages < 1 || c->n_pages >= (1 << 24) || c->Hkv < 1 || c->Hkv > 1024)
+        return fail(NE_ERR_INVALID_ARG,
+                    "need 1 <= layers <= 4096, 1 <= n_pages < 2^24, 1 <= Hkv <= 1024 (layers=%d n_pages=%d Hkv=%d)", c->layers,
+                    c->n_pages, c->Hkv);
     if (attn && c->layers != 1)
         return fail(NE_ERR_INVALID_ARG, "the call works on one layer: pass that layer's pools with layers = 1");
     if (c->page_size < 8 || c->page_size > 256 || (c->page_size & (c->page_size - 1)))
@@ -269,7 +270,7 @@ PagesWs pages_ws(int n_pages, int n, int W) {
     const size_t most = std::max(taken, (size_t)n_pages / 2 + 1);
     PagesWs w;
     w.off = 256;
-    w.free_ids = w.off + round_up(((size_t)n + 1) * 4, 256);
+    w.free_ids = w.off + round_up((size_t)n * 8, 256);
     w.list = w.free_ids + round_up(most * 4, 256);
     w.total = w.list + round_up(most * 16, 256);
     return w;
@@ -326,7 +327,7 @@ ne_status pages_args(ne::PagesArgs* a, const ne_paged_cache* c, const int* ref, 
     a->cap = W * c->page_size;
     char* base = static_cast<char*>(ws);
     a->head = reinterpret_cast<int*>(base);
-    a->off = reinterpret_cast<int*>(base + w.off);
+    a->off = reinterpret_cast<int2*>(base + w.off);
     a->free_ids = reinterpret_cast<int*>(base + w.free_ids);
     a->list = reinterpret_cast<int4*>(base + w.list);
     return NE_OK;

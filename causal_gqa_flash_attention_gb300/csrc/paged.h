@@ -37,6 +37,8 @@ struct AppendArgs {
     int rot, layout, pos_offset;      // rot 0: no rotation
     float mscale;
     int tpc;                          // tokens per CTA
+    int vec_shift;                    // log2 of the 16-byte units of a head
+    FastDiv div_per;                  // by the units of a token
     int* err;
 };
 struct RopeTurns {
@@ -105,11 +107,13 @@ struct PagesArgs {
     int* short_out;                   // pages missing, or n_live (compact)
     int B, W, n, deep, cap;           // n: sequences that take pages
     // workspace
-    int* head;                        // [0] copies + takes in the list, [1] pages missing
-    int* off;                         // [n + 1] first list entry of every sequence
-    int* free_ids;                    // free pages in ascending order, as many as are listed
-    int4* list;                       // (source page or -1, target page, slots, 0)
+    int* head;                        // [0] copies, [1] pages missing, [2] pages taken
+    int2* off;                        // [n] a sequence's first page in free_ids; its copy in list, or -1
+    int* free_ids;                    // free pages in ascending order, as many as are taken
+    int4* list;                       // copies: (source page or -1, target page, slots, 0)
     int* err;
+    int chunks, pieces;               // pieces of a page and pool; of a copy (all layers, both pools)
+    FastDiv div_pieces, div_chunks, div_heads, div_w;
 };
 enum PagesOp : int { PAGES_FORK = 0, PAGES_RESIZE, PAGES_COMPACT };
 cudaError_t launch_pages(PagesOp op, const PagesArgs& a, cudaStream_t st);

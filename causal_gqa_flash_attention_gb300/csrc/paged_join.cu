@@ -154,7 +154,7 @@ PagedSplit paged_split(PagedKind kind, int D, int Hkv, int G) {
         p.hg = Hkv * ((G + p.gs - 1) / p.gs);
     };
     p.ovh = 128;
-    p.min_work = 512;
+    p.min_work = 192;
     switch (kind) {
         case PAGED_SHORT16:
         case PAGED_SHORT32:
@@ -180,6 +180,8 @@ PagedSplit paged_split(PagedKind kind, int D, int Hkv, int G) {
             p.hg = Hkv;
             p.bn = 128;
             p.C = kSms;
+            p.ovh = 256;
+            p.min_work = 512;
             break;
     }
     return p;

@@ -21,6 +21,13 @@
 
 namespace ne {
 
+// a / b for b > 0, a >= 0, in 32 bits where both fit: the 64-bit divide is a long
+// sequence, and a CTA's share of the work is found by a few of them one after another.
+__device__ __forceinline__ long long paged_div(long long a, long long b) {
+    if ((((unsigned long long)a | (unsigned long long)b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+    return a / b;
+}
+
 struct PagedSeq {
     int tok0, n, len;
 };
@@ -95,7 +102,7 @@ struct PagedWalk {
         load(a);
         const long long S = paged_group_cost(q, a.p.tpt, a.p.ovh);
         const long long off = w0 - start;
-        hg = (int)(off / S);
+        hg = (int)paged_div(off, S);
         const long long x = off - (long long)hg * S;
         int lo = 0, hi = nt - 1;                           // the last tile whose start is at or before x
         while (lo < hi) {
@@ -113,8 +120,8 @@ struct PagedWalk {
             const int kv = r == nt - 1 ? q.len : max(0, base + (r + 1) * a.p.tpt);
             const int cost = a.p.ovh + kv;
             const int ntk = (kv + a.p.bn - 1) / a.p.bn;
-            g.t0 = w0 <= cur ? 0 : (int)(((w0 - cur) * ntk + cost / 2) / cost);
-            g.t1 = w1 >= cur + cost ? ntk : (int)(((w1 - cur) * ntk + cost / 2) / cost);
+            g.t0 = w0 <= cur ? 0 : (int)paged_div((w0 - cur) * ntk + cost / 2, cost);
+            g.t1 = w1 >= cur + cost ? ntk : (int)paged_div((w1 - cur) * ntk + cost / 2, cost);
             g.b = b;
             g.hg = hg;
             g.r = r;
@@ -184,9 +191,9 @@ __device__ __forceinline__ void paged_locate(const PagedAttnArgs& a, int c, Page
         return x + (warp ? sm.warp_sum[warp - 1] : 0);
     };
     auto interval = [&](long long total) {
-        const long long most = total / a.p.min_work;
+        const long long most = paged_div(total, a.p.min_work);
         const int C = most < 1 ? 1 : (most < a.p.C ? (int)most : a.p.C);
-        const long long each = total / C, rest = total % C;
+        const long long each = paged_div(total, C), rest = total - each * C;
         const long long i = min(c, C), j = min(c + 1, C);
         sm.w0 = each * i + min(i, rest);
         sm.w1 = each * j + min(j, rest);

@@ -13,14 +13,16 @@
 // cycle.  The two subtiles alternate: while the softmax warps of one work on its S tile, the
 // tensor core runs the other's PV and next S.  Roles (12 warps):
 //   warp 0       producer: Q pair of the unit, then K and V tiles through an NS-slot ring.
-//   warp 1       UMMA issuer (owns the 512 TMEM columns).  Per tile t and subtile u, once P_u(t)
-//                is there: O_u += P_u(t) V(t), then S_u(t + 1) = Q_u K(t + 1)^T into the same
-//                columns (one thread's UMMAs run in order, so S(t + 1) cannot overtake the PV that
-//                reads P(t) there, and S(t + 1) complete means PV(t) complete).
+//   warp 1       UMMA issuer (owns the 512 TMEM columns).  Per tile t and subtile u:
+//                O_u += P_u(t) V(t) once P_u(t) is there, and S_u(t + 1) = Q_u K(t + 1)^T.  Where P
+//                lies over S, S(t + 1) goes right behind the PV (one thread's UMMAs run in order, so it
+//                cannot overtake it, and S(t + 1) complete means PV(t) complete); where P has columns
+//                of its own, S(t + 1) goes first, as soon as S(t) is in registers.
 //   warp 2       zeroes the V rows behind a sequence's length in the tile that holds it (P is 0
 //                there, but 0 x NaN is not).
 //   warps 4-11   softmax: thread r of subtile u owns row r (TMEM lane r).
-// TMEM: S_u (and P_u, bf16, over its first half) at 128 u; O_u at 256 + 128 u.
+// TMEM: S_u at 128 u, O_u behind both; P_u (bf16) over S_u's first half at D 128, where TMEM
+// is full, in columns of its own at D 64.
 // Weights are rounded to bf16 for the product (half a step, 2^-8 of each weight, as the
 // training forward does); maximum and sum stay fp32, and the sum is of the unrounded weights.
 // Every wait is bounded; a CTA that gives up reports, drains its copies and UMMAs, frees its
@@ -41,7 +43,12 @@ struct TileCfg {
     static constexpr int NS = D == 128 ? 5 : 12;           // ring slots
     static constexpr int SMEM = 1024 + 2 * TILE + NS * TILE;
     static constexpr int THREADS = 384;
-    static constexpr int O_COL = 256;
+    static constexpr int O_COL = 256;                      // O_u at O_COL + u D
+    // P in columns of its own where TMEM has them left (D 64): the next S then starts as soon as
+    // this one has been read into registers, instead of after its PV.
+    static constexpr bool SEP = D == 64;
+    static constexpr int P_COL = SEP ? O_COL + 2 * D : 0;  // P_u at P_COL + u P_STEP
+    static constexpr int P_STEP = SEP ? 64 : 128;
     static_assert(SMEM + 1536 <= 227 * 1024, "shared memory");
 };
 
@@ -68,7 +75,7 @@ __global__ void __launch_bounds__(384, 1)
     uint8_t* sRing = smem + 2 * C::TILE;
     __shared__ __align__(8) uint64_t bar_q_full, bar_q_empty, bar_vfix[2], bar_final;
     __shared__ __align__(8) uint64_t bar_full[C::NS], bar_empty[C::NS];
-    __shared__ __align__(8) uint64_t bar_s_full[2], bar_p_ready[2], bar_o_full[2];
+    __shared__ __align__(8) uint64_t bar_s_full[2], bar_p_ready[2], bar_o_full[2], bar_s_free[2];
     __shared__ PagedLocate loc;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
@@ -85,7 +92,8 @@ __global__ void __launch_bounds__(384, 1)
         for (int u = 0; u < 2; ++u) {
             mbar_init(smem_u32(&bar_s_full[u]), 1);
             mbar_init(smem_u32(&bar_p_ready[u]), 128);
-            mbar_init(smem_u32(&bar_o_full[u]), 1);
+            mbar_init(smem_u32(&bar_o_full[u]), 1);        // a part's last PV; SEP: every PV
+            mbar_init(smem_u32(&bar_s_free[u]), 128);      // SEP: S is in registers
             mbar_init(smem_u32(&bar_vfix[u]), 32);         // the k-th fix arrives on k % 2: warp 2 can be one
                                                            // fix ahead of the issuer (one part, by its Q), not two
         }
@@ -125,17 +133,6 @@ __global__ void __launch_bounds__(384, 1)
         const int rows = 128 / npg;
         while (ok && walk.next(a, g)) {
             if (g.t0 == g.t1) continue;                    // no keys: the softmax warps write the rows
-            if (seg > 0 && !(ok = mbar_wait_warp(smem_u32(&bar_q_empty), (seg - 1) & 1, w, SITE_PAGED_Q))) break;
-            const int n_sub = g.ntok > sub ? 2 : 1;
-            if (lane == 0) {
-                const uint32_t qf = smem_u32(&bar_q_full);
-                mbar_arrive_expect_tx(qf, n_sub * C::NCH * sub * a.G * 128);
-                for (int u = 0; u < n_sub; ++u)
-                    for (int c = 0; c < C::NCH; ++c)
-                        tma_load_3d(smem_u32(sQ + u * C::TILE + c * C::CHUNK), &tm_q, qf, c * 64, g.hg * a.G,
-                                    g.tok0 + g.tok + u * sub);
-            }
-            ++seg;
             const int* trow = a.s.table + (size_t)g.b * a.s.W;
             auto page = [&](int t) -> int {                // page of this lane's part of tile t
                 const int pos = t * C::BN + lane * rows;
@@ -148,6 +145,17 @@ __global__ void __launch_bounds__(384, 1)
                 return p;
             };
             int next = page(g.t0);
+            if (seg > 0 && !(ok = mbar_wait_warp(smem_u32(&bar_q_empty), (seg - 1) & 1, w, SITE_PAGED_Q))) break;
+            const int n_sub = g.ntok > sub ? 2 : 1;
+            if (lane == 0) {
+                const uint32_t qf = smem_u32(&bar_q_full);
+                mbar_arrive_expect_tx(qf, n_sub * C::NCH * sub * a.G * 128);
+                for (int u = 0; u < n_sub; ++u)
+                    for (int c = 0; c < C::NCH; ++c)
+                        tma_load_3d(smem_u32(sQ + u * C::TILE + c * C::CHUNK), &tm_q, qf, c * 64, g.hg * a.G,
+                                    g.tok0 + g.tok + u * sub);
+            }
+            ++seg;
             for (int t = g.t0; ok && t < g.t1; ++t) {
                 const int p = next;
                 if (t + 1 < g.t1) next = page(t + 1);
@@ -182,7 +190,7 @@ __global__ void __launch_bounds__(384, 1)
         const uint64_t dq0 = sdesc(smem_u32(sQ), 16, 1024);
         const uint64_t dk0 = sdesc(smem_u32(sRing), 16, 1024);
         const uint64_t dv0 = sdesc(smem_u32(sRing), C::CHUNK, 1024);
-        int seg = 0, item = 0, tiles[2] = {0, 0}, fixes = 0;
+        int seg = 0, item = 0, tiles[2] = {0, 0}, s_tiles[2] = {0, 0}, fixes = 0;
         bool ok = true;
         auto s_mmas = [&](int u, int k_item) {
             const uint64_t dq = sdesc_add(dq0, u * C::TILE), dk = sdesc_add(dk0, (k_item % C::NS) * C::TILE);
@@ -198,11 +206,19 @@ __global__ void __launch_bounds__(384, 1)
             tc_fence_after();
             return r;
         };
+        // S_u's columns hold no S that is still to be read (SEP; otherwise the PV in front of the
+        // next S, on this same thread, says so).
+        auto s_free = [&](int u) -> bool {
+            if (!C::SEP || s_tiles[u] == 0) return true;
+            const bool r = mbar_wait_warp(smem_u32(&bar_s_free[u]), (s_tiles[u] - 1) & 1, w, SITE_PAGED_S_FULL);
+            tc_fence_after();
+            return r;
+        };
         while (ok && walk.next(a, g)) {
             if (g.t0 == g.t1) continue;
             const int n_sub = g.ntok > sub ? 2 : 1, nt = g.t1 - g.t0;
             if (!(ok = mbar_wait_warp(smem_u32(&bar_q_full), seg & 1, w, SITE_PAGED_Q))) break;
-            if (!(ok = full(item))) break;
+            if (!(ok = full(item) && s_free(0) && (n_sub == 1 || s_free(1)))) break;
             if (elect_one()) {
                 s_mmas(0, item);
                 if (n_sub == 2) s_mmas(1, item);
@@ -210,16 +226,37 @@ __global__ void __launch_bounds__(384, 1)
                 if (nt == 1) umma_commit(smem_u32(&bar_q_empty));
             }
             __syncwarp();
+            ++s_tiles[0];
+            if (n_sub == 2) ++s_tiles[1];
             for (int t = 0; ok && t < nt; ++t) {
                 const int vi = item + 2 * t + 1, kn = item + 2 * t + 2;
                 const bool more = t + 1 < nt, fix = (g.t0 + t + 1) * C::BN > g.len;
+                const uint64_t dv = sdesc_add(dv0, (vi % C::NS) * C::TILE);
+                // After the last subtile's S(t + 1): its K slot, and after the part's last S the Q.
+                auto s_done = [&]() {
+                    umma_commit(smem_u32(&bar_empty[kn % C::NS]));
+                    if (t + 2 == nt) umma_commit(smem_u32(&bar_q_empty));
+                };
+                if (C::SEP && more) {
+                    if (!(ok = full(kn))) break;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        if (u >= n_sub || !(ok = s_free(u))) break;
+                        ++s_tiles[u];
+                        if (elect_one()) {
+                            s_mmas(u, kn);
+                            if (u == n_sub - 1) s_done();
+                        }
+                        __syncwarp();
+                    }
+                    if (!ok) break;
+                }
                 if (!(ok = full(vi))) break;
                 if (fix) {
                     if (!(ok = mbar_wait_warp(smem_u32(&bar_vfix[fixes & 1]), (fixes >> 1) & 1, w, SITE_PAGED_KV_FULL))) break;
                     ++fixes;
                 }
-                if (more && !(ok = full(kn))) break;
-                const uint64_t dv = sdesc_add(dv0, (vi % C::NS) * C::TILE);
+                if (!C::SEP && more && !(ok = full(kn))) break;
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     if (u >= n_sub) break;
@@ -229,16 +266,13 @@ __global__ void __launch_bounds__(384, 1)
                     if (elect_one()) {
 #pragma unroll
                         for (int ks = 0; ks < C::BN / 16; ++ks)
-                            umma_ts<false>(tm + C::O_COL + u * 128, tm + u * 128 + ks * 8, sdesc_add(dv, ks * 16 * 128), id_o,
-                                           (t > 0 || ks > 0) ? 1u : 0u);
-                        if (!more) umma_commit(smem_u32(&bar_o_full[u]));
-                        if (more) s_mmas(u, kn);
+                            umma_ts<false>(tm + C::O_COL + u * D, tm + C::P_COL + u * C::P_STEP + ks * 8,
+                                           sdesc_add(dv, ks * 16 * 128), id_o, (t > 0 || ks > 0) ? 1u : 0u);
+                        if (C::SEP || !more) umma_commit(smem_u32(&bar_o_full[u]));
+                        if (!C::SEP && more) s_mmas(u, kn);
                         if (u == n_sub - 1) {
                             umma_commit(smem_u32(&bar_empty[vi % C::NS]));
-                            if (more) {
-                                umma_commit(smem_u32(&bar_empty[kn % C::NS]));
-                                if (t + 2 == nt) umma_commit(smem_u32(&bar_q_empty));
-                            }
+                            if (!C::SEP && more) s_done();
                         }
                     }
                     __syncwarp();
@@ -277,7 +311,7 @@ __global__ void __launch_bounds__(384, 1)
         const int u = (warp - 4) >> 2;
         const int r = (warp & 3) * 32 + lane;              // row = TMEM lane
         const uint32_t lt = tm + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t sc = lt + u * 128, oc = lt + C::O_COL + u * 128;
+        const uint32_t sc = lt + u * 128, oc = lt + C::O_COL + u * D, pc = lt + C::P_COL + u * C::P_STEP;
         const float sl2 = a.scale_log2;
         int tiles = 0, parts = 0;
         bool ok = true;
@@ -303,13 +337,26 @@ __global__ void __launch_bounds__(384, 1)
             float m = -INFINITY, l = 0.f;
             for (int t = g.t0; t < g.t1; ++t, ++tiles) {
                 if (!(ok = mbar_wait_warp(smem_u32(&bar_s_full[u]), tiles & 1, w, SITE_PAGED_S_FULL))) break;
+                // SEP: P(t - 1) is read and O_u at rest once PV(t - 1) is complete.  (Every warp waits
+                // for it, so that none arrives for a tile while others still owe the one before.)
+                auto pv_before = [&]() {
+                    return !C::SEP || tiles == 0 ||
+                           mbar_wait_warp(smem_u32(&bar_o_full[u]), (tiles - 1) & 1, w, SITE_PAGED_O_FULL);
+                };
                 if (!warp_live) {                          // rows of nobody: their P may be anything
+                    if (C::SEP) mbar_arrive(smem_u32(&bar_s_free[u]));
+                    ok = pv_before();
+                    if (!ok) break;
                     mbar_arrive(smem_u32(&bar_p_ready[u]));
                     continue;
                 }
                 tc_fence_after();
                 uint32_t s[128];
                 tmem_ld_cols<4>(sc, s);
+                if (C::SEP) {
+                    tc_fence_before();
+                    mbar_arrive(smem_u32(&bar_s_free[u]));
+                }
                 const int kv0 = t * C::BN;
                 if (kv0 + C::BN > first_lim) {
 #pragma unroll
@@ -328,7 +375,10 @@ __global__ void __launch_bounds__(384, 1)
                 const float m_tile = __fmul_rn(fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]), sl2);
                 // A row whose maximum grew by more than 2^8 rescales its sum and output; the
                 // others keep the old reference (weights up to 2^8 lose nothing).  PV(t - 1) is
-                // complete: S(t) was issued behind it.
+                // complete: waited for (SEP), or S(t) was issued behind it.
+                ok = pv_before();
+                if (!ok) break;
+                if (C::SEP) tc_fence_after();
                 const bool need = t > g.t0 && m_tile > m + 8.f;
                 if (t == g.t0) m = m_tile;
                 if (__any_sync(0xffffffffu, need)) {
@@ -360,7 +410,7 @@ __global__ void __launch_bounds__(384, 1)
                         s2[(e >> 1) & 3] = __fadd2_rn(s2[(e >> 1) & 3], p);
                         pk[e >> 1] = pack2(p.x, p.y);
                     }
-                    tmem_st16(sc + (c >> 1), pk);
+                    tmem_st16(pc + (c >> 1), pk);
                 }
                 l += ((s2[0].x + s2[0].y) + (s2[1].x + s2[1].y)) + ((s2[2].x + s2[2].y) + (s2[3].x + s2[3].y));
                 tmem_wait_st();
@@ -368,7 +418,7 @@ __global__ void __launch_bounds__(384, 1)
                 mbar_arrive(smem_u32(&bar_p_ready[u]));
             }
             if (!ok) break;
-            if (!(ok = mbar_wait_warp(smem_u32(&bar_o_full[u]), parts & 1, w, SITE_PAGED_O_FULL))) break;
+            if (!(ok = mbar_wait_warp(smem_u32(&bar_o_full[u]), (C::SEP ? tiles - 1 : parts) & 1, w, SITE_PAGED_O_FULL))) break;
             ++parts;
             if (!warp_live) continue;
             tc_fence_after();

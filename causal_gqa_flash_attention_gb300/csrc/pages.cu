@@ -27,7 +27,7 @@ constexpr int kBulkThreads = 256;
 struct ScanSmem {
     int warp[32];
     int total;
-    int cta[2][kCluster][2];           // [exchange] two totals of every CTA of the cluster, written by it
+    int cta[2][kCluster][3];           // [exchange] three totals of every CTA of the cluster, written by it
 };
 
 // Inclusive sum over the CTA; the total in sm.total.
@@ -55,15 +55,16 @@ __device__ __forceinline__ int cta_scan(int x, ScanSmem& sm) {
     return x + (warp ? sm.warp[warp - 1] : 0);
 }
 
-// Tells every CTA of the cluster this CTA's two totals, and waits for theirs.  ROUND: a
+// Tells every CTA of the cluster this CTA's three totals, and waits for theirs.  ROUND: a
 // kernel's exchanges have a place each, as a faster CTA may be one ahead of a reader.
 template <int ROUND>
-__device__ __forceinline__ void exchange(cg::cluster_group& cl, ScanSmem& sm, int x, int y) {
+__device__ __forceinline__ void exchange(cg::cluster_group& cl, ScanSmem& sm, int x, int y, int z) {
     const int me = (int)cl.block_rank();
     if (threadIdx.x < kCluster) {
         int* dst = cl.map_shared_rank(&sm.cta[ROUND][me][0], (int)threadIdx.x);
         dst[0] = x;
         dst[1] = y;
+        dst[2] = z;
     }
     cl.sync();
 }
@@ -141,6 +142,27 @@ __device__ __forceinline__ Take take_resize(const PagesArgs& a, int b, const int
     return t;
 }
 
+// Adds `by` to the counts of the pages behind the new lengths: -1 gives them back, 1 takes
+// that back.  Eight lanes per sequence.
+__device__ __forceinline__ void give_back(const PagesArgs& a, int gt, int GT, int by) {
+    for (int b = gt >> 3; b < a.n; b += GT / 8) {
+        const int old = clamp_len(a.lens[b], a.cap, nullptr), now = clamp_len(a.other[b], a.cap, nullptr);
+        const int po = (old + a.ps - 1) >> a.ps_shift, pn = (now + a.ps - 1) >> a.ps_shift;
+        const int* row = a.table + (size_t)b * a.W;
+        for (int i0 = pn + (gt & 7); i0 < po; i0 += 32) {
+            int p[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) p[k] = i0 + 8 * k < po ? __ldg(row + i0 + 8 * k) : 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (i0 + 8 * k >= po) continue;
+                if (page_ok(a, p[k])) atomicAdd(a.ref_out + p[k], by);
+                else report_error(a.err, SITE_PAGED_PAGE);
+            }
+        }
+    }
+}
+
 // ------------------------------------------------------------------ first kernel
 template <int OP>
 __global__ void __launch_bounds__(kThreads, 1) pages_plan_kernel(const PagesArgs a) {
@@ -154,8 +176,21 @@ __global__ void __launch_bounds__(kThreads, 1) pages_plan_kernel(const PagesArgs
     int lo, hi;
     share(a.n_pages, me, lo, hi);
     // The counts, where the outputs are another array.
-    if (a.ref_out != a.ref && OP != PAGES_COMPACT)
-        for (int i = lo + tid; i < hi; i += kThreads) a.ref_out[i] = a.ref[i];
+    if (a.ref_out != a.ref && OP != PAGES_COMPACT) {
+        const int4* src = reinterpret_cast<const int4*>(a.ref);
+        int4* dst = reinterpret_cast<int4*>(a.ref_out);
+        const int q1 = hi / 4;                             // (lo is a multiple of four)
+        for (int i0 = lo / 4 + tid; i0 < q1; i0 += 4 * kThreads) {
+            int4 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (i0 + k * kThreads < q1) v[k] = __ldg(src + i0 + k * kThreads);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (i0 + k * kThreads < q1) dst[i0 + k * kThreads] = v[k];
+        }
+        if (tid < hi - max(lo, q1 * 4)) a.ref_out[q1 * 4 + tid] = a.ref[q1 * 4 + tid];
+    }
 
     if constexpr (OP == PAGES_COMPACT) {
         int live = 0;
@@ -164,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1) pages_plan_kernel(const PagesArgs
             live += (v.x > 0) + (v.y > 0) + (v.z > 0) + (v.w > 0);
         }
         cta_scan(live, sm);
-        exchange<0>(cl, sm, sm.total, 0);
+        exchange<0>(cl, sm, sm.total, 0, 0);
         const int n_live = whole<0>(sm, 0);
         // Live pages at or behind n_live move, free ones in front of it receive.
         int mv = 0, ho = 0;
@@ -181,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1) pages_plan_kernel(const PagesArgs
         const int mv_all = sm.total;
         cta_scan(ho, sm);
         const int ho_all = sm.total;
-        exchange<1>(cl, sm, mv_all, ho_all);
+        exchange<1>(cl, sm, mv_all, ho_all, 0);
         int mv_at = before<1>(sm, me, 0), ho_at = before<1>(sm, me, 1);
         for (int i0 = lo; i0 < hi; i0 += kThreads * 4) {
             const int i = i0 + tid * 4;
@@ -216,6 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1) pages_plan_kernel(const PagesArgs
         if (gt == 0) {
             a.head[0] = moves;
             a.head[1] = 0;
+            a.head[2] = 0;
             a.short_out[0] = n_live;
         }
         cl.sync();
@@ -224,115 +260,104 @@ __global__ void __launch_bounds__(kThreads, 1) pages_plan_kernel(const PagesArgs
         const int* counts = OP == PAGES_FORK ? a.ref : a.ref_out;
         if constexpr (OP == PAGES_RESIZE) {
             cl.sync();                                     // the counts are copied
-            // Pages behind the new length are given back: a warp per sequence.
-            for (int b = gt >> 5; b < a.n; b += GT / 32) {
-                const int old = clamp_len(a.lens[b], a.cap, nullptr), now = clamp_len(a.other[b], a.cap, nullptr);
-                const int po = (old + a.ps - 1) >> a.ps_shift, pn = (now + a.ps - 1) >> a.ps_shift;
-                for (int i = pn + lane; i < po; i += 32) {
-                    const int p = a.table[(size_t)b * a.W + i];
-                    if (page_ok(a, p)) atomicSub(a.ref_out + p, 1);
-                    else report_error(a.err, SITE_PAGED_PAGE);
-                }
-            }
+            give_back(a, gt, GT, -1);
             cl.sync();
         }
         // What every sequence takes, and its place in the line.
         int slo, shi;
         share(a.n, me, slo, shi);
-        int need = 0;
+        auto take = [&](int i) { return OP == PAGES_FORK ? take_fork(a, i) : take_resize(a, i, counts); };
+        int need = 0, splits = 0;
         for (int i = slo + tid; i < shi; i += kThreads) {
-            const Take t = OP == PAGES_FORK ? take_fork(a, i) : take_resize(a, i, counts);
+            const Take t = take(i);
             need += t.split + t.count;
+            splits += t.split;
         }
-        int nfree = 0;
-        for (int i = lo + tid * 4; i < hi; i += kThreads * 4) {
-            int4 v;
-            if (i + 4 <= hi) {
-                v = __ldcg(reinterpret_cast<const int4*>(counts + i));
-            } else {
-                v = make_int4(1, 1, 1, 1);
-                if (i < hi) v.x = __ldcg(counts + i);
-                if (i + 1 < hi) v.y = __ldcg(counts + i + 1);
-                if (i + 2 < hi) v.z = __ldcg(counts + i + 2);
+        // Sixteen counts per thread and pass; bit k of the mask: page i + k is free.
+        auto free_mask = [&](int i) -> unsigned {
+            unsigned m = 0;
+#pragma unroll
+            for (int k = 0; k < 16; k += 4) {
+                if (i + k + 4 <= hi) {
+                    const int4 v = __ldcg(reinterpret_cast<const int4*>(counts + i + k));
+                    m |= ((v.x <= 0) | (v.y <= 0) << 1 | (v.z <= 0) << 2 | (v.w <= 0) << 3) << k;
+                } else {
+                    for (int j = 0; j < 4; ++j)
+                        if (i + k + j < hi && __ldcg(counts + i + k + j) <= 0) m |= 1u << (k + j);
+                }
             }
-            nfree += (v.x <= 0) + (v.y <= 0) + (v.z <= 0) + (v.w <= 0);
-        }
+            return m;
+        };
+        int nfree = 0;
+        for (int i = lo + tid * 16; i < hi; i += kThreads * 16) nfree += __popc(free_mask(i));
         cta_scan(need, sm);
         const int need_cta = sm.total;
+        cta_scan(splits, sm);
+        const int splits_cta = sm.total;
         cta_scan(nfree, sm);
-        exchange<0>(cl, sm, need_cta, sm.total);
+        exchange<0>(cl, sm, need_cta, sm.total, splits_cta);
         const int need_all = whole<0>(sm, 0), free_all = whole<0>(sm, 1);
         const int missing = max(0, need_all - free_all);
         if (gt == 0) {
-            a.head[0] = missing ? 0 : need_all;
+            a.head[0] = missing ? 0 : OP == PAGES_FORK ? need_all : whole<0>(sm, 2);
             a.head[1] = missing;
+            a.head[2] = missing ? 0 : need_all;
             a.short_out[0] = missing;
         }
         if (missing) {
             // Nothing changes: what was given back is taken again.
-            if constexpr (OP == PAGES_RESIZE)
-                for (int b = gt >> 5; b < a.n; b += GT / 32) {
-                    const int old = clamp_len(a.lens[b], a.cap, nullptr), now = clamp_len(a.other[b], a.cap, nullptr);
-                    const int po = (old + a.ps - 1) >> a.ps_shift, pn = (now + a.ps - 1) >> a.ps_shift;
-                    for (int i = pn + lane; i < po; i += 32) {
-                        const int p = a.table[(size_t)b * a.W + i];
-                        if (page_ok(a, p)) atomicAdd(a.ref_out + p, 1);
-                    }
-                }
+            if constexpr (OP == PAGES_RESIZE) give_back(a, gt, GT, 1);
             cl.sync();
             return;
         }
         // The free pages' ids in ascending order, as many as are needed.
         int at = before<0>(sm, me, 1);
-        for (int i0 = lo; i0 < hi && at < need_all; i0 += kThreads * 4) {
-            const int i = i0 + tid * 4;
-            int c[4] = {1, 1, 1, 1};
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (i + k < hi) c[k] = __ldcg(counts + i + k);
-            const int f = (c[0] <= 0) + (c[1] <= 0) + (c[2] <= 0) + (c[3] <= 0);
+        for (int i0 = lo; i0 < hi && at < need_all; i0 += kThreads * 16) {
+            const int i = i0 + tid * 16;
+            unsigned m = i < hi ? free_mask(i) : 0u;
+            const int f = __popc(m);
             int r = at + cta_scan(f, sm) - f;
             at += sm.total;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (c[k] <= 0) {
-                    if (r < need_all) a.free_ids[r] = i + k;
-                    ++r;
-                }
+            for (; m && r < need_all; m &= m - 1) a.free_ids[r++] = i + __ffs(m) - 1;
         }
-        // Offsets of the sequences' entries.
-        int off = before<0>(sm, me, 0);
+        // First place of every sequence; a sequence that splits a page off: its copy's, too.
+        int off = before<0>(sm, me, 0), soff = before<0>(sm, me, 2);
         for (int i0 = slo; i0 < shi; i0 += kThreads) {
             const int i = i0 + tid;
-            int x = 0;
+            int x = 0, sp = 0;
             if (i < shi) {
-                const Take t = OP == PAGES_FORK ? take_fork(a, i) : take_resize(a, i, counts);
+                const Take t = take(i);
                 x = t.split + t.count;
+                sp = t.split;
             }
             const int r = off + cta_scan(x, sm) - x;
             off += sm.total;
-            if (i < shi) a.off[i] = r;
+            int rs = 0;
+            if (OP == PAGES_RESIZE) {
+                rs = soff + cta_scan(sp, sm) - sp;
+                soff += sm.total;
+            }
+            if (i < shi) a.off[i] = make_int2(r, sp ? rs : -1);
         }
         cl.sync();
-        // The list: a warp per sequence.
-        for (int i = gt >> 5; i < a.n; i += GT / 32) {
-            const Take t = OP == PAGES_FORK ? take_fork(a, i) : take_resize(a, i, counts);
-            const int r0 = __ldcg(a.off + i);
-            if (t.split && lane == 0) {
-                const int low = min(t.len, t.now);
-                a.list[r0] = make_int4(a.table[(size_t)i * a.W + (low >> a.ps_shift)], __ldcg(a.free_ids + r0),
-                                       low & (a.ps - 1), 1);
+        // The copies.
+        if constexpr (OP == PAGES_RESIZE) {
+            for (int i = gt; i < a.n; i += GT) {
+                const int2 o = __ldcg(a.off + i);
+                if (o.y < 0) continue;
+                const int low = min(clamp_len(a.lens[i], a.cap, nullptr), clamp_len(a.other[i], a.cap, nullptr));
+                a.list[o.y] = make_int4(a.table[(size_t)i * a.W + (low >> a.ps_shift)], __ldcg(a.free_ids + o.x),
+                                        low & (a.ps - 1), 0);
             }
-            for (int k = lane; k < t.count; k += 32) {
-                const int r = r0 + t.split + k, e = t.first + k;
-                int4 it = make_int4(-1, __ldcg(a.free_ids + r), 0, 0);
-                if (OP == PAGES_FORK) {
-                    const int p = a.table[(size_t)t.parent * a.W + e];
-                    it.z = min(a.ps, t.len - e * a.ps);
-                    if (page_ok(a, p)) it.x = p;
-                    else report_error(a.err, SITE_PAGED_PAGE);
+        } else {
+            for (int i = gt >> 5; i < a.n; i += GT / 32) {     // a warp per child
+                const Take t = take_fork(a, i);
+                const int r0 = __ldcg(&a.off[i].x);
+                for (int k = lane; k < t.count; k += 32) {
+                    const int e = t.first + k, p = a.table[(size_t)t.parent * a.W + e];
+                    if (!page_ok(a, p)) report_error(a.err, SITE_PAGED_PAGE);
+                    a.list[r0 + k] = make_int4(page_ok(a, p) ? p : -1, __ldcg(a.free_ids + r0 + k), min(a.ps, t.len - e * a.ps), 0);
                 }
-                a.list[r] = it;
             }
         }
         cl.sync();
@@ -341,17 +366,20 @@ __global__ void __launch_bounds__(kThreads, 1) pages_plan_kernel(const PagesArgs
 
 // ------------------------------------------------------------------ second kernel
 // Table entries, counts and page contents.
+constexpr int kVec = 8;                                    // 16-byte units in flight per lane
+
 template <int OP>
 __global__ void __launch_bounds__(kBulkThreads) pages_bulk_kernel(const PagesArgs a) {
     griddep_launch_dependents();
     griddep_wait();
     const long long gt = (long long)blockIdx.x * kBulkThreads + threadIdx.x, GT = (long long)gridDim.x * kBulkThreads;
-    const int entries = a.head[0], missing = a.head[1];
+    const int copies = a.head[0], missing = a.head[1], taken = a.head[2];
 
     // Table entries.
-    const long long cells = (long long)(OP == PAGES_COMPACT ? a.B : a.n) * a.W;
-    for (long long i = gt; i < cells; i += GT) {
-        const int s = (int)(i / a.W), e = (int)(i - (long long)s * a.W);
+    const int rows = OP == PAGES_COMPACT ? a.B : a.n;
+    const uint32_t cells = (uint32_t)rows * (uint32_t)a.W;     // (below 2^31)
+    for (uint32_t i = (uint32_t)gt; i < cells; i += (uint32_t)GT) {
+        const int s = (int)fast_div(i, a.div_w), e = (int)(i - (uint32_t)s * (uint32_t)a.W);
         if (OP == PAGES_COMPACT) {
             const int p = a.table[i];
             if (p >= a.n_pages) report_error(a.err, SITE_PAGED_PAGE);
@@ -365,7 +393,7 @@ __global__ void __launch_bounds__(kBulkThreads) pages_bulk_kernel(const PagesArg
             const Take t = take_fork(a, s);
             int v = -1;
             if (e >= t.first && e < t.first + t.count) {
-                v = a.free_ids[a.off[s] + e - t.first];
+                v = a.free_ids[a.off[s].x + e - t.first];
             } else if (e < t.first) {                      // a shared whole page
                 const int p = a.table[(size_t)t.parent * a.W + e];
                 if (page_ok(a, p)) {
@@ -383,17 +411,13 @@ __global__ void __launch_bounds__(kBulkThreads) pages_bulk_kernel(const PagesArg
                 a.table_out[i] = v;
                 continue;
             }
+            const int2 off = a.off[s];
             const int old = clamp_len(a.lens[s], a.cap, nullptr), now = clamp_len(a.other[s], a.cap, nullptr);
             const int po = (old + a.ps - 1) >> a.ps_shift, pn = (now + a.ps - 1) >> a.ps_shift;
-            const int low = min(old, now);
+            const int split = off.y >= 0 ? 1 : 0;
             int out = -1;
-            // A split is marked in the first list entry of its sequence.
-            const bool maybe = (low & (a.ps - 1)) != 0 || (e >= po && e < pn);
-            const int r0 = maybe ? a.off[s] : 0;
-            const int next = s + 1 < a.n ? 1 : 0;
-            const bool split = (low & (a.ps - 1)) != 0 && r0 < (next ? a.off[s + 1] : entries) && a.list[r0].w == 1;
-            if (e < min(po, pn)) out = split && e == (low >> a.ps_shift) ? a.list[r0].y : v;
-            else if (e >= po && e < pn) out = a.list[r0 + (split ? 1 : 0) + e - po].y;
+            if (e < min(po, pn)) out = split && e == (min(old, now) >> a.ps_shift) ? a.free_ids[off.x] : v;
+            else if (e >= po && e < pn) out = a.free_ids[off.x + split + e - po];
             a.table_out[i] = out;
         }
     }
@@ -413,55 +437,59 @@ __global__ void __launch_bounds__(kBulkThreads) pages_bulk_kernel(const PagesArg
             }
         }
     } else {
-        for (long long i = gt; i < entries; i += GT) {
-            const int4 it = a.list[i];
-            a.ref_out[it.y] = 1;
-            if (OP == PAGES_RESIZE && it.w == 1) atomicSub(a.ref_out + it.x, 1);
-        }
+        for (long long i = gt; i < taken; i += GT) a.ref_out[a.free_ids[i]] = 1;
+        if (OP == PAGES_RESIZE)
+            for (long long i = gt; i < copies; i += GT) atomicSub(a.ref_out + a.list[i].x, 1);
     }
-    // Page contents: each CTA takes 1024 16-byte units of one page, layer and pool at a time.
-    const int unit_shift = a.row_shift;
-    const int rows_per = a.ps * a.Hkv;
-    const long long vecs = (long long)rows_per << unit_shift;      // units of a page
-    const int chunks = (int)((vecs + 4 * kBulkThreads - 1) / (4 * kBulkThreads));
+    // Page contents: a warp takes 32 kVec units (4 KB) of one page, layer and pool at a time,
+    // all loads before the stores.  (A CTA per piece left half of it idle on 8 KB pages.)
+    const int lane = threadIdx.x & 31;
+    const long long warps = GT / 32;
+    const int units = a.ps * a.Hkv << a.row_shift;         // of a page
     const bool head_major = a.head_stride > a.tok_stride;
-    const long long items = (long long)entries * a.layers * 2 * chunks;
-    for (long long it = blockIdx.x; it < items; it += gridDim.x) {
-        const int ch = (int)(it % chunks);
-        long long rest = it / chunks;
-        const int kv = (int)(rest & 1);
-        rest >>= 1;
-        const int layer = (int)(rest % a.layers);
-        const int4 li = a.list[rest / a.layers];
-        if (li.x < 0 || li.z <= 0) continue;
-        char* pool = (kv ? a.v : a.k) + layer * a.layer_stride;
+    const long long items = (long long)copies * a.pieces;
+    for (long long it = gt >> 5; it < items; it += warps) {
+        const int c = items < (1LL << 31) ? (int)fast_div((uint32_t)it, a.div_pieces) : (int)(it / a.pieces);
+        const int piece = (int)(it - (long long)c * a.pieces);
+        const int part = (int)fast_div((uint32_t)piece, a.div_chunks), ch = piece - part * a.chunks;
+        const int4 li = a.list[c];
+        if (li.x < 0) continue;
+        char* pool = (part & 1 ? a.v : a.k) + (part >> 1) * a.layer_stride;
         const char* src = pool + li.x * a.page_stride;
         char* dst = pool + li.y * a.page_stride;
-        uint4 x[4];
-        long long at[4];
+        uint4 x[kVec];
+        long long at[kVec];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const long long v = (long long)ch * 4 * kBulkThreads + k * kBulkThreads + threadIdx.x;
-            const int row = (int)(v >> unit_shift), u = (int)(v & ((1 << unit_shift) - 1));
+        for (int k = 0; k < kVec; ++k) {
+            const int v = ch * 32 * kVec + k * 32 + lane;
+            const int row = v >> a.row_shift, u = v & ((1 << a.row_shift) - 1);
             int tok, h;
             if (head_major) {
                 h = row >> a.ps_shift;
                 tok = row & (a.ps - 1);
             } else {
-                tok = row / a.Hkv;
+                tok = (int)fast_div((uint32_t)row, a.div_heads);
                 h = row - tok * a.Hkv;
             }
-            at[k] = v < vecs && tok < li.z ? tok * a.tok_stride + h * a.head_stride + u * 16 : -1;
-            if (at[k] >= 0) x[k] = *reinterpret_cast<const uint4*>(src + at[k]);
+            at[k] = v < units && tok < li.z ? tok * a.tok_stride + h * a.head_stride + u * 16 : -1;
+            if (at[k] >= 0) x[k] = __ldcs(reinterpret_cast<const uint4*>(src + at[k]));
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (at[k] >= 0) *reinterpret_cast<uint4*>(dst + at[k]) = x[k];
+        for (int k = 0; k < kVec; ++k)
+            if (at[k] >= 0) __stcs(reinterpret_cast<uint4*>(dst + at[k]), x[k]);
     }
 }
 
 template <int OP>
-cudaError_t launch_op(const PagesArgs& a, cudaStream_t st) {
+cudaError_t launch_op(const PagesArgs& a0, cudaStream_t st) {
+    PagesArgs a = a0;
+    const int units = a.ps * a.Hkv << a.row_shift;
+    a.chunks = (units + 32 * kVec - 1) / (32 * kVec);
+    a.pieces = a.layers * 2 * a.chunks;
+    a.div_pieces = make_fastdiv((uint32_t)a.pieces);
+    a.div_chunks = make_fastdiv((uint32_t)a.chunks);
+    a.div_heads = make_fastdiv((uint32_t)a.Hkv);
+    a.div_w = make_fastdiv((uint32_t)a.W);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kCluster);
     cfg.blockDim = dim3(kThreads);

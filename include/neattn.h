@@ -284,7 +284,8 @@ ne_status ne_qkv_prologue(const void* x, const void* gamma, const void* w, void*
  * every layer at once.
  * Supported: page_size a power of two from 8 to 256; D in {32, 64, 128} for bf16
  * (elem_bytes 2) and {32, 64} for f32 (elem_bytes 4); k, v 16-byte aligned and strides
- * multiples of 16 bytes, below 2^39 elements, the strides of an extent above 1 at least D; n_pages < 2^24. */
+ * multiples of 16 bytes, below 2^39 elements, the strides of an extent above 1 at least D; n_pages < 2^24, layers <= 4096,
+ * Hkv <= 1024. */
 typedef struct {
     void* k;
     void* v;
@@ -326,7 +327,7 @@ ne_status ne_rope_spec_init(ne_rope_spec* out, int D, int rot_dim, int layout, d
  *   (one row per sequence, N == B); device memory, 4-byte aligned.
  *   pos_offset: added to every position for the rotation alone (a cache that dropped its
  *   first pages); 0 <= pos_offset < 2^30.
- * Rows outside [cu_new[0], cu_new[B]) are neither read nor written.  A row whose position
+ * Rows outside [cu_new[0], cu_new[B]) have no effect and are not written.  A row whose position
  * is negative (n_b > seq_lens[b]) is not stored and gets q_out = 0.  Bad device-side
  * arguments never reach memory: a cu_new entry outside [0, N] or decreasing, a length
  * outside [0, max_pages * page_size], a page id outside [0, n_pages) are clamped or skipped

@@ -136,11 +136,11 @@ def test_workspace_sizes(lib):
     assert lib.ne_paged_attn_workspace_size(4, 8, 12, 4, 96) == 0
     assert lib.ne_paged_attn_workspace_size(4, 8, 12, 4, 64) % 256 == 0
     assert lib.ne_pages_workspace_size(0, 4, 4) == 0
-    # Header, offsets [n + 1], free ids and (source, target, slots, flag) of every listed page:
-    # min(pages, entries) when pages are taken, half of the pool when they are moved.
+    # Header, two offsets per sequence, free ids and (source, target, slots, 0) of every listed
+    # page: min(pages, entries) when pages are taken, half of the pool when they are moved.
     r = lambda x: -(-x // 256) * 256  # noqa: E731
-    assert lib.ne_pages_workspace_size(1000, 10, 8) == 256 + r(11 * 4) + r(501 * 4) + r(501 * 16)
-    assert lib.ne_pages_workspace_size(100, 10, 80) == 256 + r(11 * 4) + r(100 * 4) + r(100 * 16)
+    assert lib.ne_pages_workspace_size(1000, 10, 8) == 256 + r(10 * 8) + r(501 * 4) + r(501 * 16)
+    assert lib.ne_pages_workspace_size(100, 10, 80) == 256 + r(10 * 8) + r(100 * 4) + r(100 * 16)
 
 
 # ---------------------------------------------------------------- rope spec
