@@ -28,7 +28,7 @@ enum WaitSite : int {
     // or a fork got a parent that is not a sequence.
     SITE_PAGED_CU = 0x404, SITE_PAGED_LEN = 0x405, SITE_PAGED_PAGE = 0x406, SITE_PAGES_PARENT = 0x407,
     SITE_PAGED_Q = 0x601, SITE_PAGED_KV_FULL, SITE_PAGED_KV_EMPTY, SITE_PAGED_S_FULL, SITE_PAGED_P_READY,
-    SITE_PAGED_O_FULL, SITE_PAGED_DRAIN,
+    SITE_PAGED_O_FULL, SITE_PAGED_DRAIN, SITE_PAGED_SEG,
 };
 
 // Length of sequence b: T when the call has no per-sequence lengths, else seq_lens[b]

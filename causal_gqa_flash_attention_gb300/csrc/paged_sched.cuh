@@ -149,6 +149,17 @@ struct PagedWalk {
     }
 };
 
+// The CTA's share of `total`: CTA c of at most p.C, none with less than min_work but the last few
+// keys of a small call.
+__device__ __forceinline__ void paged_interval(const PagedSplit& p, long long total, int c, long long& w0, long long& w1) {
+    const long long most = paged_div(total, p.min_work);
+    const int C = most < 1 ? 1 : (most < p.C ? (int)most : p.C);
+    const long long each = paged_div(total, C), rest = total - each * C;
+    const long long i = min(c, C), j = min(c + 1, C);
+    w0 = each * i + min(i, rest);
+    w1 = each * j + min(j, rest);
+}
+
 // Shared scratch of paged_locate.
 struct PagedLocate {
     long long warp_sum[32];
@@ -190,16 +201,6 @@ __device__ __forceinline__ void paged_locate(const PagedAttnArgs& a, int c, Page
         __syncthreads();
         return x + (warp ? sm.warp_sum[warp - 1] : 0);
     };
-    auto interval = [&](long long total) {
-        const long long most = paged_div(total, a.p.min_work);
-        const int C = most < 1 ? 1 : (most < a.p.C ? (int)most : a.p.C);
-        const long long each = paged_div(total, C), rest = total - each * C;
-        const long long i = min(c, C), j = min(c + 1, C);
-        sm.w0 = each * i + min(i, rest);
-        sm.w1 = each * j + min(j, rest);
-        sm.start = 0;
-        sm.b = 0;
-    };
     long long mine = work(tid), incl = scan(mine);
     long long total = sm.warp_sum[T / 32 - 1];
     for (int b0 = T; b0 < B; b0 += T) {
@@ -207,7 +208,14 @@ __device__ __forceinline__ void paged_locate(const PagedAttnArgs& a, int c, Page
         scan(work(b0 + tid));
         total += sm.warp_sum[T / 32 - 1];
     }
-    if (tid == 0) interval(total);
+    if (tid == 0) {
+        long long w0, w1;
+        paged_interval(a.p, total, c, w0, w1);
+        sm.w0 = w0;
+        sm.w1 = w1;
+        sm.start = 0;
+        sm.b = 0;
+    }
     __syncthreads();
     const long long w0 = sm.w0, w1 = sm.w1;
     if (w0 < w1) {
@@ -229,6 +237,45 @@ __device__ __forceinline__ void paged_locate(const PagedAttnArgs& a, int c, Page
     }
     if (report && bad) report_error(a.err, bad);
     __syncthreads();
+}
+
+// paged_locate for one warp: the walk of CTA c from its first unit on.
+__device__ __forceinline__ void paged_locate_warp(const PagedAttnArgs& a, int c, PagedWalk& walk, bool report) {
+    const int lane = threadIdx.x & 31, B = a.s.B;
+    int bad = 0;
+    auto work = [&](int b) -> long long {
+        if (b >= B) return 0;
+        const PagedSeq q = paged_seq(a.s, b, bad);
+        return paged_group_cost(q, a.p.tpt, a.p.ovh) * a.p.hg;
+    };
+    long long total = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < B; b0 += 32) total += work(b0 + lane);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    long long w0, w1, start = 0;
+    paged_interval(a.p, total, c, w0, w1);
+    int b = 0;
+#pragma unroll 1
+    for (int b0 = 0; w0 < w1 && b0 < B; b0 += 32) {
+        const long long mine = work(b0 + lane);
+        long long x = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, mine > 0 && w0 < start + x);
+        if (hit) {
+            const int l = __ffs(hit) - 1;
+            b = b0 + l;
+            start += __shfl_sync(0xffffffffu, x - mine, l);
+            break;
+        }
+        start += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (report && bad) report_error(a.err, bad);
+    walk.init(a, w0, w1, b, start);
 }
 
 // The records of both slots of CTA c are written by every call (state 0: no such part).

@@ -20,6 +20,7 @@
 //                of its own, S(t + 1) goes first, as soon as S(t) is in registers.
 //   warp 2       zeroes the V rows behind a sequence's length in the tile that holds it (P is 0
 //                there, but 0 x NaN is not).
+//   warp 3       finds the CTA's parts (paged_sched.cuh) and queues them for the others.
 //   warps 4-11   softmax: thread r of subtile u owns row r (TMEM lane r).
 // TMEM: S_u at 128 u, O_u behind both; P_u (bf16) over S_u's first half at D 128, where TMEM
 // is full, in columns of its own at D 64.
@@ -32,6 +33,9 @@
 
 namespace ne {
 namespace {
+
+constexpr int kSegs = 4;               // parts in the queue from warp 3 to the others
+constexpr int kSegReaders = 11;        // warps 0, 1, 2 and 4-11
 
 template <int D>
 struct TileCfg {
@@ -64,6 +68,31 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// Transposes a 4 x 4 block of 16-byte units held by four neighbouring lanes: afterwards lane l
+// of the four holds unit l of each of them.
+__device__ __forceinline__ uint4 shfl_xor4(const uint4& v, int m) {
+    return make_uint4(__shfl_xor_sync(0xffffffffu, v.x, m), __shfl_xor_sync(0xffffffffu, v.y, m),
+                      __shfl_xor_sync(0xffffffffu, v.z, m), __shfl_xor_sync(0xffffffffu, v.w, m));
+}
+__device__ __forceinline__ void transpose4(uint4 (&v)[4], int l) {
+    const uint4 a = shfl_xor4(l & 1 ? v[0] : v[1], 1), b = shfl_xor4(l & 1 ? v[2] : v[3], 1);
+    if (l & 1) {
+        v[0] = a;
+        v[2] = b;
+    } else {
+        v[1] = a;
+        v[3] = b;
+    }
+    const uint4 c = shfl_xor4(l & 2 ? v[0] : v[2], 2), d = shfl_xor4(l & 2 ? v[1] : v[3], 2);
+    if (l & 2) {
+        v[0] = c;
+        v[1] = d;
+    } else {
+        v[2] = c;
+        v[3] = d;
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(384, 1)
     paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -76,7 +105,8 @@ __global__ void __launch_bounds__(384, 1)
     __shared__ __align__(8) uint64_t bar_q_full, bar_q_empty, bar_vfix[2], bar_final;
     __shared__ __align__(8) uint64_t bar_full[C::NS], bar_empty[C::NS];
     __shared__ __align__(8) uint64_t bar_s_full[2], bar_p_ready[2], bar_o_full[2], bar_s_free[2];
-    __shared__ PagedLocate loc;
+    __shared__ __align__(8) uint64_t bar_seg_full[kSegs], bar_seg_empty[kSegs];
+    __shared__ PagedSeg s_seg[kSegs];                      // the CTA's parts in order (b < 0: the end)
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -97,6 +127,10 @@ __global__ void __launch_bounds__(384, 1)
             mbar_init(smem_u32(&bar_vfix[u]), 32);         // the k-th fix arrives on k % 2: warp 2 can be one
                                                            // fix ahead of the issuer (one part, by its Q), not two
         }
+        for (int s = 0; s < kSegs; ++s) {
+            mbar_init(smem_u32(&bar_seg_full[s]), 1);
+            mbar_init(smem_u32(&bar_seg_empty[s]), kSegReaders);
+        }
         abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tm_q);
@@ -113,15 +147,23 @@ __global__ void __launch_bounds__(384, 1)
     tc_fence_after();
     griddep_launch_dependents();                           // after the TMEM allocation
     griddep_wait();
-    paged_locate<C::THREADS>(a, blockIdx.x, loc, blockIdx.x == 0);
-    if (tid < 2) a.part_info[blockIdx.x * 2 + tid] = make_int4(0, 0, 0, 0);
-    __syncthreads();                                       // (the records' writers below come after)
     const uint32_t tm = tmem_slot;
     const WaitCtx w{a.err, &abort_flag, a.timeout_ns};
     const int sub = a.p.sub;                               // tokens of a subtile
-    PagedWalk walk;
-    walk.init(a, loc.w0, loc.w1, loc.b, loc.start);
     PagedSeg g;
+    int nseg = 0;
+    // The CTA's next part, from the queue; false at its end (or when a wait ran out).  One warp
+    // finds the parts for all: the arithmetic has long latencies and a copy of it in every role
+    // cost each of them microseconds of instruction fetches at the start.
+    auto next_part = [&]() -> bool {
+        const int s = nseg % kSegs;
+        if (!mbar_wait_warp(smem_u32(&bar_seg_full[s]), (nseg / kSegs) & 1, w, SITE_PAGED_SEG)) return false;
+        ++nseg;
+        g = s_seg[s];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bar_seg_empty[s]));
+        return g.b >= 0;
+    };
     // A part's K tile t sits at ring index 2 i, its V tile at 2 i + 1, i counting the CTA's tiles.
 
     if (warp == 0) {
@@ -131,7 +173,7 @@ __global__ void __launch_bounds__(384, 1)
         const int mask = (1 << a.c.ps_shift) - 1;
         const int npg = a.c.ps_shift >= 7 ? 1 : 128 >> a.c.ps_shift;   // pages of a tile
         const int rows = 128 / npg;
-        while (ok && walk.next(a, g)) {
+        while (ok && next_part()) {
             if (g.t0 == g.t1) continue;                    // no keys: the softmax warps write the rows
             const int* trow = a.s.table + (size_t)g.b * a.s.W;
             auto page = [&](int t) -> int {                // page of this lane's part of tile t
@@ -214,7 +256,7 @@ __global__ void __launch_bounds__(384, 1)
             tc_fence_after();
             return r;
         };
-        while (ok && walk.next(a, g)) {
+        while (ok && next_part()) {
             if (g.t0 == g.t1) continue;
             const int n_sub = g.ntok > sub ? 2 : 1, nt = g.t1 - g.t0;
             if (!(ok = mbar_wait_warp(smem_u32(&bar_q_full), seg & 1, w, SITE_PAGED_Q))) break;
@@ -288,7 +330,7 @@ __global__ void __launch_bounds__(384, 1)
         // fall a phase behind the other.
         int item = 0, fixes = 0;
         bool ok = true;
-        while (ok && walk.next(a, g)) {
+        while (ok && next_part()) {
             for (int i = 0; ok && i < 2 * (g.t1 - g.t0); ++i, ++item) {
                 const int s = item % C::NS;
                 if (!(ok = mbar_wait_warp(smem_u32(&bar_full[s]), (item / C::NS) & 1, w, SITE_PAGED_KV_FULL))) break;
@@ -306,7 +348,26 @@ __global__ void __launch_bounds__(384, 1)
                 if (lane == 0) mbar_arrive(smem_u32(&bar_empty[s]));
             }
         }
-    } else if (warp >= 4) {
+    } else if (warp == 3) {
+        // ------------------------------------------------------------ the CTA's parts
+        if (lane < 2) a.part_info[blockIdx.x * 2 + lane] = make_int4(0, 0, 0, 0);
+        PagedWalk walk;
+        paged_locate_warp(a, blockIdx.x, walk, blockIdx.x == 0);
+        bool more = true;
+        for (int k = 0; more; ++k) {
+            const int s = k % kSegs;
+            more = walk.next(a, g);
+            if (!more) g.b = -1;
+            if (k >= kSegs &&
+                !mbar_wait_warp(smem_u32(&bar_seg_empty[s]), (k / kSegs - 1) & 1, w, SITE_PAGED_SEG))
+                break;
+            if (lane == 0) {
+                s_seg[s] = g;
+                mbar_arrive(smem_u32(&bar_seg_full[s]));
+            }
+            __syncwarp();
+        }
+    } else {
         // ------------------------------------------------------------ softmax of subtile u
         const int u = (warp - 4) >> 2;
         const int r = (warp & 3) * 32 + lane;              // row = TMEM lane
@@ -315,7 +376,7 @@ __global__ void __launch_bounds__(384, 1)
         const float sl2 = a.scale_log2;
         int tiles = 0, parts = 0;
         bool ok = true;
-        while (ok && walk.next(a, g)) {
+        while (ok && next_part()) {
             const int ntok = min(sub, g.ntok - u * sub);   // tokens of this subtile
             const int live_rows = ntok * a.G;
             if (ntok <= 0) continue;
@@ -424,27 +485,45 @@ __global__ void __launch_bounds__(384, 1)
             tc_fence_after();
             const bool whole = g.whole();
             const float inv = !whole ? 1.f : l > 0.f ? 1.f / l : 0.f;
-            const size_t prow = (size_t)(blockIdx.x * 2 + g.slot()) * a.p.rows + u * 128 + r;
+            // A thread holds a row's columns; four neighbours exchange 16-byte units, so that a store
+            // writes 64 bytes of each of eight rows instead of 16 of each of 32 (at D 128 the
+            // scattered stores took 4 us a part).
+            const int prow = (blockIdx.x * 2 + g.slot()) * a.p.rows + u * 128 + r;
+            const int q0 = r & ~3, ql = lane & 3;
+            int row4[4];                                   // rows q0 .. q0 + 3 of the output (or the part)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) row4[k] = whole ? __shfl_sync(0xffffffffu, (int)orow, (lane & ~3) + k) : prow - ql + k;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
-                __syncwarp();                              // (TMEM loads are warp-wide: the lanes meet again)
                 tmem_ld_cols<1>(oc + c, o);
-                if (!live) {
-                } else if (whole) {
-                    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + orow * D + c);
+                if (whole) {
+                    uint4 v[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         uint32_t pk[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             pk[i] = pack2(__uint_as_float(o[8 * k + 2 * i]) * inv, __uint_as_float(o[8 * k + 2 * i + 1]) * inv);
-                        dst[k] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                        v[k] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
                     }
-                } else {
-                    uint4* dst = reinterpret_cast<uint4*>(a.part_o + prow * D + c);
+                    transpose4(v, ql);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                    for (int k = 0; k < 4; ++k)
+                        if (q0 + k < live_rows)
+                            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + (long long)row4[k] * D + c + 8 * ql) = v[k];
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 32; h += 16) {
+                        uint4 v[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) v[k] = make_uint4(o[h + 4 * k], o[h + 4 * k + 1], o[h + 4 * k + 2], o[h + 4 * k + 3]);
+                        transpose4(v, ql);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (q0 + k < live_rows)
+                                *reinterpret_cast<uint4*>(a.part_o + (size_t)row4[k] * D + c + h + 4 * ql) = v[k];
+                    }
                 }
             }
             __syncwarp();
