@@ -51,9 +51,10 @@ struct PagedSplit {
     int tpt;                          // tokens per work unit
     int hg;                           // head groups: Hkv * ceil(G / rows) (rows < G only in the short kernels)
     int gs;                           // query heads of a group
-    int bn;                           // keys per tile: what a unit may be cut into
+    int bn_shift;                     // log2 of the keys per tile: what a unit may be cut into
+    FastDiv div_tpt;                  // by tpt
     int ovh;                          // fixed cost of a unit, in keys
-    int min_work;                     // least work of a CTA, in keys
+    int min_shift;                    // log2 of a CTA's least work, in keys
     int rows;                         // rows of a unit (partials are stored at this pitch)
     int sub;                          // tokens of a unit's first 128-row subtile (0: rows are contiguous)
 };

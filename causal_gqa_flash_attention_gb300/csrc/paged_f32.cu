@@ -98,13 +98,15 @@ __global__ void __launch_bounds__(F32Cfg<D, MANY>::THREADS) paged_f32_kernel(con
         const int first = g.t0 * C::BN + wk * 32;
         const int lfirst = first + (MANY ? warp * LROWS : 0);
         int pid = page_of(a.c, trow, lfirst + lane, g.kv, a.err);
+        int pid1 = nsteps > 1 ? page_of(a.c, trow, lfirst + C::BN + lane, g.kv, a.err) : -1;
         auto issue = [&](int j) {
             if (j < nsteps) {
                 const int at = lfirst + j * C::BN;
-                const int pnext = j + 1 < nsteps ? page_of(a.c, trow, at + C::BN + lane, g.kv, a.err) : -1;
+                const int pid2 = j + 2 < nsteps ? page_of(a.c, trow, at + 2 * C::BN + lane, g.kv, a.err) : -1;
                 const uint32_t st = ring0 + (j % kStages) * 2 * C::TILE;
                 load_rows<LROWS, U>(st, st + C::TILE, kp, vp, a.c, 4, MANY ? warp * LROWS : 0, at, g.kv, pid, lane);
-                pid = pnext;
+                pid = pid1;
+                pid1 = pid2;
             }
             cp_async_commit();
         };

@@ -79,20 +79,28 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedAttnArg
         put(static_cast<T*>(a.o) + row * D + e, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
         if (e == 0) a.lse[row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
     };
-    if (np <= 12) {                                        // few parts: a row per lane group
+    if (live > 2 * (int)gridDim.y) {                       // many rows: one per lane group, four parts in flight
         for (int i = blockIdx.y * GR + grp; i < live; i += gridDim.y * GR) {
             float m = -INFINITY, l = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int k = 0; k < np; ++k) {
-                const size_t at = (size_t)s_part[k] * a.p.rows + stored(i);
-                const float2 ml = a.part_ml[at];
-                add_part(m, l, o, ml.x, ml.y, *reinterpret_cast<const float4*>(a.part_o + at * D + e));
+            for (int k0 = 0; k0 < np; k0 += 4) {
+                float2 ml[4];
+                float4 x[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const size_t at = (size_t)s_part[min(k0 + k, np - 1)] * a.p.rows + stored(i);
+                    ml[k] = a.part_ml[at];
+                    x[k] = *reinterpret_cast<const float4*>(a.part_o + at * D + e);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (k0 + k < np) add_part(m, l, o, ml[k].x, ml[k].y, x[k]);
             }
             finish(i, m, l, o);
         }
         return;
     }
-    for (int i = blockIdx.y; i < live; i += gridDim.y) {   // many parts: the groups share a row's
+    for (int i = blockIdx.y; i < live; i += gridDim.y) {   // few rows: the groups share a row's parts
         float m = -INFINITY, l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         const int per = (np + GR - 1) / GR;
@@ -118,7 +126,7 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedAttnArg
 }  // namespace
 
 cudaError_t launch_paged_join(bool f32, int D, const PagedAttnArgs& a, cudaStream_t st) {
-    const dim3 grid(a.p.C, a.p.rows < 8 ? a.p.rows : 8), block(kThreads);
+    const dim3 grid(a.p.C, a.p.rows <= 32 ? 4 : 8), block(kThreads);
     switch (D) {
         case 32:
             return f32 ? launch_k(paged_join_kernel<float, 32>, grid, block, 0, st, a)
@@ -154,22 +162,25 @@ PagedSplit paged_split(PagedKind kind, int D, int Hkv, int G) {
         p.hg = Hkv * ((G + p.gs - 1) / p.gs);
     };
     p.ovh = 128;
-    p.min_work = 192;
+    p.min_shift = 7;
+    auto tile = [&](int keys) {
+        while ((1 << p.bn_shift) < keys) ++p.bn_shift;
+    };
     switch (kind) {
         case PAGED_SHORT16:
         case PAGED_SHORT32:
             rows(kind == PAGED_SHORT16 ? 16 : 32);
-            p.bn = paged_short_bn(D);
+            tile(paged_short_bn(D));
             p.C = 2 * kSms;
             break;
         case PAGED_F32_FEW:
             rows(8);
-            p.bn = paged_f32_bn(false);
+            tile(paged_f32_bn(false));
             p.C = D == 32 ? 2 * kSms : kSms;
             break;
         case PAGED_F32_MANY:
             rows(64);
-            p.bn = paged_f32_bn(true);
+            tile(paged_f32_bn(true));
             p.C = 2 * kSms;
             break;
         case PAGED_TILES:                                  // G <= 128
@@ -178,12 +189,13 @@ PagedSplit paged_split(PagedKind kind, int D, int Hkv, int G) {
             p.sub = 128 / G;
             p.tpt = 2 * p.sub;
             p.hg = Hkv;
-            p.bn = 128;
+            tile(128);
             p.C = kSms;
             p.ovh = 256;
-            p.min_work = 512;
+            p.min_shift = 9;
             break;
     }
+    p.div_tpt = make_fastdiv((uint32_t)p.tpt);
     return p;
 }
 

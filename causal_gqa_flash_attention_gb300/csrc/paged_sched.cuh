@@ -52,17 +52,22 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedBatch& s, int b, int& b
 }
 
 // Cost of tiles 0 .. r-1 of a sequence (r below its tile count): each ovh + max(0, base + (k+1) tpt).
-__device__ __forceinline__ long long paged_prefix(int r, int base, int tpt, int ovh) {
-    const int r0 = base < 0 ? min(r, -base / tpt) : 0;    // tiles without a key
+__device__ __forceinline__ long long paged_prefix(int r, int base, const PagedSplit& p) {
+    if (r == 0) return 0;
+    const int r0 = base < 0 ? min(r, (int)fast_div((uint32_t)-base, p.div_tpt)) : 0;   // tiles without a key
     const long long m = r - r0;
-    return (long long)r * ovh + m * base + (long long)tpt * (((long long)r * (r + 1) - (long long)r0 * (r0 + 1)) / 2);
+    return (long long)r * p.ovh + m * base + (long long)p.tpt * (((long long)r * (r + 1) - (long long)r0 * (r0 + 1)) / 2);
+}
+
+// Tiles of a sequence.
+__device__ __forceinline__ int paged_tiles(int n, const PagedSplit& p) {
+    return (int)fast_div((uint32_t)(n + p.tpt - 1), p.div_tpt);
 }
 
 // Cost of one head group of a sequence.
-__device__ __forceinline__ long long paged_group_cost(const PagedSeq& q, int tpt, int ovh) {
+__device__ __forceinline__ long long paged_group_cost(const PagedSeq& q, const PagedSplit& p) {
     if (q.n == 0) return 0;
-    const int nt = (q.n + tpt - 1) / tpt;
-    return paged_prefix(nt - 1, q.len - q.n, tpt, ovh) + ovh + q.len;
+    return paged_prefix(paged_tiles(q.n, p) - 1, q.len - q.n, p) + p.ovh + q.len;
 }
 
 // What a CTA does with one unit: key tiles [t0, t1) of nt_keys, for tokens tok .. tok+ntok-1
@@ -87,10 +92,11 @@ struct PagedWalk {
     __device__ __forceinline__ void load(const PagedAttnArgs& a) {
         int bad = 0;
         q = paged_seq(a.s, b, bad);
-        nt = (q.n + a.p.tpt - 1) / a.p.tpt;
+        nt = paged_tiles(q.n, a.p);
     }
-    // From the sequence that holds w0 and where that sequence starts.
-    __device__ __forceinline__ void init(const PagedAttnArgs& a, long long w0_, long long w1_, int b_, long long start) {
+    // From the sequence that holds w0 (q, set by the caller or by load) and where it starts.
+    __device__ __forceinline__ void init(const PagedAttnArgs& a, long long w0_, long long w1_, int b_, long long start,
+                                         bool loaded = false) {
         w0 = w0_;
         w1 = w1_;
         b = b_;
@@ -99,19 +105,20 @@ struct PagedWalk {
             cur = w1;
             return;
         }
-        load(a);
-        const long long S = paged_group_cost(q, a.p.tpt, a.p.ovh);
+        if (loaded) nt = paged_tiles(q.n, a.p);
+        else load(a);
+        const long long S = paged_group_cost(q, a.p);
         const long long off = w0 - start;
         hg = (int)paged_div(off, S);
         const long long x = off - (long long)hg * S;
         int lo = 0, hi = nt - 1;                           // the last tile whose start is at or before x
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (paged_prefix(mid, q.len - q.n, a.p.tpt, a.p.ovh) <= x) lo = mid;
+            if (paged_prefix(mid, q.len - q.n, a.p) <= x) lo = mid;
             else hi = mid - 1;
         }
         r = lo;
-        cur = start + (long long)hg * S + paged_prefix(r, q.len - q.n, a.p.tpt, a.p.ovh);
+        cur = start + (long long)hg * S + paged_prefix(r, q.len - q.n, a.p);
     }
     // The next part of the interval, false at its end.
     __device__ __forceinline__ bool next(const PagedAttnArgs& a, PagedSeg& g) {
@@ -119,7 +126,7 @@ struct PagedWalk {
             const int base = q.len - q.n;
             const int kv = r == nt - 1 ? q.len : max(0, base + (r + 1) * a.p.tpt);
             const int cost = a.p.ovh + kv;
-            const int ntk = (kv + a.p.bn - 1) / a.p.bn;
+            const int ntk = (kv + (1 << a.p.bn_shift) - 1) >> a.p.bn_shift;
             g.t0 = w0 <= cur ? 0 : (int)paged_div((w0 - cur) * ntk + cost / 2, cost);
             g.t1 = w1 >= cur + cost ? ntk : (int)paged_div((w1 - cur) * ntk + cost / 2, cost);
             g.b = b;
@@ -152,7 +159,7 @@ struct PagedWalk {
 // The CTA's share of `total`: CTA c of at most p.C, none with less than min_work but the last few
 // keys of a small call.
 __device__ __forceinline__ void paged_interval(const PagedSplit& p, long long total, int c, long long& w0, long long& w1) {
-    const long long most = paged_div(total, p.min_work);
+    const long long most = total >> p.min_shift;
     const int C = most < 1 ? 1 : (most < p.C ? (int)most : p.C);
     const long long each = paged_div(total, C), rest = total - each * C;
     const long long i = min(c, C), j = min(c + 1, C);
@@ -178,7 +185,7 @@ __device__ __forceinline__ void paged_locate(const PagedAttnArgs& a, int c, Page
     auto work = [&](int b) -> long long {
         if (b >= B) return 0;
         const PagedSeq q = paged_seq(a.s, b, bad);
-        return paged_group_cost(q, a.p.tpt, a.p.ovh) * a.p.hg;
+        return paged_group_cost(q, a.p) * a.p.hg;
     };
     // Inclusive sums over the CTA; the total in sm.warp_sum[T / 32 - 1].
     auto scan = [&](long long x) -> long long {
@@ -239,26 +246,31 @@ __device__ __forceinline__ void paged_locate(const PagedAttnArgs& a, int c, Page
     __syncthreads();
 }
 
-// paged_locate for one warp: the walk of CTA c from its first unit on.
+// paged_locate for one warp: the walk of CTA c from its first unit on.  Written for few
+// dependent steps: all CTAs wait for it at the start of a call.
 __device__ __forceinline__ void paged_locate_warp(const PagedAttnArgs& a, int c, PagedWalk& walk, bool report) {
     const int lane = threadIdx.x & 31, B = a.s.B;
     int bad = 0;
+    PagedSeq q = {0, 0, 0};
     auto work = [&](int b) -> long long {
         if (b >= B) return 0;
-        const PagedSeq q = paged_seq(a.s, b, bad);
-        return paged_group_cost(q, a.p.tpt, a.p.ovh) * a.p.hg;
+        q = paged_seq(a.s, b, bad);
+        return paged_group_cost(q, a.p) * a.p.hg;
     };
-    long long total = 0;
+    long long mine = work(lane), total = mine;
 #pragma unroll 1
-    for (int b0 = 0; b0 < B; b0 += 32) total += work(b0 + lane);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    for (int b0 = 32; b0 < B; b0 += 32) total += work(b0 + lane);
+    // The sum over the warp in three limbs of 21 bits, one reduction each (total is below 2^58).
+    const unsigned l0 = __reduce_add_sync(0xffffffffu, (unsigned)total & 0x1fffffu);
+    const unsigned l1 = __reduce_add_sync(0xffffffffu, (unsigned)(total >> 21) & 0x1fffffu);
+    const unsigned l2 = __reduce_add_sync(0xffffffffu, (unsigned)(total >> 42));
+    total = (long long)l0 + ((long long)l1 << 21) + ((long long)l2 << 42);
     long long w0, w1, start = 0;
     paged_interval(a.p, total, c, w0, w1);
     int b = 0;
 #pragma unroll 1
     for (int b0 = 0; w0 < w1 && b0 < B; b0 += 32) {
-        const long long mine = work(b0 + lane);
+        if (B > 32) mine = work(b0 + lane);
         long long x = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -270,12 +282,15 @@ __device__ __forceinline__ void paged_locate_warp(const PagedAttnArgs& a, int c,
             const int l = __ffs(hit) - 1;
             b = b0 + l;
             start += __shfl_sync(0xffffffffu, x - mine, l);
+            walk.q.tok0 = __shfl_sync(0xffffffffu, q.tok0, l);
+            walk.q.n = __shfl_sync(0xffffffffu, q.n, l);
+            walk.q.len = __shfl_sync(0xffffffffu, q.len, l);
             break;
         }
         start += __shfl_sync(0xffffffffu, x, 31);
     }
     if (report && bad) report_error(a.err, bad);
-    walk.init(a, w0, w1, b, start);
+    walk.init(a, w0, w1, b, start, true);
 }
 
 // The records of both slots of CTA c are written by every call (state 0: no such part).

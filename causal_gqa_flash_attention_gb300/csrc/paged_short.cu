@@ -65,21 +65,39 @@ __global__ void __launch_bounds__(kThreads, 2) paged_short_kernel(const PagedAtt
     using C = ShortCfg<D>;
     constexpr int KT = C::KT, U = C::U, NT = KT / 8, NO = D / 8;
     extern __shared__ __align__(128) uint8_t ring[];
-    __shared__ PagedLocate loc;
+    __shared__ PagedSeg s_part[2];                         // the CTA's parts in turn (b < 0: the end)
     __shared__ float s_m[kWarps][16 * MT], s_l[kWarps][16 * MT];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g8 = lane >> 2, t4 = lane & 3;
     griddep_launch_dependents();
     griddep_wait();
-    paged_locate<kThreads>(a, blockIdx.x, loc, blockIdx.x == 0);
-    if (tid < 2) a.part_info[blockIdx.x * 2 + tid] = make_int4(0, 0, 0, 0);
-
-    PagedWalk walk;
-    walk.init(a, loc.w0, loc.w1, loc.b, loc.start);
     const uint32_t ring0 = smem_u32(ring) + warp * C::RING;
+    // Warp 0 finds the CTA's parts.  Meanwhile the others run the loop below once on a part
+    // without rows and keys (it reads and writes nothing but their own rings): a kernel's first
+    // pass through its code waits for the code itself, three microseconds that are then spent
+    // beside the search instead of behind it.
+    PagedWalk walk;
     PagedSeg g;
-    while (walk.next(a, g)) {
+    bool dry = warp != 0;
+    int turn = 0;
+    if (dry) {
+        if (warp == 1) prefetch_table(a.s, blockIdx.x, gridDim.x, lane);
+        g.b = g.hg = g.r = g.tok = g.ntok = g.tok0 = g.base = g.len = g.kv = g.t0 = 0;
+        g.t1 = g.nt = 1;
+    } else {
+        paged_locate_warp(a, blockIdx.x, walk, blockIdx.x == 0);
+        if (lane < 2) a.part_info[blockIdx.x * 2 + lane] = make_int4(0, 0, 0, 0);
+        if (!walk.next(a, g)) g.b = -1;
+        if (lane == 0) s_part[0] = g;
+    }
+    while (true) {
+        if (!dry) {
+            __syncthreads();                               // the part is there, the rings are free
+            g = s_part[turn & 1];
+            ++turn;
+            if (g.b < 0) break;
+        }
         const int hs = a.G > a.p.gs ? g.hg % ((a.G + a.p.gs - 1) / a.p.gs) : 0;
         const int hkv = a.G > a.p.gs ? g.hg / ((a.G + a.p.gs - 1) / a.p.gs) : g.hg;
         const int h0 = hkv * a.G + hs * a.p.gs;            // first query head of the unit
@@ -126,23 +144,26 @@ __global__ void __launch_bounds__(kThreads, 2) paged_short_kernel(const PagedAtt
         // Steps of this warp: keys (t C::BN + warp KT) of the part's tiles t.
         const int nsteps = g.t1 - g.t0;
         const int first = g.t0 * C::BN + warp * KT;
+        // Page ids are fetched two steps ahead of the copies that need them, which run two steps
+        // ahead of the products.
         int pid = page_of(a.c, trow, first + lane, g.kv, a.err);
-        auto issue = [&](int j) {                          // step j of the part, stage j % kStages
-            if (j < nsteps) {
-                const int at = first + j * C::BN;
-                const int pnext = j + 1 < nsteps ? page_of(a.c, trow, at + C::BN + lane, g.kv, a.err) : -1;
-                const uint32_t st = ring0 + (j % kStages) * 2 * C::TILE;
+        int pid1 = nsteps > 1 ? page_of(a.c, trow, first + C::BN + lane, g.kv, a.err) : -1;
+#pragma unroll 1
+        for (int j = 1 - kStages; j < nsteps; ++j) {
+            __syncwarp();                                  // step j - 1 has been read by the whole warp
+            const int jn = j + kStages - 1;                // into the stage of step j - 1
+            if (jn < nsteps) {
+                const int at = first + jn * C::BN;
+                const int pid2 = jn + 2 < nsteps ? page_of(a.c, trow, at + 2 * C::BN + lane, g.kv, a.err) : -1;
+                const uint32_t st = ring0 + (jn % kStages) * 2 * C::TILE;
                 load_rows<KT, U>(st, st + C::TILE, kp, vp, a.c, 2, 0, at, g.kv, pid, lane);
-                pid = pnext;
+                pid = pid1;
+                pid1 = pid2;
             }
             cp_async_commit();
-        };
-#pragma unroll
-        for (int j = 0; j < kStages - 1; ++j) issue(j);
-        for (int j = 0; j < nsteps; ++j) {
-            cp_async_wait<kStages - 2>();
-            __syncwarp();                                  // step j has landed for the whole warp; step j-1 has been read
-            issue(j + kStages - 1);
+            if (j < 0) continue;
+            cp_async_wait<kStages - 1>();
+            __syncwarp();                                  // step j has landed for the whole warp
             const uint32_t sk = ring0 + (j % kStages) * 2 * C::TILE, sv = sk + C::TILE;
             const int k0 = first + j * C::BN;
 
@@ -238,6 +259,16 @@ __global__ void __launch_bounds__(kThreads, 2) paged_short_kernel(const PagedAtt
         }
         cp_async_wait<0>();
 
+        if (dry) {
+            dry = false;
+            continue;
+        }
+        if (warp == 0) {
+            PagedSeg n;
+            if (!walk.next(a, n)) n.b = -1;
+            if (lane == 0) s_part[turn & 1] = n;
+        }
+
         // Join the four warps: their outputs take the place of the rings.
 #pragma unroll
         for (int m = 0; m < MT; ++m)
@@ -294,7 +325,6 @@ __global__ void __launch_bounds__(kThreads, 2) paged_short_kernel(const PagedAtt
             }
         }
         if (!g.whole() && tid == 0) a.part_info[pslot] = paged_record(g);
-        __syncthreads();                                   // the rings are free again
     }
 }
 

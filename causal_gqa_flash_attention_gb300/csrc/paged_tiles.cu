@@ -29,6 +29,7 @@
 // Every wait is bounded; a CTA that gives up reports, drains its copies and UMMAs, frees its
 // TMEM and ends.
 #include <cuda_bf16.h>
+#include "paged_load.cuh"
 #include "paged_sched.cuh"
 
 namespace ne {
@@ -186,7 +187,7 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 return p;
             };
-            int next = page(g.t0);
+            int next = page(g.t0), next1 = g.t0 + 1 < g.t1 ? page(g.t0 + 1) : 0;   // two tiles ahead
             if (seg > 0 && !(ok = mbar_wait_warp(smem_u32(&bar_q_empty), (seg - 1) & 1, w, SITE_PAGED_Q))) break;
             const int n_sub = g.ntok > sub ? 2 : 1;
             if (lane == 0) {
@@ -200,7 +201,8 @@ __global__ void __launch_bounds__(384, 1)
             ++seg;
             for (int t = g.t0; ok && t < g.t1; ++t) {
                 const int p = next;
-                if (t + 1 < g.t1) next = page(t + 1);
+                next = next1;
+                if (t + 2 < g.t1) next1 = page(t + 2);
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv, ++item) {
                     const int s = item % C::NS;
@@ -328,6 +330,7 @@ __global__ void __launch_bounds__(384, 1)
         // ------------------------------------------------------------ V rows behind the length
         // It follows every slot's phases and releases each along with the issuer, so neither can
         // fall a phase behind the other.
+        prefetch_table(a.s, blockIdx.x, gridDim.x, lane);
         int item = 0, fixes = 0;
         bool ok = true;
         while (ok && next_part()) {

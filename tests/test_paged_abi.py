@@ -199,7 +199,7 @@ def test_binding_refuses_host_tensors_and_mismatches(lib):
 class Split:
     """How the attention kernels cut a call, step by step as in paged_sched.cuh."""
 
-    def __init__(self, n, lens, Hkv, G, rows, bn, C, ovh=128, min_work=512):
+    def __init__(self, n, lens, Hkv, G, rows, bn, C, ovh=128, min_work=128):
         self.n, self.lens, self.bn, self.ovh = n, lens, bn, ovh
         self.gs = min(G, rows)
         self.tpt = rows // self.gs
