@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -385,7 +386,7 @@ def rope_spec(D: int, rot_dim: int | None = None, theta: float = 10000.0, layout
 
 def _launch(fn, index, *args):
     """Calls fn with the device's current stream as last argument, on that device."""
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(index):
@@ -394,16 +395,19 @@ def _launch(fn, index, *args):
         _check(status)
 
 
-def _paged_cache(k_pages, v_pages, layers: bool) -> PagedCache:
+_CACHE = struct.Struct("=QQ6i4q")                            # the fields of PagedCache in order
+assert _CACHE.size == ctypes.sizeof(PagedCache)
+
+
+def _paged_cache(k_pages, v_pages, layers: bool):
     """The pools [P, page_size, Hkv, D] ([L, P, page_size, Hkv, D] with `layers`) as the C
-    struct.  Any strides in multiples of 16 bytes with D dense (head-major pages are a
-    transposed view), the same for both."""
-    shape, st = k_pages.shape, k_pages.stride()
+    struct (bytes), their dtype, pages, heads and head_dim.  Any strides in multiples of 16
+    bytes with D dense (head-major pages are a transposed view), the same for both."""
+    shape, st, dt = k_pages.shape, k_pages.stride(), k_pages.dtype
     nd = len(shape)
     if nd not in ((4, 5) if layers else (4,)) or v_pages.shape != shape:
         raise ValueError(f"k_pages and v_pages must be [{'L, ' if layers else ''}P, page_size, Hkv, D]; got "
                          f"{tuple(shape)}, {tuple(v_pages.shape)}")
-    dt = k_pages.dtype
     if not k_pages.is_cuda or v_pages.device != k_pages.device:
         raise ValueError("k_pages and v_pages must be CUDA tensors on one device")
     if (dt is not torch.bfloat16 and dt is not torch.float32) or v_pages.dtype is not dt:
@@ -412,8 +416,8 @@ def _paged_cache(k_pages, v_pages, layers: bool) -> PagedCache:
         raise ValueError("k_pages and v_pages must have the same strides, D dense")
     L, ls = (shape[0], st[0]) if nd == 5 else (1, 0)
     P, ps, H, D = shape[-4:]
-    return PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), 2 if dt is torch.bfloat16 else 4, L, P, ps, H, D, ls, st[-4],
-                      st[-3], st[-2])
+    return _CACHE.pack(k_pages.data_ptr(), v_pages.data_ptr(), 2 if dt is torch.bfloat16 else 4, L, P, ps, H, D, ls,
+                       st[-4], st[-3], st[-2]), dt, P, H, D
 
 
 def _ws(t, device):
@@ -442,11 +446,10 @@ def _paged_batch(page_table, seq_lens, cu_new, N, device):
             0 if cu_new is None else _ints(cu_new, (B + 1,), device, "cu_new"))
 
 
-def _rows(t, name, N, heads, c, like, device):
+def _rows(t, name, N, heads, D, dtype, device):
     """Row stride of a [N, heads, D] tensor whose rows are dense."""
-    D = c.D
-    if t.shape != (N, heads, D) or t.dtype is not like.dtype or t.device != device:
-        raise ValueError(f"{name} must be a {[N, heads, D]} {like.dtype} tensor on the pages' device; got "
+    if t.shape != (N, heads, D) or t.dtype is not dtype or t.device != device:
+        raise ValueError(f"{name} must be a {[N, heads, D]} {dtype} tensor on the pages' device; got "
                          f"{tuple(t.shape)} {t.dtype}")
     s0, s1, s2 = t.stride()
     if s2 != 1 or (heads > 1 and s1 != D):
@@ -462,23 +465,23 @@ def paged_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_new=None, rope
     not).  With q [N, Hq, D] the query rows are rotated into q_out (which may be q), returned.
     Row slices of one fused projection are taken as they are."""
     lib = _lib or load()
-    c = _paged_cache(k_pages, v_pages, False)
+    c, dt, P, Hkv, D = _paged_cache(k_pages, v_pages, False)
     dev = k_pages.device
     N = k.shape[0]
     B, W, pt, ln, cu = _paged_batch(page_table, seq_lens, cu_new, N, dev)
-    k_ld, v_ld = _rows(k, "k", N, c.Hkv, c, k_pages, dev), _rows(v, "v", N, c.Hkv, c, k_pages, dev)
+    k_ld, v_ld = _rows(k, "k", N, Hkv, D, dt, dev), _rows(v, "v", N, Hkv, D, dt, dev)
     Hq = q_ld = qo_ld = qp = qop = 0
     if q is not None:
         Hq = q.shape[1]
-        q_ld = _rows(q, "q", N, Hq, c, k_pages, dev)
+        q_ld = _rows(q, "q", N, Hq, D, dt, dev)
         if q_out is None:
-            q_out = torch.zeros((N, Hq, c.D), dtype=q.dtype, device=dev)
-        qo_ld = _rows(q_out, "q_out", N, Hq, c, k_pages, dev)
+            q_out = torch.zeros((N, Hq, D), dtype=dt, device=dev)
+        qo_ld = _rows(q_out, "q_out", N, Hq, D, dt, dev)
         qp, qop = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out needs q")
-    _launch(lib.ne_paged_append if c.elem_bytes == 2 else lib.ne_paged_append_f32, dev.index, qp, k.data_ptr(), v.data_ptr(),
-            ctypes.byref(c), pt, ln, cu, ctypes.byref(rope) if rope is not None else None, pos_offset, qop, q_ld, k_ld, v_ld,
+    _launch(lib.ne_paged_append if dt is torch.bfloat16 else lib.ne_paged_append_f32, dev.index, qp, k.data_ptr(), v.data_ptr(),
+            c, pt, ln, cu, ctypes.byref(rope) if rope is not None else None, pos_offset, qop, q_ld, k_ld, v_ld,
             qo_ld, B, N, Hq, W)
     return q_out
 
@@ -500,22 +503,22 @@ def paged_attn(q, k_pages, v_pages, page_table, seq_lens, cu_new=None, max_new: 
     outside the sequences are not written (zeros in a fresh o and lse).  max_new: the most
     new tokens of a sequence, if known (a choice of kernel, not of results)."""
     lib = _lib or load()
-    c = _paged_cache(k_pages, v_pages, False)
+    c, dt, P, Hkv, D = _paged_cache(k_pages, v_pages, False)
     dev = k_pages.device
     N, Hq = q.shape[:2]
     B, W, pt, ln, cu = _paged_batch(page_table, seq_lens, cu_new, N, dev)
-    q_ld = _rows(q, "q", N, Hq, c, k_pages, dev)
+    q_ld = _rows(q, "q", N, Hq, D, dt, dev)
     if o is None:
-        o = torch.zeros((N, Hq, c.D), dtype=q.dtype, device=dev)
-    elif o.shape != q.shape or o.dtype is not q.dtype or o.device != dev or not o.is_contiguous():
+        o = torch.zeros((N, Hq, D), dtype=dt, device=dev)
+    elif o.shape != q.shape or o.dtype is not dt or o.device != dev or not o.is_contiguous():
         raise ValueError("o must be contiguous and match q")
     if lse is None:
         lse = torch.zeros((N, Hq), dtype=torch.float32, device=dev)
     elif lse.shape != (N, Hq) or lse.dtype is not torch.float32 or lse.device != dev or not lse.is_contiguous():
         raise ValueError("lse must be contiguous fp32 [N, Hq]")
     if workspace is None:
-        workspace = alloc_paged_workspace(B, N, Hq, c.Hkv, c.D, dev)
-    _launch(lib.ne_paged_attn if c.elem_bytes == 2 else lib.ne_paged_attn_f32, dev.index, q.data_ptr(), ctypes.byref(c), pt,
+        workspace = alloc_paged_workspace(B, N, Hq, Hkv, D, dev)
+    _launch(lib.ne_paged_attn if dt is torch.bfloat16 else lib.ne_paged_attn_f32, dev.index, q.data_ptr(), c, pt,
             ln, cu, o.data_ptr(), lse.data_ptr(), q_ld, B, N, Hq, W, max(1, N) if max_new is None else max_new,
             *_ws(workspace, dev))
     return o, lse
@@ -527,8 +530,12 @@ def alloc_pages_workspace(n_pages: int, n: int, max_pages: int, device="cuda"):
                        device=device)
 
 
-def _new_ints(shape, device):
-    return torch.empty(shape, dtype=torch.int32, device=device)
+def _out_ints(t, shape, device, name):
+    """An int32 output and its address: the caller's, or a new one."""
+    if t is None:
+        t = torch.empty(shape, dtype=torch.int32, device=device)
+        return t, t.data_ptr()
+    return t, _ints(t, shape, device, name)
 
 
 def pages_fork(refcount, page_table, seq_lens, parents, k_pages, v_pages, deep: bool = False, refcount_out=None,
@@ -539,23 +546,21 @@ def pages_fork(refcount, page_table, seq_lens, parents, k_pages, v_pages, deep: 
     [C, max_pages], child_lens [C], short [1]); short > 0: that many pages were missing and
     nothing changed.  refcount_out may be refcount."""
     lib = _lib or load()
-    c = _paged_cache(k_pages, v_pages, True)
+    c, dt, n_pages, _, _ = _paged_cache(k_pages, v_pages, True)
     dev = k_pages.device
-    P = (c.n_pages,)
+    P = (n_pages,)
     if page_table.dim() != 2 or parents.dim() != 1:
         raise ValueError("page_table must be [B, max_pages] and parents [C]")
     B, W = page_table.shape
     C = parents.shape[0]
-    refcount_out = _new_ints(P, dev) if refcount_out is None else refcount_out
-    child_table = _new_ints((C, W), dev) if child_table is None else child_table
-    child_lens = _new_ints((C,), dev) if child_lens is None else child_lens
-    short = _new_ints((1,), dev) if short is None else short
-    workspace = alloc_pages_workspace(c.n_pages, C, W, dev) if workspace is None else workspace
-    _launch(lib.ne_pages_fork, dev.index, ctypes.byref(c), _ints(refcount, P, dev, "refcount"),
+    refcount_out, ro = _out_ints(refcount_out, P, dev, "refcount_out")
+    child_table, ct = _out_ints(child_table, (C, W), dev, "child_table")
+    child_lens, cl = _out_ints(child_lens, (C,), dev, "child_lens")
+    short, sh = _out_ints(short, (1,), dev, "short")
+    workspace = alloc_pages_workspace(n_pages, C, W, dev) if workspace is None else workspace
+    _launch(lib.ne_pages_fork, dev.index, c, _ints(refcount, P, dev, "refcount"),
             _ints(page_table, (B, W), dev, "page_table"), _ints(seq_lens, (B,), dev, "seq_lens"),
-            _ints(parents, (C,), dev, "parents"), 1 if deep else 0, _ints(refcount_out, P, dev, "refcount_out"),
-            _ints(child_table, (C, W), dev, "child_table"), _ints(child_lens, (C,), dev, "child_lens"),
-            _ints(short, (1,), dev, "short"), B, C, W, *_ws(workspace, dev))
+            _ints(parents, (C,), dev, "parents"), 1 if deep else 0, ro, ct, cl, sh, B, C, W, *_ws(workspace, dev))
     return refcount_out, child_table, child_lens, short
 
 
@@ -566,20 +571,19 @@ def pages_resize(refcount, page_table, seq_lens, new_lens, k_pages, v_pages, ref
     taken, lowest free ids first.  Returns (refcount_out, table_out, short [1]); short > 0:
     that many pages were missing and nothing changed.  Both outputs may be the inputs."""
     lib = _lib or load()
-    c = _paged_cache(k_pages, v_pages, True)
+    c, dt, n_pages, _, _ = _paged_cache(k_pages, v_pages, True)
     dev = k_pages.device
-    P, T = (c.n_pages,), page_table.shape
+    P, T = (n_pages,), page_table.shape
     if len(T) != 2:
         raise ValueError("page_table must be [B, max_pages]")
     B, W = T
-    refcount_out = _new_ints(P, dev) if refcount_out is None else refcount_out
-    table_out = _new_ints(T, dev) if table_out is None else table_out
-    short = _new_ints((1,), dev) if short is None else short
-    workspace = alloc_pages_workspace(c.n_pages, B, W, dev) if workspace is None else workspace
-    _launch(lib.ne_pages_resize, dev.index, ctypes.byref(c), _ints(refcount, P, dev, "refcount"),
+    refcount_out, ro = _out_ints(refcount_out, P, dev, "refcount_out")
+    table_out, to = _out_ints(table_out, T, dev, "table_out")
+    short, sh = _out_ints(short, (1,), dev, "short")
+    workspace = alloc_pages_workspace(n_pages, B, W, dev) if workspace is None else workspace
+    _launch(lib.ne_pages_resize, dev.index, c, _ints(refcount, P, dev, "refcount"),
             _ints(page_table, T, dev, "page_table"), _ints(seq_lens, (B,), dev, "seq_lens"),
-            _ints(new_lens, (B,), dev, "new_lens"), _ints(refcount_out, P, dev, "refcount_out"),
-            _ints(table_out, T, dev, "table_out"), _ints(short, (1,), dev, "short"), B, W,
+            _ints(new_lens, (B,), dev, "new_lens"), ro, to, sh, B, W,
             *_ws(workspace, dev))
     return refcount_out, table_out, short
 
@@ -590,20 +594,19 @@ def pages_compact(refcount, page_table, k_pages, v_pages, refcount_out=None, tab
     table_out, remap [P]: new id of every live page, -1 for free ones, n_live [1]).  Both
     outputs may be the inputs; further tables go through remap."""
     lib = _lib or load()
-    c = _paged_cache(k_pages, v_pages, True)
+    c, dt, n_pages, _, _ = _paged_cache(k_pages, v_pages, True)
     dev = k_pages.device
-    P, T = (c.n_pages,), page_table.shape
+    P, T = (n_pages,), page_table.shape
     if len(T) != 2:
         raise ValueError("page_table must be [B, max_pages]")
     B, W = T
-    refcount_out = _new_ints(P, dev) if refcount_out is None else refcount_out
-    table_out = _new_ints(T, dev) if table_out is None else table_out
-    remap = _new_ints(P, dev) if remap is None else remap
-    n_live = _new_ints((1,), dev) if n_live is None else n_live
-    workspace = alloc_pages_workspace(c.n_pages, B, W, dev) if workspace is None else workspace
-    _launch(lib.ne_pages_compact, dev.index, ctypes.byref(c), _ints(refcount, P, dev, "refcount"),
-            _ints(page_table, T, dev, "page_table"), _ints(refcount_out, P, dev, "refcount_out"),
-            _ints(table_out, T, dev, "table_out"), _ints(remap, P, dev, "remap"), _ints(n_live, (1,), dev, "n_live"), B, W,
+    refcount_out, ro = _out_ints(refcount_out, P, dev, "refcount_out")
+    table_out, to = _out_ints(table_out, T, dev, "table_out")
+    remap, rm = _out_ints(remap, P, dev, "remap")
+    n_live, nl = _out_ints(n_live, (1,), dev, "n_live")
+    workspace = alloc_pages_workspace(n_pages, B, W, dev) if workspace is None else workspace
+    _launch(lib.ne_pages_compact, dev.index, c, _ints(refcount, P, dev, "refcount"),
+            _ints(page_table, T, dev, "page_table"), ro, to, rm, nl, B, W,
             *_ws(workspace, dev))
     return refcount_out, table_out, remap, n_live
 

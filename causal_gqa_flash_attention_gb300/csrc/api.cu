@@ -2,6 +2,7 @@
 // codes, per-device caches (RoPE tables, device error word), TMA tensor-map encoding
 // and kernel launches.  No compute happens here; every step runs in the kernels.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -77,14 +78,19 @@ unsigned long long timeout_ns() {
 }
 
 ne_status current_device(int* dev) {
+    // Devices found to be sm_103 ones, a bit each (the first 64): the answer cannot change.
+    static std::atomic<uint64_t> known{0};
     cudaError_t e = cudaGetDevice(dev);
     if (e != cudaSuccess) return fail(NE_ERR_NO_DEVICE, "no CUDA device: %s", cudaGetErrorString(e));
+    const uint64_t bit = *dev >= 0 && *dev < 64 ? (uint64_t)1 << *dev : 0;
+    if (known.load(std::memory_order_relaxed) & bit) return NE_OK;
     int major = 0, minor = 0;
     cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, *dev);
     cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, *dev);
     if (major != 10 || minor != 3)
         return fail(NE_ERR_NO_DEVICE, "device %d is sm_%d%d; libneattn is built for sm_103a only", *dev, major,
                     minor);
+    known.fetch_or(bit, std::memory_order_relaxed);
     return NE_OK;
 }
 

@@ -201,7 +201,7 @@ size_t attn_ws_bytes(int D, int Hkv, int G) {
         for (int rows : {1, 8, 9, 16, 17, 32, 33, 1 << 20}) {
             if (f32 && D > 64) continue;
             const ne::PagedKind kind = ne::paged_kind(f32 != 0, D, G, rows);
-            most = std::max(most, ne::paged_part_bytes(ne::paged_split(kind, D, Hkv, G), D));
+            most = std::max(most, ne::paged_part_bytes(ne::paged_split(kind, D, Hkv, G, 1 << 30), D));
         }
     return round_up(most, 256);
 }
@@ -231,7 +231,7 @@ ne_status attn_impl(int eb, const void* q, const ne_paged_cache* c, const int* t
     const ne::PagedKind kind = ne::paged_kind(f32, c->D, G, cu ? std::min(max_new, N) : 1);
     a.c = view_of(c);
     a.s = batch_of(c, table, lens, cu, B, N, W);
-    a.p = ne::paged_split(kind, c->D, c->Hkv, G);
+    a.p = ne::paged_split(kind, c->D, c->Hkv, G, a.s.cap);
     a.q = q;
     a.o = o;
     a.lse = lse;
@@ -254,6 +254,7 @@ ne_status attn_impl(int eb, const void* q, const ne_paged_cache* c, const int* t
     } else if (f32) e = ne::launch_paged_f32(kind, c->D, a, st);
     else e = ne::launch_paged_short(kind, c->D, a, st);
     if (e != cudaSuccess) return cuda_fail(e, "paged_attn launch");
+    if (a.p.nocut) return NE_OK;
     e = ne::launch_paged_join(f32, c->D, a, st);
     if (e != cudaSuccess) return cuda_fail(e, "paged_attn join launch");
     return NE_OK;

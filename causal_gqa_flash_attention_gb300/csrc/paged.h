@@ -1,5 +1,6 @@
 // paged.h -- internal interface between api_paged.cu and the paged-cache kernels.
 #pragma once
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -38,7 +39,6 @@ struct AppendArgs {
     float mscale;
     int tpc;                          // tokens per CTA
     int vec_shift;                    // log2 of the 16-byte units of a head
-    FastDiv div_per;                  // by the units of a token
     int* err;
 };
 struct RopeTurns {
@@ -55,6 +55,7 @@ struct PagedSplit {
     FastDiv div_tpt;                  // by tpt
     int ovh;                          // fixed cost of a unit, in keys
     int min_shift;                    // log2 of a CTA's least work, in keys
+    int nocut;                        // units are not cut (short contexts): no join
     int rows;                         // rows of a unit (partials are stored at this pitch)
     int sub;                          // tokens of a unit's first 128-row subtile (0: rows are contiguous)
 };
@@ -76,10 +77,24 @@ struct PagedAttnArgs {
     unsigned long long timeout_ns;
 };
 
+// Dynamic shared memory of a kernel, set once per device (the first 64).
+template <typename F>
+cudaError_t allow_smem(F kfn, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev >= 0 && dev < 64 ? (uint64_t)1 << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
 // Which kernel a call runs, and its split.
 enum PagedKind : int { PAGED_SHORT16 = 0, PAGED_SHORT32, PAGED_F32_FEW, PAGED_F32_MANY, PAGED_TILES };
 PagedKind paged_kind(bool f32, int D, int G, int max_new);
-PagedSplit paged_split(PagedKind kind, int D, int Hkv, int G);
+// cap: the longest length the page tables can hold.
+PagedSplit paged_split(PagedKind kind, int D, int Hkv, int G, int cap);
 // Bytes of a call's workspace: the largest over the kernels its type and shape may run.
 size_t paged_part_bytes(const PagedSplit& p, int D);
 

@@ -73,65 +73,71 @@ __device__ __forceinline__ int find_seq(const int* cu, int B, int t, int lane) {
     return lo < B ? lo : -1;
 }
 
-// 16-byte unit `u` at element e0 of a row, rotated; `pair` holds the other elements of its
-// pairs (half layout with whole units per half; elsewhere they come from the row itself).
-template <typename T>
-__device__ __forceinline__ uint4 rotated(const uint4& u, const uint4& pair, const T* row, int e0, const float2* cs, int rot,
-                                         int layout) {
-    constexpr int N = Vec<T>::N;
-    if (e0 >= rot) return u;
-    float x[N], y[N];
-    Vec<T>::get(u, x);
-    if (layout == 0) {
+// What a lane needs to rotate its unit (elements e0 .. e0 + N-1) of every head of a token:
+// the (cos, sin) of its pairs, fetched once.  HALF: pairs (i, i + rot/2), one per element;
+// else pairs (2i, 2i+1), one per two elements.
+template <typename T, bool HALF>
+struct Turn {
+    static constexpr int N = Vec<T>::N;
+    static constexpr int P = HALF ? N : N / 2;
+    float2 cs[P];
+    __device__ __forceinline__ void load(const float2* s, int e0, int rot) {
+        const int half = rot >> 1;
 #pragma unroll
-        for (int i = 0; i < N; i += 2) {
-            if (e0 + i < rot) {
-                const float2 c = cs[(e0 + i) >> 1];
-                y[i] = x[i] * c.x - x[i + 1] * c.y;
-                y[i + 1] = x[i] * c.y + x[i + 1] * c.x;
+        for (int i = 0; i < P; ++i) {
+            const int e = HALF ? e0 + i : e0 + 2 * i;
+            const int p = HALF ? (e < half ? e : e - half) : e >> 1;
+            cs[i] = e < rot ? s[p] : make_float2(1.f, 0.f);
+        }
+    }
+    // `pair`: the unit that holds the other elements of the pairs (whole units per half);
+    // otherwise they are read from the row.
+    __device__ __forceinline__ uint4 apply(const uint4& u, const uint4& pair, const T* row, int e0, int rot) const {
+        float x[N], y[N];
+        Vec<T>::get(u, x);
+        if constexpr (!HALF) {
+#pragma unroll
+            for (int i = 0; i < N; i += 2) {
+                const float2 c = cs[i >> 1];
+                const bool in = e0 + i < rot;              // (the rest passes, infinities too)
+                y[i] = in ? x[i] * c.x - x[i + 1] * c.y : x[i];
+                y[i + 1] = in ? x[i] * c.y + x[i + 1] * c.x : x[i + 1];
+            }
+        } else {
+            const int half = rot >> 1;
+            if (half % N == 0) {
+                float z[N];
+                Vec<T>::get(pair, z);
+                const float sign = e0 < half ? -1.f : 1.f;
+#pragma unroll
+                for (int i = 0; i < N; ++i) y[i] = x[i] * cs[i].x + (sign * z[i]) * cs[i].y;
             } else {
-                y[i] = x[i];
-                y[i + 1] = x[i + 1];
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const int e = e0 + i;
+                    if (e >= rot) {
+                        y[i] = x[i];
+                    } else {
+                        const float o = Vec<T>::one(row + (e < half ? e + half : e - half));
+                        y[i] = x[i] * cs[i].x + (e < half ? -o : o) * cs[i].y;
+                    }
+                }
             }
         }
         return Vec<T>::put(y);
     }
-    const int half = rot >> 1;
-    float z[N];
-    if (half % N == 0) {
-        Vec<T>::get(pair, z);
-        const bool first = e0 < half;
-        const float4* c4 = reinterpret_cast<const float4*>(cs + (first ? e0 : e0 - half));
-        const float sign = first ? -1.f : 1.f;
-#pragma unroll
-        for (int i = 0; i < N; i += 2) {
-            const float4 c = c4[i >> 1];                   // (cos, sin) of two pairs
-            y[i] = x[i] * c.x + sign * (z[i] * c.y);
-            y[i + 1] = x[i + 1] * c.z + sign * (z[i + 1] * c.w);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int e = e0 + i;
-            if (e >= rot) {
-                y[i] = x[i];
-            } else {
-                const bool first = e < half;
-                const float o = Vec<T>::one(row + (first ? e + half : e - half));
-                const float2 c = cs[first ? e : e - half];
-                y[i] = first ? x[i] * c.x - o * c.y : x[i] * c.x + o * c.y;
-            }
-        }
-    }
-    return Vec<T>::put(y);
-}
+};
 
-// Units in flight per thread.  Their loads need no position, so the first ones go out before
+// Heads in flight per lane.  Their loads need no position, so the first ones go out before
 // the CTA has looked its tokens up.
-constexpr int kUnits = 4;
+constexpr int kBatch = 4;
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendArgs a, const __grid_constant__ RopeTurns turns) {
+// A lane keeps one 16-byte unit of a head and walks over the heads of one token: 32 / vecs heads
+// to a warp, kThreads / 32 / tpc warps to a token.  (Units dealt out flat cost 250 instructions
+// each for indices and angles, and bound the kernel by its instructions.)  A warp holds whole
+// heads and reads a batch of them before it writes any, so q_out may be q itself.
+template <typename T, bool HALF>
+__global__ void __launch_bounds__(kThreads, 3) paged_append_kernel(const AppendArgs a, const __grid_constant__ RopeTurns turns) {
     constexpr int N = Vec<T>::N;
     __shared__ __align__(16) float2 s_cs[kTok][64];
     __shared__ int s_pos[kTok];                            // position, -1: not stored, -2: not a row of the call
@@ -140,52 +146,36 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendArgs
     griddep_launch_dependents();
     griddep_wait();
     const int t0 = blockIdx.x * a.tpc, nt = min(a.tpc, a.s.N - t0);
-
-    // Unit i of the CTA: token i / per, head, 16-byte unit of the head.  A head's units are
-    // neighbours within one warp (at most 32 of them), and a warp reads a batch of units
-    // before it writes any of them, so q_out may be q itself.
-    const int vshift = a.vec_shift, qh = a.q ? a.Hq : 0;
-    const int per = (qh + 2 * a.Hkv) << vshift, total = nt * per;
-    struct Unit {
-        int t, h, e0;
-        const T* row;
-    };
-    auto unit = [&](int i) {
-        Unit x;
-        x.t = (int)fast_div((uint32_t)i, a.div_per);
-        const int r = i - x.t * per;
-        x.h = r >> vshift;
-        x.e0 = (r & ((1 << vshift) - 1)) * N;
-        const long long row = t0 + x.t;
-        x.row = x.h < qh ? static_cast<const T*>(a.q) + row * a.q_ld + (long long)x.h * a.D
-                : x.h < qh + a.Hkv ? static_cast<const T*>(a.k_in) + row * a.k_ld + (long long)(x.h - qh) * a.D
-                                   : static_cast<const T*>(a.v_in) + row * a.v_ld + (long long)(x.h - qh - a.Hkv) * a.D;
-        return x;
-    };
-    uint4 raw[kUnits];
-    auto fetch = [&](int base) {
+    const int wpt = (kThreads / 32) / a.tpc;               // warps of a token
+    const int t = warp / wpt;
+    const long long row = t0 + t;
+    const int e0 = (lane & ((1 << a.vec_shift) - 1)) * N;  // this lane's unit
+    const int hpw = 32 >> a.vec_shift;                     // heads of a warp's pass
+    const int qh = a.q ? a.Hq : 0, heads = t < nt ? qh + 2 * a.Hkv : 0;
+    const int step = wpt * hpw;
+    const int h0 = (warp - t * wpt) * hpw + (lane >> a.vec_shift);
+    const T* qrow = static_cast<const T*>(a.q) + row * a.q_ld + e0;
+    const T* krow = static_cast<const T*>(a.k_in) + row * a.k_ld + e0;
+    const T* vrow = static_cast<const T*>(a.v_in) + row * a.v_ld + e0;
+    auto source = [&](int h) { return h < qh ? qrow + h * a.D : h < qh + a.Hkv ? krow + (h - qh) * a.D : vrow + (h - qh - a.Hkv) * a.D; };
+    uint4 raw[kBatch];
+    auto fetch = [&](int h) {
 #pragma unroll
-        for (int k = 0; k < kUnits; ++k) {
-            const int i = base + k * kThreads + lane;
-            raw[k] = make_uint4(0u, 0u, 0u, 0u);
-            if (i < total) {
-                const Unit x = unit(i);
-                raw[k] = *reinterpret_cast<const uint4*>(x.row + x.e0);
-            }
-        }
+        for (int k = 0; k < kBatch; ++k, h += step)
+            raw[k] = h < heads ? *reinterpret_cast<const uint4*>(source(h)) : make_uint4(0u, 0u, 0u, 0u);
     };
-    fetch(warp * 32);
+    fetch(h0);
 
-    if (warp < nt) {
-        const int t = t0 + warp;
-        const int b = a.s.cu ? find_seq(a.s.cu, a.s.B, t, lane) : t;
+    if (t < nt && warp == t * wpt) {
+        const int r = t0 + t;
+        const int b = a.s.cu ? find_seq(a.s.cu, a.s.B, r, lane) : r;
         int pos = -2;
         long long slot = -1;
         if (b >= 0) {
             int bad = 0;
             const PagedSeq q = paged_seq(a.s, b, bad);
-            if (t >= q.tok0 && t < q.tok0 + q.n) {
-                pos = q.len - q.n + (t - q.tok0);
+            if (r >= q.tok0 && r < q.tok0 + q.n) {
+                pos = q.len - q.n + (r - q.tok0);
                 if (pos < 0) {
                     pos = -1;
                 } else {
@@ -200,8 +190,8 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendArgs
             if (bad && lane == 0) report_error(a.err, bad);
         }
         if (lane == 0) {
-            s_pos[warp] = pos;
-            s_slot[warp] = slot;
+            s_pos[t] = pos;
+            s_slot[t] = slot;
         }
         if (pos >= 0)
             for (int p = lane; p < a.rot >> 1; p += 32) {
@@ -209,7 +199,7 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendArgs
                 const long long f = (long long)((unsigned long long)(pos + a.pos_offset) * turns.t[p]);
                 float s, c;
                 sincospif((float)f * 1.0842021724855044e-19f, &s, &c);   // 2^-63: half turns
-                s_cs[warp][p] = make_float2(c * a.mscale, s * a.mscale);
+                s_cs[t][p] = make_float2(c * a.mscale, s * a.mscale);
             }
     }
     // Sequences without rows are looked at too, or a bad entry of theirs would go unnoticed.
@@ -219,44 +209,46 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendArgs
         if (bad) report_error(a.err, bad);
     }
     __syncthreads();
+    if (t >= nt) return;
 
-    const int pair_lanes = (a.rot >> 1) / N;               // half layout: lanes between the units of a pair
-    for (int base = warp * 32; base < total; base += kUnits * kThreads) {
-        uint4 val[kUnits];
-        T* dst[kUnits];
+    const int pos = s_pos[t];
+    const long long slot = s_slot[t];
+    const bool turned = e0 < a.rot && pos >= 0;
+    Turn<T, HALF> turn;
+    if (turned) turn.load(s_cs[t], e0, a.rot);
+    // HALF: the lane that holds the other elements of this one's pairs.
+    const int other = HALF ? lane + (e0 < a.rot >> 1 ? (a.rot >> 1) / N : -((a.rot >> 1) / N)) : 0;
+    T* qdst = pos != -2 && a.q ? static_cast<T*>(a.q_out) + row * a.qo_ld + e0 : nullptr;
+    T* kdst = slot >= 0 ? static_cast<T*>(const_cast<void*>(a.c.k)) + slot + e0 : nullptr;
+    T* vdst = slot >= 0 ? static_cast<T*>(const_cast<void*>(a.c.v)) + slot + e0 : nullptr;
+    // (The loop runs on the warp's first head, so that every lane takes the same passes.)
+    for (int hw = h0 - (lane >> a.vec_shift); hw < heads; hw += kBatch * step) {
+        const int h = hw + (lane >> a.vec_shift);
 #pragma unroll
-        for (int k = 0; k < kUnits; ++k) {
-            const int i = base + k * kThreads + lane;
-            const Unit x = unit(min(i, total - 1));
+        for (int k = 0; k < kBatch; ++k) {
             uint4 pair = raw[k];
-            if (a.layout == 1) {
-                const int from = (lane + (x.e0 < a.rot >> 1 ? pair_lanes : -pair_lanes)) & 31;
-                pair.x = __shfl_sync(0xffffffffu, raw[k].x, from);
-                pair.y = __shfl_sync(0xffffffffu, raw[k].y, from);
-                pair.z = __shfl_sync(0xffffffffu, raw[k].z, from);
-                pair.w = __shfl_sync(0xffffffffu, raw[k].w, from);
+            if (HALF) {
+                pair.x = __shfl_sync(0xffffffffu, raw[k].x, other & 31);
+                pair.y = __shfl_sync(0xffffffffu, raw[k].y, other & 31);
+                pair.z = __shfl_sync(0xffffffffu, raw[k].z, other & 31);
+                pair.w = __shfl_sync(0xffffffffu, raw[k].w, other & 31);
             }
-            dst[k] = nullptr;
-            val[k] = raw[k];
-            const int pos = s_pos[x.t];
-            const long long slot = s_slot[x.t];
-            if (i < total) {
-                if (x.h < qh) {
-                    if (pos != -2) dst[k] = static_cast<T*>(a.q_out) + (long long)(t0 + x.t) * a.qo_ld + (long long)x.h * a.D + x.e0;
-                } else if (slot >= 0) {
-                    const bool key = x.h - qh < a.Hkv;
-                    dst[k] = static_cast<T*>(const_cast<void*>(key ? a.c.k : a.c.v)) + slot +
-                             (long long)(key ? x.h - qh : x.h - qh - a.Hkv) * a.c.head_stride + x.e0;
-                }
-                if (pos < 0) val[k] = make_uint4(0u, 0u, 0u, 0u);
-                else if (x.h < qh + a.Hkv) val[k] = rotated<T>(raw[k], pair, x.row, x.e0, s_cs[x.t], a.rot, a.layout);
-            }
+            const int hk = h + k * step;
+            if (hk < qh + a.Hkv && hk < heads && turned)
+                raw[k] = turn.apply(raw[k], pair, source(hk) - e0, e0, a.rot);
         }
         __syncwarp();                                      // every read of this batch is done
 #pragma unroll
-        for (int k = 0; k < kUnits; ++k)
-            if (dst[k]) *reinterpret_cast<uint4*>(dst[k]) = val[k];
-        fetch(base + kUnits * kThreads);
+        for (int k = 0; k < kBatch; ++k) {
+            const int hk = h + k * step;
+            if (hk >= heads) continue;
+            T* dst;
+            if (hk < qh) dst = qdst ? qdst + hk * a.D : nullptr;
+            else if (hk < qh + a.Hkv) dst = kdst ? kdst + (hk - qh) * a.c.head_stride : nullptr;
+            else dst = vdst ? vdst + (hk - qh - a.Hkv) * a.c.head_stride : nullptr;
+            if (dst) *reinterpret_cast<uint4*>(dst) = pos < 0 ? make_uint4(0u, 0u, 0u, 0u) : raw[k];
+        }
+        fetch(h + kBatch * step);
     }
 }
 
@@ -264,14 +256,17 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendArgs
 
 cudaError_t launch_paged_append(bool f32, const AppendArgs& a0, const RopeTurns& t, cudaStream_t st) {
     AppendArgs a = a0;
-    // A CTA per token while there are no more than four per SM, then up to eight tokens each.
-    a.tpc = a.s.N <= 4 * 152 ? 1 : (a.s.N <= 16 * 152 ? 4 : kTok);
+    // A CTA per token while there are no more than four per SM; then a warp or two per token:
+    // the lookups of a CTA's tokens take as long as two batches of heads, whatever their number.
+    a.tpc = a.s.N <= 4 * 152 ? 1 : a.s.N <= 16 * 152 ? 4 : kTok;
     const int vecs = a.D / (f32 ? 4 : 8);
     while ((1 << a.vec_shift) < vecs) ++a.vec_shift;
-    a.div_per = make_fastdiv((uint32_t)(((a.q ? a.Hq : 0) + 2 * a.Hkv) * vecs));
-    const dim3 grid((a.s.N + a.tpc - 1) / a.tpc);
-    return f32 ? launch_k(paged_append_kernel<float>, grid, dim3(kThreads), 0, st, a, t)
-               : launch_k(paged_append_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, st, a, t);
+    const dim3 grid((a.s.N + a.tpc - 1) / a.tpc), block(kThreads);
+    if (a.layout == 1)
+        return f32 ? launch_k(paged_append_kernel<float, true>, grid, block, 0, st, a, t)
+                   : launch_k(paged_append_kernel<__nv_bfloat16, true>, grid, block, 0, st, a, t);
+    return f32 ? launch_k(paged_append_kernel<float, false>, grid, block, 0, st, a, t)
+               : launch_k(paged_append_kernel<__nv_bfloat16, false>, grid, block, 0, st, a, t);
 }
 
 }  // namespace ne

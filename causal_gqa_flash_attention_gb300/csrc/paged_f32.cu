@@ -232,7 +232,8 @@ cudaError_t launch_f32_t(const PagedAttnArgs& a, cudaStream_t st) {
     using C = F32Cfg<D, MANY>;
     auto kfn = paged_f32_kernel<D, MANY>;
     static_assert(C::SMEM + 4096 <= 227 * 1024, "shared memory");
-    cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(kfn, C::SMEM, done);
     if (e != cudaSuccess) return e;
     return launch_k(kfn, dim3(a.p.C), dim3(C::THREADS), C::SMEM, st, a);
 }

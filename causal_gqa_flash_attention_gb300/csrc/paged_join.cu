@@ -153,7 +153,7 @@ PagedKind paged_kind(bool f32, int D, int G, int max_new) {
     return rows <= 32 || D == 32 || G > 128 ? PAGED_SHORT32 : PAGED_TILES;
 }
 
-PagedSplit paged_split(PagedKind kind, int D, int Hkv, int G) {
+PagedSplit paged_split(PagedKind kind, int D, int Hkv, int G, int cap) {
     PagedSplit p = {};
     auto rows = [&](int r) {
         p.rows = r;
@@ -195,6 +195,8 @@ PagedSplit paged_split(PagedKind kind, int D, int Hkv, int G) {
             p.min_shift = 9;
             break;
     }
+    // Contexts of at most 256 positions: a unit's keys take less time than the join would.
+    p.nocut = cap <= 256;
     p.div_tpt = make_fastdiv((uint32_t)p.tpt);
     return p;
 }

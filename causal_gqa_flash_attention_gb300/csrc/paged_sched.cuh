@@ -127,8 +127,14 @@ struct PagedWalk {
             const int kv = r == nt - 1 ? q.len : max(0, base + (r + 1) * a.p.tpt);
             const int cost = a.p.ovh + kv;
             const int ntk = (kv + (1 << a.p.bn_shift) - 1) >> a.p.bn_shift;
-            g.t0 = w0 <= cur ? 0 : (int)paged_div((w0 - cur) * ntk + cost / 2, cost);
-            g.t1 = w1 >= cur + cost ? ntk : (int)paged_div((w1 - cur) * ntk + cost / 2, cost);
+            // The tile nearest to each end of the interval; a whole unit goes to whoever holds its
+            // middle.
+            auto cut = [&](long long x) -> int {
+                if (a.p.nocut) return 2 * x >= cost ? ntk : 0;
+                return (int)paged_div(x * ntk + cost / 2, cost);
+            };
+            g.t0 = w0 <= cur ? 0 : cut(w0 - cur);
+            g.t1 = w1 >= cur + cost ? ntk : cut(w1 - cur);
             g.b = b;
             g.hg = hg;
             g.r = r;

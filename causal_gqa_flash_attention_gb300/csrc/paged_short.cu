@@ -335,7 +335,8 @@ cudaError_t launch_short_t(const PagedAttnArgs& a, cudaStream_t st) {
     constexpr int smem = kWarps * C::RING;
     static_assert(smem >= kWarps * 16 * MT * D * 4, "the join fits into the rings");
     static_assert(2 * (smem + 4096) <= 227 * 1024, "two CTAs per SM");
-    cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(kfn, smem, done);
     if (e != cudaSuccess) return e;
     return launch_k(kfn, dim3(a.p.C), dim3(kThreads), smem, st, a);
 }

@@ -555,7 +555,8 @@ cudaError_t launch_tiles_t(const CUtensorMap& tq, const CUtensorMap& tk, const C
                            cudaStream_t st) {
     using C = TileCfg<D>;
     auto kfn = paged_tiles_kernel<D>;
-    cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(kfn, C::SMEM, done);
     if (e != cudaSuccess) return e;
     return launch_k(kfn, dim3(a.p.C), dim3(C::THREADS), C::SMEM, st, tq, tk, tv, a);
 }
