@@ -53,8 +53,9 @@ struct PagedSplit {
     int gs;                           // query heads of a group
     int bn_shift;                     // log2 of the keys per tile: what a unit may be cut into
     FastDiv div_tpt;                  // by tpt
-    int ovh;                          // fixed cost of a unit, in keys
-    int min_shift;                    // log2 of a CTA's least work, in keys
+    int ovh;                          // fixed cost of a unit
+    int w_full, w_part;               // cost of a key of a unit with more than `sub` tokens, and with fewer
+    int min_shift;                    // log2 of a CTA's least work
     int nocut;                        // units are not cut (short contexts): no join
     int rows;                         // rows of a unit (partials are stored at this pitch)
     int sub;                          // tokens of a unit's first 128-row subtile (0: rows are contiguous)
@@ -72,7 +73,7 @@ struct PagedAttnArgs {
     float scale_log2;                 // log2(e) / sqrt(D)
     float* part_o;                    // [2C, rows, D] unnormalised outputs of cut units
     float2* part_ml;                  // [2C, rows] (running max in log2 units, sum)
-    int4* part_info;                  // [2C] (state, sequence, head group, tile)
+    int4* part_info;                  // [2C] (state: 0 none, 1, 2 the unit's last; first row, tokens, head group)
     int* err;
     unsigned long long timeout_ns;
 };

@@ -45,6 +45,8 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedAttnArg
     griddep_launch_dependents();
     griddep_wait();
     const int4 rec = a.part_info[j * 2 + 1];
+    auto state = [&](int c) { return c < a.p.C ? a.part_info[c * 2].x : 0; };
+    int st = tid < 32 ? state(j + 1 + tid) : 0;            // (beside the record's load)
     if (rec.x == 0) return;
     if (tid < 32) {
         // The parts in order: this slot, then the following CTAs' slots 0 up to the last.
@@ -52,7 +54,7 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedAttnArg
         if (tid == 0) s_part[0] = j * 2 + 1;
         for (int c0 = j + 1; c0 < a.p.C; c0 += 32) {
             const int c = c0 + tid;
-            const int st = c < a.p.C ? a.part_info[c * 2].x : 0;
+            if (c0 > j + 1) st = state(c);
             const unsigned ends = __ballot_sync(0xffffffffu, st == 2);
             const unsigned upto = ends ? (ends & (0u - ends)) * 2u - 1u : 0xffffffffu;   // lanes up to the first end
             const unsigned have = __ballot_sync(0xffffffffu, st != 0) & upto;
@@ -64,17 +66,14 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedAttnArg
     }
     __syncthreads();
     const int np = s_n;
-    int bad = 0;
-    const PagedSeq q = paged_seq(a.s, rec.y, bad);
     const int ngrp = (a.G + a.p.gs - 1) / a.p.gs;
-    const int hkv = rec.z / ngrp, hs = rec.z % ngrp;
+    const int hkv = rec.w / ngrp, hs = rec.w % ngrp;
     const int gs = min(a.p.gs, a.G - hs * a.p.gs);
-    const int tok = rec.w * a.p.tpt;
-    const int live = min(a.p.tpt, q.n - tok) * gs;
+    const int live = rec.z * gs;
     const int grp = tid / LPR, e = (tid % LPR) * 4;
     auto stored = [&](int i) { return a.p.sub == 0 || i < a.p.sub * gs ? i : i - a.p.sub * gs + 128; };
     auto finish = [&](int i, float m, float l, const float4& o) {
-        const long long row = (long long)(q.tok0 + tok + i / gs) * a.Hq + hkv * a.G + hs * a.p.gs + i % gs;
+        const long long row = (long long)(rec.y + i / gs) * a.Hq + hkv * a.G + hs * a.p.gs + i % gs;
         const float inv = l > 0.f ? 1.f / l : 0.f;
         put(static_cast<T*>(a.o) + row * D + e, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
         if (e == 0) a.lse[row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
@@ -162,6 +161,7 @@ PagedSplit paged_split(PagedKind kind, int D, int Hkv, int G, int cap) {
         p.hg = Hkv * ((G + p.gs - 1) / p.gs);
     };
     p.ovh = 128;
+    p.w_full = p.w_part = 1;
     p.min_shift = 7;
     auto tile = [&](int keys) {
         while ((1 << p.bn_shift) < keys) ++p.bn_shift;
@@ -191,8 +191,12 @@ PagedSplit paged_split(PagedKind kind, int D, int Hkv, int G, int cap) {
             p.hg = Hkv;
             tile(128);
             p.C = kSms;
-            p.ovh = 256;
-            p.min_shift = 9;
+            // A key tile takes a unit with both subtiles 1.35 us and one with a single subtile 1.0 us
+            // (D 64), the ends of a unit about two tiles.
+            p.w_full = 5;
+            p.w_part = 4;
+            p.ovh = 1024;
+            p.min_shift = 11;
             break;
     }
     // Contexts of at most 256 positions: a unit's keys take less time than the join would.

@@ -51,12 +51,14 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedBatch& s, int b, int& b
     return q;
 }
 
-// Cost of tiles 0 .. r-1 of a sequence (r below its tile count): each ovh + max(0, base + (k+1) tpt).
+// Cost of tiles 0 .. r-1 of a sequence (r below its tile count, so they are full): each
+// ovh + w_full max(0, base + (k+1) tpt).
 __device__ __forceinline__ long long paged_prefix(int r, int base, const PagedSplit& p) {
     if (r == 0) return 0;
     const int r0 = base < 0 ? min(r, (int)fast_div((uint32_t)-base, p.div_tpt)) : 0;   // tiles without a key
     const long long m = r - r0;
-    return (long long)r * p.ovh + m * base + (long long)p.tpt * (((long long)r * (r + 1) - (long long)r0 * (r0 + 1)) / 2);
+    return (long long)r * p.ovh +
+           p.w_full * (m * base + (long long)p.tpt * (((long long)r * (r + 1) - (long long)r0 * (r0 + 1)) / 2));
 }
 
 // Tiles of a sequence.
@@ -64,10 +66,14 @@ __device__ __forceinline__ int paged_tiles(int n, const PagedSplit& p) {
     return (int)fast_div((uint32_t)(n + p.tpt - 1), p.div_tpt);
 }
 
+// Cost of a key of a unit with ntok tokens.
+__device__ __forceinline__ int paged_weight(int ntok, const PagedSplit& p) { return ntok > p.sub ? p.w_full : p.w_part; }
+
 // Cost of one head group of a sequence.
 __device__ __forceinline__ long long paged_group_cost(const PagedSeq& q, const PagedSplit& p) {
     if (q.n == 0) return 0;
-    return paged_prefix(paged_tiles(q.n, p) - 1, q.len - q.n, p) + p.ovh + q.len;
+    const int last = paged_tiles(q.n, p) - 1;
+    return paged_prefix(last, q.len - q.n, p) + p.ovh + (long long)paged_weight(q.n - last * p.tpt, p) * q.len;
 }
 
 // What a CTA does with one unit: key tiles [t0, t1) of nt_keys, for tokens tok .. tok+ntok-1
@@ -125,7 +131,8 @@ struct PagedWalk {
         while (cur < w1) {
             const int base = q.len - q.n;
             const int kv = r == nt - 1 ? q.len : max(0, base + (r + 1) * a.p.tpt);
-            const int cost = a.p.ovh + kv;
+            const int ntok = min(a.p.tpt, q.n - r * a.p.tpt);
+            const long long cost = a.p.ovh + (long long)paged_weight(ntok, a.p) * kv;
             const int ntk = (kv + (1 << a.p.bn_shift) - 1) >> a.p.bn_shift;
             // The tile nearest to each end of the interval; a whole unit goes to whoever holds its
             // middle.
@@ -139,7 +146,7 @@ struct PagedWalk {
             g.hg = hg;
             g.r = r;
             g.tok = r * a.p.tpt;
-            g.ntok = min(a.p.tpt, q.n - g.tok);
+            g.ntok = ntok;
             g.tok0 = q.tok0;
             g.base = base;
             g.len = q.len;
@@ -301,7 +308,7 @@ __device__ __forceinline__ void paged_locate_warp(const PagedAttnArgs& a, int c,
 
 // The records of both slots of CTA c are written by every call (state 0: no such part).
 __device__ __forceinline__ int4 paged_record(const PagedSeg& g) {
-    return make_int4(g.t1 == g.nt ? 2 : 1, g.b, g.hg, g.r);
+    return make_int4(g.t1 == g.nt ? 2 : 1, g.tok0 + g.tok, g.ntok, g.hg);
 }
 
 }  // namespace ne

@@ -262,16 +262,25 @@ __global__ void __launch_bounds__(384, 1)
             if (g.t0 == g.t1) continue;
             const int n_sub = g.ntok > sub ? 2 : 1, nt = g.t1 - g.t0;
             if (!(ok = mbar_wait_warp(smem_u32(&bar_q_full), seg & 1, w, SITE_PAGED_Q))) break;
-            if (!(ok = full(item) && s_free(0) && (n_sub == 1 || s_free(1)))) break;
+            ok = full(item) && s_free(0);
+            if (!ok) break;
+            if (elect_one()) s_mmas(0, item);
+            __syncwarp();
+            ++s_tiles[0];
+            if (n_sub == 2) {
+                // SEP: the second subtile starts half a tile behind the first, so that one's
+                // exponentials run beside the other's loads and maxima.
+                ok = s_free(1) && s_free(0);
+                if (!ok) break;
+                if (elect_one()) s_mmas(1, item);
+                __syncwarp();
+                ++s_tiles[1];
+            }
             if (elect_one()) {
-                s_mmas(0, item);
-                if (n_sub == 2) s_mmas(1, item);
                 umma_commit(smem_u32(&bar_empty[item % C::NS]));
                 if (nt == 1) umma_commit(smem_u32(&bar_q_empty));
             }
             __syncwarp();
-            ++s_tiles[0];
-            if (n_sub == 2) ++s_tiles[1];
             for (int t = 0; ok && t < nt; ++t) {
                 const int vi = item + 2 * t + 1, kn = item + 2 * t + 2;
                 const bool more = t + 1 < nt, fix = (g.t0 + t + 1) * C::BN > g.len;
@@ -417,10 +426,6 @@ __global__ void __launch_bounds__(384, 1)
                 tc_fence_after();
                 uint32_t s[128];
                 tmem_ld_cols<4>(sc, s);
-                if (C::SEP) {
-                    tc_fence_before();
-                    mbar_arrive(smem_u32(&bar_s_free[u]));
-                }
                 const int kv0 = t * C::BN;
                 if (kv0 + C::BN > first_lim) {
 #pragma unroll
@@ -440,6 +445,10 @@ __global__ void __launch_bounds__(384, 1)
                 // A row whose maximum grew by more than 2^8 rescales its sum and output; the
                 // others keep the old reference (weights up to 2^8 lose nothing).  PV(t - 1) is
                 // complete: waited for (SEP), or S(t) was issued behind it.
+                if (C::SEP) {
+                    tc_fence_before();
+                    mbar_arrive(smem_u32(&bar_s_free[u]));
+                }
                 ok = pv_before();
                 if (!ok) break;
                 if (C::SEP) tc_fence_after();

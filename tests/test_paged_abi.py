@@ -199,7 +199,7 @@ def test_binding_refuses_host_tensors_and_mismatches(lib):
 class Split:
     """How the attention kernels cut a call, step by step as in paged_sched.cuh."""
 
-    def __init__(self, n, lens, Hkv, G, rows, bn, C, ovh=128, min_work=128):
+    def __init__(self, n, lens, Hkv, G, rows, bn, C, ovh=128, min_work=128, w_full=1, w_part=1, sub=0):
         self.n, self.lens, self.bn, self.ovh = n, lens, bn, ovh
         self.gs = min(G, rows)
         self.tpt = rows // self.gs
@@ -209,9 +209,9 @@ class Split:
             for hg in range(self.hg):
                 for r in range(-(-nb // self.tpt)):
                     kv = L if r == -(-nb // self.tpt) - 1 else max(0, L - nb + (r + 1) * self.tpt)
-                    units.append((b, hg, r, kv))
+                    units.append((b, hg, r, kv, w_full if min(self.tpt, nb - r * self.tpt) > sub else w_part))
         self.units = units
-        self.start = np.concatenate([[0], np.cumsum([ovh + u[3] for u in units])]).astype(object)
+        self.start = np.concatenate([[0], np.cumsum([ovh + u[3] * u[4] for u in units])]).astype(object)
         W = int(self.start[-1])
         self.C = max(1, min(C, W // min_work))
         each, rest = divmod(W, self.C)
@@ -219,8 +219,8 @@ class Split:
 
     def parts(self, c):
         out = []
-        for (b, hg, r, kv), u0 in zip(self.units, self.start):
-            cost, nt = self.ovh + kv, -(-kv // self.bn)
+        for (b, hg, r, kv, weight), u0 in zip(self.units, self.start):
+            cost, nt = self.ovh + kv * weight, -(-kv // self.bn)
             w0, w1 = self.w[c], self.w[c + 1]
             if u0 + cost <= w0 or u0 >= w1:
                 continue
@@ -235,11 +235,12 @@ class Split:
 def test_split_covers_every_key_tile_once_and_parts_can_be_joined(seed):
     rng = random.Random(seed)
     G, Hkv = rng.choice([1, 2, 3, 5, 8, 20]), rng.choice([1, 2, 4])
-    rows, bn, C = rng.choice([(16, 64, 304), (32, 128, 304), (8, 128, 152), (64, 32, 304), (128, 128, 152)])
+    rows, bn, C, more = rng.choice([(16, 64, 304, {}), (32, 128, 304, {}), (8, 128, 152, {}), (64, 32, 304, {}),
+                                    (256, 128, 152, dict(ovh=1024, min_work=2048, w_full=5, w_part=4, sub=128 // G))])
     B = rng.randint(1, 9)
     n = [rng.choice([0, 1, 1, rng.randint(1, 60)]) for _ in range(B)]
     lens = [rng.choice([0, 1, rng.randint(1, 200), rng.randint(1, 9000)]) for _ in range(B)]
-    s = Split(n, lens, Hkv, G, rows, bn, C)
+    s = Split(n, lens, Hkv, G, rows, bn, C, **more)
     seen, records = {}, {}
     for c in range(s.C):
         heads = tails = 0
