@@ -24,6 +24,15 @@ bool overlap(const void* p, size_t n, const void* q, size_t m) {
     return a < b + m && b < a + n;
 }
 
+// Rows of `w` bytes, n of them, ld bytes apart at p, against rows of wq bytes, ldq apart, at
+// q.  Slices of one buffer (the parts of a fused projection) interleave without sharing.
+bool rows_overlap(const void* p, int64_t w, int64_t ld, const void* q, int64_t wq, int64_t ldq, int64_t n) {
+    if (!p || !q || !overlap(p, (size_t)(ld * (n - 1) + w), q, (size_t)(ldq * (n - 1) + wq))) return false;
+    if (n == 1 || ld != ldq) return true;
+    const int64_t d = ((reinterpret_cast<intptr_t>(q) - reinterpret_cast<intptr_t>(p)) % ld + ld) % ld;
+    return d < w || d + wq > ld;
+}
+
 ne_status check_cache(const ne_paged_cache* c, int want_bytes, bool attn) {
     if (!c) return fail(NE_ERR_INVALID_ARG, "null cache");
     if (c->elem_bytes != 2 && c->elem_bytes != 4)
@@ -141,7 +150,11 @@ ne_status append_impl(int eb, const void* q, const void* k, const void* v, const
     if (q) {
         if ((s = check_rows("q", q, q_ld, Hq, c)) != NE_OK) return s;
         if ((s = check_rows("q_out", q_out, qo_ld, Hq, c)) != NE_OK) return s;
-        if (q == q_out && q_ld != qo_ld) return fail(NE_ERR_INVALID_ARG, "q_out may be q only with the same row stride");
+        const int64_t e = c->elem_bytes, qw = (int64_t)Hq * c->D * e, kw = (int64_t)c->Hkv * c->D * e;
+        if (q == q_out ? q_ld != qo_ld : rows_overlap(q_out, qw, qo_ld * e, q, qw, q_ld * e, N))
+            return fail(NE_ERR_INVALID_ARG, "q_out must be q itself, with the same row stride, or not overlap it");
+        if (rows_overlap(q_out, qw, qo_ld * e, k, kw, k_ld * e, N) || rows_overlap(q_out, qw, qo_ld * e, v, kw, v_ld * e, N))
+            return fail(NE_ERR_INVALID_ARG, "q_out must not overlap k or v");
     }
     ne::AppendArgs a = {};
     if ((s = ready((cudaStream_t)stream, &a.err)) != NE_OK) return s;
@@ -219,6 +232,10 @@ ne_status attn_impl(int eb, const void* q, const ne_paged_cache* c, const int* t
     if (B == 0 || N == 0) return NE_OK;
     if ((s = check_rows("q", q, q_ld, Hq, c)) != NE_OK) return s;
     if ((s = check_ptrs({o, lse})) != NE_OK) return s;
+    const int64_t row = (int64_t)Hq * c->D * eb;
+    if (rows_overlap(o, row, row, q, row, q_ld * eb, N) || rows_overlap(lse, Hq * 4, Hq * 4, q, row, q_ld * eb, N) ||
+        overlap(o, (size_t)(row * N), lse, (size_t)N * Hq * 4))
+        return fail(NE_ERR_INVALID_ARG, "o, lse and q must not overlap");
     const int G = Hq / c->Hkv;
     const size_t need = attn_ws_bytes(c->D, c->Hkv, G);
     if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
@@ -277,10 +294,11 @@ PagesWs pages_ws(int n_pages, int n, int W) {
     return w;
 }
 
-// Everything the three calls share.  n: sequences that take pages.  same_ok: table_out
-// may be page_table.
-ne_status pages_args(ne::PagesArgs* a, const ne_paged_cache* c, const int* ref, const int* table, int* ref_out,
-                     int* table_out, int* one_out, int B, int W, int n, bool same_ok, void* ws, size_t ws_bytes) {
+// Everything the three calls share.  n: sequences that take pages; more_out [more_n]: child
+// lengths or remap; same_ok: table_out may be page_table.
+ne_status pages_args(ne::PagesArgs* a, const ne_paged_cache* c, const int* ref, const int* table, const int* lens,
+                     const int* other, int* ref_out, int* table_out, int* more_out, size_t more_n, int* one_out, int B, int W,
+                     int n, bool same_ok, void* ws, size_t ws_bytes) {
     clear_error();
     ne_status s = check_cache(c, 0, false);
     if (s != NE_OK) return s;
@@ -288,15 +306,33 @@ ne_status pages_args(ne::PagesArgs* a, const ne_paged_cache* c, const int* ref, 
     if (W < 1 || (long long)W * c->page_size > (1 << 30) || (long long)std::max(B, n) * W >= (1LL << 31))
         return fail(NE_ERR_INVALID_ARG, "need max_pages >= 1, max_pages * page_size <= 2^30 and sequences * max_pages < 2^31 "
                     "(max_pages=%d)", W);
-    if ((s = check_ptrs({ref, ref_out, one_out})) != NE_OK) return s;
-    if (B > 0 && (s = check_ptrs({table})) != NE_OK) return s;
-    if (n > 0 && (s = check_ptrs({table_out})) != NE_OK) return s;
-    const size_t rb = (size_t)c->n_pages * 4, tb = (size_t)B * W * 4, ob = (size_t)n * W * 4;
-    if (ref_out != ref && overlap(ref, rb, ref_out, rb))
-        return fail(NE_ERR_INVALID_ARG, "refcount_out must be refcount itself or not overlap it");
-    if (!(same_ok && table_out == table) && overlap(table, tb, table_out, ob))
-        return fail(NE_ERR_INVALID_ARG, same_ok ? "table_out must be page_table itself or not overlap it"
-                                                : "child_table must not overlap page_table");
+    if ((s = check_ptrs({ref, ref_out})) != NE_OK) return s;
+    // The int arrays: inputs first, then outputs.  No output overlaps anything but the input it
+    // may be itself.
+    struct Ints {
+        const int* p;
+        size_t n;
+        const char* name;
+    };
+    const size_t P = c->n_pages;
+    const Ints in[4] = {{ref, P, "refcount"}, {table, (size_t)B * W, "page_table"}, {lens, lens ? (size_t)B : 0, "seq_lens"},
+                        {other, other ? (size_t)n : 0, "parents or new_lens"}};
+    const Ints out[4] = {{ref_out, P, "refcount_out"}, {table_out, (size_t)n * W, "table_out"}, {more_out, more_n, "child_lens or remap"},
+                         {one_out, 1, "short_out or n_live"}};
+    for (int i = 0; i < 4; ++i)
+        for (const Ints* a1 : {&in[i], &out[i]})
+            if (a1->n > 0 && !aligned4(a1->p))
+                return fail(NE_ERR_INVALID_ARG, "%s must be a non-null, 4-byte aligned device pointer", a1->name);
+    for (int i = 0; i < 4; ++i) {
+        for (int k = 0; k < 4; ++k) {
+            const bool itself = out[i].p == in[k].p && i == k && (i == 0 || (i == 1 && same_ok));
+            if (out[i].n > 0 && in[k].n > 0 && !itself && overlap(out[i].p, out[i].n * 4, in[k].p, in[k].n * 4))
+                return fail(NE_ERR_INVALID_ARG, "%s must not overlap %s", out[i].name, in[k].name);
+        }
+        for (int k = 0; k < i; ++k)
+            if (out[i].n > 0 && out[k].n > 0 && overlap(out[i].p, out[i].n * 4, out[k].p, out[k].n * 4))
+                return fail(NE_ERR_INVALID_ARG, "%s must not overlap %s", out[i].name, out[k].name);
+    }
     const PagesWs w = pages_ws(c->n_pages, n, W);
     if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
         return fail(NE_ERR_INVALID_ARG, "workspace must be non-null and 256-byte aligned (%zu bytes needed)", w.total);
@@ -425,13 +461,11 @@ ne_status ne_pages_fork(const ne_paged_cache* cache, const int* refcount, const 
                         int* short_out, int B, int C, int max_pages, void* workspace, size_t workspace_bytes,
                         ne_stream_t stream) {
     ne::PagesArgs a;
-    ne_status s = pages_args(&a, cache, refcount, page_table, refcount_out, child_table, short_out, B, max_pages, C, false,
-                             workspace, workspace_bytes);
+    clear_error();
+    if ((B > 0 && !seq_lens) || (C > 0 && !parents)) return fail(NE_ERR_INVALID_ARG, "null seq_lens or parents");
+    ne_status s = pages_args(&a, cache, refcount, page_table, seq_lens, parents, refcount_out, child_table, child_lens,
+                             C > 0 ? (size_t)C : 0, short_out, B, max_pages, C, false, workspace, workspace_bytes);
     if (s != NE_OK) return s;
-    if (B > 0 && (s = check_ptrs({seq_lens})) != NE_OK) return s;
-    if (C > 0 && (s = check_ptrs({parents, child_lens})) != NE_OK) return s;
-    if (C > 0 && overlap(seq_lens, (size_t)B * 4, child_lens, (size_t)C * 4))
-        return fail(NE_ERR_INVALID_ARG, "child_lens must not overlap seq_lens");
     if ((s = ready((cudaStream_t)stream, &a.err)) != NE_OK) return s;
     a.lens = seq_lens;
     a.other = parents;
@@ -446,10 +480,11 @@ ne_status ne_pages_resize(const ne_paged_cache* cache, const int* refcount, cons
                           const int* new_lens, int* refcount_out, int* table_out, int* short_out, int B, int max_pages,
                           void* workspace, size_t workspace_bytes, ne_stream_t stream) {
     ne::PagesArgs a;
-    ne_status s = pages_args(&a, cache, refcount, page_table, refcount_out, table_out, short_out, B, max_pages, B, true,
-                             workspace, workspace_bytes);
+    clear_error();
+    if (B > 0 && (!seq_lens || !new_lens)) return fail(NE_ERR_INVALID_ARG, "null seq_lens or new_lens");
+    ne_status s = pages_args(&a, cache, refcount, page_table, seq_lens, new_lens, refcount_out, table_out, nullptr, 0,
+                             short_out, B, max_pages, B, true, workspace, workspace_bytes);
     if (s != NE_OK) return s;
-    if (B > 0 && (s = check_ptrs({seq_lens, new_lens})) != NE_OK) return s;
     if ((s = ready((cudaStream_t)stream, &a.err)) != NE_OK) return s;
     a.lens = seq_lens;
     a.other = new_lens;
@@ -462,10 +497,10 @@ ne_status ne_pages_compact(const ne_paged_cache* cache, const int* refcount, con
                            int* table_out, int* remap, int* n_live, int B, int max_pages, void* workspace,
                            size_t workspace_bytes, ne_stream_t stream) {
     ne::PagesArgs a;
-    ne_status s = pages_args(&a, cache, refcount, page_table, refcount_out, table_out, n_live, B, max_pages, B, true,
-                             workspace, workspace_bytes);
+    ne_status s = pages_args(&a, cache, refcount, page_table, nullptr, nullptr, refcount_out, table_out, remap,
+                             cache && cache->n_pages > 0 ? (size_t)cache->n_pages : 0, n_live, B, max_pages, B, true, workspace,
+                             workspace_bytes);
     if (s != NE_OK) return s;
-    if ((s = check_ptrs({remap})) != NE_OK) return s;
     if ((s = ready((cudaStream_t)stream, &a.err)) != NE_OK) return s;
     a.lens_out = remap;
     cudaError_t e = ne::launch_pages(ne::PAGES_COMPACT, a, (cudaStream_t)stream);

@@ -211,11 +211,11 @@ __global__ void __launch_bounds__(F32Cfg<D, MANY>::THREADS) paged_f32_kernel(con
                 acc.w += x.w * wt;
             }
             if (g.whole()) {
-                const float inv = ll > 0.f ? 1.f / ll : 0.f;
+                const float inv = ll == 0.f ? 0.f : 1.f / ll;
                 const long long orow = (long long)(g.tok0 + g.tok + row / gs) * a.Hq + h0 + row % gs;
                 *reinterpret_cast<float4*>(static_cast<float*>(a.o) + orow * D + e) =
                     make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-                if (e == 0) a.lse[orow] = ll > 0.f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+                if (e == 0) a.lse[orow] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
             } else {
                 const size_t prow = (size_t)pslot * a.p.rows + row;
                 *reinterpret_cast<float4*>(a.part_o + prow * D + e) = acc;

@@ -74,9 +74,9 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedAttnArg
     auto stored = [&](int i) { return a.p.sub == 0 || i < a.p.sub * gs ? i : i - a.p.sub * gs + 128; };
     auto finish = [&](int i, float m, float l, const float4& o) {
         const long long row = (long long)(rec.y + i / gs) * a.Hq + hkv * a.G + hs * a.p.gs + i % gs;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
         put(static_cast<T*>(a.o) + row * D + e, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-        if (e == 0) a.lse[row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        if (e == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
     };
     if (live > 2 * (int)gridDim.y) {                       // many rows: one per lane group, four parts in flight
         for (int i = blockIdx.y * GR + grp; i < live; i += gridDim.y * GR) {

@@ -313,11 +313,11 @@ __global__ void __launch_bounds__(kThreads, 2) paged_short_kernel(const PagedAtt
                 acc.w += x.w * wt;
             }
             if (g.whole()) {
-                const float inv = l > 0.f ? 1.f / l : 0.f;
+                const float inv = l == 0.f ? 0.f : 1.f / l;
                 const long long orow = (long long)(g.tok0 + g.tok + row / gs) * a.Hq + h0 + row % gs;
                 uint2 pk = make_uint2(pack2(acc.x * inv, acc.y * inv), pack2(acc.z * inv, acc.w * inv));
                 *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + orow * D + e) = pk;
-                if (e == 0) a.lse[orow] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+                if (e == 0) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
             } else {
                 const size_t prow = (size_t)pslot * a.p.rows + row;
                 *reinterpret_cast<float4*>(a.part_o + prow * D + e) = acc;

@@ -262,25 +262,17 @@ __global__ void __launch_bounds__(384, 1)
             if (g.t0 == g.t1) continue;
             const int n_sub = g.ntok > sub ? 2 : 1, nt = g.t1 - g.t0;
             if (!(ok = mbar_wait_warp(smem_u32(&bar_q_full), seg & 1, w, SITE_PAGED_Q))) break;
-            ok = full(item) && s_free(0);
+            ok = full(item) && s_free(0) && (n_sub == 1 || s_free(1));
             if (!ok) break;
-            if (elect_one()) s_mmas(0, item);
-            __syncwarp();
-            ++s_tiles[0];
-            if (n_sub == 2) {
-                // SEP: the second subtile starts half a tile behind the first, so that one's
-                // exponentials run beside the other's loads and maxima.
-                ok = s_free(1) && s_free(0);
-                if (!ok) break;
-                if (elect_one()) s_mmas(1, item);
-                __syncwarp();
-                ++s_tiles[1];
-            }
             if (elect_one()) {
+                s_mmas(0, item);
+                if (n_sub == 2) s_mmas(1, item);
                 umma_commit(smem_u32(&bar_empty[item % C::NS]));
                 if (nt == 1) umma_commit(smem_u32(&bar_q_empty));
             }
             __syncwarp();
+            ++s_tiles[0];
+            if (n_sub == 2) ++s_tiles[1];
             for (int t = 0; ok && t < nt; ++t) {
                 const int vi = item + 2 * t + 1, kn = item + 2 * t + 2;
                 const bool more = t + 1 < nt, fix = (g.t0 + t + 1) * C::BN > g.len;
@@ -496,7 +488,7 @@ __global__ void __launch_bounds__(384, 1)
             if (!warp_live) continue;
             tc_fence_after();
             const bool whole = g.whole();
-            const float inv = !whole ? 1.f : l > 0.f ? 1.f / l : 0.f;
+            const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
             // A thread holds a row's columns; four neighbours exchange 16-byte units, so that a store
             // writes 64 bytes of each of eight rows instead of 16 of each of 32 (at D 128 the
             // scattered stores took 4 us a part).
@@ -541,7 +533,7 @@ __global__ void __launch_bounds__(384, 1)
             __syncwarp();
             tc_fence_before();
             if (live) {
-                if (whole) a.lse[orow] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+                if (whole) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
                 else a.part_ml[prow] = make_float2(m, l);
             }
             if (!whole && u == 0 && r == 0) a.part_info[blockIdx.x * 2 + g.slot()] = paged_record(g);

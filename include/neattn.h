@@ -358,7 +358,8 @@ ne_status ne_paged_append_f32(const float* q, const float* k, const float* v, co
  * bf16: tensor-core products of bf16 inputs with fp32 accumulation and fp32 softmax
  * statistics; f32: fp32 throughout (no TF32).  Work is split over the key axis by counted
  * work, so results depend on the shape, lengths and device but never on timing: the same
- * call gives the same bits.  workspace: ne_paged_attn_workspace_size() bytes, 256-byte
+ * call gives the same bits.  o and lse overlap neither q nor each other.  workspace:
+ * ne_paged_attn_workspace_size() bytes (10 to 40 MB, whatever B and N), 256-byte
  * aligned, caller-owned, rewritten by every call (two calls that may overlap need two).
  * Device-side arguments are checked as in ne_paged_append; a bad page id reads as zeros. */
 size_t ne_paged_attn_workspace_size(int B, int N, int Hq, int Hkv, int D);
@@ -376,11 +377,11 @@ ne_status ne_paged_attn_f32(const float* q, const ne_paged_cache* cache, const i
  * call is all or nothing: when the pool has too few free pages, short_out[0] is how many
  * are missing, the outputs equal the inputs (for a fork: every child empty) and no page is
  * written; otherwise it is 0.  refcount_out (and, but for a fork, table_out) may be the
- * input itself; partial overlaps are refused.  Nothing synchronises: a whole scheduling
+ * input itself; any other overlap of an output is refused.  Nothing synchronises: a whole scheduling
  * step can be captured.  page_table entries behind a sequence's pages are -1 on output.
  * workspace: ne_pages_workspace_size(n_pages, n, max_pages) bytes, n the number of
- * sequences (for a fork: of children), 256-byte aligned, caller-owned, rewritten by every call.  int arrays
- * are 16-byte aligned.  Bad ids are skipped and reported by ne_get_device_error().
+ * sequences (for a fork: of children), 256-byte aligned, caller-owned, rewritten by every call.  refcount
+ * and refcount_out are 16-byte aligned, the other int arrays 4-byte.  Bad ids are skipped and reported by ne_get_device_error().
  *
  * ne_pages_fork: child c continues sequence parents[c] (-1: an empty child).  Shared
  * (deep == 0): whole pages are shared (their counts rise), the partly filled last page is

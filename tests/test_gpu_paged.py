@@ -167,6 +167,13 @@ CHUNKS = [
 ]
 
 
+def test_attn_contexts_too_short_to_cut():
+    """Tables of at most 256 positions: whole units only, no join."""
+    for dtype in (BF16, F32):
+        for mn in (1, None):
+            attn_case(dtype, 12, 4, 64, 16, [1, 3, 0, 60, 1, 9], [239, 3, 17, 200, 1, 5], 91, max_new=mn, tail=1)
+
+
 @pytest.mark.parametrize("Hq,Hkv,D,ps,n,lens", CHUNKS)
 @pytest.mark.parametrize("max_new", [1, 4, None])
 def test_attn_chunks_bf16(Hq, Hkv, D, ps, n, lens, max_new):
@@ -212,6 +219,51 @@ def test_attn_queries_from_a_fused_projection_and_side_by_side_pools():
         o, lse = ne.paged_attn(q, kp, vp, i32(t), i32(lens), i32(cu), max_new=mn)
         ok()
         check_attn(q.contiguous(), kp, vp, i32(t), lens, cu, o, lse, BF16, HALF[BF16])
+
+
+@pytest.mark.parametrize("dtype,mn", [(BF16, 1), (BF16, None), (F32, 1), (F32, None)])
+def test_attn_pages_beyond_32_bit_offsets(dtype, mn):
+    """Pages 2^30 elements apart: the last starts at element 2^32 of its pool."""
+    ps, Hkv, D, P = 16, 2, 64, 5
+    flat = [torch.empty((P - 1) * 2 ** 30 + ps * Hkv * D, dtype=dtype, device="cuda") for _ in range(2)]
+    kp, vp = (x.as_strided((P, ps, Hkv, D), (2 ** 30, Hkv * D, D, 1)) for x in flat)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(9)
+    kp.copy_(torch.randn(P, ps, Hkv, D, generator=g, device="cuda"))
+    vp.copy_(torch.randn(P, ps, Hkv, D, generator=g, device="cuda"))
+    n, lens, t = [20, 1], [30, 39], np.array([[4, 1, 0], [3, 0, 2]], np.int32)
+    q = synthetic.randn((21, 6, D), 4, 1.0, dtype).cuda()
+    cu = [0, 20, 21]
+    k = synthetic.randn((21, Hkv, D), 5, 1.0, dtype).cuda()
+    ne.paged_append(k, k, kp, vp, i32(t), i32(lens), i32(cu))
+    o, lse = ne.paged_attn(q, kp, vp, i32(t), i32(lens), i32(cu), max_new=mn)
+    ok()
+    check_attn(q, kp, vp, i32(t), lens, cu, o, lse, dtype, HALF[BF16] if dtype == BF16 else 0.0)
+    assert torch.equal(kp[4, 10:], k[:6]) and torch.equal(vp[2, 6], k[20])
+    # A copy from the last page to the first free one.
+    refc = np.array([2, 1, 1, 0, 1], np.int32)
+    ref4 = kp[4].clone()
+    out = ne.pages_fork(i32(refc), i32([[4, 1]]), i32([10]), i32([0]), kp, vp)
+    ok()
+    assert out[1].tolist() == [[3, -1]] and torch.equal(kp[3, :10], ref4[:10])
+
+
+@pytest.mark.parametrize("dtype,mn", [(BF16, 1), (BF16, None), (F32, 1), (F32, None)])
+def test_attn_nan_in_a_key_in_use_shows(dtype, mn):
+    """A NaN key in front of a row's position makes that row NaN (o and lse) and no row that
+    does not see it, in its own or another sequence."""
+    ps, lens, n = 16, [300, 90], [40, 1]
+    t, P = tables(lens, ps, 3)
+    kp, vp = pool(P, ps, 4, 64, dtype, 4), pool(P, ps, 4, 64, dtype, 5)
+    at = 280                                               # the 20th new token's own key
+    kp[t[0, at // ps], at % ps, 2] = math.nan
+    q = synthetic.randn((41, 12, 64), 6, 1.0, dtype).cuda()
+    o, lse = ne.paged_attn(q, kp, vp, i32(t), i32(lens), i32([0, 40, 41]), max_new=mn)
+    ok()
+    hit = torch.zeros(41, 12, dtype=torch.bool, device="cuda")
+    hit[20:40, 6:9] = True                                 # kv head 2
+    assert bool(torch.isnan(lse)[hit].all()) and bool(torch.isnan(o.float())[hit].all())
+    assert bool(torch.isfinite(lse)[~hit].all()) and bool(torch.isfinite(o.float())[~hit].all())
 
 
 @pytest.mark.parametrize("dtype,mn", [(BF16, 1), (BF16, None), (F32, 1), (F32, None)])

@@ -31,12 +31,12 @@ def cache(**kw):
     return ctypes.byref(ne.PagedCache(*[c[n] for n, _ in ne.PagedCache._fields_]))
 
 
-def attn(lib, c=None, q=P, table=P, lens=P, cu=P, o=P, lse=P, q_ld=256, B=2, N=5, Hq=4, W=4, max_new=3, ws=P, nb=WS, f32=False):
+def attn(lib, c=None, q=P, table=P, lens=P, cu=P, o=vp(1 << 20), lse=vp(2 << 20), q_ld=256, B=2, N=5, Hq=4, W=4, max_new=3, ws=P, nb=WS, f32=False):
     fn = lib.ne_paged_attn_f32 if f32 else lib.ne_paged_attn
     return fn(q, cache() if c is None else c, table, lens, cu, o, lse, q_ld, B, N, Hq, W, max_new, ws, nb, NULL)
 
 
-def append(lib, c=None, q=P, k=P, v=P, table=P, lens=P, cu=P, spec=None, off=0, qo=vp(8192), lds=(256, 128, 128, 256), B=2, N=5,
+def append(lib, c=None, q=P, k=vp(1 << 20), v=vp(2 << 20), table=P, lens=P, cu=P, spec=None, off=0, qo=vp(3 << 20), lds=(256, 128, 128, 256), B=2, N=5,
            Hq=4, W=4):
     return lib.ne_paged_append(q, k, v, cache() if c is None else c, table, lens, cu, spec, off, qo, *lds, B, N, Hq, W, NULL)
 
@@ -70,6 +70,7 @@ def test_attn_and_append_refuse_bad_caches(lib, kw, status, word):
     (dict(cu=vp(4097)), "4-byte"), (dict(max_new=0), "max_new"), (dict(q=NULL), "q must"), (dict(q=vp(4104)), "aligned"),
     (dict(q_ld=255), "rows"), (dict(q_ld=260), "rows"), (dict(o=NULL), "null"), (dict(lse=vp(4100)), "aligned"),
     (dict(ws=NULL), "workspace"), (dict(ws=vp(4112)), "workspace"), (dict(nb=1024), "too small"), (dict(N=1 << 24), "2^31"),
+    (dict(o=vp(4096 + 512)), "overlap"), (dict(lse=vp(1 << 20)), "overlap"), (dict(lse=vp(4096 + 64)), "overlap"),
 ])
 def test_attn_refuses_bad_arguments(lib, kw, word):
     assert attn(lib, **kw) == ne.NE_ERR_INVALID_ARG and word in lib.ne_last_error().decode()
@@ -84,6 +85,7 @@ def test_f32_attn_refuses_head_dim_128_and_bf16_pools(lib):
     (dict(q=NULL), "together"), (dict(qo=NULL), "together"), (dict(k=NULL), "k must"), (dict(v=vp(4104)), "v must"),
     (dict(lds=(256, 64, 128, 256)), "k rows"), (dict(lds=(256, 128, 132, 256)), "v rows"), (dict(lds=(248, 128, 128, 256)), "q rows"),
     (dict(lds=(256, 128, 128, 128)), "q_out rows"), (dict(qo=P, lds=(256, 128, 128, 512)), "same row stride"),
+    (dict(qo=vp(4096 + 256)), "q_out"), (dict(qo=vp((1 << 20) + 64)), "k or v"),
     (dict(off=-1), "pos_offset"), (dict(off=1 << 30), "pos_offset"), (dict(cu=NULL), "N == B"), (dict(N=1 << 25), "2^31"),
 ])
 def test_append_refuses_bad_arguments(lib, kw, word):
@@ -112,20 +114,20 @@ def pages(lib, op, c=None, ref=vp(1 << 20), table=vp(2 << 20), lens=vp(3 << 20),
 
 @pytest.mark.parametrize("op", ["fork", "resize", "compact"])
 @pytest.mark.parametrize("kw,word", [
-    (dict(ref=NULL), "null"), (dict(table=NULL), "null"), (dict(ro=vp(4100)), "aligned"), (dict(to=NULL), "null"),
-    (dict(one=NULL), "null"), (dict(B=-1), ">= 0"), (dict(W=0), "max_pages"), (dict(W=1 << 27), "max_pages"),
-    (dict(ro=vp((1 << 20) + 16)), "refcount_out"), (dict(to=vp((2 << 20) + 16)), "overlap"), (dict(ws=NULL), "workspace"),
+    (dict(ref=NULL), "null"), (dict(table=NULL), "null"), (dict(ro=vp(4104)), "aligned"), (dict(to=NULL), "null"),
+    (dict(one=NULL), "null"), (dict(table=vp(4098)), "aligned"), (dict(one=vp(1 << 20)), "overlap"),
+    (dict(to=vp(5 << 20)), "overlap"), (dict(B=-1), ">= 0"), (dict(W=0), "max_pages"), (dict(W=1 << 27), "max_pages"),
+    (dict(ro=vp((1 << 20) + 16)), "refcount_out"), (dict(to=vp((2 << 20) + 16)), "table_out"), (dict(ws=NULL), "workspace"),
     (dict(nb=512), "too small"),
 ])
 def test_pages_calls_refuse_bad_arguments(lib, op, kw, word):
-    if "overlap" in word and op != "fork":
-        word = "table_out"
     assert pages(lib, op, **kw) == ne.NE_ERR_INVALID_ARG and word in lib.ne_last_error().decode()
 
 
 def test_a_fork_refuses_its_own_table_and_lengths_as_outputs(lib):
     assert pages(lib, "fork", to=vp(2 << 20)) == ne.NE_ERR_INVALID_ARG
-    assert pages(lib, "fork", lo=vp(3 << 20)) == ne.NE_ERR_INVALID_ARG and "child_lens" in lib.ne_last_error().decode()
+    for other in (3 << 20, (4 << 20) + 8):                 # seq_lens; inside parents
+        assert pages(lib, "fork", lo=vp(other)) == ne.NE_ERR_INVALID_ARG and "child_lens" in lib.ne_last_error().decode()
     assert pages(lib, "fork", other=NULL) == ne.NE_ERR_INVALID_ARG
     assert pages(lib, "resize", lens=NULL) == ne.NE_ERR_INVALID_ARG
     assert pages(lib, "compact", lo=NULL) == ne.NE_ERR_INVALID_ARG
