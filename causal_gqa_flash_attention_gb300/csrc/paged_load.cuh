@@ -60,13 +60,4 @@ __device__ __forceinline__ int page_of(const PagedView& c, const int* row, int p
     return p;
 }
 
-// The table into the L2, a share per CTA, while the CTAs look for their parts: a cache
-// larger than the L2 has pushed it out since the last call, and a part's first page ids would
-// each cost a trip to memory.  (Bounded: 128 lines of 128 bytes per CTA.)
-__device__ __forceinline__ void prefetch_table(const PagedBatch& s, int cta, int ctas, int lane) {
-    const long long lines = ((long long)s.B * s.W + 31) / 32;
-    for (long long i = (long long)lane * ctas + cta, n = 0; i < lines && n < 4; i += 32LL * ctas, ++n)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(s.table + i * 32));
-}
-
 }  // namespace ne

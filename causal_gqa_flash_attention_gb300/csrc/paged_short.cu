@@ -73,31 +73,21 @@ __global__ void __launch_bounds__(kThreads, 2) paged_short_kernel(const PagedAtt
     griddep_launch_dependents();
     griddep_wait();
     const uint32_t ring0 = smem_u32(ring) + warp * C::RING;
-    // Warp 0 finds the CTA's parts.  Meanwhile the others run the loop below once on a part
-    // without rows and keys (it reads and writes nothing but their own rings): a kernel's first
-    // pass through its code waits for the code itself, three microseconds that are then spent
-    // beside the search instead of behind it.
+    // Warp 0 finds the CTA's parts.
     PagedWalk walk;
     PagedSeg g;
-    bool dry = warp != 0;
     int turn = 0;
-    if (dry) {
-        if (warp == 1) prefetch_table(a.s, blockIdx.x, gridDim.x, lane);
-        g.b = g.hg = g.r = g.tok = g.ntok = g.tok0 = g.base = g.len = g.kv = g.t0 = 0;
-        g.t1 = g.nt = 1;
-    } else {
+    if (warp == 0) {
         paged_locate_warp(a, blockIdx.x, walk, blockIdx.x == 0);
         if (lane < 2) a.part_info[blockIdx.x * 2 + lane] = make_int4(0, 0, 0, 0);
         if (!walk.next(a, g)) g.b = -1;
         if (lane == 0) s_part[0] = g;
     }
     while (true) {
-        if (!dry) {
-            __syncthreads();                               // the part is there, the rings are free
-            g = s_part[turn & 1];
-            ++turn;
-            if (g.b < 0) break;
-        }
+        __syncthreads();                                   // the part is there, the rings are free
+        g = s_part[turn & 1];
+        ++turn;
+        if (g.b < 0) break;
         const int hs = a.G > a.p.gs ? g.hg % ((a.G + a.p.gs - 1) / a.p.gs) : 0;
         const int hkv = a.G > a.p.gs ? g.hg / ((a.G + a.p.gs - 1) / a.p.gs) : g.hg;
         const int h0 = hkv * a.G + hs * a.p.gs;            // first query head of the unit
@@ -259,10 +249,6 @@ __global__ void __launch_bounds__(kThreads, 2) paged_short_kernel(const PagedAtt
         }
         cp_async_wait<0>();
 
-        if (dry) {
-            dry = false;
-            continue;
-        }
         if (warp == 0) {
             PagedSeg n;
             if (!walk.next(a, n)) n.b = -1;

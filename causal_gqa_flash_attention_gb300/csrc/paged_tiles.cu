@@ -29,7 +29,6 @@
 // Every wait is bounded; a CTA that gives up reports, drains its copies and UMMAs, frees its
 // TMEM and ends.
 #include <cuda_bf16.h>
-#include "paged_load.cuh"
 #include "paged_sched.cuh"
 
 namespace ne {
@@ -331,7 +330,6 @@ __global__ void __launch_bounds__(384, 1)
         // ------------------------------------------------------------ V rows behind the length
         // It follows every slot's phases and releases each along with the issuer, so neither can
         // fall a phase behind the other.
-        prefetch_table(a.s, blockIdx.x, gridDim.x, lane);
         int item = 0, fixes = 0;
         bool ok = true;
         while (ok && next_part()) {
