@@ -211,7 +211,7 @@ ne_status tile_maps(CUtensorMap* tq, CUtensorMap* tk, CUtensorMap* tv, const ne_
 size_t attn_ws_bytes(int D, int Hkv, int G) {
     size_t most = 0;
     for (int f32 = 0; f32 < 2; ++f32)
-        for (int rows : {1, 8, 9, 16, 17, 32, 33, 1 << 20}) {
+        for (int rows : {1, 2, 4, 5, 8, 9, 16, 17, 32, 33, 1 << 20}) {
             if (f32 && D > 64) continue;
             const ne::PagedKind kind = ne::paged_kind(f32 != 0, D, G, rows);
             most = std::max(most, ne::paged_part_bytes(ne::paged_split(kind, D, Hkv, G, 1 << 30), D));

@@ -8,7 +8,7 @@
 //
 // A warp holds RW query rows.  S: lane = key, the query rows broadcast from shared memory;
 // O: lane = two (or one) elements of D, the weights broadcast.  FEW: four warps take
-// interleaved 32-key steps of the same 8 rows, each with a private ring, and are joined at
+// interleaved 32-key steps of the same 4 or 8 rows, each with a private ring, and are joined at
 // the end of a unit.  MANY: eight warps take 8 of 64 rows each over one shared ring.
 #include "paged_load.cuh"
 #include "paged_sched.cuh"
@@ -17,9 +17,8 @@ namespace ne {
 namespace {
 
 constexpr int kStages = 3;
-constexpr int RW = 8;                                      // query rows per warp
-
-template <int D, bool MANY>
+// RW: query rows per warp.
+template <int D, int RW, bool MANY>
 struct F32Cfg {
     static constexpr int WK = MANY ? 1 : 4;                // warps along the keys
     static constexpr int WR = MANY ? 8 : 1;                // warps along the rows
@@ -37,9 +36,9 @@ struct F32Cfg {
     static_assert(WK * ROWS * D * 4 <= RINGS, "the join fits into the rings");
 };
 
-template <int D, bool MANY>
-__global__ void __launch_bounds__(F32Cfg<D, MANY>::THREADS) paged_f32_kernel(const PagedAttnArgs a) {
-    using C = F32Cfg<D, MANY>;
+template <int D, int RW, bool MANY>
+__global__ void __launch_bounds__(F32Cfg<D, RW, MANY>::THREADS) paged_f32_kernel(const PagedAttnArgs a) {
+    using C = F32Cfg<D, RW, MANY>;
     constexpr int U = C::U, DL = C::DL;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ PagedLocate loc;
@@ -97,14 +96,15 @@ __global__ void __launch_bounds__(F32Cfg<D, MANY>::THREADS) paged_f32_kernel(con
         const int nsteps = g.t1 - g.t0;
         const int first = g.t0 * C::BN + wk * 32;
         const int lfirst = first + (MANY ? warp * LROWS : 0);
-        int pid = page_of(a.c, trow, lfirst + lane, g.kv, a.err);
-        int pid1 = nsteps > 1 ? page_of(a.c, trow, lfirst + C::BN + lane, g.kv, a.err) : -1;
+        int pid = page_at(a.c, trow, lfirst + lane, g.kv);
+        int pid1 = nsteps > 1 ? page_at(a.c, trow, lfirst + C::BN + lane, g.kv) : -1;
         auto issue = [&](int j) {
             if (j < nsteps) {
                 const int at = lfirst + j * C::BN;
-                const int pid2 = j + 2 < nsteps ? page_of(a.c, trow, at + 2 * C::BN + lane, g.kv, a.err) : -1;
+                const int pid2 = j + 2 < nsteps ? page_at(a.c, trow, at + 2 * C::BN + lane, g.kv) : -1;
                 const uint32_t st = ring0 + (j % kStages) * 2 * C::TILE;
-                load_rows<LROWS, U>(st, st + C::TILE, kp, vp, a.c, 4, MANY ? warp * LROWS : 0, at, g.kv, pid, lane);
+                load_rows<LROWS, U>(st, st + C::TILE, kp, vp, a.c, 4, MANY ? warp * LROWS : 0, at, g.kv,
+                                    checked_page(a.c, pid, at + lane, g.kv, a.err), lane);
                 pid = pid1;
                 pid1 = pid2;
             }
@@ -151,14 +151,21 @@ __global__ void __launch_bounds__(F32Cfg<D, MANY>::THREADS) paged_f32_kernel(con
 #pragma unroll
                 for (int e = 0; e < DL; ++e) o[r][e] *= al;
             }
-            *reinterpret_cast<float4*>(s_p + lane * RW) = make_float4(p[0], p[1], p[2], p[3]);
-            *reinterpret_cast<float4*>(s_p + lane * RW + 4) = make_float4(p[4], p[5], p[6], p[7]);
+#pragma unroll
+            for (int r = 0; r < RW; r += 4)
+                *reinterpret_cast<float4*>(s_p + lane * RW + r) = make_float4(p[r], p[r + 1], p[r + 2], p[r + 3]);
             __syncwarp();
 #pragma unroll 4
             for (int k = 0; k < 32; ++k) {
-                const float4 pa = *reinterpret_cast<const float4*>(s_p + k * RW);
-                const float4 pb = *reinterpret_cast<const float4*>(s_p + k * RW + 4);
-                const float pr[RW] = {pa.x, pa.y, pa.z, pa.w, pb.x, pb.y, pb.z, pb.w};
+                float pr[RW];
+#pragma unroll
+                for (int r = 0; r < RW; r += 4) {
+                    const float4 x = *reinterpret_cast<const float4*>(s_p + k * RW + r);
+                    pr[r] = x.x;
+                    pr[r + 1] = x.y;
+                    pr[r + 2] = x.z;
+                    pr[r + 3] = x.w;
+                }
                 if constexpr (DL == 2) {
                     const float2 v = *reinterpret_cast<const float2*>(sv + tile_unit<U>(k, lane >> 1) * 4 + (lane & 1) * 2);
 #pragma unroll
@@ -227,10 +234,10 @@ __global__ void __launch_bounds__(F32Cfg<D, MANY>::THREADS) paged_f32_kernel(con
     }
 }
 
-template <int D, bool MANY>
+template <int D, int RW, bool MANY>
 cudaError_t launch_f32_t(const PagedAttnArgs& a, cudaStream_t st) {
-    using C = F32Cfg<D, MANY>;
-    auto kfn = paged_f32_kernel<D, MANY>;
+    using C = F32Cfg<D, RW, MANY>;
+    auto kfn = paged_f32_kernel<D, RW, MANY>;
     static_assert(C::SMEM + 4096 <= 227 * 1024, "shared memory");
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(kfn, C::SMEM, done);
@@ -238,16 +245,22 @@ cudaError_t launch_f32_t(const PagedAttnArgs& a, cudaStream_t st) {
     return launch_k(kfn, dim3(a.p.C), dim3(C::THREADS), C::SMEM, st, a);
 }
 
+template <int D>
+cudaError_t launch_f32_d(PagedKind kind, const PagedAttnArgs& a, cudaStream_t st) {
+    switch (kind) {
+        case PAGED_F32_FEW4: return launch_f32_t<D, 4, false>(a, st);
+        case PAGED_F32_FEW8: return launch_f32_t<D, 8, false>(a, st);
+        default: return launch_f32_t<D, 8, true>(a, st);
+    }
+}
+
 }  // namespace
 
-int paged_f32_bn(bool many) { return many ? F32Cfg<64, true>::BN : F32Cfg<64, false>::BN; }
+int paged_f32_bn(bool many) { return many ? F32Cfg<64, 8, true>::BN : F32Cfg<64, 8, false>::BN; }
 
 cudaError_t launch_paged_f32(PagedKind kind, int D, const PagedAttnArgs& a, cudaStream_t st) {
-    const bool many = kind == PAGED_F32_MANY;
-    switch (D) {
-        case 32: return many ? launch_f32_t<32, true>(a, st) : launch_f32_t<32, false>(a, st);
-        case 64: return many ? launch_f32_t<64, true>(a, st) : launch_f32_t<64, false>(a, st);
-    }
+    if (D == 32) return launch_f32_d<32>(kind, a, st);
+    if (D == 64) return launch_f32_d<64>(kind, a, st);
     return cudaErrorInvalidValue;
 }
 

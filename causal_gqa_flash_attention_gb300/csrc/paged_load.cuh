@@ -48,16 +48,17 @@ __device__ __forceinline__ void load_rows(uint32_t sk, uint32_t sv, const char* 
     }
 }
 
-// Page of position pos of a sequence (row: its table row), -1 at or behind kv_end or for
-// an id outside the pool (reported).
-__device__ __forceinline__ int page_of(const PagedView& c, const int* row, int pos, int kv_end, int* err) {
-    if (pos >= kv_end) return -1;
-    const int p = __ldg(row + (pos >> c.ps_shift));
-    if ((unsigned)p >= (unsigned)c.n_pages) {
-        report_error(err, SITE_PAGED_PAGE);
-        return -1;
-    }
-    return p;
+// Page of position pos of a sequence (row: its table row), -1 at or behind kv_end.  The id
+// is looked at only when it is used (checked_page): a branch on it here would hold the warp
+// for the load.
+__device__ __forceinline__ int page_at(const PagedView& c, const int* row, int pos, int kv_end) {
+    return pos < kv_end ? __ldg(row + (pos >> c.ps_shift)) : -1;
+}
+// The same id, -1 when it lies outside the pool (reported).
+__device__ __forceinline__ int checked_page(const PagedView& c, int page, int pos, int kv_end, int* err) {
+    if ((unsigned)page < (unsigned)c.n_pages) return page;
+    if (pos < kv_end) report_error(err, SITE_PAGED_PAGE);
+    return -1;
 }
 
 }  // namespace ne

@@ -136,17 +136,18 @@ __global__ void __launch_bounds__(kThreads, 2) paged_short_kernel(const PagedAtt
         const int first = g.t0 * C::BN + warp * KT;
         // Page ids are fetched two steps ahead of the copies that need them, which run two steps
         // ahead of the products.
-        int pid = page_of(a.c, trow, first + lane, g.kv, a.err);
-        int pid1 = nsteps > 1 ? page_of(a.c, trow, first + C::BN + lane, g.kv, a.err) : -1;
+        int pid = page_at(a.c, trow, first + lane, g.kv);
+        int pid1 = nsteps > 1 ? page_at(a.c, trow, first + C::BN + lane, g.kv) : -1;
 #pragma unroll 1
         for (int j = 1 - kStages; j < nsteps; ++j) {
             __syncwarp();                                  // step j - 1 has been read by the whole warp
             const int jn = j + kStages - 1;                // into the stage of step j - 1
             if (jn < nsteps) {
                 const int at = first + jn * C::BN;
-                const int pid2 = jn + 2 < nsteps ? page_of(a.c, trow, at + 2 * C::BN + lane, g.kv, a.err) : -1;
+                const int pid2 = jn + 2 < nsteps ? page_at(a.c, trow, at + 2 * C::BN + lane, g.kv) : -1;
                 const uint32_t st = ring0 + (jn % kStages) * 2 * C::TILE;
-                load_rows<KT, U>(st, st + C::TILE, kp, vp, a.c, 2, 0, at, g.kv, pid, lane);
+                load_rows<KT, U>(st, st + C::TILE, kp, vp, a.c, 2, 0, at, g.kv,
+                                 checked_page(a.c, pid, at + lane, g.kv, a.err), lane);
                 pid = pid1;
                 pid1 = pid2;
             }

@@ -178,13 +178,7 @@ __global__ void __launch_bounds__(384, 1)
             const int* trow = a.s.table + (size_t)g.b * a.s.W;
             auto page = [&](int t) -> int {                // page of this lane's part of tile t
                 const int pos = t * C::BN + lane * rows;
-                if (lane >= npg || pos >= g.kv) return a.c.n_pages;    // behind the pool: zeros
-                const int p = __ldg(trow + (pos >> a.c.ps_shift));
-                if ((unsigned)p >= (unsigned)a.c.n_pages) {
-                    report_error(a.err, SITE_PAGED_PAGE);
-                    return a.c.n_pages;
-                }
-                return p;
+                return lane < npg && pos < g.kv ? __ldg(trow + (pos >> a.c.ps_shift)) : -1;
             };
             int next = page(g.t0), next1 = g.t0 + 1 < g.t1 ? page(g.t0 + 1) : 0;   // two tiles ahead
             if (seg > 0 && !(ok = mbar_wait_warp(smem_u32(&bar_q_empty), (seg - 1) & 1, w, SITE_PAGED_Q))) break;
@@ -199,7 +193,13 @@ __global__ void __launch_bounds__(384, 1)
             }
             ++seg;
             for (int t = g.t0; ok && t < g.t1; ++t) {
-                const int p = next;
+                // (Looked at only now: a branch on the id at its load would wait for it.)  An id
+                // outside the pool reads as zeros: TMA fills what lies behind the last page.
+                int p = next;
+                if ((unsigned)p >= (unsigned)a.c.n_pages) {
+                    if (lane < npg && t * C::BN + lane * rows < g.kv) report_error(a.err, SITE_PAGED_PAGE);
+                    p = a.c.n_pages;
+                }
                 next = next1;
                 if (t + 2 < g.t1) next1 = page(t + 2);
 #pragma unroll
