@@ -64,6 +64,7 @@ template <int D, int MT>
 __global__ void __launch_bounds__(kThreads, 2) paged_short_kernel(const PagedAttnArgs a) {
     using C = ShortCfg<D>;
     constexpr int KT = C::KT, U = C::U, NT = KT / 8, NO = D / 8;
+    constexpr bool PRE = 16 * MT * D * 4 <= 2 * C::TILE;   // a warp's output fits into one stage
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ PagedSeg s_part[2];                         // the CTA's parts in turn (b < 0: the end)
     __shared__ float s_m[kWarps][16 * MT], s_l[kWarps][16 * MT];
@@ -73,29 +74,55 @@ __global__ void __launch_bounds__(kThreads, 2) paged_short_kernel(const PagedAtt
     griddep_launch_dependents();
     griddep_wait();
     const uint32_t ring0 = smem_u32(ring) + warp * C::RING;
-    // Warp 0 finds the CTA's parts.
+    const int ngrp = (a.G + a.p.gs - 1) / a.p.gs;          // head groups of a kv head
+    // This warp's stream of the part begun last: step j, keys first + j C::BN on, goes through
+    // stage (s0 + j) % kStages.
+    const int* trow = nullptr;
+    const char *kp = nullptr, *vp = nullptr;
+    int first = 0, nsteps = 0, kv = 0, s0 = 0, pid = -1, pid1 = -1;
+    // Page ids are fetched two steps ahead of the copies that need them, which run two steps
+    // ahead of the products.
+    auto issue = [&](int j) {
+        if (j < nsteps) {
+            const int at = first + j * C::BN;
+            const int pid2 = j + 2 < nsteps ? page_at(a.c, trow, at + 2 * C::BN + lane, kv) : -1;
+            const uint32_t st = ring0 + ((s0 + j) % kStages) * 2 * C::TILE;
+            load_rows<KT, U>(st, st + C::TILE, kp, vp, a.c, 2, 0, at, kv, checked_page(a.c, pid, at + lane, kv, a.err), lane);
+            pid = pid1;
+            pid1 = pid2;
+        }
+        cp_async_commit();
+    };
+    auto begin = [&](const PagedSeg& p) {
+        const long long head = (long long)(p.hg / ngrp) * a.c.head_stride * 2;
+        trow = a.s.table + (size_t)p.b * a.s.W;
+        kp = static_cast<const char*>(a.c.k) + head;
+        vp = static_cast<const char*>(a.c.v) + head;
+        kv = p.kv;
+        nsteps = p.t1 - p.t0;
+        first = p.t0 * C::BN + warp * KT;                  // keys (t C::BN + warp KT) of the part's tiles t
+        pid = nsteps > 0 ? page_at(a.c, trow, first + lane, kv) : -1;
+        pid1 = nsteps > 1 ? page_at(a.c, trow, first + C::BN + lane, kv) : -1;
+#pragma unroll 1
+        for (int j = 0; j < kStages - 1; ++j) issue(j);
+    };
+    // Warp 0 finds the CTA's parts, one ahead.
     PagedWalk walk;
-    PagedSeg g;
     int turn = 0;
     if (warp == 0) {
+        PagedSeg n;
         paged_locate_warp(a, blockIdx.x, walk, blockIdx.x == 0);
         if (lane < 2) a.part_info[blockIdx.x * 2 + lane] = make_int4(0, 0, 0, 0);
-        if (!walk.next(a, g)) g.b = -1;
-        if (lane == 0) s_part[0] = g;
+        if (!walk.next(a, n)) n.b = -1;
+        if (lane == 0) s_part[0] = n;
     }
-    while (true) {
-        __syncthreads();                                   // the part is there, the rings are free
-        g = s_part[turn & 1];
-        ++turn;
-        if (g.b < 0) break;
-        const int hs = a.G > a.p.gs ? g.hg % ((a.G + a.p.gs - 1) / a.p.gs) : 0;
-        const int hkv = a.G > a.p.gs ? g.hg / ((a.G + a.p.gs - 1) / a.p.gs) : g.hg;
-        const int h0 = hkv * a.G + hs * a.p.gs;            // first query head of the unit
-        const int gs = min(a.p.gs, a.G - hs * a.p.gs);     // its heads
+    __syncthreads();
+    PagedSeg g = s_part[0];
+    if (PRE && g.b >= 0) begin(g);
+    while (g.b >= 0) {
+        const int h0 = (g.hg / ngrp) * a.G + (g.hg % ngrp) * a.p.gs;   // first query head of the unit
+        const int gs = min(a.p.gs, a.G - (g.hg % ngrp) * a.p.gs);      // its heads
         const int live_rows = g.ntok * gs;
-        const int* trow = a.s.table + (size_t)g.b * a.s.W;
-        const char* kp = static_cast<const char*>(a.c.k) + (long long)hkv * a.c.head_stride * 2;
-        const char* vp = static_cast<const char*>(a.c.v) + (long long)hkv * a.c.head_stride * 2;
 
         // The unit's query rows as A fragments, from global memory.
         uint32_t qf[MT][D / 16][4];
@@ -131,31 +158,21 @@ __global__ void __launch_bounds__(kThreads, 2) paged_short_kernel(const PagedAtt
                 for (int e = 0; e < 4; ++e) o[m][n][e] = 0.f;
         }
 
-        // Steps of this warp: keys (t C::BN + warp KT) of the part's tiles t.
-        const int nsteps = g.t1 - g.t0;
-        const int first = g.t0 * C::BN + warp * KT;
-        // Page ids are fetched two steps ahead of the copies that need them, which run two steps
-        // ahead of the products.
-        int pid = page_at(a.c, trow, first + lane, g.kv);
-        int pid1 = nsteps > 1 ? page_at(a.c, trow, first + C::BN + lane, g.kv) : -1;
+        ++turn;
+        if (warp == 0) {
+            PagedSeg n;
+            if (!walk.next(a, n)) n.b = -1;
+            if (lane == 0) s_part[turn & 1] = n;
+        }
+        __syncthreads();                                   // the next part is known, the join before has been read
+        if (!PRE) begin(g);
 #pragma unroll 1
-        for (int j = 1 - kStages; j < nsteps; ++j) {
+        for (int j = 0; j < nsteps; ++j) {
             __syncwarp();                                  // step j - 1 has been read by the whole warp
-            const int jn = j + kStages - 1;                // into the stage of step j - 1
-            if (jn < nsteps) {
-                const int at = first + jn * C::BN;
-                const int pid2 = jn + 2 < nsteps ? page_at(a.c, trow, at + 2 * C::BN + lane, g.kv) : -1;
-                const uint32_t st = ring0 + (jn % kStages) * 2 * C::TILE;
-                load_rows<KT, U>(st, st + C::TILE, kp, vp, a.c, 2, 0, at, g.kv,
-                                 checked_page(a.c, pid, at + lane, g.kv, a.err), lane);
-                pid = pid1;
-                pid1 = pid2;
-            }
-            cp_async_commit();
-            if (j < 0) continue;
+            issue(j + kStages - 1);                        // into its stage
             cp_async_wait<kStages - 1>();
             __syncwarp();                                  // step j has landed for the whole warp
-            const uint32_t sk = ring0 + (j % kStages) * 2 * C::TILE, sv = sk + C::TILE;
+            const uint32_t sk = ring0 + ((s0 + j) % kStages) * 2 * C::TILE, sv = sk + C::TILE;
             const int k0 = first + j * C::BN;
 
             float s[MT][NT][4];
@@ -248,15 +265,23 @@ __global__ void __launch_bounds__(kThreads, 2) paged_short_kernel(const PagedAtt
                 }
             }
         }
-        cp_async_wait<0>();
-
-        if (warp == 0) {
-            PagedSeg n;
-            if (!walk.next(a, n)) n.b = -1;
-            if (lane == 0) s_part[turn & 1] = n;
+        // The next part's first steps go out before this one is joined: they take the two stages
+        // that the last step did not use.  The join takes that one (PRE), or all rings.
+        const int last = (s0 + nsteps + kStages - 1) % kStages;
+        const PagedSeg next = s_part[turn & 1];
+        if (PRE) {
+            __syncwarp();
+            if (next.b >= 0) {
+                s0 = (s0 + nsteps) % kStages;
+                begin(next);
+            }
+        } else {
+            cp_async_wait<0>();
+            __syncthreads();                               // every ring is idle
         }
+        float* const s_o = reinterpret_cast<float*>(PRE ? ring + last * 2 * C::TILE : ring);
+        constexpr int S_O = (PRE ? C::RING : 16 * MT * D * 4) / 4;     // from one warp's rows [16 MT][D] to the next's
 
-        // Join the four warps: their outputs take the place of the rings.
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -269,15 +294,13 @@ __global__ void __launch_bounds__(kThreads, 2) paged_short_kernel(const PagedAtt
                     s_l[warp][m * 16 + g8 + 8 * i] = x;
                 }
             }
-        __syncthreads();                                   // every ring is idle
-        float* s_o = reinterpret_cast<float*>(ring);       // [kWarps][16 MT][D]
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int n = 0; n < NO; ++n)
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
-                    *reinterpret_cast<float2*>(s_o + ((size_t)(warp * 16 * MT + m * 16 + g8 + 8 * i)) * D + n * 8 + t4 * 2) =
+                    *reinterpret_cast<float2*>(s_o + warp * S_O + (m * 16 + g8 + 8 * i) * D + n * 8 + t4 * 2) =
                         make_float2(o[m][n][2 * i], o[m][n][2 * i + 1]);
         __syncthreads();
         const int pslot = blockIdx.x * 2 + g.slot();
@@ -292,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_short_kernel(const PagedAtt
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 const float wt = ex2(s_m[w][row] - ref);
-                const float4 x = *reinterpret_cast<const float4*>(s_o + (size_t)(w * 16 * MT + row) * D + e);
+                const float4 x = *reinterpret_cast<const float4*>(s_o + w * S_O + row * D + e);
                 l += s_l[w][row] * wt;
                 acc.x += x.x * wt;
                 acc.y += x.y * wt;
@@ -312,6 +335,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_short_kernel(const PagedAtt
             }
         }
         if (!g.whole() && tid == 0) a.part_info[pslot] = paged_record(g);
+        g = next;
     }
 }
 
