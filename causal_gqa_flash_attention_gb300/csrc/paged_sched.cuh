@@ -32,23 +32,29 @@ struct PagedSeq {
     int tok0, n, len;
 };
 
-// Row range and length of sequence b, clamped to what the tensors hold; `bad` collects
-// which argument was out of range.
-__device__ __forceinline__ PagedSeq paged_seq(const PagedBatch& s, int b, int& bad) {
+// Row offsets and length of sequence b as they stand in memory.
+struct PagedRaw {
+    int c0, c1, l;
+};
+__device__ __forceinline__ PagedRaw paged_raw(const PagedBatch& s, int b) {
+    PagedRaw r;
+    r.c0 = s.cu ? __ldg(s.cu + b) : b;
+    r.c1 = s.cu ? __ldg(s.cu + b + 1) : b + 1;
+    r.l = __ldg(s.lens + b);
+    return r;
+}
+// The same, clamped to what the tensors hold; `bad` collects which argument was out of range.
+__device__ __forceinline__ PagedSeq paged_clamp(const PagedBatch& s, const PagedRaw& r, int& bad) {
     PagedSeq q;
-    if (s.cu) {
-        const int c0 = __ldg(s.cu + b), c1 = __ldg(s.cu + b + 1);
-        if (c0 < 0 || c1 > s.N || c1 < c0) bad = SITE_PAGED_CU;
-        q.tok0 = min(max(c0, 0), s.N);
-        q.n = min(max(c1, q.tok0), s.N) - q.tok0;
-    } else {
-        q.tok0 = b;
-        q.n = 1;
-    }
-    const int l = __ldg(s.lens + b);
-    if (l < 0 || l > s.cap) bad = SITE_PAGED_LEN;
-    q.len = min(max(l, 0), s.cap);
+    if (r.c0 < 0 || r.c1 > s.N || r.c1 < r.c0) bad = SITE_PAGED_CU;
+    q.tok0 = min(max(r.c0, 0), s.N);
+    q.n = min(max(r.c1, q.tok0), s.N) - q.tok0;
+    if (r.l < 0 || r.l > s.cap) bad = SITE_PAGED_LEN;
+    q.len = min(max(r.l, 0), s.cap);
     return q;
+}
+__device__ __forceinline__ PagedSeq paged_seq(const PagedBatch& s, int b, int& bad) {
+    return paged_clamp(s, paged_raw(s, b), bad);
 }
 
 // Cost of tiles 0 .. r-1 of a sequence (r below its tile count, so they are full): each
@@ -93,12 +99,22 @@ struct PagedWalk {
     long long w0, w1;   // the CTA's interval
     long long cur;      // start of the current unit
     PagedSeq q;
+    PagedRaw ahead;     // the next sequence's, fetched while this one is walked
     int b, hg, r, nt;
 
-    __device__ __forceinline__ void load(const PagedAttnArgs& a) {
+    __device__ __forceinline__ void fetch(const PagedAttnArgs& a) {
+        if (b + 1 < a.s.B) ahead = paged_raw(a.s, b + 1);
+    }
+    // Sequence b, whose values were fetched ahead.
+    __device__ __forceinline__ void take(const PagedAttnArgs& a) {
         int bad = 0;
-        q = paged_seq(a.s, b, bad);
+        q = paged_clamp(a.s, ahead, bad);
         nt = paged_tiles(q.n, a.p);
+        fetch(a);
+    }
+    __device__ __forceinline__ void load(const PagedAttnArgs& a) {
+        ahead = paged_raw(a.s, b);
+        take(a);
     }
     // From the sequence that holds w0 (q, set by the caller or by load) and where it starts.
     __device__ __forceinline__ void init(const PagedAttnArgs& a, long long w0_, long long w1_, int b_, long long start,
@@ -111,8 +127,12 @@ struct PagedWalk {
             cur = w1;
             return;
         }
-        if (loaded) nt = paged_tiles(q.n, a.p);
-        else load(a);
+        if (loaded) {
+            nt = paged_tiles(q.n, a.p);
+            fetch(a);
+        } else {
+            load(a);
+        }
         const long long S = paged_group_cost(q, a.p);
         const long long off = w0 - start;
         hg = (int)paged_div(off, S);
@@ -159,7 +179,7 @@ struct PagedWalk {
                 if (++hg == a.p.hg) {
                     hg = 0;
                     do ++b;
-                    while (b < a.s.B && (load(a), q.n == 0));
+                    while (b < a.s.B && (take(a), q.n == 0));
                     if (b >= a.s.B) cur = w1 > cur ? w1 : cur;         // (the line ends here)
                 }
             }

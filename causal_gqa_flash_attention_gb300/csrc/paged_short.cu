@@ -93,6 +93,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_short_kernel(const PagedAtt
         }
         cp_async_commit();
     };
+    uint32_t qf[MT][D / 16][4];                            // the part's query rows as A fragments
+    int lim[MT][2];                                        // keys that rows g8 and g8 + 8 see
     auto begin = [&](const PagedSeg& p) {
         const long long head = (long long)(p.hg / ngrp) * a.c.head_stride * 2;
         trow = a.s.table + (size_t)p.b * a.s.W;
@@ -105,6 +107,24 @@ __global__ void __launch_bounds__(kThreads, 2) paged_short_kernel(const PagedAtt
         pid1 = nsteps > 1 ? page_at(a.c, trow, first + C::BN + lane, kv) : -1;
 #pragma unroll 1
         for (int j = 0; j < kStages - 1; ++j) issue(j);
+        const int h0 = (p.hg / ngrp) * a.G + (p.hg % ngrp) * a.p.gs;   // first query head of the unit
+        const int gs = min(a.p.gs, a.G - (p.hg % ngrp) * a.p.gs);      // its heads
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int row = m * 16 + g8 + 8 * i;
+                const bool live = row < p.ntok * gs;
+                const int tok = live ? row / gs : 0, h = live ? row - tok * gs : 0;
+                lim[m][i] = live ? p.base + p.tok + tok + 1 : 0;
+                const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) +
+                                           (long long)(p.tok0 + p.tok + tok) * a.q_ld + (long long)(h0 + h) * D;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    qf[m][ks][i] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + ks * 16 + t4 * 2)) : 0u;
+                    qf[m][ks][2 + i] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + ks * 16 + 8 + t4 * 2)) : 0u;
+                }
+            }
     };
     // Warp 0 finds the CTA's parts, one ahead.
     PagedWalk walk;
@@ -123,26 +143,6 @@ __global__ void __launch_bounds__(kThreads, 2) paged_short_kernel(const PagedAtt
         const int h0 = (g.hg / ngrp) * a.G + (g.hg % ngrp) * a.p.gs;   // first query head of the unit
         const int gs = min(a.p.gs, a.G - (g.hg % ngrp) * a.p.gs);      // its heads
         const int live_rows = g.ntok * gs;
-
-        // The unit's query rows as A fragments, from global memory.
-        uint32_t qf[MT][D / 16][4];
-        int lim[MT][2];                                    // keys that rows g8 and g8 + 8 see
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int row = m * 16 + g8 + 8 * i;
-                const bool live = row < live_rows;
-                const int tok = live ? row / gs : 0, h = live ? row % gs : 0;
-                lim[m][i] = live ? g.base + g.tok + tok + 1 : 0;
-                const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) +
-                                           (long long)(g.tok0 + g.tok + tok) * a.q_ld + (long long)(h0 + h) * D;
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    qf[m][ks][i] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + ks * 16 + t4 * 2)) : 0u;
-                    qf[m][ks][2 + i] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + ks * 16 + 8 + t4 * 2)) : 0u;
-                }
-            }
 
         float mx[MT][2], sum[MT][2], o[MT][NO][4];
 #pragma unroll
