@@ -66,6 +66,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_short_kernel(const PagedAtt
     constexpr int KT = C::KT, U = C::U, NT = KT / 8, NO = D / 8;
     constexpr bool PRE = 16 * MT * D * 4 <= 2 * C::TILE;   // a warp's output fits into one stage
     extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ PagedLocate loc;
     __shared__ PagedSeg s_part[2];                         // the CTA's parts in turn (b < 0: the end)
     __shared__ float s_m[kWarps][16 * MT], s_l[kWarps][16 * MT];
 
@@ -126,12 +127,15 @@ __global__ void __launch_bounds__(kThreads, 2) paged_short_kernel(const PagedAtt
                 }
             }
     };
-    // Warp 0 finds the CTA's parts, one ahead.
+    // Warp 0 finds the CTA's parts, one ahead; where its share begins, it finds alone among up to
+    // 32 sequences, and the whole CTA among more (256 sequences: 29.7 us a call instead of 32.7).
     PagedWalk walk;
     int turn = 0;
+    if (a.s.B > 32) paged_locate<kThreads>(a, blockIdx.x, loc, blockIdx.x == 0);
     if (warp == 0) {
         PagedSeg n;
-        paged_locate_warp(a, blockIdx.x, walk, blockIdx.x == 0);
+        if (a.s.B <= 32) paged_locate_warp(a, blockIdx.x, walk, blockIdx.x == 0);
+        else walk.init(a, loc.w0, loc.w1, loc.b, loc.start);
         if (lane < 2) a.part_info[blockIdx.x * 2 + lane] = make_int4(0, 0, 0, 0);
         if (!walk.next(a, n)) n.b = -1;
         if (lane == 0) s_part[0] = n;
