@@ -8,6 +8,9 @@
 // its heads.  Bound: every row is read once and written once, 2 (Hq + 2 Hkv) D elements
 // per token at the copy bandwidth; a step of a few tokens is latency (find the token's
 // sequence, its page, then one load and one store).
+// Measured (GB300): 6250 tokens, 16 + 2 x 4 heads of 128, half of each head rotated: 17.8 us,
+// 4.3 TB/s (64% of the copy rate; 40% of the issue slots, the rest the latency of the lookups);
+// 16 tokens of 12 + 2 x 4 heads of 64: 3.6 us.
 #include <cuda_bf16.h>
 #include "paged_sched.cuh"
 

@@ -10,6 +10,10 @@
 // O: lane = two (or one) elements of D, the weights broadcast.  FEW: four warps take
 // interleaved 32-key steps of the same 4 or 8 rows, each with a private ring, and are joined at
 // the end of a unit.  MANY: eight warps take 8 of 64 rows each over one shared ring.
+//
+// Measured (GB300): one step over 8 x 16384 positions, 12/4 heads of 64: 60 us, 4.5 TB/s (one
+// CTA of four warps per SM: its rings fill the shared memory, so latency shows); 512 new tokens
+// over 4096 positions, 12/4 heads of 64: 211 us, 28 TFLOP/s of the 75 that fp32 FMAs give.
 #include "paged_load.cuh"
 #include "paged_sched.cuh"
 
