@@ -474,8 +474,8 @@ def paged_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_new=None, rope
     if q is not None:
         Hq = q.shape[1]
         q_ld = _rows(q, "q", N, Hq, D, dt, dev)
-        if q_out is None:
-            q_out = torch.zeros((N, Hq, D), dtype=dt, device=dev)
+        if q_out is None:                                  # (without cu_new every row is written)
+            q_out = (torch.empty if cu_new is None else torch.zeros)((N, Hq, D), dtype=dt, device=dev)
         qo_ld = _rows(q_out, "q_out", N, Hq, D, dt, dev)
         qp, qop = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
@@ -508,12 +508,13 @@ def paged_attn(q, k_pages, v_pages, page_table, seq_lens, cu_new=None, max_new: 
     N, Hq = q.shape[:2]
     B, W, pt, ln, cu = _paged_batch(page_table, seq_lens, cu_new, N, dev)
     q_ld = _rows(q, "q", N, Hq, D, dt, dev)
+    new = torch.empty if cu_new is None else torch.zeros   # (without cu_new every row is written)
     if o is None:
-        o = torch.zeros((N, Hq, D), dtype=dt, device=dev)
+        o = new((N, Hq, D), dtype=dt, device=dev)
     elif o.shape != q.shape or o.dtype is not dt or o.device != dev or not o.is_contiguous():
         raise ValueError("o must be contiguous and match q")
     if lse is None:
-        lse = torch.zeros((N, Hq), dtype=torch.float32, device=dev)
+        lse = new((N, Hq), dtype=torch.float32, device=dev)
     elif lse.shape != (N, Hq) or lse.dtype is not torch.float32 or lse.device != dev or not lse.is_contiguous():
         raise ValueError("lse must be contiguous fp32 [N, Hq]")
     if workspace is None:

@@ -293,7 +293,8 @@ __device__ __forceinline__ void paged_locate_warp(const PagedAttnArgs& a, int c,
     long long mine = work(lane), total = mine;
 #pragma unroll 1
     for (int b0 = 32; b0 < B; b0 += 32) total += work(b0 + lane);
-    // The sum over the warp in three limbs of 21 bits, one reduction each (total is below 2^58).
+    // The sum over the warp in three limbs of 21 bits, one reduction each (units times 5 x 2^30
+    // keys: below 2^60).
     const unsigned l0 = __reduce_add_sync(0xffffffffu, (unsigned)total & 0x1fffffu);
     const unsigned l1 = __reduce_add_sync(0xffffffffu, (unsigned)(total >> 21) & 0x1fffffu);
     const unsigned l2 = __reduce_add_sync(0xffffffffu, (unsigned)(total >> 42));

@@ -61,7 +61,7 @@ struct TileCfg {
     static constexpr bool SEP = D == 64;
     static constexpr int P_COL = SEP ? O_COL + 2 * D : 0;  // P_u at P_COL + u P_STEP
     static constexpr int P_STEP = SEP ? 64 : 128;
-    static_assert(SMEM + 1536 <= 227 * 1024, "shared memory");
+    static_assert(SMEM + 1536 <= 227 * 1024, "shared memory (with the static part)");
 };
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2) {
@@ -114,6 +114,7 @@ __global__ void __launch_bounds__(384, 1)
     __shared__ __align__(8) uint64_t bar_full[C::NS], bar_empty[C::NS];
     __shared__ __align__(8) uint64_t bar_s_full[2], bar_p_ready[2], bar_o_full[2], bar_s_free[2];
     __shared__ __align__(8) uint64_t bar_seg_full[kSegs], bar_seg_empty[kSegs];
+    __shared__ PagedLocate loc;
     __shared__ PagedSeg s_seg[kSegs];                      // the CTA's parts in order (b < 0: the end)
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
@@ -172,6 +173,8 @@ __global__ void __launch_bounds__(384, 1)
         if (lane == 0) mbar_arrive(smem_u32(&bar_seg_empty[s]));
         return g.b >= 0;
     };
+    // Where the CTA's share begins, warp 3 finds alone among up to 32 sequences, all warps among more.
+    if (a.s.B > 32) paged_locate<C::THREADS>(a, blockIdx.x, loc, blockIdx.x == 0);
     // A part's K tile t sits at ring index 2 i, its V tile at 2 i + 1, i counting the CTA's tiles.
 
     if (warp == 0) {
@@ -362,7 +365,8 @@ __global__ void __launch_bounds__(384, 1)
         // ------------------------------------------------------------ the CTA's parts
         if (lane < 2) a.part_info[blockIdx.x * 2 + lane] = make_int4(0, 0, 0, 0);
         PagedWalk walk;
-        paged_locate_warp(a, blockIdx.x, walk, blockIdx.x == 0);
+        if (a.s.B <= 32) paged_locate_warp(a, blockIdx.x, walk, blockIdx.x == 0);
+        else walk.init(a, loc.w0, loc.w1, loc.b, loc.start);
         bool more = true;
         for (int k = 0; more; ++k) {
             const int s = k % kSegs;

@@ -164,7 +164,32 @@ CHUNKS = [
     (71, 1, 64, 64, [3, 5], [500, 5]),
     (12, 4, 64, 256, [600], [600]),
     (40, 1, 128, 16, [19, 2], [400, 1111]),
+    (130, 1, 64, 32, [2, 3], [300, 3]),                            # more heads than a tile has rows
+    (12, 4, 64, 8, [300, 1], [555, 130]),                          # sixteen pages to a tile
 ]
+
+
+@pytest.mark.parametrize("dtype,D", [(BF16, 64), (BF16, 128), (F32, 64)])
+@pytest.mark.parametrize("ps", [8, 64, 256])
+def test_attn_head_major_pages(dtype, D, ps):
+    for mn in (1, None):
+        attn_case(dtype, 12, 4, D, ps, [70, 1, 5], [333, 500, 5], 87, hnd=True, max_new=mn)
+
+
+@pytest.mark.parametrize("dtype,n,max_new", [(BF16, 1, 1), (BF16, 16, None), (F32, 1, 1), (F32, 16, None)])
+def test_attn_one_unit_over_many_ctas(dtype, n, max_new):
+    """One kv head and few rows: a single unit is cut into dozens or hundreds of parts."""
+    attn_case(dtype, 4, 1, 64, 64, [n], [40003], 95, max_new=max_new)
+
+
+def test_attn_many_sequences_of_chunks():
+    """More sequences than one warp looks through at once, for the tile kernel."""
+    rng = random.Random(5)
+    lens = [rng.choice([0, 1, rng.randint(1, 300)]) for _ in range(460)]
+    n = [rng.choice([0, 1, min(x, 20)]) if x else 0 for x in lens]
+    for D in (64, 128):
+        attn_case(BF16, 4, 2, D, 16, n, lens, 97, max_new=None, tail=1)
+    attn_case(F32, 4, 2, 64, 16, n, lens, 98, max_new=None, tail=1)
 
 
 def test_attn_contexts_too_short_to_cut():
