@@ -381,16 +381,21 @@ def rope_spec(D: int, rot_dim: int | None = None, theta: float = 10000.0, layout
 
 
 # A generation step is a few small kernels, so these bindings keep the host's share low:
-# plain comparisons, addresses as integers, and no stream object (the current stream's
-# handle is all the C calls take).
+# plain comparisons, devices by index, addresses as integers, and no stream object (the
+# current stream's handle is all the C calls take).
+
+_I32, _BF16, _F32 = torch.int32, torch.bfloat16, torch.float32
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
+
 
 def _launch(fn, index, *args):
     """Calls fn with the device's current stream as last argument, on that device."""
-    if torch._C._cuda_getDevice() == index:
-        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if _current_device() == index:
+        status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
-            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+            status = fn(*args, _raw_stream(index))
     if status != NE_OK:
         _check(status)
 
@@ -401,54 +406,62 @@ assert _CACHE.size == ctypes.sizeof(PagedCache)
 
 def _paged_cache(k_pages, v_pages, layers: bool):
     """The pools [P, page_size, Hkv, D] ([L, P, page_size, Hkv, D] with `layers`) as the C
-    struct (bytes), their dtype, pages, heads and head_dim.  Any strides in multiples of 16
-    bytes with D dense (head-major pages are a transposed view), the same for both."""
-    shape, st, dt = k_pages.shape, k_pages.stride(), k_pages.dtype
+    struct (bytes), their device index, dtype, pages, heads and head_dim.  Any strides in
+    multiples of 16 bytes with D dense (head-major pages are a transposed view), the same
+    for both."""
+    shape, st, dt, dev = k_pages.shape, k_pages.stride(), k_pages.dtype, k_pages.get_device()
     nd = len(shape)
-    if nd not in ((4, 5) if layers else (4,)) or v_pages.shape != shape:
+    if nd == 4:
+        P, ps, H, D = shape
+        sp, stk, sh, sd = st
+        L, ls = 1, 0
+    elif nd == 5 and layers:
+        L, P, ps, H, D = shape
+        ls, sp, stk, sh, sd = st
+    else:
+        nd = 0
+    if nd == 0 or v_pages.shape != shape:
         raise ValueError(f"k_pages and v_pages must be [{'L, ' if layers else ''}P, page_size, Hkv, D]; got "
                          f"{tuple(shape)}, {tuple(v_pages.shape)}")
-    if not k_pages.is_cuda or v_pages.device != k_pages.device:
+    if dev < 0 or v_pages.get_device() != dev:
         raise ValueError("k_pages and v_pages must be CUDA tensors on one device")
-    if (dt is not torch.bfloat16 and dt is not torch.float32) or v_pages.dtype is not dt:
+    if (dt is not _BF16 and dt is not _F32) or v_pages.dtype is not dt:
         raise ValueError("k_pages and v_pages must both be bfloat16 or float32")
-    if v_pages.stride() != st or st[-1] != 1:
+    if sd != 1 or v_pages.stride() != st:
         raise ValueError("k_pages and v_pages must have the same strides, D dense")
-    L, ls = (shape[0], st[0]) if nd == 5 else (1, 0)
-    P, ps, H, D = shape[-4:]
-    return _CACHE.pack(k_pages.data_ptr(), v_pages.data_ptr(), 2 if dt is torch.bfloat16 else 4, L, P, ps, H, D, ls,
-                       st[-4], st[-3], st[-2]), dt, P, H, D
+    return _CACHE.pack(k_pages.data_ptr(), v_pages.data_ptr(), 2 if dt is _BF16 else 4, L, P, ps, H, D, ls, sp, stk,
+                       sh), dev, dt, P, H, D
 
 
-def _ws(t, device):
+def _ws(t, dev):
     """Address and bytes of a workspace."""
-    if t.device != device or not t.is_contiguous():
+    if t.get_device() != dev or not t.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor on the pages' device")
     return t.data_ptr(), t.nbytes
 
 
-def _ints(t, shape, device, name):
+def _ints(t, shape, dev, name):
     """Address of an int32 tensor of that shape."""
-    if t.dtype is not torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor {list(shape)} on the pages' device")
-    return t.data_ptr()
+    if t.dtype is _I32 and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous int32 CUDA tensor {list(shape)} on the pages' device")
 
 
-def _paged_batch(page_table, seq_lens, cu_new, N, device):
+def _paged_batch(page_table, seq_lens, cu_new, N, dev):
     """B, max_pages and the addresses of page_table, seq_lens and cu_new (0: one row each)."""
     shape = page_table.shape
     if len(shape) != 2:
         raise ValueError("page_table must be [B, max_pages]")
-    B = shape[0]
+    B, W = shape
     if cu_new is None and N != B:
         raise ValueError(f"without cu_new every sequence has one row: {N} rows for {B} sequences")
-    return (B, shape[1], _ints(page_table, shape, device, "page_table"), _ints(seq_lens, (B,), device, "seq_lens"),
-            0 if cu_new is None else _ints(cu_new, (B + 1,), device, "cu_new"))
+    return (B, W, _ints(page_table, shape, dev, "page_table"), _ints(seq_lens, (B,), dev, "seq_lens"),
+            0 if cu_new is None else _ints(cu_new, (B + 1,), dev, "cu_new"))
 
 
-def _rows(t, name, N, heads, D, dtype, device):
+def _rows(t, name, N, heads, D, dtype, dev):
     """Row stride of a [N, heads, D] tensor whose rows are dense."""
-    if t.shape != (N, heads, D) or t.dtype is not dtype or t.device != device:
+    if t.shape != (N, heads, D) or t.dtype is not dtype or t.get_device() != dev:
         raise ValueError(f"{name} must be a {[N, heads, D]} {dtype} tensor on the pages' device; got "
                          f"{tuple(t.shape)} {t.dtype}")
     s0, s1, s2 = t.stride()
@@ -465,8 +478,7 @@ def paged_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_new=None, rope
     not).  With q [N, Hq, D] the query rows are rotated into q_out (which may be q), returned.
     Row slices of one fused projection are taken as they are."""
     lib = _lib or load()
-    c, dt, P, Hkv, D = _paged_cache(k_pages, v_pages, False)
-    dev = k_pages.device
+    c, dev, dt, _, Hkv, D = _paged_cache(k_pages, v_pages, False)
     N = k.shape[0]
     B, W, pt, ln, cu = _paged_batch(page_table, seq_lens, cu_new, N, dev)
     k_ld, v_ld = _rows(k, "k", N, Hkv, D, dt, dev), _rows(v, "v", N, Hkv, D, dt, dev)
@@ -475,12 +487,12 @@ def paged_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_new=None, rope
         Hq = q.shape[1]
         q_ld = _rows(q, "q", N, Hq, D, dt, dev)
         if q_out is None:                                  # (without cu_new every row is written)
-            q_out = (torch.empty if cu_new is None else torch.zeros)((N, Hq, D), dtype=dt, device=dev)
+            q_out = (torch.empty if cu_new is None else torch.zeros)((N, Hq, D), dtype=dt, device=k_pages.device)
         qo_ld = _rows(q_out, "q_out", N, Hq, D, dt, dev)
         qp, qop = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out needs q")
-    _launch(lib.ne_paged_append if dt is torch.bfloat16 else lib.ne_paged_append_f32, dev.index, qp, k.data_ptr(), v.data_ptr(),
+    _launch(lib.ne_paged_append if dt is _BF16 else lib.ne_paged_append_f32, dev, qp, k.data_ptr(), v.data_ptr(),
             c, pt, ln, cu, ctypes.byref(rope) if rope is not None else None, pos_offset, qop, q_ld, k_ld, v_ld,
             qo_ld, B, N, Hq, W)
     return q_out
@@ -503,23 +515,22 @@ def paged_attn(q, k_pages, v_pages, page_table, seq_lens, cu_new=None, max_new: 
     outside the sequences are not written (zeros in a fresh o and lse).  max_new: the most
     new tokens of a sequence, if known (a choice of kernel, not of results)."""
     lib = _lib or load()
-    c, dt, P, Hkv, D = _paged_cache(k_pages, v_pages, False)
-    dev = k_pages.device
+    c, dev, dt, _, Hkv, D = _paged_cache(k_pages, v_pages, False)
     N, Hq = q.shape[:2]
     B, W, pt, ln, cu = _paged_batch(page_table, seq_lens, cu_new, N, dev)
     q_ld = _rows(q, "q", N, Hq, D, dt, dev)
     new = torch.empty if cu_new is None else torch.zeros   # (without cu_new every row is written)
     if o is None:
-        o = new((N, Hq, D), dtype=dt, device=dev)
-    elif o.shape != q.shape or o.dtype is not dt or o.device != dev or not o.is_contiguous():
+        o = new((N, Hq, D), dtype=dt, device=k_pages.device)
+    elif o.shape != q.shape or o.dtype is not dt or o.get_device() != dev or not o.is_contiguous():
         raise ValueError("o must be contiguous and match q")
     if lse is None:
-        lse = new((N, Hq), dtype=torch.float32, device=dev)
-    elif lse.shape != (N, Hq) or lse.dtype is not torch.float32 or lse.device != dev or not lse.is_contiguous():
+        lse = new((N, Hq), dtype=torch.float32, device=k_pages.device)
+    elif lse.shape != (N, Hq) or lse.dtype is not torch.float32 or lse.get_device() != dev or not lse.is_contiguous():
         raise ValueError("lse must be contiguous fp32 [N, Hq]")
     if workspace is None:
-        workspace = alloc_paged_workspace(B, N, Hq, Hkv, D, dev)
-    _launch(lib.ne_paged_attn if dt is torch.bfloat16 else lib.ne_paged_attn_f32, dev.index, q.data_ptr(), c, pt,
+        workspace = alloc_paged_workspace(B, N, Hq, Hkv, D, k_pages.device)
+    _launch(lib.ne_paged_attn if dt is _BF16 else lib.ne_paged_attn_f32, dev, q.data_ptr(), c, pt,
             ln, cu, o.data_ptr(), lse.data_ptr(), q_ld, B, N, Hq, W, max(1, N) if max_new is None else max_new,
             *_ws(workspace, dev))
     return o, lse
@@ -531,12 +542,12 @@ def alloc_pages_workspace(n_pages: int, n: int, max_pages: int, device="cuda"):
                        device=device)
 
 
-def _out_ints(t, shape, device, name):
-    """An int32 output and its address: the caller's, or a new one."""
+def _out_ints(t, shape, dev, name, like):
+    """An int32 output and its address: the caller's, or a new one beside `like`."""
     if t is None:
-        t = torch.empty(shape, dtype=torch.int32, device=device)
+        t = torch.empty(shape, dtype=_I32, device=like.device)
         return t, t.data_ptr()
-    return t, _ints(t, shape, device, name)
+    return t, _ints(t, shape, dev, name)
 
 
 def pages_fork(refcount, page_table, seq_lens, parents, k_pages, v_pages, deep: bool = False, refcount_out=None,
@@ -547,19 +558,18 @@ def pages_fork(refcount, page_table, seq_lens, parents, k_pages, v_pages, deep: 
     [C, max_pages], child_lens [C], short [1]); short > 0: that many pages were missing and
     nothing changed.  refcount_out may be refcount."""
     lib = _lib or load()
-    c, dt, n_pages, _, _ = _paged_cache(k_pages, v_pages, True)
-    dev = k_pages.device
+    c, dev, _, n_pages, _, _ = _paged_cache(k_pages, v_pages, True)
     P = (n_pages,)
     if page_table.dim() != 2 or parents.dim() != 1:
         raise ValueError("page_table must be [B, max_pages] and parents [C]")
     B, W = page_table.shape
     C = parents.shape[0]
-    refcount_out, ro = _out_ints(refcount_out, P, dev, "refcount_out")
-    child_table, ct = _out_ints(child_table, (C, W), dev, "child_table")
-    child_lens, cl = _out_ints(child_lens, (C,), dev, "child_lens")
-    short, sh = _out_ints(short, (1,), dev, "short")
-    workspace = alloc_pages_workspace(n_pages, C, W, dev) if workspace is None else workspace
-    _launch(lib.ne_pages_fork, dev.index, c, _ints(refcount, P, dev, "refcount"),
+    refcount_out, ro = _out_ints(refcount_out, P, dev, "refcount_out", k_pages)
+    child_table, ct = _out_ints(child_table, (C, W), dev, "child_table", k_pages)
+    child_lens, cl = _out_ints(child_lens, (C,), dev, "child_lens", k_pages)
+    short, sh = _out_ints(short, (1,), dev, "short", k_pages)
+    workspace = alloc_pages_workspace(n_pages, C, W, k_pages.device) if workspace is None else workspace
+    _launch(lib.ne_pages_fork, dev, c, _ints(refcount, P, dev, "refcount"),
             _ints(page_table, (B, W), dev, "page_table"), _ints(seq_lens, (B,), dev, "seq_lens"),
             _ints(parents, (C,), dev, "parents"), 1 if deep else 0, ro, ct, cl, sh, B, C, W, *_ws(workspace, dev))
     return refcount_out, child_table, child_lens, short
@@ -572,17 +582,16 @@ def pages_resize(refcount, page_table, seq_lens, new_lens, k_pages, v_pages, ref
     taken, lowest free ids first.  Returns (refcount_out, table_out, short [1]); short > 0:
     that many pages were missing and nothing changed.  Both outputs may be the inputs."""
     lib = _lib or load()
-    c, dt, n_pages, _, _ = _paged_cache(k_pages, v_pages, True)
-    dev = k_pages.device
+    c, dev, _, n_pages, _, _ = _paged_cache(k_pages, v_pages, True)
     P, T = (n_pages,), page_table.shape
     if len(T) != 2:
         raise ValueError("page_table must be [B, max_pages]")
     B, W = T
-    refcount_out, ro = _out_ints(refcount_out, P, dev, "refcount_out")
-    table_out, to = _out_ints(table_out, T, dev, "table_out")
-    short, sh = _out_ints(short, (1,), dev, "short")
-    workspace = alloc_pages_workspace(n_pages, B, W, dev) if workspace is None else workspace
-    _launch(lib.ne_pages_resize, dev.index, c, _ints(refcount, P, dev, "refcount"),
+    refcount_out, ro = _out_ints(refcount_out, P, dev, "refcount_out", k_pages)
+    table_out, to = _out_ints(table_out, T, dev, "table_out", k_pages)
+    short, sh = _out_ints(short, (1,), dev, "short", k_pages)
+    workspace = alloc_pages_workspace(n_pages, B, W, k_pages.device) if workspace is None else workspace
+    _launch(lib.ne_pages_resize, dev, c, _ints(refcount, P, dev, "refcount"),
             _ints(page_table, T, dev, "page_table"), _ints(seq_lens, (B,), dev, "seq_lens"),
             _ints(new_lens, (B,), dev, "new_lens"), ro, to, sh, B, W,
             *_ws(workspace, dev))
@@ -595,18 +604,17 @@ def pages_compact(refcount, page_table, k_pages, v_pages, refcount_out=None, tab
     table_out, remap [P]: new id of every live page, -1 for free ones, n_live [1]).  Both
     outputs may be the inputs; further tables go through remap."""
     lib = _lib or load()
-    c, dt, n_pages, _, _ = _paged_cache(k_pages, v_pages, True)
-    dev = k_pages.device
+    c, dev, _, n_pages, _, _ = _paged_cache(k_pages, v_pages, True)
     P, T = (n_pages,), page_table.shape
     if len(T) != 2:
         raise ValueError("page_table must be [B, max_pages]")
     B, W = T
-    refcount_out, ro = _out_ints(refcount_out, P, dev, "refcount_out")
-    table_out, to = _out_ints(table_out, T, dev, "table_out")
-    remap, rm = _out_ints(remap, P, dev, "remap")
-    n_live, nl = _out_ints(n_live, (1,), dev, "n_live")
-    workspace = alloc_pages_workspace(n_pages, B, W, dev) if workspace is None else workspace
-    _launch(lib.ne_pages_compact, dev.index, c, _ints(refcount, P, dev, "refcount"),
+    refcount_out, ro = _out_ints(refcount_out, P, dev, "refcount_out", k_pages)
+    table_out, to = _out_ints(table_out, T, dev, "table_out", k_pages)
+    remap, rm = _out_ints(remap, P, dev, "remap", k_pages)
+    n_live, nl = _out_ints(n_live, (1,), dev, "n_live", k_pages)
+    workspace = alloc_pages_workspace(n_pages, B, W, k_pages.device) if workspace is None else workspace
+    _launch(lib.ne_pages_compact, dev, c, _ints(refcount, P, dev, "refcount"),
             _ints(page_table, T, dev, "page_table"), ro, to, rm, nl, B, W,
             *_ws(workspace, dev))
     return refcount_out, table_out, remap, n_live
