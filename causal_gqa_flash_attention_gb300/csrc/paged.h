@@ -37,7 +37,7 @@ struct AppendArgs {
     int Hq, Hkv, D;
     int rot, layout, pos_offset;      // rot 0: no rotation
     float mscale;
-    int tpc;                          // tokens per CTA
+    int wpt_shift;                    // log2 of the warps per token
     int vec_shift;                    // log2 of the 16-byte units of a head
     int* err;
 };

@@ -467,6 +467,15 @@ def test_append_shapes(Hq, Hkv, D, ps, n, lens, hnd):
     append_case(BF16, Hq, Hkv, D, ps, n, lens, 3 * D, hnd=hnd, layout="half" if hnd else "interleaved")
 
 
+@pytest.mark.parametrize("N", [600, 1100, 2400, 5000])     # eight, four, two warps and one to a token
+@pytest.mark.parametrize("dtype,Hq,Hkv,D,layout,rot,inplace", [
+    (F32, 3, 1, 64, "half", 48, True), (BF16, 5, 1, 32, "half", 16, False), (F32, 2, 2, 32, "interleaved", 30, True),
+    (BF16, 3, 3, 128, "half", 100, True)])
+def test_append_every_share_of_a_token(N, dtype, Hq, Hkv, D, layout, rot, inplace):
+    n = [N // 3, N - N // 3 - 1, 1]
+    append_case(dtype, Hq, Hkv, D, 16, n, [x + 11 for x in n], N, layout=layout, rot_dim=rot, inplace=inplace, tail=3)
+
+
 @pytest.mark.parametrize("rope", [dict(scaling="linear", factor=4.0), dict(scaling="base", factor=8.0, layout="half"),
                                   dict(scaling="parts", factor=8.0, orig_len=2048, mscale=1.2079441541679836),
                                   dict(theta=500000.0)])
