@@ -92,7 +92,7 @@ cudaError_t allow_smem(F kfn, int bytes, std::atomic<uint64_t>& done) {
 }
 
 // Which kernel a call runs, and its split.
-enum PagedKind : int { PAGED_SHORT16 = 0, PAGED_SHORT32, PAGED_F32_FEW4, PAGED_F32_FEW8, PAGED_F32_MANY, PAGED_TILES };
+enum PagedKind : int { PAGED_SHORT16 = 0, PAGED_SHORT32, PAGED_F32_FEW4, PAGED_F32_FEW8, PAGED_F32_FEW16, PAGED_F32_MANY, PAGED_TILES };
 PagedKind paged_kind(bool f32, int D, int G, int max_new);
 // cap: the longest length the page tables can hold.
 PagedSplit paged_split(PagedKind kind, int D, int Hkv, int G, int cap);

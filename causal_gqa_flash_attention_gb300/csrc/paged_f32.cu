@@ -7,13 +7,16 @@
 // bandwidth); many rows by the FMAs and the shared-memory reads that feed them.
 //
 // A warp holds RW query rows.  S: lane = key, the query rows broadcast from shared memory;
-// O: lane = two (or one) elements of D, the weights broadcast.  FEW: four warps take
-// interleaved 32-key steps of the same 4 or 8 rows, each with a private ring, and are joined at
-// the end of a unit.  MANY: eight warps take 8 of 64 rows each over one shared ring.
+// O: lane = two (or one) elements of D, the weights broadcast.  FEW (up to 32 rows per kv head):
+// eight warps take interleaved 32-key steps of the same 4, 8 or 16 rows, each with a private ring
+// of three K or V tiles, and are joined at the end of a unit.  MANY: eight warps take 8 of 64
+// rows each over one shared ring.
 //
-// Measured (GB300): one step over 8 x 16384 positions, 12/4 heads of 64: 60 us, 4.5 TB/s (one
-// CTA of four warps per SM: its rings fill the shared memory, so latency shows); 512 new tokens
-// over 4096 positions, 12/4 heads of 64: 211 us, 28 TFLOP/s of the 75 that fp32 FMAs give.
+// Measured (GB300): one step over 8 x 16384 positions, 12/4 heads of 64: 49 us, 5.5 TB/s; with
+// 32/4 heads 54 us; four new tokens each, 12/4 heads: 81 us (MANY would take 279: its warps
+// without rows wait); 512 new tokens over 4096 positions: 214 us, 28 TFLOP/s of the 75 that fp32
+// FMAs give.  Four warps with twice the keys in flight took 54, 64 and 99 us (a scheduler with
+// one warp waits for its chain), a ring of whole K and V steps 60, 89 and -.
 #include "paged_load.cuh"
 #include "paged_sched.cuh"
 
@@ -24,7 +27,7 @@ constexpr int kStages = 3;
 // RW: query rows per warp.
 template <int D, int RW, bool MANY>
 struct F32Cfg {
-    static constexpr int WK = MANY ? 1 : 4;                // warps along the keys
+    static constexpr int WK = MANY ? 1 : 8;                // warps along the keys
     static constexpr int WR = MANY ? 8 : 1;                // warps along the rows
     static constexpr int WARPS = WK * WR;
     static constexpr int THREADS = WARPS * 32;
@@ -32,16 +35,18 @@ struct F32Cfg {
     static constexpr int BN = 32 * WK;
     static constexpr int U = D / 4;                        // 16-byte units per row
     static constexpr int TILE = 32 * D * 4;                // one K or V step of 32 keys
-    static constexpr int RINGS = WK * kStages * 2 * TILE;
+    static constexpr int SLOTS = MANY ? 2 * kStages : 3;   // tiles of a ring
+    static constexpr int RINGS = WK * SLOTS * TILE;
     static constexpr int Q_BYTES = ROWS * D * 4;
     static constexpr int P_BYTES = WARPS * 32 * RW * 4;
     static constexpr int SMEM = RINGS + Q_BYTES + P_BYTES;
     static constexpr int DL = D / 32;                      // output elements per lane
+    static constexpr int CTAS = MANY || (D == 32 && RW < 16) ? 2 : 1;   // of an SM: what shared memory and registers hold
     static_assert(WK * ROWS * D * 4 <= RINGS, "the join fits into the rings");
 };
 
 template <int D, int RW, bool MANY>
-__global__ void __launch_bounds__(F32Cfg<D, RW, MANY>::THREADS) paged_f32_kernel(const PagedAttnArgs a) {
+__global__ void __launch_bounds__(F32Cfg<D, RW, MANY>::THREADS, F32Cfg<D, RW, MANY>::CTAS) paged_f32_kernel(const PagedAttnArgs a) {
     using C = F32Cfg<D, RW, MANY>;
     constexpr int U = C::U, DL = C::DL;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -54,13 +59,13 @@ __global__ void __launch_bounds__(F32Cfg<D, RW, MANY>::THREADS) paged_f32_kernel
 
     griddep_launch_dependents();
     griddep_wait();
+    PagedWalk walk;
     paged_locate<C::THREADS>(a, blockIdx.x, loc, blockIdx.x == 0);
+    walk.init(a, loc.w0, loc.w1, loc.b, loc.start);
     if (tid < 2) a.part_info[blockIdx.x * 2 + tid] = make_int4(0, 0, 0, 0);
 
     const int ngrp = (a.G + a.p.gs - 1) / a.p.gs;          // head groups of a kv head
-    const uint32_t ring0 = smem_u32(smem) + wk * kStages * 2 * C::TILE;
-    PagedWalk walk;
-    walk.init(a, loc.w0, loc.w1, loc.b, loc.start);
+    const uint32_t ring0 = smem_u32(smem) + wk * C::SLOTS * C::TILE;
     PagedSeg g;
     while (walk.next(a, g)) {
         const int hkv = g.hg / ngrp, hs = g.hg % ngrp;
@@ -71,7 +76,12 @@ __global__ void __launch_bounds__(F32Cfg<D, RW, MANY>::THREADS) paged_f32_kernel
         const char* kp = static_cast<const char*>(a.c.k) + (long long)hkv * a.c.head_stride * 4;
         const char* vp = static_cast<const char*>(a.c.v) + (long long)hkv * a.c.head_stride * 4;
 
-        // Query rows, in log2 units of the scaled logit.
+        // Pages of the warp's first two steps, on their way while the query rows are staged.
+        const int nsteps = g.t1 - g.t0;
+        const int first = g.t0 * C::BN + wk * 32;
+        const int lfirst = first + (MANY ? warp * 4 : 0);  // (MANY: a warp loads four rows of every step)
+        int pid = page_at(a.c, trow, lfirst + lane, g.kv);
+        int pid1 = nsteps > 1 ? page_at(a.c, trow, lfirst + C::BN + lane, g.kv) : -1;
         for (int i = tid; i < C::ROWS * U; i += C::THREADS) {
             const int row = i / U, u = i % U;
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -95,41 +105,12 @@ __global__ void __launch_bounds__(F32Cfg<D, RW, MANY>::THREADS) paged_f32_kernel
             for (int e = 0; e < DL; ++e) o[r][e] = 0.f;
         }
 
-        // Loading: a private 32-key step per warp (FEW), or four rows of the shared step (MANY).
-        constexpr int LROWS = MANY ? 4 : 32;
-        const int nsteps = g.t1 - g.t0;
-        const int first = g.t0 * C::BN + wk * 32;
-        const int lfirst = first + (MANY ? warp * LROWS : 0);
-        int pid = page_at(a.c, trow, lfirst + lane, g.kv);
-        int pid1 = nsteps > 1 ? page_at(a.c, trow, lfirst + C::BN + lane, g.kv) : -1;
-        auto issue = [&](int j) {
-            if (j < nsteps) {
-                const int at = lfirst + j * C::BN;
-                const int pid2 = j + 2 < nsteps ? page_at(a.c, trow, at + 2 * C::BN + lane, g.kv) : -1;
-                const uint32_t st = ring0 + (j % kStages) * 2 * C::TILE;
-                load_rows<LROWS, U>(st, st + C::TILE, kp, vp, a.c, 4, MANY ? warp * LROWS : 0, at, g.kv,
-                                    checked_page(a.c, pid, at + lane, g.kv, a.err), lane);
-                pid = pid1;
-                pid1 = pid2;
-            }
-            cp_async_commit();
-        };
-#pragma unroll
-        for (int j = 0; j < kStages - 1; ++j) issue(j);
-        __syncthreads();                                   // the query rows are there
-        for (int j = 0; j < nsteps; ++j) {
-            cp_async_wait<kStages - 2>();
-            if (MANY) __syncthreads();
-            else __syncwarp();
-            issue(j + kStages - 1);
-            const float4* sk = reinterpret_cast<const float4*>(smem + wk * kStages * 2 * C::TILE + (j % kStages) * 2 * C::TILE);
-            const float* sv = reinterpret_cast<const float*>(sk) + C::TILE / 4;
-            const int key = first + j * C::BN + lane;
-
+        // Scores of the warp's rows against 32 keys (lane: key `key`), softmax, weights to s_p.
+        auto scores = [&](const float4* sk, int key) {
             float2 acc[RW];
 #pragma unroll
             for (int r = 0; r < RW; ++r) acc[r] = make_float2(0.f, 0.f);
-#pragma unroll 4
+#pragma unroll (RW == 4 ? 8 : 4)
             for (int u = 0; u < U; ++u) {
                 const float4 kf = sk[tile_unit<U>(lane, u)];
 #pragma unroll
@@ -158,8 +139,9 @@ __global__ void __launch_bounds__(F32Cfg<D, RW, MANY>::THREADS) paged_f32_kernel
 #pragma unroll
             for (int r = 0; r < RW; r += 4)
                 *reinterpret_cast<float4*>(s_p + lane * RW + r) = make_float4(p[r], p[r + 1], p[r + 2], p[r + 3]);
-            __syncwarp();
-#pragma unroll 4
+        };
+        auto outputs = [&](const float* sv) {
+#pragma unroll (RW == 4 ? 8 : 4)
             for (int k = 0; k < 32; ++k) {
                 float pr[RW];
 #pragma unroll
@@ -183,6 +165,94 @@ __global__ void __launch_bounds__(F32Cfg<D, RW, MANY>::THREADS) paged_f32_kernel
 #pragma unroll
                     for (int r = 0; r < RW; ++r) o[r][0] = fmaf(pr[r], v, o[r][0]);
                 }
+            }
+        };
+
+        const uint8_t* ring = smem + wk * C::SLOTS * C::TILE;
+        if constexpr (!MANY) {
+            // A private ring of three tiles, K and V of a step in turn: the next two are in flight
+            // while one is worked on.
+            int page = -1;                                 // this step's, checked
+            long long off[4] = {0, 0, 0, 0};               // its four groups of eight rows (a page has eight or more)
+            bool full = false;                             // every row of it is there
+            const int mask = (1 << a.c.ps_shift) - 1;
+            const long long tok_bytes = a.c.tok_stride * 4;
+            const long long lane_off = (lane / U) * tok_bytes + (lane % U) * 16;
+            int slot = 0;                                  // of the next tile to load
+            auto load = [&](const char* src, int j) {
+                const uint32_t st = ring0 + slot * C::TILE;
+                if (j < nsteps && full) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const char* s = src + off[x];
+#pragma unroll
+                        for (int i = 0; i < 8; i += 32 / U, s += 32 / U * tok_bytes)
+                            cp_async16(st + tile_unit<U>(8 * x + i + lane / U, lane % U) * 16, s, true);
+                    }
+                } else if (j < nsteps) {
+                    load_tile<U>(st, src, a.c, 4, first + j * C::BN, g.kv, page, lane);
+                }
+                cp_async_commit();
+                slot = slot == 2 ? 0 : slot + 1;
+            };
+            auto load_k = [&](int j) {
+                if (j < nsteps) {
+                    const int at = first + j * C::BN;
+                    page = checked_page(a.c, pid, at + lane, g.kv, a.err);
+                    pid = pid1;
+                    pid1 = j + 2 < nsteps ? page_at(a.c, trow, at + 2 * C::BN + lane, g.kv) : -1;
+                    full = __all_sync(0xffffffffu, page >= 0);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        off[x] = ((long long)__shfl_sync(0xffffffffu, page, 8 * x) * a.c.page_stride) * 4 +
+                                 ((at + 8 * x) & mask) * tok_bytes + lane_off;
+                }
+                load(kp, j);
+            };
+            load_k(0);
+            load(vp, 0);
+            __syncthreads();                               // the query rows are there
+            int at = 0;                                    // slot of the tile to work on
+            for (int j = 0; j < nsteps; ++j) {
+                cp_async_wait<1>();
+                __syncwarp();                              // K is there; the last step's V is read
+                load_k(j + 1);
+                const int key0 = first + j * C::BN;        // (behind the unit's keys: this warp's share of the last tile)
+                if (key0 < g.kv) scores(reinterpret_cast<const float4*>(ring + at * C::TILE), key0 + lane);
+                at = at == 2 ? 0 : at + 1;
+                cp_async_wait<1>();
+                __syncwarp();                              // V and the weights are there, K is read
+                load(vp, j + 1);
+                if (key0 < g.kv) outputs(reinterpret_cast<const float*>(ring + at * C::TILE));
+                at = at == 2 ? 0 : at + 1;
+            }
+        } else {
+            // One ring for all warps.
+            constexpr int LROWS = 4;
+            auto issue = [&](int j) {
+                if (j < nsteps) {
+                    const int at = lfirst + j * C::BN;
+                    const int pid2 = j + 2 < nsteps ? page_at(a.c, trow, at + 2 * C::BN + lane, g.kv) : -1;
+                    const uint32_t st = ring0 + (j % kStages) * 2 * C::TILE;
+                    load_rows<LROWS, U>(st, st + C::TILE, kp, vp, a.c, 4, warp * LROWS, at, g.kv,
+                                        checked_page(a.c, pid, at + lane, g.kv, a.err), lane);
+                    pid = pid1;
+                    pid1 = pid2;
+                }
+                cp_async_commit();
+            };
+#pragma unroll
+            for (int j = 0; j < kStages - 1; ++j) issue(j);
+            __syncthreads();                               // the query rows are there
+            for (int j = 0; j < nsteps; ++j) {
+                cp_async_wait<kStages - 2>();
+                __syncthreads();
+                issue(j + kStages - 1);
+                if (row0 >= live_rows) continue;           // (a warp without rows only loads)
+                const uint8_t* st = ring + (j % kStages) * 2 * C::TILE;
+                scores(reinterpret_cast<const float4*>(st), first + j * C::BN + lane);
+                __syncwarp();
+                outputs(reinterpret_cast<const float*>(st + C::TILE));
             }
         }
         cp_async_wait<0>();
@@ -254,6 +324,7 @@ cudaError_t launch_f32_d(PagedKind kind, const PagedAttnArgs& a, cudaStream_t st
     switch (kind) {
         case PAGED_F32_FEW4: return launch_f32_t<D, 4, false>(a, st);
         case PAGED_F32_FEW8: return launch_f32_t<D, 8, false>(a, st);
+        case PAGED_F32_FEW16: return launch_f32_t<D, 16, false>(a, st);
         default: return launch_f32_t<D, 8, true>(a, st);
     }
 }

@@ -149,7 +149,7 @@ static_assert(2 * kSms <= kMaxParts, "the part list holds every CTA");
 
 PagedKind paged_kind(bool f32, int D, int G, int max_new) {
     const long long rows = (long long)G * max_new;
-    if (f32) return rows <= 4 ? PAGED_F32_FEW4 : rows <= 8 ? PAGED_F32_FEW8 : PAGED_F32_MANY;
+    if (f32) return rows <= 4 ? PAGED_F32_FEW4 : rows <= 8 ? PAGED_F32_FEW8 : rows <= 32 ? PAGED_F32_FEW16 : PAGED_F32_MANY;
     if (rows <= 16) return PAGED_SHORT16;
     return rows <= 32 || D == 32 || G > 128 ? PAGED_SHORT32 : PAGED_TILES;
 }
@@ -177,9 +177,10 @@ PagedSplit paged_split(PagedKind kind, int D, int Hkv, int G, int cap) {
             break;
         case PAGED_F32_FEW4:
         case PAGED_F32_FEW8:
-            rows(kind == PAGED_F32_FEW4 ? 4 : 8);
+        case PAGED_F32_FEW16:
+            rows(kind == PAGED_F32_FEW4 ? 4 : kind == PAGED_F32_FEW8 ? 8 : 16);
             tile(paged_f32_bn(false));
-            p.C = D == 32 ? 2 * kSms : kSms;
+            p.C = D == 32 && kind != PAGED_F32_FEW16 ? 2 * kSms : kSms;
             break;
         case PAGED_F32_MANY:
             rows(64);

@@ -48,6 +48,24 @@ __device__ __forceinline__ void load_rows(uint32_t sk, uint32_t sv, const char* 
     }
 }
 
+// 32 positions of one head of one tensor, as load_rows does it.
+template <int U>
+__device__ __forceinline__ void load_tile(uint32_t st, const char* src, const PagedView& c, int esize, int first,
+                                          int kv_end, int pid, int lane) {
+    constexpr int PER = 32 / U;
+    const int mask = (1 << c.ps_shift) - 1;
+#pragma unroll
+    for (int i = 0; i < 32; i += PER) {
+        const int r = i + lane / U, u = lane % U;
+        const int pos = first + r;
+        const int page = __shfl_sync(0xffffffffu, pid, r);
+        const bool live = pos < kv_end && page >= 0;
+        const long long off =
+            live ? ((long long)page * c.page_stride + (long long)(pos & mask) * c.tok_stride) * esize + u * 16 : 0;
+        cp_async16(st + tile_unit<U>(r, u) * 16, src + off, live);
+    }
+}
+
 // Page of position pos of a sequence (row: its table row), -1 at or behind kv_end.  The id
 // is looked at only when it is used (checked_page): a branch on it here would hold the warp
 // for the load.

@@ -176,7 +176,8 @@ def test_attn_head_major_pages(dtype, D, ps):
         attn_case(dtype, 12, 4, D, ps, [70, 1, 5], [333, 500, 5], 87, hnd=True, max_new=mn)
 
 
-@pytest.mark.parametrize("dtype,n,max_new", [(BF16, 1, 1), (BF16, 16, None), (F32, 1, 1), (F32, 16, None)])
+@pytest.mark.parametrize("dtype,n,max_new", [(BF16, 1, 1), (BF16, 16, None), (F32, 1, 1), (F32, 2, 2), (F32, 4, 4),
+                                             (F32, 16, None)])
 def test_attn_one_unit_over_many_ctas(dtype, n, max_new):
     """One kv head and few rows: a single unit is cut into dozens or hundreds of parts."""
     attn_case(dtype, 4, 1, 64, 64, [n], [40003], 95, max_new=max_new)
@@ -210,6 +211,21 @@ def test_attn_chunks_bf16(Hq, Hkv, D, ps, n, lens, max_new):
 @pytest.mark.parametrize("max_new", [1, None])
 def test_attn_chunks_f32(Hq, Hkv, D, ps, n, lens, max_new):
     attn_case(F32, Hq, Hkv, D, ps, n, lens, 51 + Hq, max_new=max_new, tail=3, lead=2)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,ps,n,lens", [c for c in CHUNKS if c[2] < 128])
+@pytest.mark.parametrize("max_new", [2, 4, 6])
+def test_attn_chunks_f32_by_few_rows(Hq, Hkv, D, ps, n, lens, max_new):
+    attn_case(F32, Hq, Hkv, D, ps, n, lens, 61 + Hq, max_new=max_new, tail=1)
+
+
+@pytest.mark.parametrize("hnd", [False, True])
+@pytest.mark.parametrize("D,G,n", [(32, 3, 1), (32, 7, 1), (32, 4, 4), (64, 1, 1), (64, 5, 1), (64, 3, 10), (64, 9, 3)])
+def test_attn_few_tokens_f32(D, G, n, hnd):
+    """Lengths around the 32 keys of a warp and the 256 of a tile, every page size."""
+    for ps in (8, 16, 32, 128):
+        lens = [n, 31, 32, 33, 255, 256, 257, 289, 511, 1500]
+        attn_case(F32, 2 * G, 2, D, ps, [min(n, x) for x in lens], lens, ps + D + G, hnd=hnd, max_new=n)
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
@@ -246,7 +262,7 @@ def test_attn_queries_from_a_fused_projection_and_side_by_side_pools():
         check_attn(q.contiguous(), kp, vp, i32(t), lens, cu, o, lse, BF16, HALF[BF16])
 
 
-@pytest.mark.parametrize("dtype,mn", [(BF16, 1), (BF16, None), (F32, 1), (F32, None)])
+@pytest.mark.parametrize("dtype,mn", [(BF16, 1), (BF16, None), (F32, 1), (F32, 8), (F32, None)])
 def test_attn_pages_beyond_32_bit_offsets(dtype, mn):
     """Pages 2^30 elements apart: the last starts at element 2^32 of its pool."""
     ps, Hkv, D, P = 16, 2, 64, 5
@@ -273,7 +289,7 @@ def test_attn_pages_beyond_32_bit_offsets(dtype, mn):
     assert out[1].tolist() == [[3, -1]] and torch.equal(kp[3, :10], ref4[:10])
 
 
-@pytest.mark.parametrize("dtype,mn", [(BF16, 1), (BF16, None), (F32, 1), (F32, None)])
+@pytest.mark.parametrize("dtype,mn", [(BF16, 1), (BF16, None), (F32, 1), (F32, 8), (F32, None)])
 def test_attn_nan_in_a_key_in_use_shows(dtype, mn):
     """A NaN key in front of a row's position makes that row NaN (o and lse) and no row that
     does not see it, in its own or another sequence."""
@@ -291,7 +307,7 @@ def test_attn_nan_in_a_key_in_use_shows(dtype, mn):
     assert bool(torch.isfinite(lse)[~hit].all()) and bool(torch.isfinite(o.float())[~hit].all())
 
 
-@pytest.mark.parametrize("dtype,mn", [(BF16, 1), (BF16, None), (F32, 1), (F32, None)])
+@pytest.mark.parametrize("dtype,mn", [(BF16, 1), (BF16, None), (F32, 1), (F32, 8), (F32, None)])
 def test_attn_same_bits_every_time(dtype, mn):
     q, kp, vp, t, ln, cu, o, lse = attn_case(dtype, 12, 4, 64, 16, [64, 1, 1, 33], [3000, 5000, 17, 900], 71, max_new=mn)
     ws = ne.alloc_paged_workspace(4, 99, 12, 4, 64)
