@@ -487,7 +487,7 @@ def paged_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_new=None, rope
         Hq = q.shape[1]
         q_ld = _rows(q, "q", N, Hq, D, dt, dev)
         if q_out is None:                                  # (without cu_new every row is written)
-            q_out = (torch.empty if cu_new is None else torch.zeros)((N, Hq, D), dtype=dt, device=k_pages.device)
+            q_out = q.new_empty((N, Hq, D)) if cu_new is None else q.new_zeros((N, Hq, D))
         qo_ld = _rows(q_out, "q_out", N, Hq, D, dt, dev)
         qp, qop = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
@@ -519,13 +519,13 @@ def paged_attn(q, k_pages, v_pages, page_table, seq_lens, cu_new=None, max_new: 
     N, Hq = q.shape[:2]
     B, W, pt, ln, cu = _paged_batch(page_table, seq_lens, cu_new, N, dev)
     q_ld = _rows(q, "q", N, Hq, D, dt, dev)
-    new = torch.empty if cu_new is None else torch.zeros   # (without cu_new every row is written)
+    new = q.new_empty if cu_new is None else q.new_zeros   # (without cu_new every row is written)
     if o is None:
-        o = new((N, Hq, D), dtype=dt, device=k_pages.device)
+        o = new((N, Hq, D))
     elif o.shape != q.shape or o.dtype is not dt or o.get_device() != dev or not o.is_contiguous():
         raise ValueError("o must be contiguous and match q")
     if lse is None:
-        lse = new((N, Hq), dtype=torch.float32, device=k_pages.device)
+        lse = new((N, Hq), dtype=_F32)
     elif lse.shape != (N, Hq) or lse.dtype is not torch.float32 or lse.get_device() != dev or not lse.is_contiguous():
         raise ValueError("lse must be contiguous fp32 [N, Hq]")
     if workspace is None:
@@ -543,9 +543,9 @@ def alloc_pages_workspace(n_pages: int, n: int, max_pages: int, device="cuda"):
 
 
 def _out_ints(t, shape, dev, name, like):
-    """An int32 output and its address: the caller's, or a new one beside `like`."""
+    """An int32 output and its address: the caller's, or a new one beside `like` (int32)."""
     if t is None:
-        t = torch.empty(shape, dtype=_I32, device=like.device)
+        t = like.new_empty(shape)
         return t, t.data_ptr()
     return t, _ints(t, shape, dev, name)
 
@@ -564,10 +564,10 @@ def pages_fork(refcount, page_table, seq_lens, parents, k_pages, v_pages, deep: 
         raise ValueError("page_table must be [B, max_pages] and parents [C]")
     B, W = page_table.shape
     C = parents.shape[0]
-    refcount_out, ro = _out_ints(refcount_out, P, dev, "refcount_out", k_pages)
-    child_table, ct = _out_ints(child_table, (C, W), dev, "child_table", k_pages)
-    child_lens, cl = _out_ints(child_lens, (C,), dev, "child_lens", k_pages)
-    short, sh = _out_ints(short, (1,), dev, "short", k_pages)
+    refcount_out, ro = _out_ints(refcount_out, P, dev, "refcount_out", refcount)
+    child_table, ct = _out_ints(child_table, (C, W), dev, "child_table", refcount)
+    child_lens, cl = _out_ints(child_lens, (C,), dev, "child_lens", refcount)
+    short, sh = _out_ints(short, (1,), dev, "short", refcount)
     workspace = alloc_pages_workspace(n_pages, C, W, k_pages.device) if workspace is None else workspace
     _launch(lib.ne_pages_fork, dev, c, _ints(refcount, P, dev, "refcount"),
             _ints(page_table, (B, W), dev, "page_table"), _ints(seq_lens, (B,), dev, "seq_lens"),
@@ -587,9 +587,9 @@ def pages_resize(refcount, page_table, seq_lens, new_lens, k_pages, v_pages, ref
     if len(T) != 2:
         raise ValueError("page_table must be [B, max_pages]")
     B, W = T
-    refcount_out, ro = _out_ints(refcount_out, P, dev, "refcount_out", k_pages)
-    table_out, to = _out_ints(table_out, T, dev, "table_out", k_pages)
-    short, sh = _out_ints(short, (1,), dev, "short", k_pages)
+    refcount_out, ro = _out_ints(refcount_out, P, dev, "refcount_out", refcount)
+    table_out, to = _out_ints(table_out, T, dev, "table_out", refcount)
+    short, sh = _out_ints(short, (1,), dev, "short", refcount)
     workspace = alloc_pages_workspace(n_pages, B, W, k_pages.device) if workspace is None else workspace
     _launch(lib.ne_pages_resize, dev, c, _ints(refcount, P, dev, "refcount"),
             _ints(page_table, T, dev, "page_table"), _ints(seq_lens, (B,), dev, "seq_lens"),
@@ -609,10 +609,10 @@ def pages_compact(refcount, page_table, k_pages, v_pages, refcount_out=None, tab
     if len(T) != 2:
         raise ValueError("page_table must be [B, max_pages]")
     B, W = T
-    refcount_out, ro = _out_ints(refcount_out, P, dev, "refcount_out", k_pages)
-    table_out, to = _out_ints(table_out, T, dev, "table_out", k_pages)
-    remap, rm = _out_ints(remap, P, dev, "remap", k_pages)
-    n_live, nl = _out_ints(n_live, (1,), dev, "n_live", k_pages)
+    refcount_out, ro = _out_ints(refcount_out, P, dev, "refcount_out", refcount)
+    table_out, to = _out_ints(table_out, T, dev, "table_out", refcount)
+    remap, rm = _out_ints(remap, P, dev, "remap", refcount)
+    n_live, nl = _out_ints(n_live, (1,), dev, "n_live", refcount)
     workspace = alloc_pages_workspace(n_pages, B, W, k_pages.device) if workspace is None else workspace
     _launch(lib.ne_pages_compact, dev, c, _ints(refcount, P, dev, "refcount"),
             _ints(page_table, T, dev, "page_table"), ro, to, rm, nl, B, W,

@@ -48,6 +48,7 @@ struct RopeTurns {
 // Split of the attention over CTAs (paged_sched.cuh).
 struct PagedSplit {
     int C;                            // CTAs of the main kernel
+    unsigned long long inv_C;         // 2^64 / C, rounded down
     int tpt;                          // tokens per work unit
     int hg;                           // head groups: Hkv * ceil(G / rows) (rows < G only in the short kernels)
     int gs;                           // query heads of a group

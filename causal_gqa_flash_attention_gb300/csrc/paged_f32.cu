@@ -12,9 +12,9 @@
 // of three K or V tiles, and are joined at the end of a unit.  MANY: eight warps take 8 of 64
 // rows each over one shared ring.
 //
-// Measured (GB300): one step over 8 x 16384 positions, 12/4 heads of 64: 49 us, 5.5 TB/s; with
-// 32/4 heads 54 us; four new tokens each, 12/4 heads: 81 us (MANY would take 279: its warps
-// without rows wait); 512 new tokens over 4096 positions: 214 us, 28 TFLOP/s of the 75 that fp32
+// Measured (GB300): one step over 8 x 16384 positions, 12/4 heads of 64: 48 us, 5.6 TB/s; with
+// 32/4 heads 53 us; four new tokens each, 12/4 heads: 78 us (MANY would take 279: its warps
+// without rows wait); 512 new tokens over 4096 positions: 217 us, 28 TFLOP/s of the 75 that fp32
 // FMAs give.  Four warps with twice the keys in flight took 54, 64 and 99 us (a scheduler with
 // one warp waits for its chain), a ring of whole K and V steps 60, 89 and -.
 #include "paged_load.cuh"
@@ -51,6 +51,7 @@ __global__ void __launch_bounds__(F32Cfg<D, RW, MANY>::THREADS, F32Cfg<D, RW, MA
     constexpr int U = C::U, DL = C::DL;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ PagedLocate loc;
+    __shared__ int s_lim[C::ROWS];                         // keys that a row sees
     __shared__ float s_m[C::WK][C::ROWS], s_l[C::WK][C::ROWS];
     float* s_q = reinterpret_cast<float*>(smem + C::RINGS);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -92,9 +93,7 @@ __global__ void __launch_bounds__(F32Cfg<D, RW, MANY>::THREADS, F32Cfg<D, RW, MA
             }
             reinterpret_cast<float4*>(s_q)[i] = x;
         }
-        int lim[RW];
-#pragma unroll
-        for (int r = 0; r < RW; ++r) lim[r] = row0 + r < live_rows ? g.base + g.tok + (row0 + r) / gs + 1 : 0;
+        if (tid < C::ROWS) s_lim[tid] = tid < live_rows ? g.base + g.tok + tid / gs + 1 : 0;
 
         float m[RW], l[RW], o[RW][DL];
 #pragma unroll
@@ -105,8 +104,11 @@ __global__ void __launch_bounds__(F32Cfg<D, RW, MANY>::THREADS, F32Cfg<D, RW, MA
             for (int e = 0; e < DL; ++e) o[r][e] = 0.f;
         }
 
-        // Scores of the warp's rows against 32 keys (lane: key `key`), softmax, weights to s_p.
-        auto scores = [&](const float4* sk, int key) {
+        // Scores of the warp's rows against keys key0 .. key0 + 31 (lane: key), softmax, weights to s_p.
+        auto scores = [&](const float4* sk, int key0) {
+            // Behind the first token's position rows are masked.  (MANY always looks: the branch
+            // cost its loop 4 to 11%.)
+            const bool edge = MANY || key0 + 32 > g.base + g.tok + 1;
             float2 acc[RW];
 #pragma unroll
             for (int r = 0; r < RW; ++r) acc[r] = make_float2(0.f, 0.f);
@@ -123,7 +125,7 @@ __global__ void __launch_bounds__(F32Cfg<D, RW, MANY>::THREADS, F32Cfg<D, RW, MA
             float p[RW];
 #pragma unroll
             for (int r = 0; r < RW; ++r) {
-                const float s = key < lim[r] ? (acc[r].x + acc[r].y) * a.scale_log2 : -INFINITY;
+                const float s = !edge || key0 + lane < s_lim[row0 + r] ? (acc[r].x + acc[r].y) * a.scale_log2 : -INFINITY;
                 float x = s;
 #pragma unroll
                 for (int off = 16; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
@@ -218,7 +220,7 @@ __global__ void __launch_bounds__(F32Cfg<D, RW, MANY>::THREADS, F32Cfg<D, RW, MA
                 __syncwarp();                              // K is there; the last step's V is read
                 load_k(j + 1);
                 const int key0 = first + j * C::BN;        // (behind the unit's keys: this warp's share of the last tile)
-                if (key0 < g.kv) scores(reinterpret_cast<const float4*>(ring + at * C::TILE), key0 + lane);
+                if (key0 < g.kv) scores(reinterpret_cast<const float4*>(ring + at * C::TILE), key0);
                 at = at == 2 ? 0 : at + 1;
                 cp_async_wait<1>();
                 __syncwarp();                              // V and the weights are there, K is read
@@ -250,7 +252,7 @@ __global__ void __launch_bounds__(F32Cfg<D, RW, MANY>::THREADS, F32Cfg<D, RW, MA
                 issue(j + kStages - 1);
                 if (row0 >= live_rows) continue;           // (a warp without rows only loads)
                 const uint8_t* st = ring + (j % kStages) * 2 * C::TILE;
-                scores(reinterpret_cast<const float4*>(st), first + j * C::BN + lane);
+                scores(reinterpret_cast<const float4*>(st), first + j * C::BN);
                 __syncwarp();
                 outputs(reinterpret_cast<const float*>(st + C::TILE));
             }

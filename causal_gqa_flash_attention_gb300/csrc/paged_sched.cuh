@@ -21,13 +21,6 @@
 
 namespace ne {
 
-// a / b for b > 0, a >= 0, in 32 bits where both fit: the 64-bit divide is a long
-// sequence, and a CTA's share of the work is found by a few of them one after another.
-__device__ __forceinline__ long long paged_div(long long a, long long b) {
-    if ((((unsigned long long)a | (unsigned long long)b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
-    return a / b;
-}
-
 struct PagedSeq {
     int tok0, n, len;
 };
@@ -135,8 +128,16 @@ struct PagedWalk {
         }
         const long long S = paged_group_cost(q, a.p);
         const long long off = w0 - start;
-        hg = (int)paged_div(off, S);
-        const long long x = off - (long long)hg * S;
+        // off / S by an estimate (off < S times the head groups, so it is off by one at most).
+        hg = min(a.p.hg - 1, (int)__fdividef((float)off, (float)S));
+        long long x = off - (long long)hg * S;
+        if (x < 0) {
+            --hg;
+            x += S;
+        } else if (x >= S) {
+            ++hg;
+            x -= S;
+        }
         int lo = 0, hi = nt - 1;                           // the last tile whose start is at or before x
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -154,11 +155,13 @@ struct PagedWalk {
             const int ntok = min(a.p.tpt, q.n - r * a.p.tpt);
             const long long cost = a.p.ovh + (long long)paged_weight(ntok, a.p) * kv;
             const int ntk = (kv + (1 << a.p.bn_shift) - 1) >> a.p.bn_shift;
-            // The tile nearest to each end of the interval; a whole unit goes to whoever holds its
-            // middle.
+            // The tile nearest to each end of the interval (nocut: a whole unit goes to whoever holds
+            // its middle).  In fp32: both CTAs at a cut compute it alike, it grows with x, and what
+            // it is off by for units of more than 2^24 keys is a tile.
+            const float per = __fdividef((float)ntk, (float)cost);
             auto cut = [&](long long x) -> int {
                 if (a.p.nocut) return 2 * x >= cost ? ntk : 0;
-                return (int)paged_div(x * ntk + cost / 2, cost);
+                return min(ntk, __float2int_rn(__fmul_rn((float)x, per)));
             };
             g.t0 = w0 <= cur ? 0 : cut(w0 - cur);
             g.t1 = w1 >= cur + cost ? ntk : cut(w1 - cur);
@@ -189,15 +192,15 @@ struct PagedWalk {
     }
 };
 
-// The CTA's share of `total`: CTA c of at most p.C, none with less than min_work but the last few
-// keys of a small call.
+// The CTA's share of `total`: CTA c of p.C, or of as many as have min_work each in a small call.
 __device__ __forceinline__ void paged_interval(const PagedSplit& p, long long total, int c, long long& w0, long long& w1) {
-    const long long most = total >> p.min_shift;
-    const int C = most < 1 ? 1 : (most < p.C ? (int)most : p.C);
-    const long long each = paged_div(total, C), rest = total - each * C;
-    const long long i = min(c, C), j = min(c + 1, C);
-    w0 = each * i + min(i, rest);
-    w1 = each * j + min(j, rest);
+    if (total < (long long)p.C << p.min_shift) {
+        w0 = min((long long)c << p.min_shift, total);
+        w1 = min((long long)(c + 1) << p.min_shift, total);
+    } else {
+        w0 = (long long)__umul64hi((unsigned long long)total, p.inv_C * c);
+        w1 = c + 1 == p.C ? total : (long long)__umul64hi((unsigned long long)total, p.inv_C * (c + 1));
+    }
 }
 
 // Shared scratch of paged_locate.

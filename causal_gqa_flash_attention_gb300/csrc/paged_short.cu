@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_short_kernel(const PagedAtt
             }
     };
     // Warp 0 finds the CTA's parts, one ahead; where its share begins, it finds alone among up to
-    // 32 sequences, and the whole CTA among more (256 sequences: 29.7 us a call instead of 32.7).
+    // 32 sequences, and the whole CTA among more (256 sequences: 3 us less a call).
     PagedWalk walk;
     int turn = 0;
     if (a.s.B > 32) paged_locate<kThreads>(a, blockIdx.x, loc, blockIdx.x == 0);

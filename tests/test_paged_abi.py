@@ -201,7 +201,7 @@ def test_binding_refuses_host_tensors_and_mismatches(lib):
 class Split:
     """How the attention kernels cut a call, step by step as in paged_sched.cuh."""
 
-    def __init__(self, n, lens, Hkv, G, rows, bn, C, ovh=128, min_work=128, w_full=1, w_part=1, sub=0):
+    def __init__(self, n, lens, Hkv, G, rows, bn, C, ovh=384, min_work=128, w_full=1, w_part=1, sub=0):
         self.n, self.lens, self.bn, self.ovh = n, lens, bn, ovh
         self.gs = min(G, rows)
         self.tpt = rows // self.gs
@@ -215,9 +215,11 @@ class Split:
         self.units = units
         self.start = np.concatenate([[0], np.cumsum([ovh + u[3] * u[4] for u in units])]).astype(object)
         W = int(self.start[-1])
-        self.C = max(1, min(C, W // min_work))
-        each, rest = divmod(W, self.C)
-        self.w = [each * c + min(c, rest) for c in range(self.C + 1)]
+        self.C = C
+        if W < C * min_work:
+            self.w = [min(c * min_work, W) for c in range(C + 1)]
+        else:
+            self.w = [W * (c * ((2 ** 64 - 1) // C)) >> 64 for c in range(C)] + [W]
 
     def parts(self, c):
         out = []
@@ -226,8 +228,9 @@ class Split:
             w0, w1 = self.w[c], self.w[c + 1]
             if u0 + cost <= w0 or u0 >= w1:
                 continue
-            t0 = 0 if w0 <= u0 else ((w0 - u0) * nt + cost // 2) // cost
-            t1 = nt if w1 >= u0 + cost else ((w1 - u0) * nt + cost // 2) // cost
+            per = np.float32(nt) / np.float32(cost)
+            t0 = 0 if w0 <= u0 else min(nt, int(np.rint(np.float32(w0 - u0) * per)))
+            t1 = nt if w1 >= u0 + cost else min(nt, int(np.rint(np.float32(w1 - u0) * per)))
             if t0 < t1 or (nt == 0 and w0 <= u0):
                 out.append((b, hg, r, t0, t1, nt))
         return out
@@ -237,7 +240,7 @@ class Split:
 def test_split_covers_every_key_tile_once_and_parts_can_be_joined(seed):
     rng = random.Random(seed)
     G, Hkv = rng.choice([1, 2, 3, 5, 8, 20]), rng.choice([1, 2, 4])
-    rows, bn, C, more = rng.choice([(16, 64, 304, {}), (32, 128, 304, {}), (8, 128, 152, {}), (64, 32, 304, {}),
+    rows, bn, C, more = rng.choice([(16, 64, 304, {}), (32, 128, 304, {}), (8, 256, 152, {}), (64, 32, 304, {}),
                                     (256, 128, 152, dict(ovh=1024, min_work=2048, w_full=5, w_part=4, sub=128 // G))])
     B = rng.randint(1, 9)
     n = [rng.choice([0, 1, 1, rng.randint(1, 60)]) for _ in range(B)]
