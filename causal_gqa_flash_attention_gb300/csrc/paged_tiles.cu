@@ -13,11 +13,12 @@
 // so products bound D 128 and exponentials come close to them at D 64.  The two subtiles alternate: while the softmax warps of one work on its S tile, the
 // tensor core runs the other's PV and next S.  Roles (12 warps):
 //   warp 0       producer: Q pair of the unit, then K and V tiles through an NS-slot ring.
-//   warp 1       UMMA issuer (owns the 512 TMEM columns).  Per tile t and subtile u:
-//                O_u += P_u(t) V(t) once P_u(t) is there, and S_u(t + 1) = Q_u K(t + 1)^T.  Where P
-//                lies over S, S(t + 1) goes right behind the PV (one thread's UMMAs run in order, so it
-//                cannot overtake it, and S(t + 1) complete means PV(t) complete); where P has columns
-//                of its own, S(t + 1) goes first, as soon as S(t) is in registers.
+//   warp 1       UMMA issuer (owns the 512 TMEM columns); at D 64 one of two, warp 2 the other, each
+//                for a subtile.  Per tile t: O_u += P_u(t) V(t) once P_u(t) is there, and S_u(t + 1) =
+//                Q_u K(t + 1)^T.  At D 64, where P has columns of its own, S(t + 1) goes first, as soon
+//                as S(t) is in registers.  At D 128 P lies over S, and S(t + 1) goes right behind the PV
+//                (one thread's UMMAs run in order, so it cannot overtake it, and S(t + 1) complete means
+//                PV(t) complete).
 //   warp 2       zeroes the V rows behind a sequence's length in the tile that holds it (P is 0
 //                there, but 0 x NaN is not).
 //   warp 3       finds the CTA's parts (paged_sched.cuh) and queues them for the others.
@@ -26,14 +27,16 @@
 // is full, in columns of its own at D 64.
 // Weights are rounded to bf16 for the product (half a step, 2^-8 of each weight, as the
 // training forward does); maximum and sum stay fp32, and the sum is of the unrounded weights.
-// Measured (GB300): 2048 new tokens over 16384 positions, 16/4 heads of 128: 181-184 us with the
-// join, 1.41-1.43 PFLOP/s (75% of the 1.89 measured for a bf16 GEMM), the tensor pipe 63% busy:
-// a subtile's chain, PV + S on the tensor core (0.54 us) and its softmax (0.7 us, then waits),
-// takes 1.45 us per tile, longer than both subtiles' tensor work.  At D 64 the two softmaxes share
-// the exponential units (32 results a clock per SM): 1.3 us per tile, 0.79 PFLOP/s.  Tried and
-// left out: two threads per row in 16 softmax warps (chunk 199 us), PV in two halves (0.4% at
-// D 128), the second subtile started half a tile late (no change), weights taken before the
-// tile's maximum is known (the scores stay live: 2 KB of spills).
+// Measured (GB300): 2048 new tokens over 16384 positions, 16/4 heads of 128: 182 us with the join,
+// 1.41 PFLOP/s (75% of the 1.89 measured for a bf16 GEMM), the tensor pipe 63% busy: a subtile's
+// chain, PV + S on the tensor core (0.54 us) and its softmax (0.7 us, then waits), takes 1.45 us per
+// tile, longer than both subtiles' tensor work.  12/4 heads of 64: 100 us, 0.96 PFLOP/s.  With one
+// issuer for both subtiles that took 122 us: waiting for one subtile's P it could not start the
+// other's S, which tied the two softmaxes to the same phase.  At D 128 two issuers are slower (196
+// us): the tensor core is the longer half there, and two streams of UMMAs delay each other.
+// Tried and left out: two threads per row in 16 softmax warps (chunk 199 us), PV in two halves
+// (0.4% at D 128), the second subtile started half a tile late (no change), weights taken before
+// the tile's maximum is known (the scores stay live: 2 KB of spills).
 // Every wait is bounded; a CTA that gives up reports, drains its copies and UMMAs, frees its
 // TMEM and ends.
 #include <cuda_bf16.h>
@@ -61,6 +64,7 @@ struct TileCfg {
     static constexpr bool SEP = D == 64;
     static constexpr int P_COL = SEP ? O_COL + 2 * D : 0;  // P_u at P_COL + u P_STEP
     static constexpr int P_STEP = SEP ? 64 : 128;
+    static constexpr int ISSUERS = SEP ? 2 : 1;
     static_assert(SMEM + 1536 <= 227 * 1024, "shared memory (with the static part)");
 };
 
@@ -122,11 +126,11 @@ __global__ void __launch_bounds__(384, 1)
 
     if (tid == 0) {
         mbar_init(smem_u32(&bar_q_full), 1);
-        mbar_init(smem_u32(&bar_q_empty), 1);              // the issuer's commit after a unit's last S
-        mbar_init(smem_u32(&bar_final), 1);
+        mbar_init(smem_u32(&bar_q_empty), C::ISSUERS);     // their commits after a unit's last S
+        mbar_init(smem_u32(&bar_final), C::ISSUERS);
         for (int s = 0; s < C::NS; ++s) {
             mbar_init(smem_u32(&bar_full[s]), 1);
-            mbar_init(smem_u32(&bar_empty[s]), 2);         // the issuer's commit and warp 2
+            mbar_init(smem_u32(&bar_empty[s]), 2);         // warps 1 and 2, by a commit where they multiply
         }
         for (int u = 0; u < 2; ++u) {
             mbar_init(smem_u32(&bar_s_full[u]), 1);
@@ -176,6 +180,16 @@ __global__ void __launch_bounds__(384, 1)
     // Where the CTA's share begins, warp 3 finds alone among up to 32 sequences, all warps among more.
     if (a.s.B > 32) paged_locate<C::THREADS>(a, blockIdx.x, loc, blockIdx.x == 0);
     // A part's K tile t sits at ring index 2 i, its V tile at 2 i + 1, i counting the CTA's tiles.
+    // Zeros for the rows of the V tile at ring index i (keys of tile t) that lie behind the length.
+    auto zero_v = [&](int i, int t) {
+        uint8_t* v = sRing + (i % C::NS) * C::TILE;
+        const int r0 = g.len - t * C::BN;
+        for (int x = lane; x < (C::BN - r0) * C::NCH * 8; x += 32) {
+            const int r = r0 + x / (C::NCH * 8), e = x % (C::NCH * 8);
+            *reinterpret_cast<uint4*>(v + (e >> 3) * C::CHUNK + sw128_offset(r, e & 7)) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+    };
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
@@ -237,86 +251,104 @@ __global__ void __launch_bounds__(384, 1)
             for (int i = max(0, item - C::NS); i < item; ++i)
                 mbar_wait_drain(smem_u32(&bar_full[i % C::NS]), (i / C::NS) & 1, w, SITE_PAGED_DRAIN);
         }
-    } else if (warp == 1) {
-        // ------------------------------------------------------------ UMMA issuer
+    } else if (warp == 1 || (C::SEP && warp == 2)) {
+        // ------------------------------------------------------------ UMMA issuers
+        constexpr int NU = C::SEP ? 1 : 2;                 // subtiles of this warp: u0 .. u0 + NU-1
+        const int u0 = C::SEP ? warp - 1 : 0;
         constexpr uint32_t id_s = idesc_make(FMT_BF16, 128, C::BN, false, false);
         constexpr uint32_t id_o = idesc_make(FMT_BF16, 128, D, false, true);
-        const uint64_t dq0 = sdesc(smem_u32(sQ), 16, 1024);
+        const uint64_t dq0 = sdesc(smem_u32(sQ) + u0 * C::TILE, 16, 1024);
         const uint64_t dk0 = sdesc(smem_u32(sRing), 16, 1024);
         const uint64_t dv0 = sdesc(smem_u32(sRing), C::CHUNK, 1024);
-        int seg = 0, item = 0, tiles[2] = {0, 0}, s_tiles[2] = {0, 0}, fixes = 0;
+        int seg = 0, item = 0, tiles[NU] = {}, s_tiles = 0, fixes = 0;
         bool ok = true;
-        auto s_mmas = [&](int u, int k_item) {
-            const uint64_t dq = sdesc_add(dq0, u * C::TILE), dk = sdesc_add(dk0, (k_item % C::NS) * C::TILE);
+        auto s_mmas = [&](int i, int k_item) {             // S of subtile u0 + i
+            const uint64_t dq = sdesc_add(dq0, i * C::TILE), dk = sdesc_add(dk0, (k_item % C::NS) * C::TILE);
 #pragma unroll
             for (int ks = 0; ks < C::ROWB / 32; ++ks) {
                 const uint32_t off = ((ks * 32) >> 7) * C::CHUNK + ((ks * 32) & 127);
-                umma_ss<false>(tm + u * 128, sdesc_add(dq, off), sdesc_add(dk, off), id_s, ks > 0);
+                umma_ss<false>(tm + (u0 + i) * 128, sdesc_add(dq, off), sdesc_add(dk, off), id_s, ks > 0);
             }
-            umma_commit(smem_u32(&bar_s_full[u]));
+            umma_commit(smem_u32(&bar_s_full[u0 + i]));
+        };
+        // After this warp's last S of a K tile: its slot, and after the part's last S the Q.
+        auto s_done = [&](int k_item, bool last) {
+            umma_commit(smem_u32(&bar_empty[k_item % C::NS]));
+            if (last) umma_commit(smem_u32(&bar_q_empty));
         };
         auto full = [&](int i) {
             const bool r = mbar_wait_warp(smem_u32(&bar_full[i % C::NS]), (i / C::NS) & 1, w, SITE_PAGED_KV_FULL);
             tc_fence_after();
             return r;
         };
-        // S_u's columns hold no S that is still to be read (SEP; otherwise the PV in front of the
+        // S's columns hold no S that is still to be read (SEP; otherwise the PV in front of the
         // next S, on this same thread, says so).
-        auto s_free = [&](int u) -> bool {
-            if (!C::SEP || s_tiles[u] == 0) return true;
-            const bool r = mbar_wait_warp(smem_u32(&bar_s_free[u]), (s_tiles[u] - 1) & 1, w, SITE_PAGED_S_FULL);
+        auto s_free = [&]() -> bool {
+            if (!C::SEP || s_tiles == 0) return true;
+            const bool r = mbar_wait_warp(smem_u32(&bar_s_free[u0]), (s_tiles - 1) & 1, w, SITE_PAGED_S_FULL);
             tc_fence_after();
             return r;
         };
+        // The V tile at ring index i, with zeros behind the length.
+        auto v_tile = [&](int i, int t) -> bool {
+            if (!full(i)) return false;
+            if ((t + 1) * C::BN <= g.len) return true;
+            const int k = fixes++;
+            if (!C::SEP || u0 == 0) return mbar_wait_warp(smem_u32(&bar_vfix[k & 1]), (k >> 1) & 1, w, SITE_PAGED_KV_FULL);
+            zero_v(i, t);
+            mbar_arrive(smem_u32(&bar_vfix[k & 1]));
+            __syncwarp();
+            return true;
+        };
         while (ok && next_part()) {
             if (g.t0 == g.t1) continue;
-            const int n_sub = g.ntok > sub ? 2 : 1, nt = g.t1 - g.t0;
+            const int nt = g.t1 - g.t0;
+            const int mine = C::SEP ? (g.ntok > u0 * sub ? 1 : 0) : (g.ntok > sub ? 2 : 1);
+            // (SEP: a warp without a subtile in this part waits for its Q too, or it could take the
+            // next part's wait for this one's.)
             if (!(ok = mbar_wait_warp(smem_u32(&bar_q_full), seg & 1, w, SITE_PAGED_Q))) break;
-            ok = full(item) && s_free(0) && (n_sub == 1 || s_free(1));
-            if (!ok) break;
+            if (C::SEP && mine == 0) {                     // nothing to multiply: it zeroes V and lets go
+                for (int i = 0; ok && i < 2 * nt; ++i) {
+                    if (!(ok = i & 1 ? v_tile(item + i, g.t0 + (i >> 1)) : full(item + i))) break;
+                    if (lane == 0) {
+                        mbar_arrive(smem_u32(&bar_empty[(item + i) % C::NS]));
+                        if (i == 0) mbar_arrive(smem_u32(&bar_q_empty));
+                    }
+                    __syncwarp();
+                }
+                item += 2 * nt;
+                ++seg;
+                continue;
+            }
+            if (!(ok = full(item) && s_free())) break;
+            ++s_tiles;
             if (elect_one()) {
                 s_mmas(0, item);
-                if (n_sub == 2) s_mmas(1, item);
-                umma_commit(smem_u32(&bar_empty[item % C::NS]));
-                if (nt == 1) umma_commit(smem_u32(&bar_q_empty));
+                if (NU == 2 && mine == 2) s_mmas(NU - 1, item);
+                s_done(item, nt == 1);
             }
             __syncwarp();
-            ++s_tiles[0];
-            if (n_sub == 2) ++s_tiles[1];
             for (int t = 0; ok && t < nt; ++t) {
                 const int vi = item + 2 * t + 1, kn = item + 2 * t + 2;
-                const bool more = t + 1 < nt, fix = (g.t0 + t + 1) * C::BN > g.len;
+                const bool more = t + 1 < nt;
                 const uint64_t dv = sdesc_add(dv0, (vi % C::NS) * C::TILE);
-                // After the last subtile's S(t + 1): its K slot, and after the part's last S the Q.
-                auto s_done = [&]() {
-                    umma_commit(smem_u32(&bar_empty[kn % C::NS]));
-                    if (t + 2 == nt) umma_commit(smem_u32(&bar_q_empty));
-                };
                 if (C::SEP && more) {
-                    if (!(ok = full(kn))) break;
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        if (u >= n_sub || !(ok = s_free(u))) break;
-                        ++s_tiles[u];
-                        if (elect_one()) {
-                            s_mmas(u, kn);
-                            if (u == n_sub - 1) s_done();
-                        }
-                        __syncwarp();
+                    if (!(ok = full(kn) && s_free())) break;
+                    ++s_tiles;
+                    if (elect_one()) {
+                        s_mmas(0, kn);
+                        s_done(kn, t + 2 == nt);
                     }
-                    if (!ok) break;
+                    __syncwarp();
                 }
-                if (!(ok = full(vi))) break;
-                if (fix) {
-                    if (!(ok = mbar_wait_warp(smem_u32(&bar_vfix[fixes & 1]), (fixes >> 1) & 1, w, SITE_PAGED_KV_FULL))) break;
-                    ++fixes;
-                }
+                if (!(ok = v_tile(vi, g.t0 + t))) break;
                 if (!C::SEP && more && !(ok = full(kn))) break;
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    if (u >= n_sub) break;
-                    if (!(ok = mbar_wait_warp(smem_u32(&bar_p_ready[u]), tiles[u] & 1, w, SITE_PAGED_P_READY))) break;
-                    ++tiles[u];
+                for (int i = 0; i < NU; ++i) {
+                    if (i >= mine) break;
+                    const int u = u0 + i;
+                    if (!(ok = mbar_wait_warp(smem_u32(&bar_p_ready[u]), tiles[i] & 1, w, SITE_PAGED_P_READY))) break;
+                    ++tiles[i];
                     tc_fence_after();
                     if (elect_one()) {
 #pragma unroll
@@ -324,10 +356,10 @@ __global__ void __launch_bounds__(384, 1)
                             umma_ts<false>(tm + C::O_COL + u * D, tm + C::P_COL + u * C::P_STEP + ks * 8,
                                            sdesc_add(dv, ks * 16 * 128), id_o, (t > 0 || ks > 0) ? 1u : 0u);
                         if (C::SEP || !more) umma_commit(smem_u32(&bar_o_full[u]));
-                        if (!C::SEP && more) s_mmas(u, kn);
-                        if (u == n_sub - 1) {
+                        if (!C::SEP && more) s_mmas(i, kn);
+                        if (i == mine - 1) {
                             umma_commit(smem_u32(&bar_empty[vi % C::NS]));
-                            if (!C::SEP && more) s_done();
+                            if (!C::SEP && more) s_done(kn, t + 2 == nt);
                         }
                     }
                     __syncwarp();
@@ -338,23 +370,17 @@ __global__ void __launch_bounds__(384, 1)
         }
         umma_commit_e(smem_u32(&bar_final));
     } else if (warp == 2) {
-        // ------------------------------------------------------------ V rows behind the length
+        // ------------------------------------------------------------ V rows behind the length (D 128)
         // It follows every slot's phases and releases each along with the issuer, so neither can
         // fall a phase behind the other.
         int item = 0, fixes = 0;
         bool ok = true;
         while (ok && next_part()) {
             for (int i = 0; ok && i < 2 * (g.t1 - g.t0); ++i, ++item) {
-                const int s = item % C::NS;
+                const int s = item % C::NS, t = g.t0 + (i >> 1);
                 if (!(ok = mbar_wait_warp(smem_u32(&bar_full[s]), (item / C::NS) & 1, w, SITE_PAGED_KV_FULL))) break;
-                const int r0 = g.len - (g.t0 + (i >> 1)) * C::BN;      // first row behind the length
-                if ((i & 1) && r0 < C::BN) {
-                    uint8_t* v = sRing + s * C::TILE;
-                    for (int x = lane; x < (C::BN - r0) * C::NCH * 8; x += 32) {
-                        const int r = r0 + x / (C::NCH * 8), e = x % (C::NCH * 8);
-                        *reinterpret_cast<uint4*>(v + (e >> 3) * C::CHUNK + sw128_offset(r, e & 7)) = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    fence_proxy_async_smem();
+                if ((i & 1) && (t + 1) * C::BN > g.len) {
+                    zero_v(item, t);
                     mbar_arrive(smem_u32(&bar_vfix[fixes++ & 1]));
                 }
                 __syncwarp();
