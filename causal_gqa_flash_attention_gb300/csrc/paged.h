@@ -57,6 +57,7 @@ struct PagedSplit {
     int ovh;                          // fixed cost of a unit
     int w_full, w_part;               // cost of a key of a unit with more than `sub` tokens, and with fewer
     int min_shift;                    // log2 of a CTA's least work
+    int snap, snap_shift;             // cuts near a unit's end (paged_snap)
     int nocut;                        // units are not cut (short contexts): no join
     int rows;                         // rows of a unit (partials are stored at this pitch)
     int sub;                          // tokens of a unit's first 128-row subtile (0: rows are contiguous)

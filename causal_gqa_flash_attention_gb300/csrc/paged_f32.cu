@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(F32Cfg<D, RW, MANY>::THREADS, F32Cfg<D, RW, MA
     griddep_wait();
     PagedWalk walk;
     paged_locate<C::THREADS>(a, blockIdx.x, loc, blockIdx.x == 0);
-    walk.init(a, loc.w0, loc.w1, loc.b, loc.start);
+    walk.init(a, loc.w0, loc.w1, loc.snap, loc.b, loc.start);
     if (tid < 2) a.part_info[blockIdx.x * 2 + tid] = make_int4(0, 0, 0, 0);
 
     const int ngrp = (a.G + a.p.gs - 1) / a.p.gs;          // head groups of a kv head

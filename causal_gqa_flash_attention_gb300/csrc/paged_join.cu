@@ -176,6 +176,8 @@ PagedSplit paged_split(PagedKind kind, int D, int Hkv, int G, int cap) {
             rows(kind == PAGED_SHORT16 ? 16 : 32);
             tile(paged_short_bn(D));
             p.C = 2 * kSms;
+            p.snap = 3;                                    // (64 sequences of 2048: 31.4 -> 30.5 us)
+            p.snap_shift = p.bn_shift + 2;                 // but a quarter of a CTA's share at most
             break;
         case PAGED_F32_FEW4:
         case PAGED_F32_FEW8:
@@ -203,6 +205,7 @@ PagedSplit paged_split(PagedKind kind, int D, int Hkv, int G, int cap) {
             p.w_part = 4;
             p.ovh = 1024;
             p.min_shift = 11;
+            p.snap = 1;                                    // (a prompt of 2048 at D 128: 35.4 -> 34.0 us)
             break;
     }
     // Contexts of at most 256 positions: a unit's keys take less time than the join would.

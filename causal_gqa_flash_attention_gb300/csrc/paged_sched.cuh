@@ -6,8 +6,8 @@
 // the new tokens).  A unit costs ovh + kv(r) keys.  The units stand in one line, sequence
 // by sequence, head group by head group, tile by tile; CTA c of C takes the interval
 // [W c / C, W (c + 1) / C) of the total W and walks the units that it touches.  A unit that
-// an interval's end cuts is cut at the key tile nearest to it; both sides compute that tile
-// alike.  So every CTA has the same work whatever the lengths (one sequence of 100,000
+// an interval's end cuts is cut at the key tile nearest to it (or not at all, where that leaves
+// a part too small for its ends); both sides compute that tile alike.  So every CTA has the same work whatever the lengths (one sequence of 100,000
 // positions beside fifty of ten, a prompt beside single tokens), no list is built, and the
 // split depends on the lengths alone, never on timing.
 //
@@ -91,6 +91,7 @@ struct PagedSeg {
 struct PagedWalk {
     long long w0, w1;   // the CTA's interval
     long long cur;      // start of the current unit
+    int snap;           // a cut this near to a unit's end, in tiles, moves there
     PagedSeq q;
     PagedRaw ahead;     // the next sequence's, fetched while this one is walked
     int b, hg, r, nt;
@@ -110,8 +111,9 @@ struct PagedWalk {
         take(a);
     }
     // From the sequence that holds w0 (q, set by the caller or by load) and where it starts.
-    __device__ __forceinline__ void init(const PagedAttnArgs& a, long long w0_, long long w1_, int b_, long long start,
-                                         bool loaded = false) {
+    __device__ __forceinline__ void init(const PagedAttnArgs& a, long long w0_, long long w1_, int snap_, int b_,
+                                         long long start, bool loaded = false) {
+        snap = snap_;
         w0 = w0_;
         w1 = w1_;
         b = b_;
@@ -161,7 +163,8 @@ struct PagedWalk {
             const float per = __fdividef((float)ntk, (float)cost);
             auto cut = [&](long long x) -> int {
                 if (a.p.nocut) return 2 * x >= cost ? ntk : 0;
-                return min(ntk, __float2int_rn(__fmul_rn((float)x, per)));
+                const int c = min(ntk, __float2int_rn(__fmul_rn((float)x, per)));
+                return c <= snap ? 0 : ntk - c <= snap ? ntk : c;
             };
             g.t0 = w0 <= cur ? 0 : cut(w0 - cur);
             g.t1 = w1 >= cur + cost ? ntk : cut(w1 - cur);
@@ -203,11 +206,17 @@ __device__ __forceinline__ void paged_interval(const PagedSplit& p, long long to
     }
 }
 
+// Parts of up to so many tiles are not worth their ends (a join more, a unit more to begin):
+// at most p.snap, and less than the share of a CTA in a small call.
+__device__ __forceinline__ int paged_snap(const PagedSplit& p, long long total) {
+    return (int)min((long long)p.snap, (long long)__umul64hi((unsigned long long)total, p.inv_C) >> p.snap_shift);
+}
+
 // Shared scratch of paged_locate.
 struct PagedLocate {
     long long warp_sum[32];
     long long w0, w1, start;
-    int b;
+    int b, snap;
 };
 
 // All T threads of the CTA: the total work, this CTA's interval, and the sequence that its
@@ -258,6 +267,7 @@ __device__ __forceinline__ void paged_locate(const PagedAttnArgs& a, int c, Page
         sm.w1 = w1;
         sm.start = 0;
         sm.b = 0;
+        sm.snap = paged_snap(a.p, total);
     }
     __syncthreads();
     const long long w0 = sm.w0, w1 = sm.w1;
@@ -327,7 +337,7 @@ __device__ __forceinline__ void paged_locate_warp(const PagedAttnArgs& a, int c,
         start += __shfl_sync(0xffffffffu, x, 31);
     }
     if (report && bad) report_error(a.err, bad);
-    walk.init(a, w0, w1, b, start, true);
+    walk.init(a, w0, w1, paged_snap(a.p, total), b, start, true);
 }
 
 // The records of both slots of CTA c are written by every call (state 0: no such part).

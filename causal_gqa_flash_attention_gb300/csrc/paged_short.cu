@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_short_kernel(const PagedAtt
     if (warp == 0) {
         PagedSeg n;
         if (a.s.B <= 32) paged_locate_warp(a, blockIdx.x, walk, blockIdx.x == 0);
-        else walk.init(a, loc.w0, loc.w1, loc.b, loc.start);
+        else walk.init(a, loc.w0, loc.w1, loc.snap, loc.b, loc.start);
         if (lane < 2) a.part_info[blockIdx.x * 2 + lane] = make_int4(0, 0, 0, 0);
         if (!walk.next(a, n)) n.b = -1;
         if (lane == 0) s_part[0] = n;

@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(384, 1)
         if (lane < 2) a.part_info[blockIdx.x * 2 + lane] = make_int4(0, 0, 0, 0);
         PagedWalk walk;
         if (a.s.B <= 32) paged_locate_warp(a, blockIdx.x, walk, blockIdx.x == 0);
-        else walk.init(a, loc.w0, loc.w1, loc.b, loc.start);
+        else walk.init(a, loc.w0, loc.w1, loc.snap, loc.b, loc.start);
         bool more = true;
         for (int k = 0; more; ++k) {
             const int s = k % kSegs;

@@ -201,7 +201,7 @@ def test_binding_refuses_host_tensors_and_mismatches(lib):
 class Split:
     """How the attention kernels cut a call, step by step as in paged_sched.cuh."""
 
-    def __init__(self, n, lens, Hkv, G, rows, bn, C, ovh=384, min_work=128, w_full=1, w_part=1, sub=0):
+    def __init__(self, n, lens, Hkv, G, rows, bn, C, ovh=384, min_work=128, w_full=1, w_part=1, sub=0, snap=0, snap_shift=0):
         self.n, self.lens, self.bn, self.ovh = n, lens, bn, ovh
         self.gs = min(G, rows)
         self.tpt = rows // self.gs
@@ -216,6 +216,7 @@ class Split:
         self.start = np.concatenate([[0], np.cumsum([ovh + u[3] * u[4] for u in units])]).astype(object)
         W = int(self.start[-1])
         self.C = C
+        self.snap = min(snap, (W * ((2 ** 64 - 1) // C) >> 64) >> snap_shift)
         if W < C * min_work:
             self.w = [min(c * min_work, W) for c in range(C + 1)]
         else:
@@ -229,8 +230,12 @@ class Split:
             if u0 + cost <= w0 or u0 >= w1:
                 continue
             per = np.float32(nt) / np.float32(cost)
-            t0 = 0 if w0 <= u0 else min(nt, int(np.rint(np.float32(w0 - u0) * per)))
-            t1 = nt if w1 >= u0 + cost else min(nt, int(np.rint(np.float32(w1 - u0) * per)))
+
+            def cut(x):
+                c = min(nt, int(np.rint(np.float32(x) * per)))
+                return 0 if c <= self.snap else nt if nt - c <= self.snap else c
+            t0 = 0 if w0 <= u0 else cut(w0 - u0)
+            t1 = nt if w1 >= u0 + cost else cut(w1 - u0)
             if t0 < t1 or (nt == 0 and w0 <= u0):
                 out.append((b, hg, r, t0, t1, nt))
         return out
@@ -240,8 +245,8 @@ class Split:
 def test_split_covers_every_key_tile_once_and_parts_can_be_joined(seed):
     rng = random.Random(seed)
     G, Hkv = rng.choice([1, 2, 3, 5, 8, 20]), rng.choice([1, 2, 4])
-    rows, bn, C, more = rng.choice([(16, 64, 304, {}), (32, 128, 304, {}), (8, 256, 152, {}), (64, 32, 304, {}),
-                                    (256, 128, 152, dict(ovh=1024, min_work=2048, w_full=5, w_part=4, sub=128 // G))])
+    rows, bn, C, more = rng.choice([(16, 64, 304, dict(snap=3, snap_shift=8)), (32, 128, 304, dict(snap=3, snap_shift=9)), (8, 256, 152, {}), (64, 32, 304, {}),
+                                    (256, 128, 152, dict(ovh=1024, min_work=2048, w_full=5, w_part=4, sub=128 // G, snap=1))])
     B = rng.randint(1, 9)
     n = [rng.choice([0, 1, 1, rng.randint(1, 60)]) for _ in range(B)]
     lens = [rng.choice([0, 1, rng.randint(1, 200), rng.randint(1, 9000)]) for _ in range(B)]
