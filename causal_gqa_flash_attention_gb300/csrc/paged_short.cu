@@ -17,8 +17,8 @@
 // ring keeps 2 x 8 KB of loads per warp in flight, 128 KB per SM: bandwidth times latency is
 // about 45 KB.
 //
-// Measured (GB300): 8 sequences x 65536 positions, 12/4 heads of 64, 86.5 us with the join,
-// 6.2 TB/s (92% of the 6.78 TB/s copy); x 16384 29.5-30.0 us (19.8 at the copy rate): 2.8 us to
+// Measured (GB300): 8 sequences x 65536 positions, 12/4 heads of 64, 87.5 us with the join,
+// 6.1 TB/s (90% of the 6.78 TB/s copy); x 16384 29.5-30.0 us (19.8 at the copy rate): 2.3 us to
 // find the shares, 21 us of reading, the spread of the CTAs' ends and 3 us of join.  More CTAs
 // than fit at once (36 us at three per SM), 16-key steps, 2 or 4 stages, a warm-up pass through
 // the code and an L2 prefetch of the page table measured no better; cache hints on the copies

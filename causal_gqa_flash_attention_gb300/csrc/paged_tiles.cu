@@ -10,8 +10,9 @@
 //
 // Per unit and key tile, 4 * 256 * 128 * D flops against 512 D bytes: 16 D cycles of the tensor
 // core (8192 dense bf16 flops a cycle) and 1024 of the exponential units (32 results a cycle),
-// so products bound D 128 and exponentials come close to them at D 64.  The two subtiles alternate: while the softmax warps of one work on its S tile, the
-// tensor core runs the other's PV and next S.  Roles (12 warps):
+// so products bound D 128 and exponentials come close to them at D 64.  The two subtiles
+// alternate: while the softmax warps of one work on its S tile, the tensor core runs the other's
+// PV and next S.  Roles (12 warps):
 //   warp 0       producer: Q pair of the unit, then K and V tiles through an NS-slot ring.
 //   warp 1       UMMA issuer (owns the 512 TMEM columns); at D 64 one of two, warp 2 the other, each
 //                for a subtile.  Per tile t: O_u += P_u(t) V(t) once P_u(t) is there, and S_u(t + 1) =
