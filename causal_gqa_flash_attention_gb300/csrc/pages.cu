@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1) pages_plan_kernel(const PagesArgs
     constexpr int GT = kCluster * kThreads;
     griddep_launch_dependents();
     griddep_wait();
+    if constexpr (OP != PAGES_RESIZE) cl.sync();           // every CTA runs before one writes into its shared memory
     int lo, hi;
     share(a.n_pages, me, lo, hi);
     // The counts, where the outputs are another array.
