@@ -34,6 +34,26 @@ __device__ __forceinline__ void load_rows(uint32_t sk, uint32_t sv, const char* 
                                           int esize, int r0, int first, int kv_end, int pid, int lane) {
     constexpr int PER = 32 / U > 0 ? 32 / U : 1;           // rows per pass of the warp
     const int mask = (1 << c.ps_shift) - 1;
+    // All rows there (any step but a sequence's last): an address per eight rows, which lie in one
+    // page, and additions from it (a step of 24 rows over 16384 positions: 37.5 -> 36.1 us).
+    if constexpr (ROWS >= 8 && PER <= 8) {                 // (first is a multiple of 8 then)
+        if (__all_sync(0xffffffffu, pid >= 0 || lane >= ROWS)) {
+            const long long tok_bytes = c.tok_stride * esize;
+            const long long lane_off = (lane / U) * tok_bytes + (lane % U) * 16;
+#pragma unroll
+            for (int x = 0; x < ROWS; x += 8) {
+                long long off = (long long)__shfl_sync(0xffffffffu, pid, x) * c.page_stride * esize +
+                                ((first + x) & mask) * tok_bytes + lane_off;
+#pragma unroll
+                for (int i = 0; i < 8; i += PER, off += PER * tok_bytes) {
+                    const uint32_t at = tile_unit<U>(r0 + x + i + lane / U, lane % U) * 16;
+                    cp_async16(sk + at, k + off, true);
+                    cp_async16(sv + at, v + off, true);
+                }
+            }
+            return;
+        }
+    }
 #pragma unroll
     for (int i = 0; i < ROWS; i += PER) {
         const int r = i + lane / U, u = lane % U;          // (ROWS >= PER)
