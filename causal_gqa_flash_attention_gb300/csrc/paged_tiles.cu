@@ -391,6 +391,7 @@ __global__ void __launch_bounds__(384, 1)
     } else if (warp == 3) {
         // ------------------------------------------------------------ the CTA's parts
         if (lane < 2) a.part_info[blockIdx.x * 2 + lane] = make_int4(0, 0, 0, 0);
+        __syncwarp();                                      // both in front of lane 0's arrivals, and so of any record
         PagedWalk walk;
         if (a.s.B <= 32) paged_locate_warp(a, blockIdx.x, walk, blockIdx.x == 0);
         else walk.init(a, loc.w0, loc.w1, loc.snap, loc.b, loc.start);
