@@ -364,6 +364,16 @@ ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
 ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "parts": 3}
 
 
+_INT_MAX = 2 ** 31 - 1
+
+
+def _c_ints(**values):
+    """Refuses what a C int does not hold: ctypes passes on the low 32 bits of any int."""
+    for name, x in values.items():
+        if not -_INT_MAX <= x <= _INT_MAX:
+            raise ValueError(f"{name} = {x} does not fit into 32 bits")
+
+
 def rope_spec(D: int, rot_dim: int | None = None, theta: float = 10000.0, layout: str = "interleaved",
               scaling: str = "none", factor: float = 1.0, orig_len: int = 0, beta_fast: float = 32.0,
               beta_slow: float = 1.0, mscale: float = 1.0) -> RopeSpec:
@@ -373,8 +383,10 @@ def rope_spec(D: int, rot_dim: int | None = None, theta: float = 10000.0, layout
     longer than trained.  A host value: make it once and keep it."""
     if layout not in ROPE_LAYOUTS or scaling not in ROPE_SCALINGS:
         raise ValueError(f"layout must be one of {tuple(ROPE_LAYOUTS)}, scaling one of {tuple(ROPE_SCALINGS)}")
+    rot_dim = D if rot_dim is None else rot_dim
+    _c_ints(D=D, rot_dim=rot_dim, orig_len=orig_len)
     out = RopeSpec()
-    _check(load().ne_rope_spec_init(ctypes.byref(out), D, D if rot_dim is None else rot_dim, ROPE_LAYOUTS[layout],
+    _check(load().ne_rope_spec_init(ctypes.byref(out), D, rot_dim, ROPE_LAYOUTS[layout],
                                     float(theta), ROPE_SCALINGS[scaling], float(factor), orig_len, float(beta_fast),
                                     float(beta_slow), float(mscale)))
     return out
@@ -453,6 +465,8 @@ def _paged_batch(page_table, seq_lens, cu_new, N, dev):
     if len(shape) != 2:
         raise ValueError("page_table must be [B, max_pages]")
     B, W = shape
+    if (B | W | N) > _INT_MAX:
+        _c_ints(sequences=B, max_pages=W, rows=N)
     if cu_new is None and N != B:
         raise ValueError(f"without cu_new every sequence has one row: {N} rows for {B} sequences")
     return (B, W, _ints(page_table, shape, dev, "page_table"), _ints(seq_lens, (B,), dev, "seq_lens"),
@@ -477,6 +491,8 @@ def paged_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_new=None, rope
     seq_lens[b] - n_b .. seq_lens[b] - 1 of its pages, k rotated by `rope` (a rope_spec, None:
     not).  With q [N, Hq, D] the query rows are rotated into q_out (which may be q), returned.
     Row slices of one fused projection are taken as they are."""
+    if not 0 <= pos_offset <= _INT_MAX:
+        _c_ints(pos_offset=pos_offset)
     lib = _lib or load()
     c, dev, dt, _, Hkv, D = _paged_cache(k_pages, v_pages, False)
     N = k.shape[0]
@@ -499,6 +515,7 @@ def paged_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_new=None, rope
 
 
 def paged_workspace_size(B, N, Hq, Hkv, D) -> int:
+    _c_ints(B=B, N=N, Hq=Hq, Hkv=Hkv, D=D)
     return int(load().ne_paged_attn_workspace_size(B, N, Hq, Hkv, D))
 
 
@@ -514,6 +531,8 @@ def paged_attn(q, k_pages, v_pages, page_table, seq_lens, cu_new=None, max_new: 
     seq_lens[b] - n_b + i + 1 positions.  Returns (o [N, Hq, D], lse [N, Hq] fp32); rows
     outside the sequences are not written (zeros in a fresh o and lse).  max_new: the most
     new tokens of a sequence, if known (a choice of kernel, not of results)."""
+    if max_new is not None and not 1 <= max_new <= _INT_MAX:
+        _c_ints(max_new=max_new)
     lib = _lib or load()
     c, dev, dt, _, Hkv, D = _paged_cache(k_pages, v_pages, False)
     N, Hq = q.shape[:2]
@@ -538,6 +557,7 @@ def paged_attn(q, k_pages, v_pages, page_table, seq_lens, cu_new=None, max_new: 
 
 def alloc_pages_workspace(n_pages: int, n: int, max_pages: int, device="cuda"):
     """Workspace of pages_* calls over a pool of n_pages and tables of n sequences (a fork: children)."""
+    _c_ints(n_pages=n_pages, n=n, max_pages=max_pages)
     return torch.empty(max(int(load().ne_pages_workspace_size(n_pages, n, max_pages)), 256), dtype=torch.uint8,
                        device=device)
 
@@ -564,6 +584,8 @@ def pages_fork(refcount, page_table, seq_lens, parents, k_pages, v_pages, deep: 
         raise ValueError("page_table must be [B, max_pages] and parents [C]")
     B, W = page_table.shape
     C = parents.shape[0]
+    if (B | W | C) > _INT_MAX:
+        _c_ints(sequences=B, max_pages=W, children=C)
     refcount_out, ro = _out_ints(refcount_out, P, dev, "refcount_out", refcount)
     child_table, ct = _out_ints(child_table, (C, W), dev, "child_table", refcount)
     child_lens, cl = _out_ints(child_lens, (C,), dev, "child_lens", refcount)
@@ -587,6 +609,8 @@ def pages_resize(refcount, page_table, seq_lens, new_lens, k_pages, v_pages, ref
     if len(T) != 2:
         raise ValueError("page_table must be [B, max_pages]")
     B, W = T
+    if (B | W) > _INT_MAX:
+        _c_ints(sequences=B, max_pages=W)
     refcount_out, ro = _out_ints(refcount_out, P, dev, "refcount_out", refcount)
     table_out, to = _out_ints(table_out, T, dev, "table_out", refcount)
     short, sh = _out_ints(short, (1,), dev, "short", refcount)
@@ -609,6 +633,8 @@ def pages_compact(refcount, page_table, k_pages, v_pages, refcount_out=None, tab
     if len(T) != 2:
         raise ValueError("page_table must be [B, max_pages]")
     B, W = T
+    if (B | W) > _INT_MAX:
+        _c_ints(sequences=B, max_pages=W)
     refcount_out, ro = _out_ints(refcount_out, P, dev, "refcount_out", refcount)
     table_out, to = _out_ints(table_out, T, dev, "table_out", refcount)
     remap, rm = _out_ints(remap, P, dev, "remap", refcount)
