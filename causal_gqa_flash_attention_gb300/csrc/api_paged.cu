@@ -1,6 +1,7 @@
 // api_paged.cu -- the paged-cache entry points of include/neattn.h: argument validation,
 // kernel choice and launches.  Every step runs in the kernels.
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 
@@ -383,7 +384,7 @@ ne_status ne_rope_spec_init(ne_rope_spec* out, int D, int rot_dim, int layout, d
         return fail(NE_ERR_INVALID_ARG, "rot_dim must be even, 2 to D (rot_dim=%d D=%d)", rot_dim, D);
     if (layout != 0 && layout != 1) return fail(NE_ERR_INVALID_ARG, "layout must be 0 (interleaved) or 1 (half)");
     if (!(theta > 0.0) || !std::isfinite(theta)) return fail(NE_ERR_INVALID_ARG, "theta must be finite and > 0");
-    if (!std::isfinite(mscale)) return fail(NE_ERR_INVALID_ARG, "mscale must be finite");
+    if (!(std::fabs(mscale) <= FLT_MAX)) return fail(NE_ERR_INVALID_ARG, "mscale must be finite in fp32");
     if (scaling < NE_ROPE_NONE || scaling > NE_ROPE_PARTS) return fail(NE_ERR_INVALID_ARG, "unknown scaling %d", scaling);
     if (scaling != NE_ROPE_NONE && (!(factor > 0.0) || !std::isfinite(factor)))
         return fail(NE_ERR_INVALID_ARG, "factor must be finite and > 0");
@@ -391,13 +392,15 @@ ne_status ne_rope_spec_init(ne_rope_spec* out, int D, int rot_dim, int layout, d
     if (scaling == NE_ROPE_PARTS && (orig_len < 1 || !(beta_fast > beta_slow) || !std::isfinite(beta_fast) ||
                                      !std::isfinite(beta_slow)))
         return fail(NE_ERR_INVALID_ARG, "scaling by parts needs orig_len >= 1 and finite beta_fast > beta_slow");
-    *out = ne_rope_spec();
-    out->D = D;
-    out->rot_dim = rot_dim;
-    out->layout = layout;
-    out->mscale = (float)mscale;
     double base = theta;
     if (scaling == NE_ROPE_BASE) base = theta * std::pow(factor, rot_dim / (rot_dim - 2.0));
+    if (!(base > 0.0) || !std::isfinite(base))
+        return fail(NE_ERR_INVALID_ARG, "the scaled base theta * factor^(rot_dim / (rot_dim - 2)) must be finite and > 0 (%g)", base);
+    ne_rope_spec spec = ne_rope_spec();
+    spec.D = D;
+    spec.rot_dim = rot_dim;
+    spec.layout = layout;
+    spec.mscale = (float)mscale;
     for (int i = 0; i < rot_dim / 2; ++i) {
         double f = std::pow(base, -2.0 * i / rot_dim);
         if (scaling == NE_ROPE_LINEAR) f /= factor;
@@ -406,13 +409,15 @@ ne_status ne_rope_spec_init(ne_rope_spec* out, int D, int rot_dim, int layout, d
             const double g = std::min(1.0, std::max(0.0, (n - beta_slow) / (beta_fast - beta_slow)));
             f *= g + (1.0 - g) / factor;
         }
+        if (!std::isfinite(f)) return fail(NE_ERR_INVALID_ARG, "the frequency of pair %d is not finite (%g)", i, f);
         // Turns per position, whole turns dropped, in units of 2^-64.
         double t = f / kTwoPi;
         t -= std::floor(t);
         const double hi = std::floor(t * 4294967296.0);    // two exact halves of the 64-bit fraction
         const double lo = std::floor((t * 4294967296.0 - hi) * 4294967296.0 + 0.5);
-        out->turns[i] = ((uint64_t)hi << 32) + (uint64_t)lo;
+        spec.turns[i] = ((uint64_t)hi << 32) + (uint64_t)lo;
     }
+    *out = spec;
     return NE_OK;
 }
 

@@ -306,7 +306,8 @@ typedef struct {
  *                  the trained context: fast pairs keep their angle, slow ones interpolate.
  * cos and sin are multiplied by mscale.  The angle is kept as a 64-bit fraction of a turn
  * (turns[i] = f_i / (2 pi) * 2^64), so p * turns[i] mod 2^64 is exact for every position:
- * far positions lose nothing and no table is built. */
+ * far positions lose nothing and no table is built.  Refused: parameters that leave an angle
+ * (or the scaled theta) infinite or no number, and an mscale beyond fp32. */
 enum { NE_ROPE_NONE = 0, NE_ROPE_LINEAR = 1, NE_ROPE_BASE = 2, NE_ROPE_PARTS = 3 };
 typedef struct {
     int D, rot_dim, layout;
