@@ -14,7 +14,7 @@
 // Measured (GB300, both kernels): compaction of 4096 pages x 16 layers, 411 MB, 72.5 us, 5.7 TB/s
 // (84% of the copy rate); private copies of eight sequences of 2048 x 16 layers 49.5 us, 5.2
 // TB/s; a sweep over 1024 sequences of a pool of 131072 pages 25.5 us; 64 sequences one token
-// longer 11.8 us.
+// longer 12.0 us (0.2 of it looking at the ids of the pages that stay).
 #include <cooperative_groups.h>
 #include "paged.h"
 #include "ptx.cuh"
@@ -387,15 +387,16 @@ __global__ void __launch_bounds__(kBulkThreads) pages_bulk_kernel(const PagesArg
         const int s = (int)fast_div(i, a.div_w), e = (int)(i - (uint32_t)s * (uint32_t)a.W);
         if (OP == PAGES_COMPACT) {
             const int p = a.table[i];
-            if (p >= a.n_pages) report_error(a.err, SITE_PAGED_PAGE);
+            if (p != -1 && !page_ok(a, p)) report_error(a.err, SITE_PAGED_PAGE);   // (-1: no page)
             a.table_out[i] = page_ok(a, p) ? a.lens_out[p] : -1;
         } else if (OP == PAGES_FORK) {
-            if (missing) {
+            const Take t = take_fork(a, s);
+            if (missing) {                                 // (its ids are looked at all the same)
+                if (e < t.first + t.count && !page_ok(a, a.table[(size_t)t.parent * a.W + e])) report_error(a.err, SITE_PAGED_PAGE);
                 a.table_out[i] = -1;
                 if (e == 0) a.lens_out[s] = 0;
                 continue;
             }
-            const Take t = take_fork(a, s);
             int v = -1;
             if (e >= t.first && e < t.first + t.count) {
                 v = a.free_ids[a.off[s].x + e - t.first];
@@ -412,17 +413,18 @@ __global__ void __launch_bounds__(kBulkThreads) pages_bulk_kernel(const PagesArg
             if (e == 0) a.lens_out[s] = t.len;
         } else {
             const int v = a.table[i];
-            if (missing) {
-                a.table_out[i] = v;
-                continue;
-            }
-            const int2 off = a.off[s];
+            const int2 off = a.off[s];                     // (not written, nor used, when pages are missing)
             const int old = clamp_len(a.lens[s], a.cap, nullptr), now = clamp_len(a.other[s], a.cap, nullptr);
             const int po = (old + a.ps - 1) >> a.ps_shift, pn = (now + a.ps - 1) >> a.ps_shift;
-            const int split = off.y >= 0 ? 1 : 0;
             int out = -1;
-            if (e < min(po, pn)) out = split && e == (min(old, now) >> a.ps_shift) ? a.free_ids[off.x] : v;
-            else if (e >= po && e < pn) out = a.free_ids[off.x + split + e - po];
+            if (e < min(po, pn)) {                         // kept (those given back: in the first kernel)
+                if (!page_ok(a, v)) report_error(a.err, SITE_PAGED_PAGE);
+                out = !missing && off.y >= 0 && e == (min(old, now) >> a.ps_shift) ? a.free_ids[off.x] : v;
+            } else if (missing) {
+                out = v;
+            } else if (e >= po && e < pn) {
+                out = a.free_ids[off.x + (off.y >= 0 ? 1 : 0) + e - po];
+            }
             a.table_out[i] = out;
         }
     }

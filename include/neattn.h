@@ -382,7 +382,10 @@ ne_status ne_paged_attn_f32(const float* q, const ne_paged_cache* cache, const i
  * step can be captured.  page_table entries behind a sequence's pages are -1 on output.
  * workspace: ne_pages_workspace_size(n_pages, n, max_pages) bytes, n the number of
  * sequences (for a fork: of children), 256-byte aligned, caller-owned, rewritten by every call.  refcount
- * and refcount_out are 16-byte aligned, the other int arrays 4-byte.  Bad ids are skipped and reported by ne_get_device_error().
+ * and refcount_out are 16-byte aligned, the other int arrays 4-byte.  A table entry in front of a
+ * sequence's length (compact: any entry but -1) that is no page of the pool is reported by
+ * ne_get_device_error(), whether the call is short or not: it is neither counted nor copied,
+ * a resize keeps it as it is, a fork and a compaction write -1 for it.
  *
  * ne_pages_fork: child c continues sequence parents[c] (-1: an empty child).  Shared
  * (deep == 0): whole pages are shared (their counts rise), the partly filled last page is
