@@ -357,7 +357,10 @@ ne_status ne_paged_append_f32(const float* q, const float* k, const float* v, co
  * kernels (a few rows per kv head stream the cache through registers; more use tcgen05
  * tiles) and changes no result beyond rounding: any n_b is right with any max_new >= 1.
  * bf16: tensor-core products of bf16 inputs with fp32 accumulation and fp32 softmax
- * statistics; f32: fp32 throughout (no TF32).  Work is split over the key axis by counted
+ * statistics.  The weights of the product with V are rounded: the kernels for a few rows (max_new
+ * times Hq / Hkv up to 32; any max_new at D 32 or above 128 heads per kv head) keep two bf16 terms
+ * of each, off by at most 2^-16 of it, the tcgen05 tiles one, 2^-8, as the training forward does;
+ * so o is off by that much of sum p |v| beside its own rounding.  f32: fp32 throughout (no TF32).  Work is split over the key axis by counted
  * work, so results depend on the shape, lengths and device but never on timing: the same
  * call gives the same bits.  o and lse overlap neither q nor each other.  workspace:
  * ne_paged_attn_workspace_size() bytes (10 to 40 MB, whatever B and N), 256-byte
