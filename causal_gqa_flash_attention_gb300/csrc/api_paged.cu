@@ -209,6 +209,7 @@ ne_status tile_maps(CUtensorMap* tq, CUtensorMap* tk, CUtensorMap* tv, const ne_
     return encode(tv, a.c.v, 4, kd, ks, kb);
 }
 
+// Bytes of a call's workspace: the largest over the kernels that its head_dim and heads may run.
 size_t attn_ws_bytes(int D, int Hkv, int G) {
     size_t most = 0;
     for (int f32 = 0; f32 < 2; ++f32)

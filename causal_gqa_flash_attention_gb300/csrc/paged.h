@@ -98,7 +98,7 @@ enum PagedKind : int { PAGED_SHORT16 = 0, PAGED_SHORT32, PAGED_F32_FEW4, PAGED_F
 PagedKind paged_kind(bool f32, int D, int G, int max_new);
 // cap: the longest length the page tables can hold.
 PagedSplit paged_split(PagedKind kind, int D, int Hkv, int G, int cap);
-// Bytes of a call's workspace: the largest over the kernels its type and shape may run.
+// Bytes of the workspace that a split takes.
 size_t paged_part_bytes(const PagedSplit& p, int D);
 
 cudaError_t launch_paged_append(bool f32, const AppendArgs& a, const RopeTurns& t, cudaStream_t st);

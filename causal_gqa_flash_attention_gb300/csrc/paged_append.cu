@@ -8,9 +8,11 @@
 // warp's heads.  Bound: every row is read once and written once, 2 (Hq + 2 Hkv) D elements
 // per token at the copy bandwidth; a step of a few tokens is latency (find the token's
 // sequence, its page, then one load and one store).
-// Measured (GB300): 6250 tokens, 16 + 2 x 4 heads of 128, half of each head rotated in halves:
-// 13.8 us, 5.6 TB/s (82% of the copy rate); 32768 tokens 64.5 us (92%); 16 tokens of 12 + 2 x 4
-// heads of 64: 3.1 us.
+// Measured (GB300), inputs and pages from DRAM: 6250 tokens, 16 + 2 x 4 heads of 128, half of each
+// head rotated in halves: 18.6 us, 4.1 TB/s (61% of the copy rate: 1.3 waves of one warp per token,
+// each of which loads its next heads only when it has stored the last; 14 us where the L2 holds
+// everything); 2048 tokens 8.1 us (3.7 at the copy rate); 32768 tokens 65 us (91%).  fp32, heads of
+// 64: 17.0 and 62 us (6250 and 32768 tokens, 67% and 96%).  16 tokens of 12 + 2 x 4 heads of 64: 3.2 us.
 #include <cuda_bf16.h>
 #include "paged_sched.cuh"
 

@@ -12,8 +12,8 @@
 // of three K or V tiles, and are joined at the end of a unit.  MANY: eight warps take 8 of 64
 // rows each over one shared ring.
 //
-// Measured (GB300): one step over 8 x 16384 positions, 12/4 heads of 64: 48 us, 5.6 TB/s; with
-// 32/4 heads 53 us; four new tokens each, 12/4 heads: 78 us (MANY would take 279: its warps
+// Measured (GB300): one step over 8 x 16384 positions, 12/4 heads of 64: 49 us, 5.5 TB/s; with
+// 32/4 heads 54 us; four new tokens each, 12/4 heads: 78 us (MANY would take 279: its warps
 // without rows wait); 512 new tokens over 4096 positions: 217 us, 28 TFLOP/s of the 75 that fp32
 // FMAs give.  Four warps with twice the keys in flight took 54, 64 and 99 us (a scheduler with
 // one warp waits for its chain), a ring of whole K and V steps 60, 89 and -.

@@ -7,9 +7,10 @@
 // by sequence, head group by head group, tile by tile; CTA c of C takes the interval
 // [W c / C, W (c + 1) / C) of the total W and walks the units that it touches.  A unit that
 // an interval's end cuts is cut at the key tile nearest to it (or not at all, where that leaves
-// a part too small for its ends); both sides compute that tile alike.  So every CTA has the same work whatever the lengths (one sequence of 100,000
-// positions beside fifty of ten, a prompt beside single tokens), no list is built, and the
-// split depends on the lengths alone, never on timing.
+// a part too small for its ends); both sides compute that tile alike.  So every CTA has the same
+// work whatever the lengths (one sequence of 100,000 positions beside fifty of ten, a prompt
+// beside single tokens), no list is built, and the split depends on the lengths alone, never on
+// timing.
 //
 // Parts of cut units go to the workspace: a CTA has at most one part that begins inside a
 // unit (its first, slot 0) and one that begins a unit and leaves its end to others (its
@@ -78,7 +79,7 @@ __device__ __forceinline__ long long paged_group_cost(const PagedSeq& q, const P
 // What a CTA does with one unit: key tiles [t0, t1) of nt_keys, for tokens tok .. tok+ntok-1
 // of the sequence.
 struct PagedSeg {
-    int b, hg, r;
+    int b, hg;
     int tok, ntok;      // first token of the unit within the sequence, and how many
     int tok0, base;     // the sequence's first row; position of its token 0
     int len;            // the sequence's length
@@ -170,7 +171,6 @@ struct PagedWalk {
             g.t1 = w1 >= cur + cost ? ntk : cut(w1 - cur);
             g.b = b;
             g.hg = hg;
-            g.r = r;
             g.tok = r * a.p.tpt;
             g.ntok = ntok;
             g.tok0 = q.tok0;

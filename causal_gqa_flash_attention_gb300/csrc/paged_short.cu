@@ -17,12 +17,15 @@
 // ring keeps 2 x 8 KB of loads per warp in flight, 128 KB per SM: bandwidth times latency is
 // about 45 KB.
 //
-// Measured (GB300): 8 sequences x 65536 positions, 12/4 heads of 64, 87.5 us with the join,
-// 6.1 TB/s (90% of the 6.78 TB/s copy); x 16384 29.5-30.0 us (19.8 at the copy rate): 2.3 us to
-// find the shares, 21 us of reading, the spread of the CTAs' ends and 3 us of join.  More CTAs
-// than fit at once (36 us at three per SM), 16-key steps, 2 or 4 stages, a warm-up pass through
-// the code and an L2 prefetch of the page table measured no better; cache hints on the copies
-// were taken out again (an illegal-instruction error in the fp32 kernel came with them).
+// Measured (GB300): 8 sequences x 65536 positions, 12/4 heads of 64, 86-88 us with the join (by
+// GPU), 6.1-6.3 TB/s (91% of the 6.78 TB/s copy); x 16384 29.5-30.0 us (19.8 at the copy rate): 2.3
+// us to find the shares, 21 us of reading, the spread of the CTAs' ends and 3 us of join; 16/4
+// heads of 128 50 us (39.6), 12/4 heads of 32 25 us (9.9: half the bytes for the same steps).  More
+// CTAs than fit at once (36 us at three per SM), 16-key steps, 2 or 4 stages, a warm-up pass
+// through the code and an L2 prefetch of the page table measured no better; cache hints on the
+// copies were taken out again (an illegal-instruction error in the fp32 kernel came with them).
+// Chunks at head_dim 32 or with more than 128 heads per kv head come here too, whatever their
+// rows: 2048 tokens over 16384 at head_dim 32 300 us, 0.16 PFLOP/s (the tile kernel has neither).
 #include <cuda_bf16.h>
 #include "paged_load.cuh"
 #include "paged_sched.cuh"

@@ -28,10 +28,12 @@
 // is full, in columns of its own at D 64.
 // Weights are rounded to bf16 for the product (half a step, 2^-8 of each weight, as the
 // training forward does); maximum and sum stay fp32, and the sum is of the unrounded weights.
-// Measured (GB300): 2048 new tokens over 16384 positions, 16/4 heads of 128: 182 us with the join,
-// 1.41 PFLOP/s (75% of the 1.89 measured for a bf16 GEMM), the tensor pipe 63% busy: a subtile's
-// chain, PV + S on the tensor core (0.54 us) and its softmax (0.7 us, then waits), takes 1.45 us per
-// tile, longer than both subtiles' tensor work.  12/4 heads of 64: 100 us, 0.96 PFLOP/s.  With one
+// Measured (GB300): 2048 new tokens over 16384 positions, 16/4 heads of 128, pages of 64: 185 us
+// with the join, 1.39 PFLOP/s (73% of the 1.89 measured for a bf16 GEMM; 182 us with the cache in
+// the L2, 192 with pages of 16, where a tile takes 8 boxes of each kind), the tensor pipe 63% busy:
+// a subtile's chain, PV + S on the tensor core (0.54 us) and its softmax (0.7 us, then waits), takes 1.45 us per
+// tile, longer than both subtiles' tensor work.  12/4 heads of 64: 102 us, 0.94 PFLOP/s (100 in
+// the L2; pages of 16: 110).  With one
 // issuer for both subtiles that took 122 us: waiting for one subtile's P it could not start the
 // other's S, which tied the two softmaxes to the same phase.  At D 128 two issuers are slower (196
 // us): the tensor core is the longer half there, and two streams of UMMAs delay each other.
@@ -81,12 +83,12 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Transposes a 4 x 4 block of 16-byte units held by four neighbouring lanes: afterwards lane l
-// of the four holds unit l of each of them.
 __device__ __forceinline__ uint4 shfl_xor4(const uint4& v, int m) {
     return make_uint4(__shfl_xor_sync(0xffffffffu, v.x, m), __shfl_xor_sync(0xffffffffu, v.y, m),
                       __shfl_xor_sync(0xffffffffu, v.z, m), __shfl_xor_sync(0xffffffffu, v.w, m));
 }
+// Transposes a 4 x 4 block of 16-byte units held by four neighbouring lanes: afterwards lane l
+// of the four holds unit l of each of them.
 __device__ __forceinline__ void transpose4(uint4 (&v)[4], int l) {
     const uint4 a = shfl_xor4(l & 1 ? v[0] : v[1], 1), b = shfl_xor4(l & 1 ? v[2] : v[3], 1);
     if (l & 1) {

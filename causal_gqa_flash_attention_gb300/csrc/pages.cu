@@ -11,10 +11,10 @@
 // Bound: the bookkeeping reads the counts two or three times out of the L2 (4 bytes per
 // page) and is latency otherwise: a handful of cluster barriers and dependent loads.  The
 // copies read and write 2 layers x 2 x slots x Hkv x D elements at the copy bandwidth.
-// Measured (GB300, both kernels): compaction of 4096 pages x 16 layers, 411 MB, 72.5 us, 5.7 TB/s
-// (84% of the copy rate); private copies of eight sequences of 2048 x 16 layers 49.5 us, 5.2
+// Measured (GB300, both kernels): compaction of 4096 pages x 16 layers, 411 MB, 73 us, 5.6 TB/s
+// (83% of the copy rate); private copies of eight sequences of 2048 x 16 layers 49 us, 5.3
 // TB/s; a sweep over 1024 sequences of a pool of 131072 pages 25.5 us; 64 sequences one token
-// longer 12.0 us (0.2 of it looking at the ids of the pages that stay).
+// longer 11.8 us (0.15 of it looking at the ids of the pages that stay).
 #include <cooperative_groups.h>
 #include "paged.h"
 #include "ptx.cuh"

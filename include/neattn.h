@@ -363,9 +363,12 @@ ne_status ne_paged_append_f32(const float* q, const float* k, const float* v, co
  * so o is off by that much of sum p |v| beside its own rounding.  f32: fp32 throughout (no TF32).  Work is split over the key axis by counted
  * work, so results depend on the shape, lengths and device but never on timing: the same
  * call gives the same bits.  o and lse overlap neither q nor each other.  workspace:
- * ne_paged_attn_workspace_size() bytes (10 to 40 MB, whatever B and N), 256-byte
+ * ne_paged_attn_workspace_size() bytes (5 to 41 MB by D and Hq / Hkv, whatever B and N), 256-byte
  * aligned, caller-owned, rewritten by every call (two calls that may overlap need two).
- * Device-side arguments are checked as in ne_paged_append; a bad page id reads as zeros. */
+ * Device-side arguments are checked as in ne_paged_append; a bad page id reads as zeros.
+ * In a bf16 chunk a part may wait for as long as a pass of 256 rows over its keys takes, about 1.5
+ * us per 128: beyond some 1.5e8 positions raise the limit of the waits (ne_set_wait_timeout_ms), or
+ * the call ends with NE_ERR_DEVICE_TIMEOUT. */
 size_t ne_paged_attn_workspace_size(int B, int N, int Hq, int Hkv, int D);
 ne_status ne_paged_attn(const void* q, const ne_paged_cache* cache, const int* page_table, const int* seq_lens,
                         const int* cu_new, void* o, float* lse, int64_t q_ld, int B, int N, int Hq,
