@@ -38,6 +38,7 @@ EXPORTS = (
     "ne_attn_fwd_train_f32", "ne_attn_bwd_train", "ne_attn_bwd_train_f32", "ne_qkv_prologue_workspace_size",
     "ne_rope_spec_init", "ne_paged_append", "ne_paged_append_f32", "ne_paged_attn_workspace_size", "ne_paged_attn",
     "ne_paged_attn_f32", "ne_pages_workspace_size", "ne_pages_fork", "ne_pages_resize", "ne_pages_compact",
+    "ne_paged_append_at", "ne_paged_append_at_f32", "ne_pages_evict_workspace_size", "ne_pages_evict",
 )
 
 
@@ -123,12 +124,18 @@ def load(path: str | None = None):
         lib.ne_pages_fork.argtypes = [vp] * 5 + [i] + [vp] * 4 + [i] * 3 + [vp, sz, vp]
         lib.ne_pages_resize.argtypes = [vp] * 8 + [i] * 2 + [vp, sz, vp]
         lib.ne_pages_compact.argtypes = [vp] * 7 + [i] * 2 + [vp, sz, vp]
+        lib.ne_paged_append_at.argtypes = [vp] * 8 + [vp, vp] + [i64] * 4 + [i] * 4 + [vp]
+        lib.ne_paged_append_at_f32.argtypes = lib.ne_paged_append_at.argtypes
+        lib.ne_pages_evict_workspace_size.argtypes = [i] * 4
+        lib.ne_pages_evict_workspace_size.restype = sz
+        lib.ne_pages_evict.argtypes = [vp] * 7 + [i, i] + [vp] * 3 + [i, i, vp, sz, vp]
         for f in ("ne_rope_table", "ne_attn_fwd", "ne_attn_fwd_f32", "ne_attn_bwd", "ne_attn_bwd_f32",
                   "ne_get_device_error", "ne_selftest_wait_timeout", "ne_attn_bwd_noalloc", "ne_attn_decode",
                   "ne_noalloc_get_device_error", "ne_attn_fwd_varlen", "ne_attn_fwd_varlen_f32",
                   "ne_attn_bwd_varlen", "ne_attn_bwd_varlen_f32", "ne_qkv_prologue",
                   "ne_attn_decode_f32", "ne_rope_spec_init", "ne_paged_append", "ne_paged_append_f32", "ne_paged_attn",
-                  "ne_paged_attn_f32", "ne_pages_fork", "ne_pages_resize", "ne_pages_compact"):
+                  "ne_paged_attn_f32", "ne_pages_fork", "ne_pages_resize", "ne_pages_compact", "ne_paged_append_at",
+                  "ne_paged_append_at_f32", "ne_pages_evict"):
             getattr(lib, f).restype = i
         _lib = lib
     return _lib
@@ -484,16 +491,18 @@ def _rows(t, name, N, heads, D, dtype, dev):
     return s0 if N > 1 else heads * D
 
 
-def paged_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_new=None, rope=None, pos_offset: int = 0, q=None,
+def paged_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_new=None, rope=None, pos_offset=0, q=None,
                  q_out=None):
     """New tokens into the paged cache (ne_paged_append): k, v [N, Hkv, D] packed rows
     cu_new[b] .. cu_new[b+1]-1 of sequence b (None: one row each) go to positions
     seq_lens[b] - n_b .. seq_lens[b] - 1 of its pages, k rotated by `rope` (a rope_spec, None:
-    not).  With q [N, Hq, D] the query rows are rotated into q_out (which may be q), returned.
-    Row slices of one fused projection are taken as they are."""
-    if not 0 <= pos_offset <= _INT_MAX:
-        _c_ints(pos_offset=pos_offset)
+    not) at its position plus pos_offset: an int, or int32 [B] on the device, one per sequence
+    (ne_paged_append_at; what pages_evict returns).  With q [N, Hq, D] the query rows are rotated into
+    q_out (which may be q), returned.  Row slices of one fused projection are taken as they are."""
     lib = _lib or load()
+    at = isinstance(pos_offset, torch.Tensor)
+    if not at and not 0 <= pos_offset <= _INT_MAX:
+        _c_ints(pos_offset=pos_offset)
     c, dev, dt, _, Hkv, D = _paged_cache(k_pages, v_pages, False)
     N = k.shape[0]
     B, W, pt, ln, cu = _paged_batch(page_table, seq_lens, cu_new, N, dev)
@@ -508,7 +517,12 @@ def paged_append(k, v, k_pages, v_pages, page_table, seq_lens, cu_new=None, rope
         qp, qop = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out needs q")
-    _launch(lib.ne_paged_append if dt is _BF16 else lib.ne_paged_append_f32, dev, qp, k.data_ptr(), v.data_ptr(),
+    if at:
+        pos_offset = _ints(pos_offset, (B,), dev, "pos_offset")
+        fn = lib.ne_paged_append_at if dt is _BF16 else lib.ne_paged_append_at_f32
+    else:
+        fn = lib.ne_paged_append if dt is _BF16 else lib.ne_paged_append_f32
+    _launch(fn, dev, qp, k.data_ptr(), v.data_ptr(),
             c, pt, ln, cu, ctypes.byref(rope) if rope is not None else None, pos_offset, qop, q_ld, k_ld, v_ld,
             qo_ld, B, N, Hq, W)
     return q_out
@@ -644,6 +658,53 @@ def pages_compact(refcount, page_table, k_pages, v_pages, refcount_out=None, tab
             _ints(page_table, T, dev, "page_table"), ro, to, rm, nl, B, W,
             *_ws(workspace, dev))
     return refcount_out, table_out, remap, n_live
+
+
+def alloc_evict_workspace(layers: int, B: int, Hkv: int, T: int, device="cuda"):
+    """Workspace of pages_evict calls over weights [layers, B, Hkv, T] that run one after another."""
+    _c_ints(layers=layers, B=B, Hkv=Hkv, T=T)
+    return torch.empty(max(int(load().ne_pages_evict_workspace_size(layers, B, Hkv, T)), 256), dtype=torch.uint8,
+                       device=device)
+
+
+def _out_like(t, like, dev, name):
+    """Address of a contiguous output with the shape and dtype of `like`."""
+    if t.dtype is not like.dtype or t.shape != like.shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {like.dtype} CUDA tensor {list(like.shape)} on the pages' device")
+    return t.data_ptr()
+
+
+def pages_evict(weights, positions, pos_offset, page_table, seq_lens, new_lens, k_pages, v_pages, sink: int = 0,
+                recent: int = 0, weights_out=None, positions_out=None, pos_offset_out=None, workspace=None):
+    """Sequences go from seq_lens to at most new_lens positions: of every layer and kv head those
+    with the largest accumulated weight stay, after positions below `sink` and the `recent` newest
+    (ne_pages_evict).  weights fp32 and positions int32 (-1 at first) are [L, B, Hkv, T] ([B, Hkv, T] for
+    pools of one layer), T = max_pages * page_size, pos_offset int32 [B] the positions given up so
+    far.  Kept rows of the pools move into the slots below new_lens in place.  Returns
+    (weights_out, positions_out, pos_offset_out), each of which may be its input; fresh ones hold 0
+    and -1 behind the lengths.  pages_resize(seq_lens -> new_lens) then gives the pages back, and
+    paged_append takes pos_offset_out."""
+    lib = _lib or load()
+    c, dev, _, _, Hkv, _ = _paged_cache(k_pages, v_pages, True)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    B, W = page_table.shape
+    lead = tuple(k_pages.shape[:-4])
+    T = W * k_pages.shape[-3]
+    _c_ints(sequences=B, max_pages=W, T=T, sink=sink, recent=recent)
+    for t, dt, name in ((weights, _F32, "weights"), (positions, _I32, "positions")):
+        if t.dtype is not dt or t.shape != (*lead, B, Hkv, T) or t.get_device() != dev or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dt} CUDA tensor {[*lead, B, Hkv, T]} on the pages' device")
+    weights_out = torch.zeros_like(weights) if weights_out is None else weights_out
+    positions_out = torch.full_like(positions, -1) if positions_out is None else positions_out
+    pos_offset_out, po = _out_ints(pos_offset_out, (B,), dev, "pos_offset_out", page_table)
+    if workspace is None:
+        workspace = alloc_evict_workspace(lead[0] if lead else 1, B, Hkv, T, k_pages.device)
+    _launch(lib.ne_pages_evict, dev, c, weights.data_ptr(), positions.data_ptr(), _ints(pos_offset, (B,), dev, "pos_offset"),
+            _ints(page_table, (B, W), dev, "page_table"), _ints(seq_lens, (B,), dev, "seq_lens"),
+            _ints(new_lens, (B,), dev, "new_lens"), sink, recent, _out_like(weights_out, weights, dev, "weights_out"),
+            _out_like(positions_out, positions, dev, "positions_out"), po, B, W, *_ws(workspace, dev))
+    return weights_out, positions_out, pos_offset_out
 
 
 def get_device_error(device=None) -> int:

@@ -551,6 +551,10 @@ ne_status read_and_clear(int* err) {
                     "outputs of that sequence are invalid");
     if (h == ne::SITE_PAGES_PARENT)
         return fail(NE_ERR_INVALID_ARG, "a fork got a parent outside [-1, B); that child is empty");
+    if (h == ne::SITE_PAGED_GROUP)
+        return fail(NE_ERR_INVALID_ARG,
+                    "a shared-prefix call got groups outside [0, B] or decreasing, or a group whose shared positions do not "
+                    "all lie in front of its sequences' new tokens; the outputs of that group are invalid");
     return fail(NE_ERR_DEVICE_TIMEOUT, "a bounded wait inside a kernel ran out (site 0x%x)", h);
 }
 

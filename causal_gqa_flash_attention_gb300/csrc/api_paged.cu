@@ -134,8 +134,8 @@ ne_status ready(cudaStream_t st, int** err) {
 }
 
 ne_status append_impl(int eb, const void* q, const void* k, const void* v, const ne_paged_cache* c, const int* table,
-                      const int* lens, const int* cu, const ne_rope_spec* spec, int pos_offset, void* q_out, int64_t q_ld,
-                      int64_t k_ld, int64_t v_ld, int64_t qo_ld, int B, int N, int Hq, int W, ne_stream_t stream) {
+                      const int* lens, const int* cu, const ne_rope_spec* spec, int pos_offset, const int* pos_offsets, void* q_out,
+                      int64_t q_ld, int64_t k_ld, int64_t v_ld, int64_t qo_ld, int B, int N, int Hq, int W, ne_stream_t stream) {
     clear_error();
     ne_status s = check_cache(c, eb, true);
     if (s != NE_OK) return s;
@@ -176,6 +176,7 @@ ne_status append_impl(int eb, const void* q, const void* k, const void* v, const
     a.layout = spec ? spec->layout : 0;
     a.mscale = spec ? spec->mscale : 1.f;
     a.pos_offset = pos_offset;
+    a.pos_offsets = pos_offsets;
     ne::RopeTurns turns = {};
     if (spec)
         for (int i = 0; i < spec->rot_dim / 2; ++i) turns.t[i] = spec->turns[i];
@@ -372,6 +373,44 @@ ne_status pages_args(ne::PagesArgs* a, const ne_paged_cache* c, const int* ref, 
     return NE_OK;
 }
 
+// ---------------------------------------------------------------- cuts by weight
+struct EvictWs {
+    size_t list, total;
+};
+EvictWs evict_ws(size_t rows, size_t T) {
+    EvictWs w;
+    w.list = round_up(rows * 4, 256);
+    w.total = w.list + round_up(rows * T * 4, 256);
+    return w;
+}
+
+// Arrays of a call: no output overlaps anything but the input that it may be itself (same: its
+// index among the inputs, -1 for none).
+struct CallArray {
+    const void* p;
+    size_t bytes;
+    const char* name;
+    int same;
+};
+ne_status check_arrays(std::initializer_list<CallArray> in, std::initializer_list<CallArray> out) {
+    for (const auto* list : {&in, &out})
+        for (const CallArray& x : *list)
+            if (x.bytes > 0 && !aligned4(x.p))
+                return fail(NE_ERR_INVALID_ARG, "%s must be a non-null, 4-byte aligned device pointer", x.name);
+    for (const CallArray& o : out) {
+        int k = 0;
+        for (const CallArray& i : in) {
+            const bool itself = k++ == o.same && o.p == i.p;
+            if (o.bytes > 0 && i.bytes > 0 && !itself && overlap(o.p, o.bytes, i.p, i.bytes))
+                return fail(NE_ERR_INVALID_ARG, "%s must not overlap %s", o.name, i.name);
+        }
+        for (const CallArray& i : out)
+            if (&i < &o && o.bytes > 0 && i.bytes > 0 && overlap(o.p, o.bytes, i.p, i.bytes))
+                return fail(NE_ERR_INVALID_ARG, "%s must not overlap %s", o.name, i.name);
+    }
+    return NE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -426,15 +465,35 @@ ne_status ne_paged_append(const void* q, const void* k, const void* v, const ne_
                           const int* seq_lens, const int* cu_new, const ne_rope_spec* spec, int pos_offset, void* q_out,
                           int64_t q_ld, int64_t k_ld, int64_t v_ld, int64_t q_out_ld, int B, int N, int Hq, int max_pages,
                           ne_stream_t stream) {
-    return append_impl(2, q, k, v, cache, page_table, seq_lens, cu_new, spec, pos_offset, q_out, q_ld, k_ld, v_ld, q_out_ld,
-                       B, N, Hq, max_pages, stream);
+    return append_impl(2, q, k, v, cache, page_table, seq_lens, cu_new, spec, pos_offset, nullptr, q_out, q_ld, k_ld, v_ld,
+                       q_out_ld, B, N, Hq, max_pages, stream);
 }
 
 ne_status ne_paged_append_f32(const float* q, const float* k, const float* v, const ne_paged_cache* cache,
                               const int* page_table, const int* seq_lens, const int* cu_new, const ne_rope_spec* spec,
                               int pos_offset, float* q_out, int64_t q_ld, int64_t k_ld, int64_t v_ld, int64_t q_out_ld,
                               int B, int N, int Hq, int max_pages, ne_stream_t stream) {
-    return append_impl(4, q, k, v, cache, page_table, seq_lens, cu_new, spec, pos_offset, q_out, q_ld, k_ld, v_ld, q_out_ld,
+    return append_impl(4, q, k, v, cache, page_table, seq_lens, cu_new, spec, pos_offset, nullptr, q_out, q_ld, k_ld, v_ld,
+                       q_out_ld, B, N, Hq, max_pages, stream);
+}
+
+ne_status ne_paged_append_at(const void* q, const void* k, const void* v, const ne_paged_cache* cache, const int* page_table,
+                             const int* seq_lens, const int* cu_new, const ne_rope_spec* spec, const int* pos_offsets,
+                             void* q_out, int64_t q_ld, int64_t k_ld, int64_t v_ld, int64_t q_out_ld, int B, int N, int Hq,
+                             int max_pages, ne_stream_t stream) {
+    clear_error();
+    if (B > 0 && N > 0 && !aligned4(pos_offsets)) return fail(NE_ERR_INVALID_ARG, "pos_offsets must be a non-null, 4-byte aligned device pointer");
+    return append_impl(2, q, k, v, cache, page_table, seq_lens, cu_new, spec, 0, pos_offsets, q_out, q_ld, k_ld, v_ld, q_out_ld,
+                       B, N, Hq, max_pages, stream);
+}
+
+ne_status ne_paged_append_at_f32(const float* q, const float* k, const float* v, const ne_paged_cache* cache,
+                                 const int* page_table, const int* seq_lens, const int* cu_new, const ne_rope_spec* spec,
+                                 const int* pos_offsets, float* q_out, int64_t q_ld, int64_t k_ld, int64_t v_ld,
+                                 int64_t q_out_ld, int B, int N, int Hq, int max_pages, ne_stream_t stream) {
+    clear_error();
+    if (B > 0 && N > 0 && !aligned4(pos_offsets)) return fail(NE_ERR_INVALID_ARG, "pos_offsets must be a non-null, 4-byte aligned device pointer");
+    return append_impl(4, q, k, v, cache, page_table, seq_lens, cu_new, spec, 0, pos_offsets, q_out, q_ld, k_ld, v_ld, q_out_ld,
                        B, N, Hq, max_pages, stream);
 }
 
@@ -511,6 +570,74 @@ ne_status ne_pages_compact(const ne_paged_cache* cache, const int* refcount, con
     a.lens_out = remap;
     cudaError_t e = ne::launch_pages(ne::PAGES_COMPACT, a, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "pages_compact launch");
+    return NE_OK;
+}
+
+size_t ne_pages_evict_workspace_size(int layers, int B, int Hkv, int T) {
+    if (layers < 1 || B < 0 || Hkv < 1 || T < 1 || (long long)layers * B * Hkv >= (1LL << 31)) return 0;
+    return evict_ws((size_t)layers * B * Hkv, T).total;
+}
+
+ne_status ne_pages_evict(const ne_paged_cache* cache, const float* weights, const int* positions, const int* pos_offset,
+                         const int* page_table, const int* seq_lens, const int* new_lens, int sink, int recent,
+                         float* weights_out, int* positions_out, int* pos_offset_out, int B, int max_pages, void* workspace,
+                         size_t workspace_bytes, ne_stream_t stream) {
+    clear_error();
+    ne_status s = check_cache(cache, 0, false);
+    if (s != NE_OK) return s;
+    if (B < 0 || (long long)cache->layers * B * cache->Hkv >= (1LL << 31))
+        return fail(NE_ERR_INVALID_ARG, "need B >= 0 and layers * B * Hkv < 2^31 (B=%d)", B);
+    if (max_pages < 1 || (long long)max_pages * cache->page_size > (1 << 30) || (long long)B * max_pages >= (1LL << 31))
+        return fail(NE_ERR_INVALID_ARG, "need max_pages >= 1, max_pages * page_size <= 2^30 and B * max_pages < 2^31 (max_pages=%d)",
+                    max_pages);
+    if (sink < 0 || recent < 0 || sink > (1 << 30) || recent > (1 << 30))
+        return fail(NE_ERR_INVALID_ARG, "sink and recent must be 0 to 2^30 (sink=%d recent=%d)", sink, recent);
+    if (B == 0) return NE_OK;
+    const size_t rows = (size_t)cache->layers * B * cache->Hkv, T = (size_t)max_pages * cache->page_size;
+    s = check_arrays({{weights, rows * T * 4, "weights", -1}, {positions, rows * T * 4, "positions", -1},
+                      {pos_offset, (size_t)B * 4, "pos_offset", -1}, {page_table, (size_t)B * max_pages * 4, "page_table", -1},
+                      {seq_lens, (size_t)B * 4, "seq_lens", -1}, {new_lens, (size_t)B * 4, "new_lens", -1}},
+                     {{weights_out, rows * T * 4, "weights_out", 0}, {positions_out, rows * T * 4, "positions_out", 1},
+                      {pos_offset_out, (size_t)B * 4, "pos_offset_out", 2}});
+    if (s != NE_OK) return s;
+    const EvictWs w = evict_ws(rows, T);
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return fail(NE_ERR_INVALID_ARG, "workspace must be non-null and 256-byte aligned (%zu bytes needed)", w.total);
+    if (workspace_bytes < w.total)
+        return fail(NE_ERR_INVALID_ARG, "workspace too small: %zu bytes given, %zu needed", workspace_bytes, w.total);
+    ne::EvictArgs a = {};
+    if ((s = ready((cudaStream_t)stream, &a.err)) != NE_OK) return s;
+    const int e = cache->elem_bytes;
+    a.k = static_cast<char*>(cache->k);
+    a.v = static_cast<char*>(cache->v);
+    a.layers = cache->layers;
+    a.n_pages = cache->n_pages;
+    a.ps_shift = log2_of(cache->page_size);
+    a.Hkv = cache->Hkv;
+    a.row_vecs = cache->D * e / 16;
+    a.row_shift = log2_of(a.row_vecs);
+    a.layer_stride = cache->layers > 1 ? cache->layer_stride * e : 0;
+    a.page_stride = cache->n_pages > 1 ? cache->page_stride * e : 0;
+    a.tok_stride = cache->tok_stride * e;
+    a.head_stride = cache->Hkv > 1 ? cache->head_stride * e : 0;
+    a.w = weights;
+    a.pos = positions;
+    a.off = pos_offset;
+    a.table = page_table;
+    a.lens = seq_lens;
+    a.new_lens = new_lens;
+    a.w_out = weights_out;
+    a.pos_out = positions_out;
+    a.off_out = pos_offset_out;
+    a.B = B;
+    a.W = max_pages;
+    a.T = (int)T;
+    a.sink = sink;
+    a.recent = recent;
+    a.moves = static_cast<int*>(workspace);
+    a.list = reinterpret_cast<int*>(static_cast<char*>(workspace) + w.list);
+    cudaError_t err = ne::launch_evict(a, (cudaStream_t)stream);
+    if (err != cudaSuccess) return cuda_fail(err, "pages_evict launch");
     return NE_OK;
 }
 

@@ -25,8 +25,9 @@ enum WaitSite : int {
     // Not a wait: a variable-length call got a sequence length outside [0, T].
     SITE_VARLEN_LEN = 0x403,
     // Not waits: a paged call got bad row offsets, a bad length, a page id outside the pool,
-    // or a fork got a parent that is not a sequence.
+    // a fork got a parent that is not a sequence, or a group of sequences does not share what it says.
     SITE_PAGED_CU = 0x404, SITE_PAGED_LEN = 0x405, SITE_PAGED_PAGE = 0x406, SITE_PAGES_PARENT = 0x407,
+    SITE_PAGED_GROUP = 0x408,
     SITE_PAGED_Q = 0x601, SITE_PAGED_KV_FULL, SITE_PAGED_KV_EMPTY, SITE_PAGED_S_FULL, SITE_PAGED_P_READY,
     SITE_PAGED_O_FULL, SITE_PAGED_DRAIN, SITE_PAGED_SEG,
 };

@@ -36,6 +36,7 @@ struct AppendArgs {
     long long q_ld, k_ld, v_ld, qo_ld;
     int Hq, Hkv, D;
     int rot, layout, pos_offset;      // rot 0: no rotation
+    const int* pos_offsets;           // [B], or null: pos_offset for all
     float mscale;
     int wpt_shift;                    // log2 of the warps per token
     int vec_shift;                    // log2 of the 16-byte units of a head
@@ -134,6 +135,29 @@ struct PagesArgs {
     int chunks, pieces;               // pieces of a page and pool; of a copy (all layers, both pools)
     FastDiv div_pieces, div_chunks, div_heads, div_w;
 };
+// Sequences cut by accumulated weight.
+struct EvictArgs {
+    char* k;
+    char* v;
+    int layers, n_pages, ps_shift, Hkv, row_vecs, row_shift;   // row_vecs: 16-byte units of a slot of one head
+    long long layer_stride, page_stride, tok_stride, head_stride;   // bytes
+    const float* w;                   // [layers, B, Hkv, T]
+    const int* pos;
+    const int* off;                   // [B]
+    const int* table;
+    const int* lens;
+    const int* new_lens;
+    float* w_out;
+    int* pos_out;
+    int* off_out;
+    int B, W, T, sink, recent;
+    // workspace
+    int* moves;                       // [layers, B, Hkv]
+    int* list;                        // [layers, B, Hkv, T]: T / 2 targets, T / 2 sources
+    int* err;
+};
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st);
+
 enum PagesOp : int { PAGES_FORK = 0, PAGES_RESIZE, PAGES_COMPACT };
 cudaError_t launch_pages(PagesOp op, const PagesArgs& a, cudaStream_t st);
 

@@ -197,10 +197,16 @@ __global__ void __launch_bounds__(kThreads, 4) paged_append_kernel(const AppendA
     const int r = (int)row;
     const int b = a.s.cu ? find_seq(a.s.cu, a.s.B, r, lane) : r;
     int pos = -2;                                          // -1: not stored, -2: not a row of the call
+    int shift = a.pos_offset;                              // the rotation's position behind the slot's
     long long slot = -1;                                   // the slot's offset in the pools (elements), -1: none
     if (b >= 0) {
         int bad = 0;
         const PagedSeq q = paged_seq(a.s, b, bad);
+        if (a.pos_offsets) {
+            const int o = __ldg(a.pos_offsets + b);
+            if ((unsigned)o >= 1u << 30) bad = SITE_PAGED_LEN;
+            shift = min(max(o, 0), (1 << 30) - 1);
+        }
         if (r >= q.tok0 && r < q.tok0 + q.n) {
             pos = q.len - q.n + (r - q.tok0);
             if (pos < 0) {
@@ -220,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 4) paged_append_kernel(const AppendA
     if (pos >= 0 && a.rot) {
         for (int p = lane; p < a.rot >> 1; p += 32) {
             // Fraction of a turn in [-1/2, 1/2), as a signed 64-bit number over 2^64.
-            const long long f = (long long)((unsigned long long)(pos + a.pos_offset) * turns.t[p]);
+            const long long f = (long long)((unsigned long long)(pos + shift) * turns.t[p]);
             float s, c;
             sincospif((float)f * 1.0842021724855044e-19f, &s, &c);   // 2^-63: half turns
             s_cs[warp][p] = make_float2(c * a.mscale, s * a.mscale);

@@ -344,6 +344,19 @@ ne_status ne_paged_append_f32(const float* q, const float* k, const float* v, co
                               const ne_rope_spec* spec, int pos_offset, float* q_out, int64_t q_ld, int64_t k_ld, int64_t v_ld,
                               int64_t q_out_ld, int B, int N, int Hq, int max_pages, ne_stream_t stream);
 
+/* The same with an offset per sequence: row i of sequence b is rotated at its slot's position plus
+ * pos_offsets[b] (int32 [B], device memory; 0 <= pos_offsets[b] < 2^30, clamped and reported otherwise),
+ * for sequences that ne_pages_evict has cut. */
+ne_status ne_paged_append_at(const void* q, const void* k, const void* v, const ne_paged_cache* cache,
+                             const int* page_table, const int* seq_lens, const int* cu_new,
+                             const ne_rope_spec* spec, const int* pos_offsets, void* q_out, int64_t q_ld, int64_t k_ld,
+                             int64_t v_ld, int64_t q_out_ld, int B, int N, int Hq, int max_pages, ne_stream_t stream);
+ne_status ne_paged_append_at_f32(const float* q, const float* k, const float* v, const ne_paged_cache* cache,
+                                 const int* page_table, const int* seq_lens, const int* cu_new,
+                                 const ne_rope_spec* spec, const int* pos_offsets, float* q_out, int64_t q_ld,
+                                 int64_t k_ld, int64_t v_ld, int64_t q_out_ld, int B, int N, int Hq, int max_pages,
+                                 ne_stream_t stream);
+
 /* Attention of the new tokens over the pages: row i of sequence b (packed as above), at
  * position seq_lens[b] - n_b + i, attends to the cached positions up to its own.  n_b = 1 is
  * a generation step, n_b = seq_lens[b] a whole prompt, anything between a chunk; one call
@@ -420,6 +433,32 @@ ne_status ne_pages_resize(const ne_paged_cache* cache, const int* refcount, cons
 ne_status ne_pages_compact(const ne_paged_cache* cache, const int* refcount, const int* page_table,
                            int* refcount_out, int* table_out, int* remap, int* n_live, int B, int max_pages,
                            void* workspace, size_t workspace_bytes, ne_stream_t stream);
+
+/* Sequences cut to fewer positions, those with the least accumulated attention weight given up
+ * (ne_paged_weights sums it): sequence b keeps m = min(new_lens[b], seq_lens[b]) of its n = seq_lens[b]
+ * slots, chosen for every layer and kv head by itself.  Guarded slots stay first: those of positions below
+ * `sink`, and of the `recent` newest; then the largest weights, ties to the lowest slot (also among
+ * guarded slots where m does not hold them all; -0 counts as 0, NaN below every number).  A kept row
+ * stays in its slot, but those in slots m .. n-1 move into the slots below m that were given up, the j-th of
+ * them (in slot order) into the j-th: keys, values, weight and position.  Attention over the cut
+ * sequence is attention over the kept positions, whose order does not matter to it; new tokens follow in
+ * slots m, m+1, ..., rotated at slot + pos_offset_out[b] (ne_paged_append_at).
+ *   weights, weights_out      [layers, B, Hkv, T] fp32, T = max_pages * page_size
+ *   positions, positions_out  [layers, B, Hkv, T] int32: the position that a slot holds; -1 (what a caller
+ *                             fills in at first, and what a cut leaves behind m): slot + pos_offset[b]
+ *   pos_offset, pos_offset_out [B] int32: positions given up so far; pos_offset_out = pos_offset + n - m.
+ *                             0 <= pos_offset[b] < 2^30
+ * Slots m .. n-1 get weight 0 and position -1; entries at and behind n stay as they were.  Each output
+ * may be its input; any other overlap is refused.  The pages that hold a sequence's slots must belong to it alone
+ * (ne_pages_fork with deep sees to that), and ne_pages_resize from seq_lens to new_lens then gives back the
+ * pages behind m.  Bad lengths, offsets and page ids are clamped or skipped and reported by
+ * ne_get_device_error().  workspace: ne_pages_evict_workspace_size() bytes (4 per entry of weights), 256-byte
+ * aligned, caller-owned, rewritten by every call.  layers * B * Hkv < 2^31; 0 <= sink, recent <= 2^30. */
+size_t ne_pages_evict_workspace_size(int layers, int B, int Hkv, int T);
+ne_status ne_pages_evict(const ne_paged_cache* cache, const float* weights, const int* positions, const int* pos_offset,
+                         const int* page_table, const int* seq_lens, const int* new_lens, int sink, int recent,
+                         float* weights_out, int* positions_out, int* pos_offset_out, int B, int max_pages,
+                         void* workspace, size_t workspace_bytes, ne_stream_t stream);
 
 /* Human-readable name of a status code (static string). */
 const char* ne_status_string(ne_status s);
