@@ -39,6 +39,7 @@ EXPORTS = (
     "ne_rope_spec_init", "ne_paged_append", "ne_paged_append_f32", "ne_paged_attn_workspace_size", "ne_paged_attn",
     "ne_paged_attn_f32", "ne_pages_workspace_size", "ne_pages_fork", "ne_pages_resize", "ne_pages_compact",
     "ne_paged_append_at", "ne_paged_append_at_f32", "ne_pages_evict_workspace_size", "ne_pages_evict",
+    "ne_paged_weights_workspace_size", "ne_paged_weights", "ne_paged_weights_f32",
 )
 
 
@@ -129,13 +130,17 @@ def load(path: str | None = None):
         lib.ne_pages_evict_workspace_size.argtypes = [i] * 4
         lib.ne_pages_evict_workspace_size.restype = sz
         lib.ne_pages_evict.argtypes = [vp] * 7 + [i, i] + [vp] * 3 + [i, i, vp, sz, vp]
+        lib.ne_paged_weights_workspace_size.argtypes = []
+        lib.ne_paged_weights_workspace_size.restype = sz
+        lib.ne_paged_weights.argtypes = [vp] * 8 + [i64] + [i] * 5 + [vp, sz, vp]
+        lib.ne_paged_weights_f32.argtypes = lib.ne_paged_weights.argtypes
         for f in ("ne_rope_table", "ne_attn_fwd", "ne_attn_fwd_f32", "ne_attn_bwd", "ne_attn_bwd_f32",
                   "ne_get_device_error", "ne_selftest_wait_timeout", "ne_attn_bwd_noalloc", "ne_attn_decode",
                   "ne_noalloc_get_device_error", "ne_attn_fwd_varlen", "ne_attn_fwd_varlen_f32",
                   "ne_attn_bwd_varlen", "ne_attn_bwd_varlen_f32", "ne_qkv_prologue",
                   "ne_attn_decode_f32", "ne_rope_spec_init", "ne_paged_append", "ne_paged_append_f32", "ne_paged_attn",
                   "ne_paged_attn_f32", "ne_pages_fork", "ne_pages_resize", "ne_pages_compact", "ne_paged_append_at",
-                  "ne_paged_append_at_f32", "ne_pages_evict"):
+                  "ne_paged_append_at_f32", "ne_pages_evict", "ne_paged_weights", "ne_paged_weights_f32"):
             getattr(lib, f).restype = i
         _lib = lib
     return _lib
@@ -567,6 +572,40 @@ def paged_attn(q, k_pages, v_pages, page_table, seq_lens, cu_new=None, max_new: 
             ln, cu, o.data_ptr(), lse.data_ptr(), q_ld, B, N, Hq, W, max(1, N) if max_new is None else max_new,
             *_ws(workspace, dev))
     return o, lse
+
+
+def alloc_weights_workspace(device="cuda"):
+    """Workspace of paged_weights calls that run one after another."""
+    return torch.empty(int(load().ne_paged_weights_workspace_size()), dtype=torch.uint8, device=device)
+
+
+def paged_weights(q, lse, k_pages, page_table, seq_lens, weights=None, cu_new=None, max_new: int | None = None,
+                  weights_out=None, workspace=None):
+    """The attention weight that every cached position receives from the new tokens, added to
+    `weights` (ne_paged_weights): q [N, Hq, D] and lse [N, Hq] as paged_attn takes and returns them;
+    weights fp32 [B, Hkv, T], T = max_pages * page_size (None: zeros).  Returns weights_out, which may
+    be weights; entries behind a sequence's length are not written (zeros in a fresh one)."""
+    if max_new is not None and not 1 <= max_new <= _INT_MAX:
+        _c_ints(max_new=max_new)
+    lib = _lib or load()
+    c, dev, dt, _, Hkv, D = _paged_cache(k_pages, k_pages, False)
+    N, Hq = q.shape[:2]
+    B, W, pt, ln, cu = _paged_batch(page_table, seq_lens, cu_new, N, dev)
+    q_ld = _rows(q, "q", N, Hq, D, dt, dev)
+    if lse.shape != (N, Hq) or lse.dtype is not _F32 or lse.get_device() != dev or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous fp32 [N, Hq]")
+    shape = (B, Hkv, W * k_pages.shape[1])
+    if weights_out is None:
+        weights_out = q.new_zeros(shape, dtype=_F32)
+    for t, name in ((weights, "weights"), (weights_out, "weights_out")):
+        if t is not None and (t.shape != shape or t.dtype is not _F32 or t.get_device() != dev or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous fp32 CUDA tensor {list(shape)} on the pages' device")
+    if workspace is None:
+        workspace = alloc_weights_workspace(k_pages.device)
+    _launch(lib.ne_paged_weights if dt is _BF16 else lib.ne_paged_weights_f32, dev, q.data_ptr(), lse.data_ptr(), c, pt, ln, cu,
+            0 if weights is None else weights.data_ptr(), weights_out.data_ptr(), q_ld, B, N, Hq, W,
+            max(1, N) if max_new is None else max_new, *_ws(workspace, dev))
+    return weights_out
 
 
 def alloc_pages_workspace(n_pages: int, n: int, max_pages: int, device="cuda"):

@@ -185,9 +185,10 @@ ne_status append_impl(int eb, const void* q, const void* k, const void* v, const
     return NE_OK;
 }
 
-// Tensor maps of the tile kernel: a query box is (64 columns, G heads, `sub` tokens), a
-// key or value box (64 columns, one head, the rows of a page that fall into one tile).
-ne_status tile_maps(CUtensorMap* tq, CUtensorMap* tk, CUtensorMap* tv, const ne_paged_cache* c, const ne::PagedAttnArgs& a) {
+// Tensor maps of the tile kernels: a query box is (64 columns, `heads` heads, `sub` tokens), a
+// key or value box (64 columns, one head, the rows of a page that fall into one tile).  tv null: keys alone.
+ne_status tile_maps(CUtensorMap* tq, CUtensorMap* tk, CUtensorMap* tv, const ne_paged_cache* c, const ne::PagedView& v, const void* q,
+                    int64_t q_ld, int Hq, int N, int heads, int sub) {
     EncodeTiledFn enc;
     ne_status s = encode_fn(&enc);
     if (s != NE_OK) return s;
@@ -199,15 +200,15 @@ ne_status tile_maps(CUtensorMap* tq, CUtensorMap* tk, CUtensorMap* tv, const ne_
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
         return r == CUDA_SUCCESS ? NE_OK : fail(NE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
     };
-    const cuuint64_t qd[3] = {(cuuint64_t)c->D, (cuuint64_t)a.Hq, (cuuint64_t)a.s.N};
-    const cuuint64_t qs[2] = {(cuuint64_t)c->D * 2, (cuuint64_t)a.q_ld * 2};
-    const cuuint32_t qb[3] = {64, (cuuint32_t)a.G, (cuuint32_t)a.p.sub};
-    if ((s = encode(tq, a.q, 3, qd, qs, qb)) != NE_OK) return s;
+    const cuuint64_t qd[3] = {(cuuint64_t)c->D, (cuuint64_t)Hq, (cuuint64_t)N};
+    const cuuint64_t qs[2] = {(cuuint64_t)c->D * 2, (cuuint64_t)q_ld * 2};
+    const cuuint32_t qb[3] = {64, (cuuint32_t)heads, (cuuint32_t)sub};
+    if ((s = encode(tq, q, 3, qd, qs, qb)) != NE_OK) return s;
     const cuuint64_t kd[4] = {(cuuint64_t)c->D, (cuuint64_t)c->Hkv, (cuuint64_t)c->page_size, (cuuint64_t)c->n_pages};
-    const cuuint64_t ks[3] = {(cuuint64_t)a.c.head_stride * 2, (cuuint64_t)a.c.tok_stride * 2, (cuuint64_t)a.c.page_stride * 2};
+    const cuuint64_t ks[3] = {(cuuint64_t)v.head_stride * 2, (cuuint64_t)v.tok_stride * 2, (cuuint64_t)v.page_stride * 2};
     const cuuint32_t kb[4] = {64, 1, (cuuint32_t)std::min(c->page_size, 128), 1};
-    if ((s = encode(tk, a.c.k, 4, kd, ks, kb)) != NE_OK) return s;
-    return encode(tv, a.c.v, 4, kd, ks, kb);
+    if ((s = encode(tk, v.k, 4, kd, ks, kb)) != NE_OK || !tv) return s;
+    return encode(tv, v.v, 4, kd, ks, kb);
 }
 
 // Bytes of a call's workspace: the largest over the kernels that its head_dim and heads may run.
@@ -269,7 +270,7 @@ ne_status attn_impl(int eb, const void* q, const ne_paged_cache* c, const int* t
     cudaError_t e;
     if (kind == ne::PAGED_TILES) {
         CUtensorMap tq, tk, tv;
-        if ((s = tile_maps(&tq, &tk, &tv, c, a)) != NE_OK) return s;
+        if ((s = tile_maps(&tq, &tk, &tv, c, a.c, q, q_ld, Hq, N, a.G, a.p.sub)) != NE_OK) return s;
         e = ne::launch_paged_tiles(c->D, tq, tk, tv, a, st);
     } else if (f32) e = ne::launch_paged_f32(kind, c->D, a, st);
     else e = ne::launch_paged_short(kind, c->D, a, st);
@@ -277,6 +278,65 @@ ne_status attn_impl(int eb, const void* q, const ne_paged_cache* c, const int* t
     if (a.p.nocut) return NE_OK;
     e = ne::launch_paged_join(f32, c->D, a, st);
     if (e != cudaSuccess) return cuda_fail(e, "paged_attn join launch");
+    return NE_OK;
+}
+
+// ---------------------------------------------------------------- accumulated weights
+constexpr size_t kWeightParts = 2 * (size_t)ne::kWeightCtas;
+constexpr size_t kWeightWs = kWeightParts * (128 * sizeof(float) + sizeof(int4));
+
+ne_status weights_impl(int eb, const void* q, const float* lse, const ne_paged_cache* c, const int* table, const int* lens,
+                       const int* cu, const float* weights, float* weights_out, int64_t q_ld, int B, int N, int Hq, int W,
+                       int max_new, void* ws, size_t ws_bytes, ne_stream_t stream) {
+    clear_error();
+    ne_status s = check_cache(c, eb, true);
+    if (s != NE_OK) return s;
+    if (Hq < 1 || Hq % c->Hkv != 0)
+        return fail(NE_ERR_INVALID_ARG, "need Hq > 0 and Hq %% Hkv == 0 (Hq=%d Hkv=%d)", Hq, c->Hkv);
+    if (B < 0 || N < 0) return fail(NE_ERR_INVALID_ARG, "B and N must be >= 0 (B=%d N=%d)", B, N);
+    if (max_new < 1) return fail(NE_ERR_INVALID_ARG, "max_new must be >= 1 (max_new=%d)", max_new);
+    if (B == 0) return NE_OK;
+    // (Without new tokens the weights are still copied: the batch is checked as if it had one.)
+    if (!cu && N != B) return fail(NE_ERR_INVALID_ARG, "without cu_new every sequence has one row: N == B (N=%d B=%d)", N, B);
+    if ((s = check_batch(c, table, lens, N > 0 ? cu : lens, B, std::max(N, 1), Hq, W)) != NE_OK) return s;
+    if (N == 0 && cu && !aligned4(cu)) return fail(NE_ERR_INVALID_ARG, "cu_new must be a 4-byte aligned device pointer");
+    const size_t row = (size_t)Hq * c->D * eb, wb = (size_t)B * c->Hkv * W * c->page_size * 4;
+    if (!aligned4(weights_out) || (weights && !aligned4(weights)))
+        return fail(NE_ERR_INVALID_ARG, "weights and weights_out must be 4-byte aligned device pointers, weights_out non-null");
+    if (weights && weights != weights_out && overlap(weights, wb, weights_out, wb))
+        return fail(NE_ERR_INVALID_ARG, "weights_out must be weights itself or not overlap it");
+    if (N > 0) {
+        if ((s = check_rows("q", q, q_ld, Hq, c)) != NE_OK) return s;
+        if (!aligned4(lse)) return fail(NE_ERR_INVALID_ARG, "lse must be a non-null, 4-byte aligned device pointer");
+        if (overlap(weights_out, wb, q, (size_t)(q_ld * eb * (N - 1)) + row) || overlap(weights_out, wb, lse, (size_t)N * Hq * 4))
+            return fail(NE_ERR_INVALID_ARG, "weights_out must not overlap q or lse");
+    }
+    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
+        return fail(NE_ERR_INVALID_ARG, "workspace must be non-null and 256-byte aligned (%zu bytes needed)", kWeightWs);
+    if (ws_bytes < kWeightWs)
+        return fail(NE_ERR_INVALID_ARG, "workspace too small: %zu bytes given, %zu needed", ws_bytes, kWeightWs);
+    ne::WeightArgs a = {};
+    if ((s = ready((cudaStream_t)stream, &a.err)) != NE_OK) return s;
+    a.c = view_of(c);
+    a.s = batch_of(c, table, lens, cu, B, N, W);
+    a.q = q;
+    a.lse = lse;
+    a.w = weights;
+    a.w_out = weights_out;
+    a.q_ld = q_ld;
+    a.Hq = Hq;
+    a.Hkv = c->Hkv;
+    a.G = Hq / c->Hkv;
+    a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)c->D));
+    a.part = static_cast<float*>(ws);
+    a.part_info = reinterpret_cast<int4*>(a.part + kWeightParts * 128);
+    a.timeout_ns = timeout_ns();
+    const ne::WeightKind kind = N == 0 ? ne::WEIGHTS_FEW4 : ne::weight_kind(eb == 4, a.G, cu ? std::min(max_new, N) : 1);
+    ne::weight_split(kind, a);
+    CUtensorMap tq = {}, tk = {};
+    if (kind == ne::WEIGHTS_MANY && (s = tile_maps(&tq, &tk, nullptr, c, a.c, q, q_ld, Hq, N, a.gs, a.sub)) != NE_OK) return s;
+    const cudaError_t e = ne::launch_paged_weights(kind, eb == 4, c->D, tq, tk, a, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "paged_weights launch");
     return NE_OK;
 }
 
@@ -514,6 +574,24 @@ ne_status ne_paged_attn_f32(const float* q, const ne_paged_cache* cache, const i
                             int max_new, void* workspace, size_t workspace_bytes, ne_stream_t stream) {
     return attn_impl(4, q, cache, page_table, seq_lens, cu_new, o, lse, q_ld, B, N, Hq, max_pages, max_new, workspace,
                      workspace_bytes, stream);
+}
+
+size_t ne_paged_weights_workspace_size(void) { return kWeightWs; }
+
+ne_status ne_paged_weights(const void* q, const float* lse, const ne_paged_cache* cache, const int* page_table,
+                           const int* seq_lens, const int* cu_new, const float* weights, float* weights_out, int64_t q_ld,
+                           int B, int N, int Hq, int max_pages, int max_new, void* workspace, size_t workspace_bytes,
+                           ne_stream_t stream) {
+    return weights_impl(2, q, lse, cache, page_table, seq_lens, cu_new, weights, weights_out, q_ld, B, N, Hq, max_pages, max_new,
+                        workspace, workspace_bytes, stream);
+}
+
+ne_status ne_paged_weights_f32(const float* q, const float* lse, const ne_paged_cache* cache, const int* page_table,
+                               const int* seq_lens, const int* cu_new, const float* weights, float* weights_out, int64_t q_ld,
+                               int B, int N, int Hq, int max_pages, int max_new, void* workspace, size_t workspace_bytes,
+                               ne_stream_t stream) {
+    return weights_impl(4, q, lse, cache, page_table, seq_lens, cu_new, weights, weights_out, q_ld, B, N, Hq, max_pages, max_new,
+                        workspace, workspace_bytes, stream);
 }
 
 size_t ne_pages_workspace_size(int n_pages, int n, int max_pages) {

@@ -110,6 +110,31 @@ cudaError_t launch_paged_tiles(int D, const CUtensorMap& tq, const CUtensorMap& 
 // Joins the parts of cut units.
 cudaError_t launch_paged_join(bool f32, int D, const PagedAttnArgs& a, cudaStream_t st);
 
+// ---------------------------------------------------------------- accumulated weights
+constexpr int kWeightCtas = 152;      // shares of the kernels for many rows
+struct WeightArgs {
+    PagedView c;
+    PagedBatch s;                     // cap: entries of a row of weights
+    const void* q;
+    const float* lse;
+    const float* w;                   // [B, Hkv, cap], or null (zeros)
+    float* w_out;
+    long long q_ld;
+    int Hq, Hkv, G;
+    float scale_log2;
+    int gs, ngrp, sub;                // heads of a query tile, head groups of a kv head, tokens of a query tile
+    int ovh;                          // fixed cost of a unit, in tokens
+    float* part;                      // [2 kWeightCtas, 128] sums of cut units
+    int4* part_info;                  // [2 kWeightCtas] (state: 0 none, 1, 2 the unit's last; sequence, kv head, key tile)
+    int* err;
+    unsigned long long timeout_ns;
+};
+enum WeightKind : int { WEIGHTS_FEW4 = 0, WEIGHTS_FEW8, WEIGHTS_FEW16, WEIGHTS_FEW32, WEIGHTS_MANY, WEIGHTS_MANY_F32 };
+WeightKind weight_kind(bool f32, int G, int max_new);
+void weight_split(WeightKind kind, WeightArgs& a);
+cudaError_t launch_paged_weights(WeightKind kind, bool f32, int D, const CUtensorMap& tq, const CUtensorMap& tk,
+                                 const WeightArgs& a, cudaStream_t st);
+
 // ---------------------------------------------------------------- pages
 struct PagesArgs {
     char* k;

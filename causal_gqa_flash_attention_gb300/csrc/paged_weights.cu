@@ -1,0 +1,948 @@
+// paged_weights.cu -- the attention weight that every cached position has received from the new
+// tokens of its sequence: for sequence b, kv head g and key j
+//   out[b][g][j] = w[b][g][j] + sum over tokens i at t_i >= j and heads h of g of
+//                  2^(s log2(e) q_ih k_j - log2(e) lse_ih).
+// The log-sum-exp is the attention's own, so there is no running maximum, no second product and
+// no join of rows: keys are independent of each other.  Every kernel therefore has the keys as rows
+// of its product and sums along the query rows, within one thread or four.
+//
+// Few rows (up to 32 per kv head): read of the keys (2 D bytes against 2 D flops per row).  The line of
+// all 32-key steps is cut into one share per warp; a warp streams its steps through a private ring
+// (16-byte cp.async) and multiplies with mma.sync, keys as the 16-row operand and query rows as its 8
+// columns, so that three rows waste five eighths of a product instead of thirteen sixteenths.
+// Many rows, bf16: tcgen05, 128 keys (a TMEM lane each) times 128 query rows per tile.  2 * 128 *
+// 128 * D flops, 512 cycles of the tensor core at D 128, and 16384 exponentials, 512 cycles: the
+// exponentials bound D 64 and both D 128.  A unit is (sequence, kv head, 128 keys) and the query tiles
+// that see it; a share cuts units between query tiles, cut units' sums are added by a join.
+// Many rows, fp32: the same units on fp32 FMAs, two keys per lane in registers, the query rows
+// broadcast from shared memory.
+#include <cuda_bf16.h>
+#include "paged_line.cuh"
+#include "paged_load.cuh"
+
+namespace ne {
+namespace {
+
+// ------------------------------------------------------------------ few rows
+constexpr int kFewWarps = 8;
+constexpr int kFewThreads = kFewWarps * 32;
+constexpr int kFewStages = 3;
+
+// One step's 32 keys of a head into a tile (load_rows' layout, keys alone).
+template <int U>
+__device__ __forceinline__ void load_keys(uint32_t st, const char* k, const PagedView& c, int esize, int first, int kv, int pid,
+                                          int lane) {
+    constexpr int PER = 32 / U;
+    const int mask = (1 << c.ps_shift) - 1;
+    const long long tok_bytes = c.tok_stride * esize;
+    if (PER <= 8 && __all_sync(0xffffffffu, pid >= 0)) {
+        const long long lane_off = (lane / U) * tok_bytes + (lane % U) * 16;
+#pragma unroll
+        for (int x = 0; x < 32; x += 8) {
+            long long off = (long long)__shfl_sync(0xffffffffu, pid, x) * c.page_stride * esize + ((first + x) & mask) * tok_bytes + lane_off;
+#pragma unroll
+            for (int i = 0; i < 8; i += PER, off += PER * tok_bytes)
+                cp_async16(st + tile_unit<U>(x + i + lane / U, lane % U) * 16, k + off, true);
+        }
+        return;
+    }
+    load_tile<U>(st, k, c, esize, first, kv, pid, lane);
+}
+
+// A warp's place in the line of steps: sequence, kv head, step.
+struct StepWalk {
+    int b, h, st, steps, len;
+    long long left;                    // steps that are still to come, this one included
+    __device__ __forceinline__ void take(const WeightArgs& a) {
+        len = min(max(__ldg(a.s.lens + b), 0), a.s.cap);
+        steps = (len + 31) >> 5;
+    }
+    __device__ __forceinline__ void init(const WeightArgs& a, int b_, long long off, long long n) {
+        b = b_;
+        left = n;
+        h = st = 0;
+        if (left <= 0) return;
+        take(a);
+        h = (int)(off / steps);
+        st = (int)(off - (long long)h * steps);
+    }
+    // True where the next step is another head's.
+    __device__ __forceinline__ bool next(const WeightArgs& a) {
+        if (--left <= 0 || ++st < steps) return false;
+        st = 0;
+        if (++h == a.Hkv) {
+            h = 0;
+            do ++b;
+            while (take(a), steps == 0);                   // (left > 0: there is a sequence with steps)
+        }
+        return true;
+    }
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// RC query rows at a time; a sequence with more takes its rows in turn over every step.
+template <int D, int RC>
+struct FewBf16 {
+    static constexpr int ESIZE = 2, U = D / 8, NT = RC / 8, EXTRA = 0;
+    uint32_t qf[NT][D / 16][2];
+    float nl[NT][2];                   // -log2(e) lse of the lane's two rows of every eight (-inf: nobody)
+    int lim[NT][2];                    // keys that they see
+
+    __device__ __forceinline__ void rows(const WeightArgs& a, float*, const PagedSeq& q, int h, int r0, int lane) {
+        const int g8 = lane >> 2, t4 = lane & 3, R = q.n * a.G;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int r = r0 + n * 8 + g8;
+            const bool live = r < R;
+            const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q);
+            if (live) src += (long long)(q.tok0 + r / a.G) * a.q_ld + (long long)(h * a.G + r % a.G) * D;
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                qf[n][ks][0] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + ks * 16 + t4 * 2)) : 0u;
+                qf[n][ks][1] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + ks * 16 + 8 + t4 * 2)) : 0u;
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int c = r0 + n * 8 + t4 * 2 + i;
+                const bool in = c < R;
+                nl[n][i] = in ? -kLog2e * __ldg(a.lse + (long long)(q.tok0 + c / a.G) * a.Hq + h * a.G + c % a.G) : -INFINITY;
+                lim[n][i] = in ? q.len - q.n + c / a.G + 1 : 0;
+            }
+        }
+    }
+    // Adds this chunk's weights of the step's keys: sums [m][i] of keys 16 m + 8 i + lane / 4.
+    __device__ __forceinline__ void add(const WeightArgs& a, uint32_t st, const float*, int k0, bool edge, float (&sum)[2][2], int lane) const {
+        const int g8 = lane >> 2;
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            float c[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) c[n][e] = 0.f;
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                uint32_t kf[4];
+                ldsm4(st + tile_unit<U>(m * 16 + (lane & 15), ks * 2 + (lane >> 4)) * 16, kf);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma16816(c[n], kf, qf[n][ks][0], qf[n][ks][1]);
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float p = ex2(fmaf(c[n][e], a.scale_log2, nl[n][e & 1]));
+                    const bool seen = !edge || k0 + m * 16 + (e >> 1) * 8 + g8 < lim[n][e & 1];
+                    sum[m][e >> 1] += seen ? p : 0.f;
+                }
+        }
+    }
+    // The lane's key among the step's 32 and its sum.
+    static __device__ __forceinline__ int key(int lane) { return ((lane & 2) >> 1) * 16 + (lane & 1) * 8 + (lane >> 2); }
+    static __device__ __forceinline__ float total(const float (&sum)[2][2], int lane) {
+        float s[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            s[i] = sum[i >> 1][i & 1];
+            s[i] += __shfl_xor_sync(0xffffffffu, s[i], 1);
+            s[i] += __shfl_xor_sync(0xffffffffu, s[i], 2);
+        }
+        return lane & 2 ? (lane & 1 ? s[3] : s[2]) : (lane & 1 ? s[1] : s[0]);
+    }
+};
+
+template <int D, int RC>
+struct FewF32 {
+    static constexpr int ESIZE = 4, U = D / 4, EXTRA = RC * D;   // floats of shared memory per warp: the rows
+    float nl[RC];
+    int lim[RC];
+
+    __device__ __forceinline__ void rows(const WeightArgs& a, float* s_q, const PagedSeq& q, int h, int r0, int lane) {
+        const int R = q.n * a.G;
+        __syncwarp();                                      // the rows before have been read
+        for (int i = lane; i < RC * U; i += 32) {
+            const int r = r0 + i / U;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < R)
+                x = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + (long long)(q.tok0 + r / a.G) * a.q_ld +
+                                                          (long long)(h * a.G + r % a.G) * D) + i % U);
+            reinterpret_cast<float4*>(s_q)[i] = x;
+        }
+#pragma unroll
+        for (int i = 0; i < RC; ++i) {
+            const int r = r0 + i;
+            nl[i] = r < R ? -kLog2e * __ldg(a.lse + (long long)(q.tok0 + r / a.G) * a.Hq + h * a.G + r % a.G) : -INFINITY;
+            lim[i] = r < R ? q.len - q.n + r / a.G + 1 : 0;
+        }
+        __syncwarp();
+    }
+    __device__ __forceinline__ void add(const WeightArgs& a, uint32_t, const float* tile, int k0, bool, float (&sum)[2][2], int lane,
+                                        const float* s_q) const {
+        float2 acc[RC];
+#pragma unroll
+        for (int r = 0; r < RC; ++r) acc[r] = make_float2(0.f, 0.f);
+#pragma unroll 4
+        for (int u = 0; u < U; ++u) {
+            const float4 kf = reinterpret_cast<const float4*>(tile)[tile_unit<U>(lane, u)];
+#pragma unroll
+            for (int r = 0; r < RC; ++r) {
+                const float4 qv = reinterpret_cast<const float4*>(s_q)[r * U + u];
+                acc[r] = __ffma2_rn(make_float2(kf.x, kf.y), make_float2(qv.x, qv.y), acc[r]);
+                acc[r] = __ffma2_rn(make_float2(kf.z, kf.w), make_float2(qv.z, qv.w), acc[r]);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < RC; ++r) {
+            const float p = ex2(fmaf(acc[r].x + acc[r].y, a.scale_log2, nl[r]));
+            sum[0][0] += k0 + lane < lim[r] ? p : 0.f;
+        }
+    }
+    static __device__ __forceinline__ int key(int lane) { return lane; }
+    static __device__ __forceinline__ float total(const float (&sum)[2][2], int) { return sum[0][0]; }
+};
+
+template <int D, int RC, bool F32>
+struct FewPick {
+    typedef FewBf16<D, RC> type;
+};
+template <int D, int RC>
+struct FewPick<D, RC, true> {
+    typedef FewF32<D, RC> type;
+};
+
+template <int D, int RC, bool F32>
+struct FewCfg {
+    typedef typename FewPick<D, RC, F32>::type Rows;
+    static constexpr int TILE = 32 * D * Rows::ESIZE;
+    static constexpr int RING = kFewStages * TILE;
+    static constexpr int SMEM = kFewWarps * (RING + Rows::EXTRA * 4);
+    static constexpr int CTAS = SMEM > 108 * 1024 ? 1 : 2;
+};
+
+template <int D, int RC, bool F32>
+__global__ void __launch_bounds__(kFewThreads, FewCfg<D, RC, F32>::CTAS) weights_few_kernel(const WeightArgs a) {
+    using C = FewCfg<D, RC, F32>;
+    using Rows = typename C::Rows;
+    constexpr int U = Rows::U;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ Line<kFewThreads> line;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    griddep_launch_dependents();
+    griddep_wait();
+    int bad = 0;
+    auto cost = [&](int b) -> long long {
+        const PagedSeq q = paged_seq(a.s, b, bad);
+        return (long long)((q.len + 31) >> 5) * a.Hkv;
+    };
+    const long long total = line_total(line, a.s.B, cost);
+    if (blockIdx.x == 0 && bad) report_error(a.err, bad);
+    const int gw = blockIdx.x * kFewWarps + warp, GW = gridDim.x * kFewWarps;
+    const long long x0 = total * gw / GW, x1 = total * (gw + 1) / GW;
+    int b;
+    long long start;
+    line_find(line, a.s.B, cost, x0, b, start);
+    if (x0 >= x1) return;
+
+    uint8_t* const ring = smem + warp * C::RING;
+    float* const s_q = reinterpret_cast<float*>(smem + kFewWarps * C::RING) + warp * Rows::EXTRA;
+    const uint32_t ring0 = smem_u32(ring);
+    StepWalk in, at;                                       // of the copies, and of the products
+    in.init(a, b, x0 - start, x1 - x0);
+    at = in;
+    auto fetch = [&]() { return page_at(a.c, a.s.table + (size_t)in.b * a.s.W, in.st * 32 + lane, in.len); };
+    int pid = fetch(), filled = 0;
+    auto issue = [&]() {
+        if (in.left > 0) {
+            const int first = in.st * 32;
+            const int page = checked_page(a.c, pid, first + lane, in.len, a.err);
+            load_keys<U>(ring0 + filled * C::TILE, static_cast<const char*>(a.c.k) + (long long)in.h * a.c.head_stride * Rows::ESIZE, a.c,
+                         Rows::ESIZE, first, in.len, page, lane);
+            in.next(a);
+            if (in.left > 0) pid = fetch();
+        }
+        cp_async_commit();
+        filled = filled == kFewStages - 1 ? 0 : filled + 1;
+    };
+    for (int j = 0; j < kFewStages - 1; ++j) issue();
+    Rows rows;
+    PagedSeq q = {0, 0, 0};
+    bool fresh = true;                                     // the head's rows are still to be loaded
+    for (int slot = 0; at.left > 0; slot = slot == kFewStages - 1 ? 0 : slot + 1) {
+        const int k0 = at.st * 32, key = k0 + Rows::key(lane);
+        const long long o = ((long long)at.b * a.Hkv + at.h) * a.s.cap + key;
+        const float old = a.w && key < at.len ? a.w[o] : 0.f;
+        if (fresh) q = paged_seq(a.s, at.b, bad);
+        const int R = q.n * a.G, base = q.len - q.n;
+        if (fresh && R > 0) rows.rows(a, s_q, q, at.h, 0, lane);
+        __syncwarp();                                      // the step before has been read by the whole warp
+        issue();                                           // into its place
+        cp_async_wait<kFewStages - 1>();
+        __syncwarp();
+        float sum[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+        for (int r0 = 0; r0 < R; r0 += RC) {
+            if (R > RC) {
+                if (base + (min(R, r0 + RC) - 1) / a.G < k0) continue;   // none of them sees a key of the step
+                rows.rows(a, s_q, q, at.h, r0, lane);
+            }
+            const bool edge = k0 + 32 > base + r0 / a.G + 1;
+            if constexpr (F32) rows.add(a, 0, reinterpret_cast<const float*>(ring + slot * C::TILE), k0, edge, sum, lane, s_q);
+            else rows.add(a, ring0 + slot * C::TILE, nullptr, k0, edge, sum, lane);
+        }
+        const float got = Rows::total(sum, lane);
+        if (key < at.len) a.w_out[o] = old + got;
+        fresh = at.next(a);
+    }
+}
+
+// ------------------------------------------------------------------ many rows: units and shares
+// What a CTA does with one unit: query tiles [t0, t1) of [tf, nt) for keys 128 kt .. of head h.  Query tile
+// t holds tokens (t / ngrp) sub .. and heads (t % ngrp) gs .. of the kv head.
+struct WeightPart {
+    int b, h, kt;
+    int tok0, n, len;
+    int tf, nt, t0, t1;
+    __device__ __forceinline__ bool whole() const { return t0 == tf && t1 == nt; }
+};
+
+// Cost of key tiles 0 .. k-1 of a head, in tokens: each ovh + the tokens that see its first key.
+__device__ __forceinline__ long long weight_prefix(const PagedSeq& q, long long k, int ovh) {
+    const long long base = q.len - q.n, all = k * (ovh + q.n);
+    const long long k1 = base < 0 ? 0 : base / 128 + 1;    // the first tile that not every token sees
+    if (k <= k1) return all;
+    return all - (64 * (k * (k - 1) - k1 * (k1 - 1)) - base * (k - k1));
+}
+__device__ __forceinline__ long long weight_cost(const PagedSeq& q, int ovh) { return weight_prefix(q, (q.len + 127) / 128, ovh); }
+
+struct WeightWalk {
+    long long w0, w1, cur;
+    PagedSeq q;
+    int b, h, kt, nk;
+    __device__ __forceinline__ void take(const WeightArgs& a) {
+        int bad = 0;
+        q = paged_seq(a.s, b, bad);
+        nk = (q.len + 127) / 128;
+    }
+    __device__ __forceinline__ void init(const WeightArgs& a, long long w0_, long long w1_, int b_, long long start) {
+        w0 = w0_;
+        w1 = w1_;
+        b = b_;
+        cur = start;
+        h = kt = 0;
+        if (w0 >= w1) {
+            cur = w1;
+            return;
+        }
+        take(a);
+        const long long S = weight_cost(q, a.ovh);
+        h = (int)((w0 - start) / S);
+        const long long x = w0 - start - h * S;
+        int lo = 0, hi = nk - 1;                           // the last tile that starts at or before x
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (weight_prefix(q, mid, a.ovh) <= x) lo = mid;
+            else hi = mid - 1;
+        }
+        kt = lo;
+        cur = start + h * S + weight_prefix(q, kt, a.ovh);
+    }
+    __device__ __forceinline__ bool next(const WeightArgs& a, WeightPart& p) {
+        while (cur < w1) {
+            const int first = max(0, kt * 128 - (q.len - q.n));         // the first token that sees the tile
+            const long long cost = a.ovh + q.n - first;
+            p.b = b;
+            p.h = h;
+            p.kt = kt;
+            p.tok0 = q.tok0;
+            p.n = q.n;
+            p.len = q.len;
+            p.tf = first / a.sub * a.ngrp;
+            p.nt = (q.n + a.sub - 1) / a.sub * a.ngrp;
+            const int tiles = p.nt - p.tf;
+            // The tile boundary nearest to each end of the share; both CTAs at a cut compute it alike.
+            auto cut = [&](long long x) { return p.tf + min(tiles, __float2int_rn(__fdividef(__fmul_rn((float)x, (float)tiles), (float)cost))); };
+            p.t0 = w0 <= cur ? p.tf : cut(w0 - cur);
+            p.t1 = w1 >= cur + cost ? p.nt : cut(w1 - cur);
+            const bool mine = p.t0 < p.t1 || (tiles == 0 && w0 <= cur);   // (a unit without rows: its weights are copied)
+            cur += cost;
+            if (++kt == nk) {
+                kt = 0;
+                if (++h == a.Hkv) {
+                    h = 0;
+                    do ++b;
+                    while (b < a.s.B && (take(a), nk == 0));
+                    if (b >= a.s.B) cur = w1 > cur ? w1 : cur;
+                }
+            }
+            if (mine) return true;
+        }
+        return false;
+    }
+};
+
+// All T threads: the CTA's share.
+template <int T>
+__device__ __forceinline__ void weight_locate(const WeightArgs& a, Line<T>& line, WeightWalk& walk) {
+    int bad = 0;
+    auto cost = [&](int b) { return weight_cost(paged_seq(a.s, b, bad), a.ovh) * a.Hkv; };
+    const long long total = line_total(line, a.s.B, cost);
+    if (blockIdx.x == 0 && bad) report_error(a.err, bad);
+    const long long w0 = total / gridDim.x * blockIdx.x + total % gridDim.x * blockIdx.x / gridDim.x;
+    const int c = blockIdx.x + 1;
+    const long long w1 = total / gridDim.x * c + total % gridDim.x * c / gridDim.x;
+    int b;
+    long long start;
+    line_find(line, a.s.B, cost, w0, b, start);
+    walk.init(a, w0, w1, b, start);
+}
+
+// The sums of a unit, or of a part of it: one key per thread (key: within the tile).
+__device__ __forceinline__ void weight_put(const WeightArgs& a, const WeightPart& p, int key, float sum, float old) {
+    const int j = p.kt * 128 + key;
+    if (p.whole()) {
+        if (j < p.len) a.w_out[((long long)p.b * a.Hkv + p.h) * a.s.cap + j] = old + sum;
+        return;
+    }
+    const int slot = blockIdx.x * 2 + (p.t0 == p.tf ? 1 : 0);
+    a.part[slot * 128 + key] = sum;
+    if (key == 0) a.part_info[slot] = make_int4(p.t1 == p.nt ? 2 : 1, p.b, p.h, p.kt);
+}
+__device__ __forceinline__ float weight_old(const WeightArgs& a, const WeightPart& p, int key) {
+    const int j = p.kt * 128 + key;
+    return a.w && p.whole() && j < p.len ? a.w[((long long)p.b * a.Hkv + p.h) * a.s.cap + j] : 0.f;
+}
+
+// Block j: the unit whose first part CTA j left in its slot 1; the following CTAs' slots 0 up to the one
+// marked last are added in order.
+__global__ void __launch_bounds__(128) weights_join_kernel(const WeightArgs a) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int4 rec = a.part_info[blockIdx.x * 2 + 1];
+    if (rec.x == 0) return;
+    const int j = rec.w * 128 + threadIdx.x;
+    const PagedRaw raw = paged_raw(a.s, rec.y);
+    const bool in = j < min(max(raw.l, 0), a.s.cap);
+    const long long o = ((long long)rec.y * a.Hkv + rec.z) * a.s.cap + j;
+    const float old = a.w && in ? a.w[o] : 0.f;
+    float sum = a.part[(blockIdx.x * 2 + 1) * 128 + threadIdx.x];
+    const int lane = threadIdx.x & 31;
+    for (int c0 = blockIdx.x + 1; c0 < gridDim.x; c0 += 32) {
+        const int st = c0 + lane < gridDim.x ? a.part_info[(c0 + lane) * 2].x : 0;
+        const unsigned ends = __ballot_sync(0xffffffffu, st == 2);
+        unsigned have = __ballot_sync(0xffffffffu, st != 0) & (ends ? (ends & (0u - ends)) * 2u - 1u : 0xffffffffu);
+        while (have) {                                     // four loads at a time, added in order
+            float x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                x[k] = have ? a.part[(c0 + __ffs(have) - 1) * 256 + threadIdx.x] : 0.f;
+                have &= have - 1;
+            }
+            sum += (x[0] + x[1]) + (x[2] + x[3]);
+        }
+        if (ends) break;
+    }
+    if (in) a.w_out[o] = old + sum;
+}
+
+// ------------------------------------------------------------------ many rows, bf16
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+
+constexpr int kParts = 4;              // parts in the queue from warp 3 to the others
+constexpr int kPartReaders = 11;       // warps 0, 1, 2 and 4-11
+constexpr int kSBufs = 4;              // S tiles in TMEM
+
+// D 32 runs as 64: TMA fills the columns behind a row's end with zeros.
+template <int D>
+struct ManyCfg {
+    static constexpr int NCH = D / 64;
+    static constexpr int CHUNK = 128 * 128;
+    static constexpr int TILE = NCH * CHUNK;               // 128 rows of K or Q
+    static constexpr int NS = D == 128 ? 4 : 8;            // query tiles in the ring
+    static constexpr int SMEM = 1024 + (2 + NS) * TILE;
+    static constexpr int THREADS = 384;
+};
+
+// Roles (12 warps): 0 producer (keys of a part, then query tiles through the ring), 1 UMMA issuer, 2 the
+// log-sum-exps of every query tile, 3 the CTA's parts, 4-11 two groups of exponential warps that take the
+// S tiles in turn, a thread per key.  Dead rows of a query tile: those that TMA never writes are zero and
+// their lse entry -inf; those that hold other sequences' rows are masked where they occur.
+template <int D>
+__global__ void __launch_bounds__(384, 1)
+    weights_many_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const WeightArgs a) {
+    using C = ManyCfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sK = smem;                                    // two
+    uint8_t* sQ = smem + 2 * C::TILE;
+    __shared__ __align__(16) float s_nl[C::NS][128];       // -log2(e) lse
+    __shared__ __align__(8) uint64_t bar_k_full[2], bar_k_empty[2], bar_q_full[C::NS], bar_q_empty[C::NS];
+    __shared__ __align__(8) uint64_t bar_s_full[kSBufs], bar_s_free[kSBufs], bar_part_full[kParts], bar_part_empty[kParts], bar_final;
+    __shared__ Line<C::THREADS> line;
+    __shared__ WeightPart s_part[kParts];
+    __shared__ __align__(8) uint64_t bar_sum_full[2], bar_sum_free[2];
+    __shared__ float s_sum[2][128];                        // group 1's sums, for parts in turn
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&bar_k_full[i]), 1);
+            mbar_init(smem_u32(&bar_k_empty[i]), 1);
+        }
+        for (int i = 0; i < C::NS; ++i) {
+            mbar_init(smem_u32(&bar_q_full[i]), 2);        // the copy and the lse warp
+            mbar_init(smem_u32(&bar_q_empty[i]), 5);       // the products and four exponential warps
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&bar_sum_full[i]), 4);
+            mbar_init(smem_u32(&bar_sum_free[i]), 4);
+        }
+        for (int i = 0; i < kSBufs; ++i) {
+            mbar_init(smem_u32(&bar_s_full[i]), 1);
+            mbar_init(smem_u32(&bar_s_free[i]), 4);
+        }
+        for (int i = 0; i < kParts; ++i) {
+            mbar_init(smem_u32(&bar_part_full[i]), 1);
+            mbar_init(smem_u32(&bar_part_empty[i]), kPartReaders);
+        }
+        mbar_init(smem_u32(&bar_final), 1);
+        abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_k);
+    }
+    if (warp == 1) {
+        __syncwarp();
+        tmem_alloc(smem_u32(&tmem_slot), 512);
+        tmem_relinquish();
+    }
+    const int box = a.sub * a.gs;                          // rows of a query tile that TMA writes
+    for (int i = tid; i < C::NS * C::NCH * (128 - box) * 8; i += C::THREADS) {
+        const int u = i % 8, r = box + i / 8 % (128 - box), c = i / 8 / (128 - box);
+        *reinterpret_cast<uint4*>(sQ + c * C::CHUNK + sw128_offset(r, u)) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    griddep_launch_dependents();                           // after the TMEM allocation
+    griddep_wait();
+    const uint32_t tm = tmem_slot;
+    const WaitCtx w{a.err, &abort_flag, a.timeout_ns};
+    WeightWalk walk;
+    weight_locate(a, line, walk);
+    WeightPart p;
+    int npart = 0;
+    auto next_part = [&]() -> bool {
+        const int s = npart % kParts;
+        if (!mbar_wait_warp(smem_u32(&bar_part_full[s]), (npart / kParts) & 1, w, SITE_PAGED_SEG)) return false;
+        ++npart;
+        p = s_part[s];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bar_part_empty[s]));
+        return p.b >= 0;
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        int part = 0, item = 0;                            // parts with query tiles, query tiles
+        bool ok = true;
+        const int mask = (1 << a.c.ps_shift) - 1;
+        const int npg = a.c.ps_shift >= 7 ? 1 : 128 >> a.c.ps_shift, rows = 128 / npg;
+        while (ok && next_part()) {
+            if (p.t0 == p.t1) continue;
+            const int pos = p.kt * 128 + lane * rows;
+            int page = lane < npg && pos < p.len ? __ldg(a.s.table + (size_t)p.b * a.s.W + (pos >> a.c.ps_shift)) : -1;
+            const int s = part & 1;
+            if (part >= 2 && !(ok = mbar_wait_warp(smem_u32(&bar_k_empty[s]), (part / 2 - 1) & 1, w, SITE_PAGED_KV_EMPTY))) break;
+            if ((unsigned)page >= (unsigned)a.c.n_pages) {  // (outside the pool TMA fills with zeros)
+                if (lane < npg && pos < p.len) report_error(a.err, SITE_PAGED_PAGE);
+                page = a.c.n_pages;
+            }
+            const uint32_t kf = smem_u32(&bar_k_full[s]);
+            if (lane == 0) mbar_arrive_expect_tx(kf, C::TILE);
+            __syncwarp();
+            if (lane < npg)
+#pragma unroll
+                for (int c = 0; c < C::NCH; ++c)
+                    tma_load_4d(smem_u32(sK + s * C::TILE + c * C::CHUNK + lane * rows * 128), &tm_k, kf, c * 64, p.h, (p.kt * 128) & mask, page);
+            ++part;
+            for (int t = p.t0; t < p.t1; ++t, ++item) {
+                const int i = item % C::NS;
+                if (item >= C::NS && !(ok = mbar_wait_warp(smem_u32(&bar_q_empty[i]), (item / C::NS - 1) & 1, w, SITE_PAGED_Q))) break;
+                if (lane == 0) {
+                    const uint32_t qf = smem_u32(&bar_q_full[i]);
+                    mbar_arrive_expect_tx(qf, C::NCH * box * 128);
+                    for (int c = 0; c < C::NCH; ++c)
+                        tma_load_3d(smem_u32(sQ + i * C::TILE + c * C::CHUNK), &tm_q, qf, c * 64, p.h * a.G + t % a.ngrp * a.gs,
+                                    p.tok0 + t / a.ngrp * a.sub);
+                }
+                __syncwarp();
+            }
+        }
+        // Every copy this CTA started has landed before it ends.  (A query tile's barrier also waits
+        // for the lse warp, which gives up only with an error.)
+        __syncwarp();
+        if (lane == 0) {
+            for (int i = max(0, part - 2); i < part; ++i) mbar_wait_drain(smem_u32(&bar_k_full[i & 1]), (i / 2) & 1, w, SITE_PAGED_DRAIN);
+            for (int i = max(0, item - C::NS); i < item; ++i)
+                mbar_wait_drain(smem_u32(&bar_q_full[i % C::NS]), (i / C::NS) & 1, w, SITE_PAGED_DRAIN);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ UMMA issuer
+        constexpr uint32_t id_s = idesc_make(FMT_BF16, 128, 128, false, false);
+        const uint64_t dk0 = sdesc(smem_u32(sK), 16, 1024), dq0 = sdesc(smem_u32(sQ), 16, 1024);
+        int part = 0, item = 0;
+        bool ok = true;
+        while (ok && next_part()) {
+            if (p.t0 == p.t1) continue;
+            if (!(ok = mbar_wait_warp(smem_u32(&bar_k_full[part & 1]), (part / 2) & 1, w, SITE_PAGED_KV_FULL))) break;
+            for (int t = p.t0; t < p.t1; ++t, ++item) {
+                const int i = item % C::NS, s = item % kSBufs;
+                if (!(ok = mbar_wait_warp(smem_u32(&bar_q_full[i]), (item / C::NS) & 1, w, SITE_PAGED_Q))) break;
+                if (item >= kSBufs && !(ok = mbar_wait_warp(smem_u32(&bar_s_free[s]), (item / kSBufs - 1) & 1, w, SITE_PAGED_S_FULL))) break;
+                tc_fence_after();
+                const uint64_t dk = sdesc_add(dk0, (part & 1) * C::TILE), dq = sdesc_add(dq0, i * C::TILE);
+                if (elect_one()) {
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        const uint32_t off = ((ks * 32) >> 7) * C::CHUNK + ((ks * 32) & 127);
+                        umma_ss<false>(tm + s * 128, sdesc_add(dk, off), sdesc_add(dq, off), id_s, ks > 0);
+                    }
+                    umma_commit(smem_u32(&bar_s_full[s]));
+                    umma_commit(smem_u32(&bar_q_empty[i]));
+                    if (t + 1 == p.t1) umma_commit(smem_u32(&bar_k_empty[part & 1]));
+                }
+                __syncwarp();
+            }
+            ++part;
+        }
+        umma_commit_e(smem_u32(&bar_final));
+    } else if (warp == 2) {
+        // ------------------------------------------------------------ log-sum-exps
+        int tk[4], hd[4];                                  // token and head of rows lane, lane + 32, ... of a tile
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            tk[k] = (lane + 32 * k) / a.gs;
+            hd[k] = (lane + 32 * k) % a.gs;
+        }
+        int item = 0;
+        bool ok = true;
+        while (ok && next_part())
+            for (int t = p.t0; t < p.t1; ++t, ++item) {
+                const int i = item % C::NS, tok = t / a.ngrp * a.sub, h0 = t % a.ngrp * a.gs;
+                float v[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    v[k] = lane + 32 * k < box && tok + tk[k] < p.n && h0 + hd[k] < a.G
+                               ? -kLog2e * __ldg(a.lse + (long long)(p.tok0 + tok + tk[k]) * a.Hq + p.h * a.G + h0 + hd[k])
+                               : -INFINITY;
+                if (item >= C::NS && !(ok = mbar_wait_warp(smem_u32(&bar_q_empty[i]), (item / C::NS - 1) & 1, w, SITE_PAGED_Q))) break;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) s_nl[i][lane + 32 * k] = v[k];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bar_q_full[i]));
+            }
+    } else if (warp == 3) {
+        // ------------------------------------------------------------ the CTA's parts
+        if (lane < 2) a.part_info[blockIdx.x * 2 + lane] = make_int4(0, 0, 0, 0);
+        __syncwarp();                                      // both in front of lane 0's arrivals, and so of any record
+        bool more = true;
+        for (int k = 0; more; ++k) {
+            const int s = k % kParts;
+            more = walk.next(a, p);
+            if (!more) p.b = -1;
+            if (k >= kParts && !mbar_wait_warp(smem_u32(&bar_part_empty[s]), (k / kParts - 1) & 1, w, SITE_PAGED_SEG)) break;
+            if (lane == 0) {
+                s_part[s] = p;
+                mbar_arrive(smem_u32(&bar_part_full[s]));
+            }
+            __syncwarp();
+        }
+    } else {
+        // ------------------------------------------------------------ exponentials
+        const int grp = (warp - 4) >> 2, key = (warp & 3) * 32 + lane;
+        const uint32_t lt = tm + ((uint32_t)((warp & 3) * 32) << 16);
+        const float2 sl2 = make_float2(a.scale_log2, a.scale_log2);
+        int item = 0, parts = 0;                           // of the CTA; this group's are items with item % 2 == grp
+        bool ok = true;
+        while (ok && next_part()) {
+            const float old = grp == 0 ? weight_old(a, p, key) : 0.f;
+            float2 s2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            for (int t = p.t0; t < p.t1; ++t, ++item) {
+                if ((item & 1) != grp) continue;
+                const int s = item % kSBufs, i = item % C::NS;
+                const int tok = t / a.ngrp * a.sub, live = min(a.gs, a.G - t % a.ngrp * a.gs) * min(a.sub, p.n - tok);
+                // Rows c_min .. live-1 of the tile see this thread's key.
+                const int d = p.kt * 128 + key - (p.len - p.n) - tok;
+                const int c_min = d <= 0 ? 0 : d >= a.sub ? 128 : d * a.gs;
+                const bool edge = p.kt * 128 + 127 > p.len - p.n + tok || live < box;
+                // (The query tile's barrier stands for its lse entries.)
+                if (!(ok = mbar_wait_warp(smem_u32(&bar_q_full[i]), (item / C::NS) & 1, w, SITE_PAGED_Q) &&
+                           mbar_wait_warp(smem_u32(&bar_s_full[s]), (item / kSBufs) & 1, w, SITE_PAGED_S_FULL)))
+                    break;
+                tc_fence_after();
+                const float4* nl = reinterpret_cast<const float4*>(s_nl[i]);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t x[64];
+                    tmem_ld_cols<2>(lt + s * 128 + half * 64, x);
+                    if (half == 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&bar_s_free[s]));
+                    }
+#pragma unroll
+                    for (int e = 0; e < 64; e += 4) {
+                        const float4 l4 = nl[half * 16 + e / 4];
+                        const float2 y0 = __ffma2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), sl2, make_float2(l4.x, l4.y));
+                        const float2 y1 = __ffma2_rn(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), sl2, make_float2(l4.z, l4.w));
+                        float2 p0 = make_float2(ex2(y0.x), ex2(y0.y)), p1 = make_float2(ex2(y1.x), ex2(y1.y));
+                        if (edge) {
+                            const int c = half * 64 + e;
+                            p0.x = c >= c_min && c < live ? p0.x : 0.f;
+                            p0.y = c + 1 >= c_min && c + 1 < live ? p0.y : 0.f;
+                            p1.x = c + 2 >= c_min && c + 2 < live ? p1.x : 0.f;
+                            p1.y = c + 3 >= c_min && c + 3 < live ? p1.y : 0.f;
+                        }
+                        s2[e / 4 % 2 * 2] = __fadd2_rn(s2[e / 4 % 2 * 2], p0);
+                        s2[e / 4 % 2 * 2 + 1] = __fadd2_rn(s2[e / 4 % 2 * 2 + 1], p1);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bar_q_empty[i]));
+            }
+            if (!ok) break;
+            const float sum = ((s2[0].x + s2[0].y) + (s2[1].x + s2[1].y)) + ((s2[2].x + s2[2].y) + (s2[3].x + s2[3].y));
+            // The two groups' sums together.
+            const int k = parts & 1;
+            if (grp == 1) {
+                if (parts >= 2 && !(ok = mbar_wait_warp(smem_u32(&bar_sum_free[k]), (parts / 2 - 1) & 1, w, SITE_PAGED_O_FULL))) break;
+                s_sum[k][key] = sum;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bar_sum_full[k]));
+            } else {
+                if (!(ok = mbar_wait_warp(smem_u32(&bar_sum_full[k]), (parts / 2) & 1, w, SITE_PAGED_O_FULL))) break;
+                const float other = s_sum[k][key];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bar_sum_free[k]));
+                weight_put(a, p, key, sum + other, old);
+            }
+            ++parts;
+        }
+    }
+
+    // ---------------------------------------------------------------- teardown
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        mbar_wait_drain(smem_u32(&bar_final), 0, w, SITE_PAGED_DRAIN);
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tm, 512);
+    }
+}
+
+// ------------------------------------------------------------------ many rows, fp32
+// Eight warps: two halves of the 128 keys (two keys per lane, their rows in registers) times four shares of
+// every tile of 64 query rows, which lie in shared memory and are broadcast: 16 bytes feed four packed
+// FMAs, so the FMAs bound it.
+template <int D>
+struct ManyF32Cfg {
+    static constexpr int U = D / 4, RT = 64;
+    static constexpr int K_BYTES = 128 * D * 4, Q_BYTES = RT * D * 4;
+    static constexpr int SMEM = K_BYTES + 2 * Q_BYTES;
+    static constexpr int THREADS = 256;
+};
+
+template <int D>
+__global__ void __launch_bounds__(256, 1) weights_many_f32_kernel(const WeightArgs a) {
+    using C = ManyF32Cfg<D>;
+    constexpr int U = C::U, RT = C::RT;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ Line<C::THREADS> line;
+    __shared__ WeightPart s_part;
+    __shared__ float s_nl[2][RT], s_sum[4][128];
+    __shared__ int s_lim[2][RT];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int half = warp & 1, rg = warp >> 1;
+    uint8_t* const sQ = smem + C::K_BYTES;
+    griddep_launch_dependents();
+    griddep_wait();
+    WeightWalk walk;
+    weight_locate(a, line, walk);
+    if (tid < 2) a.part_info[blockIdx.x * 2 + tid] = make_int4(0, 0, 0, 0);
+    for (;;) {
+        __syncthreads();                                   // (the records are cleared; the part before is done)
+        if (warp == 0) {
+            WeightPart n;
+            if (!walk.next(a, n)) n.b = -1;
+            if (lane == 0) s_part = n;
+        }
+        __syncthreads();
+        const WeightPart p = s_part;
+        if (p.b < 0) break;
+        const int base = p.len - p.n;
+        auto load_q = [&](int t, int buf) {
+            if (t < p.t1) {
+                const int tok = t / a.ngrp * a.sub, h0 = t % a.ngrp * a.gs;
+                auto live = [&](int r) { return r < a.sub * a.gs && tok + r / a.gs < p.n && h0 + r % a.gs < a.G; };
+#pragma unroll
+                for (int i = tid; i < RT * U; i += C::THREADS) {
+                    const int r = i / U;
+                    const bool in = live(r);
+                    const float* src = static_cast<const float*>(a.q);
+                    if (in) src += (long long)(p.tok0 + tok + r / a.gs) * a.q_ld + (long long)(p.h * a.G + h0 + r % a.gs) * D + i % U * 4;
+                    cp_async16(smem_u32(sQ + buf * C::Q_BYTES) + i * 16, src, in);
+                }
+                if (tid < RT) {
+                    const bool in = live(tid);
+                    s_nl[buf][tid] = in ? -kLog2e * __ldg(a.lse + (long long)(p.tok0 + tok + tid / a.gs) * a.Hq + p.h * a.G + h0 + tid % a.gs)
+                                        : -INFINITY;
+                    s_lim[buf][tid] = in ? base + tok + tid / a.gs + 1 : 0;
+                }
+            }
+            cp_async_commit();
+        };
+        if (p.t0 < p.t1 && warp < 4) {
+            const int first = p.kt * 128 + warp * 32;
+            const int page = checked_page(a.c, page_at(a.c, a.s.table + (size_t)p.b * a.s.W, first + lane, p.len), first + lane, p.len, a.err);
+            load_keys<U>(smem_u32(smem) + warp * 32 * D * 4, static_cast<const char*>(a.c.k) + (long long)p.h * a.c.head_stride * 4, a.c, 4,
+                         first, p.len, page, lane);
+        }
+        load_q(p.t0, 0);                                   // (the keys are of this group of copies)
+        const float old = tid < 128 ? weight_old(a, p, tid) : 0.f;
+        float4 kf[2][U];
+        float sum[2] = {0.f, 0.f};
+        for (int t = p.t0; t < p.t1; ++t) {
+            const int buf = (t - p.t0) & 1;
+            load_q(t + 1, buf ^ 1);
+            cp_async_wait<1>();
+            __syncthreads();
+            if (t == p.t0)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        kf[k][u] = reinterpret_cast<const float4*>(smem)[(half * 2 + k) * 32 * U + tile_unit<U>(lane, u)];
+            const float4* q4 = reinterpret_cast<const float4*>(sQ + buf * C::Q_BYTES);
+            const int j0 = p.kt * 128 + half * 64 + lane;
+#pragma unroll 2
+            for (int r = rg; r < RT; r += 4) {
+                float2 s[2][2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) s[k][0] = s[k][1] = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const float4 qv = q4[r * U + u];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        s[k][0] = __ffma2_rn(make_float2(kf[k][u].x, kf[k][u].y), make_float2(qv.x, qv.y), s[k][0]);
+                        s[k][1] = __ffma2_rn(make_float2(kf[k][u].z, kf[k][u].w), make_float2(qv.z, qv.w), s[k][1]);
+                    }
+                }
+                const float nl = s_nl[buf][r];
+                const int lim = s_lim[buf][r];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float x = (s[k][0].x + s[k][0].y) + (s[k][1].x + s[k][1].y);
+                    const float e = ex2(fmaf(x, a.scale_log2, nl));
+                    sum[k] += j0 + 32 * k < lim ? e : 0.f;
+                }
+            }
+            __syncthreads();                               // the buffer is read before it is filled again
+        }
+        cp_async_wait<0>();
+        s_sum[rg][half * 64 + lane] = sum[0];
+        s_sum[rg][half * 64 + 32 + lane] = sum[1];
+        __syncthreads();
+        if (tid < 128) weight_put(a, p, tid, (s_sum[0][tid] + s_sum[1][tid]) + (s_sum[2][tid] + s_sum[3][tid]), old);
+    }
+}
+
+template <int D, int RC, bool F32>
+cudaError_t launch_few_t(const WeightArgs& a, cudaStream_t st) {
+    using C = FewCfg<D, RC, F32>;
+    static_assert(C::CTAS * (C::SMEM + 4096) <= 227 * 1024, "shared memory");
+    auto kfn = weights_few_kernel<D, RC, F32>;
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(kfn, C::SMEM, done);
+    if (e != cudaSuccess) return e;
+    return launch_k(kfn, dim3(C::CTAS * kWeightCtas), dim3(kFewThreads), C::SMEM, st, a);
+}
+
+template <int D>
+cudaError_t launch_many_t(const CUtensorMap& tq, const CUtensorMap& tk, const WeightArgs& a, cudaStream_t st) {
+    using C = ManyCfg<D>;
+    static_assert(C::SMEM + 12 * 1024 <= 227 * 1024, "shared memory");
+    auto kfn = weights_many_kernel<D>;
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(kfn, C::SMEM, done);
+    if (e != cudaSuccess) return e;
+    return launch_k(kfn, dim3(kWeightCtas), dim3(C::THREADS), C::SMEM, st, tq, tk, a);
+}
+
+template <int D>
+cudaError_t launch_many_f32_t(const WeightArgs& a, cudaStream_t st) {
+    using C = ManyF32Cfg<D>;
+    auto kfn = weights_many_f32_kernel<D>;
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(kfn, C::SMEM, done);
+    if (e != cudaSuccess) return e;
+    return launch_k(kfn, dim3(kWeightCtas), dim3(C::THREADS), C::SMEM, st, a);
+}
+
+}  // namespace
+
+WeightKind weight_kind(bool f32, int G, int max_new) {
+    const long long rows = (long long)G * max_new;
+    if (rows > 32) return f32 ? WEIGHTS_MANY_F32 : WEIGHTS_MANY;
+    return rows <= 4 ? WEIGHTS_FEW4 : rows <= 8 ? WEIGHTS_FEW8 : rows <= 16 ? WEIGHTS_FEW16 : WEIGHTS_FEW32;
+}
+
+void weight_split(WeightKind kind, WeightArgs& a) {
+    const int rt = kind == WEIGHTS_MANY_F32 ? 64 : 128;
+    a.gs = a.G < rt ? a.G : rt;
+    a.ngrp = (a.G + a.gs - 1) / a.gs;
+    a.sub = rt / a.gs;
+    a.ovh = 2 * a.sub;                                     // the ends of a unit, in tokens
+}
+
+cudaError_t launch_paged_weights(WeightKind kind, bool f32, int D, const CUtensorMap& tq, const CUtensorMap& tk,
+                                 const WeightArgs& a, cudaStream_t st) {
+    cudaError_t e = cudaErrorInvalidValue;
+    if (kind == WEIGHTS_MANY) e = D == 128 ? launch_many_t<128>(tq, tk, a, st) : launch_many_t<64>(tq, tk, a, st);
+    else if (kind == WEIGHTS_MANY_F32) e = D == 64 ? launch_many_f32_t<64>(a, st) : launch_many_f32_t<32>(a, st);
+    else if (f32) {                                        // (eight rows at a time; K is read again from shared memory)
+        if (D == 32) e = kind == WEIGHTS_FEW4 ? launch_few_t<32, 4, true>(a, st) : launch_few_t<32, 8, true>(a, st);
+        if (D == 64) e = kind == WEIGHTS_FEW4 ? launch_few_t<64, 4, true>(a, st) : launch_few_t<64, 8, true>(a, st);
+    } else {
+        const int rc = kind == WEIGHTS_FEW32 ? 32 : kind == WEIGHTS_FEW16 ? 16 : 8;
+        if (D == 32) e = rc == 8 ? launch_few_t<32, 8, false>(a, st) : rc == 16 ? launch_few_t<32, 16, false>(a, st) : launch_few_t<32, 32, false>(a, st);
+        if (D == 64) e = rc == 8 ? launch_few_t<64, 8, false>(a, st) : rc == 16 ? launch_few_t<64, 16, false>(a, st) : launch_few_t<64, 32, false>(a, st);
+        if (D == 128) e = rc == 8 ? launch_few_t<128, 8, false>(a, st) : rc == 16 ? launch_few_t<128, 16, false>(a, st) : launch_few_t<128, 32, false>(a, st);
+    }
+    if (e != cudaSuccess || (kind != WEIGHTS_MANY && kind != WEIGHTS_MANY_F32)) return e;
+    return launch_k(weights_join_kernel, dim3(kWeightCtas), dim3(128), 0, st, a);
+}
+
+}  // namespace ne

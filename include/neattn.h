@@ -391,6 +391,30 @@ ne_status ne_paged_attn_f32(const float* q, const ne_paged_cache* cache, const i
                             int N, int Hq, int max_pages, int max_new, void* workspace, size_t workspace_bytes,
                             ne_stream_t stream);
 
+/* The attention weight that every cached position receives from the new tokens, added to what it had:
+ * for sequence b, kv head g and slot j < seq_lens[b]
+ *   weights_out[b][g][j] = weights[b][g][j] + sum over the rows i of b at positions t_i >= j and the query
+ *                          heads h of g of exp(q_ih . k_j / sqrt(D) - lse_ih),
+ * q, lse, cu_new and max_new as ne_paged_attn takes and gives them (one layer).  What ne_pages_evict chooses by;
+ * to count a part of the new tokens, pass the last rows of each sequence alone.
+ *   weights     [B, Hkv, T] fp32, T = max_pages * page_size, or NULL (zeros)
+ *   weights_out [B, Hkv, T] fp32: weights itself, or no overlap with it.  Entries at and behind
+ *               seq_lens[b] stay as they were; a sequence without new tokens is copied.
+ * bf16: tensor-core products of bf16 inputs, fp32 sums; f32: fp32 throughout.  The order of the sums depends
+ * on the shape, lengths and device, never on timing.  cache->v is not read (a valid pointer all the same).  Slots at or
+ * behind a length may hold anything, rows outside [cu_new[0], cu_new[B]) too.  Device-side arguments are checked as in
+ * ne_paged_attn.  workspace: ne_paged_weights_workspace_size() bytes (155 KB), 256-byte aligned,
+ * caller-owned, rewritten by every call. */
+size_t ne_paged_weights_workspace_size(void);
+ne_status ne_paged_weights(const void* q, const float* lse, const ne_paged_cache* cache, const int* page_table,
+                           const int* seq_lens, const int* cu_new, const float* weights, float* weights_out, int64_t q_ld,
+                           int B, int N, int Hq, int max_pages, int max_new, void* workspace, size_t workspace_bytes,
+                           ne_stream_t stream);
+ne_status ne_paged_weights_f32(const float* q, const float* lse, const ne_paged_cache* cache, const int* page_table,
+                               const int* seq_lens, const int* cu_new, const float* weights, float* weights_out, int64_t q_ld,
+                               int B, int N, int Hq, int max_pages, int max_new, void* workspace, size_t workspace_bytes,
+                               ne_stream_t stream);
+
 /* Pages of sequences.  The pool's state is refcount [n_pages] int32 (device memory, owned
  * by the caller, zero at first): a page is free when its count is 0.  New pages are always
  * the lowest free ids, in the order of the sequences, so a call has one result.  Every
