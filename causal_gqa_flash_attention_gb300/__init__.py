@@ -600,11 +600,13 @@ def paged_weights(q, lse, k_pages, page_table, seq_lens, weights=None, cu_new=No
     for t, name in ((weights, "weights"), (weights_out, "weights_out")):
         if t is not None and (t.shape != shape or t.dtype is not _F32 or t.get_device() != dev or not t.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous fp32 CUDA tensor {list(shape)} on the pages' device")
-    if workspace is None:
-        workspace = alloc_weights_workspace(k_pages.device)
+    new = 1 if cu_new is None else max(1, N) if max_new is None else max_new
+    if workspace is not None:
+        ws = _ws(workspace, dev)
+    else:                                                  # (few rows need none)
+        ws = _ws(alloc_weights_workspace(k_pages.device), dev) if min(new, N) * (Hq // Hkv) > 32 else (0, 0)
     _launch(lib.ne_paged_weights if dt is _BF16 else lib.ne_paged_weights_f32, dev, q.data_ptr(), lse.data_ptr(), c, pt, ln, cu,
-            0 if weights is None else weights.data_ptr(), weights_out.data_ptr(), q_ld, B, N, Hq, W,
-            max(1, N) if max_new is None else max_new, *_ws(workspace, dev))
+            0 if weights is None else weights.data_ptr(), weights_out.data_ptr(), q_ld, B, N, Hq, W, new, *ws)
     return weights_out
 
 

@@ -283,7 +283,7 @@ ne_status attn_impl(int eb, const void* q, const ne_paged_cache* c, const int* t
 
 // ---------------------------------------------------------------- accumulated weights
 constexpr size_t kWeightParts = 2 * (size_t)ne::kWeightCtas;
-constexpr size_t kWeightWs = kWeightParts * (128 * sizeof(float) + sizeof(int4));
+constexpr size_t kWeightWs = kWeightParts * (ne::kWeightKeys * sizeof(float) + sizeof(int4));
 
 ne_status weights_impl(int eb, const void* q, const float* lse, const ne_paged_cache* c, const int* table, const int* lens,
                        const int* cu, const float* weights, float* weights_out, int64_t q_ld, int B, int N, int Hq, int W,
@@ -311,10 +311,13 @@ ne_status weights_impl(int eb, const void* q, const float* lse, const ne_paged_c
         if (overlap(weights_out, wb, q, (size_t)(q_ld * eb * (N - 1)) + row) || overlap(weights_out, wb, lse, (size_t)N * Hq * 4))
             return fail(NE_ERR_INVALID_ARG, "weights_out must not overlap q or lse");
     }
-    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
-        return fail(NE_ERR_INVALID_ARG, "workspace must be non-null and 256-byte aligned (%zu bytes needed)", kWeightWs);
-    if (ws_bytes < kWeightWs)
-        return fail(NE_ERR_INVALID_ARG, "workspace too small: %zu bytes given, %zu needed", ws_bytes, kWeightWs);
+    const ne::WeightKind kind = N == 0 ? ne::WEIGHTS_FEW4 : ne::weight_kind(eb == 4, Hq / c->Hkv, cu ? std::min(max_new, N) : 1);
+    if (kind >= ne::WEIGHTS_MANY) {
+        if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
+            return fail(NE_ERR_INVALID_ARG, "workspace must be non-null and 256-byte aligned (%zu bytes needed)", kWeightWs);
+        if (ws_bytes < kWeightWs)
+            return fail(NE_ERR_INVALID_ARG, "workspace too small: %zu bytes given, %zu needed", ws_bytes, kWeightWs);
+    }
     ne::WeightArgs a = {};
     if ((s = ready((cudaStream_t)stream, &a.err)) != NE_OK) return s;
     a.c = view_of(c);
@@ -329,9 +332,8 @@ ne_status weights_impl(int eb, const void* q, const float* lse, const ne_paged_c
     a.G = Hq / c->Hkv;
     a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)c->D));
     a.part = static_cast<float*>(ws);
-    a.part_info = reinterpret_cast<int4*>(a.part + kWeightParts * 128);
+    a.part_info = reinterpret_cast<int4*>(a.part + kWeightParts * ne::kWeightKeys);
     a.timeout_ns = timeout_ns();
-    const ne::WeightKind kind = N == 0 ? ne::WEIGHTS_FEW4 : ne::weight_kind(eb == 4, a.G, cu ? std::min(max_new, N) : 1);
     ne::weight_split(kind, a);
     CUtensorMap tq = {}, tk = {};
     if (kind == ne::WEIGHTS_MANY && (s = tile_maps(&tq, &tk, nullptr, c, a.c, q, q_ld, Hq, N, a.gs, a.sub)) != NE_OK) return s;

@@ -112,6 +112,7 @@ cudaError_t launch_paged_join(bool f32, int D, const PagedAttnArgs& a, cudaStrea
 
 // ---------------------------------------------------------------- accumulated weights
 constexpr int kWeightCtas = 152;      // shares of the kernels for many rows
+constexpr int kWeightKeys = 256;      // keys of a unit at most
 struct WeightArgs {
     PagedView c;
     PagedBatch s;                     // cap: entries of a row of weights
@@ -124,7 +125,8 @@ struct WeightArgs {
     float scale_log2;
     int gs, ngrp, sub;                // heads of a query tile, head groups of a kv head, tokens of a query tile
     int ovh;                          // fixed cost of a unit, in tokens
-    float* part;                      // [2 kWeightCtas, 128] sums of cut units
+    int key_shift;                    // log2 of its keys
+    float* part;                      // [2 kWeightCtas, kWeightKeys] sums of cut units
     int4* part_info;                  // [2 kWeightCtas] (state: 0 none, 1, 2 the unit's last; sequence, kv head, key tile)
     int* err;
     unsigned long long timeout_ns;

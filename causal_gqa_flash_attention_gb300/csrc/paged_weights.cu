@@ -12,11 +12,12 @@
 // columns, so that three rows waste five eighths of a product instead of thirteen sixteenths.
 // Many rows, bf16: tcgen05, 128 keys (a TMEM lane each) times 128 query rows per tile.  2 * 128 *
 // 128 * D flops, 512 cycles of the tensor core at D 128, and 16384 exponentials, 512 cycles: the
-// exponentials bound D 64 and both D 128.  A unit is (sequence, kv head, 128 keys) and the query tiles
+// exponentials bound D 64 and both D 128.  A unit is (sequence, kv head, 256 keys) and the query tiles
 // that see it; a share cuts units between query tiles, cut units' sums are added by a join.
-// Many rows, fp32: the same units on fp32 FMAs, two keys per lane in registers, the query rows
+// Many rows, fp32: units of 128 keys on fp32 FMAs, two keys per lane in registers, the query rows
 // broadcast from shared memory.
 #include <cuda_bf16.h>
+#include <type_traits>
 #include "paged_line.cuh"
 #include "paged_load.cuh"
 
@@ -308,8 +309,8 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, RC, F32>::CTAS) weights
 }
 
 // ------------------------------------------------------------------ many rows: units and shares
-// What a CTA does with one unit: query tiles [t0, t1) of [tf, nt) for keys 128 kt .. of head h.  Query tile
-// t holds tokens (t / ngrp) sub .. and heads (t % ngrp) gs .. of the kv head.
+// What a CTA does with one unit: query tiles [t0, t1) of [tf, nt) for keys kt 2^key_shift .. of head h.  Query
+// tile t holds tokens (t / ngrp) sub .. and heads (t % ngrp) gs .. of the kv head.
 struct WeightPart {
     int b, h, kt;
     int tok0, n, len;
@@ -318,13 +319,14 @@ struct WeightPart {
 };
 
 // Cost of key tiles 0 .. k-1 of a head, in tokens: each ovh + the tokens that see its first key.
-__device__ __forceinline__ long long weight_prefix(const PagedSeq& q, long long k, int ovh) {
-    const long long base = q.len - q.n, all = k * (ovh + q.n);
-    const long long k1 = base < 0 ? 0 : base / 128 + 1;    // the first tile that not every token sees
+__device__ __forceinline__ long long weight_prefix(const PagedSeq& q, long long k, const WeightArgs& a) {
+    const long long base = q.len - q.n, all = k * (a.ovh + q.n);
+    const long long k1 = base < 0 ? 0 : (base >> a.key_shift) + 1;      // the first tile that not every token sees
     if (k <= k1) return all;
-    return all - (64 * (k * (k - 1) - k1 * (k1 - 1)) - base * (k - k1));
+    return all - (((k * (k - 1) - k1 * (k1 - 1)) >> 1 << a.key_shift) - base * (k - k1));
 }
-__device__ __forceinline__ long long weight_cost(const PagedSeq& q, int ovh) { return weight_prefix(q, (q.len + 127) / 128, ovh); }
+__device__ __forceinline__ int weight_tiles(const PagedSeq& q, const WeightArgs& a) { return (q.len + (1 << a.key_shift) - 1) >> a.key_shift; }
+__device__ __forceinline__ long long weight_cost(const PagedSeq& q, const WeightArgs& a) { return weight_prefix(q, weight_tiles(q, a), a); }
 
 struct WeightWalk {
     long long w0, w1, cur;
@@ -333,7 +335,7 @@ struct WeightWalk {
     __device__ __forceinline__ void take(const WeightArgs& a) {
         int bad = 0;
         q = paged_seq(a.s, b, bad);
-        nk = (q.len + 127) / 128;
+        nk = weight_tiles(q, a);
     }
     __device__ __forceinline__ void init(const WeightArgs& a, long long w0_, long long w1_, int b_, long long start) {
         w0 = w0_;
@@ -346,21 +348,21 @@ struct WeightWalk {
             return;
         }
         take(a);
-        const long long S = weight_cost(q, a.ovh);
+        const long long S = weight_cost(q, a);
         h = (int)((w0 - start) / S);
         const long long x = w0 - start - h * S;
         int lo = 0, hi = nk - 1;                           // the last tile that starts at or before x
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (weight_prefix(q, mid, a.ovh) <= x) lo = mid;
+            if (weight_prefix(q, mid, a) <= x) lo = mid;
             else hi = mid - 1;
         }
         kt = lo;
-        cur = start + h * S + weight_prefix(q, kt, a.ovh);
+        cur = start + h * S + weight_prefix(q, kt, a);
     }
     __device__ __forceinline__ bool next(const WeightArgs& a, WeightPart& p) {
         while (cur < w1) {
-            const int first = max(0, kt * 128 - (q.len - q.n));         // the first token that sees the tile
+            const int first = max(0, (kt << a.key_shift) - (q.len - q.n));         // the first token that sees the tile
             const long long cost = a.ovh + q.n - first;
             p.b = b;
             p.h = h;
@@ -396,7 +398,7 @@ struct WeightWalk {
 template <int T>
 __device__ __forceinline__ void weight_locate(const WeightArgs& a, Line<T>& line, WeightWalk& walk) {
     int bad = 0;
-    auto cost = [&](int b) { return weight_cost(paged_seq(a.s, b, bad), a.ovh) * a.Hkv; };
+    auto cost = [&](int b) { return weight_cost(paged_seq(a.s, b, bad), a) * a.Hkv; };
     const long long total = line_total(line, a.s.B, cost);
     if (blockIdx.x == 0 && bad) report_error(a.err, bad);
     const long long w0 = total / gridDim.x * blockIdx.x + total % gridDim.x * blockIdx.x / gridDim.x;
@@ -410,33 +412,33 @@ __device__ __forceinline__ void weight_locate(const WeightArgs& a, Line<T>& line
 
 // The sums of a unit, or of a part of it: one key per thread (key: within the tile).
 __device__ __forceinline__ void weight_put(const WeightArgs& a, const WeightPart& p, int key, float sum, float old) {
-    const int j = p.kt * 128 + key;
+    const int j = (p.kt << a.key_shift) + key;
     if (p.whole()) {
         if (j < p.len) a.w_out[((long long)p.b * a.Hkv + p.h) * a.s.cap + j] = old + sum;
         return;
     }
     const int slot = blockIdx.x * 2 + (p.t0 == p.tf ? 1 : 0);
-    a.part[slot * 128 + key] = sum;
+    a.part[slot * kWeightKeys + key] = sum;
     if (key == 0) a.part_info[slot] = make_int4(p.t1 == p.nt ? 2 : 1, p.b, p.h, p.kt);
 }
 __device__ __forceinline__ float weight_old(const WeightArgs& a, const WeightPart& p, int key) {
-    const int j = p.kt * 128 + key;
+    const int j = (p.kt << a.key_shift) + key;
     return a.w && p.whole() && j < p.len ? a.w[((long long)p.b * a.Hkv + p.h) * a.s.cap + j] : 0.f;
 }
 
 // Block j: the unit whose first part CTA j left in its slot 1; the following CTAs' slots 0 up to the one
 // marked last are added in order.
-__global__ void __launch_bounds__(128) weights_join_kernel(const WeightArgs a) {
+__global__ void __launch_bounds__(kWeightKeys) weights_join_kernel(const WeightArgs a) {
     griddep_launch_dependents();
     griddep_wait();
     const int4 rec = a.part_info[blockIdx.x * 2 + 1];
     if (rec.x == 0) return;
-    const int j = rec.w * 128 + threadIdx.x;
+    const int j = (rec.w << a.key_shift) + threadIdx.x;
     const PagedRaw raw = paged_raw(a.s, rec.y);
-    const bool in = j < min(max(raw.l, 0), a.s.cap);
+    const bool in = (threadIdx.x >> a.key_shift) == 0 && j < min(max(raw.l, 0), a.s.cap);
     const long long o = ((long long)rec.y * a.Hkv + rec.z) * a.s.cap + j;
     const float old = a.w && in ? a.w[o] : 0.f;
-    float sum = a.part[(blockIdx.x * 2 + 1) * 128 + threadIdx.x];
+    float sum = a.part[(blockIdx.x * 2 + 1) * kWeightKeys + threadIdx.x];
     const int lane = threadIdx.x & 31;
     for (int c0 = blockIdx.x + 1; c0 < gridDim.x; c0 += 32) {
         const int st = c0 + lane < gridDim.x ? a.part_info[(c0 + lane) * 2].x : 0;
@@ -446,7 +448,7 @@ __global__ void __launch_bounds__(128) weights_join_kernel(const WeightArgs a) {
             float x[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                x[k] = have ? a.part[(c0 + __ffs(have) - 1) * 256 + threadIdx.x] : 0.f;
+                x[k] = have ? a.part[(c0 + __ffs(have) - 1) * 2 * kWeightKeys + threadIdx.x] : 0.f;
                 have &= have - 1;
             }
             sum += (x[0] + x[1]) + (x[2] + x[3]);
@@ -467,7 +469,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, 
 
 constexpr int kParts = 4;              // parts in the queue from warp 3 to the others
 constexpr int kPartReaders = 11;       // warps 0, 1, 2 and 4-11
-constexpr int kSBufs = 4;              // S tiles in TMEM
 
 // D 32 runs as 64: TMA fills the columns behind a row's end with zeros.
 template <int D>
@@ -475,48 +476,45 @@ struct ManyCfg {
     static constexpr int NCH = D / 64;
     static constexpr int CHUNK = 128 * 128;
     static constexpr int TILE = NCH * CHUNK;               // 128 rows of K or Q
-    static constexpr int NS = D == 128 ? 4 : 8;            // query tiles in the ring
-    static constexpr int SMEM = 1024 + (2 + NS) * TILE;
+    static constexpr int NK = D == 128 ? 3 : 4;            // key tiles (two to a unit) in shared memory
+    static constexpr int NS = D == 128 ? 3 : 8;            // query tiles in the ring
+    static constexpr int SMEM = 1024 + (NK + NS) * TILE;
     static constexpr int THREADS = 384;
 };
 
-// Roles (12 warps): 0 producer (keys of a part, then query tiles through the ring), 1 UMMA issuer, 2 the
-// log-sum-exps of every query tile, 3 the CTA's parts, 4-11 two groups of exponential warps that take the
-// S tiles in turn, a thread per key.  Dead rows of a query tile: those that TMA never writes are zero and
-// their lse entry -inf; those that hold other sequences' rows are masked where they occur.
+// A unit holds two tiles of 128 keys, so that a query tile (16 KB at D 64, 32 at D 128; an SM receives some 35
+// bytes a cycle) feeds two products.  Roles (12 warps): 0 producer (keys of a part, then query tiles through
+// the ring), 1 UMMA issuer, 2 the log-sum-exps of every query tile, 3 the CTA's parts, 4-11 the
+// exponentials: warps 4-7 the first 128 keys, 8-11 the others, a thread per key (TMEM lane).  S of key tile
+// u and query tile i lies in TMEM columns 256 u + 128 (i % 2).  Dead rows of a query tile: those that TMA never
+// writes are zero and their lse entry -inf; those that hold other sequences' rows are masked where they occur.
 template <int D>
 __global__ void __launch_bounds__(384, 1)
     weights_many_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const WeightArgs a) {
     using C = ManyCfg<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* sK = smem;                                    // two
-    uint8_t* sQ = smem + 2 * C::TILE;
+    uint8_t* sK = smem;
+    uint8_t* sQ = smem + C::NK * C::TILE;
     __shared__ __align__(16) float s_nl[C::NS][128];       // -log2(e) lse
-    __shared__ __align__(8) uint64_t bar_k_full[2], bar_k_empty[2], bar_q_full[C::NS], bar_q_empty[C::NS];
-    __shared__ __align__(8) uint64_t bar_s_full[kSBufs], bar_s_free[kSBufs], bar_part_full[kParts], bar_part_empty[kParts], bar_final;
+    __shared__ __align__(8) uint64_t bar_k_full[C::NK], bar_k_empty[C::NK], bar_q_full[C::NS], bar_q_empty[C::NS];
+    __shared__ __align__(8) uint64_t bar_s_full[4], bar_s_free[4], bar_part_full[kParts], bar_part_empty[kParts], bar_final;
     __shared__ Line<C::THREADS> line;
     __shared__ WeightPart s_part[kParts];
-    __shared__ __align__(8) uint64_t bar_sum_full[2], bar_sum_free[2];
-    __shared__ float s_sum[2][128];                        // group 1's sums, for parts in turn
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < C::NK; ++i) {
             mbar_init(smem_u32(&bar_k_full[i]), 1);
             mbar_init(smem_u32(&bar_k_empty[i]), 1);
         }
         for (int i = 0; i < C::NS; ++i) {
             mbar_init(smem_u32(&bar_q_full[i]), 2);        // the copy and the lse warp
-            mbar_init(smem_u32(&bar_q_empty[i]), 5);       // the products and four exponential warps
+            mbar_init(smem_u32(&bar_q_empty[i]), 9);       // the products and eight exponential warps
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&bar_sum_full[i]), 4);
-            mbar_init(smem_u32(&bar_sum_free[i]), 4);
-        }
-        for (int i = 0; i < kSBufs; ++i) {
+        for (int i = 0; i < 4; ++i) {                      // 2 u + item % 2
             mbar_init(smem_u32(&bar_s_full[i]), 1);
             mbar_init(smem_u32(&bar_s_free[i]), 4);
         }
@@ -564,28 +562,38 @@ __global__ void __launch_bounds__(384, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
-        int part = 0, item = 0;                            // parts with query tiles, query tiles
+        int keys = 0, item = 0;                            // key tiles, query tiles
         bool ok = true;
         const int mask = (1 << a.c.ps_shift) - 1;
         const int npg = a.c.ps_shift >= 7 ? 1 : 128 >> a.c.ps_shift, rows = 128 / npg;
         while (ok && next_part()) {
             if (p.t0 == p.t1) continue;
-            const int pos = p.kt * 128 + lane * rows;
-            int page = lane < npg && pos < p.len ? __ldg(a.s.table + (size_t)p.b * a.s.W + (pos >> a.c.ps_shift)) : -1;
-            const int s = part & 1;
-            if (part >= 2 && !(ok = mbar_wait_warp(smem_u32(&bar_k_empty[s]), (part / 2 - 1) & 1, w, SITE_PAGED_KV_EMPTY))) break;
-            if ((unsigned)page >= (unsigned)a.c.n_pages) {  // (outside the pool TMA fills with zeros)
-                if (lane < npg && pos < p.len) report_error(a.err, SITE_PAGED_PAGE);
-                page = a.c.n_pages;
-            }
-            const uint32_t kf = smem_u32(&bar_k_full[s]);
-            if (lane == 0) mbar_arrive_expect_tx(kf, C::TILE);
-            __syncwarp();
-            if (lane < npg)
+            const int* trow = a.s.table + (size_t)p.b * a.s.W;
+            int page[2];
 #pragma unroll
-                for (int c = 0; c < C::NCH; ++c)
-                    tma_load_4d(smem_u32(sK + s * C::TILE + c * C::CHUNK + lane * rows * 128), &tm_k, kf, c * 64, p.h, (p.kt * 128) & mask, page);
-            ++part;
+            for (int u = 0; u < 2; ++u) {
+                const int pos = p.kt * 256 + u * 128 + lane * rows;
+                page[u] = lane < npg && pos < p.len ? __ldg(trow + (pos >> a.c.ps_shift)) : -1;
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int k0 = p.kt * 256 + u * 128, s = keys % C::NK;
+                if (k0 >= p.len) break;
+                if (keys >= C::NK && !(ok = mbar_wait_warp(smem_u32(&bar_k_empty[s]), (keys / C::NK - 1) & 1, w, SITE_PAGED_KV_EMPTY))) break;
+                if ((unsigned)page[u] >= (unsigned)a.c.n_pages) {  // (outside the pool TMA fills with zeros)
+                    if (lane < npg && k0 + lane * rows < p.len) report_error(a.err, SITE_PAGED_PAGE);
+                    page[u] = a.c.n_pages;
+                }
+                const uint32_t kf = smem_u32(&bar_k_full[s]);
+                if (lane == 0) mbar_arrive_expect_tx(kf, C::TILE);
+                __syncwarp();
+                if (lane < npg)
+#pragma unroll
+                    for (int c = 0; c < C::NCH; ++c)
+                        tma_load_4d(smem_u32(sK + s * C::TILE + c * C::CHUNK + lane * rows * 128), &tm_k, kf, c * 64, p.h, k0 & mask, page[u]);
+                ++keys;
+            }
+            if (!ok) break;
             for (int t = p.t0; t < p.t1; ++t, ++item) {
                 const int i = item % C::NS;
                 if (item >= C::NS && !(ok = mbar_wait_warp(smem_u32(&bar_q_empty[i]), (item / C::NS - 1) & 1, w, SITE_PAGED_Q))) break;
@@ -603,7 +611,8 @@ __global__ void __launch_bounds__(384, 1)
         // for the lse warp, which gives up only with an error.)
         __syncwarp();
         if (lane == 0) {
-            for (int i = max(0, part - 2); i < part; ++i) mbar_wait_drain(smem_u32(&bar_k_full[i & 1]), (i / 2) & 1, w, SITE_PAGED_DRAIN);
+            for (int i = max(0, keys - C::NK); i < keys; ++i)
+                mbar_wait_drain(smem_u32(&bar_k_full[i % C::NK]), (i / C::NK) & 1, w, SITE_PAGED_DRAIN);
             for (int i = max(0, item - C::NS); i < item; ++i)
                 mbar_wait_drain(smem_u32(&bar_q_full[i % C::NS]), (i / C::NS) & 1, w, SITE_PAGED_DRAIN);
         }
@@ -611,30 +620,40 @@ __global__ void __launch_bounds__(384, 1)
         // ------------------------------------------------------------ UMMA issuer
         constexpr uint32_t id_s = idesc_make(FMT_BF16, 128, 128, false, false);
         const uint64_t dk0 = sdesc(smem_u32(sK), 16, 1024), dq0 = sdesc(smem_u32(sQ), 16, 1024);
-        int part = 0, item = 0;
+        int keys = 0, item = 0, uses[2] = {0, 0};          // uses: S tiles of either key tile so far
         bool ok = true;
         while (ok && next_part()) {
             if (p.t0 == p.t1) continue;
-            if (!(ok = mbar_wait_warp(smem_u32(&bar_k_full[part & 1]), (part / 2) & 1, w, SITE_PAGED_KV_FULL))) break;
-            for (int t = p.t0; t < p.t1; ++t, ++item) {
-                const int i = item % C::NS, s = item % kSBufs;
+            const int nu = p.kt * 256 + 128 < p.len ? 2 : 1;
+            for (int u = 0; ok && u < nu; ++u)
+                ok = mbar_wait_warp(smem_u32(&bar_k_full[(keys + u) % C::NK]), ((keys + u) / C::NK) & 1, w, SITE_PAGED_KV_FULL);
+            if (!ok) break;
+            for (int t = p.t0; ok && t < p.t1; ++t, ++item) {
+                const int i = item % C::NS;
                 if (!(ok = mbar_wait_warp(smem_u32(&bar_q_full[i]), (item / C::NS) & 1, w, SITE_PAGED_Q))) break;
-                if (item >= kSBufs && !(ok = mbar_wait_warp(smem_u32(&bar_s_free[s]), (item / kSBufs - 1) & 1, w, SITE_PAGED_S_FULL))) break;
-                tc_fence_after();
-                const uint64_t dk = sdesc_add(dk0, (part & 1) * C::TILE), dq = sdesc_add(dq0, i * C::TILE);
-                if (elect_one()) {
+                const uint64_t dq = sdesc_add(dq0, i * C::TILE);
 #pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {
-                        const uint32_t off = ((ks * 32) >> 7) * C::CHUNK + ((ks * 32) & 127);
-                        umma_ss<false>(tm + s * 128, sdesc_add(dk, off), sdesc_add(dq, off), id_s, ks > 0);
+                for (int u = 0; u < 2; ++u) {
+                    if (u >= nu) break;
+                    const int s = 2 * u + (uses[u] & 1);
+                    if (uses[u] >= 2 && !(ok = mbar_wait_warp(smem_u32(&bar_s_free[s]), (uses[u] / 2 - 1) & 1, w, SITE_PAGED_S_FULL))) break;
+                    ++uses[u];
+                    tc_fence_after();
+                    const uint64_t dk = sdesc_add(dk0, (keys + u) % C::NK * C::TILE);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int ks = 0; ks < D / 16; ++ks) {
+                            const uint32_t off = ((ks * 32) >> 7) * C::CHUNK + ((ks * 32) & 127);
+                            umma_ss<false>(tm + s * 128, sdesc_add(dk, off), sdesc_add(dq, off), id_s, ks > 0);
+                        }
+                        umma_commit(smem_u32(&bar_s_full[s]));
+                        if (t + 1 == p.t1) umma_commit(smem_u32(&bar_k_empty[(keys + u) % C::NK]));
+                        if (u == nu - 1) umma_commit(smem_u32(&bar_q_empty[i]));
                     }
-                    umma_commit(smem_u32(&bar_s_full[s]));
-                    umma_commit(smem_u32(&bar_q_empty[i]));
-                    if (t + 1 == p.t1) umma_commit(smem_u32(&bar_k_empty[part & 1]));
+                    __syncwarp();
                 }
-                __syncwarp();
             }
-            ++part;
+            keys += nu;
         }
         umma_commit_e(smem_u32(&bar_final));
     } else if (warp == 2) {
@@ -680,74 +699,67 @@ __global__ void __launch_bounds__(384, 1)
         }
     } else {
         // ------------------------------------------------------------ exponentials
-        const int grp = (warp - 4) >> 2, key = (warp & 3) * 32 + lane;
-        const uint32_t lt = tm + ((uint32_t)((warp & 3) * 32) << 16);
+        const int u = (warp - 4) >> 2, lk = (warp & 3) * 32 + lane, key = u * 128 + lk;
+        const uint32_t lt = tm + ((uint32_t)((warp & 3) * 32) << 16) + u * 256;
         const float2 sl2 = make_float2(a.scale_log2, a.scale_log2);
-        int item = 0, parts = 0;                           // of the CTA; this group's are items with item % 2 == grp
+        int item = 0, uses = 0;                            // query tiles; S tiles of this key tile
         bool ok = true;
         while (ok && next_part()) {
-            const float old = grp == 0 ? weight_old(a, p, key) : 0.f;
+            const int k0 = p.kt * 256 + u * 128;           // the warps' first key
+            const bool mine = k0 < p.len;
+            const float old = weight_old(a, p, key);
             float2 s2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             for (int t = p.t0; t < p.t1; ++t, ++item) {
-                if ((item & 1) != grp) continue;
-                const int s = item % kSBufs, i = item % C::NS;
-                const int tok = t / a.ngrp * a.sub, live = min(a.gs, a.G - t % a.ngrp * a.gs) * min(a.sub, p.n - tok);
-                // Rows c_min .. live-1 of the tile see this thread's key.
-                const int d = p.kt * 128 + key - (p.len - p.n) - tok;
-                const int c_min = d <= 0 ? 0 : d >= a.sub ? 128 : d * a.gs;
-                const bool edge = p.kt * 128 + 127 > p.len - p.n + tok || live < box;
-                // (The query tile's barrier stands for its lse entries.)
-                if (!(ok = mbar_wait_warp(smem_u32(&bar_q_full[i]), (item / C::NS) & 1, w, SITE_PAGED_Q) &&
-                           mbar_wait_warp(smem_u32(&bar_s_full[s]), (item / kSBufs) & 1, w, SITE_PAGED_S_FULL)))
-                    break;
-                tc_fence_after();
-                const float4* nl = reinterpret_cast<const float4*>(s_nl[i]);
+                const int i = item % C::NS;
+                // (This barrier stands for the lse entries.)
+                if (!(ok = mbar_wait_warp(smem_u32(&bar_q_full[i]), (item / C::NS) & 1, w, SITE_PAGED_Q))) break;
+                if (mine) {
+                    const int s = uses & 1;
+                    if (!(ok = mbar_wait_warp(smem_u32(&bar_s_full[2 * u + s]), (uses / 2) & 1, w, SITE_PAGED_S_FULL))) break;
+                    ++uses;
+                    tc_fence_after();
+                    const int tok = t / a.ngrp * a.sub, live = min(a.gs, a.G - t % a.ngrp * a.gs) * min(a.sub, p.n - tok);
+                    const int base = p.len - p.n + tok;    // position of the tile's first token
+                    // Rows c_min .. live-1 of the tile see this thread's key.
+                    const int d = k0 + lk - base;
+                    const int c_min = d <= 0 ? 0 : d >= a.sub ? 128 : d * a.gs;
+                    const float4* nl = reinterpret_cast<const float4*>(s_nl[i]);
+                    auto tile = [&](auto edge) {
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t x[64];
-                    tmem_ld_cols<2>(lt + s * 128 + half * 64, x);
-                    if (half == 1) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(&bar_s_free[s]));
-                    }
+                        for (int half = 0; half < 2; ++half) {
+                            uint32_t x[64];
+                            tmem_ld_cols<2>(lt + s * 128 + half * 64, x);
+                            if (half == 1) {
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(smem_u32(&bar_s_free[2 * u + s]));
+                            }
 #pragma unroll
-                    for (int e = 0; e < 64; e += 4) {
-                        const float4 l4 = nl[half * 16 + e / 4];
-                        const float2 y0 = __ffma2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), sl2, make_float2(l4.x, l4.y));
-                        const float2 y1 = __ffma2_rn(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), sl2, make_float2(l4.z, l4.w));
-                        float2 p0 = make_float2(ex2(y0.x), ex2(y0.y)), p1 = make_float2(ex2(y1.x), ex2(y1.y));
-                        if (edge) {
-                            const int c = half * 64 + e;
-                            p0.x = c >= c_min && c < live ? p0.x : 0.f;
-                            p0.y = c + 1 >= c_min && c + 1 < live ? p0.y : 0.f;
-                            p1.x = c + 2 >= c_min && c + 2 < live ? p1.x : 0.f;
-                            p1.y = c + 3 >= c_min && c + 3 < live ? p1.y : 0.f;
+                            for (int e = 0; e < 64; e += 4) {
+                                const float4 l4 = nl[half * 16 + e / 4];
+                                const float2 y0 = __ffma2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), sl2, make_float2(l4.x, l4.y));
+                                const float2 y1 = __ffma2_rn(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), sl2, make_float2(l4.z, l4.w));
+                                float2 p0 = make_float2(ex2(y0.x), ex2(y0.y)), p1 = make_float2(ex2(y1.x), ex2(y1.y));
+                                if constexpr (decltype(edge)::value) {
+                                    const int c = half * 64 + e;
+                                    p0.x = c >= c_min && c < live ? p0.x : 0.f;
+                                    p0.y = c + 1 >= c_min && c + 1 < live ? p0.y : 0.f;
+                                    p1.x = c + 2 >= c_min && c + 2 < live ? p1.x : 0.f;
+                                    p1.y = c + 3 >= c_min && c + 3 < live ? p1.y : 0.f;
+                                }
+                                s2[e / 4 % 2 * 2] = __fadd2_rn(s2[e / 4 % 2 * 2], p0);
+                                s2[e / 4 % 2 * 2 + 1] = __fadd2_rn(s2[e / 4 % 2 * 2 + 1], p1);
+                            }
                         }
-                        s2[e / 4 % 2 * 2] = __fadd2_rn(s2[e / 4 % 2 * 2], p0);
-                        s2[e / 4 % 2 * 2 + 1] = __fadd2_rn(s2[e / 4 % 2 * 2 + 1], p1);
-                    }
+                    };
+                    if (k0 + 127 > base || live < box) tile(std::true_type());
+                    else tile(std::false_type());
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&bar_q_empty[i]));
             }
             if (!ok) break;
-            const float sum = ((s2[0].x + s2[0].y) + (s2[1].x + s2[1].y)) + ((s2[2].x + s2[2].y) + (s2[3].x + s2[3].y));
-            // The two groups' sums together.
-            const int k = parts & 1;
-            if (grp == 1) {
-                if (parts >= 2 && !(ok = mbar_wait_warp(smem_u32(&bar_sum_free[k]), (parts / 2 - 1) & 1, w, SITE_PAGED_O_FULL))) break;
-                s_sum[k][key] = sum;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bar_sum_full[k]));
-            } else {
-                if (!(ok = mbar_wait_warp(smem_u32(&bar_sum_full[k]), (parts / 2) & 1, w, SITE_PAGED_O_FULL))) break;
-                const float other = s_sum[k][key];
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bar_sum_free[k]));
-                weight_put(a, p, key, sum + other, old);
-            }
-            ++parts;
+            weight_put(a, p, key, ((s2[0].x + s2[0].y) + (s2[1].x + s2[1].y)) + ((s2[2].x + s2[2].y) + (s2[3].x + s2[3].y)), old);
         }
     }
 
@@ -925,6 +937,7 @@ void weight_split(WeightKind kind, WeightArgs& a) {
     a.ngrp = (a.G + a.gs - 1) / a.gs;
     a.sub = rt / a.gs;
     a.ovh = 2 * a.sub;                                     // the ends of a unit, in tokens
+    a.key_shift = kind == WEIGHTS_MANY_F32 ? 7 : 8;
 }
 
 cudaError_t launch_paged_weights(WeightKind kind, bool f32, int D, const CUtensorMap& tq, const CUtensorMap& tk,
@@ -942,7 +955,7 @@ cudaError_t launch_paged_weights(WeightKind kind, bool f32, int D, const CUtenso
         if (D == 128) e = rc == 8 ? launch_few_t<128, 8, false>(a, st) : rc == 16 ? launch_few_t<128, 16, false>(a, st) : launch_few_t<128, 32, false>(a, st);
     }
     if (e != cudaSuccess || (kind != WEIGHTS_MANY && kind != WEIGHTS_MANY_F32)) return e;
-    return launch_k(weights_join_kernel, dim3(kWeightCtas), dim3(128), 0, st, a);
+    return launch_k(weights_join_kernel, dim3(kWeightCtas), dim3(kWeightKeys), 0, st, a);
 }
 
 }  // namespace ne

@@ -403,8 +403,8 @@ ne_status ne_paged_attn_f32(const float* q, const ne_paged_cache* cache, const i
  * bf16: tensor-core products of bf16 inputs, fp32 sums; f32: fp32 throughout.  The order of the sums depends
  * on the shape, lengths and device, never on timing.  cache->v is not read (a valid pointer all the same).  Slots at or
  * behind a length may hold anything, rows outside [cu_new[0], cu_new[B]) too.  Device-side arguments are checked as in
- * ne_paged_attn.  workspace: ne_paged_weights_workspace_size() bytes (155 KB), 256-byte aligned,
- * caller-owned, rewritten by every call. */
+ * ne_paged_attn.  workspace: ne_paged_weights_workspace_size() bytes (316 KB), 256-byte aligned,
+ * caller-owned, rewritten by every call; NULL will do where max_new * Hq / Hkv is at most 32. */
 size_t ne_paged_weights_workspace_size(void);
 ne_status ne_paged_weights(const void* q, const float* lse, const ne_paged_cache* cache, const int* page_table,
                            const int* seq_lens, const int* cu_new, const float* weights, float* weights_out, int64_t q_ld,
