@@ -40,6 +40,7 @@ EXPORTS = (
     "ne_paged_attn_f32", "ne_pages_workspace_size", "ne_pages_fork", "ne_pages_resize", "ne_pages_compact",
     "ne_paged_append_at", "ne_paged_append_at_f32", "ne_pages_evict_workspace_size", "ne_pages_evict",
     "ne_paged_weights_workspace_size", "ne_paged_weights", "ne_paged_weights_f32",
+    "ne_paged_attn_shared_workspace_size", "ne_paged_attn_shared", "ne_paged_attn_shared_f32",
 )
 
 
@@ -130,6 +131,10 @@ def load(path: str | None = None):
         lib.ne_pages_evict_workspace_size.argtypes = [i] * 4
         lib.ne_pages_evict_workspace_size.restype = sz
         lib.ne_pages_evict.argtypes = [vp] * 7 + [i, i] + [vp] * 3 + [i, i, vp, sz, vp]
+        lib.ne_paged_attn_shared_workspace_size.argtypes = [i] * 5
+        lib.ne_paged_attn_shared_workspace_size.restype = sz
+        lib.ne_paged_attn_shared.argtypes = [vp] * 7 + [i, vp, vp, i64] + [i] * 5 + [vp, sz, vp]
+        lib.ne_paged_attn_shared_f32.argtypes = lib.ne_paged_attn_shared.argtypes
         lib.ne_paged_weights_workspace_size.argtypes = []
         lib.ne_paged_weights_workspace_size.restype = sz
         lib.ne_paged_weights.argtypes = [vp] * 8 + [i64] + [i] * 5 + [vp, sz, vp]
@@ -140,7 +145,8 @@ def load(path: str | None = None):
                   "ne_attn_bwd_varlen", "ne_attn_bwd_varlen_f32", "ne_qkv_prologue",
                   "ne_attn_decode_f32", "ne_rope_spec_init", "ne_paged_append", "ne_paged_append_f32", "ne_paged_attn",
                   "ne_paged_attn_f32", "ne_pages_fork", "ne_pages_resize", "ne_pages_compact", "ne_paged_append_at",
-                  "ne_paged_append_at_f32", "ne_pages_evict", "ne_paged_weights", "ne_paged_weights_f32"):
+                  "ne_paged_append_at_f32", "ne_pages_evict", "ne_paged_weights", "ne_paged_weights_f32", "ne_paged_attn_shared",
+                  "ne_paged_attn_shared_f32"):
             getattr(lib, f).restype = i
         _lib = lib
     return _lib
@@ -543,6 +549,20 @@ def alloc_paged_workspace(B, N, Hq, Hkv, D, device="cuda"):
     return torch.empty(max(paged_workspace_size(B, N, Hq, Hkv, D), 256), dtype=torch.uint8, device=device)
 
 
+def _attn_out(q, o, lse, cu_new, dt, dev):
+    """The outputs of an attention call: the caller's, checked, or new ones."""
+    new = q.new_empty if cu_new is None else q.new_zeros   # (without cu_new every row is written)
+    if o is None:
+        o = new(q.shape)
+    elif o.shape != q.shape or o.dtype is not dt or o.get_device() != dev or not o.is_contiguous():
+        raise ValueError("o must be contiguous and match q")
+    if lse is None:
+        lse = new(q.shape[:2], dtype=_F32)
+    elif lse.shape != q.shape[:2] or lse.dtype is not _F32 or lse.get_device() != dev or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous fp32 [N, Hq]")
+    return o, lse
+
+
 def paged_attn(q, k_pages, v_pages, page_table, seq_lens, cu_new=None, max_new: int | None = None, o=None, lse=None,
                workspace=None):
     """Attention of the new tokens over the paged cache (ne_paged_attn): q [N, Hq, D]
@@ -557,20 +577,47 @@ def paged_attn(q, k_pages, v_pages, page_table, seq_lens, cu_new=None, max_new: 
     N, Hq = q.shape[:2]
     B, W, pt, ln, cu = _paged_batch(page_table, seq_lens, cu_new, N, dev)
     q_ld = _rows(q, "q", N, Hq, D, dt, dev)
-    new = q.new_empty if cu_new is None else q.new_zeros   # (without cu_new every row is written)
-    if o is None:
-        o = new((N, Hq, D))
-    elif o.shape != q.shape or o.dtype is not dt or o.get_device() != dev or not o.is_contiguous():
-        raise ValueError("o must be contiguous and match q")
-    if lse is None:
-        lse = new((N, Hq), dtype=_F32)
-    elif lse.shape != (N, Hq) or lse.dtype is not torch.float32 or lse.get_device() != dev or not lse.is_contiguous():
-        raise ValueError("lse must be contiguous fp32 [N, Hq]")
+    o, lse = _attn_out(q, o, lse, cu_new, dt, dev)
     if workspace is None:
         workspace = alloc_paged_workspace(B, N, Hq, Hkv, D, k_pages.device)
     _launch(lib.ne_paged_attn if dt is _BF16 else lib.ne_paged_attn_f32, dev, q.data_ptr(), c, pt,
             ln, cu, o.data_ptr(), lse.data_ptr(), q_ld, B, N, Hq, W, max(1, N) if max_new is None else max_new,
             *_ws(workspace, dev))
+    return o, lse
+
+
+def paged_shared_workspace_size(B, N, Hq, Hkv, D) -> int:
+    _c_ints(B=B, N=N, Hq=Hq, Hkv=Hkv, D=D)
+    return int(load().ne_paged_attn_shared_workspace_size(B, N, Hq, Hkv, D))
+
+
+def alloc_paged_shared_workspace(B, N, Hq, Hkv, D, device="cuda"):
+    """Workspace of paged_attn_shared calls of this shape (up to N rows) that run one after another."""
+    return torch.empty(max(paged_shared_workspace_size(B, N, Hq, Hkv, D), 256), dtype=torch.uint8, device=device)
+
+
+def paged_attn_shared(q, k_pages, v_pages, page_table, seq_lens, groups, shared, cu_new=None, max_new: int | None = None,
+                      o=None, lse=None, workspace=None):
+    """paged_attn for sequences that share their first positions (ne_paged_attn_shared): sequences
+    groups[r] .. groups[r+1]-1 (int32 [R + 1]) hold the same in their first shared[r] (int32 [R]) positions,
+    in front of their new tokens; those are read and multiplied once per group.  Returns what paged_attn
+    returns, up to rounding."""
+    if max_new is not None and not 1 <= max_new <= _INT_MAX:
+        _c_ints(max_new=max_new)
+    lib = _lib or load()
+    c, dev, dt, _, Hkv, D = _paged_cache(k_pages, v_pages, False)
+    N, Hq = q.shape[:2]
+    B, W, pt, ln, cu = _paged_batch(page_table, seq_lens, cu_new, N, dev)
+    q_ld = _rows(q, "q", N, Hq, D, dt, dev)
+    if shared.dim() != 1 or shared.shape[0] > B:
+        raise ValueError("shared must be [R], at most one group per sequence")
+    R = shared.shape[0]
+    gp, sp = _ints(groups, (R + 1,), dev, "groups"), _ints(shared, (R,), dev, "shared")
+    o, lse = _attn_out(q, o, lse, cu_new, dt, dev)
+    if workspace is None:
+        workspace = alloc_paged_shared_workspace(B, N, Hq, Hkv, D, k_pages.device)
+    _launch(lib.ne_paged_attn_shared if dt is _BF16 else lib.ne_paged_attn_shared_f32, dev, q.data_ptr(), c, pt, ln, cu, gp, sp, R,
+            o.data_ptr(), lse.data_ptr(), q_ld, B, N, Hq, W, max(1, N) if max_new is None else max_new, *_ws(workspace, dev))
     return o, lse
 
 

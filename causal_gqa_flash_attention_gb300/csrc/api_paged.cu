@@ -223,10 +223,9 @@ size_t attn_ws_bytes(int D, int Hkv, int G) {
     return round_up(most, 256);
 }
 
-ne_status attn_impl(int eb, const void* q, const ne_paged_cache* c, const int* table, const int* lens, const int* cu,
-                    void* o, float* lse, int64_t q_ld, int B, int N, int Hq, int W, int max_new, void* ws,
-                    size_t ws_bytes, ne_stream_t stream) {
-    clear_error();
+// Checks of a call of ne_paged_attn but for its workspace.
+ne_status attn_check(int eb, const void* q, const ne_paged_cache* c, const int* table, const int* lens, const int* cu,
+                     const void* o, const float* lse, int64_t q_ld, int B, int N, int Hq, int W, int max_new) {
     ne_status s = check_cache(c, eb, true);
     if (s != NE_OK) return s;
     if (Hq < 1 || Hq % c->Hkv != 0)
@@ -240,32 +239,56 @@ ne_status attn_impl(int eb, const void* q, const ne_paged_cache* c, const int* t
     if (rows_overlap(o, row, row, q, row, q_ld * eb, N) || rows_overlap(lse, Hq * 4, Hq * 4, q, row, q_ld * eb, N) ||
         overlap(o, (size_t)(row * N), lse, (size_t)N * Hq * 4))
         return fail(NE_ERR_INVALID_ARG, "o, lse and q must not overlap");
-    const int G = Hq / c->Hkv;
-    const size_t need = attn_ws_bytes(c->D, c->Hkv, G);
+    return NE_OK;
+}
+
+ne_status attn_ws_check(const void* ws, size_t ws_bytes, size_t need) {
     if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
         return fail(NE_ERR_INVALID_ARG, "workspace must be non-null and 256-byte aligned (%zu bytes needed)", need);
     if (ws_bytes < need)
         return fail(NE_ERR_INVALID_ARG, "workspace too small: %zu bytes given, %zu needed", ws_bytes, need);
-    ne::PagedAttnArgs a = {};
-    if ((s = ready((cudaStream_t)stream, &a.err)) != NE_OK) return s;
-    const bool f32 = eb == 4;
-    const ne::PagedKind kind = ne::paged_kind(f32, c->D, G, cu ? std::min(max_new, N) : 1);
+    return NE_OK;
+}
+
+// What the kernels of a call are told; `ws` holds the parts.
+ne_status attn_args(ne::PagedAttnArgs* out, ne::PagedKind kind, const void* q, const ne_paged_cache* c, const int* table,
+                    const int* lens, const int* cu, void* o, float* lse, int64_t q_ld, int B, int N, int Hq, int W, void* ws,
+                    ne_stream_t stream) {
+    ne::PagedAttnArgs& a = *out;
+    a = ne::PagedAttnArgs();
+    const ne_status s = ready((cudaStream_t)stream, &a.err);
+    if (s != NE_OK) return s;
     a.c = view_of(c);
     a.s = batch_of(c, table, lens, cu, B, N, W);
-    a.p = ne::paged_split(kind, c->D, c->Hkv, G, a.s.cap);
+    a.G = Hq / c->Hkv;
+    a.p = ne::paged_split(kind, c->D, c->Hkv, a.G, a.s.cap);
     a.q = q;
     a.o = o;
     a.lse = lse;
     a.q_ld = q_ld;
     a.Hq = Hq;
     a.Hkv = c->Hkv;
-    a.G = G;
     a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)c->D));
     const size_t parts = 2 * (size_t)a.p.C;
     a.part_o = static_cast<float*>(ws);
     a.part_ml = reinterpret_cast<float2*>(a.part_o + parts * a.p.rows * c->D);
     a.part_info = reinterpret_cast<int4*>(a.part_ml + parts * a.p.rows);
     a.timeout_ns = timeout_ns();
+    return NE_OK;
+}
+
+ne_status attn_impl(int eb, const void* q, const ne_paged_cache* c, const int* table, const int* lens, const int* cu,
+                    void* o, float* lse, int64_t q_ld, int B, int N, int Hq, int W, int max_new, void* ws,
+                    size_t ws_bytes, ne_stream_t stream) {
+    clear_error();
+    ne_status s = attn_check(eb, q, c, table, lens, cu, o, lse, q_ld, B, N, Hq, W, max_new);
+    if (s != NE_OK || B == 0 || N == 0) return s;
+    const int G = Hq / c->Hkv;
+    if ((s = attn_ws_check(ws, ws_bytes, attn_ws_bytes(c->D, c->Hkv, G))) != NE_OK) return s;
+    const bool f32 = eb == 4;
+    const ne::PagedKind kind = ne::paged_kind(f32, c->D, G, cu ? std::min(max_new, N) : 1);
+    ne::PagedAttnArgs a;
+    if ((s = attn_args(&a, kind, q, c, table, lens, cu, o, lse, q_ld, B, N, Hq, W, ws, stream)) != NE_OK) return s;
     cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e;
     if (kind == ne::PAGED_TILES) {
@@ -279,6 +302,82 @@ ne_status attn_impl(int eb, const void* q, const ne_paged_cache* c, const int* t
     e = ne::launch_paged_join(f32, c->D, a, st);
     if (e != cudaSuccess) return cuda_fail(e, "paged_attn join launch");
     return NE_OK;
+}
+
+// ---------------------------------------------------------------- shared prefixes
+// Rows per kv head from which on a sequence fills the kernels' row tiles by itself, so that nothing is
+// won by putting rows of several sequences into one.
+constexpr int kSharedRows = 256;
+
+struct SharedWs {
+    size_t parts, row_o, row_ml, rec, total;   // parts, row_o, row_ml and records of one of the two lines; both
+};
+SharedWs shared_ws(int N, int Hq, int Hkv, int D) {
+    const int G = Hq / Hkv;
+    SharedWs w;
+    w.parts = attn_ws_bytes(D, Hkv, G);
+    if (G <= 128) w.parts = std::max(w.parts, round_up(ne::paged_part_bytes(ne::paged_split(ne::PAGED_TILES, D, Hkv, G, 1 << 30), D), 256));
+    const size_t rows = (size_t)N * Hq;
+    w.row_o = round_up(rows * D * 4, 256);
+    w.row_ml = round_up(rows * 8, 256);
+    w.rec = round_up(rows * 8, 256);           // (a head group has at least one head)
+    w.total = 2 * (w.parts + w.row_o + w.row_ml + w.rec);
+    return w;
+}
+
+ne_status shared_launch(ne::PagedKind kind, bool f32, const ne_paged_cache* c, const ne::PagedAttnArgs& a, cudaStream_t st) {
+    cudaError_t e;
+    if (kind == ne::PAGED_TILES) {
+        CUtensorMap tq, tk, tv;
+        const ne_status s = tile_maps(&tq, &tk, &tv, c, a.c, a.q, a.q_ld, a.Hq, a.s.N, a.G, a.p.sub);
+        if (s != NE_OK) return s;
+        e = ne::launch_shared_tiles(c->D, tq, tk, tv, a, st);
+    } else if (f32) e = ne::launch_shared_f32(kind, c->D, a, st);
+    else e = ne::launch_shared_short(kind, c->D, a, st);
+    return e == cudaSuccess ? NE_OK : cuda_fail(e, "paged_attn_shared launch");
+}
+
+ne_status shared_impl(int eb, const void* q, const ne_paged_cache* c, const int* table, const int* lens, const int* cu,
+                      const int* groups, const int* shared, int R, void* o, float* lse, int64_t q_ld, int B, int N, int Hq, int W,
+                      int max_new, void* ws, size_t ws_bytes, ne_stream_t stream) {
+    clear_error();
+    ne_status s = attn_check(eb, q, c, table, lens, cu, o, lse, q_ld, B, N, Hq, W, max_new);
+    if (s != NE_OK) return s;
+    if (R < 0 || R > B) return fail(NE_ERR_INVALID_ARG, "need 0 <= R <= B groups (R=%d B=%d)", R, B);
+    if (B == 0 || N == 0) return NE_OK;
+    if (!aligned4(groups) || (R > 0 && !aligned4(shared)))
+        return fail(NE_ERR_INVALID_ARG, "groups and shared must be non-null, 4-byte aligned device pointers");
+    const SharedWs w = shared_ws(N, Hq, c->Hkv, c->D);
+    if ((s = attn_ws_check(ws, ws_bytes, w.total)) != NE_OK) return s;
+    const int G = Hq / c->Hkv, most = cu ? std::min(max_new, N) : 1;
+    const bool f32 = eb == 4;
+    if (R == 0 || (long long)most * G >= kSharedRows)
+        return attn_impl(eb, q, c, table, lens, cu, o, lse, q_ld, B, N, Hq, W, max_new, ws, ws_bytes, stream);
+    const ne::PagedKind own_kind = ne::paged_kind(f32, c->D, G, most);
+    // All rows of a group together; head_dim 32 has a tile kernel here.
+    ne::PagedKind pre_kind = ne::paged_kind(f32, c->D, G, N);
+    if (!f32 && (long long)N * G > 32 && G <= 128) pre_kind = ne::PAGED_TILES;
+    ne::PagedAttnArgs a[2];                    // prefixes, own positions
+    char* base = static_cast<char*>(ws);
+    for (int i = 0; i < 2; ++i) {
+        if ((s = attn_args(&a[i], i ? own_kind : pre_kind, q, c, table, lens, cu, o, lse, q_ld, i ? B : R, N, Hq, W, base, stream)) != NE_OK)
+            return s;
+        a[i].s.groups = groups;
+        a[i].s.shared = shared;
+        a[i].s.R = R;
+        a[i].s.seqs = B;
+        a[i].s.prefix = !i;
+        a[i].row_o = reinterpret_cast<float*>(base + w.parts);
+        a[i].row_ml = reinterpret_cast<float2*>(base + w.parts + w.row_o);
+        a[i].rec_first = reinterpret_cast<int*>(base + w.parts + w.row_o + w.row_ml);
+        a[i].rec_last = a[i].rec_first + (size_t)N * Hq;
+        base += w.total / 2;
+    }
+    cudaStream_t st = (cudaStream_t)stream;
+    if ((s = shared_launch(pre_kind, f32, c, a[0], st)) != NE_OK) return s;
+    if ((s = shared_launch(own_kind, f32, c, a[1], st)) != NE_OK) return s;
+    const cudaError_t e = ne::launch_shared_join(f32, c->D, a[0], a[1], st);
+    return e == cudaSuccess ? NE_OK : cuda_fail(e, "paged_attn_shared join launch");
 }
 
 // ---------------------------------------------------------------- accumulated weights
@@ -576,6 +675,27 @@ ne_status ne_paged_attn_f32(const float* q, const ne_paged_cache* cache, const i
                             int max_new, void* workspace, size_t workspace_bytes, ne_stream_t stream) {
     return attn_impl(4, q, cache, page_table, seq_lens, cu_new, o, lse, q_ld, B, N, Hq, max_pages, max_new, workspace,
                      workspace_bytes, stream);
+}
+
+size_t ne_paged_attn_shared_workspace_size(int B, int N, int Hq, int Hkv, int D) {
+    if (B < 0 || N < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || (D != 32 && D != 64 && D != 128)) return 0;
+    return shared_ws(N, Hq, Hkv, D).total;
+}
+
+ne_status ne_paged_attn_shared(const void* q, const ne_paged_cache* cache, const int* page_table, const int* seq_lens,
+                               const int* cu_new, const int* groups, const int* shared, int R, void* o, float* lse,
+                               int64_t q_ld, int B, int N, int Hq, int max_pages, int max_new, void* workspace,
+                               size_t workspace_bytes, ne_stream_t stream) {
+    return shared_impl(2, q, cache, page_table, seq_lens, cu_new, groups, shared, R, o, lse, q_ld, B, N, Hq, max_pages, max_new,
+                       workspace, workspace_bytes, stream);
+}
+
+ne_status ne_paged_attn_shared_f32(const float* q, const ne_paged_cache* cache, const int* page_table, const int* seq_lens,
+                                   const int* cu_new, const int* groups, const int* shared, int R, float* o, float* lse,
+                                   int64_t q_ld, int B, int N, int Hq, int max_pages, int max_new, void* workspace,
+                                   size_t workspace_bytes, ne_stream_t stream) {
+    return shared_impl(4, q, cache, page_table, seq_lens, cu_new, groups, shared, R, o, lse, q_ld, B, N, Hq, max_pages, max_new,
+                       workspace, workspace_bytes, stream);
 }
 
 size_t ne_paged_weights_workspace_size(void) { return kWeightWs; }

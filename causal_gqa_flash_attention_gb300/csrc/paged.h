@@ -24,7 +24,15 @@ struct PagedBatch {
     const int* cu;                    // [B + 1], or null: one row per sequence
     int B, N, W;
     int cap;                          // W * page_size: the longest length a table row can hold
+    // Sequences that share a prefix (the kernels' SHARED form; otherwise unused).
+    const int* groups;                // [R + 1]
+    const int* shared;                // [R]
+    int R, seqs;                      // groups; sequences
+    int prefix;                       // 1: the line's members are the groups' prefixes (B is R), 0: the sequences' own positions
 };
+// Shared positions count in whole steps of this (a multiple of every page and key tile), so that a
+// sequence's own positions begin on a page; the rest is read by every sequence for itself.
+constexpr int kSharedStep = 256;
 
 struct AppendArgs {
     PagedView c;
@@ -77,9 +85,17 @@ struct PagedAttnArgs {
     float* part_o;                    // [2C, rows, D] unnormalised outputs of cut units
     float2* part_ml;                  // [2C, rows] (running max in log2 units, sum)
     int4* part_info;                  // [2C] (state: 0 none, 1, 2 the unit's last; first row, tokens, head group)
+    // SHARED: uncut units' rows, and for every token and head group the CTAs that hold its unit's first
+    // and last part (first: | token within the unit << 16 | kHasPrefix; -1, -2: no keys, without, with a prefix).
+    float* row_o;                     // [N, Hq, D] unnormalised
+    float2* row_ml;                   // [N, Hq]
+    int* rec_first;                   // [N, hg]
+    int* rec_last;
     int* err;
     unsigned long long timeout_ns;
 };
+
+constexpr int kHasPrefix = 1 << 30;
 
 // Dynamic shared memory of a kernel, set once per device (the first 64).
 template <typename F>
@@ -107,6 +123,13 @@ cudaError_t launch_paged_short(PagedKind kind, int D, const PagedAttnArgs& a, cu
 cudaError_t launch_paged_f32(PagedKind kind, int D, const PagedAttnArgs& a, cudaStream_t st);
 cudaError_t launch_paged_tiles(int D, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                const PagedAttnArgs& a, cudaStream_t st);
+// The same over prefixes or own positions, results as parts (a.s.groups set).
+cudaError_t launch_shared_short(PagedKind kind, int D, const PagedAttnArgs& a, cudaStream_t st);
+cudaError_t launch_shared_f32(PagedKind kind, int D, const PagedAttnArgs& a, cudaStream_t st);
+cudaError_t launch_shared_tiles(int D, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                const PagedAttnArgs& a, cudaStream_t st);
+// Puts prefixes' and own positions' parts together.
+cudaError_t launch_shared_join(bool f32, int D, const PagedAttnArgs& pre, const PagedAttnArgs& own, cudaStream_t st);
 // Joins the parts of cut units.
 cudaError_t launch_paged_join(bool f32, int D, const PagedAttnArgs& a, cudaStream_t st);
 

@@ -45,7 +45,8 @@ struct F32Cfg {
     static_assert(WK * ROWS * D * 4 <= RINGS, "the join fits into the rings");
 };
 
-template <int D, int RW, bool MANY>
+// SH: the SHARED form, results as parts alone.
+template <int D, int RW, bool MANY, bool SH>
 __global__ void __launch_bounds__(F32Cfg<D, RW, MANY>::THREADS, F32Cfg<D, RW, MANY>::CTAS) paged_f32_kernel(const PagedAttnArgs a) {
     using C = F32Cfg<D, RW, MANY>;
     constexpr int U = C::U, DL = C::DL;
@@ -60,20 +61,20 @@ __global__ void __launch_bounds__(F32Cfg<D, RW, MANY>::THREADS, F32Cfg<D, RW, MA
 
     griddep_launch_dependents();
     griddep_wait();
-    PagedWalk walk;
-    paged_locate<C::THREADS>(a, blockIdx.x, loc, blockIdx.x == 0);
+    PagedWalkOf<SH> walk;
+    paged_locate<C::THREADS, SH>(a, blockIdx.x, loc, blockIdx.x == 0);
     walk.init(a, loc.w0, loc.w1, loc.snap, loc.b, loc.start);
     if (tid < 2) a.part_info[blockIdx.x * 2 + tid] = make_int4(0, 0, 0, 0);
 
     const int ngrp = (a.G + a.p.gs - 1) / a.p.gs;          // head groups of a kv head
     const uint32_t ring0 = smem_u32(smem) + wk * C::SLOTS * C::TILE;
-    PagedSeg g;
+    typename PagedSegOf<SH>::type g;
     while (walk.next(a, g)) {
         const int hkv = g.hg / ngrp, hs = g.hg % ngrp;
         const int h0 = hkv * a.G + hs * a.p.gs;
         const int gs = min(a.p.gs, a.G - hs * a.p.gs);
         const int live_rows = g.ntok * gs;
-        const int* trow = a.s.table + (size_t)g.b * a.s.W;
+        const int* trow = paged_row(a, g);
         const char* kp = static_cast<const char*>(a.c.k) + (long long)hkv * a.c.head_stride * 4;
         const char* vp = static_cast<const char*>(a.c.v) + (long long)hkv * a.c.head_stride * 4;
 
@@ -293,7 +294,11 @@ __global__ void __launch_bounds__(F32Cfg<D, RW, MANY>::THREADS, F32Cfg<D, RW, MA
                 acc.z += x.z * wt;
                 acc.w += x.w * wt;
             }
-            if (g.whole()) {
+            if (SH && g.whole()) {
+                const long long orow = (long long)(g.tok0 + g.tok + row / gs) * a.Hq + h0 + row % gs;
+                *reinterpret_cast<float4*>(a.row_o + orow * D + e) = acc;
+                if (e == 0) a.row_ml[orow] = make_float2(mm, ll);
+            } else if (g.whole()) {
                 const float inv = ll == 0.f ? 0.f : 1.f / ll;
                 const long long orow = (long long)(g.tok0 + g.tok + row / gs) * a.Hq + h0 + row % gs;
                 *reinterpret_cast<float4*>(static_cast<float*>(a.o) + orow * D + e) =
@@ -306,14 +311,15 @@ __global__ void __launch_bounds__(F32Cfg<D, RW, MANY>::THREADS, F32Cfg<D, RW, MA
             }
         }
         if (!g.whole() && tid == 0) a.part_info[pslot] = paged_record(g);
+        if constexpr (SH) paged_where(a, g, tid, C::THREADS);
         __syncthreads();
     }
 }
 
-template <int D, int RW, bool MANY>
+template <int D, int RW, bool MANY, bool SH>
 cudaError_t launch_f32_t(const PagedAttnArgs& a, cudaStream_t st) {
     using C = F32Cfg<D, RW, MANY>;
-    auto kfn = paged_f32_kernel<D, RW, MANY>;
+    auto kfn = paged_f32_kernel<D, RW, MANY, SH>;
     static_assert(C::SMEM + 4096 <= 227 * 1024, "shared memory");
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(kfn, C::SMEM, done);
@@ -321,13 +327,13 @@ cudaError_t launch_f32_t(const PagedAttnArgs& a, cudaStream_t st) {
     return launch_k(kfn, dim3(a.p.C), dim3(C::THREADS), C::SMEM, st, a);
 }
 
-template <int D>
+template <int D, bool SH>
 cudaError_t launch_f32_d(PagedKind kind, const PagedAttnArgs& a, cudaStream_t st) {
     switch (kind) {
-        case PAGED_F32_FEW4: return launch_f32_t<D, 4, false>(a, st);
-        case PAGED_F32_FEW8: return launch_f32_t<D, 8, false>(a, st);
-        case PAGED_F32_FEW16: return launch_f32_t<D, 16, false>(a, st);
-        default: return launch_f32_t<D, 8, true>(a, st);
+        case PAGED_F32_FEW4: return launch_f32_t<D, 4, false, SH>(a, st);
+        case PAGED_F32_FEW8: return launch_f32_t<D, 8, false, SH>(a, st);
+        case PAGED_F32_FEW16: return launch_f32_t<D, 16, false, SH>(a, st);
+        default: return launch_f32_t<D, 8, true, SH>(a, st);
     }
 }
 
@@ -336,8 +342,13 @@ cudaError_t launch_f32_d(PagedKind kind, const PagedAttnArgs& a, cudaStream_t st
 int paged_f32_bn(bool many) { return many ? F32Cfg<64, 8, true>::BN : F32Cfg<64, 8, false>::BN; }
 
 cudaError_t launch_paged_f32(PagedKind kind, int D, const PagedAttnArgs& a, cudaStream_t st) {
-    if (D == 32) return launch_f32_d<32>(kind, a, st);
-    if (D == 64) return launch_f32_d<64>(kind, a, st);
+    if (D == 32) return launch_f32_d<32, false>(kind, a, st);
+    if (D == 64) return launch_f32_d<64, false>(kind, a, st);
+    return cudaErrorInvalidValue;
+}
+cudaError_t launch_shared_f32(PagedKind kind, int D, const PagedAttnArgs& a, cudaStream_t st) {
+    if (D == 32) return launch_f32_d<32, true>(kind, a, st);
+    if (D == 64) return launch_f32_d<64, true>(kind, a, st);
     return cudaErrorInvalidValue;
 }
 

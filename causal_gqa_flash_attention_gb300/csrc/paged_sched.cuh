@@ -25,6 +25,18 @@ namespace ne {
 struct PagedSeq {
     int tok0, n, len;
 };
+// A member of a SHARED line: its table row, and the positions in front of its first key.
+struct PagedSharedSeq : PagedSeq {
+    int row, skip;
+};
+template <bool SH>
+struct PagedSeqOf {
+    typedef PagedSeq type;
+};
+template <>
+struct PagedSeqOf<true> {
+    typedef PagedSharedSeq type;
+};
 
 // Row offsets and length of sequence b as they stand in memory.
 struct PagedRaw {
@@ -51,6 +63,62 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedBatch& s, int b, int& b
     return paged_clamp(s, paged_raw(s, b), bad);
 }
 
+// Shared positions of group r, which begins with sequence g0 (all in whole steps; 0 where there is
+// nothing to share).
+__device__ __forceinline__ int paged_shared(const PagedBatch& s, int r, int& g0, int& g1, int& bad) {
+    g0 = __ldg(s.groups + r);
+    g1 = __ldg(s.groups + r + 1);
+    const int n = __ldg(s.shared + r);
+    if (g0 < 0 || g1 > s.seqs || g1 < g0 || n < 0) {
+        bad = SITE_PAGED_GROUP;
+        g0 = g1 = 0;
+        return 0;
+    }
+    return g1 - g0 < 2 ? 0 : min(n, min(max(__ldg(s.lens + g0), 0), s.cap)) & ~(kSharedStep - 1);
+}
+// Member b of a SHARED line.  A prefix: the rows of all its sequences, every one of which sees every key.
+__device__ __forceinline__ PagedSharedSeq paged_shared_seq(const PagedBatch& s, int b, int& bad) {
+    PagedSharedSeq q;
+    if (s.prefix) {
+        int g0, g1;
+        q.len = paged_shared(s, b, g0, g1, bad);
+        PagedRaw w;
+        w.c0 = s.cu ? __ldg(s.cu + g0) : g0;
+        w.c1 = s.cu ? __ldg(s.cu + g1) : g1;
+        w.l = 0;
+        const PagedSeq t = paged_clamp(s, w, bad);
+        q.tok0 = t.tok0;
+        q.n = q.len ? t.n : 0;
+        q.row = g0;
+        q.skip = 0;
+        return q;
+    }
+    int lo = -1, hi = s.R - 1;                             // the last group that begins at or before b
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (__ldg(s.groups + mid) <= b) lo = mid;
+        else hi = mid - 1;
+    }
+    q.skip = 0;
+    if (lo >= 0) {
+        int g0, g1;
+        const int n = paged_shared(s, lo, g0, g1, bad);
+        if (b < g1) q.skip = n;
+    }
+    const PagedSeq t = paged_seq(s, b, bad);
+    if (q.skip > 0 && q.skip > t.len - t.n) bad = SITE_PAGED_GROUP;   // (new tokens among the shared positions)
+    q.tok0 = t.tok0;
+    q.n = t.n;
+    q.len = max(0, t.len - q.skip);
+    q.row = b;
+    return q;
+}
+template <bool SH>
+__device__ __forceinline__ typename PagedSeqOf<SH>::type paged_seq_of(const PagedBatch& s, int b, int& bad) {
+    if constexpr (SH) return paged_shared_seq(s, b, bad);
+    else return paged_seq(s, b, bad);
+}
+
 // Cost of tiles 0 .. r-1 of a sequence (r below its tile count, so they are full): each
 // ovh + w_full max(0, base + (k+1) tpt).
 __device__ __forceinline__ long long paged_prefix(int r, int base, const PagedSplit& p) {
@@ -59,6 +127,13 @@ __device__ __forceinline__ long long paged_prefix(int r, int base, const PagedSp
     const long long m = r - r0;
     return (long long)r * p.ovh +
            p.w_full * (m * base + (long long)p.tpt * (((long long)r * (r + 1) - (long long)r0 * (r0 + 1)) / 2));
+}
+
+// The same of a member of a line: every tile of a prefix has all its keys.
+template <bool SH>
+__device__ __forceinline__ long long paged_prefix_of(int r, const PagedSeq& q, const PagedAttnArgs& a) {
+    if (SH && a.s.prefix) return (long long)r * (a.p.ovh + (long long)a.p.w_full * q.len);
+    return paged_prefix(r, q.len - q.n, a.p);
 }
 
 // Tiles of a sequence.
@@ -76,6 +151,14 @@ __device__ __forceinline__ long long paged_group_cost(const PagedSeq& q, const P
     return paged_prefix(last, q.len - q.n, p) + p.ovh + (long long)paged_weight(q.n - last * p.tpt, p) * q.len;
 }
 
+template <bool SH>
+__device__ __forceinline__ long long paged_group_cost_of(const PagedSeq& q, const PagedAttnArgs& a) {
+    if (!SH || !a.s.prefix) return paged_group_cost(q, a.p);
+    if (q.n == 0) return 0;
+    const int last = paged_tiles(q.n, a.p) - 1;
+    return paged_prefix_of<SH>(last, q, a) + a.p.ovh + (long long)paged_weight(q.n - last * a.p.tpt, a.p) * q.len;
+}
+
 // What a CTA does with one unit: key tiles [t0, t1) of nt_keys, for tokens tok .. tok+ntok-1
 // of the sequence.
 struct PagedSeg {
@@ -89,26 +172,46 @@ struct PagedSeg {
     __device__ __forceinline__ int slot() const { return t0 == 0 ? 1 : 0; }
 };
 
-struct PagedWalk {
+struct PagedSharedSeg : PagedSeg {
+    int row, skip;      // its sequence's table row, and positions in front of key 0
+};
+template <bool SH>
+struct PagedSegOf {
+    typedef PagedSeg type;
+};
+template <>
+struct PagedSegOf<true> {
+    typedef PagedSharedSeg type;
+};
+// The pages of a part's keys.
+__device__ __forceinline__ const int* paged_row(const PagedAttnArgs& a, const PagedSeg& g) { return a.s.table + (size_t)g.b * a.s.W; }
+__device__ __forceinline__ const int* paged_row(const PagedAttnArgs& a, const PagedSharedSeg& g) {
+    return a.s.table + (size_t)g.row * a.s.W + (g.skip >> a.c.ps_shift);
+}
+
+template <bool SH>
+struct PagedWalkOf {
+    typedef typename PagedSegOf<SH>::type Seg;
     long long w0, w1;   // the CTA's interval
     long long cur;      // start of the current unit
     int snap;           // a cut this near to a unit's end, in tiles, moves there
-    PagedSeq q;
+    typename PagedSeqOf<SH>::type q;
     PagedRaw ahead;     // the next sequence's, fetched while this one is walked
     int b, hg, r, nt;
 
     __device__ __forceinline__ void fetch(const PagedAttnArgs& a) {
-        if (b + 1 < a.s.B) ahead = paged_raw(a.s, b + 1);
+        if (!SH && b + 1 < a.s.B) ahead = paged_raw(a.s, b + 1);
     }
     // Sequence b, whose values were fetched ahead.
     __device__ __forceinline__ void take(const PagedAttnArgs& a) {
         int bad = 0;
-        q = paged_clamp(a.s, ahead, bad);
+        if constexpr (SH) q = paged_shared_seq(a.s, b, bad);
+        else q = paged_clamp(a.s, ahead, bad);
         nt = paged_tiles(q.n, a.p);
         fetch(a);
     }
     __device__ __forceinline__ void load(const PagedAttnArgs& a) {
-        ahead = paged_raw(a.s, b);
+        if (!SH) ahead = paged_raw(a.s, b);
         take(a);
     }
     // From the sequence that holds w0 (q, set by the caller or by load) and where it starts.
@@ -129,7 +232,7 @@ struct PagedWalk {
         } else {
             load(a);
         }
-        const long long S = paged_group_cost(q, a.p);
+        const long long S = paged_group_cost_of<SH>(q, a);
         const long long off = w0 - start;
         // off / S by an estimate (off < S times the head groups, so it is off by one at most).
         hg = min(a.p.hg - 1, (int)__fdividef((float)off, (float)S));
@@ -144,17 +247,18 @@ struct PagedWalk {
         int lo = 0, hi = nt - 1;                           // the last tile whose start is at or before x
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (paged_prefix(mid, q.len - q.n, a.p) <= x) lo = mid;
+            if (paged_prefix_of<SH>(mid, q, a) <= x) lo = mid;
             else hi = mid - 1;
         }
         r = lo;
-        cur = start + (long long)hg * S + paged_prefix(r, q.len - q.n, a.p);
+        cur = start + (long long)hg * S + paged_prefix_of<SH>(r, q, a);
     }
     // The next part of the interval, false at its end.
-    __device__ __forceinline__ bool next(const PagedAttnArgs& a, PagedSeg& g) {
+    __device__ __forceinline__ bool next(const PagedAttnArgs& a, Seg& g) {
         while (cur < w1) {
-            const int base = q.len - q.n;
-            const int kv = r == nt - 1 ? q.len : max(0, base + (r + 1) * a.p.tpt);
+            const bool all = SH && a.s.prefix;             // every row sees every key
+            const int base = all ? q.len : q.len - q.n;
+            const int kv = r == nt - 1 || all ? q.len : max(0, base + (r + 1) * a.p.tpt);
             const int ntok = min(a.p.tpt, q.n - r * a.p.tpt);
             const long long cost = a.p.ovh + (long long)paged_weight(ntok, a.p) * kv;
             const int ntk = (kv + (1 << a.p.bn_shift) - 1) >> a.p.bn_shift;
@@ -178,6 +282,10 @@ struct PagedWalk {
             g.len = q.len;
             g.kv = kv;
             g.nt = ntk;
+            if constexpr (SH) {
+                g.row = q.row;
+                g.skip = q.skip;
+            }
             const bool mine = g.t0 < g.t1 || (ntk == 0 && w0 <= cur);   // a unit without keys: its rows are still written
             cur += cost;
             if (++r == nt) {
@@ -194,6 +302,7 @@ struct PagedWalk {
         return false;
     }
 };
+typedef PagedWalkOf<false> PagedWalk;
 
 // The CTA's share of `total`: CTA c of p.C, or of as many as have min_work each in a small call.
 __device__ __forceinline__ void paged_interval(const PagedSplit& p, long long total, int c, long long& w0, long long& w1) {
@@ -222,15 +331,15 @@ struct PagedLocate {
 // All T threads of the CTA: the total work, this CTA's interval, and the sequence that its
 // start falls into.  Two passes over the lengths when they exceed T sequences (the first
 // sums, the second finds), one otherwise.
-template <int T>
+template <int T, bool SH = false>
 __device__ __forceinline__ void paged_locate(const PagedAttnArgs& a, int c, PagedLocate& sm, bool report) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int B = a.s.B;
     int bad = 0;
     auto work = [&](int b) -> long long {
         if (b >= B) return 0;
-        const PagedSeq q = paged_seq(a.s, b, bad);
-        return paged_group_cost(q, a.p) * a.p.hg;
+        const PagedSeq q = paged_seq_of<SH>(a.s, b, bad);
+        return paged_group_cost_of<SH>(q, a) * a.p.hg;
     };
     // Inclusive sums over the CTA; the total in sm.warp_sum[T / 32 - 1].
     auto scan = [&](long long x) -> long long {
@@ -294,14 +403,15 @@ __device__ __forceinline__ void paged_locate(const PagedAttnArgs& a, int c, Page
 
 // paged_locate for one warp: the walk of CTA c from its first unit on.  Written for few
 // dependent steps: all CTAs wait for it at the start of a call.
-__device__ __forceinline__ void paged_locate_warp(const PagedAttnArgs& a, int c, PagedWalk& walk, bool report) {
+template <bool SH>
+__device__ __forceinline__ void paged_locate_warp(const PagedAttnArgs& a, int c, PagedWalkOf<SH>& walk, bool report) {
     const int lane = threadIdx.x & 31, B = a.s.B;
     int bad = 0;
-    PagedSeq q = {0, 0, 0};
+    typename PagedSeqOf<SH>::type q = {};
     auto work = [&](int b) -> long long {
         if (b >= B) return 0;
-        q = paged_seq(a.s, b, bad);
-        return paged_group_cost(q, a.p) * a.p.hg;
+        q = paged_seq_of<SH>(a.s, b, bad);
+        return paged_group_cost_of<SH>(q, a) * a.p.hg;
     };
     long long mine = work(lane), total = mine;
 #pragma unroll 1
@@ -332,6 +442,10 @@ __device__ __forceinline__ void paged_locate_warp(const PagedAttnArgs& a, int c,
             walk.q.tok0 = __shfl_sync(0xffffffffu, q.tok0, l);
             walk.q.n = __shfl_sync(0xffffffffu, q.n, l);
             walk.q.len = __shfl_sync(0xffffffffu, q.len, l);
+            if constexpr (SH) {
+                walk.q.row = __shfl_sync(0xffffffffu, q.row, l);
+                walk.q.skip = __shfl_sync(0xffffffffu, q.skip, l);
+            }
             break;
         }
         start += __shfl_sync(0xffffffffu, x, 31);
@@ -343,6 +457,16 @@ __device__ __forceinline__ void paged_locate_warp(const PagedAttnArgs& a, int c,
 // The records of both slots of CTA c are written by every call (state 0: no such part).
 __device__ __forceinline__ int4 paged_record(const PagedSeg& g) {
     return make_int4(g.t1 == g.nt ? 2 : 1, g.tok0 + g.tok, g.ntok, g.hg);
+}
+
+// SHARED: where the parts of a part's tokens are to be found (thread i of T, any number of them).
+__device__ __forceinline__ void paged_where(const PagedAttnArgs& a, const PagedSharedSeg& g, int i, int T) {
+    for (; i < g.ntok; i += T) {
+        const size_t at = (size_t)(g.tok0 + g.tok + i) * a.p.hg + g.hg;
+        if (g.nt == 0) a.rec_first[at] = g.skip ? -2 : -1;
+        else if (g.t0 == 0) a.rec_first[at] = blockIdx.x | i << 16 | (g.skip ? kHasPrefix : 0);
+        if (g.t1 == g.nt) a.rec_last[at] = blockIdx.x;
+    }
 }
 
 }  // namespace ne

@@ -108,11 +108,14 @@ __device__ __forceinline__ void transpose4(uint4 (&v)[4], int l) {
     }
 }
 
-template <int D>
+// SH: the SHARED form, results as parts alone; DR: the cache's head_dim (32 runs as 64: TMA fills the columns
+// behind a row's end with zeros).
+template <int D, int DR, bool SH>
 __global__ void __launch_bounds__(384, 1)
     paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const PagedAttnArgs a) {
     using C = TileCfg<D>;
+    using Seg = typename PagedSegOf<SH>::type;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sQ = smem;                                    // two subtiles
@@ -122,7 +125,7 @@ __global__ void __launch_bounds__(384, 1)
     __shared__ __align__(8) uint64_t bar_s_full[2], bar_p_ready[2], bar_o_full[2], bar_s_free[2];
     __shared__ __align__(8) uint64_t bar_seg_full[kSegs], bar_seg_empty[kSegs];
     __shared__ PagedLocate loc;
-    __shared__ PagedSeg s_seg[kSegs];                      // the CTA's parts in order (b < 0: the end)
+    __shared__ Seg s_seg[kSegs];                           // the CTA's parts in order (b < 0: the end)
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -166,7 +169,7 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t tm = tmem_slot;
     const WaitCtx w{a.err, &abort_flag, a.timeout_ns};
     const int sub = a.p.sub;                               // tokens of a subtile
-    PagedSeg g;
+    Seg g;
     int nseg = 0;
     // The CTA's next part, from the queue; false at its end (or when a wait ran out).  One warp
     // finds the parts for all: the arithmetic has long latencies and a copy of it in every role
@@ -181,7 +184,7 @@ __global__ void __launch_bounds__(384, 1)
         return g.b >= 0;
     };
     // Where the CTA's share begins, warp 3 finds alone among up to 32 sequences, all warps among more.
-    if (a.s.B > 32) paged_locate<C::THREADS>(a, blockIdx.x, loc, blockIdx.x == 0);
+    if (a.s.B > 32) paged_locate<C::THREADS, SH>(a, blockIdx.x, loc, blockIdx.x == 0);
     // A part's K tile t sits at ring index 2 i, its V tile at 2 i + 1, i counting the CTA's tiles.
     // Zeros for the rows of the V tile at ring index i (keys of tile t) that lie behind the length.
     auto zero_v = [&](int i, int t) {
@@ -203,7 +206,7 @@ __global__ void __launch_bounds__(384, 1)
         const int rows = 128 / npg;
         while (ok && next_part()) {
             if (g.t0 == g.t1) continue;                    // no keys: the softmax warps write the rows
-            const int* trow = a.s.table + (size_t)g.b * a.s.W;
+            const int* trow = paged_row(a, g);
             auto page = [&](int t) -> int {                // page of this lane's part of tile t
                 const int pos = t * C::BN + lane * rows;
                 return lane < npg && pos < g.kv ? __ldg(trow + (pos >> a.c.ps_shift)) : -1;
@@ -394,7 +397,7 @@ __global__ void __launch_bounds__(384, 1)
         // ------------------------------------------------------------ the CTA's parts
         if (lane < 2) a.part_info[blockIdx.x * 2 + lane] = make_int4(0, 0, 0, 0);
         __syncwarp();                                      // both in front of lane 0's arrivals, and so of any record
-        PagedWalk walk;
+        PagedWalkOf<SH> walk;
         if (a.s.B <= 32) paged_locate_warp(a, blockIdx.x, walk, blockIdx.x == 0);
         else walk.init(a, loc.w0, loc.w1, loc.snap, loc.b, loc.start);
         bool more = true;
@@ -428,7 +431,9 @@ __global__ void __launch_bounds__(384, 1)
             const int tok = g.tok + u * sub + r / a.G;
             const long long orow = (long long)(g.tok0 + tok) * a.Hq + g.hg * a.G + r % a.G;
             if (g.t0 == g.t1) {                            // nothing to attend to
-                if (live) {
+                if constexpr (SH) {
+                    if (u == 0) paged_where(a, g, r, 128);
+                } else if (live) {
                     uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + orow * D);
 #pragma unroll
                     for (int e = 0; e < D / 8; ++e) dst[e] = make_uint4(0u, 0u, 0u, 0u);
@@ -525,10 +530,13 @@ __global__ void __launch_bounds__(384, 1)
             if (!ok) break;
             if (!(ok = mbar_wait_warp(smem_u32(&bar_o_full[u]), (C::SEP ? tiles - 1 : parts) & 1, w, SITE_PAGED_O_FULL))) break;
             ++parts;
+            if constexpr (SH) {
+                if (u == 0) paged_where(a, g, r, 128);
+            }
             if (!warp_live) continue;
             tc_fence_after();
-            const bool whole = g.whole();
-            const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+            const bool whole = g.whole(), direct = whole && !SH;
+            const float inv = !direct ? 1.f : l == 0.f ? 0.f : 1.f / l;
             // A thread holds a row's columns; four neighbours exchange 16-byte units, so that a store
             // writes 64 bytes of each of eight rows instead of 16 of each of 32 (at D 128 the
             // scattered stores took 4 us a part).
@@ -537,11 +545,12 @@ __global__ void __launch_bounds__(384, 1)
             int row4[4];                                   // rows q0 .. q0 + 3 of the output (or the part)
 #pragma unroll
             for (int k = 0; k < 4; ++k) row4[k] = whole ? __shfl_sync(0xffffffffu, (int)orow, (lane & ~3) + k) : prow - ql + k;
+            float* const parts_o = SH && whole ? a.row_o : a.part_o;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
+            for (int c = 0; c < DR; c += 32) {
                 uint32_t o[32];
                 tmem_ld_cols<1>(oc + c, o);
-                if (whole) {
+                if (direct) {
                     uint4 v[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
@@ -555,7 +564,7 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         if (q0 + k < live_rows)
-                            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + (long long)row4[k] * D + c + 8 * ql) = v[k];
+                            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + (long long)row4[k] * DR + c + 8 * ql) = v[k];
                 } else {
 #pragma unroll
                     for (int h = 0; h < 32; h += 16) {
@@ -566,14 +575,15 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             if (q0 + k < live_rows)
-                                *reinterpret_cast<uint4*>(a.part_o + (size_t)row4[k] * D + c + h + 4 * ql) = v[k];
+                                *reinterpret_cast<uint4*>(parts_o + (size_t)row4[k] * DR + c + h + 4 * ql) = v[k];
                     }
                 }
             }
             __syncwarp();
             tc_fence_before();
             if (live) {
-                if (whole) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+                if (SH && whole) a.row_ml[orow] = make_float2(m, l);
+                else if (whole) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
                 else a.part_ml[prow] = make_float2(m, l);
             }
             if (!whole && u == 0 && r == 0) a.part_info[blockIdx.x * 2 + g.slot()] = paged_record(g);
@@ -591,11 +601,11 @@ __global__ void __launch_bounds__(384, 1)
     }
 }
 
-template <int D>
+template <int D, int DR, bool SH>
 cudaError_t launch_tiles_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a,
                            cudaStream_t st) {
     using C = TileCfg<D>;
-    auto kfn = paged_tiles_kernel<D>;
+    auto kfn = paged_tiles_kernel<D, DR, SH>;
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(kfn, C::SMEM, done);
     if (e != cudaSuccess) return e;
@@ -606,8 +616,16 @@ cudaError_t launch_tiles_t(const CUtensorMap& tq, const CUtensorMap& tk, const C
 
 cudaError_t launch_paged_tiles(int D, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                const PagedAttnArgs& a, cudaStream_t st) {
-    if (D == 64) return launch_tiles_t<64>(tq, tk, tv, a, st);
-    if (D == 128) return launch_tiles_t<128>(tq, tk, tv, a, st);
+    if (D == 64) return launch_tiles_t<64, 64, false>(tq, tk, tv, a, st);
+    if (D == 128) return launch_tiles_t<128, 128, false>(tq, tk, tv, a, st);
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_shared_tiles(int D, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                const PagedAttnArgs& a, cudaStream_t st) {
+    if (D == 32) return launch_tiles_t<64, 32, true>(tq, tk, tv, a, st);
+    if (D == 64) return launch_tiles_t<64, 64, true>(tq, tk, tv, a, st);
+    if (D == 128) return launch_tiles_t<128, 128, true>(tq, tk, tv, a, st);
     return cudaErrorInvalidValue;
 }
 

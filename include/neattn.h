@@ -391,6 +391,31 @@ ne_status ne_paged_attn_f32(const float* q, const ne_paged_cache* cache, const i
                             int N, int Hq, int max_pages, int max_new, void* workspace, size_t workspace_bytes,
                             ne_stream_t stream);
 
+/* Attention of sequences that share their first positions (children of one ne_pages_fork, questions
+ * about one document): the result of ne_paged_attn, with the shared keys and values read and multiplied once for
+ * all rows of a group.
+ *   groups [R + 1] int32: group r is sequences groups[r] .. groups[r+1]-1 of the batch (ascending; sequences
+ *          in front of groups[0] and from groups[R] on share nothing); 0 <= R <= B
+ *   shared [R] int32: the first shared[r] positions hold the same in every sequence of group r (whether
+ *          or not in the same pages), all in front of its new tokens: shared[r] <= seq_lens[b] - n_b
+ * Both device memory, 4-byte aligned.  They are read through the group's first sequence, in whole steps of 256
+ * positions; what is left of them, and the prefix of a group of one, every sequence reads for itself.
+ * Everything else is as in ne_paged_attn (its workspace of another size); results are the same up to
+ * rounding, and the same bits for the same call.  Groups outside [0, B] or descending, a negative shared[r], and
+ * whole steps of shared positions that reach into a sequence's new tokens are reported by
+ * ne_get_device_error() (outputs of that group invalid).  With max_new * Hq / Hkv of 256 and more, a sequence fills the kernels' tiles by itself and the call
+ * runs as ne_paged_attn does.  workspace: ne_paged_attn_shared_workspace_size() bytes (two workspaces of
+ * ne_paged_attn and 8 D + 32 bytes per row and query head). */
+size_t ne_paged_attn_shared_workspace_size(int B, int N, int Hq, int Hkv, int D);
+ne_status ne_paged_attn_shared(const void* q, const ne_paged_cache* cache, const int* page_table, const int* seq_lens,
+                               const int* cu_new, const int* groups, const int* shared, int R, void* o, float* lse,
+                               int64_t q_ld, int B, int N, int Hq, int max_pages, int max_new, void* workspace,
+                               size_t workspace_bytes, ne_stream_t stream);
+ne_status ne_paged_attn_shared_f32(const float* q, const ne_paged_cache* cache, const int* page_table, const int* seq_lens,
+                                   const int* cu_new, const int* groups, const int* shared, int R, float* o, float* lse,
+                                   int64_t q_ld, int B, int N, int Hq, int max_pages, int max_new, void* workspace,
+                                   size_t workspace_bytes, ne_stream_t stream);
+
 /* The attention weight that every cached position receives from the new tokens, added to what it had:
  * for sequence b, kv head g and slot j < seq_lens[b]
  *   weights_out[b][g][j] = weights[b][g][j] + sum over the rows i of b at positions t_i >= j and the query
