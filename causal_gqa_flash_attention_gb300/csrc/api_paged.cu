@@ -799,6 +799,7 @@ ne_status ne_pages_evict(const ne_paged_cache* cache, const float* weights, cons
                       {seq_lens, (size_t)B * 4, "seq_lens", -1}, {new_lens, (size_t)B * 4, "new_lens", -1}},
                      {{weights_out, rows * T * 4, "weights_out", 0}, {positions_out, rows * T * 4, "positions_out", 1},
                       {pos_offset_out, (size_t)B * 4, "pos_offset_out", 2}});
+    if (s == NE_OK) s = check_ptrs({weights, positions, weights_out, positions_out});
     if (s != NE_OK) return s;
     const EvictWs w = evict_ws(rows, T);
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)

@@ -8,21 +8,25 @@
 // already, positions[] remembers where a slot came from), so a step that gives up one position
 // moves one row, not half the cache, and sources and targets never overlap.
 //
-// Two kernels.  The first, a CTA per row, finds the threshold: the weights' bits, mapped so that
-// unsigned order is their order, in three digits of 11, 11 and 10 bits from the top; a histogram
-// per digit in shared memory, the digit that holds the m-th largest from a suffix sum.  Warps own
-// contiguous slots, so ranks among equal keys, holes and movers are one exchange of warp totals
-// and a running count.  The second kernel fills the GPU with the moves.
+// Two kernels.  The first, a CTA per row, reads the row once into registers and finds the threshold:
+// the weights' bits, mapped so that unsigned order is their order, in digits from the top (8 bits, 11 in
+// the wide CTAs); a histogram per digit in shared memory, the digit that holds the m-th largest from a
+// suffix sum.  Where only a few slots go, they are the minima of as many rounds instead.  Warps own
+// contiguous slots, so ranks among equal keys, holes and movers are ballots and one exchange of warp
+// totals.  Rows of more than 16384 slots keep their keys in shared memory, or form them again in every pass.
+// The second kernel fills the GPU with the moves.
 #include "paged.h"
 #include "ptx.cuh"
 
 namespace ne {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 512;          // of the kernel for long rows
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kMoveThreads = 256;
+constexpr int kRounds = 4;             // slots of a row that are found as minima, at most
+constexpr int kMoveThreads = 128;
+constexpr int kMoves = 4;              // moves of a thread at a time
 
 // Unsigned order of the key = order of the weight (-0 counts as 0, NaN below everything).
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -62,6 +66,297 @@ __device__ __forceinline__ int before_warp(int x, int* cnt) {
 __device__ __forceinline__ int all_warps(const int* cnt) {
     const int lane = threadIdx.x & 31;
     return __reduce_add_sync(0xffffffffu, lane < kWarps ? cnt[lane] : 0);
+}
+
+// Exclusive and whole sums of x over a CTA's warps; x the warp's own, the same in every lane.  Two places
+// take turns: a warp that still reads one is behind the other's barrier.
+template <int W>
+struct WarpSums {
+    int cnt[2][W];
+    __device__ __forceinline__ void exchange(int x, int turn, int& before, int& all) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        if (lane == 0) cnt[turn][warp] = x;
+        __syncthreads();
+        const int v = lane < W ? cnt[turn][lane] : 0;
+        before = __reduce_add_sync(0xffffffffu, lane < warp ? v : 0);
+        all = __reduce_add_sync(0xffffffffu, v);
+    }
+};
+
+// THREADS x KPT >= T: warp w holds slots 32 KPT w .., lane l of it slots 4 l .. 4 l + 3 of every 128.
+template <int THREADS, int KPT, int BITS>
+__global__ void __launch_bounds__(THREADS) evict_rows_kernel(const EvictArgs a) {
+    constexpr int W = THREADS / 32, Q = KPT / 4, BINS = 1 << BITS, BPT = BINS / THREADS;
+    static_assert(BPT >= 1 && KPT <= 32, "bins per thread, slots per mask");
+    __shared__ int s_hist[BINS];
+    __shared__ WarpSums<W> s_sums;
+    __shared__ int2 s_min[2][W];
+    __shared__ int s_digit, s_rest, s_left, s_n;
+    __shared__ __align__(4) uint16_t s_hole[THREADS * KPT / 2];   // targets in order; before that, keys
+    uint32_t* const s_key = reinterpret_cast<uint32_t*>(s_hole);
+    static_assert(KPT >= 4, "a key per thread fits");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int i = tid; i < BINS; i += THREADS) s_hist[i] = 0;
+    if (tid == 0) s_n = 0;
+    griddep_launch_dependents();
+    griddep_wait();
+    const int x = blockIdx.x, b = x / a.Hkv % a.B;
+    const size_t row = (size_t)x * a.T;
+    const int s0 = warp * 32 * KPT + lane * 4;             // the thread's slots: s0 + 128 i + k
+    // The row (T is a multiple of 8: whole units of four), on its way while the lengths are fetched.
+    float w[KPT];
+    int pos[KPT];
+#pragma unroll
+    for (int i = 0; i < Q; ++i)
+        if (s0 + 128 * i < a.T) {
+            const float4 f = *reinterpret_cast<const float4*>(a.w + row + s0 + 128 * i);
+            const int4 p = *reinterpret_cast<const int4*>(a.pos + row + s0 + 128 * i);
+            w[4 * i] = f.x, w[4 * i + 1] = f.y, w[4 * i + 2] = f.z, w[4 * i + 3] = f.w;
+            pos[4 * i] = p.x, pos[4 * i + 1] = p.y, pos[4 * i + 2] = p.z, pos[4 * i + 3] = p.w;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[4 * i + k] = 0.f, pos[4 * i + k] = 0;
+        }
+    bool bad;
+    const EvictSeq q = evict_seq(a, b, bad);
+    if (bad && tid == 0) report_error(a.err, SITE_PAGED_LEN);
+    const int n = q.n, m = q.m, newest = n + q.off - a.recent;
+    auto slot = [&](int j) { return s0 + 128 * (j >> 2) + (j & 3); };
+    uint32_t live = 0, guard = 0;                          // bit j: the thread's j-th slot
+#pragma unroll
+    for (int j = 0; j < KPT; ++j) {
+        if (pos[j] < 0) pos[j] = slot(j) + q.off;
+        const bool in = slot(j) < n;
+        live |= (uint32_t)in << j;
+        guard |= (uint32_t)(in && (pos[j] < a.sink || pos[j] >= newest)) << j;
+    }
+    int before, n_guard;
+    s_sums.exchange(__reduce_add_sync(0xffffffffu, __popc(guard)), 0, before, n_guard);
+    // Who competes: guarded slots among themselves where they do not all fit, else the others for
+    // what the guarded leave.
+    const bool crowd = n_guard > m;
+    const uint32_t field = crowd ? guard : live & ~guard;
+    int rest = crowd ? m : m - n_guard;
+    const int gone = (crowd ? n_guard : n - n_guard) - rest;   // slots of the field that go
+    uint32_t keep = field;
+    if (rest == 0) {
+        keep = 0;
+    } else if (gone <= kRounds) {
+#pragma unroll 1
+        for (int r = 0; r < gone; ++r) {                   // the lowest key's last slot
+            uint32_t low = 0xffffffffu;
+            int at = -1;
+#pragma unroll
+            for (int j = 0; j < KPT; ++j) {
+                const uint32_t k = weight_key(w[j]);
+                if ((keep >> j & 1u) && k <= low) low = k, at = slot(j);
+            }
+            const uint32_t wl = __reduce_min_sync(0xffffffffu, low);
+            const int wa = __reduce_max_sync(0xffffffffu, low == wl ? at : -1);
+            if (lane == 0) s_min[r & 1][warp] = make_int2((int)wl, wa);
+            __syncthreads();
+            const int2 v = lane < W ? s_min[r & 1][lane] : make_int2(-1, -1);
+            const uint32_t bl = __reduce_min_sync(0xffffffffu, (uint32_t)v.x);
+            const int ba = __reduce_max_sync(0xffffffffu, (uint32_t)v.x == bl ? v.y : -1);
+#pragma unroll
+            for (int j = 0; j < KPT; ++j)
+                if (slot(j) == ba) keep &= ~(1u << j);
+        }
+    } else if (gone > 0) {
+        // From the first bit in which the field's keys differ: digits from the top would put the
+        // few exponents that weights have into a few bins, whose atomics wait for each other.
+        uint32_t low = 0xffffffffu, high = 0;
+#pragma unroll
+        for (int j = 0; j < KPT; ++j)
+            if (field >> j & 1u) {
+                const uint32_t k = weight_key(w[j]);
+                low = min(low, k);
+                high = max(high, k);
+            }
+        low = __reduce_min_sync(0xffffffffu, low);
+        high = __reduce_max_sync(0xffffffffu, high);
+        if (lane == 0) s_min[0][warp] = make_int2((int)low, (int)high);
+        __syncthreads();
+        const int2 v = lane < W ? s_min[0][lane] : make_int2(-1, 0);
+        low = __reduce_min_sync(0xffffffffu, (uint32_t)v.x);
+        high = __reduce_max_sync(0xffffffffu, (uint32_t)v.y);
+        const int top = 32 - __clz((int)(low ^ high));     // bits below the common ones
+        uint32_t fixed = top == 32 ? 0u : ~((1u << top) - 1u), prefix = high & fixed, mine = 0;
+        int left = -1;                                     // keys that still compete, one per thread (-1: in their places)
+#pragma unroll 1
+        for (int shift = max(0, top - BITS); top > 0; shift = max(0, shift - BITS)) {
+            // (The last digit may overlap the one before: its bits above are those found already.)
+            const uint32_t digits = BINS - 1;
+            if (left >= 0) {
+                if (tid < left && (mine & fixed) == prefix) atomicAdd(&s_hist[(mine >> shift) & digits], 1);
+            } else {
+#pragma unroll
+                for (int j = 0; j < KPT; ++j) {
+                    const uint32_t k = weight_key(w[j]);
+                    if ((field >> j & 1u) && (k & fixed) == prefix) atomicAdd(&s_hist[(k >> shift) & digits], 1);
+                }
+            }
+            __syncthreads();
+            // A thread holds BPT bins, the first thread the highest; it finds the rest-th of the line in its own.
+            int c[BPT], sum = 0;
+#pragma unroll
+            for (int i = 0; i < BPT; ++i) {
+                int* bin = &s_hist[BINS - 1 - (BPT * tid + i)];
+                c[i] = *bin;
+                *bin = 0;
+                sum += c[i];
+            }
+            int incl = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            int at, all;
+            s_sums.exchange(__shfl_sync(0xffffffffu, incl, 31), 1, at, all);
+            at += incl - sum;
+            if (at < rest && rest <= at + sum) {
+#pragma unroll
+                for (int i = 0; i < BPT; ++i) {
+                    if (at < rest && rest <= at + c[i]) {
+                        s_digit = BINS - 1 - (BPT * tid + i);
+                        s_rest = rest - at;
+                        s_left = c[i];
+                    }
+                    at += c[i];
+                }
+            }
+            __syncthreads();
+            prefix |= (uint32_t)s_digit << shift;
+            fixed |= digits << shift;
+            rest = s_rest;
+            if (shift == 0) break;
+            if (left < 0 && s_left <= THREADS) {           // few are left: one per thread from here on
+                left = s_left;
+#pragma unroll
+                for (int j = 0; j < KPT; ++j) {
+                    const uint32_t k = weight_key(w[j]);
+                    if ((field >> j & 1u) && (k & fixed) == prefix) s_key[atomicAdd(&s_n, 1)] = k;
+                }
+                __syncthreads();
+                if (tid < left) mine = s_key[tid];
+            }
+        }
+        // Slots above the threshold stay, and the first `rest` of those on it.
+        uint32_t same = 0;
+        keep = 0;
+#pragma unroll
+        for (int j = 0; j < KPT; ++j) {
+            const uint32_t k = weight_key(w[j]);
+            same |= (uint32_t)(k == prefix) << j;
+            keep |= (uint32_t)(k > prefix) << j;
+        }
+        same &= field;
+        keep &= field;
+        int eq, all;
+        s_sums.exchange(__reduce_add_sync(0xffffffffu, __popc(same)), 0, eq, all);
+        if (all == rest) {
+            keep |= same;
+        } else {
+            const uint32_t lower = (1u << lane) - 1u;
+#pragma unroll
+            for (int i = 0; i < Q; ++i) {
+                uint32_t v[4];
+                int at = eq;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    v[k] = __ballot_sync(0xffffffffu, same >> (4 * i + k) & 1u);
+                    at += __popc(v[k] & lower);
+                    eq += __popc(v[k]);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (same >> (4 * i + k) & 1u) {
+                        if (at < rest) keep |= 1u << (4 * i + k);
+                        ++at;
+                    }
+            }
+        }
+    }
+    if (!crowd) keep |= guard;
+    uint32_t front = 0;                                    // slots below m
+#pragma unroll
+    for (int j = 0; j < KPT; ++j) front |= (uint32_t)(slot(j) < m) << j;
+    const uint32_t hole = front & ~keep, move = keep & ~front;
+    int hole_at, move_at, holes, moves;
+    s_sums.exchange(__reduce_add_sync(0xffffffffu, __popc(hole)), 1, hole_at, holes);
+    s_sums.exchange(__reduce_add_sync(0xffffffffu, __popc(move)), 0, move_at, moves);
+    int* dst = a.list + row;                               // targets, then sources: T / 2 of each at most
+    int* src = dst + (a.T >> 1);
+    const uint32_t lower = (1u << lane) - 1u;
+    int first[Q];                                          // rank of the thread's first mover of group i
+#pragma unroll
+    for (int i = 0; i < Q; ++i) {
+        first[i] = 0;
+        if (moves == 0) continue;
+        const int g0 = warp * 32 * KPT + 128 * i;
+        if (g0 < m) {
+            int at = hole_at;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t v = __ballot_sync(0xffffffffu, hole >> (4 * i + k) & 1u);
+                at += __popc(v & lower);
+                hole_at += __popc(v);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (hole >> (4 * i + k) & 1u) {
+                    s_hole[at] = (uint16_t)slot(4 * i + k);
+                    dst[at++] = slot(4 * i + k);
+                }
+        }
+        if (g0 + 128 > m && g0 < n) {
+            first[i] = move_at;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t v = __ballot_sync(0xffffffffu, move >> (4 * i + k) & 1u);
+                first[i] += __popc(v & lower);
+                move_at += __popc(v);
+            }
+        }
+    }
+    __syncthreads();                                       // the targets are there
+    float* w_out = a.w_out + row;
+    int* pos_out = a.pos_out + row;
+    const bool same_w = a.w == a.w_out;
+#pragma unroll
+    for (int i = 0; i < Q; ++i) {
+        int at = first[i];
+        const int s4 = slot(4 * i);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (move >> (4 * i + k) & 1u) {
+                const int d = s_hole[at];
+                src[at++] = s4 + k;
+                w_out[d] = w[4 * i + k];
+                pos_out[d] = pos[4 * i + k];
+            }
+        const uint32_t f = front >> 4 * i & 15u, l = live >> 4 * i & 15u, kp = keep >> 4 * i & f;
+        if (f == 0 && l == 15) {                           // four that go (or have moved), four that stay, or a mixture
+            *reinterpret_cast<float4*>(w_out + s4) = make_float4(0.f, 0.f, 0.f, 0.f);
+            *reinterpret_cast<int4*>(pos_out + s4) = make_int4(-1, -1, -1, -1);
+        } else if (kp == 15) {
+            if (!same_w) *reinterpret_cast<float4*>(w_out + s4) = make_float4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            *reinterpret_cast<int4*>(pos_out + s4) = make_int4(pos[4 * i], pos[4 * i + 1], pos[4 * i + 2], pos[4 * i + 3]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (kp >> k & 1u) {
+                    if (!same_w) w_out[s4 + k] = w[4 * i + k];
+                    pos_out[s4 + k] = pos[4 * i + k];
+                } else if (l & ~f & 1u << k) {
+                    w_out[s4 + k] = 0.f;
+                    pos_out[s4 + k] = -1;
+                }
+            }
+        }
+    }
+    if (tid == 0) a.moves[x] = moves;
 }
 
 // CACHED: the row's keys and guard bits fit into shared memory; otherwise they are formed again
@@ -233,9 +528,9 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
     if (tid == 0) a.moves[x] = moves;
 }
 
-// Block (x, y): rows of moves y R, (y + gridDim.y) R, ... of row x, a 16-byte unit of K and of V per
-// thread.
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a) {
+// Block (x, y): moves y kMoves R .. of row x, then gridDim.y blocks further on; a 16-byte unit of K and of V
+// per thread and move.
+__global__ void __launch_bounds__(kMoveThreads, 8) evict_move_kernel(const EvictArgs a) {
     const int x = blockIdx.x, tid = threadIdx.x;
     griddep_launch_dependents();
     griddep_wait();
@@ -253,18 +548,41 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
     const int* row = a.table + (size_t)b * a.W;
     const int mask = (1 << a.ps_shift) - 1;
     const long long base = l * a.layer_stride + h * a.head_stride + u;
-    for (int j = blockIdx.y * R + (tid >> a.row_shift); j < moves; j += gridDim.y * R) {
-        const int s = src[j], d = dst[j];
-        const int ps = __ldg(row + (s >> a.ps_shift)), pd = __ldg(row + (d >> a.ps_shift));
-        if ((unsigned)ps >= (unsigned)a.n_pages || (unsigned)pd >= (unsigned)a.n_pages) {
-            report_error(a.err, SITE_PAGED_PAGE);
-            continue;
+    // Four moves at a time: lists, table and rows are a chain of three loads.
+    for (int j0 = (blockIdx.y * kMoves) * R + (tid >> a.row_shift); j0 < moves; j0 += gridDim.y * kMoves * R) {
+        int s[kMoves], d[kMoves];
+        uint4 k[kMoves], v[kMoves];
+        long long from[kMoves], to[kMoves];
+#pragma unroll
+        for (int i = 0; i < kMoves; ++i) {
+            const bool in = j0 + i * R < moves;
+            s[i] = in ? src[j0 + i * R] : -1;
+            d[i] = in ? dst[j0 + i * R] : -1;
         }
-        const long long from = base + ps * a.page_stride + (s & mask) * a.tok_stride;
-        const long long to = base + pd * a.page_stride + (d & mask) * a.tok_stride;
-        const uint4 k = *reinterpret_cast<const uint4*>(a.k + from), v = *reinterpret_cast<const uint4*>(a.v + from);
-        *reinterpret_cast<uint4*>(a.k + to) = k;
-        *reinterpret_cast<uint4*>(a.v + to) = v;
+#pragma unroll
+        for (int i = 0; i < kMoves; ++i) {
+            from[i] = to[i] = -1;
+            if (s[i] < 0) continue;
+            const int ps = __ldg(row + (s[i] >> a.ps_shift)), pd = __ldg(row + (d[i] >> a.ps_shift));
+            if ((unsigned)ps >= (unsigned)a.n_pages || (unsigned)pd >= (unsigned)a.n_pages) {
+                report_error(a.err, SITE_PAGED_PAGE);
+                continue;
+            }
+            from[i] = base + ps * a.page_stride + (s[i] & mask) * a.tok_stride;
+            to[i] = base + pd * a.page_stride + (d[i] & mask) * a.tok_stride;
+        }
+#pragma unroll
+        for (int i = 0; i < kMoves; ++i)
+            if (from[i] >= 0) {
+                k[i] = *reinterpret_cast<const uint4*>(a.k + from[i]);
+                v[i] = *reinterpret_cast<const uint4*>(a.v + from[i]);
+            }
+#pragma unroll
+        for (int i = 0; i < kMoves; ++i)
+            if (from[i] >= 0) {
+                *reinterpret_cast<uint4*>(a.k + to[i]) = k[i];
+                *reinterpret_cast<uint4*>(a.v + to[i]) = v[i];
+            }
     }
 }
 
@@ -272,9 +590,20 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st) {
     const int rows = a.layers * a.B * a.Hkv;
+    // The narrowest CTA that holds a row in registers.
     const size_t bytes = (size_t)a.T * 4 + ((size_t)a.T + 31) / 32 * 4;
     cudaError_t e;
-    if (bytes <= 200 * 1024) {
+    if (a.T <= 1024) {
+        e = launch_k(evict_rows_kernel<128, 8, 8>, dim3(rows), dim3(128), 0, st, a);
+    } else if (a.T <= 2048) {
+        e = launch_k(evict_rows_kernel<256, 8, 8>, dim3(rows), dim3(256), 0, st, a);
+    } else if (a.T <= 4096) {
+        e = launch_k(evict_rows_kernel<512, 8, 11>, dim3(rows), dim3(512), 0, st, a);
+    } else if (a.T <= 8192) {
+        e = launch_k(evict_rows_kernel<1024, 8, 11>, dim3(rows), dim3(1024), 0, st, a);
+    } else if (a.T <= 16384) {
+        e = launch_k(evict_rows_kernel<1024, 16, 11>, dim3(rows), dim3(1024), 0, st, a);
+    } else if (bytes <= 200 * 1024) {
         static std::atomic<uint64_t> done{0};
         if ((e = allow_smem(evict_select_kernel<true>, 200 * 1024, done)) != cudaSuccess) return e;
         e = launch_k(evict_select_kernel<true>, dim3(rows), dim3(kThreads), bytes, st, a);
@@ -282,10 +611,11 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st) {
         e = launch_k(evict_select_kernel<false>, dim3(rows), dim3(kThreads), 0, st, a);
     }
     if (e != cudaSuccess) return e;
-    // About two waves of blocks (eight to an SM), at most as many as a row has moves for.
-    const int R = kMoveThreads >> a.row_shift;
-    const int most = (a.T / 2 + R - 1) / R, want = (2 * 8 * 152 + rows - 1) / rows;
-    const int y = most < 1 ? 1 : most < want ? most : want;
+    // Up to three waves of blocks (eight to an SM: rows differ in their moves), each of them with at
+    // least four passes' worth where a row moves all it can.
+    const int R = (kMoveThreads >> a.row_shift) * kMoves;
+    const int most = (a.T / 2 + 4 * R - 1) / (4 * R), want = 3 * 8 * 152 / rows;
+    const int y = most < 1 || want < 1 ? 1 : most < want ? most : want;
     return launch_k(evict_move_kernel, dim3(rows, y), dim3(kMoveThreads), 0, st, a);
 }
 

@@ -497,6 +497,7 @@ ne_status ne_pages_compact(const ne_paged_cache* cache, const int* refcount, con
  *                             fills in at first, and what a cut leaves behind m): slot + pos_offset[b]
  *   pos_offset, pos_offset_out [B] int32: positions given up so far; pos_offset_out = pos_offset + n - m.
  *                             0 <= pos_offset[b] < 2^30
+ * weights, positions and their outputs are 16-byte aligned, the other arrays 4.
  * Slots m .. n-1 get weight 0 and position -1; entries at and behind n stay as they were.  Each output
  * may be its input; any other overlap is refused.  The pages that hold a sequence's slots must belong to it alone
  * (ne_pages_fork with deep sees to that), and ne_pages_resize from seq_lens to new_lens then gives back the

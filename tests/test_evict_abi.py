@@ -35,7 +35,7 @@ def evict(lib, c=None, **kw):
 
 
 @pytest.mark.parametrize("kw,text", [
-    (dict(w=NULL), "weights"), (dict(pos=vp(2 * MB + 2)), "positions"), (dict(off=NULL), "pos_offset"), (dict(table=NULL), "page_table"),
+    (dict(w=NULL), "weights"), (dict(pos=vp(2 * MB + 2)), "positions"), (dict(w=vp(MB + 8)), "aligned"), (dict(pos_out=vp(8 * MB + 8)), "aligned"), (dict(off=NULL), "pos_offset"), (dict(table=NULL), "page_table"),
     (dict(lens=NULL), "seq_lens"), (dict(new=NULL), "new_lens"), (dict(w_out=NULL), "weights_out"), (dict(pos_out=NULL), "positions_out"),
     (dict(off_out=NULL), "pos_offset_out"), (dict(sink=-1), "sink"), (dict(recent=(1 << 30) + 1), "recent"), (dict(B=-1), "B"),
     (dict(W=0), "max_pages"), (dict(W=(1 << 26) + 1), "max_pages"), (dict(B=1 << 30), "layers"), (dict(ws=NULL), "workspace"),

@@ -126,6 +126,21 @@ def test_long_rows(n, m, same):
     check([n], [m], [n // 3], NL=1, H=1, D=32, ps=64, recent=1000, sink=4, kind="ties" if n % 2 else "exp", same=same, seed=11)
 
 
+@pytest.mark.parametrize("same", [False, True])
+@pytest.mark.parametrize("n", [1000, 1024, 1030, 2048, 2056, 4096, 4100, 8192, 8200, 16384, 16400])
+@pytest.mark.parametrize("gone", [1, 3, 4, 5, 400])
+def test_few_and_many_go(n, gone, same):
+    """On either side of every width of the kernels, and of the count from which on a threshold is searched."""
+    check([n], [n - gone], [n // 2], NL=1, H=2, D=32, ps=8, recent=7, sink=3, kind="ties" if gone % 2 else "exp", same=same, seed=n + gone)
+
+
+@pytest.mark.parametrize("gone", [2, 300])
+@pytest.mark.parametrize("n", [900, 3000, 9000])
+def test_a_crowd_of_guarded_slots(n, gone):
+    """More guarded slots than stay: they compete among themselves, and all others go."""
+    check([n], [n - 100 - gone], [n], NL=1, H=2, D=32, ps=8, recent=n - 100, sink=0, kind="ties", seed=n + gone)
+
+
 def test_fresh_outputs_and_one_layer_pools():
     table, w, pos, off, k, v = state([90, 40], [90, 40], 1, 2, 64, 16, BF16, 13)
     w[:, 0, :, 90:], w[:, 1, :, 40:] = 0, 0
