@@ -325,18 +325,6 @@ SharedWs shared_ws(int N, int Hq, int Hkv, int D) {
     return w;
 }
 
-ne_status shared_launch(ne::PagedKind kind, bool f32, const ne_paged_cache* c, const ne::PagedAttnArgs& a, cudaStream_t st) {
-    cudaError_t e;
-    if (kind == ne::PAGED_TILES) {
-        CUtensorMap tq, tk, tv;
-        const ne_status s = tile_maps(&tq, &tk, &tv, c, a.c, a.q, a.q_ld, a.Hq, a.s.N, a.G, a.p.sub);
-        if (s != NE_OK) return s;
-        e = ne::launch_shared_tiles(c->D, tq, tk, tv, a, st);
-    } else if (f32) e = ne::launch_shared_f32(kind, c->D, a, st);
-    else e = ne::launch_shared_short(kind, c->D, a, st);
-    return e == cudaSuccess ? NE_OK : cuda_fail(e, "paged_attn_shared launch");
-}
-
 ne_status shared_impl(int eb, const void* q, const ne_paged_cache* c, const int* table, const int* lens, const int* cu,
                       const int* groups, const int* shared, int R, void* o, float* lse, int64_t q_ld, int B, int N, int Hq, int W,
                       int max_new, void* ws, size_t ws_bytes, ne_stream_t stream) {
@@ -351,33 +339,43 @@ ne_status shared_impl(int eb, const void* q, const ne_paged_cache* c, const int*
     if ((s = attn_ws_check(ws, ws_bytes, w.total)) != NE_OK) return s;
     const int G = Hq / c->Hkv, most = cu ? std::min(max_new, N) : 1;
     const bool f32 = eb == 4;
-    if (R == 0 || (long long)most * G >= kSharedRows)
+    if (R == 0 || (long long)most * G >= kSharedRows || (!f32 && G > 128))
         return attn_impl(eb, q, c, table, lens, cu, o, lse, q_ld, B, N, Hq, W, max_new, ws, ws_bytes, stream);
-    const ne::PagedKind own_kind = ne::paged_kind(f32, c->D, G, most);
-    // All rows of a group together; head_dim 32 has a tile kernel here.
-    ne::PagedKind pre_kind = ne::paged_kind(f32, c->D, G, N);
-    if (!f32 && (long long)N * G > 32 && G <= 128) pre_kind = ne::PAGED_TILES;
-    ne::PagedAttnArgs a[2];                    // prefixes, own positions
-    char* base = static_cast<char*>(ws);
-    for (int i = 0; i < 2; ++i) {
-        if ((s = attn_args(&a[i], i ? own_kind : pre_kind, q, c, table, lens, cu, o, lse, q_ld, i ? B : R, N, Hq, W, base, stream)) != NE_OK)
+    // bf16: one line of prefixes and own positions, tiles for all.  fp32: a line and a kernel for each,
+    // chosen by the rows of a group and of a sequence.
+    const int lines = f32 ? 2 : 1;
+    ne::PagedAttnArgs a[2];                    // prefixes (and own positions), own positions
+    ne::PagedKind kind[2] = {f32 ? ne::paged_kind(true, c->D, G, N) : ne::PAGED_TILES, ne::paged_kind(true, c->D, G, most)};
+    char* rows = static_cast<char*>(ws) + 2 * w.parts;
+    for (int i = 0; i < lines; ++i) {
+        if ((s = attn_args(&a[i], kind[i], q, c, table, lens, cu, o, lse, q_ld, lines == 1 ? R + B : i ? B : R, N, Hq, W,
+                           static_cast<char*>(ws) + i * w.parts, stream)) != NE_OK)
             return s;
         a[i].s.groups = groups;
         a[i].s.shared = shared;
         a[i].s.R = R;
         a[i].s.seqs = B;
-        a[i].s.prefix = !i;
-        a[i].row_o = reinterpret_cast<float*>(base + w.parts);
-        a[i].row_ml = reinterpret_cast<float2*>(base + w.parts + w.row_o);
-        a[i].rec_first = reinterpret_cast<int*>(base + w.parts + w.row_o + w.row_ml);
-        a[i].rec_last = a[i].rec_first + (size_t)N * Hq;
-        base += w.total / 2;
+        a[i].s.pre = i ? 0 : R;
+        for (int k = 0; k < 2; ++k) {
+            char* base = rows + k * (w.row_o + w.row_ml + w.rec);
+            a[i].row_o[k] = reinterpret_cast<float*>(base);
+            a[i].row_ml[k] = reinterpret_cast<float2*>(base + w.row_o);
+            a[i].rec_first[k] = reinterpret_cast<int*>(base + w.row_o + w.row_ml);
+            a[i].rec_last[k] = a[i].rec_first[k] + (size_t)N * Hq;
+        }
     }
     cudaStream_t st = (cudaStream_t)stream;
-    if ((s = shared_launch(pre_kind, f32, c, a[0], st)) != NE_OK) return s;
-    if ((s = shared_launch(own_kind, f32, c, a[1], st)) != NE_OK) return s;
-    const cudaError_t e = ne::launch_shared_join(f32, c->D, a[0], a[1], st);
-    return e == cudaSuccess ? NE_OK : cuda_fail(e, "paged_attn_shared join launch");
+    cudaError_t e;
+    if (!f32) {
+        CUtensorMap tq, tk, tv;
+        if ((s = tile_maps(&tq, &tk, &tv, c, a[0].c, q, q_ld, Hq, N, G, a[0].p.sub)) != NE_OK) return s;
+        e = ne::launch_shared_tiles(c->D, tq, tk, tv, a[0], st);
+    } else {
+        e = ne::launch_shared_f32(kind[0], c->D, a[0], st);
+        if (e == cudaSuccess) e = ne::launch_shared_f32(kind[1], c->D, a[1], st);
+    }
+    if (e == cudaSuccess) e = ne::launch_shared_join(f32, c->D, a[0], a[lines - 1], st);
+    return e == cudaSuccess ? NE_OK : cuda_fail(e, "paged_attn_shared launch");
 }
 
 // ---------------------------------------------------------------- accumulated weights

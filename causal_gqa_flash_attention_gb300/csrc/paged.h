@@ -28,7 +28,8 @@ struct PagedBatch {
     const int* groups;                // [R + 1]
     const int* shared;                // [R]
     int R, seqs;                      // groups; sequences
-    int prefix;                       // 1: the line's members are the groups' prefixes (B is R), 0: the sequences' own positions
+    int pre;                          // the line's first `pre` members are the groups' prefixes (R or 0), the others the
+                                      // sequences' own positions
 };
 // Shared positions count in whole steps of this (a multiple of every page and key tile), so that a
 // sequence's own positions begin on a page; the rest is read by every sequence for itself.
@@ -87,10 +88,11 @@ struct PagedAttnArgs {
     int4* part_info;                  // [2C] (state: 0 none, 1, 2 the unit's last; first row, tokens, head group)
     // SHARED: uncut units' rows, and for every token and head group the CTAs that hold its unit's first
     // and last part (first: | token within the unit << 16 | kHasPrefix; -1, -2: no keys, without, with a prefix).
-    float* row_o;                     // [N, Hq, D] unnormalised
-    float2* row_ml;                   // [N, Hq]
-    int* rec_first;                   // [N, hg]
-    int* rec_last;
+    // Own positions' at [0], prefixes' at [1].
+    float* row_o[2];                  // [N, Hq, D] unnormalised
+    float2* row_ml[2];                // [N, Hq]
+    int* rec_first[2];                // [N, hg]
+    int* rec_last[2];
     int* err;
     unsigned long long timeout_ns;
 };
@@ -124,11 +126,10 @@ cudaError_t launch_paged_f32(PagedKind kind, int D, const PagedAttnArgs& a, cuda
 cudaError_t launch_paged_tiles(int D, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                const PagedAttnArgs& a, cudaStream_t st);
 // The same over prefixes or own positions, results as parts (a.s.groups set).
-cudaError_t launch_shared_short(PagedKind kind, int D, const PagedAttnArgs& a, cudaStream_t st);
 cudaError_t launch_shared_f32(PagedKind kind, int D, const PagedAttnArgs& a, cudaStream_t st);
 cudaError_t launch_shared_tiles(int D, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                 const PagedAttnArgs& a, cudaStream_t st);
-// Puts prefixes' and own positions' parts together.
+// Puts prefixes' and own positions' parts together (one line of both, or two).
 cudaError_t launch_shared_join(bool f32, int D, const PagedAttnArgs& pre, const PagedAttnArgs& own, cudaStream_t st);
 // Joins the parts of cut units.
 cudaError_t launch_paged_join(bool f32, int D, const PagedAttnArgs& a, cudaStream_t st);

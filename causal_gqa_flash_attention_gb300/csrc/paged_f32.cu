@@ -62,7 +62,13 @@ __global__ void __launch_bounds__(F32Cfg<D, RW, MANY>::THREADS, F32Cfg<D, RW, MA
     griddep_launch_dependents();
     griddep_wait();
     PagedWalkOf<SH> walk;
-    paged_locate<C::THREADS, SH>(a, blockIdx.x, loc, blockIdx.x == 0);
+    __shared__ PagedGroups groups;                         // (SH)
+    if constexpr (SH) {
+        paged_load_groups(a.s, groups);
+        __syncthreads();
+    }
+    walk.gs = &groups;
+    paged_locate<C::THREADS, SH>(a, blockIdx.x, loc, blockIdx.x == 0, &groups);
     walk.init(a, loc.w0, loc.w1, loc.snap, loc.b, loc.start);
     if (tid < 2) a.part_info[blockIdx.x * 2 + tid] = make_int4(0, 0, 0, 0);
 
@@ -294,10 +300,15 @@ __global__ void __launch_bounds__(F32Cfg<D, RW, MANY>::THREADS, F32Cfg<D, RW, MA
                 acc.z += x.z * wt;
                 acc.w += x.w * wt;
             }
-            if (SH && g.whole()) {
-                const long long orow = (long long)(g.tok0 + g.tok + row / gs) * a.Hq + h0 + row % gs;
-                *reinterpret_cast<float4*>(a.row_o + orow * D + e) = acc;
-                if (e == 0) a.row_ml[orow] = make_float2(mm, ll);
+            bool done = false;
+            if constexpr (SH)
+                if (g.whole()) {
+                    const long long orow = (long long)(g.tok0 + g.tok + row / gs) * a.Hq + h0 + row % gs;
+                    *reinterpret_cast<float4*>(a.row_o[g.pre] + orow * D + e) = acc;
+                    if (e == 0) a.row_ml[g.pre][orow] = make_float2(mm, ll);
+                    done = true;
+                }
+            if (done) {
             } else if (g.whole()) {
                 const float inv = ll == 0.f ? 0.f : 1.f / ll;
                 const long long orow = (long long)(g.tok0 + g.tok + row / gs) * a.Hq + h0 + row % gs;

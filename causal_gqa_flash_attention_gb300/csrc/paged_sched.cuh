@@ -25,9 +25,16 @@ namespace ne {
 struct PagedSeq {
     int tok0, n, len;
 };
-// A member of a SHARED line: its table row, and the positions in front of its first key.
+// A member of a SHARED line: its table row, the positions in front of its first key, and whether it is a
+// group's prefix (whose rows all see all keys).
 struct PagedSharedSeq : PagedSeq {
     int row, skip;
+    bool pre;
+};
+// The groups of a SHARED call, up to so many of them in shared memory.
+struct PagedGroups {
+    static constexpr int MAX = 64;
+    int first[MAX + 1], len[MAX];      // first sequence; shared positions in use
 };
 template <bool SH>
 struct PagedSeqOf {
@@ -76,10 +83,23 @@ __device__ __forceinline__ int paged_shared(const PagedBatch& s, int r, int& g0,
     }
     return g1 - g0 < 2 ? 0 : min(n, min(max(__ldg(s.lens + g0), 0), s.cap)) & ~(kSharedStep - 1);
 }
-// Member b of a SHARED line.  A prefix: the rows of all its sequences, every one of which sees every key.
-__device__ __forceinline__ PagedSharedSeq paged_shared_seq(const PagedBatch& s, int b, int& bad) {
+// Fills gs (all threads of the CTA; a barrier has to follow).
+__device__ __forceinline__ void paged_load_groups(const PagedBatch& s, PagedGroups& gs) {
+    if (s.R > PagedGroups::MAX) return;
+    int bad = 0;
+    for (int r = threadIdx.x; r < s.R; r += blockDim.x) {
+        int g0, g1;
+        gs.len[r] = paged_shared(s, r, g0, g1, bad);
+        gs.first[r] = __ldg(s.groups + r);
+        if (r == s.R - 1) gs.first[s.R] = __ldg(s.groups + s.R);
+    }
+}
+// Member b of a SHARED line.
+__device__ __forceinline__ PagedSharedSeq paged_shared_seq(const PagedBatch& s, int b, int& bad, const PagedGroups& gs) {
     PagedSharedSeq q;
-    if (s.prefix) {
+    const bool near = s.R <= PagedGroups::MAX;
+    q.pre = b < s.pre;
+    if (q.pre) {
         int g0, g1;
         q.len = paged_shared(s, b, g0, g1, bad);
         PagedRaw w;
@@ -93,19 +113,23 @@ __device__ __forceinline__ PagedSharedSeq paged_shared_seq(const PagedBatch& s, 
         q.skip = 0;
         return q;
     }
+    b -= s.pre;
+    const PagedRaw raw = paged_raw(s, b);
     int lo = -1, hi = s.R - 1;                             // the last group that begins at or before b
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (__ldg(s.groups + mid) <= b) lo = mid;
+        if ((near ? gs.first[mid] : __ldg(s.groups + mid)) <= b) lo = mid;
         else hi = mid - 1;
     }
     q.skip = 0;
-    if (lo >= 0) {
+    if (lo >= 0 && near) {
+        if (b < gs.first[lo + 1]) q.skip = gs.len[lo];
+    } else if (lo >= 0) {
         int g0, g1;
         const int n = paged_shared(s, lo, g0, g1, bad);
         if (b < g1) q.skip = n;
     }
-    const PagedSeq t = paged_seq(s, b, bad);
+    const PagedSeq t = paged_clamp(s, raw, bad);
     if (q.skip > 0 && q.skip > t.len - t.n) bad = SITE_PAGED_GROUP;   // (new tokens among the shared positions)
     q.tok0 = t.tok0;
     q.n = t.n;
@@ -114,8 +138,8 @@ __device__ __forceinline__ PagedSharedSeq paged_shared_seq(const PagedBatch& s, 
     return q;
 }
 template <bool SH>
-__device__ __forceinline__ typename PagedSeqOf<SH>::type paged_seq_of(const PagedBatch& s, int b, int& bad) {
-    if constexpr (SH) return paged_shared_seq(s, b, bad);
+__device__ __forceinline__ typename PagedSeqOf<SH>::type paged_seq_of(const PagedBatch& s, int b, int& bad, const PagedGroups* gs) {
+    if constexpr (SH) return paged_shared_seq(s, b, bad, *gs);
     else return paged_seq(s, b, bad);
 }
 
@@ -130,10 +154,11 @@ __device__ __forceinline__ long long paged_prefix(int r, int base, const PagedSp
 }
 
 // The same of a member of a line: every tile of a prefix has all its keys.
-template <bool SH>
-__device__ __forceinline__ long long paged_prefix_of(int r, const PagedSeq& q, const PagedAttnArgs& a) {
-    if (SH && a.s.prefix) return (long long)r * (a.p.ovh + (long long)a.p.w_full * q.len);
-    return paged_prefix(r, q.len - q.n, a.p);
+__device__ __forceinline__ long long paged_prefix_of(int r, const PagedSeq& q, const PagedSplit& p) {
+    return paged_prefix(r, q.len - q.n, p);
+}
+__device__ __forceinline__ long long paged_prefix_of(int r, const PagedSharedSeq& q, const PagedSplit& p) {
+    return q.pre ? (long long)r * (p.ovh + (long long)p.w_full * q.len) : paged_prefix(r, q.len - q.n, p);
 }
 
 // Tiles of a sequence.
@@ -151,12 +176,11 @@ __device__ __forceinline__ long long paged_group_cost(const PagedSeq& q, const P
     return paged_prefix(last, q.len - q.n, p) + p.ovh + (long long)paged_weight(q.n - last * p.tpt, p) * q.len;
 }
 
-template <bool SH>
-__device__ __forceinline__ long long paged_group_cost_of(const PagedSeq& q, const PagedAttnArgs& a) {
-    if (!SH || !a.s.prefix) return paged_group_cost(q, a.p);
+__device__ __forceinline__ long long paged_group_cost(const PagedSharedSeq& q, const PagedSplit& p) {
+    if (!q.pre) return paged_group_cost(static_cast<const PagedSeq&>(q), p);
     if (q.n == 0) return 0;
-    const int last = paged_tiles(q.n, a.p) - 1;
-    return paged_prefix_of<SH>(last, q, a) + a.p.ovh + (long long)paged_weight(q.n - last * a.p.tpt, a.p) * q.len;
+    const int last = paged_tiles(q.n, p) - 1;
+    return paged_prefix_of(last, q, p) + p.ovh + (long long)paged_weight(q.n - last * p.tpt, p) * q.len;
 }
 
 // What a CTA does with one unit: key tiles [t0, t1) of nt_keys, for tokens tok .. tok+ntok-1
@@ -174,6 +198,7 @@ struct PagedSeg {
 
 struct PagedSharedSeg : PagedSeg {
     int row, skip;      // its sequence's table row, and positions in front of key 0
+    bool pre;           // of a prefix
 };
 template <bool SH>
 struct PagedSegOf {
@@ -196,6 +221,7 @@ struct PagedWalkOf {
     long long cur;      // start of the current unit
     int snap;           // a cut this near to a unit's end, in tiles, moves there
     typename PagedSeqOf<SH>::type q;
+    const PagedGroups* gs;   // (SHARED)
     PagedRaw ahead;     // the next sequence's, fetched while this one is walked
     int b, hg, r, nt;
 
@@ -205,7 +231,7 @@ struct PagedWalkOf {
     // Sequence b, whose values were fetched ahead.
     __device__ __forceinline__ void take(const PagedAttnArgs& a) {
         int bad = 0;
-        if constexpr (SH) q = paged_shared_seq(a.s, b, bad);
+        if constexpr (SH) q = paged_shared_seq(a.s, b, bad, *gs);
         else q = paged_clamp(a.s, ahead, bad);
         nt = paged_tiles(q.n, a.p);
         fetch(a);
@@ -232,7 +258,7 @@ struct PagedWalkOf {
         } else {
             load(a);
         }
-        const long long S = paged_group_cost_of<SH>(q, a);
+        const long long S = paged_group_cost(q, a.p);
         const long long off = w0 - start;
         // off / S by an estimate (off < S times the head groups, so it is off by one at most).
         hg = min(a.p.hg - 1, (int)__fdividef((float)off, (float)S));
@@ -247,16 +273,17 @@ struct PagedWalkOf {
         int lo = 0, hi = nt - 1;                           // the last tile whose start is at or before x
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (paged_prefix_of<SH>(mid, q, a) <= x) lo = mid;
+            if (paged_prefix_of(mid, q, a.p) <= x) lo = mid;
             else hi = mid - 1;
         }
         r = lo;
-        cur = start + (long long)hg * S + paged_prefix_of<SH>(r, q, a);
+        cur = start + (long long)hg * S + paged_prefix_of(r, q, a.p);
     }
     // The next part of the interval, false at its end.
     __device__ __forceinline__ bool next(const PagedAttnArgs& a, Seg& g) {
         while (cur < w1) {
-            const bool all = SH && a.s.prefix;             // every row sees every key
+            bool all = false;                              // every row sees every key
+            if constexpr (SH) all = q.pre;
             const int base = all ? q.len : q.len - q.n;
             const int kv = r == nt - 1 || all ? q.len : max(0, base + (r + 1) * a.p.tpt);
             const int ntok = min(a.p.tpt, q.n - r * a.p.tpt);
@@ -285,6 +312,7 @@ struct PagedWalkOf {
             if constexpr (SH) {
                 g.row = q.row;
                 g.skip = q.skip;
+                g.pre = q.pre;
             }
             const bool mine = g.t0 < g.t1 || (ntk == 0 && w0 <= cur);   // a unit without keys: its rows are still written
             cur += cost;
@@ -332,14 +360,14 @@ struct PagedLocate {
 // start falls into.  Two passes over the lengths when they exceed T sequences (the first
 // sums, the second finds), one otherwise.
 template <int T, bool SH = false>
-__device__ __forceinline__ void paged_locate(const PagedAttnArgs& a, int c, PagedLocate& sm, bool report) {
+__device__ __forceinline__ void paged_locate(const PagedAttnArgs& a, int c, PagedLocate& sm, bool report, const PagedGroups* gs = nullptr) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int B = a.s.B;
     int bad = 0;
     auto work = [&](int b) -> long long {
         if (b >= B) return 0;
-        const PagedSeq q = paged_seq_of<SH>(a.s, b, bad);
-        return paged_group_cost_of<SH>(q, a) * a.p.hg;
+        const auto q = paged_seq_of<SH>(a.s, b, bad, gs);
+        return paged_group_cost(q, a.p) * a.p.hg;
     };
     // Inclusive sums over the CTA; the total in sm.warp_sum[T / 32 - 1].
     auto scan = [&](long long x) -> long long {
@@ -410,8 +438,8 @@ __device__ __forceinline__ void paged_locate_warp(const PagedAttnArgs& a, int c,
     typename PagedSeqOf<SH>::type q = {};
     auto work = [&](int b) -> long long {
         if (b >= B) return 0;
-        q = paged_seq_of<SH>(a.s, b, bad);
-        return paged_group_cost_of<SH>(q, a) * a.p.hg;
+        q = paged_seq_of<SH>(a.s, b, bad, walk.gs);
+        return paged_group_cost(q, a.p) * a.p.hg;
     };
     long long mine = work(lane), total = mine;
 #pragma unroll 1
@@ -445,6 +473,7 @@ __device__ __forceinline__ void paged_locate_warp(const PagedAttnArgs& a, int c,
             if constexpr (SH) {
                 walk.q.row = __shfl_sync(0xffffffffu, q.row, l);
                 walk.q.skip = __shfl_sync(0xffffffffu, q.skip, l);
+                walk.q.pre = __shfl_sync(0xffffffffu, (int)q.pre, l);
             }
             break;
         }
@@ -463,9 +492,9 @@ __device__ __forceinline__ int4 paged_record(const PagedSeg& g) {
 __device__ __forceinline__ void paged_where(const PagedAttnArgs& a, const PagedSharedSeg& g, int i, int T) {
     for (; i < g.ntok; i += T) {
         const size_t at = (size_t)(g.tok0 + g.tok + i) * a.p.hg + g.hg;
-        if (g.nt == 0) a.rec_first[at] = g.skip ? -2 : -1;
-        else if (g.t0 == 0) a.rec_first[at] = blockIdx.x | i << 16 | (g.skip ? kHasPrefix : 0);
-        if (g.t1 == g.nt) a.rec_last[at] = blockIdx.x;
+        if (g.nt == 0) a.rec_first[g.pre][at] = g.skip ? -2 : -1;
+        else if (g.t0 == 0) a.rec_first[g.pre][at] = blockIdx.x | i << 16 | (g.skip ? kHasPrefix : 0);
+        if (g.t1 == g.nt) a.rec_last[g.pre][at] = blockIdx.x;
     }
 }
 

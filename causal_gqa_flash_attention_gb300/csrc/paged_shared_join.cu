@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kThreads) paged_shared_join_kernel(const Paged
             return (size_t)tok * a.p.hg + hkv * ngrp + g / a.p.gs;
         };
         const size_t io = at(own), ip = at(pre);
-        const int of = own.rec_first[io], ol = own.rec_last[io], pf = pre.rec_first[ip], pl = pre.rec_last[ip];
+        const int of = own.rec_first[0][io], ol = own.rec_last[0][io], pf = pre.rec_first[1][ip], pl = pre.rec_last[1][ip];
         const RowParts po = row_parts(own, of, ol, g);
         RowParts pp = row_parts(pre, pf, pl, g);
         if (of == -1 || (of >= 0 && !(of & kHasPrefix))) pp.n = 0;
@@ -83,8 +83,8 @@ __global__ void __launch_bounds__(kThreads) paged_shared_join_kernel(const Paged
             const int j = mine ? k : k - po.n, c = p.first + j;
             const size_t r = p.whole ? (size_t)row : (size_t)(2 * c + (j == 0 ? 1 : 0)) * a.p.rows + p.row;
             const int st = p.whole || j == 0 ? 1 : a.part_info[2 * c].x;
-            ml = (p.whole ? a.row_ml : a.part_ml)[r];
-            x = *reinterpret_cast<const float4*>((p.whole ? a.row_o : a.part_o) + r * D + e);
+            ml = (p.whole ? a.row_ml[!mine] : a.part_ml)[r];
+            x = *reinterpret_cast<const float4*>((p.whole ? a.row_o[!mine] : a.part_o) + r * D + e);
             return st != 0;
         };
         const int n = po.n + pp.n;

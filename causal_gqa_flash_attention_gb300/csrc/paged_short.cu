@@ -71,16 +71,15 @@ __device__ __forceinline__ float2 unpack2(uint32_t v) {
     return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
 
-// MT: 16-row tiles of a unit.  SH: the SHARED form, results as parts alone.
-template <int D, int MT, bool SH>
+// MT: 16-row tiles of a unit.
+template <int D, int MT>
 __global__ void __launch_bounds__(kThreads, 2) paged_short_kernel(const PagedAttnArgs a) {
     using C = ShortCfg<D>;
-    using Seg = typename PagedSegOf<SH>::type;
     constexpr int KT = C::KT, U = C::U, NT = KT / 8, NO = D / 8;
     constexpr bool PRE = 16 * MT * D * 4 <= 2 * C::TILE;   // a warp's output fits into one stage
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ PagedLocate loc;
-    __shared__ Seg s_part[2];                              // the CTA's parts in turn (b < 0: the end)
+    __shared__ PagedSeg s_part[2];                         // the CTA's parts in turn (b < 0: the end)
     __shared__ float s_m[kWarps][16 * MT], s_l[kWarps][16 * MT];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -109,9 +108,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_short_kernel(const PagedAtt
     };
     uint32_t qf[MT][D / 16][4];                            // the part's query rows as A fragments
     int lim[MT][2];                                        // keys that rows g8 and g8 + 8 see
-    auto begin = [&](const Seg& p) {
+    auto begin = [&](const PagedSeg& p) {
         const long long head = (long long)(p.hg / ngrp) * a.c.head_stride * 2;
-        trow = paged_row(a, p);
+        trow = a.s.table + (size_t)p.b * a.s.W;
         kp = static_cast<const char*>(a.c.k) + head;
         vp = static_cast<const char*>(a.c.v) + head;
         kv = p.kv;
@@ -142,11 +141,11 @@ __global__ void __launch_bounds__(kThreads, 2) paged_short_kernel(const PagedAtt
     };
     // Warp 0 finds the CTA's parts, one ahead; where its share begins, it finds alone among up to
     // 32 sequences, and the whole CTA among more (256 sequences: 3 us less a call).
-    PagedWalkOf<SH> walk;
+    PagedWalk walk;
     int turn = 0;
-    if (a.s.B > 32) paged_locate<kThreads, SH>(a, blockIdx.x, loc, blockIdx.x == 0);
+    if (a.s.B > 32) paged_locate<kThreads>(a, blockIdx.x, loc, blockIdx.x == 0);
     if (warp == 0) {
-        Seg n;
+        PagedSeg n;
         if (a.s.B <= 32) paged_locate_warp(a, blockIdx.x, walk, blockIdx.x == 0);
         else walk.init(a, loc.w0, loc.w1, loc.snap, loc.b, loc.start);
         if (lane < 2) a.part_info[blockIdx.x * 2 + lane] = make_int4(0, 0, 0, 0);
@@ -154,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_short_kernel(const PagedAtt
         if (lane == 0) s_part[0] = n;
     }
     __syncthreads();
-    Seg g = s_part[0];
+    PagedSeg g = s_part[0];
     if (PRE && g.b >= 0) begin(g);
     while (g.b >= 0) {
         const int h0 = (g.hg / ngrp) * a.G + (g.hg % ngrp) * a.p.gs;   // first query head of the unit
@@ -177,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_short_kernel(const PagedAtt
 
         ++turn;
         if (warp == 0) {
-            Seg n;
+            PagedSeg n;
             if (!walk.next(a, n)) n.b = -1;
             if (lane == 0) s_part[turn & 1] = n;
         }
@@ -285,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_short_kernel(const PagedAtt
         // The next part's first steps go out before this one is joined: they take the two stages
         // that the last step did not use.  The join takes that one (PRE), or all rings.
         const int last = (s0 + nsteps + kStages - 1) % kStages;
-        const Seg next = s_part[turn & 1];
+        const PagedSeg next = s_part[turn & 1];
         if (PRE) {
             __syncwarp();
             if (next.b >= 0) {
@@ -339,11 +338,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_short_kernel(const PagedAtt
                 acc.z += x.z * wt;
                 acc.w += x.w * wt;
             }
-            if (SH && g.whole()) {
-                const long long orow = (long long)(g.tok0 + g.tok + row / gs) * a.Hq + h0 + row % gs;
-                *reinterpret_cast<float4*>(a.row_o + orow * D + e) = acc;
-                if (e == 0) a.row_ml[orow] = make_float2(m, l);
-            } else if (g.whole()) {
+            if (g.whole()) {
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 const long long orow = (long long)(g.tok0 + g.tok + row / gs) * a.Hq + h0 + row % gs;
                 uint2 pk = make_uint2(pack2(acc.x * inv, acc.y * inv), pack2(acc.z * inv, acc.w * inv));
@@ -356,15 +351,14 @@ __global__ void __launch_bounds__(kThreads, 2) paged_short_kernel(const PagedAtt
             }
         }
         if (!g.whole() && tid == 0) a.part_info[pslot] = paged_record(g);
-        if constexpr (SH) paged_where(a, g, tid, kThreads);
         g = next;
     }
 }
 
-template <int D, int MT, bool SH>
+template <int D, int MT>
 cudaError_t launch_short_t(const PagedAttnArgs& a, cudaStream_t st) {
     using C = ShortCfg<D>;
-    auto kfn = paged_short_kernel<D, MT, SH>;
+    auto kfn = paged_short_kernel<D, MT>;
     constexpr int smem = kWarps * C::RING;
     static_assert(smem >= kWarps * 16 * MT * D * 4, "the join fits into the rings");
     static_assert(2 * (smem + 4096) <= 227 * 1024, "two CTAs per SM");
@@ -378,21 +372,14 @@ cudaError_t launch_short_t(const PagedAttnArgs& a, cudaStream_t st) {
 
 int paged_short_bn(int D) { return D == 128 ? ShortCfg<128>::BN : ShortCfg<64>::BN; }
 
-template <bool SH>
-static cudaError_t launch_short(PagedKind kind, int D, const PagedAttnArgs& a, cudaStream_t st) {
+cudaError_t launch_paged_short(PagedKind kind, int D, const PagedAttnArgs& a, cudaStream_t st) {
     const bool two = kind == PAGED_SHORT32;
     switch (D) {
-        case 32: return two ? launch_short_t<32, 2, SH>(a, st) : launch_short_t<32, 1, SH>(a, st);
-        case 64: return two ? launch_short_t<64, 2, SH>(a, st) : launch_short_t<64, 1, SH>(a, st);
-        case 128: return two ? launch_short_t<128, 2, SH>(a, st) : launch_short_t<128, 1, SH>(a, st);
+        case 32: return two ? launch_short_t<32, 2>(a, st) : launch_short_t<32, 1>(a, st);
+        case 64: return two ? launch_short_t<64, 2>(a, st) : launch_short_t<64, 1>(a, st);
+        case 128: return two ? launch_short_t<128, 2>(a, st) : launch_short_t<128, 1>(a, st);
     }
     return cudaErrorInvalidValue;
-}
-cudaError_t launch_paged_short(PagedKind kind, int D, const PagedAttnArgs& a, cudaStream_t st) {
-    return launch_short<false>(kind, D, a, st);
-}
-cudaError_t launch_shared_short(PagedKind kind, int D, const PagedAttnArgs& a, cudaStream_t st) {
-    return launch_short<true>(kind, D, a, st);
 }
 
 }  // namespace ne

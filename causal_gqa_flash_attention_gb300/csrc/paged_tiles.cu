@@ -126,6 +126,7 @@ __global__ void __launch_bounds__(384, 1)
     __shared__ __align__(8) uint64_t bar_seg_full[kSegs], bar_seg_empty[kSegs];
     __shared__ PagedLocate loc;
     __shared__ Seg s_seg[kSegs];                           // the CTA's parts in order (b < 0: the end)
+    __shared__ PagedGroups groups;                         // (SH)
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -184,7 +185,11 @@ __global__ void __launch_bounds__(384, 1)
         return g.b >= 0;
     };
     // Where the CTA's share begins, warp 3 finds alone among up to 32 sequences, all warps among more.
-    if (a.s.B > 32) paged_locate<C::THREADS, SH>(a, blockIdx.x, loc, blockIdx.x == 0);
+    if constexpr (SH) {
+        paged_load_groups(a.s, groups);
+        __syncthreads();
+    }
+    if (a.s.B > 32) paged_locate<C::THREADS, SH>(a, blockIdx.x, loc, blockIdx.x == 0, &groups);
     // A part's K tile t sits at ring index 2 i, its V tile at 2 i + 1, i counting the CTA's tiles.
     // Zeros for the rows of the V tile at ring index i (keys of tile t) that lie behind the length.
     auto zero_v = [&](int i, int t) {
@@ -398,6 +403,7 @@ __global__ void __launch_bounds__(384, 1)
         if (lane < 2) a.part_info[blockIdx.x * 2 + lane] = make_int4(0, 0, 0, 0);
         __syncwarp();                                      // both in front of lane 0's arrivals, and so of any record
         PagedWalkOf<SH> walk;
+        walk.gs = &groups;
         if (a.s.B <= 32) paged_locate_warp(a, blockIdx.x, walk, blockIdx.x == 0);
         else walk.init(a, loc.w0, loc.w1, loc.snap, loc.b, loc.start);
         bool more = true;
@@ -545,7 +551,13 @@ __global__ void __launch_bounds__(384, 1)
             int row4[4];                                   // rows q0 .. q0 + 3 of the output (or the part)
 #pragma unroll
             for (int k = 0; k < 4; ++k) row4[k] = whole ? __shfl_sync(0xffffffffu, (int)orow, (lane & ~3) + k) : prow - ql + k;
-            float* const parts_o = SH && whole ? a.row_o : a.part_o;
+            float *parts_o = a.part_o;
+            float2* parts_ml = a.part_ml + prow;
+            if constexpr (SH)
+                if (whole) {
+                    parts_o = a.row_o[g.pre];
+                    parts_ml = a.row_ml[g.pre] + orow;
+                }
 #pragma unroll 1
             for (int c = 0; c < DR; c += 32) {
                 uint32_t o[32];
@@ -582,9 +594,8 @@ __global__ void __launch_bounds__(384, 1)
             __syncwarp();
             tc_fence_before();
             if (live) {
-                if (SH && whole) a.row_ml[orow] = make_float2(m, l);
-                else if (whole) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-                else a.part_ml[prow] = make_float2(m, l);
+                if (direct) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+                else *parts_ml = make_float2(m, l);
             }
             if (!whole && u == 0 && r == 0) a.part_info[blockIdx.x * 2 + g.slot()] = paged_record(g);
         }
