@@ -33,7 +33,7 @@ struct PagedSharedSeq : PagedSeq {
 };
 // The groups of a SHARED call, up to so many of them in shared memory.
 struct PagedGroups {
-    static constexpr int MAX = 64;
+    static constexpr int MAX = 16;
     int first[MAX + 1], len[MAX];      // first sequence; shared positions in use
 };
 template <bool SH>
