@@ -316,7 +316,7 @@ SharedWs shared_ws(int N, int Hq, int Hkv, int D) {
     const int G = Hq / Hkv;
     SharedWs w;
     w.parts = attn_ws_bytes(D, Hkv, G);
-    if (G <= 128) w.parts = std::max(w.parts, round_up(ne::paged_part_bytes(ne::paged_split(ne::PAGED_SHARED, D, Hkv, G, 1 << 30), D), 256));
+    if (G <= 128) w.parts = std::max(w.parts, round_up(ne::paged_part_bytes(ne::paged_split(ne::PAGED_TILES, D, Hkv, G, 1 << 30), D), 256));
     const size_t rows = (size_t)N * Hq;
     w.row_o = round_up(rows * D * 4, 256);
     w.row_ml = round_up(rows * 8, 256);
@@ -345,7 +345,7 @@ ne_status shared_impl(int eb, const void* q, const ne_paged_cache* c, const int*
     // chosen by the rows of a group and of a sequence.
     const int lines = f32 ? 2 : 1;
     ne::PagedAttnArgs a[2];                    // prefixes (and own positions), own positions
-    ne::PagedKind kind[2] = {f32 ? ne::paged_kind(true, c->D, G, N) : ne::PAGED_SHARED, ne::paged_kind(true, c->D, G, most)};
+    ne::PagedKind kind[2] = {f32 ? ne::paged_kind(true, c->D, G, N) : ne::PAGED_TILES, ne::paged_kind(true, c->D, G, most)};
     char* rows = static_cast<char*>(ws) + 2 * w.parts;
     for (int i = 0; i < lines; ++i) {
         if ((s = attn_args(&a[i], kind[i], q, c, table, lens, cu, o, lse, q_ld, lines == 1 ? R + B : i ? B : R, N, Hq, W,
@@ -356,6 +356,7 @@ ne_status shared_impl(int eb, const void* q, const ne_paged_cache* c, const int*
         a[i].s.R = R;
         a[i].s.seqs = B;
         a[i].s.pre = i ? 0 : R;
+        a[i].s.err = a[i].err;
         for (int k = 0; k < 2; ++k) {
             char* base = rows + k * (w.row_o + w.row_ml + w.rec);
             a[i].row_o[k] = reinterpret_cast<float*>(base);

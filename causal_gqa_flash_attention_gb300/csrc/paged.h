@@ -30,6 +30,7 @@ struct PagedBatch {
     int R, seqs;                      // groups; sequences
     int pre;                          // the line's first `pre` members are the groups' prefixes (R or 0), the others the
                                       // sequences' own positions
+    int* err;
 };
 // Shared positions count in whole steps of this (a multiple of every page and key tile), so that a
 // sequence's own positions begin on a page; the rest is read by every sequence for itself.
@@ -113,8 +114,7 @@ cudaError_t allow_smem(F kfn, int bytes, std::atomic<uint64_t>& done) {
 }
 
 // Which kernel a call runs, and its split.
-enum PagedKind : int { PAGED_SHORT16 = 0, PAGED_SHORT32, PAGED_F32_FEW4, PAGED_F32_FEW8, PAGED_F32_FEW16, PAGED_F32_MANY, PAGED_TILES,
-                        PAGED_SHARED };
+enum PagedKind : int { PAGED_SHORT16 = 0, PAGED_SHORT32, PAGED_F32_FEW4, PAGED_F32_FEW8, PAGED_F32_FEW16, PAGED_F32_MANY, PAGED_TILES };
 PagedKind paged_kind(bool f32, int D, int G, int max_new);
 // cap: the longest length the page tables can hold.
 PagedSplit paged_split(PagedKind kind, int D, int Hkv, int G, int cap);

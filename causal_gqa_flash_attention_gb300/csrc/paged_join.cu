@@ -192,7 +192,6 @@ PagedSplit paged_split(PagedKind kind, int D, int Hkv, int G, int cap) {
             p.C = 2 * kSms;
             break;
         case PAGED_TILES:                                  // G <= 128
-        case PAGED_SHARED:
             p.rows = 256;
             p.gs = G;
             p.sub = 128 / G;
@@ -207,12 +206,6 @@ PagedSplit paged_split(PagedKind kind, int D, int Hkv, int G, int cap) {
             p.ovh = 1024;
             p.min_shift = 11;
             p.snap = 1;                                    // (a prompt of 2048 at D 128: 35.4 -> 34.0 us)
-            if (kind == PAGED_SHARED) {                    // parts of one subtile split their keys over both
-                p.w_full = 2;
-                p.w_part = 1;
-                p.ovh = 400;
-                p.min_shift = 9;
-            }
             break;
     }
     // Contexts of at most 256 positions: a unit's keys take less time than the join would.

@@ -35,6 +35,7 @@ struct PagedSharedSeq : PagedSeq {
 struct PagedGroups {
     static constexpr int MAX = 16;
     int first[MAX + 1], len[MAX];      // first sequence; shared positions in use
+    int tok0[MAX], n[MAX];             // rows of all its sequences
 };
 template <bool SH>
 struct PagedSeqOf {
@@ -83,36 +84,51 @@ __device__ __forceinline__ int paged_shared(const PagedBatch& s, int r, int& g0,
     }
     return g1 - g0 < 2 ? 0 : min(n, min(max(__ldg(s.lens + g0), 0), s.cap)) & ~(kSharedStep - 1);
 }
+// Group r's prefix.
+__device__ __forceinline__ PagedSharedSeq paged_prefix_seq(const PagedBatch& s, int r, int& bad) {
+    PagedSharedSeq q;
+    int g1;
+    q.len = paged_shared(s, r, q.row, g1, bad);
+    PagedRaw w;
+    w.c0 = s.cu ? __ldg(s.cu + q.row) : q.row;
+    w.c1 = s.cu ? __ldg(s.cu + g1) : g1;
+    w.l = 0;
+    const PagedSeq t = paged_clamp(s, w, bad);
+    q.tok0 = t.tok0;
+    q.n = q.len ? t.n : 0;
+    q.skip = 0;
+    q.pre = true;
+    return q;
+}
 // Fills gs (all threads of the CTA; a barrier has to follow).
 __device__ __forceinline__ void paged_load_groups(const PagedBatch& s, PagedGroups& gs) {
     if (s.R > PagedGroups::MAX) return;
     int bad = 0;
     for (int r = threadIdx.x; r < s.R; r += blockDim.x) {
-        int g0, g1;
-        gs.len[r] = paged_shared(s, r, g0, g1, bad);
         gs.first[r] = __ldg(s.groups + r);
         if (r == s.R - 1) gs.first[s.R] = __ldg(s.groups + s.R);
+        const PagedSharedSeq q = paged_prefix_seq(s, r, bad);
+        gs.len[r] = q.len;
+        gs.tok0[r] = q.tok0;
+        gs.n[r] = q.n;
     }
+    if (blockIdx.x == 0 && bad) report_error(s.err, bad);
 }
 // Member b of a SHARED line.
 __device__ __forceinline__ PagedSharedSeq paged_shared_seq(const PagedBatch& s, int b, int& bad, const PagedGroups& gs) {
     PagedSharedSeq q;
     const bool near = s.R <= PagedGroups::MAX;
-    q.pre = b < s.pre;
-    if (q.pre) {
-        int g0, g1;
-        q.len = paged_shared(s, b, g0, g1, bad);
-        PagedRaw w;
-        w.c0 = s.cu ? __ldg(s.cu + g0) : g0;
-        w.c1 = s.cu ? __ldg(s.cu + g1) : g1;
-        w.l = 0;
-        const PagedSeq t = paged_clamp(s, w, bad);
-        q.tok0 = t.tok0;
-        q.n = q.len ? t.n : 0;
-        q.row = g0;
+    if (b < s.pre) {
+        if (!near) return paged_prefix_seq(s, b, bad);
+        q.tok0 = gs.tok0[b];
+        q.n = gs.n[b];
+        q.len = gs.len[b];
+        q.row = gs.first[b];
         q.skip = 0;
+        q.pre = true;
         return q;
     }
+    q.pre = false;
     b -= s.pre;
     const PagedRaw raw = paged_raw(s, b);
     int lo = -1, hi = s.R - 1;                             // the last group that begins at or before b
@@ -354,6 +370,7 @@ struct PagedLocate {
     long long warp_sum[32];
     long long w0, w1, start;
     int b, snap;
+    PagedSharedSeq q;                  // SHARED: member b
 };
 
 // All T threads of the CTA: the total work, this CTA's interval, and the sequence that its
@@ -364,9 +381,10 @@ __device__ __forceinline__ void paged_locate(const PagedAttnArgs& a, int c, Page
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int B = a.s.B;
     int bad = 0;
+    typename PagedSeqOf<SH>::type q = {};
     auto work = [&](int b) -> long long {
         if (b >= B) return 0;
-        const auto q = paged_seq_of<SH>(a.s, b, bad, gs);
+        q = paged_seq_of<SH>(a.s, b, bad, gs);
         return paged_group_cost(q, a.p) * a.p.hg;
     };
     // Inclusive sums over the CTA; the total in sm.warp_sum[T / 32 - 1].
@@ -420,6 +438,7 @@ __device__ __forceinline__ void paged_locate(const PagedAttnArgs& a, int c, Page
             if (mine > 0 && w0 >= end - mine && w0 < end) {   // exactly one thread of one pass
                 sm.b = b0 + tid;
                 sm.start = end - mine;
+                if constexpr (SH) sm.q = q;
             }
             before += sm.warp_sum[T / 32 - 1];
             if (w0 < before) break;                           // (uniform)

@@ -124,12 +124,7 @@ __global__ void __launch_bounds__(384, 1)
     __shared__ __align__(8) uint64_t bar_full[C::NS], bar_empty[C::NS];
     __shared__ __align__(8) uint64_t bar_s_full[2], bar_p_ready[2], bar_o_full[2], bar_s_free[2];
     __shared__ __align__(8) uint64_t bar_seg_full[kSegs], bar_seg_empty[kSegs];
-    __shared__ union {
-        PagedLocate loc;                                   // (read before the first part is queued)
-        float2 ml[128];                                    // maximum and sum of the second half of a split part's rows
-    } sh;
-    PagedLocate& loc = sh.loc;
-    __shared__ __align__(8) uint64_t bar_ml_full, bar_ml_free;
+    __shared__ PagedLocate loc;
     __shared__ Seg s_seg[kSegs];                           // the CTA's parts in order (b < 0: the end)
     __shared__ PagedGroups groups;                         // (SH)
     __shared__ uint32_t tmem_slot;
@@ -152,8 +147,6 @@ __global__ void __launch_bounds__(384, 1)
             mbar_init(smem_u32(&bar_vfix[u]), 32);         // the k-th fix arrives on k % 2: warp 2 can be one
                                                            // fix ahead of the issuer (one part, by its Q), not two
         }
-        mbar_init(smem_u32(&bar_ml_full), 4);
-        mbar_init(smem_u32(&bar_ml_free), 4);
         for (int s = 0; s < kSegs; ++s) {
             mbar_init(smem_u32(&bar_seg_full[s]), 1);
             mbar_init(smem_u32(&bar_seg_empty[s]), kSegReaders);
@@ -191,10 +184,6 @@ __global__ void __launch_bounds__(384, 1)
         if (lane == 0) mbar_arrive(smem_u32(&bar_seg_empty[s]));
         return g.b >= 0;
     };
-    // SH: a part whose rows fit into one subtile is split along its keys: both subtiles hold its rows, the
-    // first takes the even tiles, the second the odd ones, and its softmax warps hand their maxima and sums over
-    // at the end of the part.
-    auto is_split = [&]() { return SH && g.ntok <= sub && g.t1 - g.t0 >= 2; };
     // Where the CTA's share begins, warp 3 finds alone among up to 32 sequences, all warps among more.
     if constexpr (SH) {
         paged_load_groups(a.s, groups);
@@ -229,15 +218,14 @@ __global__ void __launch_bounds__(384, 1)
             };
             int next = page(g.t0), next1 = g.t0 + 1 < g.t1 ? page(g.t0 + 1) : 0;   // two tiles ahead
             if (seg > 0 && !(ok = mbar_wait_warp(smem_u32(&bar_q_empty), (seg - 1) & 1, w, SITE_PAGED_Q))) break;
-            const bool split = is_split();
-            const int n_sub = g.ntok > sub || split ? 2 : 1;
+            const int n_sub = g.ntok > sub ? 2 : 1;
             if (lane == 0) {
                 const uint32_t qf = smem_u32(&bar_q_full);
                 mbar_arrive_expect_tx(qf, n_sub * C::NCH * sub * a.G * 128);
                 for (int u = 0; u < n_sub; ++u)
                     for (int c = 0; c < C::NCH; ++c)
                         tma_load_3d(smem_u32(sQ + u * C::TILE + c * C::CHUNK), &tm_q, qf, c * 64, g.hg * a.G,
-                                    g.tok0 + g.tok + (split ? 0 : u * sub));
+                                    g.tok0 + g.tok + u * sub);
             }
             ++seg;
             for (int t = g.t0; ok && t < g.t1; ++t) {
@@ -330,81 +318,6 @@ __global__ void __launch_bounds__(384, 1)
             // (SEP: a warp without a subtile in this part waits for its Q too, or it could take the
             // next part's wait for this one's.)
             if (!(ok = mbar_wait_warp(smem_u32(&bar_q_full), seg & 1, w, SITE_PAGED_Q))) break;
-            if (SH && is_split()) {
-                // PV of tile t, in subtile t % 2.
-                auto pv = [&](int i, int t, bool last, int next_k) {
-                    const int u = u0 + i, vi = item + 2 * t + 1;
-                    const uint64_t dv = sdesc_add(dv0, (vi % C::NS) * C::TILE);
-#pragma unroll
-                    for (int ks = 0; ks < C::BN / 16; ++ks)
-                        umma_ts<false>(tm + C::O_COL + u * D, tm + C::P_COL + u * C::P_STEP + ks * 8,
-                                       sdesc_add(dv, ks * 16 * 128), id_o, (t > 1 || ks > 0) ? 1u : 0u);
-                    if (C::SEP || last) umma_commit(smem_u32(&bar_o_full[u]));
-                    if (next_k >= 0) s_mmas(i, next_k);
-                    umma_commit(smem_u32(&bar_empty[vi % C::NS]));
-                };
-                if constexpr (C::SEP) {
-                    // The other warp's tile at ring index i is let go of as it comes.
-                    auto let_go = [&](int t, bool v) -> bool {
-                        const int i = item + 2 * t + (v ? 1 : 0);
-                        if (!(v ? v_tile(i, g.t0 + t) : full(i))) return false;
-                        if (lane == 0) mbar_arrive(smem_u32(&bar_empty[i % C::NS]));
-                        __syncwarp();
-                        return true;
-                    };
-                    auto s_tile = [&](int t) -> bool {
-                        const int i = item + 2 * t;
-                        if (!(full(i) && s_free())) return false;
-                        ++s_tiles;
-                        if (elect_one()) {
-                            s_mmas(0, i);
-                            s_done(i, t + 2 >= nt);
-                        }
-                        __syncwarp();
-                        return true;
-                    };
-                    ok = (u0 == 0 || (let_go(0, false) && let_go(0, true))) && s_tile(u0);
-                    for (int t = u0; ok && t < nt; t += 2) {
-                        if (t + 1 < nt && !(ok = let_go(t + 1, false))) break;
-                        if (t + 2 < nt && !(ok = s_tile(t + 2))) break;
-                        if (!(ok = v_tile(item + 2 * t + 1, g.t0 + t) &&
-                                   mbar_wait_warp(smem_u32(&bar_p_ready[u0]), tiles[0] & 1, w, SITE_PAGED_P_READY)))
-                            break;
-                        ++tiles[0];
-                        tc_fence_after();
-                        if (elect_one()) pv(0, t, true, -1);
-                        __syncwarp();
-                        if (t + 1 < nt) ok = let_go(t + 1, true);
-                    }
-                } else {
-                    ok = full(item) && full(item + 2);
-                    if (ok && elect_one()) {
-                        s_mmas(0, item);
-                        s_done(item, false);
-                        s_mmas(NU - 1, item + 2);
-                        s_done(item + 2, nt == 2);
-                    }
-                    __syncwarp();
-                    for (int t = 0; ok && t < nt; ++t) {
-                        const bool more = t + 2 < nt;
-                        const int i = t & 1, kn = item + 2 * t + 4;
-                        if (!(ok = v_tile(item + 2 * t + 1, g.t0 + t) && (!more || full(kn)) &&
-                                   mbar_wait_warp(smem_u32(&bar_p_ready[i]), (i ? tiles[NU - 1] : tiles[0]) & 1, w, SITE_PAGED_P_READY)))
-                            break;
-                        if (i) ++tiles[NU - 1];
-                        else ++tiles[0];
-                        tc_fence_after();
-                        if (elect_one()) {
-                            pv(i, t, !more, more ? kn : -1);
-                            if (more) s_done(kn, t + 3 >= nt);
-                        }
-                        __syncwarp();
-                    }
-                }
-                item += 2 * nt;
-                ++seg;
-                continue;
-            }
             if (C::SEP && mine == 0) {                     // nothing to multiply: it zeroes V and lets go
                 for (int i = 0; ok && i < 2 * nt; ++i) {
                     if (!(ok = i & 1 ? v_tile(item + i, g.t0 + (i >> 1)) : full(item + i))) break;
@@ -492,12 +405,17 @@ __global__ void __launch_bounds__(384, 1)
         PagedWalkOf<SH> walk;
         walk.gs = &groups;
         if (a.s.B <= 32) paged_locate_warp(a, blockIdx.x, walk, blockIdx.x == 0);
-        else walk.init(a, loc.w0, loc.w1, loc.snap, loc.b, loc.start);
+        else {
+            if constexpr (SH) walk.q = loc.q;
+            walk.init(a, loc.w0, loc.w1, loc.snap, loc.b, loc.start, SH);
+        }
         bool more = true;
         for (int k = 0; more; ++k) {
             const int s = k % kSegs;
             more = walk.next(a, g);
             if (!more) g.b = -1;
+            if constexpr (SH)
+                if (more) paged_where(a, g, lane, 32);
             if (k >= kSegs &&
                 !mbar_wait_warp(smem_u32(&bar_seg_empty[s]), (k / kSegs - 1) & 1, w, SITE_PAGED_SEG))
                 break;
@@ -514,21 +432,17 @@ __global__ void __launch_bounds__(384, 1)
         const uint32_t lt = tm + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t sc = lt + u * 128, oc = lt + C::O_COL + u * D, pc = lt + C::P_COL + u * C::P_STEP;
         const float sl2 = a.scale_log2;
-        int tiles = 0, parts = 0, merges = 0;
-        bool ok = true, owed = false;                      // owed: the other half still reads this one's outputs
+        int tiles = 0, parts = 0;
+        bool ok = true;
         while (ok && next_part()) {
-            const bool split = is_split();
-            const int us = split ? 0 : u;                  // subtile of the rows
-            const int ntok = min(sub, g.ntok - us * sub);  // tokens of this subtile
+            const int ntok = min(sub, g.ntok - u * sub);   // tokens of this subtile
             const int live_rows = ntok * a.G;
             if (ntok <= 0) continue;
             const bool live = r < live_rows;
-            const int tok = g.tok + us * sub + r / a.G;
+            const int tok = g.tok + u * sub + r / a.G;
             const long long orow = (long long)(g.tok0 + tok) * a.Hq + g.hg * a.G + r % a.G;
             if (g.t0 == g.t1) {                            // nothing to attend to
-                if constexpr (SH) {
-                    if (u == 0) paged_where(a, g, r, 128);
-                } else if (live) {
+                if (!SH && live) {
                     uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + orow * D);
 #pragma unroll
                     for (int e = 0; e < D / 8; ++e) dst[e] = make_uint4(0u, 0u, 0u, 0u);
@@ -536,16 +450,11 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 continue;
             }
-            const int first_lim = g.base + g.tok + us * sub + 1;       // keys that the subtile's first token sees
+            const int first_lim = g.base + g.tok + u * sub + 1;        // keys that the subtile's first token sees
             const int lim = live ? g.base + tok + 1 : 0;
             const bool warp_live = (warp & 3) * 32 < live_rows;
             float m = -INFINITY, l = 0.f;
-            if (SH && owed) {
-                if (!(ok = mbar_wait_warp(smem_u32(&bar_ml_free), (merges - 1) & 1, w, SITE_PAGED_O_FULL))) break;
-                owed = false;
-            }
-            const int tf = split ? g.t0 + u : g.t0;        // this half's first tile
-            for (int t = tf; t < g.t1; t += split ? 2 : 1, ++tiles) {
+            for (int t = g.t0; t < g.t1; ++t, ++tiles) {
                 if (!(ok = mbar_wait_warp(smem_u32(&bar_s_full[u]), tiles & 1, w, SITE_PAGED_S_FULL))) break;
                 // SEP: P(t - 1) is read and O_u at rest once PV(t - 1) is complete.  (Every warp waits
                 // for it, so that none arrives for a tile while others still owe the one before.)
@@ -589,8 +498,8 @@ __global__ void __launch_bounds__(384, 1)
                 ok = pv_before();
                 if (!ok) break;
                 if (C::SEP) tc_fence_after();
-                const bool need = t > tf && m_tile > m + 8.f;
-                if (t == tf) m = m_tile;
+                const bool need = t > g.t0 && m_tile > m + 8.f;
+                if (t == g.t0) m = m_tile;
                 if (__any_sync(0xffffffffu, need)) {
                     const float alpha = need ? ex2(m - m_tile) : 1.f;
                     if (need) {
@@ -630,34 +539,6 @@ __global__ void __launch_bounds__(384, 1)
             if (!ok) break;
             if (!(ok = mbar_wait_warp(smem_u32(&bar_o_full[u]), (C::SEP ? tiles - 1 : parts) & 1, w, SITE_PAGED_O_FULL))) break;
             ++parts;
-            float w0 = 1.f, w1 = 0.f;                      // weights of the two halves
-            if constexpr (SH) {
-                if (split && u == 1) {
-                    tc_fence_after();
-                    sh.ml[r] = make_float2(m, l);
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&bar_ml_full));
-                    ++merges;
-                    owed = true;
-                    continue;
-                }
-                if (u == 0) paged_where(a, g, r, 128);
-                if (split) {
-                    if (!(ok = mbar_wait_warp(smem_u32(&bar_ml_full), merges & 1, w, SITE_PAGED_O_FULL))) break;
-                    ++merges;
-                    const float2 other = sh.ml[r];
-                    const float both = fmaxf(m, other.x), ref = both == -INFINITY ? 0.f : both;
-                    w0 = ex2(m - ref);
-                    w1 = ex2(other.x - ref);
-                    l = l * w0 + other.y * w1;
-                    m = both;
-                    if (!warp_live) {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(&bar_ml_free));
-                    }
-                }
-            }
             if (!warp_live) continue;
             tc_fence_after();
             const bool whole = g.whole(), direct = whole && !SH;
@@ -681,13 +562,6 @@ __global__ void __launch_bounds__(384, 1)
             for (int c = 0; c < DR; c += 32) {
                 uint32_t o[32];
                 tmem_ld_cols<1>(oc + c, o);
-                if constexpr (SH)
-                    if (split) {
-                        uint32_t o1[32];
-                        tmem_ld_cols<1>(oc + D + c, o1);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * w0 + __uint_as_float(o1[e]) * w1);
-                    }
                 if (direct) {
                     uint4 v[4];
 #pragma unroll
@@ -719,7 +593,6 @@ __global__ void __launch_bounds__(384, 1)
             }
             __syncwarp();
             tc_fence_before();
-            if (SH && split && lane == 0) mbar_arrive(smem_u32(&bar_ml_free));
             if (live) {
                 if (direct) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
                 else *parts_ml = make_float2(m, l);
