@@ -305,9 +305,14 @@ ne_status attn_impl(int eb, const void* q, const ne_paged_cache* c, const int* t
 }
 
 // ---------------------------------------------------------------- shared prefixes
-// Rows per kv head from which on a sequence fills the kernels' row tiles by itself, so that nothing is
-// won by putting rows of several sequences into one.
-constexpr int kSharedRows = 256;
+// Where a call runs as ne_paged_attn.  (1) From so many rows per kv head on a sequence fills the kernels'
+// row tiles by itself: 16 sequences of 252 rows over 8192 shared positions 48 us against 63, 64 of up to 192
+// rows 129 against 96.  (2) While all sequences' caches, as large as their tables, take no more bytes than
+// this, reading them all beats a join of two lines: bf16, 33 MB 13.1 us against 15.1, 66 MB 16.1 against
+// 15.2, 134 MB 21.8 against 16.1; fp32 with few rows 134 MB 22 against 32, 537 MB 59 against 54 (its
+// products take as long either way).
+constexpr int kSharedRows = 224;
+constexpr long long kSharedBytes = 64LL << 20, kSharedBytesF32 = 256LL << 20;
 
 struct SharedWs {
     size_t parts, row_o, row_ml, rec, total;   // parts, row_o, row_ml and records of one of the two lines; both
@@ -339,7 +344,9 @@ ne_status shared_impl(int eb, const void* q, const ne_paged_cache* c, const int*
     if ((s = attn_ws_check(ws, ws_bytes, w.total)) != NE_OK) return s;
     const int G = Hq / c->Hkv, most = cu ? std::min(max_new, N) : 1;
     const bool f32 = eb == 4;
-    if (R == 0 || (long long)most * G >= kSharedRows || (!f32 && G > 128))
+    const long long bytes = (long long)B * W * c->page_size * c->Hkv * 2 * c->D * eb;
+    if (R == 0 || (long long)most * G >= kSharedRows || (!f32 && G > 128) ||
+        bytes <= (f32 && (long long)most * G <= 16 ? kSharedBytesF32 : kSharedBytes))
         return attn_impl(eb, q, c, table, lens, cu, o, lse, q_ld, B, N, Hq, W, max_new, ws, ws_bytes, stream);
     // bf16: one line of prefixes and own positions, tiles for all.  fp32: a line and a kernel for each,
     // chosen by the rows of a group and of a sequence.

@@ -60,19 +60,21 @@ __global__ void __launch_bounds__(kThreads) paged_shared_join_kernel(const Paged
     griddep_wait();
     const int tid = threadIdx.x, grp = tid / LPR, e = (tid % LPR) * 4, lg = grp % LG;
     const long long row = (long long)blockIdx.x * ROWS + grp / LG;
-    const int tok = (int)(row / own.Hq), h = (int)(row - (long long)tok * own.Hq);
+    // (In 32 bits: N Hq D is below 2^31.  A block's rows behind the last one look at that.)
+    const uint32_t at_row = (uint32_t)min(row, (long long)own.s.N * own.Hq - 1);
+    const int tok = (int)(at_row / (uint32_t)own.Hq), h = (int)(at_row - (uint32_t)tok * own.Hq);
+    const int hkv = h / own.G, g = h - hkv * own.G;
+    auto at = [&](const PagedAttnArgs& a) {
+        const int ngrp = (a.G + a.p.gs - 1) / a.p.gs;
+        return (size_t)tok * a.p.hg + hkv * ngrp + g / a.p.gs;
+    };
+    const size_t io = at(own), ip = at(pre);
+    const int of = own.rec_first[0][io], ol = own.rec_last[0][io], pf = pre.rec_first[1][ip], pl = pre.rec_last[1][ip];
     const int c0 = own.s.cu ? max(__ldg(own.s.cu), 0) : 0, c1 = own.s.cu ? __ldg(own.s.cu + own.s.seqs) : own.s.N;
-    const bool live = tok >= c0 && tok < min(c1, own.s.N);
+    const bool live = row == (long long)at_row && tok >= c0 && tok < min(c1, own.s.N);
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (live) {
-        const int hkv = h / own.G, g = h - hkv * own.G;
-        auto at = [&](const PagedAttnArgs& a) {
-            const int ngrp = (a.G + a.p.gs - 1) / a.p.gs;
-            return (size_t)tok * a.p.hg + hkv * ngrp + g / a.p.gs;
-        };
-        const size_t io = at(own), ip = at(pre);
-        const int of = own.rec_first[0][io], ol = own.rec_last[0][io], pf = pre.rec_first[1][ip], pl = pre.rec_last[1][ip];
         const RowParts po = row_parts(own, of, ol, g);
         RowParts pp = row_parts(pre, pf, pl, g);
         if (of == -1 || (of >= 0 && !(of & kHasPrefix))) pp.n = 0;
@@ -106,8 +108,17 @@ __global__ void __launch_bounds__(kThreads) paged_shared_join_kernel(const Paged
             s_l[grp] = l;
         }
         __syncthreads();
-        if (lg == 0)
-            for (int k = 1; k < LG; ++k) add_part(m, l, o, s_m[grp + k], s_l[grp + k], s_o[tid + k * LPR]);
+        for (int half = LG / 2; half > 0; half >>= 1) {    // (LG is a power of two)
+            if (lg < half) {
+                add_part(m, l, o, s_m[grp + half], s_l[grp + half], s_o[tid + half * LPR]);
+                s_o[tid] = o;
+                if (e == 0) {
+                    s_m[grp] = m;
+                    s_l[grp] = l;
+                }
+            }
+            __syncthreads();
+        }
     }
     if (live && lg == 0) {
         const float inv = l == 0.f ? 0.f : 1.f / l;

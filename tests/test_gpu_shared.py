@@ -34,11 +34,13 @@ def i32(x):
     return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
 
 
-def make(dtype, Hq, Hkv, D, ps, groups, shared, n, lens, seed=1, hnd=False, tail=0, lead=0, copies=False):
+def make(dtype, Hq, Hkv, D, ps, groups, shared, n, lens, seed=1, hnd=False, tail=0, lead=0, copies=False, wide=True):
     """Sequences of a group hold the same shared positions, in the same pages (or, copies, in their
     own); everything that no sequence holds is NaN, unused table entries lie outside the pool."""
     rng = np.random.default_rng(seed)
     B, W = len(lens), max(1, max(-(-x // ps) for x in lens)) + 1
+    if wide:                                                # (tables that could hold much: the call does share)
+        W = max(W, (300 << 20) // (B * ps * Hkv * 2 * D * (2 if dtype == BF16 else 4)) + 1)
     cu = np.concatenate([[0], np.cumsum(n)]) + lead
     N = int(cu[-1]) + tail
     P = sum(-(-x // ps) for x in lens) + 2
@@ -151,7 +153,7 @@ def test_many_groups(dtype, D, n):
 @pytest.mark.parametrize("max_new", [1, 8, 22, 4000])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_any_max_new_is_right(dtype, max_new):
-    """22 times 12 rows: tiles are full, the call runs as paged_attn; below it a hint that is too small."""
+    """22 times 12 rows: tiles are full, the call runs as paged_attn; below it hints that are too small."""
     check(dtype, 12, 1, 64, 16, [0, 3], [512], [25, 1, 70], [600, 513, 700], max_new=max_new, seed=11)
 
 
@@ -163,6 +165,16 @@ def test_more_than_128_query_heads():
 @pytest.mark.parametrize("dtype,n", [(BF16, [1, 1, 1]), (BF16, [14, 2, 9]), (F32, [1, 1, 1]), (F32, [14, 2, 9])])
 def test_padding_and_layouts(dtype, n):
     check(dtype, 8, 4, 64, 32, [0, 3], [300], n, [400, 302, 310], hnd=True, tail=5, lead=3, max_new=max(n), seed=13)
+
+
+def test_small_caches_run_as_paged_attn():
+    for dtype, D in ((BF16, 64), (F32, 32)):
+        q, kp, vp, table, ln, gr, sh, cu, *_ = make(dtype, 12, 4, D, 16, [0, 3], [512], [1, 2, 3], [600, 514, 700], wide=False)
+        a = ne.paged_attn_shared(q, kp, vp, table, ln, gr, sh, cu, max_new=3)
+        b = ne.paged_attn(q, kp, vp, table, ln, cu, max_new=3)
+        ok()
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        check(dtype, 12, 4, D, 16, [0, 3], [512], [1, 2, 3], [600, 514, 700], max_new=3, wide=False)
 
 
 def test_negative_positions():
@@ -227,6 +239,7 @@ def test_offsets_beyond_32_bits():
     small = [x[ids].clone() for x in (kp, vp)]
     row = np.arange(P - 40, P - 20)
     table = np.stack([row, np.concatenate([row[:8], row[8:] + 20])])
+    table = np.concatenate([table, np.full((2, 500), P + 9)], 1)       # (of 67 MB: the call does share)
     q = synthetic.randn((2, 8, D), 3, 1.0, BF16).cuda()
     a = ne.paged_attn_shared(q, kp, vp, i32(table), i32([1200, 700]), i32([0, 2]), i32([512]))
     b = ne.paged_attn_shared(q, *small, i32(table - (P - 40)), i32([1200, 700]), i32([0, 2]), i32([512]))
