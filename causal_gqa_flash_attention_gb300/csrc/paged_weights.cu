@@ -478,6 +478,8 @@ struct ManyCfg {
     static constexpr int TILE = NCH * CHUNK;               // 128 rows of K or Q
     static constexpr int NK = D == 128 ? 3 : 4;            // key tiles (two to a unit) in shared memory
     static constexpr int NS = D == 128 ? 3 : 8;            // query tiles in the ring
+    static constexpr int NL = 8;                           // log-sum-exps of so many (a slot of Q is free behind its
+                                                           // products, they are read until the exponentials are done)
     static constexpr int SMEM = 1024 + (NK + NS) * TILE;
     static constexpr int THREADS = 384;
 };
@@ -496,9 +498,10 @@ __global__ void __launch_bounds__(384, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sK = smem;
     uint8_t* sQ = smem + C::NK * C::TILE;
-    __shared__ __align__(16) float s_nl[C::NS][128];       // -log2(e) lse
+    __shared__ __align__(16) float s_nl[C::NL][128];       // -log2(e) lse
     __shared__ __align__(8) uint64_t bar_k_full[C::NK], bar_k_empty[C::NK], bar_q_full[C::NS], bar_q_empty[C::NS];
     __shared__ __align__(8) uint64_t bar_s_full[4], bar_s_free[4], bar_part_full[kParts], bar_part_empty[kParts], bar_final;
+    __shared__ __align__(8) uint64_t bar_l_full[C::NL], bar_l_empty[C::NL];
     __shared__ Line<C::THREADS> line;
     __shared__ WeightPart s_part[kParts];
     __shared__ uint32_t tmem_slot;
@@ -511,8 +514,12 @@ __global__ void __launch_bounds__(384, 1)
             mbar_init(smem_u32(&bar_k_empty[i]), 1);
         }
         for (int i = 0; i < C::NS; ++i) {
-            mbar_init(smem_u32(&bar_q_full[i]), 2);        // the copy and the lse warp
-            mbar_init(smem_u32(&bar_q_empty[i]), 9);       // the products and eight exponential warps
+            mbar_init(smem_u32(&bar_q_full[i]), 1);
+            mbar_init(smem_u32(&bar_q_empty[i]), 1);
+        }
+        for (int i = 0; i < C::NL; ++i) {
+            mbar_init(smem_u32(&bar_l_full[i]), 1);
+            mbar_init(smem_u32(&bar_l_empty[i]), 8);       // the exponential warps
         }
         for (int i = 0; i < 4; ++i) {                      // 2 u + item % 2
             mbar_init(smem_u32(&bar_s_full[i]), 1);
@@ -607,8 +614,7 @@ __global__ void __launch_bounds__(384, 1)
                 __syncwarp();
             }
         }
-        // Every copy this CTA started has landed before it ends.  (A query tile's barrier also waits
-        // for the lse warp, which gives up only with an error.)
+        // Every copy this CTA started has landed before it ends.
         __syncwarp();
         if (lane == 0) {
             for (int i = max(0, keys - C::NK); i < keys; ++i)
@@ -668,18 +674,18 @@ __global__ void __launch_bounds__(384, 1)
         bool ok = true;
         while (ok && next_part())
             for (int t = p.t0; t < p.t1; ++t, ++item) {
-                const int i = item % C::NS, tok = t / a.ngrp * a.sub, h0 = t % a.ngrp * a.gs;
+                const int i = item % C::NL, tok = t / a.ngrp * a.sub, h0 = t % a.ngrp * a.gs;
                 float v[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     v[k] = lane + 32 * k < box && tok + tk[k] < p.n && h0 + hd[k] < a.G
                                ? -kLog2e * __ldg(a.lse + (long long)(p.tok0 + tok + tk[k]) * a.Hq + p.h * a.G + h0 + hd[k])
                                : -INFINITY;
-                if (item >= C::NS && !(ok = mbar_wait_warp(smem_u32(&bar_q_empty[i]), (item / C::NS - 1) & 1, w, SITE_PAGED_Q))) break;
+                if (item >= C::NL && !(ok = mbar_wait_warp(smem_u32(&bar_l_empty[i]), (item / C::NL - 1) & 1, w, SITE_PAGED_Q))) break;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) s_nl[i][lane + 32 * k] = v[k];
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bar_q_full[i]));
+                if (lane == 0) mbar_arrive(smem_u32(&bar_l_full[i]));
             }
     } else if (warp == 3) {
         // ------------------------------------------------------------ the CTA's parts
@@ -710,9 +716,8 @@ __global__ void __launch_bounds__(384, 1)
             const float old = weight_old(a, p, key);
             float2 s2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             for (int t = p.t0; t < p.t1; ++t, ++item) {
-                const int i = item % C::NS;
-                // (This barrier stands for the lse entries.)
-                if (!(ok = mbar_wait_warp(smem_u32(&bar_q_full[i]), (item / C::NS) & 1, w, SITE_PAGED_Q))) break;
+                const int i = item % C::NL;
+                if (!(ok = mbar_wait_warp(smem_u32(&bar_l_full[i]), (item / C::NL) & 1, w, SITE_PAGED_Q))) break;
                 if (mine) {
                     const int s = uses & 1;
                     if (!(ok = mbar_wait_warp(smem_u32(&bar_s_full[2 * u + s]), (uses / 2) & 1, w, SITE_PAGED_S_FULL))) break;
@@ -756,7 +761,7 @@ __global__ void __launch_bounds__(384, 1)
                     else tile(std::false_type());
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bar_q_empty[i]));
+                if (lane == 0) mbar_arrive(smem_u32(&bar_l_empty[i]));
             }
             if (!ok) break;
             weight_put(a, p, key, ((s2[0].x + s2[0].y) + (s2[1].x + s2[1].y)) + ((s2[2].x + s2[2].y) + (s2[3].x + s2[3].y)), old);
