@@ -709,11 +709,14 @@ __global__ void __launch_bounds__(384, 1)
         const uint32_t lt = tm + ((uint32_t)((warp & 3) * 32) << 16) + u * 256;
         const float2 sl2 = make_float2(a.scale_log2, a.scale_log2);
         int item = 0, uses = 0;                            // query tiles; S tiles of this key tile
+        int tg = 0, th = 0;                                // t / ngrp and t % ngrp of the query tile at hand
         bool ok = true;
         while (ok && next_part()) {
             const int k0 = p.kt * 256 + u * 128;           // the warps' first key
             const bool mine = k0 < p.len;
             const float old = weight_old(a, p, key);
+            tg = p.t0 / a.ngrp;
+            th = p.t0 - tg * a.ngrp;
             float2 s2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             for (int t = p.t0; t < p.t1; ++t, ++item) {
                 const int i = item % C::NL;
@@ -723,7 +726,7 @@ __global__ void __launch_bounds__(384, 1)
                     if (!(ok = mbar_wait_warp(smem_u32(&bar_s_full[2 * u + s]), (uses / 2) & 1, w, SITE_PAGED_S_FULL))) break;
                     ++uses;
                     tc_fence_after();
-                    const int tok = t / a.ngrp * a.sub, live = min(a.gs, a.G - t % a.ngrp * a.gs) * min(a.sub, p.n - tok);
+                    const int tok = tg * a.sub, live = min(a.gs, a.G - th * a.gs) * min(a.sub, p.n - tok);
                     const int base = p.len - p.n + tok;    // position of the tile's first token
                     // Rows c_min .. live-1 of the tile see this thread's key.
                     const int d = k0 + lk - base;
@@ -762,6 +765,10 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&bar_l_empty[i]));
+                if (++th == a.ngrp) {
+                    th = 0;
+                    ++tg;
+                }
             }
             if (!ok) break;
             weight_put(a, p, key, ((s2[0].x + s2[0].y) + (s2[1].x + s2[1].y)) + ((s2[2].x + s2[2].y) + (s2[3].x + s2[3].y)), old);
