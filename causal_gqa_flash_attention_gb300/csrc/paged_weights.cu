@@ -468,7 +468,7 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, 
 }
 
 constexpr int kParts = 4;              // parts in the queue from warp 3 to the others
-constexpr int kPartReaders = 11;       // warps 0, 1, 2 and 4-11
+constexpr int kPartReaders = 19;       // all warps but 3
 
 // D 32 runs as 64: TMA fills the columns behind a row's end with zeros.
 template <int D>
@@ -481,17 +481,19 @@ struct ManyCfg {
     static constexpr int NL = 8;                           // log-sum-exps of so many (a slot of Q is free behind its
                                                            // products, they are read until the exponentials are done)
     static constexpr int SMEM = 1024 + (NK + NS) * TILE;
-    static constexpr int THREADS = 384;
+    static constexpr int THREADS = 640;
 };
 
 // A unit holds two tiles of 128 keys, so that a query tile (16 KB at D 64, 32 at D 128; an SM receives some 35
-// bytes a cycle) feeds two products.  Roles (12 warps): 0 producer (keys of a part, then query tiles through
-// the ring), 1 UMMA issuer, 2 the log-sum-exps of every query tile, 3 the CTA's parts, 4-11 the
-// exponentials: warps 4-7 the first 128 keys, 8-11 the others, a thread per key (TMEM lane).  S of key tile
+// bytes a cycle) feeds two products.  Roles (20 warps): 0 producer (keys of a part, then query tiles through
+// the ring), 1 UMMA issuer, 2 the log-sum-exps of every query tile, 3 the CTA's parts, 4-19 the
+// exponentials, a thread per key (TMEM lane): warps 4-7 and 12-15 the first 128 keys, the others the second,
+// warps 4-11 the even query tiles, 12-19 the odd ones (a warp's loads and waits need three others' products
+// to fill the exponential units: with all tiles in eight warps 119 us at D 64).  S of key tile
 // u and query tile i lies in TMEM columns 256 u + 128 (i % 2).  Dead rows of a query tile: those that TMA never
 // writes are zero and their lse entry -inf; those that hold other sequences' rows are masked where they occur.
 template <int D>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(640, 1)
     weights_many_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const WeightArgs a) {
     using C = ManyCfg<D>;
     extern __shared__ uint8_t smem_raw[];
@@ -504,6 +506,8 @@ __global__ void __launch_bounds__(384, 1)
     __shared__ __align__(8) uint64_t bar_l_full[C::NL], bar_l_empty[C::NL];
     __shared__ Line<C::THREADS> line;
     __shared__ WeightPart s_part[kParts];
+    __shared__ __align__(8) uint64_t bar_sum_full[2], bar_sum_free[2];
+    __shared__ float s_sum[2][256];                        // the second half of the rows' sums, for parts in turn
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -519,11 +523,15 @@ __global__ void __launch_bounds__(384, 1)
         }
         for (int i = 0; i < C::NL; ++i) {
             mbar_init(smem_u32(&bar_l_full[i]), 1);
-            mbar_init(smem_u32(&bar_l_empty[i]), 8);       // the exponential warps
+            mbar_init(smem_u32(&bar_l_empty[i]), 8);       // the exponential warps of every second tile
         }
         for (int i = 0; i < 4; ++i) {                      // 2 u + item % 2
             mbar_init(smem_u32(&bar_s_full[i]), 1);
             mbar_init(smem_u32(&bar_s_free[i]), 4);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&bar_sum_full[i]), 8);
+            mbar_init(smem_u32(&bar_sum_free[i]), 8);
         }
         for (int i = 0; i < kParts; ++i) {
             mbar_init(smem_u32(&bar_part_full[i]), 1);
@@ -626,7 +634,7 @@ __global__ void __launch_bounds__(384, 1)
         // ------------------------------------------------------------ UMMA issuer
         constexpr uint32_t id_s = idesc_make(FMT_BF16, 128, 128, false, false);
         const uint64_t dk0 = sdesc(smem_u32(sK), 16, 1024), dq0 = sdesc(smem_u32(sQ), 16, 1024);
-        int keys = 0, item = 0, uses[2] = {0, 0};          // uses: S tiles of either key tile so far
+        int keys = 0, item = 0, uses[4] = {0, 0, 0, 0};    // uses: of S buffers 2 u + item % 2 so far
         bool ok = true;
         while (ok && next_part()) {
             if (p.t0 == p.t1) continue;
@@ -635,15 +643,14 @@ __global__ void __launch_bounds__(384, 1)
                 ok = mbar_wait_warp(smem_u32(&bar_k_full[(keys + u) % C::NK]), ((keys + u) / C::NK) & 1, w, SITE_PAGED_KV_FULL);
             if (!ok) break;
             for (int t = p.t0; ok && t < p.t1; ++t, ++item) {
-                const int i = item % C::NS;
+                const int i = item % C::NS, odd = item & 1;
                 if (!(ok = mbar_wait_warp(smem_u32(&bar_q_full[i]), (item / C::NS) & 1, w, SITE_PAGED_Q))) break;
                 const uint64_t dq = sdesc_add(dq0, i * C::TILE);
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     if (u >= nu) break;
-                    const int s = 2 * u + (uses[u] & 1);
-                    if (uses[u] >= 2 && !(ok = mbar_wait_warp(smem_u32(&bar_s_free[s]), (uses[u] / 2 - 1) & 1, w, SITE_PAGED_S_FULL))) break;
-                    ++uses[u];
+                    const int s = 2 * u + odd, n = odd ? uses[2 * u + 1]++ : uses[2 * u]++;
+                    if (n >= 1 && !(ok = mbar_wait_warp(smem_u32(&bar_s_free[s]), (n - 1) & 1, w, SITE_PAGED_S_FULL))) break;
                     tc_fence_after();
                     const uint64_t dk = sdesc_add(dk0, (keys + u) % C::NK * C::TILE);
                     if (elect_one()) {
@@ -672,21 +679,40 @@ __global__ void __launch_bounds__(384, 1)
         }
         int item = 0;
         bool ok = true;
-        while (ok && next_part())
-            for (int t = p.t0; t < p.t1; ++t, ++item) {
-                const int i = item % C::NL, tok = t / a.ngrp * a.sub, h0 = t % a.ngrp * a.gs;
-                float v[4];
+        while (ok && next_part()) {
+            int tg = p.t0 / a.ngrp, th = p.t0 - tg * a.ngrp;
+            const float* lse = a.lse + (long long)p.tok0 * a.Hq + p.h * a.G;
+            for (int t0 = p.t0; ok && t0 < p.t1; t0 += 4) {   // four tiles' loads at a time: one by one their latency bounds all
+                // (Loads without a condition, or each would be waited for in a branch of its own.)
+                float v[4][4];
+                unsigned in = 0;
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    v[k] = lane + 32 * k < box && tok + tk[k] < p.n && h0 + hd[k] < a.G
-                               ? -kLog2e * __ldg(a.lse + (long long)(p.tok0 + tok + tk[k]) * a.Hq + p.h * a.G + h0 + hd[k])
-                               : -INFINITY;
-                if (item >= C::NL && !(ok = mbar_wait_warp(smem_u32(&bar_l_empty[i]), (item / C::NL - 1) & 1, w, SITE_PAGED_Q))) break;
+                for (int j = 0; j < 4; ++j) {
+                    const int tok = tg * a.sub, h0 = th * a.gs;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) s_nl[i][lane + 32 * k] = v[k];
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bar_l_full[i]));
+                    for (int k = 0; k < 4; ++k) {
+                        const bool live = t0 + j < p.t1 && lane + 32 * k < box && tok + tk[k] < p.n && h0 + hd[k] < a.G;
+                        in |= (unsigned)live << (4 * j + k);
+                        v[j][k] = __ldg(lse + (live ? (long long)(tok + tk[k]) * a.Hq + h0 + hd[k] : 0));
+                    }
+                    if (++th == a.ngrp) {
+                        th = 0;
+                        ++tg;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (t0 + j >= p.t1) break;
+                    const int i = item % C::NL;
+                    if (item >= C::NL && !(ok = mbar_wait_warp(smem_u32(&bar_l_empty[i]), (item / C::NL - 1) & 1, w, SITE_PAGED_Q))) break;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) s_nl[i][lane + 32 * k] = in >> (4 * j + k) & 1u ? -kLog2e * v[j][k] : -INFINITY;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&bar_l_full[i]));
+                    ++item;
+                }
             }
+        }
     } else if (warp == 3) {
         // ------------------------------------------------------------ the CTA's parts
         if (lane < 2) a.part_info[blockIdx.x * 2 + lane] = make_int4(0, 0, 0, 0);
@@ -705,25 +731,24 @@ __global__ void __launch_bounds__(384, 1)
         }
     } else {
         // ------------------------------------------------------------ exponentials
-        const int u = (warp - 4) >> 2, lk = (warp & 3) * 32 + lane, key = u * 128 + lk;
+        const int u = ((warp - 4) >> 2) & 1, half = (warp - 4) >> 3, lk = (warp & 3) * 32 + lane, key = u * 128 + lk;
         const uint32_t lt = tm + ((uint32_t)((warp & 3) * 32) << 16) + u * 256;
         const float2 sl2 = make_float2(a.scale_log2, a.scale_log2);
-        int item = 0, uses = 0;                            // query tiles; S tiles of this key tile
-        int tg = 0, th = 0;                                // t / ngrp and t % ngrp of the query tile at hand
+        int item = 0, uses = 0, parts = 0;                 // query tiles; those of this half; parts
         bool ok = true;
         while (ok && next_part()) {
             const int k0 = p.kt * 256 + u * 128;           // the warps' first key
             const bool mine = k0 < p.len;
-            const float old = weight_old(a, p, key);
-            tg = p.t0 / a.ngrp;
-            th = p.t0 - tg * a.ngrp;
+            const float old = half == 0 ? weight_old(a, p, key) : 0.f;
             float2 s2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            for (int t = p.t0; t < p.t1; ++t, ++item) {
-                const int i = item % C::NL;
-                if (!(ok = mbar_wait_warp(smem_u32(&bar_l_full[i]), (item / C::NL) & 1, w, SITE_PAGED_Q))) break;
+            // Every second query tile is this half's, in S buffer `half`.
+            const int skip = (item ^ half) & 1, n = p.t1 - p.t0;
+            int tg = (p.t0 + skip) / a.ngrp, th = p.t0 + skip - tg * a.ngrp;   // t / ngrp, t % ngrp
+            for (int j = skip; j < n; j += 2) {
+                const int i = (item + j) % C::NL;
+                if (!(ok = mbar_wait_warp(smem_u32(&bar_l_full[i]), ((item + j) / C::NL) & 1, w, SITE_PAGED_Q))) break;
                 if (mine) {
-                    const int s = uses & 1;
-                    if (!(ok = mbar_wait_warp(smem_u32(&bar_s_full[2 * u + s]), (uses / 2) & 1, w, SITE_PAGED_S_FULL))) break;
+                    if (!(ok = mbar_wait_warp(smem_u32(&bar_s_full[2 * u + half]), uses & 1, w, SITE_PAGED_S_FULL))) break;
                     ++uses;
                     tc_fence_after();
                     const int tok = tg * a.sub, live = min(a.gs, a.G - th * a.gs) * min(a.sub, p.n - tok);
@@ -734,22 +759,22 @@ __global__ void __launch_bounds__(384, 1)
                     const float4* nl = reinterpret_cast<const float4*>(s_nl[i]);
                     auto tile = [&](auto edge) {
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            uint32_t x[64];
-                            tmem_ld_cols<2>(lt + s * 128 + half * 64, x);
-                            if (half == 1) {
+                        for (int c0 = 0; c0 < 128; c0 += 32) {
+                            uint32_t x[32];
+                            tmem_ld_cols<1>(lt + half * 128 + c0, x);
+                            if (c0 == 96) {
                                 tc_fence_before();
                                 __syncwarp();
-                                if (lane == 0) mbar_arrive(smem_u32(&bar_s_free[2 * u + s]));
+                                if (lane == 0) mbar_arrive(smem_u32(&bar_s_free[2 * u + half]));
                             }
 #pragma unroll
-                            for (int e = 0; e < 64; e += 4) {
-                                const float4 l4 = nl[half * 16 + e / 4];
+                            for (int e = 0; e < 32; e += 4) {
+                                const float4 l4 = nl[(c0 + e) / 4];
                                 const float2 y0 = __ffma2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), sl2, make_float2(l4.x, l4.y));
                                 const float2 y1 = __ffma2_rn(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), sl2, make_float2(l4.z, l4.w));
                                 float2 p0 = make_float2(ex2(y0.x), ex2(y0.y)), p1 = make_float2(ex2(y1.x), ex2(y1.y));
                                 if constexpr (decltype(edge)::value) {
-                                    const int c = half * 64 + e;
+                                    const int c = c0 + e;
                                     p0.x = c >= c_min && c < live ? p0.x : 0.f;
                                     p0.y = c + 1 >= c_min && c + 1 < live ? p0.y : 0.f;
                                     p1.x = c + 2 >= c_min && c + 2 < live ? p1.x : 0.f;
@@ -765,13 +790,25 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&bar_l_empty[i]));
-                if (++th == a.ngrp) {
-                    th = 0;
-                    ++tg;
-                }
+                for (th += 2; th >= a.ngrp; th -= a.ngrp) ++tg;
             }
+            item += n;
             if (!ok) break;
-            weight_put(a, p, key, ((s2[0].x + s2[0].y) + (s2[1].x + s2[1].y)) + ((s2[2].x + s2[2].y) + (s2[3].x + s2[3].y)), old);
+            const float sum = ((s2[0].x + s2[0].y) + (s2[1].x + s2[1].y)) + ((s2[2].x + s2[2].y) + (s2[3].x + s2[3].y));
+            const int k = parts & 1;
+            if (half == 1) {
+                if (parts >= 2 && !(ok = mbar_wait_warp(smem_u32(&bar_sum_free[k]), (parts / 2 - 1) & 1, w, SITE_PAGED_O_FULL))) break;
+                s_sum[k][key] = sum;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bar_sum_full[k]));
+            } else {
+                if (!(ok = mbar_wait_warp(smem_u32(&bar_sum_full[k]), (parts / 2) & 1, w, SITE_PAGED_O_FULL))) break;
+                const float other = s_sum[k][key];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bar_sum_free[k]));
+                weight_put(a, p, key, sum + other, old);
+            }
+            ++parts;
         }
     }
 
