@@ -83,8 +83,63 @@ struct WarpSums {
     }
 };
 
+// The offset of sequence b behind the cut.
+__device__ __forceinline__ void put_offset(const EvictArgs& a, int b) {
+    bool bad;
+    const EvictSeq q = evict_seq(a, b, bad);
+    a.off_out[b] = q.off + q.n - q.m;
+}
+
+// Moves of row x: a CTA of THREADS, the y-th of ny for it.  Four moves of a thread at a time: lists, table and
+// rows are a chain of three loads.
+template <int THREADS, typename L>
+__device__ __forceinline__ void move_rows(const EvictArgs& a, int x, int moves, const L* src, const L* dst, int y, int ny) {
+    const int tid = threadIdx.x;
+    const int h = x % a.Hkv, b = x / a.Hkv % a.B, l = x / a.Hkv / a.B;
+    const int R = THREADS >> a.row_shift;                  // moves per pass of the CTA
+    const int* row = a.table + (size_t)b * a.W;
+    const int mask = (1 << a.ps_shift) - 1;
+    const long long base = l * a.layer_stride + h * a.head_stride + (tid & (a.row_vecs - 1)) * 16;
+    for (int j0 = y * kMoves * R + (tid >> a.row_shift); j0 < moves; j0 += ny * kMoves * R) {
+        int s[kMoves], d[kMoves];
+        uint4 k[kMoves], v[kMoves];
+        long long from[kMoves], to[kMoves];
+#pragma unroll
+        for (int i = 0; i < kMoves; ++i) {
+            const bool in = j0 + i * R < moves;
+            s[i] = in ? (int)src[j0 + i * R] : -1;
+            d[i] = in ? (int)dst[j0 + i * R] : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < kMoves; ++i) {
+            from[i] = to[i] = -1;
+            if (s[i] < 0) continue;
+            const int ps = __ldg(row + (s[i] >> a.ps_shift)), pd = __ldg(row + (d[i] >> a.ps_shift));
+            if ((unsigned)ps >= (unsigned)a.n_pages || (unsigned)pd >= (unsigned)a.n_pages) {
+                report_error(a.err, SITE_PAGED_PAGE);
+                continue;
+            }
+            from[i] = base + ps * a.page_stride + (s[i] & mask) * a.tok_stride;
+            to[i] = base + pd * a.page_stride + (d[i] & mask) * a.tok_stride;
+        }
+#pragma unroll
+        for (int i = 0; i < kMoves; ++i)
+            if (from[i] >= 0) {
+                k[i] = *reinterpret_cast<const uint4*>(a.k + from[i]);
+                v[i] = *reinterpret_cast<const uint4*>(a.v + from[i]);
+            }
+#pragma unroll
+        for (int i = 0; i < kMoves; ++i)
+            if (from[i] >= 0) {
+                *reinterpret_cast<uint4*>(a.k + to[i]) = k[i];
+                *reinterpret_cast<uint4*>(a.v + to[i]) = v[i];
+            }
+    }
+}
+
 // THREADS x KPT >= T: warp w holds slots 32 KPT w .., lane l of it slots 4 l .. 4 l + 3 of every 128.
-template <int THREADS, int KPT, int BITS>
+// MOVE: the CTA moves its row's keys and values itself.
+template <int THREADS, int KPT, int BITS, bool MOVE>
 __global__ void __launch_bounds__(THREADS) evict_rows_kernel(const EvictArgs a) {
     constexpr int W = THREADS / 32, Q = KPT / 4, BINS = 1 << BITS, BPT = BINS / THREADS;
     static_assert(BPT >= 1 && KPT <= 32, "bins per thread, slots per mask");
@@ -93,6 +148,7 @@ __global__ void __launch_bounds__(THREADS) evict_rows_kernel(const EvictArgs a) 
     __shared__ int2 s_min[2][W];
     __shared__ int s_digit, s_rest, s_left, s_n;
     __shared__ __align__(4) uint16_t s_hole[THREADS * KPT / 2];   // targets in order; before that, keys
+    __shared__ uint16_t s_src[MOVE ? THREADS * KPT / 2 : 1];      // sources
     uint32_t* const s_key = reinterpret_cast<uint32_t*>(s_hole);
     static_assert(KPT >= 4, "a key per thread fits");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -307,7 +363,8 @@ __global__ void __launch_bounds__(THREADS) evict_rows_kernel(const EvictArgs a) 
             for (int k = 0; k < 4; ++k)
                 if (hole >> (4 * i + k) & 1u) {
                     s_hole[at] = (uint16_t)slot(4 * i + k);
-                    dst[at++] = slot(4 * i + k);
+                    if (!MOVE) dst[at] = slot(4 * i + k);
+                    ++at;
                 }
         }
         if (g0 + 128 > m && g0 < n) {
@@ -332,7 +389,9 @@ __global__ void __launch_bounds__(THREADS) evict_rows_kernel(const EvictArgs a) 
         for (int k = 0; k < 4; ++k)
             if (move >> (4 * i + k) & 1u) {
                 const int d = s_hole[at];
-                src[at++] = s4 + k;
+                if (MOVE) s_src[at] = (uint16_t)(s4 + k);
+                else src[at] = s4 + k;
+                ++at;
                 w_out[d] = w[4 * i + k];
                 pos_out[d] = pos[4 * i + k];
             }
@@ -356,7 +415,13 @@ __global__ void __launch_bounds__(THREADS) evict_rows_kernel(const EvictArgs a) 
             }
         }
     }
-    if (tid == 0) a.moves[x] = moves;
+    if constexpr (MOVE) {
+        if (x < a.Hkv * a.B && x % a.Hkv == 0 && tid == 0 && a.off != a.off_out) a.off_out[b] = q.off + n - m;
+        __syncthreads();                                   // the sources are there
+        move_rows<THREADS>(a, x, moves, s_src, s_hole, 0, 1);
+    } else if (tid == 0) {
+        a.moves[x] = moves;
+    }
 }
 
 // CACHED: the row's keys and guard bits fit into shared memory; otherwise they are formed again
@@ -530,60 +595,21 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictArgs 
 
 // Block (x, y): moves y kMoves R .. of row x, then gridDim.y blocks further on; a 16-byte unit of K and of V
 // per thread and move.
-__global__ void __launch_bounds__(kMoveThreads, 8) evict_move_kernel(const EvictArgs a) {
-    const int x = blockIdx.x, tid = threadIdx.x;
+__global__ void __launch_bounds__(kMoveThreads, 6) evict_move_kernel(const EvictArgs a) {
+    const int x = blockIdx.x;
     griddep_launch_dependents();
     griddep_wait();
-    const int h = x % a.Hkv, b = x / a.Hkv % a.B, l = x / a.Hkv / a.B;
-    if (h == 0 && l == 0 && blockIdx.y == 0 && tid == 0) {
-        bool bad;
-        const EvictSeq q = evict_seq(a, b, bad);
-        a.off_out[b] = q.off + q.n - q.m;
-    }
-    const int moves = a.moves[x];
-    const int R = kMoveThreads >> a.row_shift;             // moves per pass of the block
-    const int u = (tid & (a.row_vecs - 1)) * 16;
+    if (x < a.Hkv * a.B && x % a.Hkv == 0 && blockIdx.y == 0 && threadIdx.x == 0) put_offset(a, x / a.Hkv);
     const int* dst = a.list + (size_t)x * a.T;
-    const int* src = dst + (a.T >> 1);
-    const int* row = a.table + (size_t)b * a.W;
-    const int mask = (1 << a.ps_shift) - 1;
-    const long long base = l * a.layer_stride + h * a.head_stride + u;
-    // Four moves at a time: lists, table and rows are a chain of three loads.
-    for (int j0 = (blockIdx.y * kMoves) * R + (tid >> a.row_shift); j0 < moves; j0 += gridDim.y * kMoves * R) {
-        int s[kMoves], d[kMoves];
-        uint4 k[kMoves], v[kMoves];
-        long long from[kMoves], to[kMoves];
-#pragma unroll
-        for (int i = 0; i < kMoves; ++i) {
-            const bool in = j0 + i * R < moves;
-            s[i] = in ? src[j0 + i * R] : -1;
-            d[i] = in ? dst[j0 + i * R] : -1;
-        }
-#pragma unroll
-        for (int i = 0; i < kMoves; ++i) {
-            from[i] = to[i] = -1;
-            if (s[i] < 0) continue;
-            const int ps = __ldg(row + (s[i] >> a.ps_shift)), pd = __ldg(row + (d[i] >> a.ps_shift));
-            if ((unsigned)ps >= (unsigned)a.n_pages || (unsigned)pd >= (unsigned)a.n_pages) {
-                report_error(a.err, SITE_PAGED_PAGE);
-                continue;
-            }
-            from[i] = base + ps * a.page_stride + (s[i] & mask) * a.tok_stride;
-            to[i] = base + pd * a.page_stride + (d[i] & mask) * a.tok_stride;
-        }
-#pragma unroll
-        for (int i = 0; i < kMoves; ++i)
-            if (from[i] >= 0) {
-                k[i] = *reinterpret_cast<const uint4*>(a.k + from[i]);
-                v[i] = *reinterpret_cast<const uint4*>(a.v + from[i]);
-            }
-#pragma unroll
-        for (int i = 0; i < kMoves; ++i)
-            if (from[i] >= 0) {
-                *reinterpret_cast<uint4*>(a.k + to[i]) = k[i];
-                *reinterpret_cast<uint4*>(a.v + to[i]) = v[i];
-            }
-    }
+    move_rows<kMoveThreads>(a, x, a.moves[x], dst + (a.T >> 1), dst, blockIdx.y, gridDim.y);
+}
+
+// pos_offset_out in its input's place: behind the kernel whose rows all read it.
+__global__ void evict_offset_kernel(const EvictArgs a) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int b = blockIdx.x * blockDim.x + threadIdx.x;
+    if (b < a.B) put_offset(a, b);
 }
 
 }  // namespace
@@ -594,15 +620,19 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st) {
     const size_t bytes = (size_t)a.T * 4 + ((size_t)a.T + 31) / 32 * 4;
     cudaError_t e;
     if (a.T <= 1024) {
-        e = launch_k(evict_rows_kernel<128, 8, 8>, dim3(rows), dim3(128), 0, st, a);
+        // Up to 512 moves per row: a launch for them costs more than it spreads (16 layers x 16 sequences of
+        // 513 slots, one given up each: 7.5 us with, 6.3 without).
+        e = launch_k(evict_rows_kernel<128, 8, 8, true>, dim3(rows), dim3(128), 0, st, a);
+        if (e != cudaSuccess || a.off != a.off_out) return e;
+        return launch_k(evict_offset_kernel, dim3((a.B + 255) / 256), dim3(256), 0, st, a);
     } else if (a.T <= 2048) {
-        e = launch_k(evict_rows_kernel<256, 8, 8>, dim3(rows), dim3(256), 0, st, a);
+        e = launch_k(evict_rows_kernel<256, 8, 8, false>, dim3(rows), dim3(256), 0, st, a);
     } else if (a.T <= 4096) {
-        e = launch_k(evict_rows_kernel<512, 8, 11>, dim3(rows), dim3(512), 0, st, a);
+        e = launch_k(evict_rows_kernel<512, 8, 11, false>, dim3(rows), dim3(512), 0, st, a);
     } else if (a.T <= 8192) {
-        e = launch_k(evict_rows_kernel<1024, 8, 11>, dim3(rows), dim3(1024), 0, st, a);
+        e = launch_k(evict_rows_kernel<1024, 8, 11, false>, dim3(rows), dim3(1024), 0, st, a);
     } else if (a.T <= 16384) {
-        e = launch_k(evict_rows_kernel<1024, 16, 11>, dim3(rows), dim3(1024), 0, st, a);
+        e = launch_k(evict_rows_kernel<1024, 16, 11, false>, dim3(rows), dim3(1024), 0, st, a);
     } else if (bytes <= 200 * 1024) {
         static std::atomic<uint64_t> done{0};
         if ((e = allow_smem(evict_select_kernel<true>, 200 * 1024, done)) != cudaSuccess) return e;
