@@ -644,16 +644,15 @@ def paged_weights(q, lse, k_pages, page_table, seq_lens, weights=None, cu_new=No
     shape = (B, Hkv, W * k_pages.shape[1])
     if weights_out is None:
         weights_out = q.new_zeros(shape, dtype=_F32)
-    for t, name in ((weights, "weights"), (weights_out, "weights_out")):
-        if t is not None and (t.shape != shape or t.dtype is not _F32 or t.get_device() != dev or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous fp32 CUDA tensor {list(shape)} on the pages' device")
+    op = _rows_of(weights_out, _F32, shape, dev, "weights_out")
+    wp = 0 if weights is None else op if weights is weights_out else _rows_of(weights, _F32, shape, dev, "weights")
     new = 1 if cu_new is None else max(1, N) if max_new is None else max_new
     if workspace is not None:
         ws = _ws(workspace, dev)
     else:                                                  # (few rows need none)
         ws = _ws(alloc_weights_workspace(k_pages.device), dev) if min(new, N) * (Hq // Hkv) > 32 else (0, 0)
     _launch(lib.ne_paged_weights if dt is _BF16 else lib.ne_paged_weights_f32, dev, q.data_ptr(), lse.data_ptr(), c, pt, ln, cu,
-            0 if weights is None else weights.data_ptr(), weights_out.data_ptr(), q_ld, B, N, Hq, W, new, *ws)
+            wp, op, q_ld, B, N, Hq, W, new, *ws)
     return weights_out
 
 
@@ -755,11 +754,11 @@ def alloc_evict_workspace(layers: int, B: int, Hkv: int, T: int, device="cuda"):
                        device=device)
 
 
-def _out_like(t, like, dev, name):
-    """Address of a contiguous output with the shape and dtype of `like`."""
-    if t.dtype is not like.dtype or t.shape != like.shape or t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {like.dtype} CUDA tensor {list(like.shape)} on the pages' device")
-    return t.data_ptr()
+def _rows_of(t, dtype, shape, dev, name):
+    """Address of a contiguous tensor of that dtype and shape."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor {list(shape)} on the pages' device")
 
 
 def pages_evict(weights, positions, pos_offset, page_table, seq_lens, new_lens, k_pages, v_pages, sink: int = 0,
@@ -774,24 +773,28 @@ def pages_evict(weights, positions, pos_offset, page_table, seq_lens, new_lens, 
     paged_append takes pos_offset_out."""
     lib = _lib or load()
     c, dev, _, _, Hkv, _ = _paged_cache(k_pages, v_pages, True)
-    if page_table.dim() != 2:
+    T2 = page_table.shape
+    if len(T2) != 2:
         raise ValueError("page_table must be [B, max_pages]")
-    B, W = page_table.shape
-    lead = tuple(k_pages.shape[:-4])
-    T = W * k_pages.shape[-3]
-    _c_ints(sequences=B, max_pages=W, T=T, sink=sink, recent=recent)
-    for t, dt, name in ((weights, _F32, "weights"), (positions, _I32, "positions")):
-        if t.dtype is not dt or t.shape != (*lead, B, Hkv, T) or t.get_device() != dev or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {dt} CUDA tensor {[*lead, B, Hkv, T]} on the pages' device")
-    weights_out = torch.zeros_like(weights) if weights_out is None else weights_out
-    positions_out = torch.full_like(positions, -1) if positions_out is None else positions_out
+    B, W = T2
+    pool = k_pages.shape
+    T = W * pool[-3]
+    if (B | W | T) > _INT_MAX or not 0 <= sink <= _INT_MAX or not 0 <= recent <= _INT_MAX:
+        _c_ints(sequences=B, max_pages=W, T=T, sink=sink, recent=recent)
+    shape = (B, Hkv, T) if len(pool) == 4 else (pool[0], B, Hkv, T)
+    wp, pp = _rows_of(weights, _F32, shape, dev, "weights"), _rows_of(positions, _I32, shape, dev, "positions")
+    if weights_out is None:
+        weights_out = torch.zeros_like(weights)
+    if positions_out is None:
+        positions_out = torch.full_like(positions, -1)
     pos_offset_out, po = _out_ints(pos_offset_out, (B,), dev, "pos_offset_out", page_table)
     if workspace is None:
-        workspace = alloc_evict_workspace(lead[0] if lead else 1, B, Hkv, T, k_pages.device)
-    _launch(lib.ne_pages_evict, dev, c, weights.data_ptr(), positions.data_ptr(), _ints(pos_offset, (B,), dev, "pos_offset"),
-            _ints(page_table, (B, W), dev, "page_table"), _ints(seq_lens, (B,), dev, "seq_lens"),
-            _ints(new_lens, (B,), dev, "new_lens"), sink, recent, _out_like(weights_out, weights, dev, "weights_out"),
-            _out_like(positions_out, positions, dev, "positions_out"), po, B, W, *_ws(workspace, dev))
+        workspace = alloc_evict_workspace(1 if len(pool) == 4 else pool[0], B, Hkv, T, k_pages.device)
+    _launch(lib.ne_pages_evict, dev, c, wp, pp, _ints(pos_offset, (B,), dev, "pos_offset"), _ints(page_table, T2, dev, "page_table"),
+            _ints(seq_lens, (B,), dev, "seq_lens"), _ints(new_lens, (B,), dev, "new_lens"), sink, recent,
+            wp if weights_out is weights else _rows_of(weights_out, _F32, shape, dev, "weights_out"),
+            pp if positions_out is positions else _rows_of(positions_out, _I32, shape, dev, "positions_out"), po, B, W,
+            *_ws(workspace, dev))
     return weights_out, positions_out, pos_offset_out
 
 

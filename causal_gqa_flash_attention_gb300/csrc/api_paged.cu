@@ -213,6 +213,11 @@ ne_status tile_maps(CUtensorMap* tq, CUtensorMap* tk, CUtensorMap* tv, const ne_
 
 // Bytes of a call's workspace: the largest over the kernels that its head_dim and heads may run.
 size_t attn_ws_bytes(int D, int Hkv, int G) {
+    static thread_local struct {
+        int D, Hkv, G;
+        size_t bytes;
+    } last = {0, 0, 0, 0};                     // (twenty splits to look through: a loop over layers asks for one shape)
+    if (D == last.D && Hkv == last.Hkv && G == last.G) return last.bytes;
     size_t most = 0;
     for (int f32 = 0; f32 < 2; ++f32)
         for (int rows : {1, 2, 4, 5, 8, 9, 16, 17, 32, 33, 1 << 20}) {
@@ -220,7 +225,8 @@ size_t attn_ws_bytes(int D, int Hkv, int G) {
             const ne::PagedKind kind = ne::paged_kind(f32 != 0, D, G, rows);
             most = std::max(most, ne::paged_part_bytes(ne::paged_split(kind, D, Hkv, G, 1 << 30), D));
         }
-    return round_up(most, 256);
+    last = {D, Hkv, G, round_up(most, 256)};
+    return last.bytes;
 }
 
 // Checks of a call of ne_paged_attn but for its workspace.
@@ -277,14 +283,11 @@ ne_status attn_args(ne::PagedAttnArgs* out, ne::PagedKind kind, const void* q, c
     return NE_OK;
 }
 
-ne_status attn_impl(int eb, const void* q, const ne_paged_cache* c, const int* table, const int* lens, const int* cu,
-                    void* o, float* lse, int64_t q_ld, int B, int N, int Hq, int W, int max_new, void* ws,
-                    size_t ws_bytes, ne_stream_t stream) {
-    clear_error();
-    ne_status s = attn_check(eb, q, c, table, lens, cu, o, lse, q_ld, B, N, Hq, W, max_new);
-    if (s != NE_OK || B == 0 || N == 0) return s;
+// The call behind its checks.
+ne_status attn_run(int eb, const void* q, const ne_paged_cache* c, const int* table, const int* lens, const int* cu,
+                   void* o, float* lse, int64_t q_ld, int B, int N, int Hq, int W, int max_new, void* ws, ne_stream_t stream) {
     const int G = Hq / c->Hkv;
-    if ((s = attn_ws_check(ws, ws_bytes, attn_ws_bytes(c->D, c->Hkv, G))) != NE_OK) return s;
+    ne_status s;
     const bool f32 = eb == 4;
     const ne::PagedKind kind = ne::paged_kind(f32, c->D, G, cu ? std::min(max_new, N) : 1);
     ne::PagedAttnArgs a;
@@ -302,6 +305,16 @@ ne_status attn_impl(int eb, const void* q, const ne_paged_cache* c, const int* t
     e = ne::launch_paged_join(f32, c->D, a, st);
     if (e != cudaSuccess) return cuda_fail(e, "paged_attn join launch");
     return NE_OK;
+}
+
+ne_status attn_impl(int eb, const void* q, const ne_paged_cache* c, const int* table, const int* lens, const int* cu,
+                    void* o, float* lse, int64_t q_ld, int B, int N, int Hq, int W, int max_new, void* ws,
+                    size_t ws_bytes, ne_stream_t stream) {
+    clear_error();
+    ne_status s = attn_check(eb, q, c, table, lens, cu, o, lse, q_ld, B, N, Hq, W, max_new);
+    if (s != NE_OK || B == 0 || N == 0) return s;
+    if ((s = attn_ws_check(ws, ws_bytes, attn_ws_bytes(c->D, c->Hkv, Hq / c->Hkv))) != NE_OK) return s;
+    return attn_run(eb, q, c, table, lens, cu, o, lse, q_ld, B, N, Hq, W, max_new, ws, stream);
 }
 
 // ---------------------------------------------------------------- shared prefixes
@@ -347,7 +360,7 @@ ne_status shared_impl(int eb, const void* q, const ne_paged_cache* c, const int*
     const long long bytes = (long long)B * W * c->page_size * c->Hkv * 2 * c->D * eb;
     if (R == 0 || (long long)most * G >= kSharedRows || (!f32 && G > 128) ||
         bytes <= (f32 && (long long)most * G <= 16 ? kSharedBytesF32 : kSharedBytes))
-        return attn_impl(eb, q, c, table, lens, cu, o, lse, q_ld, B, N, Hq, W, max_new, ws, ws_bytes, stream);
+        return attn_run(eb, q, c, table, lens, cu, o, lse, q_ld, B, N, Hq, W, max_new, ws, stream);
     // bf16: one line of prefixes and own positions, tiles for all.  fp32: a line and a kernel for each,
     // chosen by the rows of a group and of a sequence.
     const int lines = f32 ? 2 : 1;

@@ -155,6 +155,25 @@ def test_fresh_outputs_and_one_layer_pools():
     assert np.array_equal(k.float().cpu().numpy(), kr)
 
 
+def test_the_binding_refuses():
+    table, w, pos, off, k, v = state([64], [64], 2, 2, 64, 16, BF16, 29)
+    good = [torch.tensor(w).cuda(), i32(pos), i32(off), i32(table), i32([64]), i32([32]), k, v]
+    for kw in (dict(sink=1 << 32), dict(recent=-(1 << 40)), dict(workspace=torch.zeros(256, dtype=torch.uint8)),
+               dict(weights_out=torch.zeros(2, 1, 2, 32, device="cuda")), dict(pos_offset_out=i32([0, 0]))):
+        with pytest.raises(ValueError):
+            ne.pages_evict(*good, **kw)
+    for i, bad in ((0, good[0][:1]), (0, good[0].double()), (1, good[1].long()), (1, good[1].cpu()), (2, i32([0, 0])), (3, good[3][0]), (4, i32([64, 1])),
+                   (6, k[0])):
+        args = list(good)
+        args[i] = bad
+        with pytest.raises(ValueError):
+            ne.pages_evict(*args)
+    for kw in (dict(sink=-1), dict(recent=(1 << 30) + 1), dict(workspace=torch.zeros(256, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(ne.NeError):
+            ne.pages_evict(*good, **kw)
+    ok()
+
+
 def test_nothing_to_do():
     k = torch.zeros(1, 4, 16, 2, 64, dtype=BF16, device="cuda")
     e = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
