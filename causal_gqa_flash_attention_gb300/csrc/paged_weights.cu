@@ -486,7 +486,7 @@ struct ManyCfg {
 
 // A unit holds two tiles of 128 keys, so that a query tile (16 KB at D 64, 32 at D 128; an SM receives some 35
 // bytes a cycle) feeds two products.  Roles (20 warps): 0 producer (keys of a part, then query tiles through
-// the ring), 1 UMMA issuer, 2 the log-sum-exps of every query tile, 3 the CTA's parts, 4-19 the
+// the ring), 1 and 2 UMMA issuers, 3 the CTA's parts and the log-sum-exps of every query tile, 4-19 the
 // exponentials, a thread per key (TMEM lane): warps 4-7 and 12-15 the first 128 keys, the others the second,
 // warps 4-11 the even query tiles, 12-19 the odd ones (a warp's loads and waits need three others' products
 // to fill the exponential units: with all tiles in eight warps 119 us at D 64).  S of key tile
@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(640, 1)
         }
         for (int i = 0; i < C::NS; ++i) {
             mbar_init(smem_u32(&bar_q_full[i]), 1);
-            mbar_init(smem_u32(&bar_q_empty[i]), 1);
+            mbar_init(smem_u32(&bar_q_empty[i]), 2);       // the issuers
         }
         for (int i = 0; i < C::NL; ++i) {
             mbar_init(smem_u32(&bar_l_full[i]), 1);
@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(640, 1)
             mbar_init(smem_u32(&bar_part_full[i]), 1);
             mbar_init(smem_u32(&bar_part_empty[i]), kPartReaders);
         }
-        mbar_init(smem_u32(&bar_final), 1);
+        mbar_init(smem_u32(&bar_final), 2);
         abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tm_q);
@@ -630,56 +630,77 @@ __global__ void __launch_bounds__(640, 1)
             for (int i = max(0, item - C::NS); i < item; ++i)
                 mbar_wait_drain(smem_u32(&bar_q_full[i % C::NS]), (i / C::NS) & 1, w, SITE_PAGED_DRAIN);
         }
-    } else if (warp == 1) {
-        // ------------------------------------------------------------ UMMA issuer
+    } else if (warp < 3) {
+        // ------------------------------------------------------------ UMMA issuer of key tile u
         constexpr uint32_t id_s = idesc_make(FMT_BF16, 128, 128, false, false);
         const uint64_t dk0 = sdesc(smem_u32(sK), 16, 1024), dq0 = sdesc(smem_u32(sQ), 16, 1024);
-        int keys = 0, item = 0, uses[4] = {0, 0, 0, 0};    // uses: of S buffers 2 u + item % 2 so far
+        const int u = warp - 1;
+        int keys = 0, item = 0, uses[2] = {0, 0};          // uses: of S buffers 2 u + item % 2 so far
         bool ok = true;
         while (ok && next_part()) {
             if (p.t0 == p.t1) continue;
-            const int nu = p.kt * 256 + 128 < p.len ? 2 : 1;
-            for (int u = 0; ok && u < nu; ++u)
-                ok = mbar_wait_warp(smem_u32(&bar_k_full[(keys + u) % C::NK]), ((keys + u) / C::NK) & 1, w, SITE_PAGED_KV_FULL);
-            if (!ok) break;
-            for (int t = p.t0; ok && t < p.t1; ++t, ++item) {
-                const int i = item % C::NS, odd = item & 1;
+            const int nu = p.kt * 256 + 128 < p.len ? 2 : 1, kslot = (keys + u) % C::NK;
+            const bool mine = u < nu;
+            if (mine && !(ok = mbar_wait_warp(smem_u32(&bar_k_full[kslot]), ((keys + u) / C::NK) & 1, w, SITE_PAGED_KV_FULL))) break;
+            const uint64_t dk = sdesc_add(dk0, kslot * C::TILE);
+            for (int t = p.t0; t < p.t1; ++t, ++item) {
+                const int i = item % C::NS, odd = item & 1, s = 2 * u + odd;
                 if (!(ok = mbar_wait_warp(smem_u32(&bar_q_full[i]), (item / C::NS) & 1, w, SITE_PAGED_Q))) break;
-                const uint64_t dq = sdesc_add(dq0, i * C::TILE);
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    if (u >= nu) break;
-                    const int s = 2 * u + odd, n = odd ? uses[2 * u + 1]++ : uses[2 * u]++;
-                    if (n >= 1 && !(ok = mbar_wait_warp(smem_u32(&bar_s_free[s]), (n - 1) & 1, w, SITE_PAGED_S_FULL))) break;
-                    tc_fence_after();
-                    const uint64_t dk = sdesc_add(dk0, (keys + u) % C::NK * C::TILE);
-                    if (elect_one()) {
-#pragma unroll
-                        for (int ks = 0; ks < D / 16; ++ks) {
-                            const uint32_t off = ((ks * 32) >> 7) * C::CHUNK + ((ks * 32) & 127);
-                            umma_ss<false>(tm + s * 128, sdesc_add(dk, off), sdesc_add(dq, off), id_s, ks > 0);
-                        }
-                        umma_commit(smem_u32(&bar_s_full[s]));
-                        if (t + 1 == p.t1) umma_commit(smem_u32(&bar_k_empty[(keys + u) % C::NK]));
-                        if (u == nu - 1) umma_commit(smem_u32(&bar_q_empty[i]));
-                    }
+                if (!mine) {
+                    if (lane == 0) mbar_arrive(smem_u32(&bar_q_empty[i]));
                     __syncwarp();
+                    continue;
                 }
+                const int n = odd ? uses[1]++ : uses[0]++;
+                if (n >= 1 && !(ok = mbar_wait_warp(smem_u32(&bar_s_free[s]), (n - 1) & 1, w, SITE_PAGED_S_FULL))) break;
+                tc_fence_after();
+                const uint64_t dq = sdesc_add(dq0, i * C::TILE);
+                if (elect_one()) {
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        const uint32_t off = ((ks * 32) >> 7) * C::CHUNK + ((ks * 32) & 127);
+                        umma_ss<false>(tm + s * 128, sdesc_add(dk, off), sdesc_add(dq, off), id_s, ks > 0);
+                    }
+                    umma_commit(smem_u32(&bar_s_full[s]));
+                    umma_commit(smem_u32(&bar_q_empty[i]));
+                    if (t + 1 == p.t1) umma_commit(smem_u32(&bar_k_empty[kslot]));
+                }
+                __syncwarp();
             }
             keys += nu;
         }
         umma_commit_e(smem_u32(&bar_final));
-    } else if (warp == 2) {
-        // ------------------------------------------------------------ log-sum-exps
+    } else if (warp == 3) {
+        // ------------------------------------------------------------ the CTA's parts, and their log-sum-exps
         int tk[4], hd[4];                                  // token and head of rows lane, lane + 32, ... of a tile
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             tk[k] = (lane + 32 * k) / a.gs;
             hd[k] = (lane + 32 * k) % a.gs;
         }
-        int item = 0;
-        bool ok = true;
-        while (ok && next_part()) {
+        if (lane < 2) a.part_info[blockIdx.x * 2 + lane] = make_int4(0, 0, 0, 0);
+        __syncwarp();                                      // both in front of lane 0's arrivals, and so of any record
+        // Part k + 1 is queued before the log-sum-exps of part k, which wait for the exponentials.
+        int queued = 0, item = 0;
+        bool more = true, ok = true;
+        auto queue = [&](WeightPart& q) -> bool {
+            const int s = queued % kParts;
+            more = walk.next(a, q);
+            if (!more) q.b = -1;
+            if (queued >= kParts && !mbar_wait_warp(smem_u32(&bar_part_empty[s]), (queued / kParts - 1) & 1, w, SITE_PAGED_SEG)) return false;
+            if (lane == 0) {
+                s_part[s] = q;
+                mbar_arrive(smem_u32(&bar_part_full[s]));
+            }
+            __syncwarp();
+            ++queued;
+            return true;
+        };
+        WeightPart ahead;
+        ok = queue(ahead);
+        while (ok && ahead.b >= 0) {
+            p = ahead;
+            if (!(ok = queue(ahead))) break;
             int tg = p.t0 / a.ngrp, th = p.t0 - tg * a.ngrp;
             const float* lse = a.lse + (long long)p.tok0 * a.Hq + p.h * a.G;
             for (int t0 = p.t0; ok && t0 < p.t1; t0 += 4) {   // four tiles' loads at a time: one by one their latency bounds all
@@ -712,22 +733,6 @@ __global__ void __launch_bounds__(640, 1)
                     ++item;
                 }
             }
-        }
-    } else if (warp == 3) {
-        // ------------------------------------------------------------ the CTA's parts
-        if (lane < 2) a.part_info[blockIdx.x * 2 + lane] = make_int4(0, 0, 0, 0);
-        __syncwarp();                                      // both in front of lane 0's arrivals, and so of any record
-        bool more = true;
-        for (int k = 0; more; ++k) {
-            const int s = k % kParts;
-            more = walk.next(a, p);
-            if (!more) p.b = -1;
-            if (k >= kParts && !mbar_wait_warp(smem_u32(&bar_part_empty[s]), (k / kParts - 1) & 1, w, SITE_PAGED_SEG)) break;
-            if (lane == 0) {
-                s_part[s] = p;
-                mbar_arrive(smem_u32(&bar_part_full[s]));
-            }
-            __syncwarp();
         }
     } else {
         // ------------------------------------------------------------ exponentials
