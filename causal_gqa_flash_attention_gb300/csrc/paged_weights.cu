@@ -16,6 +16,17 @@
 // that see it; a share cuts units between query tiles, cut units' sums are added by a join.
 // Many rows, fp32: units of 128 keys on fp32 FMAs, two keys per lane in registers, the query rows
 // broadcast from shared memory.
+//
+// Measured (GB300): one token over 8 x 16384 positions, 12/4 heads of 64: 17.1 us, 4.2 TB/s (10.6 at the copy
+// rate; 3.7 to begin and find the shares, then 5.3 TB/s); the small fp32 step 3.8.  2048 tokens over 16384
+// positions, 16/4 heads of 128: 110 us, 1.17 PFLOP/s (61% of the bf16 GEMM); of 64: 105 us, 0.61 PFLOP/s, the
+// exponential units 62% busy: the four warps of a scheduler wait for S and begin tiles together.  Twelve
+// sequences, single tokens beside chunks up to 512 over up to 4096: 22 us (2.0), 9 before the first product,
+// then 5 query tiles in 3 parts per CTA, then the join.
+// Tried for many rows and left out: part of the exponentials as a polynomial on the FMA pipes (D 64 119 -> 144
+// us, then with eight exponential warps), keys as the TMEM operand with 96-row query tiles (D 128 120 ->
+// 138: it is the issue of products, some 90 cycles each, that counts), S in halves with buffers of their own
+// (D 64 105 -> 113), all 128 columns of S in registers at once (119 -> 133).
 #include <cuda_bf16.h>
 #include <type_traits>
 #include "paged_line.cuh"
@@ -488,8 +499,9 @@ struct ManyCfg {
 // bytes a cycle) feeds two products.  Roles (20 warps): 0 producer (keys of a part, then query tiles through
 // the ring), 1 and 2 UMMA issuers, 3 the CTA's parts and the log-sum-exps of every query tile, 4-19 the
 // exponentials, a thread per key (TMEM lane): warps 4-7 and 12-15 the first 128 keys, the others the second,
-// warps 4-11 the even query tiles, 12-19 the odd ones (a warp's loads and waits need three others' products
-// to fill the exponential units: with all tiles in eight warps 119 us at D 64).  S of key tile
+// warps 4-11 the even query tiles, 12-19 the odd ones (a warp's loads and waits need others' products to fill
+// the exponential units: with all tiles in eight warps 119 us at D 64 instead of 105; one issuer for both key
+// tiles 120 at D 128 instead of 110).  S of key tile
 // u and query tile i lies in TMEM columns 256 u + 128 (i % 2).  Dead rows of a query tile: those that TMA never
 // writes are zero and their lse entry -inf; those that hold other sequences' rows are masked where they occur.
 template <int D>

@@ -1,9 +1,9 @@
 """A model of the barrier protocol of the accumulated-weights kernel for many rows (weights_many_kernel of
 csrc/paged_weights.cu), run on the CPU over random lists of parts.
 
-Roles: the part finder, the TMA producer (keys of a part, then query tiles through a ring), the UMMA issuer,
-the log-sum-exp warp (a ring of its own), and four groups of exponential warps: key tile u, query tiles of
-one parity.  Each role is a coroutine of its waits and arrivals (a group arrives as one; products and
+Roles: the part finder, which also loads the log-sum-exps (a ring of their own; part k + 1 is queued before
+those of part k), the TMA producer (keys of a part, then query tiles through a ring), a UMMA issuer per key
+tile, and four groups of exponential warps: key tile u, query tiles of one parity.  Each role is a coroutine of its waits and arrivals (a group arrives as one; products and
 copies complete at once).  A run fails on a deadlock, on parity aliasing, or on an arrival that lands in
 another phase.  Kept in step with the kernel by hand.
 """
@@ -42,18 +42,29 @@ def simulate(parts, NK, NS, NL, rng, follow_absent_keys=True):
         return bars.setdefault(name, Bar(name, count))
 
     k_full, k_empty = [bar(f"k_full{i}") for i in range(NK)], [bar(f"k_empty{i}") for i in range(NK)]
-    q_full, q_empty = [bar(f"q_full{i}") for i in range(NS)], [bar(f"q_empty{i}") for i in range(NS)]
+    q_full, q_empty = [bar(f"q_full{i}") for i in range(NS)], [bar(f"q_empty{i}", 2) for i in range(NS)]
     l_full, l_empty = [bar(f"l_full{i}") for i in range(NL)], [bar(f"l_empty{i}", 2) for i in range(NL)]
     s_full, s_free = [bar(f"s_full{i}") for i in range(4)], [bar(f"s_free{i}") for i in range(4)]
+    # Seven read the parts: the producer, the issuers and the exponentials.
     part_full, part_empty = [bar(f"part_full{i}") for i in range(PARTS)], [bar(f"part_empty{i}", 7) for i in range(PARTS)]
     sum_full, sum_free = [bar(f"sum_full{i}", 2) for i in range(2)], [bar(f"sum_free{i}", 2) for i in range(2)]
     done = []
 
     def finder():
-        for k in range(len(parts) + 1):                     # (the last: the end)
+        def queue(k):                                       # (the last: the end)
             if k >= PARTS:
                 yield part_empty[k % PARTS], k // PARTS - 1, f"finder: part {k}"
             part_full[k % PARTS].arrive(k // PARTS)
+
+        yield from queue(0)
+        item = 0
+        for k, (_, n) in enumerate(parts):
+            yield from queue(k + 1)
+            for _ in range(n):
+                if item >= NL:
+                    yield l_empty[item % NL], item // NL - 1, f"finder: lse {item}"
+                l_full[item % NL].arrive(item // NL)
+                item += 1
 
     def each_part(name):
         for k in range(len(parts) + 1):
@@ -73,9 +84,8 @@ def simulate(parts, NK, NS, NL, rng, follow_absent_keys=True):
     class State:
         pass
 
-    p, i, e = State(), State(), State()
-    p.keys = p.item = i.keys = i.item = e.item = 0
-    i.uses = [0] * 4
+    p = State()
+    p.keys = p.item = 0
 
     def producer(k, nu, n):
         if n == 0:
@@ -91,33 +101,32 @@ def simulate(parts, NK, NS, NL, rng, follow_absent_keys=True):
             q_full[p.item % NS].arrive(p.item // NS)
             p.item += 1
 
-    def issuer(k, nu, n):
-        if n == 0:
-            return
-        for u in range(nu):
-            yield k_full[(i.keys + u) % NK], (i.keys + u) // NK, f"issuer: keys {i.keys + u}"
-        for t in range(n):
-            odd = i.item & 1
-            yield q_full[i.item % NS], i.item // NS, f"issuer: query tile {i.item}"
-            for u in range(nu):
-                s = 2 * u + odd
-                if i.uses[s] >= 1:
-                    yield s_free[s], i.uses[s] - 1, f"issuer: S {s}"
-                s_full[s].arrive(i.uses[s])
-                i.uses[s] += 1
-                if t + 1 == n:
-                    k_empty[(i.keys + u) % NK].arrive((i.keys + u) // NK)
-                if u == nu - 1:
-                    q_empty[i.item % NS].arrive(i.item // NS)
-            i.item += 1
-        i.keys += nu
+    def issuer(u):
+        st = State()
+        st.keys = st.item = 0
+        st.uses = [0, 0]
 
-    def lse(k, nu, n):
-        for _ in range(n):
-            if e.item >= NL:
-                yield l_empty[e.item % NL], e.item // NL - 1, f"lse: tile {e.item}"
-            l_full[e.item % NL].arrive(e.item // NL)
-            e.item += 1
+        def body(k, nu, n):
+            if n == 0:
+                return
+            ks = st.keys + u
+            if u < nu:
+                yield k_full[ks % NK], ks // NK, f"issuer {u}: keys {ks}"
+            for t in range(n):
+                it, odd = st.item, st.item & 1
+                yield q_full[it % NS], it // NS, f"issuer {u}: query tile {it}"
+                if u < nu:
+                    s = 2 * u + odd
+                    if st.uses[odd] >= 1:
+                        yield s_free[s], st.uses[odd] - 1, f"issuer {u}: S {s}"
+                    s_full[s].arrive(st.uses[odd])
+                    st.uses[odd] += 1
+                    if t + 1 == n:
+                        k_empty[ks % NK].arrive(ks // NK)
+                q_empty[it % NS].arrive(it // NS)
+                st.item += 1
+            st.keys += nu
+        return body
 
     def exps(u, half):
         st = State()
@@ -145,8 +154,9 @@ def simulate(parts, NK, NS, NL, rng, follow_absent_keys=True):
                 sum_free[k & 1].arrive(k // 2)
         return body
 
-    roles = {"finder": finder(), "producer": role("producer", producer), "issuer": role("issuer", issuer), "lse": role("lse", lse)}
+    roles = {"finder": finder(), "producer": role("producer", producer)}
     for u in range(2):
+        roles[f"issuer{u}"] = role(f"issuer{u}", issuer(u))
         for half in range(2):
             roles[f"exps{u}{half}"] = role(f"exps{u}{half}", exps(u, half))
     pending = {}
