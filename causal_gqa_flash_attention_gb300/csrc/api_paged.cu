@@ -349,7 +349,8 @@ ne_status shared_impl(int eb, const void* q, const ne_paged_cache* c, const int*
     clear_error();
     ne_status s = attn_check(eb, q, c, table, lens, cu, o, lse, q_ld, B, N, Hq, W, max_new);
     if (s != NE_OK) return s;
-    if (R < 0 || R > B) return fail(NE_ERR_INVALID_ARG, "need 0 <= R <= B groups (R=%d B=%d)", R, B);
+    if (R < 0 || R > B || (long long)R + B >= (1LL << 31))
+        return fail(NE_ERR_INVALID_ARG, "need 0 <= R <= B groups and R + B < 2^31 (R=%d B=%d)", R, B);
     if (B == 0 || N == 0) return NE_OK;
     if (!aligned4(groups) || (R > 0 && !aligned4(shared)))
         return fail(NE_ERR_INVALID_ARG, "groups and shared must be non-null, 4-byte aligned device pointers");
