@@ -63,12 +63,14 @@ __global__ void __launch_bounds__(F32Cfg<D, RW, MANY>::THREADS, F32Cfg<D, RW, MA
     griddep_wait();
     PagedWalkOf<SH> walk;
     __shared__ PagedGroups groups;                         // (SH)
+    PagedRaw raw = {};                                     // (SH) on its way while the groups are read
     if constexpr (SH) {
+        raw = paged_shared_raw(a.s, tid);
         paged_load_groups(a.s, groups);
         __syncthreads();
     }
     walk.gs = &groups;
-    paged_locate<C::THREADS, SH>(a, blockIdx.x, loc, blockIdx.x == 0, &groups);
+    paged_locate<C::THREADS, SH>(a, blockIdx.x, loc, blockIdx.x == 0, &groups, &raw);
     if constexpr (SH) walk.q = loc.q;
     walk.init(a, loc.w0, loc.w1, loc.snap, loc.b, loc.start, SH);
     if (tid < 2) a.part_info[blockIdx.x * 2 + tid] = make_int4(0, 0, 0, 0);

@@ -66,4 +66,45 @@ __device__ __forceinline__ void line_find(Line<T>& s, int B, const F& cost, long
     }
 }
 
+// Share c of C of a line, inv = line_inv(C): from x0 up to x1.
+__host__ __device__ constexpr unsigned long long line_inv(int C) { return C > 1 ? ~0ull / (unsigned)C + 1 : 0; }
+__device__ __forceinline__ void line_share(long long total, int c, int C, unsigned long long inv, long long& x0, long long& x1) {
+    x0 = (long long)__umul64hi((unsigned long long)total, inv * c);
+    x1 = c + 1 == C ? total : (long long)__umul64hi((unsigned long long)total, inv * (c + 1));
+}
+
+// off / S, and what remains in off: an estimate put right (one step off at most below 2^20), as every CTA waits
+// for this and a division in 64 bits takes longer.
+__device__ __forceinline__ int line_head(long long& off, long long S) {
+    int h = (int)__fdividef((float)off, (float)S);
+    off -= h * S;
+    while (off < 0) {
+        --h;
+        off += S;
+    }
+    while (off >= S) {
+        ++h;
+        off -= S;
+    }
+    return h;
+}
+
+// One warp, up to 32 sequences: its share of the line (share(total, x0, x1)), the sequence that holds x0, and
+// where it starts.
+template <typename F, typename G>
+__device__ __forceinline__ void line_warp(int B, const F& cost, const G& share, long long& x0, long long& x1, int& b, long long& start) {
+    const int lane = threadIdx.x & 31;
+    const long long mine = lane < B ? cost(lane) : 0;
+    long long x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    share(__shfl_sync(0xffffffffu, x, 31), x0, x1);
+    const unsigned hit = __ballot_sync(0xffffffffu, x0 < x);
+    b = hit ? __ffs(hit) - 1 : B;
+    start = __shfl_sync(0xffffffffu, x - mine, min(b, 31));
+}
+
 }  // namespace ne

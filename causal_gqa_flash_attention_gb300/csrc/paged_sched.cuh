@@ -114,8 +114,14 @@ __device__ __forceinline__ void paged_load_groups(const PagedBatch& s, PagedGrou
     }
     if (blockIdx.x == 0 && bad) report_error(s.err, bad);
 }
+// What member b of a SHARED line reads of its own sequence (a prefix: nothing).
+__device__ __forceinline__ PagedRaw paged_shared_raw(const PagedBatch& s, int b) {
+    PagedRaw r = {0, 0, 0};
+    if (b >= s.pre && b < s.B) r = paged_raw(s, b - s.pre);
+    return r;
+}
 // Member b of a SHARED line.
-__device__ __forceinline__ PagedSharedSeq paged_shared_seq(const PagedBatch& s, int b, int& bad, const PagedGroups& gs) {
+__device__ __forceinline__ PagedSharedSeq paged_shared_seq(const PagedBatch& s, int b, int& bad, const PagedGroups& gs, const PagedRaw& raw) {
     PagedSharedSeq q;
     const bool near = s.R <= PagedGroups::MAX;
     if (b < s.pre) {
@@ -130,7 +136,6 @@ __device__ __forceinline__ PagedSharedSeq paged_shared_seq(const PagedBatch& s, 
     }
     q.pre = false;
     b -= s.pre;
-    const PagedRaw raw = paged_raw(s, b);
     int lo = -1, hi = s.R - 1;                             // the last group that begins at or before b
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -154,8 +159,9 @@ __device__ __forceinline__ PagedSharedSeq paged_shared_seq(const PagedBatch& s, 
     return q;
 }
 template <bool SH>
-__device__ __forceinline__ typename PagedSeqOf<SH>::type paged_seq_of(const PagedBatch& s, int b, int& bad, const PagedGroups* gs) {
-    if constexpr (SH) return paged_shared_seq(s, b, bad, *gs);
+__device__ __forceinline__ typename PagedSeqOf<SH>::type paged_seq_of(const PagedBatch& s, int b, int& bad, const PagedGroups* gs,
+                                                                      const PagedRaw* raw = nullptr) {
+    if constexpr (SH) return paged_shared_seq(s, b, bad, *gs, raw ? *raw : paged_shared_raw(s, b));
     else return paged_seq(s, b, bad);
 }
 
@@ -247,7 +253,7 @@ struct PagedWalkOf {
     // Sequence b, whose values were fetched ahead.
     __device__ __forceinline__ void take(const PagedAttnArgs& a) {
         int bad = 0;
-        if constexpr (SH) q = paged_shared_seq(a.s, b, bad, *gs);
+        if constexpr (SH) q = paged_seq_of<true>(a.s, b, bad, gs);
         else q = paged_clamp(a.s, ahead, bad);
         nt = paged_tiles(q.n, a.p);
         fetch(a);
@@ -375,16 +381,17 @@ struct PagedLocate {
 
 // All T threads of the CTA: the total work, this CTA's interval, and the sequence that its
 // start falls into.  Two passes over the lengths when they exceed T sequences (the first
-// sums, the second finds), one otherwise.
+// sums, the second finds), one otherwise.  (SHARED: raw is what sequence tid reads, loaded early.)
 template <int T, bool SH = false>
-__device__ __forceinline__ void paged_locate(const PagedAttnArgs& a, int c, PagedLocate& sm, bool report, const PagedGroups* gs = nullptr) {
+__device__ __forceinline__ void paged_locate(const PagedAttnArgs& a, int c, PagedLocate& sm, bool report, const PagedGroups* gs = nullptr,
+                                             const PagedRaw* raw = nullptr) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int B = a.s.B;
     int bad = 0;
     typename PagedSeqOf<SH>::type q = {};
-    auto work = [&](int b) -> long long {
+    auto work = [&](int b, const PagedRaw* r) -> long long {
         if (b >= B) return 0;
-        q = paged_seq_of<SH>(a.s, b, bad, gs);
+        q = paged_seq_of<SH>(a.s, b, bad, gs, r);
         return paged_group_cost(q, a.p) * a.p.hg;
     };
     // Inclusive sums over the CTA; the total in sm.warp_sum[T / 32 - 1].
@@ -408,11 +415,11 @@ __device__ __forceinline__ void paged_locate(const PagedAttnArgs& a, int c, Page
         __syncthreads();
         return x + (warp ? sm.warp_sum[warp - 1] : 0);
     };
-    long long mine = work(tid), incl = scan(mine);
+    long long mine = work(tid, raw), incl = scan(mine);
     long long total = sm.warp_sum[T / 32 - 1];
     for (int b0 = T; b0 < B; b0 += T) {
         __syncthreads();
-        scan(work(b0 + tid));
+        scan(work(b0 + tid, nullptr));
         total += sm.warp_sum[T / 32 - 1];
     }
     if (tid == 0) {
@@ -430,7 +437,7 @@ __device__ __forceinline__ void paged_locate(const PagedAttnArgs& a, int c, Page
         long long before = 0;
         for (int b0 = 0; b0 < B; b0 += T) {
             if (B > T) {
-                mine = work(b0 + tid);
+                mine = work(b0 + tid, nullptr);
                 __syncthreads();
                 incl = scan(mine);
             }
@@ -451,18 +458,19 @@ __device__ __forceinline__ void paged_locate(const PagedAttnArgs& a, int c, Page
 // paged_locate for one warp: the walk of CTA c from its first unit on.  Written for few
 // dependent steps: all CTAs wait for it at the start of a call.
 template <bool SH>
-__device__ __forceinline__ void paged_locate_warp(const PagedAttnArgs& a, int c, PagedWalkOf<SH>& walk, bool report) {
+__device__ __forceinline__ void paged_locate_warp(const PagedAttnArgs& a, int c, PagedWalkOf<SH>& walk, bool report,
+                                                  const PagedRaw* raw = nullptr) {
     const int lane = threadIdx.x & 31, B = a.s.B;
     int bad = 0;
     typename PagedSeqOf<SH>::type q = {};
-    auto work = [&](int b) -> long long {
+    auto work = [&](int b, const PagedRaw* r) -> long long {
         if (b >= B) return 0;
-        q = paged_seq_of<SH>(a.s, b, bad, walk.gs);
+        q = paged_seq_of<SH>(a.s, b, bad, walk.gs, r);
         return paged_group_cost(q, a.p) * a.p.hg;
     };
-    long long mine = work(lane), total = mine;
+    long long mine = work(lane, raw), total = mine;
 #pragma unroll 1
-    for (int b0 = 32; b0 < B; b0 += 32) total += work(b0 + lane);
+    for (int b0 = 32; b0 < B; b0 += 32) total += work(b0 + lane, nullptr);
     // The sum over the warp in three limbs of 21 bits, one reduction each (units times 5 x 2^30
     // keys: below 2^60).
     const unsigned l0 = __reduce_add_sync(0xffffffffu, (unsigned)total & 0x1fffffu);
@@ -474,7 +482,7 @@ __device__ __forceinline__ void paged_locate_warp(const PagedAttnArgs& a, int c,
     int b = 0;
 #pragma unroll 1
     for (int b0 = 0; w0 < w1 && b0 < B; b0 += 32) {
-        if (B > 32) mine = work(b0 + lane);
+        if (B > 32) mine = work(b0 + lane, nullptr);
         long long x = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {

@@ -193,11 +193,13 @@ __global__ void __launch_bounds__(384, 1)
         return g.b >= 0;
     };
     // Where the CTA's share begins, warp 3 finds alone among up to 32 sequences, all warps among more.
+    PagedRaw raw = {};                                     // (SH) on its way while the groups are read
     if constexpr (SH) {
+        raw = paged_shared_raw(a.s, a.s.B > 32 ? tid : lane);
         paged_load_groups(a.s, groups);
         __syncthreads();
     }
-    if (a.s.B > 32) paged_locate<C::THREADS, SH>(a, blockIdx.x, loc, blockIdx.x == 0, &groups);
+    if (a.s.B > 32) paged_locate<C::THREADS, SH>(a, blockIdx.x, loc, blockIdx.x == 0, &groups, &raw);
     // A part's K tile t sits at ring index 2 i, its V tile at 2 i + 1, i counting the CTA's tiles.
     // Zeros for the rows of the V tile at ring index i (keys of tile t) that lie behind the length.
     auto zero_v = [&](int i, int t) {
@@ -412,7 +414,7 @@ __global__ void __launch_bounds__(384, 1)
         __syncwarp();                                      // both in front of lane 0's arrivals, and so of any record
         PagedWalkOf<SH> walk;
         walk.gs = &groups;
-        if (a.s.B <= 32) paged_locate_warp(a, blockIdx.x, walk, blockIdx.x == 0);
+        if (a.s.B <= 32) paged_locate_warp(a, blockIdx.x, walk, blockIdx.x == 0, &raw);
         else {
             if constexpr (SH) walk.q = loc.q;
             walk.init(a, loc.w0, loc.w1, loc.snap, loc.b, loc.start, SH);
@@ -422,8 +424,6 @@ __global__ void __launch_bounds__(384, 1)
             const int s = k % kSegs;
             more = walk.next(a, g);
             if (!more) g.b = -1;
-            if constexpr (SH)
-                if (more) paged_where(a, g, lane, 32);
             if (k >= kSegs &&
                 !mbar_wait_warp(smem_u32(&bar_seg_empty[s]), (k / kSegs - 1) & 1, w, SITE_PAGED_SEG))
                 break;
@@ -432,6 +432,8 @@ __global__ void __launch_bounds__(384, 1)
                 mbar_arrive(smem_u32(&bar_seg_full[s]));
             }
             __syncwarp();
+            if constexpr (SH)
+                if (more) paged_where(a, g, lane, 32);
         }
     } else {
         // ------------------------------------------------------------ softmax of subtile u

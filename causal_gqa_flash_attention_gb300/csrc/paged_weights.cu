@@ -75,8 +75,8 @@ struct StepWalk {
         h = st = 0;
         if (left <= 0) return;
         take(a);
-        h = (int)(off / steps);
-        st = (int)(off - (long long)h * steps);
+        h = line_head(off, steps);
+        st = (int)off;
     }
     // True where the next step is another head's.
     __device__ __forceinline__ bool next(const WeightArgs& a) {
@@ -259,13 +259,19 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<D, RC, F32>::CTAS) weights
         const PagedSeq q = paged_seq(a.s, b, bad);
         return (long long)((q.len + 31) >> 5) * a.Hkv;
     };
-    const long long total = line_total(line, a.s.B, cost);
-    if (blockIdx.x == 0 && bad) report_error(a.err, bad);
-    const int gw = blockIdx.x * kFewWarps + warp, GW = gridDim.x * kFewWarps;
-    const long long x0 = total * gw / GW, x1 = total * (gw + 1) / GW;
+    constexpr int GW = C::CTAS * kWeightCtas * kFewWarps;
+    const auto share = [&](long long total, long long& x0, long long& x1) {
+        line_share(total, blockIdx.x * kFewWarps + warp, GW, line_inv(GW), x0, x1);
+    };
     int b;
-    long long start;
-    line_find(line, a.s.B, cost, x0, b, start);
+    long long x0, x1, start;
+    if (a.s.B <= 32) {
+        line_warp(a.s.B, cost, share, x0, x1, b, start);
+    } else {
+        share(line_total(line, a.s.B, cost), x0, x1);
+        line_find(line, a.s.B, cost, x0, b, start);
+    }
+    if (blockIdx.x == 0 && bad) report_error(a.err, bad);
     if (x0 >= x1) return;
 
     uint8_t* const ring = smem + warp * C::RING;
@@ -360,8 +366,8 @@ struct WeightWalk {
         }
         take(a);
         const long long S = weight_cost(q, a);
-        h = (int)((w0 - start) / S);
-        const long long x = w0 - start - h * S;
+        long long x = w0 - start;
+        h = line_head(x, S);
         int lo = 0, hi = nk - 1;                           // the last tile that starts at or before x
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -405,20 +411,25 @@ struct WeightWalk {
     }
 };
 
-// All T threads: the CTA's share.
+// The CTA's share for the warps that are `first`: each by itself for up to 32 sequences, with all T threads for more.
 template <int T>
-__device__ __forceinline__ void weight_locate(const WeightArgs& a, Line<T>& line, WeightWalk& walk) {
+__device__ __forceinline__ void weight_locate(const WeightArgs& a, Line<T>& line, WeightWalk& walk, bool first) {
     int bad = 0;
-    auto cost = [&](int b) { return weight_cost(paged_seq(a.s, b, bad), a) * a.Hkv; };
-    const long long total = line_total(line, a.s.B, cost);
-    if (blockIdx.x == 0 && bad) report_error(a.err, bad);
-    const long long w0 = total / gridDim.x * blockIdx.x + total % gridDim.x * blockIdx.x / gridDim.x;
-    const int c = blockIdx.x + 1;
-    const long long w1 = total / gridDim.x * c + total % gridDim.x * c / gridDim.x;
+    const auto cost = [&](int b) { return weight_cost(paged_seq(a.s, b, bad), a) * a.Hkv; };
+    const auto share = [&](long long total, long long& w0, long long& w1) {
+        line_share(total, blockIdx.x, kWeightCtas, line_inv(kWeightCtas), w0, w1);
+    };
     int b;
-    long long start;
-    line_find(line, a.s.B, cost, w0, b, start);
-    walk.init(a, w0, w1, b, start);
+    long long w0, w1, start;
+    if (a.s.B <= 32) {
+        if (!first) return;
+        line_warp(a.s.B, cost, share, w0, w1, b, start);
+    } else {
+        share(line_total(line, a.s.B, cost), w0, w1);
+        line_find(line, a.s.B, cost, w0, b, start);
+    }
+    if (blockIdx.x == 0 && bad) report_error(a.err, bad);
+    if (first) walk.init(a, w0, w1, b, start);
 }
 
 // The sums of a unit, or of a part of it: one key per thread (key: within the tile).
@@ -574,7 +585,7 @@ __global__ void __launch_bounds__(640, 1)
     const uint32_t tm = tmem_slot;
     const WaitCtx w{a.err, &abort_flag, a.timeout_ns};
     WeightWalk walk;
-    weight_locate(a, line, walk);
+    weight_locate(a, line, walk, warp == 3);
     WeightPart p;
     int npart = 0;
     auto next_part = [&]() -> bool {
@@ -684,12 +695,6 @@ __global__ void __launch_bounds__(640, 1)
         umma_commit_e(smem_u32(&bar_final));
     } else if (warp == 3) {
         // ------------------------------------------------------------ the CTA's parts, and their log-sum-exps
-        int tk[4], hd[4];                                  // token and head of rows lane, lane + 32, ... of a tile
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            tk[k] = (lane + 32 * k) / a.gs;
-            hd[k] = (lane + 32 * k) % a.gs;
-        }
         if (lane < 2) a.part_info[blockIdx.x * 2 + lane] = make_int4(0, 0, 0, 0);
         __syncwarp();                                      // both in front of lane 0's arrivals, and so of any record
         // Part k + 1 is queued before the log-sum-exps of part k, which wait for the exponentials.
@@ -710,6 +715,12 @@ __global__ void __launch_bounds__(640, 1)
         };
         WeightPart ahead;
         ok = queue(ahead);
+        int tk[4], hd[4];                                  // token and head of rows lane, lane + 32, ... of a tile
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            tk[k] = (lane + 32 * k) / a.gs;
+            hd[k] = (lane + 32 * k) % a.gs;
+        }
         while (ok && ahead.b >= 0) {
             p = ahead;
             if (!(ok = queue(ahead))) break;
@@ -867,7 +878,7 @@ __global__ void __launch_bounds__(256, 1) weights_many_f32_kernel(const WeightAr
     griddep_launch_dependents();
     griddep_wait();
     WeightWalk walk;
-    weight_locate(a, line, walk);
+    weight_locate(a, line, walk, warp == 0);
     if (tid < 2) a.part_info[blockIdx.x * 2 + tid] = make_int4(0, 0, 0, 0);
     for (;;) {
         __syncthreads();                                   // (the records are cleared; the part before is done)
