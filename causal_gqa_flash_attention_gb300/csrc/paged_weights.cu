@@ -503,6 +503,7 @@ struct ManyCfg {
     static constexpr int NL = 8;                           // log-sum-exps of so many (a slot of Q is free behind its
                                                            // products, they are read until the exponentials are done)
     static constexpr int SMEM = 1024 + (NK + NS) * TILE;
+    static_assert(NS <= NL, "an issuer without keys passes the log-sum-exps of as many query tiles unseen");
     static constexpr int THREADS = 640;
 };
 
@@ -684,6 +685,11 @@ __global__ void __launch_bounds__(640, 1)
                         const uint32_t off = ((ks * 32) >> 7) * C::CHUNK + ((ks * 32) & 127);
                         umma_ss<false>(tm + s * 128, sdesc_add(dk, off), sdesc_add(dq, off), id_s, ks > 0);
                     }
+                }
+                __syncwarp();
+                // The exponentials wait for S alone: their log-sum-exps are there once it is committed.
+                if (!(ok = mbar_wait_warp(smem_u32(&bar_l_full[item % C::NL]), (item / C::NL) & 1, w, SITE_PAGED_Q))) break;
+                if (elect_one()) {
                     umma_commit(smem_u32(&bar_s_full[s]));
                     umma_commit(smem_u32(&bar_q_empty[i]));
                     if (t + 1 == p.t1) umma_commit(smem_u32(&bar_k_empty[kslot]));
@@ -774,8 +780,8 @@ __global__ void __launch_bounds__(640, 1)
             int tg = (p.t0 + skip) / a.ngrp, th = p.t0 + skip - tg * a.ngrp;   // t / ngrp, t % ngrp
             for (int j = skip; j < n; j += 2) {
                 const int i = (item + j) % C::NL;
-                if (!(ok = mbar_wait_warp(smem_u32(&bar_l_full[i]), ((item + j) / C::NL) & 1, w, SITE_PAGED_Q))) break;
-                if (mine) {
+                if (!mine && !(ok = mbar_wait_warp(smem_u32(&bar_l_full[i]), ((item + j) / C::NL) & 1, w, SITE_PAGED_Q))) break;
+                if (mine) {                                // (the issuer waited for the log-sum-exps)
                     if (!(ok = mbar_wait_warp(smem_u32(&bar_s_full[2 * u + half]), uses & 1, w, SITE_PAGED_S_FULL))) break;
                     ++uses;
                     tc_fence_after();

@@ -3,9 +3,10 @@ csrc/paged_weights.cu), run on the CPU over random lists of parts.
 
 Roles: the part finder, which also loads the log-sum-exps (a ring of their own; part k + 1 is queued before
 those of part k), the TMA producer (keys of a part, then query tiles through a ring), a UMMA issuer per key
-tile, and four groups of exponential warps: key tile u, query tiles of one parity.  Each role is a coroutine of its waits and arrivals (a group arrives as one; products and
-copies complete at once).  A run fails on a deadlock, on parity aliasing, or on an arrival that lands in
-another phase.  Kept in step with the kernel by hand.
+tile, which waits for a query tile's log-sum-exps before it commits its products, and four groups of
+exponential warps: key tile u, query tiles of one parity.  Each role is a coroutine of its waits and arrivals (a
+group arrives as one; products and copies complete at once).  A run fails on a deadlock, on parity aliasing, or on
+an arrival that lands in another phase.  Kept in step with the kernel by hand.
 """
 import random
 
@@ -119,6 +120,7 @@ def simulate(parts, NK, NS, NL, rng, follow_absent_keys=True):
                     s = 2 * u + odd
                     if st.uses[odd] >= 1:
                         yield s_free[s], st.uses[odd] - 1, f"issuer {u}: S {s}"
+                    yield l_full[it % NL], it // NL, f"issuer {u}: lse {it}"
                     s_full[s].arrive(st.uses[odd])
                     st.uses[odd] += 1
                     if t + 1 == n:
@@ -135,7 +137,7 @@ def simulate(parts, NK, NS, NL, rng, follow_absent_keys=True):
         def body(k, nu, n):
             for j in range((st.item ^ half) & 1, n, 2):
                 it = st.item + j
-                if u < nu or follow_absent_keys:
+                if u >= nu and follow_absent_keys:
                     yield l_full[it % NL], it // NL, f"exps {u}{half}: lse {it}"
                 if u < nu:
                     yield s_full[2 * u + half], st.uses, f"exps {u}{half}: S of {it}"
@@ -181,6 +183,14 @@ def simulate(parts, NK, NS, NL, rng, follow_absent_keys=True):
         else:
             raise ProtocolError("deadlock: " + "; ".join(pending[nm][2] for nm in roles))
     assert sorted(done) == sorted((k, u, j) for k, (nu, n) in enumerate(parts) for u in range(nu) for j in range(n))
+
+
+def test_the_model_finds_queries_that_run_ahead_of_their_log_sum_exps():
+    """The ring of queries is no longer than that of the log-sum-exps: an issuer without keys does not look at them."""
+    with pytest.raises(ProtocolError):
+        for seed in range(300):
+            rng = random.Random(seed)
+            simulate([(rng.choice([1, 2]), rng.choice([1, 2, 5, 17])) for _ in range(9)], 4, 12, 2, rng)
 
 
 @pytest.mark.parametrize("NK,NS", [(4, 8), (3, 3)])
