@@ -161,6 +161,7 @@ def simulate(parts, NK, NS, NL, rng, follow_absent_keys=True):
         roles[f"issuer{u}"] = role(f"issuer{u}", issuer(u))
         for half in range(2):
             roles[f"exps{u}{half}"] = role(f"exps{u}{half}", exps(u, half))
+    slow = {name: rng.choice([1, 1, 1, 20]) for name in roles}   # some roles lag behind
     pending = {}
     for name in list(roles):
         try:
@@ -168,8 +169,7 @@ def simulate(parts, NK, NS, NL, rng, follow_absent_keys=True):
         except StopIteration:
             del roles[name]
     while roles:
-        names = list(roles)
-        rng.shuffle(names)
+        names = sorted(roles, key=lambda name: rng.random() * slow[name])
         for name in names:
             b, n, _ = pending[name]
             if b.phase not in (n, n + 1):
