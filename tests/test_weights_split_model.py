@@ -24,7 +24,7 @@ def parts_of(n, lens, Hkv, G, rt, shift):
     nk = [-(-L // (1 << shift)) for L in lens]
     cost = [prefix(nb, L, k, ovh, shift) for nb, L, k in zip(n, lens, nk)]
     total = sum(cost) * Hkv
-    at = lambda c: total // C * c + total % C * c // C  # noqa: E731
+    at = lambda c: total if c == C else total * (((1 << 64) - 1) // C + 1) * c >> 64  # noqa: E731
     out = []
     for c in range(C):
         w0, w1 = at(c), at(c + 1)
