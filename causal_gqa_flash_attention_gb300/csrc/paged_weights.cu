@@ -777,7 +777,9 @@ __global__ void __launch_bounds__(640, 1)
             float2 s2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             // Every second query tile is this half's, in S buffer `half`.
             const int skip = (item ^ half) & 1, n = p.t1 - p.t0;
-            int tg = (p.t0 + skip) / a.ngrp, th = p.t0 + skip - tg * a.ngrp;   // t / ngrp, t % ngrp
+            // Tiles t_lo .. t_hi-1 are full and see all of the warps' keys.
+            const int t_lo = (max(0, k0 + 127 - (p.len - p.n)) + a.sub - 1) / a.sub * a.ngrp;
+            const int t_hi = a.G % a.gs ? 0 : p.n / a.sub * a.ngrp;
             for (int j = skip; j < n; j += 2) {
                 const int i = (item + j) % C::NL;
                 if (!mine && !(ok = mbar_wait_warp(smem_u32(&bar_l_full[i]), ((item + j) / C::NL) & 1, w, SITE_PAGED_Q))) break;
@@ -785,11 +787,8 @@ __global__ void __launch_bounds__(640, 1)
                     if (!(ok = mbar_wait_warp(smem_u32(&bar_s_full[2 * u + half]), uses & 1, w, SITE_PAGED_S_FULL))) break;
                     ++uses;
                     tc_fence_after();
-                    const int tok = tg * a.sub, live = min(a.gs, a.G - th * a.gs) * min(a.sub, p.n - tok);
-                    const int base = p.len - p.n + tok;    // position of the tile's first token
-                    // Rows c_min .. live-1 of the tile see this thread's key.
-                    const int d = k0 + lk - base;
-                    const int c_min = d <= 0 ? 0 : d >= a.sub ? 128 : d * a.gs;
+                    const int t = p.t0 + j;
+                    int c_min = 0, live = 128;             // rows c_min .. live-1 of the tile see this thread's key
                     const float4* nl = reinterpret_cast<const float4*>(s_nl[i]);
                     // (Edge tiles in a loop: a call with few tiles waits for its instructions, 21.0 -> 20 us.)
                     auto tile = [&](auto edge) {
@@ -821,12 +820,18 @@ __global__ void __launch_bounds__(640, 1)
                             }
                         }
                     };
-                    if (k0 + 127 > base || live < box) tile(std::true_type());
-                    else tile(std::false_type());
+                    if (t >= t_lo && t < t_hi) {
+                        tile(std::false_type());
+                    } else {
+                        const int tg = t / a.ngrp, th = t - tg * a.ngrp, tok = tg * a.sub;
+                        live = min(a.gs, a.G - th * a.gs) * min(a.sub, p.n - tok);
+                        const int d = k0 + lk - (p.len - p.n + tok);
+                        c_min = d <= 0 ? 0 : d >= a.sub ? 128 : d * a.gs;
+                        tile(std::true_type());
+                    }
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&bar_l_empty[i]));
-                for (th += 2; th >= a.ngrp; th -= a.ngrp) ++tg;
             }
             item += n;
             if (!ok) break;
