@@ -17,16 +17,18 @@
 // Many rows, fp32: units of 128 keys on fp32 FMAs, two keys per lane in registers, the query rows
 // broadcast from shared memory.
 //
-// Measured (GB300): one token over 8 x 16384 positions, 12/4 heads of 64: 17.1 us, 4.2 TB/s (10.6 at the copy
-// rate; 3.7 to begin and find the shares, then 5.3 TB/s); the small fp32 step 3.8.  2048 tokens over 16384
-// positions, 16/4 heads of 128: 110 us, 1.17 PFLOP/s (61% of the bf16 GEMM); of 64: 105 us, 0.61 PFLOP/s, the
-// exponential units 62% busy: the four warps of a scheduler wait for S and begin tiles together.  Twelve
-// sequences, single tokens beside chunks up to 512 over up to 4096: 22 us (2.0), 9 before the first product,
-// then 5 query tiles in 3 parts per CTA, then the join.
+// Measured (GB300): one token over 8 x 16384 positions, 12/4 heads of 64: 16.3 us, 4.4 TB/s (10.6 at the copy
+// rate; 3 to begin and find the shares, then 5.3 TB/s); the small fp32 step 3.1.  2048 tokens over 16384
+// positions, 16/4 heads of 128: 108 us, 1.19 PFLOP/s (62% of the bf16 GEMM; operands out of shared memory, 128 bytes a
+// cycle, bound the products); of 64: 100 us, 0.64 PFLOP/s, the exponential units 70% busy: of the 3000 cycles of
+// a tile its warps spend 2200 on exponentials.  Twelve sequences, single tokens beside chunks up to 512 over up
+// to 4096: 19.3 us (2.0), 5 before the first product, then 5 query tiles in 3 parts per CTA, then the join.
 // Tried for many rows and left out: part of the exponentials as a polynomial on the FMA pipes (D 64 119 -> 144
 // us, then with eight exponential warps), keys as the TMEM operand with 96-row query tiles (D 128 120 ->
 // 138: it is the issue of products, some 90 cycles each, that counts), S in halves with buffers of their own
-// (D 64 105 -> 113), all 128 columns of S in registers at once (119 -> 133).
+// (D 64 105 -> 113), all 128 columns of S in registers at once (119 -> 133), or 64 (104 -> 117), 16 columns on
+// their way behind those at work (101 -> 103), one product for two query tiles (S then has one buffer per key tile: D
+// 128 109 -> 141).
 #include <cuda_bf16.h>
 #include <type_traits>
 #include "paged_line.cuh"
