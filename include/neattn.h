@@ -403,9 +403,11 @@ ne_status ne_paged_attn_f32(const float* q, const ne_paged_cache* cache, const i
  * Everything else is as in ne_paged_attn (its workspace of another size); results are the same up to
  * rounding, and the same bits for the same call.  Groups outside [0, B] or descending, a negative shared[r], and
  * whole steps of shared positions that reach into a sequence's new tokens are reported by
- * ne_get_device_error() (outputs of that group invalid).  A call that has nothing to gain (max_new * Hq / Hkv of 224 and more, more than 128 bf16 query
- * heads per kv head, small caches) runs as ne_paged_attn does, and then looks at neither groups nor shared.  workspace: ne_paged_attn_shared_workspace_size() bytes (two workspaces of
- * ne_paged_attn and 8 D + 32 bytes per row and query head). */
+ * ne_get_device_error() (outputs of that group invalid).  A call that has nothing to gain (sequences whose rows
+ * fill tiles by themselves, judged by max_new, N / B and max_pages; small caches; more than 128 bf16 query heads per
+ * kv head) runs as ne_paged_attn does, and then looks at neither groups nor shared.
+ * workspace: ne_paged_attn_shared_workspace_size() bytes (two workspaces of ne_paged_attn and 8 D + 32 bytes per
+ * row and query head). */
 size_t ne_paged_attn_shared_workspace_size(int B, int N, int Hq, int Hkv, int D);
 ne_status ne_paged_attn_shared(const void* q, const ne_paged_cache* cache, const int* page_table, const int* seq_lens,
                                const int* cu_new, const int* groups, const int* shared, int R, void* o, float* lse,

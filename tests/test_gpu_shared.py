@@ -153,8 +153,29 @@ def test_many_groups(dtype, D, n):
 @pytest.mark.parametrize("max_new", [1, 8, 22, 4000])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_any_max_new_is_right(dtype, max_new):
-    """22 times 12 rows: tiles are full, the call runs as paged_attn; below it hints that are too small."""
+    """A hint, and no more: too small, too large."""
     check(dtype, 12, 1, 64, 16, [0, 3], [512], [25, 1, 70], [600, 513, 700], max_new=max_new, seed=11)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,ps", [(12, 4, 64, 16), (8, 2, 128, 64), (6, 2, 32, 8), (5, 5, 64, 32)])
+@pytest.mark.parametrize("n", [[200, 1, 130, 77, 256], [90] * 5, [0, 300, 2, 0, 85]])
+def test_chunks_of_several_row_tiles(Hq, Hkv, D, ps, n):
+    """Sequences of more rows than a tile, rows of several in the tiles of their prefix."""
+    lens = [1000 + x + y for x, y in zip(n, [0, 300, 5, 128, 51])]
+    check(BF16, Hq, Hkv, D, ps, [0, 3, 5], [1000, 520], n, lens, max_new=max(n), seed=17)
+
+
+@pytest.mark.parametrize("D,n", [(64, [64] * 8), (128, [60, 64, 64, 3, 64, 17, 64, 64])])
+def test_chunks_that_fill_their_tiles(D, n):
+    """The first runs as paged_attn, whatever the groups say."""
+    lens = [700 + x for x in n]
+    check(BF16, 4, 1, D, 16, [0, 8], [700], n, lens, max_new=64, seed=18)
+    if n == [64] * 8:
+        q, kp, vp, table, ln, gr, sh, cu, *_ = make(BF16, 4, 1, D, 16, [0, 8], [700], n, lens)
+        a = ne.paged_attn_shared(q, kp, vp, table, ln, i32([5, 2]), sh, cu, max_new=64)
+        b = ne.paged_attn(q, kp, vp, table, ln, cu, max_new=64)
+        ok()
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
 def test_more_than_128_query_heads():
