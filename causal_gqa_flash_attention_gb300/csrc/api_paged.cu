@@ -328,7 +328,7 @@ constexpr int kSharedRows = 224;
 // (3) bf16 with more than 32 rows a sequence, which ne_paged_attn has tiles of 256 rows for, too: shared, the tiles of a
 // prefix are full, but every sequence has a part more.  It pays where the part of the tiles that would be empty, times
 // the positions of a table, reaches this.  16 sequences, 12/4 heads of 64: 192 rows each (a quarter empty) over
-// 4096 alone 30.1 us, shared 32.6, over 16384 75 and 71; 240 rows 77 and 109; up to 768 rows over 8192 83 and 77.  200
+// 4096 alone 30.1 us, shared 32.6, over 16384 75 and 71; 240 rows 77 and 109; up to 768 rows over 8192 83 and 73.  200
 // shapes (lengths alike and different, 2048 to 16384 positions, head_dims 64 and 128): 7.6% faster than never sharing,
 // 7.8 by the better of both each time.
 constexpr double kSharedEmpty = 1200.;
@@ -399,9 +399,13 @@ ne_status shared_impl(int eb, const void* q, const ne_paged_cache* c, const int*
         if ((s = attn_args(&a[i], kind[i], q, c, table, lens, cu, o, lse, q_ld, lines == 1 ? R + B : i ? B : R, N, Hq, W,
                            static_cast<char*>(ws) + i * w.parts, stream)) != NE_OK)
             return s;
-        // A part's ends with its fp32 rows: two tiles (16 shapes, geometric mean: 30.6 us with 1024, 30.0 with 1280 to
-        // 1408, 30.6 with 2048).
-        if (!f32) a[i].p.ovh = 1344;
+        // A part's ends with its fp32 rows: two tiles where few of them are live (16 shapes, geometric mean: 30.6 us with
+        // 1024, 30.0 with 1280 to 1408, 30.6 with 2048), nearly three where all are, and then a part of one subtile
+        // waits as long per key tile (138 shapes: 66.7 us as with few, 64.8 as here).
+        if (!f32) {
+            a[i].p.ovh = rows_each > 32 ? 1792 : 1344;
+            if (rows_each > 32) a[i].p.w_part = a[i].p.w_full;
+        }
         a[i].s.groups = groups;
         a[i].s.shared = shared;
         a[i].s.R = R;

@@ -112,7 +112,7 @@ __device__ __forceinline__ void transpose4(uint4 (&v)[4], int l) {
 // (32 runs as 64: TMA fills the columns behind a row's end with zeros).
 // Measured (GB300, with the join): 64 sequences over a shared prefix of 16384 and up to 512 positions of their own, 12/4
 // heads of 64: 25.6 us (every sequence for itself: 104); 37 sequences in four groups over up to 8192, 16/4 heads
-// of 128: 31.9 us (51), the read of the cache (15 at the copy rate).  A CTA takes 4 us to
+// of 128: 31.6 us (51), the read of the cache (15 at the copy rate).  A CTA takes 4 us to
 // find its share, 2 to its first product, 1.03 per key tile of a prefix, 0.8 (D 128: 1.3) per tile of a
 // sequence and 2 for the ends of a part; the join 3 to 4.
 // Tried and left out: own positions in the kernel for few rows behind this one (34.4 us), a part's keys
