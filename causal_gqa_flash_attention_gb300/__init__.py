@@ -601,8 +601,8 @@ def paged_attn_shared(q, k_pages, v_pages, page_table, seq_lens, groups, shared,
     """paged_attn for sequences that share their first positions (ne_paged_attn_shared): sequences
     groups[r] .. groups[r+1]-1 (int32 [R + 1]) hold the same in their first shared[r] (int32 [R]) positions,
     in front of their new tokens; those are read and multiplied once per group.  Returns what paged_attn
-    returns, up to rounding.  max_new: the most new tokens of a sequence; where it is not given (and
-    cu_new is) an fp32 call of many rows cannot tell that they are of many sequences and runs as paged_attn."""
+    returns, up to rounding.  max_new: the most new tokens of a sequence (all
+    rows where it is not given and cu_new is); which kernels run depends on it, the result up to rounding not."""
     if max_new is not None and not 1 <= max_new <= _INT_MAX:
         _c_ints(max_new=max_new)
     lib = _lib or load()

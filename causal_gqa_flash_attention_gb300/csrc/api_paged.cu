@@ -321,33 +321,33 @@ ne_status attn_impl(int eb, const void* q, const ne_paged_cache* c, const int* t
 // Where a call runs as ne_paged_attn.
 // (1) While all sequences' caches, as large as their tables, take no more bytes than this, reading them all beats a
 // join of two lines: bf16, 33 MB 13.1 us against 15.1, 66 MB 16.1 against 15.2, 134 MB 21.8 against 16.1; fp32
-// with few rows 134 MB 22 against 32, 537 MB 59 against 54 (its products take as long either way).
+// with up to 32 rows a sequence 134 MB 22 against 32, 537 MB 59 against 54 (its products take as long either way).
 constexpr long long kSharedBytes = 64LL << 20, kSharedBytesF32 = 256LL << 20;
-// (2) fp32: from so many rows per kv head on a sequence fills the kernels' row tiles by itself.
-constexpr int kSharedRows = 224;
-// (3) bf16 with more than 32 rows a sequence, which ne_paged_attn has tiles of 256 rows for, too: shared, the tiles of a
+// (2) With more than 32 rows a sequence ne_paged_attn has tiles of 256 rows (fp32: 64), too: shared, the tiles of a
 // prefix are full, but every sequence has a part more.  It pays where the part of the tiles that would be empty, times
-// the positions of a table, reaches this.  16 sequences, 12/4 heads of 64: 192 rows each (a quarter empty) over
-// 4096 alone 30.1 us, shared 32.6, over 16384 75 and 71; 240 rows 77 and 109; up to 768 rows over 8192 83 and 73.  200
-// shapes (lengths alike and different, 2048 to 16384 positions, head_dims 64 and 128): 7.6% faster than never sharing,
-// 7.8 by the better of both each time.
-constexpr double kSharedEmpty = 1200.;
-// (4) The same at head_dim 32, where ne_paged_attn takes 32 rows at a time: from so many rows times positions a sequence
-// on (128 over 700: 15.4 us against 17.4, over 2200 24.6 against 21.9; 256 over 8256 112 against 48; 64 over 2100 18
-// against 28).
+// the positions of a table, reaches this.
+// bf16, 16 sequences, 12/4 heads of 64: 192 rows each (a quarter empty) over 4096 alone 30.1 us, shared 32.6, over
+// 16384 75 and 71; 240 rows 77 and 109; up to 768 rows over 8192 83 and 73.  200 shapes (lengths alike and different, 2048
+// to 16384 positions, head_dims 64 and 128): 7.6% faster than never sharing, 7.8 by the better of both each time.
+// fp32, the same with 4 heads: 80 rows (three eighths empty) over 1024 93 and 79, over 4096 297 and 203; 64 rows over
+// 4096 154 and 170; up to 64 rows over 1024 50 and 50, over 4096 148 and 107.
+constexpr double kSharedEmpty = 1200., kSharedEmptyF32 = 600.;
+// (3) The same in bf16 at head_dim 32, where ne_paged_attn takes 32 rows at a time: from so many rows times positions a
+// sequence on (128 over 700: 15.4 us against 17.4, over 2200 24.6 against 21.9; 256 over 8256 112 against 48; 64 over
+// 2100 18 against 28).
 constexpr double kSharedWork = 150e3;
 
-// (3) and (4): whether sharing pays.
-bool shared_pays(int D, int G, int most, int N, int B, long long cap) {
+// (2) and (3): whether sharing pays.
+bool shared_pays(bool f32, int D, int G, int most, int N, int B, long long cap) {
     const double mean = (double)N / B;
-    if (D == 32) return mean * G * (double)cap >= kSharedWork;
-    // Row tiles of a sequence (one with half its rows or fewer takes 0.8 of the time), and how many its rows would fill.
-    const int sub = 128 / G, tpt = 2 * sub, rem = most % tpt;
-    const double full = mean / tpt;
+    if (!f32 && D == 32) return mean * G * (double)cap >= kSharedWork;
+    // Row tiles of a sequence (bf16: one with half its rows or fewer takes 0.8 of the time), and how many its rows fill.
+    const int sub = f32 ? std::max(64 / G, 1) : 128 / G, tpt = f32 ? sub : 2 * sub, rem = most % tpt;
+    const double full = mean / tpt, half = f32 ? 1. : 0.8;
     double tiles;
-    if (N == (long long)B * most) tiles = most / tpt + (rem == 0 ? 0. : rem <= sub ? 0.8 : 1.);
-    else tiles = most <= sub ? 0.8 : most <= tpt ? 0.9 : full + 0.4;       // (lengths differ: half a tile is empty)
-    return (tiles - full) * (double)cap >= kSharedEmpty * tiles;
+    if (N == (long long)B * most) tiles = most / tpt + (rem == 0 ? 0. : rem <= sub ? half : 1.);
+    else tiles = most <= sub ? half : most <= tpt ? 0.9 : full + 0.5 * half;   // (lengths differ: half a tile is empty)
+    return (tiles - full) * (double)cap >= (f32 ? kSharedEmptyF32 : kSharedEmpty) * tiles;
 }
 
 struct SharedWs {
@@ -384,9 +384,8 @@ ne_status shared_impl(int eb, const void* q, const ne_paged_cache* c, const int*
     const long long bytes = (long long)B * W * c->page_size * c->Hkv * 2 * c->D * eb;
     const long long rows_each = (long long)most * G;
     bool alone = R == 0 || (!f32 && G > 128);
-    if (f32) alone |= rows_each >= kSharedRows || bytes <= (rows_each <= 16 ? kSharedBytesF32 : kSharedBytes);
-    else if (c->D != 32 || rows_each <= 32) alone |= bytes <= kSharedBytes;
-    if (!f32 && !alone && rows_each > 32) alone = !shared_pays(c->D, G, most, N, B, (long long)W * c->page_size);
+    if (rows_each <= 32 || (!f32 && c->D != 32)) alone |= bytes <= (f32 ? kSharedBytesF32 : kSharedBytes);
+    if (!alone && rows_each > 32) alone = !shared_pays(f32, c->D, G, most, N, B, (long long)W * c->page_size);
     if (alone)
         return attn_run(eb, q, c, table, lens, cu, o, lse, q_ld, B, N, Hq, W, max_new, ws, stream);
     // bf16: one line of prefixes and own positions, tiles for all.  fp32: a line and a kernel for each,

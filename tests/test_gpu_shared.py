@@ -157,12 +157,13 @@ def test_any_max_new_is_right(dtype, max_new):
     check(dtype, 12, 1, 64, 16, [0, 3], [512], [25, 1, 70], [600, 513, 700], max_new=max_new, seed=11)
 
 
-@pytest.mark.parametrize("Hq,Hkv,D,ps", [(12, 4, 64, 16), (8, 2, 128, 64), (6, 2, 32, 8), (5, 5, 64, 32)])
+@pytest.mark.parametrize("dtype,Hq,Hkv,D,ps", [(BF16, 12, 4, 64, 16), (BF16, 8, 2, 128, 64), (BF16, 6, 2, 32, 8), (BF16, 5, 5, 64, 32),
+                                                (F32, 6, 2, 64, 16), (F32, 2, 2, 32, 64)])
 @pytest.mark.parametrize("n", [[200, 1, 130, 77, 256], [90] * 5, [0, 300, 2, 0, 85]])
-def test_chunks_of_several_row_tiles(Hq, Hkv, D, ps, n):
+def test_chunks_of_several_row_tiles(dtype, Hq, Hkv, D, ps, n):
     """Sequences of more rows than a tile, rows of several in the tiles of their prefix."""
     lens = [1000 + x + y for x, y in zip(n, [0, 300, 5, 128, 51])]
-    check(BF16, Hq, Hkv, D, ps, [0, 3, 5], [1000, 520], n, lens, max_new=max(n), seed=17)
+    check(dtype, Hq, Hkv, D, ps, [0, 3, 5], [1000, 520], n, lens, max_new=max(n), seed=17)
 
 
 @pytest.mark.parametrize("D,n", [(64, [64] * 8), (128, [60, 64, 64, 3, 64, 17, 64, 64])])
