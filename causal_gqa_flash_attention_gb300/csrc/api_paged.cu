@@ -320,7 +320,7 @@ ne_status attn_impl(int eb, const void* q, const ne_paged_cache* c, const int* t
 // ---------------------------------------------------------------- shared prefixes
 // Where a call runs as ne_paged_attn.
 // (1) While all sequences' caches, as large as their tables, take no more bytes than this, reading them all beats a
-// join of two lines: bf16, 33 MB 13.1 us against 15.1, 66 MB 16.1 against 15.2, 134 MB 21.8 against 16.1; fp32
+// join of two lines: bf16, 33 MB 14.5 us against 16.5, 65 MB 18.1 against 17.1, 132 MB 25.8 against 19.3; fp32
 // with up to 32 rows a sequence 134 MB 22 against 32, 537 MB 59 against 54 (its products take as long either way).
 constexpr long long kSharedBytes = 64LL << 20, kSharedBytesF32 = 256LL << 20;
 // (2) With more than 32 rows a sequence ne_paged_attn has tiles of 256 rows (fp32: 64), too: shared, the tiles of a
@@ -332,15 +332,16 @@ constexpr long long kSharedBytes = 64LL << 20, kSharedBytesF32 = 256LL << 20;
 // fp32, the same with 4 heads: 80 rows (three eighths empty) over 1024 93 and 79, over 4096 297 and 203; 64 rows over
 // 4096 154 and 170; up to 64 rows over 1024 50 and 50, over 4096 148 and 107.
 constexpr double kSharedEmpty = 1200., kSharedEmptyF32 = 600.;
-// (3) The same in bf16 at head_dim 32, where ne_paged_attn takes 32 rows at a time: from so many rows times positions a
-// sequence on (128 over 700: 15.4 us against 17.4, over 2200 24.6 against 21.9; 256 over 8256 112 against 48; 64 over
-// 2100 18 against 28).
-constexpr double kSharedWork = 150e3;
+// (3) The same in bf16 at head_dim 32, where ne_paged_attn takes 32 rows at a time: from so many rows times positions of
+// all sequences on (12/4 heads: 4 sequences of 64 over 2300 19.5 us against 26.1 shared, 4 of 200 over 600 21.5 and 19.5, 16
+// of 64 over 2100 41 and 27, 16 of up to 256 over 8192 179 and 92.  85 shapes, 2 to 32 sequences, 12/4, 8/1 and 4/2 heads: 1.4%
+// slower than the better of both each time; never sharing 8.1%, always 16%).
+constexpr double kSharedWork = 9e6;
 
 // (2) and (3): whether sharing pays.
-bool shared_pays(bool f32, int D, int G, int most, int N, int B, long long cap) {
+bool shared_pays(bool f32, int D, int G, int Hq, int most, int N, int B, long long cap) {
     const double mean = (double)N / B;
-    if (!f32 && D == 32) return mean * G * (double)cap >= kSharedWork;
+    if (!f32 && D == 32) return (double)N * Hq * (double)cap >= kSharedWork;
     // Row tiles of a sequence (bf16: one with half its rows or fewer takes 0.8 of the time), and how many its rows fill.
     const int sub = f32 ? std::max(64 / G, 1) : 128 / G, tpt = f32 ? sub : 2 * sub, rem = most % tpt;
     const double full = mean / tpt, half = f32 ? 1. : 0.8;
@@ -385,7 +386,7 @@ ne_status shared_impl(int eb, const void* q, const ne_paged_cache* c, const int*
     const long long rows_each = (long long)most * G;
     bool alone = R == 0 || (!f32 && G > 128);
     if (rows_each <= 32 || (!f32 && c->D != 32)) alone |= bytes <= (f32 ? kSharedBytesF32 : kSharedBytes);
-    if (!alone && rows_each > 32) alone = !shared_pays(f32, c->D, G, most, N, B, (long long)W * c->page_size);
+    if (!alone && rows_each > 32) alone = !shared_pays(f32, c->D, G, Hq, most, N, B, (long long)W * c->page_size);
     if (alone)
         return attn_run(eb, q, c, table, lens, cu, o, lse, q_ld, B, N, Hq, W, max_new, ws, stream);
     // bf16: one line of prefixes and own positions, tiles for all.  fp32: a line and a kernel for each,
@@ -398,11 +399,11 @@ ne_status shared_impl(int eb, const void* q, const ne_paged_cache* c, const int*
         if ((s = attn_args(&a[i], kind[i], q, c, table, lens, cu, o, lse, q_ld, lines == 1 ? R + B : i ? B : R, N, Hq, W,
                            static_cast<char*>(ws) + i * w.parts, stream)) != NE_OK)
             return s;
-        // A part's ends with its fp32 rows: two tiles where few of them are live (16 shapes, geometric mean: 30.6 us with
-        // 1024, 30.0 with 1280 to 1408, 30.6 with 2048), nearly three where all are, and then a part of one subtile
-        // waits as long per key tile (138 shapes: 66.7 us as with few, 64.8 as here).
+        // A part's ends with its fp32 rows: less than two tiles where few of them are live (35 shapes, geometric mean: 21.0
+        // us with 896, 20.3 with 1024, 20.8 with 1152, 20.6 with 1280 and 1408), nearly three where all are, and then a part of
+        // one subtile waits as long per key tile (138 shapes: 66.7 us as with few, 64.8 as here).
         if (!f32) {
-            a[i].p.ovh = rows_each > 32 ? 1792 : 1344;
+            a[i].p.ovh = rows_each > 32 ? 1792 : 1024;
             if (rows_each > 32) a[i].p.w_part = a[i].p.w_full;
         }
         a[i].s.groups = groups;
@@ -424,7 +425,9 @@ ne_status shared_impl(int eb, const void* q, const ne_paged_cache* c, const int*
     if (!f32) {
         CUtensorMap tq, tk, tv;
         if ((s = tile_maps(&tq, &tk, &tv, c, a[0].c, q, q_ld, Hq, N, G, a[0].p.sub)) != NE_OK) return s;
-        e = ne::launch_shared_tiles(c->D, tq, tk, tv, a[0], st);
+        // The bits of a weight are those of ne_paged_attn: its kernels for few rows, which take head_dim 32 whatever the
+        // rows, keep two bf16 terms.
+        e = ne::launch_shared_tiles(c->D, rows_each <= 32 || c->D == 32 ? 2 : 1, tq, tk, tv, a[0], st);
     } else {
         e = ne::launch_shared_f32(kind[0], c->D, a[0], st);
         if (e == cudaSuccess) e = ne::launch_shared_f32(kind[1], c->D, a[1], st);

@@ -128,7 +128,8 @@ cudaError_t launch_paged_tiles(int D, const CUtensorMap& tq, const CUtensorMap& 
                                const PagedAttnArgs& a, cudaStream_t st);
 // The same over prefixes or own positions, results as parts (a.s.groups set).
 cudaError_t launch_shared_f32(PagedKind kind, int D, const PagedAttnArgs& a, cudaStream_t st);
-cudaError_t launch_shared_tiles(int D, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+// terms: bf16 terms of a softmax weight (head_dim 32: 2).
+cudaError_t launch_shared_tiles(int D, int terms, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                 const PagedAttnArgs& a, cudaStream_t st);
 // Puts prefixes' and own positions' parts together (one line of both, or two).
 cudaError_t launch_shared_join(bool f32, int D, const PagedAttnArgs& pre, const PagedAttnArgs& own, cudaStream_t st);

@@ -27,7 +27,9 @@
 // TMEM: S_u at 128 u, O_u behind both; P_u (bf16) over S_u's first half at D 128, where TMEM
 // is full, in columns of its own at D 64.
 // Weights are rounded to bf16 for the product (half a step, 2^-8 of each weight, as the
-// training forward does); maximum and sum stay fp32, and the sum is of the unrounded weights.
+// training forward does); maximum and sum stay fp32, and the sum is of the unrounded weights.  Over
+// shared prefixes, where rows come here that would otherwise take the kernel for few rows, they keep that kernel's
+// two bf16 terms, and P V is two products.
 // Measured (GB300): 2048 new tokens over 16384 positions, 16/4 heads of 128, pages of 64: 185 us
 // with the join, 1.39 PFLOP/s (73% of the 1.89 measured for a bf16 GEMM; 182 us with the cache in
 // the L2, 192 with pages of 16, where a tile takes 8 boxes of each kind), the tensor pipe 63% busy:
@@ -51,7 +53,8 @@ namespace {
 constexpr int kSegs = 4;               // parts in the queue from warp 3 to the others
 constexpr int kSegReaders = 11;        // warps 0, 1, 2 and 4-11
 
-template <int D>
+// TERMS: bf16 terms of a weight.
+template <int D, int TERMS>
 struct TileCfg {
     static constexpr int BN = 128;                         // keys of a tile
     static constexpr int ROWB = D * 2;
@@ -63,10 +66,14 @@ struct TileCfg {
     static constexpr int THREADS = 384;
     static constexpr int O_COL = 256;                      // O_u at O_COL + u D
     // P in columns of its own where TMEM has them left (D 64): the next S then starts as soon as
-    // this one has been read into registers, instead of after its PV.
-    static constexpr bool SEP = D == 64;
+    // this one has been read into registers, instead of after its PV.  (Two terms take as many columns as S and lie
+    // over it at D 64, too, those of 32 keys over their scores.)
+    static constexpr bool SEP = D == 64 && TERMS == 1;
     static constexpr int P_COL = SEP ? O_COL + 2 * D : 0;  // P_u at P_COL + u P_STEP
     static constexpr int P_STEP = SEP ? 64 : 128;
+    static __host__ __device__ constexpr int p_col(int ks, int j) {    // term j of keys 16 ks ..
+        return TERMS == 1 ? ks * 8 : ks / 2 * 32 + j * 16 + ks % 2 * 8;
+    }
     static constexpr int ISSUERS = SEP ? 2 : 1;
     static_assert(SMEM + 1536 <= 227 * 1024, "shared memory (with the static part)");
 };
@@ -111,19 +118,21 @@ __device__ __forceinline__ void transpose4(uint4 (&v)[4], int l) {
 // SH: the SHARED form, prefixes and own positions in one line, results as parts alone; DR: the cache's head_dim
 // (32 runs as 64: TMA fills the columns behind a row's end with zeros).
 // Measured (GB300, with the join): 64 sequences over a shared prefix of 16384 and up to 512 positions of their own, 12/4
-// heads of 64: 25.6 us (every sequence for itself: 104); 37 sequences in four groups over up to 8192, 16/4 heads
-// of 128: 31.6 us (51), the read of the cache (15 at the copy rate).  A CTA takes 4 us to
-// find its share, 2 to its first product, 1.03 per key tile of a prefix, 0.8 (D 128: 1.3) per tile of a
-// sequence and 2 for the ends of a part; the join 3 to 4.
+// heads of 64: 30.7 us (every sequence for itself: 110); 37 sequences in four groups over up to 8192, 16/4 heads
+// of 128: 36.4 us (54), the read of the cache 15 at the copy rate.  With one term per weight those took 26.4 and 33.4:
+// of the 4.3 us at D 64 the second product takes 1.2, forming it 1.3 and S, which then waits for PV, 1.8.  A CTA takes 4 us to
+// find its share, 2 to its first product and 2 for the ends of a part; the join 3 to 4.
+// Tried for the second term and left out: an issuer for each subtile at D 64 with P over S (34 us), the value cut off
+// instead of rounded (no change), both terms multiplied when all of P is there (D 128: 39 us).
 // Tried and left out: own positions in the kernel for few rows behind this one (34.4 us), a part's keys
 // split over the two subtiles where its rows fit into one (34.5; more registers live, a hand-over per part), the next
 // part's keys in front of its queries (no change), parts of one subtile taking the two in turn with scores masked in
 // a loop (16 shapes: 1% less).
-template <int D, int DR, bool SH>
+template <int D, int DR, bool SH, int TERMS>
 __global__ void __launch_bounds__(384, 1)
     paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const PagedAttnArgs a) {
-    using C = TileCfg<D>;
+    using C = TileCfg<D, TERMS>;
     using Seg = typename PagedSegOf<SH>::type;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -131,7 +140,7 @@ __global__ void __launch_bounds__(384, 1)
     uint8_t* sRing = smem + 2 * C::TILE;
     __shared__ __align__(8) uint64_t bar_q_full, bar_q_empty, bar_vfix[2], bar_final;
     __shared__ __align__(8) uint64_t bar_full[C::NS], bar_empty[C::NS];
-    __shared__ __align__(8) uint64_t bar_s_full[2], bar_p_ready[2], bar_o_full[2], bar_s_free[2];
+    __shared__ __align__(8) uint64_t bar_s_full[2], bar_p_ready[2 * TERMS], bar_o_full[2], bar_s_free[2];
     __shared__ __align__(8) uint64_t bar_seg_full[kSegs], bar_seg_empty[kSegs];
     __shared__ PagedLocate loc;
     __shared__ Seg s_seg[kSegs];                           // the CTA's parts in order (b < 0: the end)
@@ -150,7 +159,7 @@ __global__ void __launch_bounds__(384, 1)
         }
         for (int u = 0; u < 2; ++u) {
             mbar_init(smem_u32(&bar_s_full[u]), 1);
-            mbar_init(smem_u32(&bar_p_ready[u]), 128);
+            for (int h = 0; h < TERMS; ++h) mbar_init(smem_u32(&bar_p_ready[u * TERMS + h]), 128);
             mbar_init(smem_u32(&bar_o_full[u]), 1);        // a part's last PV; SEP: every PV
             mbar_init(smem_u32(&bar_s_free[u]), 128);      // SEP: S is in registers
             mbar_init(smem_u32(&bar_vfix[u]), 32);         // the k-th fix arrives on k % 2: warp 2 can be one
@@ -369,22 +378,32 @@ __global__ void __launch_bounds__(384, 1)
                 for (int i = 0; i < NU; ++i) {
                     if (i >= mine) break;
                     const int u = u0 + i;
-                    if (!(ok = mbar_wait_warp(smem_u32(&bar_p_ready[u]), tiles[i] & 1, w, SITE_PAGED_P_READY))) break;
-                    ++tiles[i];
-                    tc_fence_after();
-                    if (elect_one()) {
+                    // (Two terms: P comes in two halves of the keys, the first multiplied while the second is made.)
+                    constexpr int KS = C::BN / 16 / TERMS;
 #pragma unroll
-                        for (int ks = 0; ks < C::BN / 16; ++ks)
-                            umma_ts<false>(tm + C::O_COL + u * D, tm + C::P_COL + u * C::P_STEP + ks * 8,
-                                           sdesc_add(dv, ks * 16 * 128), id_o, (t > 0 || ks > 0) ? 1u : 0u);
-                        if (C::SEP || !more) umma_commit(smem_u32(&bar_o_full[u]));
-                        if (!C::SEP && more) s_mmas(i, kn);
-                        if (i == mine - 1) {
-                            umma_commit(smem_u32(&bar_empty[vi % C::NS]));
-                            if (!C::SEP && more) s_done(kn, t + 2 == nt);
+                    for (int h = 0; h < TERMS; ++h) {
+                        if (!(ok = mbar_wait_warp(smem_u32(&bar_p_ready[u * TERMS + h]), tiles[i] & 1, w, SITE_PAGED_P_READY))) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int ks = h * KS; ks < (h + 1) * KS; ++ks)
+#pragma unroll
+                                for (int j = 0; j < TERMS; ++j)
+                                    umma_ts<false>(tm + C::O_COL + u * D, tm + C::P_COL + u * C::P_STEP + C::p_col(ks, j),
+                                                   sdesc_add(dv, ks * 16 * 128), id_o, (t > 0 || ks > 0 || j > 0) ? 1u : 0u);
+                            if (h == TERMS - 1) {
+                                if (C::SEP || !more) umma_commit(smem_u32(&bar_o_full[u]));
+                                if (!C::SEP && more) s_mmas(i, kn);
+                                if (i == mine - 1) {
+                                    umma_commit(smem_u32(&bar_empty[vi % C::NS]));
+                                    if (!C::SEP && more) s_done(kn, t + 2 == nt);
+                                }
+                            }
                         }
+                        __syncwarp();
                     }
-                    __syncwarp();
+                    if (!ok) break;
+                    ++tiles[i];
                 }
             }
             item += 2 * nt;
@@ -477,27 +496,47 @@ __global__ void __launch_bounds__(384, 1)
                     if (C::SEP) mbar_arrive(smem_u32(&bar_s_free[u]));
                     ok = pv_before();
                     if (!ok) break;
-                    mbar_arrive(smem_u32(&bar_p_ready[u]));
+                    for (int h = 0; h < TERMS; ++h) mbar_arrive(smem_u32(&bar_p_ready[u * TERMS + h]));
                     continue;
                 }
                 tc_fence_after();
-                uint32_t s[128];
-                tmem_ld_cols<4>(sc, s);
+                // One term: the tile's scores stay in registers.  Two: they are read twice, 64 at a time, in loops, as a
+                // call of a few tiles waits for its instructions (64 sequences over 16384: 32.7 us unrolled, 30.8 so).
+                constexpr int SC = TERMS == 1 ? C::BN : 64;
+                uint32_t s[SC];
                 const int kv0 = t * C::BN;
-                if (kv0 + C::BN > first_lim) {
+                const bool edge = kv0 + C::BN > first_lim;
+                auto load = [&](int c) {
+                    tmem_ld_cols<SC / 32>(sc + c, s);
+                    if (edge) {
 #pragma unroll
-                    for (int e = 0; e < C::BN; ++e)
-                        if (kv0 + e >= lim) s[e] = 0xff800000u;        // -inf
-                }
+                        for (int e = 0; e < SC; ++e)
+                            if (kv0 + c + e >= lim) s[e] = 0xff800000u;    // -inf
+                    }
+                };
                 float m4[4];
+                if constexpr (TERMS == 1) {
+                    load(0);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) m4[k] = __uint_as_float(s[k]);
+                    for (int k = 0; k < 4; ++k) m4[k] = __uint_as_float(s[k]);
 #pragma unroll
-                for (int e = 4; e + 8 <= C::BN; e += 8)
+                    for (int e = 4; e + 8 <= C::BN; e += 8)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) m4[k] = fmax3(m4[k], __uint_as_float(s[e + k]), __uint_as_float(s[e + 4 + k]));
+                        for (int k = 0; k < 4; ++k) m4[k] = fmax3(m4[k], __uint_as_float(s[e + k]), __uint_as_float(s[e + 4 + k]));
 #pragma unroll
-                for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], __uint_as_float(s[C::BN - 4 + k]));
+                    for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], __uint_as_float(s[C::BN - 4 + k]));
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) m4[k] = -INFINITY;
+#pragma unroll 1
+                    for (int c = 0; c < C::BN; c += SC) {
+                        load(c);
+#pragma unroll
+                        for (int e = 0; e < SC; e += 8)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) m4[k] = fmax3(m4[k], __uint_as_float(s[e + k]), __uint_as_float(s[e + 4 + k]));
+                    }
+                }
                 const float m_tile = __fmul_rn(fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]), sl2);
                 // A row whose maximum grew by more than 2^8 rescales its sum and output; the
                 // others keep the old reference (weights up to 2^8 lose nothing).  PV(t - 1) is
@@ -529,23 +568,49 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 const float neg = m == -INFINITY ? 0.f : -m;
                 float2 s2[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                auto weights = [&](int at, int e, uint32_t& pk) -> float2 {    // of scores at + e, at + e + 1
+                    const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[at + e]), __uint_as_float(s[at + e + 1])),
+                                                make_float2(sl2, sl2), make_float2(neg, neg));
+                    const float2 p = make_float2(ex2(x.x), ex2(x.y));
+                    s2[(e >> 1) & 3] = __fadd2_rn(s2[(e >> 1) & 3], p);
+                    pk = pack2(p.x, p.y);
+                    return p;
+                };
+                if constexpr (TERMS == 1) {
 #pragma unroll
-                for (int c = 0; c < C::BN; c += 32) {
-                    uint32_t pk[16];
+                    for (int c = 0; c < C::BN; c += 32) {
+                        uint32_t pk[16];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[c + e]), __uint_as_float(s[c + e + 1])),
-                                                    make_float2(sl2, sl2), make_float2(neg, neg));
-                        const float2 p = make_float2(ex2(x.x), ex2(x.y));
-                        s2[(e >> 1) & 3] = __fadd2_rn(s2[(e >> 1) & 3], p);
-                        pk[e >> 1] = pack2(p.x, p.y);
+                        for (int e = 0; e < 32; e += 2) weights(c, e, pk[e >> 1]);
+                        tmem_st16(pc + (c >> 1), pk);
                     }
-                    tmem_st16(pc + (c >> 1), pk);
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < C::BN; c += SC) {
+                        load(c);
+#pragma unroll
+                        for (int h = 0; h < SC; h += 32) {
+                            uint32_t pk[32];               // 16 registers of values, 16 of what their rounding left
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2) {
+                                const float2 p = weights(h, e, pk[e >> 1]);
+                                const float2 rest = __ffma2_rn(make_float2(__uint_as_float(pk[e >> 1] << 16), __uint_as_float(pk[e >> 1] & 0xffff0000u)),
+                                                               make_float2(-1.f, -1.f), p);
+                                pk[16 + (e >> 1)] = pack2(rest.x, rest.y);
+                            }
+                            tmem_st32(pc + c + h, pk);
+                        }
+                        tmem_wait_st();
+                        tc_fence_before();
+                        mbar_arrive(smem_u32(&bar_p_ready[u * TERMS + c / SC]));
+                    }
                 }
                 l += ((s2[0].x + s2[0].y) + (s2[1].x + s2[1].y)) + ((s2[2].x + s2[2].y) + (s2[3].x + s2[3].y));
-                tmem_wait_st();
-                tc_fence_before();
-                mbar_arrive(smem_u32(&bar_p_ready[u]));
+                if constexpr (TERMS == 1) {
+                    tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(smem_u32(&bar_p_ready[u]));
+                }
             }
             if (!ok) break;
             if (!(ok = mbar_wait_warp(smem_u32(&bar_o_full[u]), (C::SEP ? tiles - 1 : parts) & 1, w, SITE_PAGED_O_FULL))) break;
@@ -623,11 +688,11 @@ __global__ void __launch_bounds__(384, 1)
     }
 }
 
-template <int D, int DR, bool SH>
+template <int D, int DR, bool SH, int TERMS>
 cudaError_t launch_tiles_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedAttnArgs& a,
                            cudaStream_t st) {
-    using C = TileCfg<D>;
-    auto kfn = paged_tiles_kernel<D, DR, SH>;
+    using C = TileCfg<D, TERMS>;
+    auto kfn = paged_tiles_kernel<D, DR, SH, TERMS>;
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(kfn, C::SMEM, done);
     if (e != cudaSuccess) return e;
@@ -638,16 +703,16 @@ cudaError_t launch_tiles_t(const CUtensorMap& tq, const CUtensorMap& tk, const C
 
 cudaError_t launch_paged_tiles(int D, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                const PagedAttnArgs& a, cudaStream_t st) {
-    if (D == 64) return launch_tiles_t<64, 64, false>(tq, tk, tv, a, st);
-    if (D == 128) return launch_tiles_t<128, 128, false>(tq, tk, tv, a, st);
+    if (D == 64) return launch_tiles_t<64, 64, false, 1>(tq, tk, tv, a, st);
+    if (D == 128) return launch_tiles_t<128, 128, false, 1>(tq, tk, tv, a, st);
     return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_shared_tiles(int D, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+cudaError_t launch_shared_tiles(int D, int terms, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                 const PagedAttnArgs& a, cudaStream_t st) {
-    if (D == 32) return launch_tiles_t<64, 32, true>(tq, tk, tv, a, st);
-    if (D == 64) return launch_tiles_t<64, 64, true>(tq, tk, tv, a, st);
-    if (D == 128) return launch_tiles_t<128, 128, true>(tq, tk, tv, a, st);
+    if (D == 32 && terms == 2) return launch_tiles_t<64, 32, true, 2>(tq, tk, tv, a, st);
+    if (D == 64) return (terms == 2 ? launch_tiles_t<64, 64, true, 2> : launch_tiles_t<64, 64, true, 1>)(tq, tk, tv, a, st);
+    if (D == 128) return (terms == 2 ? launch_tiles_t<128, 128, true, 2> : launch_tiles_t<128, 128, true, 1>)(tq, tk, tv, a, st);
     return cudaErrorInvalidValue;
 }
 
