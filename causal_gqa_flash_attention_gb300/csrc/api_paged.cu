@@ -862,6 +862,8 @@ ne_status ne_pages_evict(const ne_paged_cache* cache, const float* weights, cons
         return fail(NE_ERR_INVALID_ARG, "workspace must be non-null and 256-byte aligned (%zu bytes needed)", w.total);
     if (workspace_bytes < w.total)
         return fail(NE_ERR_INVALID_ARG, "workspace too small: %zu bytes given, %zu needed", workspace_bytes, w.total);
+    if (cache->k == cache->v)
+        return fail(NE_ERR_INVALID_ARG, "k and v are one pool: the rows of both are moved, so they must be two");
     ne::EvictArgs a = {};
     if ((s = ready((cudaStream_t)stream, &a.err)) != NE_OK) return s;
     const int e = cache->elem_bytes;
