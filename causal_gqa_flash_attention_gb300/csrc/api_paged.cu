@@ -850,16 +850,16 @@ ne_status ne_pages_evict(const ne_paged_cache* cache, const float* weights, cons
         return fail(NE_ERR_INVALID_ARG, "sink and recent must be 0 to 2^30 (sink=%d recent=%d)", sink, recent);
     if (B == 0) return NE_OK;
     const size_t rows = (size_t)cache->layers * B * cache->Hkv, T = (size_t)max_pages * cache->page_size;
+    const EvictWs w = evict_ws(rows, T);
     s = check_arrays({{weights, rows * T * 4, "weights", -1}, {positions, rows * T * 4, "positions", -1},
                       {pos_offset, (size_t)B * 4, "pos_offset", -1}, {page_table, (size_t)B * max_pages * 4, "page_table", -1},
                       {seq_lens, (size_t)B * 4, "seq_lens", -1}, {new_lens, (size_t)B * 4, "new_lens", -1}},
                      {{weights_out, rows * T * 4, "weights_out", 0}, {positions_out, rows * T * 4, "positions_out", 1},
-                      {pos_offset_out, (size_t)B * 4, "pos_offset_out", 2}});
+                      {pos_offset_out, (size_t)B * 4, "pos_offset_out", 2}, {workspace, w.total, "workspace", -1}});
     if (s == NE_OK) s = check_ptrs({weights, positions, weights_out, positions_out});
     if (s != NE_OK) return s;
-    const EvictWs w = evict_ws(rows, T);
-    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
-        return fail(NE_ERR_INVALID_ARG, "workspace must be non-null and 256-byte aligned (%zu bytes needed)", w.total);
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return fail(NE_ERR_INVALID_ARG, "workspace must be 256-byte aligned (%zu bytes needed)", w.total);
     if (workspace_bytes < w.total)
         return fail(NE_ERR_INVALID_ARG, "workspace too small: %zu bytes given, %zu needed", workspace_bytes, w.total);
     if (cache->k == cache->v)

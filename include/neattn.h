@@ -501,7 +501,8 @@ ne_status ne_pages_compact(const ne_paged_cache* cache, const int* refcount, con
  *                             0 <= pos_offset[b] < 2^30
  * weights, positions and their outputs are 16-byte aligned, the other arrays 4.
  * Slots m .. n-1 get weight 0 and position -1; entries at and behind n stay as they were.  Each output
- * may be its input; any other overlap is refused, and k and v that are one pool.  The pages that hold a sequence's slots must belong to it alone
+ * may be its input; any other overlap of these arrays and the workspace is refused, and k and v that are one pool
+ * (the pools' memory is compared with nothing else).  The pages that hold a sequence's slots must belong to it alone
  * (ne_pages_fork with deep sees to that), and ne_pages_resize from seq_lens to new_lens then gives back the
  * pages behind m.  Bad lengths, offsets and page ids are clamped or skipped and reported by
  * ne_get_device_error().  workspace: ne_pages_evict_workspace_size() bytes (4 per entry of weights), 256-byte
