@@ -770,8 +770,8 @@ def pages_evict(weights, positions, pos_offset, page_table, seq_lens, new_lens, 
     pools of one layer), T = max_pages * page_size, pos_offset int32 [B] the positions given up so
     far.  Kept rows of the pools move into the slots below new_lens in place.  Returns
     (weights_out, positions_out, pos_offset_out), each of which may be its input; fresh ones hold 0
-    and -1 behind the lengths.  pages_resize(seq_lens -> new_lens) then gives the pages back, and
-    paged_append takes pos_offset_out."""
+    and -1 behind the lengths.  pages_resize(seq_lens -> min(seq_lens, new_lens)) then gives the pages
+    back (to a new_lens above seq_lens it would grow the sequence), and paged_append takes pos_offset_out."""
     lib = _lib or load()
     c, dev, _, _, Hkv, _ = _paged_cache(k_pages, v_pages, True)
     T2 = page_table.shape

@@ -503,8 +503,9 @@ ne_status ne_pages_compact(const ne_paged_cache* cache, const int* refcount, con
  * Slots m .. n-1 get weight 0 and position -1; entries at and behind n stay as they were.  Each output
  * may be its input; any other overlap of these arrays and the workspace is refused, and k and v that are one pool
  * (the pools' memory is compared with nothing else).  The pages that hold a sequence's slots must belong to it alone
- * (ne_pages_fork with deep sees to that), and ne_pages_resize from seq_lens to new_lens then gives back the
- * pages behind m.  Bad lengths, offsets and page ids are clamped or skipped and reported by
+ * (ne_pages_fork with deep sees to that; a child's rows of these arrays are the caller's to copy, as are a new
+ * sequence's to fill in).  ne_pages_resize from seq_lens to m, not to a new_lens above it, which would grow the sequence, then
+ * gives back the pages behind m.  Bad lengths, offsets and page ids are clamped or skipped and reported by
  * ne_get_device_error().  workspace: ne_pages_evict_workspace_size() bytes (4 per entry of weights), 256-byte
  * aligned, caller-owned, rewritten by every call.  layers * B * Hkv < 2^31; 0 <= sink, recent <= 2^30. */
 size_t ne_pages_evict_workspace_size(int layers, int B, int Hkv, int T);
