@@ -398,14 +398,16 @@ ne_status ne_paged_attn_f32(const float* q, const ne_paged_cache* cache, const i
  *          in front of groups[0] and from groups[R] on share nothing); 0 <= R <= B
  *   shared [R] int32: the first shared[r] positions hold the same in every sequence of group r (whether
  *          or not in the same pages), all in front of its new tokens: shared[r] <= seq_lens[b] - n_b
- * Both device memory, 4-byte aligned.  They are read through the group's first sequence, in whole steps of 256
- * positions; what is left of them, and the prefix of a group of one, every sequence reads for itself.
+ * Both device memory, 4-byte aligned.  They are read through the group's first sequence, up to its length (what
+ * shared[r] has above it counts for nothing and is not reported) and in whole steps of 256 positions; what is left of
+ * them, and the prefix of a group of one, every sequence reads for itself.
  * Everything else is as in ne_paged_attn (its workspace of another size), the bits that are kept of a weight
- * among it; results are the same up to rounding, and the same bits for the same call.  Groups outside [0, B] or descending, a negative shared[r], and
- * whole steps of shared positions that reach into a sequence's new tokens are reported by
- * ne_get_device_error() (outputs of that group invalid).  A call that has nothing to gain (sequences whose rows
- * fill tiles by themselves, judged by max_new, N / B and max_pages; small caches; more than 128 bf16 query heads per
- * kv head) runs as ne_paged_attn does, and then looks at neither groups nor shared.
+ * among it; results are the same up to rounding, and the same bits for the same call.  Groups outside [0, B] or
+ * descending, a negative shared[r], and whole steps that so count and reach into a sequence's new tokens or behind its
+ * length are reported by ne_get_device_error() (outputs of that group invalid).  A call that has nothing to gain
+ * (sequences whose rows fill tiles by themselves, judged by max_new, N, B and max_pages; caches that are small even were
+ * every table full; more than 128 bf16 query heads per kv head) runs as ne_paged_attn does, and then looks at neither
+ * groups nor shared.
  * workspace: ne_paged_attn_shared_workspace_size() bytes (two workspaces of ne_paged_attn and 8 D + 32 bytes per
  * row and query head). */
 size_t ne_paged_attn_shared_workspace_size(int B, int N, int Hq, int Hkv, int D);
