@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(640, 1)
             mbar_init(smem_u32(&bar_l_empty[i]), 8);       // the exponential warps of every second tile
         }
         for (int i = 0; i < 4; ++i) {                      // 2 u + item % 2
-            mbar_init(smem_u32(&bar_s_full[i]), 1);
+            mbar_init(smem_u32(&bar_s_full[i]), 2);        // the products, and the log-sum-exps
             mbar_init(smem_u32(&bar_s_free[i]), 4);
         }
         for (int i = 0; i < 2; ++i) {
@@ -689,9 +689,12 @@ __global__ void __launch_bounds__(640, 1)
                     }
                 }
                 __syncwarp();
-                // Before S is committed its log-sum-exps are there, so that the exponentials' look at them never waits.
+                // The exponentials wait for S alone, so its log-sum-exps have to be there.  A commit's arrival orders this
+                // thread's products, not what warp 3 stored: an ordinary arrival beside it passes that on (a wait of
+                // the exponentials' own costs D 64 99.2 -> 101.5 us).
                 if (!(ok = mbar_wait_warp(smem_u32(&bar_l_full[item % C::NL]), (item / C::NL) & 1, w, SITE_PAGED_Q))) break;
                 if (elect_one()) {
+                    mbar_arrive(smem_u32(&bar_s_full[s]));
                     umma_commit(smem_u32(&bar_s_full[s]));
                     umma_commit(smem_u32(&bar_q_empty[i]));
                     if (t + 1 == p.t1) umma_commit(smem_u32(&bar_k_empty[kslot]));
@@ -784,15 +787,9 @@ __global__ void __launch_bounds__(640, 1)
             const int t_hi = a.G % a.gs ? 0 : p.n / a.sub * a.ngrp;
             for (int j = skip; j < n; j += 2) {
                 const int i = (item + j) % C::NL;
-                // (Every warp for itself, though the issuer has waited for them, too: a commit's arrival orders its
-                // thread's products alone, not what warp 3 stored.  One look, beside the wait for S: D 64 99.6 -> 101.4 us;
-                // behind it 102.5, a tile ahead 103.9.)
-                const bool there = mbar_test(smem_u32(&bar_l_full[i]), ((item + j) / C::NL) & 1);
-                if (mine && !(ok = mbar_wait_warp(smem_u32(&bar_s_full[2 * u + half]), uses & 1, w, SITE_PAGED_S_FULL))) break;
-                if (!__all_sync(0xffffffffu, there) &&
-                    !(ok = mbar_wait_warp(smem_u32(&bar_l_full[i]), ((item + j) / C::NL) & 1, w, SITE_PAGED_Q)))
-                    break;
-                if (mine) {
+                if (!mine && !(ok = mbar_wait_warp(smem_u32(&bar_l_full[i]), ((item + j) / C::NL) & 1, w, SITE_PAGED_Q))) break;
+                if (mine) {                                // (the issuer waited for the log-sum-exps, and passes them on)
+                    if (!(ok = mbar_wait_warp(smem_u32(&bar_s_full[2 * u + half]), uses & 1, w, SITE_PAGED_S_FULL))) break;
                     ++uses;
                     tc_fence_after();
                     const int t = p.t0 + j;

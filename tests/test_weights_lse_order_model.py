@@ -1,5 +1,5 @@
 """What orders the log-sum-exps that one warp of the accumulated-weights kernel for many rows stores in shared memory
-before the loads of the exponential warps: a model of happens-before, run on the CPU, and the waits that the source has.
+before the loads of the exponential warps: a model of happens-before, run on the CPU, and the arrivals that the source has.
 
 Every role carries the set of stores and loads that happen before its next step.  A wait on a barrier takes over what
 its arrivals released: an ordinary arrival all that its thread knows, the arrival of a tcgen05 commit nothing of
@@ -32,9 +32,10 @@ class Bar:
             self.arrived, self.now = 0, set()
 
 
-def simulate(items, NL, rng, looks):
-    """looks: the exponential warps wait for the log-sum-exps themselves."""
-    l_full, l_empty, s_full, s_free = [Bar(1) for _ in range(NL)], [Bar(2) for _ in range(NL)], [Bar(1) for _ in range(4)], [Bar(1) for _ in range(4)]
+def simulate(items, NL, rng, passes_on):
+    """passes_on: the issuer, which waited for the log-sum-exps, arrives for S beside its commit."""
+    l_full, l_empty = [Bar(1) for _ in range(NL)], [Bar(2) for _ in range(NL)]
+    s_full, s_free = [Bar(2 if passes_on else 1) for _ in range(4)], [Bar(1) for _ in range(4)]
     reads = {}                                              # item: loads of its place so far
 
     def finder(knows):
@@ -53,12 +54,12 @@ def simulate(items, NL, rng, looks):
                 yield s_free[s], use - 1
             yield l_full[n % NL], n // NL
             s_full[s].arrive(set())                         # (by a commit)
+            if passes_on:
+                s_full[s].arrive(set(knows))
 
     def exps(u, half, knows):
         for use, n in enumerate(range(half, items, 2)):
             yield s_full[2 * u + half], use
-            if looks:
-                yield l_full[n % NL], n // NL
             if ("store", n) not in knows:
                 raise Unordered(f"load of {n}")
             knows.add(("load", n, u))
@@ -91,12 +92,12 @@ def test_a_commit_alone_orders_nothing():
         simulate(1, 8, random.Random(0), False)
 
 
-def test_the_kernel_waits_as_modelled():
-    """In the exponential warps' loop over query tiles the wait for the log-sum-exps stands under no condition."""
+def test_the_kernel_arrives_as_modelled():
+    """Behind its wait for the log-sum-exps the issuer arrives on the scores' barrier, which counts that arrival."""
     with open(SOURCE) as f:
         text = f.read()
-    body = text[text.index("---- exponentials\n"):]
-    loop = body[body.index("for (int j = skip; j < n; j += 2) {"):body.index("const float4* nl")]
-    assert re.search(r"const bool there = mbar_test\(smem_u32\(&bar_l_full\[i\]\)", loop)
-    assert re.search(r"if \(!__all_sync\(0xffffffffu, there\) &&\s*!\(ok = mbar_wait_warp\(smem_u32\(&bar_l_full\[i\]\)", loop)
-    assert not re.search(r"mine[^;]*bar_l_full", loop)
+    assert re.search(r"mbar_init\(smem_u32\(&bar_s_full\[i\]\), 2\);", text)
+    issuer = text[text.index("---- UMMA issuer of key tile u\n"):text.index("---- the CTA's parts, and their log-sum-exps\n")]
+    wait = issuer.index("mbar_wait_warp(smem_u32(&bar_l_full[item % C::NL])")
+    arrive, commit = issuer.index("mbar_arrive(smem_u32(&bar_s_full[s]))"), issuer.index("umma_commit(smem_u32(&bar_s_full[s]))")
+    assert wait < arrive and wait < commit
