@@ -1,5 +1,5 @@
 // paged_tiles.cu -- attention of chunks of new tokens over the paged cache on tcgen05
-// tensor cores, bf16, head_dim 64 and 128.
+// tensor cores, bf16, head_dim 64 and 128; over shared prefixes of any new tokens, head_dim 32, too.
 //
 // The query heads of a kv head read the same keys, so a tile's 128 rows are (token, head)
 // pairs: 128 / G tokens times G heads, token first, as TMA lays a [tokens, heads, 64] box
@@ -118,12 +118,13 @@ __device__ __forceinline__ void transpose4(uint4 (&v)[4], int l) {
 // SH: the SHARED form, prefixes and own positions in one line, results as parts alone; DR: the cache's head_dim
 // (32 runs as 64: TMA fills the columns behind a row's end with zeros).
 // Measured (GB300, with the join): 64 sequences over a shared prefix of 16384 and up to 512 positions of their own, 12/4
-// heads of 64: 30.7 us (every sequence for itself: 110); 37 sequences in four groups over up to 8192, 16/4 heads
-// of 128: 36.4 us (54), the read of the cache 15 at the copy rate.  With one term per weight those took 26.4 and 33.4:
-// of the 4.3 us at D 64 the second product takes 1.2, forming it 1.3 and S, which then waits for PV, 1.8.  A CTA takes 4 us to
+// heads of 64: 30.6 us (every sequence for itself: 110); 37 sequences in four groups over up to 8192, 16/4 heads
+// of 128: 36.3 us (54), the read of the cache 15 at the copy rate.  With one term per weight those took 26.4 and 33.4:
+// of the 4.2 us at D 64 the second product takes 1.2, forming it 1.3 and S, which then waits for PV, 1.8.  A CTA takes 4 us to
 // find its share, 2 to its first product and 2 for the ends of a part; the join 3 to 4.
-// Tried for the second term and left out: an issuer for each subtile at D 64 with P over S (34 us), the value cut off
-// instead of rounded (no change), both terms multiplied when all of P is there (D 128: 39 us).
+// Tried for the second term and left out: an issuer for each subtile at D 64 with P over S (34 us), three places for S at D
+// 64 in turn, so that it runs ahead of PV (32.4: two live subtiles are bound by their softmax's instructions), the value cut
+// off instead of rounded (no change), both terms multiplied when all of P is there (D 128: 39 us).
 // Tried and left out: own positions in the kernel for few rows behind this one (34.4 us), a part's keys
 // split over the two subtiles where its rows fit into one (34.5; more registers live, a hand-over per part), the next
 // part's keys in front of its queries (no change), parts of one subtile taking the two in turn with scores masked in

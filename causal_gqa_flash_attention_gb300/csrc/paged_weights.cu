@@ -17,12 +17,13 @@
 // Many rows, fp32: units of 128 keys on fp32 FMAs, two keys per lane in registers, the query rows
 // broadcast from shared memory.
 //
-// Measured (GB300): one token over 8 x 16384 positions, 12/4 heads of 64: 16.3 us, 4.4 TB/s (10.6 at the copy
+// Measured (GB300): one token over 8 x 16384 positions, 12/4 heads of 64: 16.2 us, 4.4 TB/s (10.6 at the copy
 // rate; 3 to begin and find the shares, then 5.3 TB/s); the small fp32 step 3.1.  2048 tokens over 16384
-// positions, 16/4 heads of 128: 108 us, 1.19 PFLOP/s (62% of the bf16 GEMM; operands out of shared memory, 128 bytes a
-// cycle, bound the products); of 64: 100 us, 0.64 PFLOP/s, the exponential units 70% busy: of the 3000 cycles of
-// a tile its warps spend 2200 on exponentials.  Twelve sequences, single tokens beside chunks up to 512 over up
-// to 4096: 19.3 us (2.0), 5 before the first product, then 5 query tiles in 3 parts per CTA, then the join.
+// positions, 16/4 heads of 128: 107 us, 1.20 PFLOP/s (62% of the bf16 GEMM; the tensor pipe and the exponential units 48%
+// busy each, operands out of shared memory, 128 bytes a cycle, bound the products); of 64: 99.5 us, 0.65 PFLOP/s, the
+// exponential units 52% busy and the tensor pipe 26%: of the 3000 cycles of a tile its warps spend 2200 in the section
+// that has the exponentials; fp32, of 64: 1.94 ms, 33 TFLOP/s.  Twelve sequences, single tokens beside chunks up to 512
+// over up to 4096: 18.9 us (2.0), 5 before the first product, then 5 query tiles in 3 parts per CTA, then the join.
 // Tried for many rows and left out: part of the exponentials as a polynomial on the FMA pipes (D 64 119 -> 144
 // us, then with eight exponential warps), keys as the TMEM operand with 96-row query tiles (D 128 120 ->
 // 138: it is the issue of products, some 90 cycles each, that counts), S in halves with buffers of their own
