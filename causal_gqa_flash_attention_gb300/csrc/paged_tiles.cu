@@ -14,8 +14,8 @@
 // alternate: while the softmax warps of one work on its S tile, the tensor core runs the other's
 // PV and next S.  Roles (12 warps):
 //   warp 0       producer: Q pair of the unit, then K and V tiles through an NS-slot ring.
-//   warp 1       UMMA issuer (owns the 512 TMEM columns); at D 64 one of two, warp 2 the other, each
-//                for a subtile.  Per tile t: O_u += P_u(t) V(t) once P_u(t) is there, and S_u(t + 1) =
+//   warp 1       UMMA issuer (owns the 512 TMEM columns); at D 64, with one term per weight, one of two, warp 2 the
+//                other, each for a subtile.  Per tile t: O_u += P_u(t) V(t) once P_u(t) is there, and S_u(t + 1) =
 //                Q_u K(t + 1)^T.  At D 64, where P has columns of its own, S(t + 1) goes first, as soon
 //                as S(t) is in registers.  At D 128 P lies over S, and S(t + 1) goes right behind the PV
 //                (one thread's UMMAs run in order, so it cannot overtake it, and S(t + 1) complete means
@@ -25,7 +25,7 @@
 //   warp 3       finds the CTA's parts (paged_sched.cuh) and queues them for the others.
 //   warps 4-11   softmax: thread r of subtile u owns row r (TMEM lane r).
 // TMEM: S_u at 128 u, O_u behind both; P_u (bf16) over S_u's first half at D 128, where TMEM
-// is full, in columns of its own at D 64.
+// is full, in columns of its own at D 64; two terms of P_u over all of S_u.
 // Weights are rounded to bf16 for the product (half a step, 2^-8 of each weight, as the
 // training forward does); maximum and sum stay fp32, and the sum is of the unrounded weights.  Over
 // shared prefixes, where rows come here that would otherwise take the kernel for few rows, they keep that kernel's
